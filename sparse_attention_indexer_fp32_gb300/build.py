@@ -20,7 +20,8 @@ BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(BUILD, "libtopk_indexer.so")
 SOURCES = (["topk_abi.cu"] + [f"topk_k{k}_{o}.cu" for k in (512, 1024, 2048) for o in ("ragged", "paged")]
-           + [f"topk_short_k{k}.cu" for k in (512, 1024, 2048)] + ["topk_blocks.cu"])
+           + [f"topk_short_k{k}.cu" for k in (512, 1024, 2048)] + ["topk_blocks.cu", "step_abi.cu", "rotary.cu", "indexer_scores.cu",
+                                                                      "sparse_attention.cu"])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,7 +37,7 @@ def nvcc() -> str:
 
 def _inputs_mtime() -> float:
     paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    paths.append(os.path.join(INCLUDE, "topk_indexer.h"))
+    paths += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return max(os.path.getmtime(p) for p in paths)
 
 
