@@ -25,6 +25,7 @@
 
 #include "step_launch.cuh"
 #include "tcgen05.cuh"
+#include "tensor_map.cuh"
 
 namespace tki {
 namespace {
@@ -46,6 +47,8 @@ struct ScoreParams {
   int32_t chunks, groups;  // work units per sequence: chunks x groups
   int64_t units;
   bool q_vector;           // queries can be fetched 16 bytes at a time
+  int32_t box_rows;        // entries of one page per box of the tensor map
+  CUtensorMap map;         // of the keys, where boxes are used
 };
 
 struct ScoreShared {
@@ -97,18 +100,52 @@ struct Kind;
 template <>
 struct Kind<__nv_bfloat16> {
   static constexpr uint32_t type = 1;
+  static constexpr CUtensorMapDataType map_type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 };
 template <>
 struct Kind<__half> {
   static constexpr uint32_t type = 0;
+  static constexpr CUtensorMapDataType map_type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 };
 template <>
 struct Kind<__nv_fp8_e4m3> {
   static constexpr uint32_t type = 0;
+  static constexpr CUtensorMapDataType map_type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 };
 
-// STAGES tiles of keys in flight; STEP columns per TMEM load.
-template <typename E, int STAGES, int STEP>
+// Queries, weights and lengths of a unit into buffer `buf`, by `n` threads.
+template <typename E>
+__device__ __forceinline__ void fetch_queries(const ScoreParams& p, const Unit& r, unsigned char* smem, uint32_t q_bytes,
+                                              ScoreShared& sh, uint32_t buf, int th, int n, const void* nowhere) {
+  const E* q = static_cast<const E*>(p.a.q) + r.b * p.a.q_seq_stride;
+  const int units = p.blocks * 8;
+  for (int i = th; i < p.cols * units; i += n) {
+    const int col = i / units, j = i - col * units;
+    const int t = col / p.hp, h = col - t * p.hp;
+    const bool real = t < r.tokens && h < p.a.H && j < p.row_units;
+    const E* src = real ? q + (r.t0 + t) * p.a.q_token_stride + h * p.a.q_head_stride + j * (16 / sizeof(E)) : nullptr;
+    const uint32_t at = buf * q_bytes + (j >> 3) * p.cols * 128 + swizzled(col, j & 7);
+    if (p.q_vector) {
+      copy16(smem_addr(smem) + at, real ? src : nowhere, real);
+    } else {
+      E v[16 / sizeof(E)];
+      for (int e = 0; e < static_cast<int>(16 / sizeof(E)); ++e) v[e] = real ? src[e] : E(0.0f);
+      *reinterpret_cast<uint4*>(smem + at) = *reinterpret_cast<const uint4*>(v);
+    }
+  }
+  for (int i = th; i < p.cols; i += n) {
+    const int t = i / p.hp, h = i - t * p.hp;
+    sh.weights[buf][i] =
+        t < r.tokens && h < p.a.H ? p.a.weights[(static_cast<int64_t>(r.b) * p.a.T + r.t0 + t) * p.a.H + h] : 0.0f;
+  }
+  if (th < kMaxTokens) sh.lengths[buf][th] = th < r.tokens ? length_of(p, r.b, r.t0 + th) : 0;
+  copy_arrive(&sh.q_full[buf]);
+  mbar_arrive(&sh.q_full[buf]);
+}
+
+// STAGES tiles of keys in flight; STEP columns per TMEM load; keys by BOXES of
+// the TMA engine or by 16-byte copies.
+template <typename E, int STAGES, int STEP, bool BOXES>
 __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_constant__ ScoreParams p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -119,9 +156,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
   const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[i], 128), mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[i], BOXES ? 1 : 128), mbar_init(&sh.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], 128);
+      mbar_init(&sh.q_full[i], BOXES ? 192 : 256);  // the copies' arrivals and the stores'
       mbar_init(&sh.q_empty[i], 1 + kEpilogueWarps);
       mbar_init(&sh.t_full[i], 1);
       mbar_init(&sh.t_empty[i], 128);
@@ -136,89 +173,103 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
   const uint32_t tmem = sh.tmem;
   volatile uint32_t* stop = &sh.stop;
 
-  if (warp >= 8 && warp < 12) {
-    // ---- fetching ----
-    const int w = warp - 8, th = threadIdx.x - 256;
+  // what a copy of nothing points at
+  const void* nowhere = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p.a.q) & ~static_cast<uintptr_t>(15));
+  if (BOXES && warp == 8) {
+    // ---- keys, by boxes: lane i fetches block i / 16 of the box i % 16 of a tile ----
+    const int box = lane & 15, block = lane >> 4, boxes = kTile / p.box_rows;
+    const bool mine = box < boxes && block < p.blocks;
+    uint32_t k = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+      const Unit r = unit_of(p, u);
+      if (r.tile0 >= r.tile1) continue;
+      const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
+      auto entry = [&](int tile) -> int64_t { return static_cast<int64_t>(tile) * kTile + box * p.box_rows; };
+      auto page_at = [&](int tile) -> int32_t {
+        const int64_t s = entry(tile);
+        return mine && tile < r.tile1 && s < p.a.width ? table[static_cast<int32_t>(s) / p.a.page_size] : -1;
+      };
+      int32_t next = page_at(r.tile0);  // read a tile ahead
+      for (int tile = r.tile0; tile < r.tile1; ++tile, ++k) {
+        const uint32_t stage = k % STAGES;
+        const int32_t page = next;
+        next = page_at(tile + 1);
+        ok = wait_or_stop(&sh.empty[stage], ((k / STAGES) & 1) ^ 1, stop);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.full[stage], tile_bytes);
+        __syncwarp();
+        if (mine) {
+          const int z = page < 0 || page >= p.a.num_pages ? static_cast<int>(p.a.num_pages) : page;  // absent: zeros
+          const int y = static_cast<int>(static_cast<uint32_t>(entry(tile)) % static_cast<uint32_t>(p.a.page_size));
+          box_load(ring_addr + stage * tile_bytes + (block * kTile + box * p.box_rows) * 128, &p.map,
+                   block * (128 / static_cast<int>(sizeof(E))), y, z, &sh.full[stage]);
+        }
+      }
+    }
+    // no box may arrive after the CTA has left
+    for (uint32_t i = 0; i < STAGES && i < k; ++i)
+      mbar_wait_bounded(&sh.full[(k - 1 - i) % STAGES], ((k - 1 - i) / STAGES) & 1, 1000000000ull);
+  } else if (BOXES && warp > 8 && warp < 12) {
+    // ---- queries, a unit ahead ----
+    uint32_t nu = 0;
+    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+      const Unit r = unit_of(p, u);
+      if (r.tile0 >= r.tile1) continue;
+      if (!wait_or_stop(&sh.q_empty[nu & 1], ((nu >> 1) & 1) ^ 1, stop)) break;
+      fetch_queries<E>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - 288, 96, nowhere);
+      ++nu;
+    }
+    copy_commit();
+    copy_wait<0>();
+  } else if (!BOXES && warp >= 8 && warp < 12) {
+    // ---- keys and queries, by 16-byte copies: 8 lanes fetch a row's 128 bytes ----
+    const int w = warp - 8;
     const uint32_t unit16 = lane & 7;
-    // what a copy of nothing points at
-    const void* nowhere = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p.a.q) & ~static_cast<uintptr_t>(15));
     uint32_t k = 0, nu = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
       const Unit r = unit_of(p, u);
       if (r.tile0 >= r.tile1) continue;
-      // the slot of this lane's row of a tile: row 32 w + lane
-      auto slot_of = [&](int tile) -> int64_t {
-        const int64_t s = static_cast<int64_t>(tile) * kTile + w * 32 + lane;
-        if (s >= p.a.width) return -1;
-        const int32_t s32 = static_cast<int32_t>(s), pg = s32 / p.a.page_size;
-        const int32_t page = p.a.page_table[r.b * p.a.table_stride + pg];
-        if (page < 0 || page >= p.a.num_pages) return -1;
-        return page * p.a.key_page_stride + (s32 - pg * p.a.page_size) * p.a.key_token_stride;
+      const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
+      // this lane looks up row 32 w + lane of a tile
+      auto entry = [&](int tile) -> int64_t { return static_cast<int64_t>(tile) * kTile + w * 32 + lane; };
+      auto page_at = [&](int tile) -> int32_t {
+        const int64_t s = entry(tile);
+        return tile < r.tile1 && s < p.a.width ? table[static_cast<int32_t>(s) / p.a.page_size] : -1;
       };
-      int64_t next = slot_of(r.tile0);
-      // queries, weights and lengths
-      const uint32_t buf = nu & 1;
-      ok = wait_or_stop(&sh.q_empty[buf], ((nu >> 1) & 1) ^ 1, stop);
+      int32_t next = page_at(r.tile0);  // read a tile ahead
+      ok = wait_or_stop(&sh.q_empty[nu & 1], ((nu >> 1) & 1) ^ 1, stop);
       if (!ok) break;
+      fetch_queries<E>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - 256, 128, nowhere);
       ++nu;
-      const E* q = static_cast<const E*>(p.a.q) + r.b * p.a.q_seq_stride;
-      const int units = p.blocks * 8;
-      for (int i = th; i < p.cols * units; i += 128) {
-        const int col = i / units, j = i - col * units;
-        const int t = col / p.hp, h = col - t * p.hp;
-        const bool real = t < r.tokens && h < p.a.H && j < p.row_units;
-        const E* src = real ? q + (r.t0 + t) * p.a.q_token_stride + h * p.a.q_head_stride + j * (16 / sizeof(E)) : nullptr;
-        const uint32_t at = buf * q_bytes + (j >> 3) * p.cols * 128 + swizzled(col, j & 7);
-        if (p.q_vector) {
-          copy16(q_addr + at, real ? src : nowhere, real);
-        } else {
-          E v[16 / sizeof(E)];
-          for (int e = 0; e < static_cast<int>(16 / sizeof(E)); ++e) v[e] = real ? src[e] : E(0.0f);
-          *reinterpret_cast<uint4*>(smem + at) = *reinterpret_cast<const uint4*>(v);
-        }
-      }
-      for (int i = th; i < p.cols; i += 128) {
-        const int t = i / p.hp, h = i - t * p.hp;
-        sh.weights[buf][i] =
-            t < r.tokens && h < p.a.H ? p.a.weights[(static_cast<int64_t>(r.b) * p.a.T + r.t0 + t) * p.a.H + h] : 0.0f;
-      }
-      if (th < kMaxTokens) sh.lengths[buf][th] = th < r.tokens ? length_of(p, r.b, r.t0 + th) : 0;
-      copy_commit();
-      copy_wait<0>();
-      fence_proxy_async_smem();
-      mbar_arrive(&sh.q_full[buf]);
-      // keys: STAGES tiles in flight, each handed over when its copies are in
-      for (int tile = r.tile0; tile < r.tile1 + STAGES - 1; ++tile) {
-        if (tile < r.tile1) {
-          const uint32_t kk = k + (tile - r.tile0), stage = kk % STAGES;
-          ok = wait_or_stop(&sh.empty[stage], ((kk / STAGES) & 1) ^ 1, stop);
-          if (!ok) break;
-          const int64_t slot = next;
-          if (tile + 1 < r.tile1) next = slot_of(tile + 1);
-          const uint32_t dst = ring_addr + stage * tile_bytes;
+      for (int tile = r.tile0; tile < r.tile1; ++tile, ++k) {
+        const uint32_t stage = k % STAGES;
+        const int32_t page = next;
+        next = page_at(tile + 1);
+        ok = wait_or_stop(&sh.empty[stage], ((k / STAGES) & 1) ^ 1, stop);
+        if (!ok) break;
+        const int64_t slot = page < 0 || page >= p.a.num_pages
+                                 ? -1
+                                 : page * p.a.key_page_stride +
+                                       static_cast<int32_t>(entry(tile)) % p.a.page_size * p.a.key_token_stride;
+        const uint32_t dst = ring_addr + stage * tile_bytes;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = 4 * i + (lane >> 3);
-            const int64_t s = __shfl_sync(0xffffffffu, slot, row);
-            const E* src = static_cast<const E*>(p.a.keys) + (s < 0 ? 0 : s);
-            for (int c = 0; c < p.blocks; ++c) {
-              const uint32_t j = c * 8 + unit16;
-              const bool real = s >= 0 && j < static_cast<uint32_t>(p.row_units);
-              copy16(dst + c * kTile * 128 + swizzled(w * 32 + row, unit16), real ? src + j * (16 / sizeof(E)) : nowhere,
-                     real);
-            }
+        for (int i = 0; i < 8; ++i) {
+          const int row = 4 * i + (lane >> 3);
+          const int64_t s = __shfl_sync(0xffffffffu, slot, row);
+          const E* src = static_cast<const E*>(p.a.keys) + (s < 0 ? 0 : s);
+          for (int c = 0; c < p.blocks; ++c) {
+            const uint32_t j = c * 8 + unit16;
+            const bool real = s >= 0 && j < static_cast<uint32_t>(p.row_units);
+            copy16(dst + c * kTile * 128 + swizzled(w * 32 + row, unit16), real ? src + j * (16 / sizeof(E)) : nowhere,
+                   real);
           }
         }
-        copy_commit();
-        if (tile - r.tile0 >= STAGES - 1) {
-          copy_wait<STAGES - 1>();
-          fence_proxy_async_smem();
-          mbar_arrive(&sh.full[(k + (tile - r.tile0) - (STAGES - 1)) % STAGES]);
-        }
+        copy_arrive(&sh.full[stage]);
       }
-      k += r.tile1 - r.tile0;
     }
+    copy_commit();
     copy_wait<0>();
   } else if (warp == 12) {
     // ---- products ----
@@ -236,6 +287,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
         ok = wait_or_stop(&sh.t_empty[tb], ((k >> 1) & 1) ^ 1, stop) &&
              wait_or_stop(&sh.full[stage], (k / STAGES) & 1, stop);
         if (!ok) break;
+        fence_proxy_async_smem();  // the 16-byte copies are in; now the tensor cores may see them
         tc_fence_after();
         if (lane == 0) {
           for (int c = 0; c < p.blocks; ++c)
@@ -271,18 +323,24 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       if (!ok) break;
       ++nu;
       float* out = p.a.out + r.b * p.a.out_seq_stride + r.t0 * p.a.out_token_stride;
-      for (int tile = r.tile0; tile < r.tile1; ++tile, ++k) {
-        if ((k & 1) != static_cast<uint32_t>(group)) continue;
-        const int64_t s = static_cast<int64_t>(tile) * kTile + quarter * 32 + lane;
+      const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
+      auto entry = [&](int tile) -> int64_t { return static_cast<int64_t>(tile) * kTile + quarter * 32 + lane; };
+      auto page_at = [&](int tile) -> int32_t {
+        const int64_t s = entry(tile);
+        return tile < r.tile1 && s < p.a.width ? table[static_cast<int32_t>(s) / p.a.page_size] : -1;
+      };
+      const int mine = r.tile0 + static_cast<int>((k ^ group) & 1);  // this group's tiles: every other one
+      int32_t next = page_at(mine);
+      const uint32_t k0 = k;
+      k += mine - r.tile0;
+      for (int tile = mine; tile < r.tile1; tile += 2, k += 2) {
+        const int64_t s = entry(tile);
+        const int32_t page = next;
+        next = page_at(tile + 2);
+        const bool absent = page < 0 || page >= p.a.num_pages;
         float scale = 1.0f;
-        bool absent = true;
-        if (s < p.a.width) {
-          const int32_t s32 = static_cast<int32_t>(s), pg = s32 / p.a.page_size;
-          const int32_t page = p.a.page_table[r.b * p.a.table_stride + pg];
-          absent = page < 0 || page >= p.a.num_pages;
-          if (!absent && p.a.key_scales != nullptr)
-            scale = p.a.key_scales[static_cast<int64_t>(page) * p.a.page_size + (s32 - pg * p.a.page_size)];
-        }
+        if (!absent && p.a.key_scales != nullptr)
+          scale = p.a.key_scales[static_cast<int64_t>(page) * p.a.page_size + static_cast<int32_t>(s) % p.a.page_size];
         ok = wait_or_stop(&sh.t_full[group], (k >> 1) & 1, stop);
         if (!ok) break;
         tc_fence_after();
@@ -313,6 +371,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
             out[t * p.a.out_token_stride + s] = absent ? __int_as_float(0xff800000) : sum * scale;
         }
       }
+      k = k0 + (r.tile1 - r.tile0);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_empty[buf]);
     }
@@ -335,13 +394,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
   }
 }
 
-template <typename E, int STAGES, int STEP>
-topk_status launch_variant(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
+template <typename E, int STAGES, int STEP, bool BOXES>
+topk_status launch_variant(const ScoreParams& p, int sm_count, cudaStream_t stream) {
   static_assert(sizeof(ScoreShared) <= 3072, "barriers and weights");
   const size_t bytes = 2 * static_cast<size_t>(p.cols) * 128 * p.blocks + STAGES * static_cast<size_t>(kTile) * 128 * p.blocks +
                        sizeof(ScoreShared);
-  (void)dev;
-  auto kernel = scores_kernel<E, STAGES, STEP>;
+  auto kernel = scores_kernel<E, STAGES, STEP, BOXES>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
     return TOPK_ECUDA;
   const int64_t grid = p.units < sm_count ? p.units : sm_count;
@@ -349,16 +407,22 @@ topk_status launch_variant(const ScoreParams& p, int dev, int sm_count, cudaStre
   return cudaGetLastError() == cudaSuccess ? TOPK_OK : TOPK_ECUDA;
 }
 
+template <typename E, int STAGES, int STEP>
+topk_status launch_step(const ScoreParams& p, int sm_count, cudaStream_t stream) {
+  return p.box_rows > 0 ? launch_variant<E, STAGES, STEP, true>(p, sm_count, stream)
+                        : launch_variant<E, STAGES, STEP, false>(p, sm_count, stream);
+}
+
 template <typename E, int STEP>
-topk_status launch_step(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
+topk_status launch_ring(const ScoreParams& p, int sm_count, cudaStream_t stream) {
   // The ring gets what the queries leave of 227 KB: 6, 5 or 3 tiles.
-  if (p.cols <= 64) return launch_variant<E, 6, STEP>(p, dev, sm_count, stream);
-  if (p.cols <= 128) return launch_variant<E, 5, STEP>(p, dev, sm_count, stream);
-  return launch_variant<E, 3, STEP>(p, dev, sm_count, stream);
+  if (p.cols <= 64) return launch_step<E, 6, STEP>(p, sm_count, stream);
+  if (p.cols <= 128) return launch_step<E, 5, STEP>(p, sm_count, stream);
+  return launch_step<E, 3, STEP>(p, sm_count, stream);
 }
 
 template <typename E>
-topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream) {
+topk_status launch_typed(const sparse_scores_args& a, int sm_count, cudaStream_t stream) {
   ScoreParams p = {};
   p.a = a;
   const int size = sizeof(E);
@@ -379,16 +443,23 @@ topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cud
   p.units = static_cast<int64_t>(p.chunks) * p.groups * a.B;
   p.q_vector = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_seq_stride * size % 16 == 0 &&
                a.q_token_stride * size % 16 == 0 && a.q_head_stride * size % 16 == 0;
-  return p.hp % 32 == 0 ? launch_step<E, 32>(p, dev, sm_count, stream) : launch_step<E, 16>(p, dev, sm_count, stream);
+  // Boxes hold entries of one page: the largest power of two that divides the
+  // page, where it is at least 8, the rows of a swizzle group.
+  int rows = a.page_size & -a.page_size;
+  rows = rows < kTile ? rows : kTile;
+  const bool boxes = rows >= 8 && paged_map(&p.map, Kind<E>::map_type, size, a.keys, a.D, a.page_size, a.num_pages,
+                                            a.key_token_stride, a.key_page_stride, rows);
+  p.box_rows = boxes ? rows : 0;
+  return p.hp % 32 == 0 ? launch_ring<E, 32>(p, sm_count, stream) : launch_ring<E, 16>(p, sm_count, stream);
 }
 
 }  // namespace
 
-topk_status launch_scores(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream) {
+topk_status launch_scores(const sparse_scores_args& a, int sm_count, cudaStream_t stream) {
   switch (a.type) {
-    case SPARSE_BF16: return launch_typed<__nv_bfloat16>(a, dev, sm_count, stream);
-    case SPARSE_FP16: return launch_typed<__half>(a, dev, sm_count, stream);
-    default: return launch_typed<__nv_fp8_e4m3>(a, dev, sm_count, stream);
+    case SPARSE_BF16: return launch_typed<__nv_bfloat16>(a, sm_count, stream);
+    case SPARSE_FP16: return launch_typed<__half>(a, sm_count, stream);
+    default: return launch_typed<__nv_fp8_e4m3>(a, sm_count, stream);
   }
 }
 

@@ -7,6 +7,8 @@
 // 1024 bytes, the 16-byte unit j of row r stored at unit j ^ (r & 7).
 #pragma once
 
+#include <cuda.h>
+
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -147,10 +149,25 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
+// One arrival on `bar` when every copy16 of this thread so far is complete;
+// it counts against the arrivals the barrier was initialised with.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One box of a three-dimensional tensor map into shared memory; its bytes,
+// also those outside the tensor, which arrive as zeros, count on `bar`.
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
 }
 
 // Byte offset of the 16-byte unit `unit` of row `row` within a 128-byte wide
