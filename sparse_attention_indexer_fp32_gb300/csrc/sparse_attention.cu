@@ -1,6 +1,28 @@
 // Attention over the selected entries of a paged cache
-// (include/sparse_step.h, sparse_attention): the simple form, a warp per row
-// and head, one pass with the running maximum and sum.
+// (include/sparse_step.h, sparse_attention).
+//
+// One pass over the selected entries, 64 at a time, with the running maximum
+// and sum of a softmax: S = Q K^T and O += P V on the tensor cores, with the
+// query heads that share a key head as the 128 rows (TMEM lanes) of both, S, P
+// and O in TMEM, and one thread per row between them.
+//
+// Rows. Groups of up to 32 (64) heads leave 128 rows mostly empty, so they
+// are laid out in 4 (2) copies, and copy i of a row takes every tile's i-th
+// part of 64 / copies entries, with zero weights elsewhere: the copies' warps
+// share the exponentials, and their sums are joined at the end like those of
+// CTAs that share a row. The products cost the same either way.
+//
+// Rescaling. Each row keeps a reference r for its weights 2^(z - r) and moves
+// it only when the maximum has grown past r + 8, so that O in TMEM is rarely
+// touched; weights are then at most 2^8, which both types hold.
+//
+// Few rows. The tiles of a row are dealt over a cluster of up to 8 CTAs,
+// which join their sums through distributed shared memory: one launch, no
+// workspace, the same order on every call.
+//
+// Warps 0-3: softmax, one row per thread; 4-7: gather entries through the page
+// table into a ring with 16-byte asynchronous copies, zeros for what is not
+// seen; 8: one thread issues the products.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -8,63 +30,480 @@
 #include <cstdint>
 
 #include "step_launch.cuh"
+#include "tcgen05.cuh"
 
 namespace tki {
 namespace {
 
+constexpr int kKeys = 64;  // entries per tile
+constexpr int kAttThreads = 9 * 32;
+constexpr int kMaxStages = 6;
+constexpr float kGrowth = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct AttParams {
+  sparse_attention_args a;
+  int32_t heads;      // query heads per key head
+  int32_t m_tiles;    // tiles of 128 rows per key head
+  int32_t d_blocks, v_blocks;  // 128-byte blocks of an entry's keys and values
+  int32_t shared;     // v is a prefix of k's entries
+  int32_t stages;
+  int32_t stage_bytes, ring_at;  // bytes; the ring begins after Q
+  int32_t shared_at;  // AttShared
+  int32_t tmem_cols;
+  bool q_vector;
+};
+
+struct AttShared {
+  float away[kMaxStages][kKeys];     // position - query's, per entry of a stage
+  uint16_t seen[kMaxStages][4];      // bit per entry
+  float top[128], sum[128];          // of the rows, for joining
+  uint64_t full[kMaxStages], empty[kMaxStages], q_full, s_full[2], p_full[2], pv_done;
+  uint32_t tmem;
+  uint32_t stop;
+};
+
 template <typename E>
-__global__ void __launch_bounds__(32) attention_kernel(const sparse_attention_args a) {
-  const int64_t row = blockIdx.x / a.Hq;
-  const int h = static_cast<int>(blockIdx.x % a.Hq), g = h / (a.Hq / a.Hkv), lane = threadIdx.x;
-  const int64_t b = row / a.T, t = row % a.T;
-  const E* q = static_cast<const E*>(a.q) + b * a.q_seq_stride + t * a.q_token_stride + h * a.q_head_stride;
-  constexpr int kPer = SPARSE_ATTENTION_MAX_D / 32;
-  float o[kPer] = {};
-  float m = __int_as_float(0xff800000), l = 0.0f;
-  const int64_t qpos = a.query_positions != nullptr ? a.query_positions[row] : INT32_MAX;
-  const int64_t first = a.first != nullptr ? a.first[row] : 0;
-  for (int j = 0; j < a.K; ++j) {
-    const int64_t pos = a.indices[row * a.K + j];
-    if (pos < 0 || pos < first || pos > qpos || a.page_size == 0) continue;
-    int64_t page = pos / a.page_size;
-    const int64_t place = pos % a.page_size;
-    if (a.page_table != nullptr) {
-      if (page >= a.table_width) continue;
-      page = a.page_table[b * a.table_stride + page];
-    }
-    if (page < 0 || page >= a.num_pages) continue;
-    const E* k = static_cast<const E*>(a.k) + page * a.k_page_stride + place * a.k_token_stride + g * a.k_head_stride;
-    const E* v = static_cast<const E*>(a.v) + page * a.v_page_stride + place * a.v_token_stride + g * a.v_head_stride;
-    float z = 0.0f;
-    for (int d = lane; d < a.D; d += 32) z += static_cast<float>(q[d]) * static_cast<float>(k[d]);
-    for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-    z *= a.scale;
-    if (a.softcap > 0.0f) z = a.softcap * tanhf(z / a.softcap);
-    if (a.slopes != nullptr) z += a.slopes[h] * static_cast<float>(pos - qpos);
-    const float top = fmaxf(m, z);
-    const float base = top == __int_as_float(0xff800000) ? 0.0f : top;
-    const float old = expf(m - base), p = expf(z - base);
-    m = top;
-    l = l * old + p;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < a.Dv) o[i] = o[i] * old + p * static_cast<float>(v[lane + 32 * i]);
+struct Pack;
+template <>
+struct Pack<__nv_bfloat16> {
+  static constexpr uint32_t type = 1;
+  static __device__ __forceinline__ uint32_t two(float x, float y) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
   }
-  E* out = static_cast<E*>(a.out) + (row * a.Hq + h) * a.Dv;
+};
+template <>
+struct Pack<__half> {
+  static constexpr uint32_t type = 0;
+  static __device__ __forceinline__ uint32_t two(float x, float y) {
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// c tanh(x / c) = c - 2 c / (1 + e^(2 x / c)), good to a few 2^-24 of c.
+__device__ __forceinline__ float capped(float x, float cap, float two_log2e_over_cap) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_fast(x * two_log2e_over_cap)));
+  return cap - 2.0f * cap * r;
+}
+
+__device__ __forceinline__ bool is_low(float x) { return x == __int_as_float(0xff800000); }
+
+__device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
+  const uint4 v = ld_dsmem_v4(addr);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+
+template <typename E, int COPIES>
+__global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
+    attention_kernel(const __grid_constant__ AttParams p, const int cluster) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  constexpr int kPart = kKeys / COPIES;             // entries of a tile that a row's copy takes
+  constexpr int kStep = kPart < 32 ? kPart : 32;    // columns per TMEM load
+  constexpr int kRows = 128 / COPIES;               // rows of one copy
+  AttShared& sh = *reinterpret_cast<AttShared*>(smem + p.shared_at);
+  const sparse_attention_args& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster > 1 ? cluster_ctarank() : 0;
+  const int64_t work = blockIdx.x / cluster;
+  const int m_tile = static_cast<int>(work % p.m_tiles);
+  const int g = static_cast<int>(work / p.m_tiles % a.Hkv);
+  const int64_t row = work / p.m_tiles / a.Hkv;
+  const int64_t b = row / a.T, t = row - b * a.T;
+  const int heads = min(p.heads - m_tile * 128, 128);  // real rows of this tile
+  const int head0 = g * p.heads + m_tile * 128;
+  const int all_tiles = (a.K + kKeys - 1) / kKeys;
+  const int tiles = all_tiles > static_cast<int>(rank) ? (all_tiles - static_cast<int>(rank) + cluster - 1) / cluster : 0;
+  const uint32_t base = smem_addr(smem);
+  const uint32_t ring = base + p.ring_at;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) mbar_init(&sh.full[i], 128 + 4), mbar_init(&sh.empty[i], 1);
+    mbar_init(&sh.q_full, 256);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 128);
+    mbar_init(&sh.pv_done, 1);
+    sh.stop = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(&sh.tmem, p.tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem, tmem_o = tmem + 2 * kKeys;
+  volatile uint32_t* stop = &sh.stop;
+  const void* nowhere = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(a.q) & ~static_cast<uintptr_t>(15));
+
+  float top = __int_as_float(0xff800000), sum = 0.0f;  // of this thread's row (its reference and sum of weights)
+
+  if (warp >= 4 && warp < 8) {
+    // ---- gather ----
+    const int w = warp - 4;
+    const int32_t* indices = a.indices + row * a.K;
+    const int32_t* table = a.page_table != nullptr ? a.page_table + b * a.table_stride : nullptr;
+    const int32_t last = a.query_positions != nullptr ? a.query_positions[row] : INT32_MAX;
+    const int32_t first = a.first != nullptr ? max(a.first[row], 0) : 0;
+    const bool some = a.page_size > 0 && a.num_pages > 0;
+    // Lane i < 16 looks up entry 16 w + i of a tile: its index two tiles
+    // ahead, its page id one tile ahead.
+    auto index_of = [&](int i) -> int32_t {
+      const int64_t j = (static_cast<int64_t>(i) * cluster + rank) * kKeys + w * 16 + lane;
+      return lane < 16 && i < tiles && j < a.K && some ? indices[j] : -1;
+    };
+    auto page_of = [&](int32_t pos) -> int32_t {
+      if (pos < first || pos > last) return -1;
+      const int32_t page = pos / a.page_size;
+      return table == nullptr ? page : page < a.table_width ? table[page] : -1;
+    };
+    int32_t pos = index_of(0), pos1 = index_of(1);
+    int32_t page = page_of(pos);
+    bool ok = true;
+    for (int i = 0; i < tiles; ++i) {
+      const int32_t pos2 = index_of(i + 2);
+      const int32_t page1 = page_of(pos1);
+      const int stage = i % p.stages;
+      ok = wait_or_stop(&sh.empty[stage], ((i / p.stages) & 1) ^ 1, stop);
+      if (!ok) break;
+      const bool seen = page >= 0 && page < a.num_pages;
+      const int32_t place = seen ? pos % a.page_size : 0;
+      const int64_t k_at = seen ? page * a.k_page_stride + place * a.k_token_stride + g * a.k_head_stride : -1;
+      const int64_t v_at = seen ? page * a.v_page_stride + place * a.v_token_stride + g * a.v_head_stride : -1;
+      const uint32_t bits = __ballot_sync(0xffffffffu, seen);
+      if (lane < 16) sh.away[stage][w * 16 + lane] = static_cast<float>(seen ? pos - last : 0);
+      if (lane == 0) sh.seen[stage][w] = static_cast<uint16_t>(bits);
+      const uint32_t dst = ring + stage * p.stage_bytes;
+      const uint32_t unit16 = lane & 7;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (lane + 32 * i < a.Dv) out[lane + 32 * i] = static_cast<E>(l == 0.0f ? 0.0f : o[i] / l);
-  if (a.lse != nullptr && lane == 0) a.lse[row * a.Hq + h] = l == 0.0f ? __int_as_float(0xff800000) : logf(l) + m;
+      for (int j = 0; j < 4; ++j) {
+        const int r = 4 * j + (lane >> 3);
+        const int64_t ks = __shfl_sync(0xffffffffu, k_at, r), vs = __shfl_sync(0xffffffffu, v_at, r);
+        const uint32_t at = swizzled(w * 16 + r, unit16);
+        for (int c = 0; c < p.d_blocks; ++c) {
+          const bool real = ks >= 0 && static_cast<int>(c * 8 + unit16) * 8 < a.D;
+          copy16(dst + c * kKeys * 128 + at, real ? static_cast<const E*>(a.k) + ks + (c * 8 + unit16) * 8 : nowhere, real);
+        }
+        if (!p.shared)
+          for (int c = 0; c < p.v_blocks; ++c) {
+            const bool real = vs >= 0 && static_cast<int>(c * 8 + unit16) * 8 < a.Dv;
+            copy16(dst + (p.d_blocks + c) * kKeys * 128 + at,
+                   real ? static_cast<const E*>(a.v) + vs + (c * 8 + unit16) * 8 : nowhere, real);
+          }
+      }
+      copy_arrive(&sh.full[stage]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.full[stage]);  // seen, away
+      pos = pos1, pos1 = pos2, page = page1;
+    }
+    copy_commit();
+    copy_wait<0>();
+  } else if (warp == 8) {
+    // ---- products ----
+    const uint32_t desc_s = mma_desc(Pack<E>::type, kKeys);
+    const uint32_t desc_o = mma_desc(Pack<E>::type, (a.Dv + 15) / 16 * 16, true);
+    const int d_steps = (a.D + 15) / 16;
+    auto scores = [&](int i) -> bool {
+      if (!wait_or_stop(&sh.full[i % p.stages], (i / p.stages) & 1, stop)) return false;
+      fence_proxy_async_smem();
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t kb = ring + (i % p.stages) * p.stage_bytes;
+        for (int j = 0; j < d_steps; ++j)
+          mma_f16(tmem + (i & 1) * kKeys, operand_desc(base + (j >> 2) * 128 * 128 + (j & 3) * 32),
+                  operand_desc(kb + (j >> 2) * kKeys * 128 + (j & 3) * 32), desc_s, j > 0);
+        mma_commit(&sh.s_full[i & 1]);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = tiles > 0 && wait_or_stop(&sh.q_full, 0, stop) && scores(0);
+    for (int i = 0; i < tiles && ok; ++i) {
+      // the next scores go where the weights of tile i - 1 were
+      if (i + 1 < tiles) ok = (i == 0 || wait_or_stop(&sh.pv_done, (i - 1) & 1, stop)) && scores(i + 1);
+      ok = ok && wait_or_stop(&sh.p_full[i & 1], (i >> 1) & 1, stop);
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t vb = ring + (i % p.stages) * p.stage_bytes + (p.shared ? 0 : p.d_blocks * kKeys * 128);
+        for (int j = 0; j < kKeys / 16; ++j)
+          mma_f16_ts(tmem_o, tmem + (i & 1) * kKeys + j * 8, operand_desc(vb + j * 16 * 128, kKeys * 128), desc_o,
+                     i + j > 0);
+        mma_commit(&sh.empty[i % p.stages]);
+        mma_commit(&sh.pv_done);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---- softmax ----
+    const int copy = threadIdx.x / kRows;
+    {  // queries first
+      const int units = p.d_blocks * 8;
+      const E* q = static_cast<const E*>(a.q) + b * a.q_seq_stride + t * a.q_token_stride + head0 * a.q_head_stride;
+      for (int i = threadIdx.x; i < 128 * units; i += 128) {
+        const int r = i / units, j = i - r * units, h = r % kRows;
+        const bool real = h < heads && j * 8 < a.D;
+        const E* src = real ? q + h * a.q_head_stride + j * 8 : nullptr;
+        const uint32_t at = (j >> 3) * 128 * 128 + swizzled(r, j & 7);
+        if (p.q_vector) {
+          copy16(base + at, real ? src : nowhere, real);
+        } else {
+          E v[8];
+          for (int e = 0; e < 8; ++e) v[e] = real ? src[e] : E(0.0f);
+          *reinterpret_cast<uint4*>(smem + at) = *reinterpret_cast<const uint4*>(v);
+        }
+      }
+      copy_arrive(&sh.q_full);
+      mbar_arrive(&sh.q_full);
+    }
+    const int h = threadIdx.x % kRows;
+    const float slope = a.slopes != nullptr && h < heads ? a.slopes[head0 + h] * kLog2e : 0.0f;
+    const float cap_in = a.softcap > 0.0f ? a.scale * 2.0f * kLog2e / a.softcap : 0.0f;
+    const float cap_out = a.softcap * kLog2e, scale = a.scale * kLog2e;
+    const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
+    for (int i = 0; i < tiles; ++i) {
+      const int stage = i % p.stages;
+      if (!wait_or_stop(&sh.full[stage], (i / p.stages) & 1, stop)) break;
+      if (!wait_or_stop(&sh.s_full[i & 1], (i >> 1) & 1, stop)) break;
+      tc_fence_after();
+      const uint32_t s_at = tmem + (i & 1) * kKeys + lanes;
+      float z[kPart];
+      float high = __int_as_float(0xff800000);
+#pragma unroll
+      for (int c = 0; c < kPart; c += kStep) {
+        uint32_t v[kStep];
+        tmem_ld(v, s_at + copy * kPart + c);
+        const int e0 = copy * kPart + c;
+        uint32_t bits = sh.seen[stage][e0 / 16];
+        if (kStep == 32) bits |= static_cast<uint32_t>(sh.seen[stage][e0 / 16 + 1]) << 16;
+        tmem_wait_ld(v);
+        if (a.softcap > 0.0f) {
+#pragma unroll
+          for (int j = 0; j < kStep; ++j) z[c + j] = capped(__uint_as_float(v[j]), cap_out, cap_in);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kStep; ++j) z[c + j] = __uint_as_float(v[j]) * scale;
+        }
+        if (a.slopes != nullptr) {
+#pragma unroll
+          for (int j = 0; j < kStep; ++j) z[c + j] += slope * sh.away[stage][e0 + j];
+        }
+        if (bits != (kStep == 32 ? 0xffffffffu : 0xffffu)) {
+#pragma unroll
+          for (int j = 0; j < kStep; ++j)
+            if (((bits >> j) & 1) == 0) z[c + j] = __int_as_float(0xff800000);
+        }
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) high = fmaxf(high, z[c + j]);
+      }
+      // move the reference where the maximum has outgrown it
+      if (__any_sync(0xffffffffu, high > top + kGrowth)) {
+        const float moved = fmaxf(top, high);
+        const float factor = is_low(moved) ? 1.0f : exp2_fast(top - moved);
+        top = moved;
+        sum *= factor;
+        if (i > 0) {
+          if (!wait_or_stop(&sh.pv_done, (i - 1) & 1, stop)) break;
+          tc_fence_after();
+          for (int c = 0; c < a.Dv; c += 16) {  // past Dv: columns that nothing reads, within the allocation
+            uint32_t v[16];
+            tmem_ld(v, tmem_o + lanes + c);
+            tmem_wait_ld(v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * factor);
+            tmem_st(tmem_o + lanes + c, v);
+          }
+        }
+      }
+      const float ref = is_low(top) ? 0.0f : top;
+      float part[4] = {};
+#pragma unroll
+      for (int j = 0; j < kPart; ++j) {
+        z[j] = exp2_fast(z[j] - ref);
+        part[j & 3] += z[j];
+      }
+      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      // the weights, over the scores: columns of the other copies' parts get zeros
+#pragma unroll
+      for (int c = 0; c < kKeys / 2; c += 16) {
+        uint32_t v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int e = 2 * (c + j);  // first entry of column c + j
+          if (COPIES == 1)
+            v[j] = Pack<E>::two(z[e % kPart], z[e % kPart + 1]);
+          else
+            v[j] = e / kPart == copy ? Pack<E>::two(z[e % kPart], z[e % kPart + 1]) : 0u;
+        }
+        tmem_st(s_at + c, v);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sh.p_full[i & 1]);
+    }
+    if (tiles > 0) wait_or_stop(&sh.pv_done, (tiles - 1) & 1, stop);
+    tc_fence_after();
+    const bool failed = *stop != 0;  // a wait ran out: the rows become NaN
+    sh.top[threadIdx.x] = failed ? 0.0f : top;
+    sh.sum[threadIdx.x] = failed ? __int_as_float(0x7fc00000) : sum;
+  }
+
+  // ---- join copies and CTAs ----
+  __syncthreads();
+  if (cluster > 1) cluster_sync();
+  const int pad = p.v_blocks * 64 + 4;  // floats per row of the joining buffer: rows 4 banks apart
+  float* rows = reinterpret_cast<float*>(smem);
+  const uint32_t top_addr = smem_addr(sh.top), sum_addr = smem_addr(sh.sum);
+  float lse = 0.0f;
+  if (warp < 4) {
+    const int h = threadIdx.x % kRows;
+    float all = __int_as_float(0xff800000), total = 0.0f;
+    for (int r = 0; r < cluster; ++r)
+      for (int c = 0; c < COPIES; ++c) {
+        const uint32_t at = 4 * (c * kRows + h);
+        const float m = cluster > 1 ? __uint_as_float(ld_dsmem_u32(map_rank(top_addr + at, r))) : sh.top[c * kRows + h];
+        all = fmaxf(all, m);
+      }
+    for (int r = 0; r < cluster; ++r)
+      for (int c = 0; c < COPIES; ++c) {
+        const uint32_t at = 4 * (c * kRows + h);
+        const float m = cluster > 1 ? __uint_as_float(ld_dsmem_u32(map_rank(top_addr + at, r))) : sh.top[c * kRows + h];
+        const float l = cluster > 1 ? __uint_as_float(ld_dsmem_u32(map_rank(sum_addr + at, r))) : sh.sum[c * kRows + h];
+        if (!is_low(m)) total += l * exp2_fast(m - all);
+        if (l != l) total = l;
+      }
+    const float weight = total != total ? total : is_low(top) ? 0.0f : exp2_fast(top - all) / total;
+    lse = is_low(all) ? all : (all + log2f(total)) * kLn2;
+    if (total != total) lse = total;
+    if (rank == 0 && a.lse != nullptr && threadIdx.x < heads && threadIdx.x < kRows)
+      a.lse[row * a.Hq + head0 + h] = lse;
+    const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
+    for (int c = 0; c < a.Dv; c += 16) {
+      uint32_t v[16];
+      if (tiles > 0) {
+        tmem_ld(v, tmem_o + lanes + c);
+        tmem_wait_ld(v);
+      }
+      float* dst = rows + threadIdx.x * pad + c;
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        float4 f;
+        f.x = weight == 0.0f ? 0.0f : __uint_as_float(v[j]) * weight;
+        f.y = weight == 0.0f ? 0.0f : __uint_as_float(v[j + 1]) * weight;
+        f.z = weight == 0.0f ? 0.0f : __uint_as_float(v[j + 2]) * weight;
+        f.w = weight == 0.0f ? 0.0f : __uint_as_float(v[j + 3]) * weight;
+        *reinterpret_cast<float4*>(dst + j) = f;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (cluster > 1) cluster_sync();
+  {
+    // Eight outputs per thread, the CTAs of a cluster in turn.
+    const int per_row = a.Dv / 8, items = heads * per_row;
+    E* out = static_cast<E*>(a.out) + (row * a.Hq + head0) * a.Dv;
+    const uint32_t rows_addr = smem_addr(rows);
+    for (int i = static_cast<int>(rank) * kAttThreads + threadIdx.x; i < items; i += cluster * kAttThreads) {
+      const int h = i / per_row, c = (i - h * per_row) * 8;
+      float4 x = {}, y = {};
+      for (int r = 0; r < cluster; ++r)
+#pragma unroll
+        for (int k = 0; k < COPIES; ++k) {
+          const int at = (k * kRows + h) * pad + c;
+          float4 u, v;
+          if (cluster > 1) {
+            const uint32_t from = map_rank(rows_addr + 4 * at, r);
+            u = ld_dsmem_f4(from), v = ld_dsmem_f4(from + 16);
+          } else {
+            u = *reinterpret_cast<const float4*>(rows + at), v = *reinterpret_cast<const float4*>(rows + at + 4);
+          }
+          x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
+          y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+        }
+      *reinterpret_cast<uint4*>(out + static_cast<int64_t>(h) * a.Dv + c) =
+          make_uint4(Pack<E>::two(x.x, x.y), Pack<E>::two(x.z, x.w), Pack<E>::two(y.x, y.y), Pack<E>::two(y.z, y.w));
+    }
+  }
+  if (cluster > 1) cluster_sync();  // the others may still read this CTA's rows
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_free(tmem, p.tmem_cols);
+  }
+}
+
+template <typename E, int COPIES>
+topk_status launch_copies(const AttParams& p, int cluster, int64_t grid, size_t bytes, cudaStream_t stream) {
+  auto kernel = attention_kernel<E, COPIES>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
+    return TOPK_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kAttThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, p, cluster);
+  return err == cudaSuccess ? TOPK_OK : TOPK_ECUDA;
+}
+
+template <typename E>
+topk_status launch_typed(const sparse_attention_args& a, int sm_count, cudaStream_t stream) {
+  AttParams p = {};
+  p.a = a;
+  p.heads = a.Hq / a.Hkv;
+  p.m_tiles = (p.heads + 127) / 128;
+  p.d_blocks = (a.D + 63) / 64;
+  p.v_blocks = (a.Dv + 63) / 64;
+  p.shared = a.k == a.v && a.Dv <= a.D && a.k_page_stride == a.v_page_stride && a.k_token_stride == a.v_token_stride &&
+             a.k_head_stride == a.v_head_stride;
+  p.q_vector = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_seq_stride % 8 == 0 && a.q_token_stride % 8 == 0 &&
+               a.q_head_stride % 8 == 0;
+  const int copies = p.heads <= 32 ? 4 : p.heads <= 64 ? 2 : 1;
+  // Shared memory: Q, then the ring; at the end the same bytes hold the rows
+  // to be joined. Two CTAs share an SM where two stages each fit (and TMEM
+  // holds both), else one CTA has as many stages as fit.
+  const int q_bytes = 128 * 128 * p.d_blocks;
+  p.ring_at = q_bytes;
+  p.stage_bytes = kKeys * 128 * (p.d_blocks + (p.shared ? 0 : p.v_blocks));
+  p.tmem_cols = 2 * kKeys + p.v_blocks * 64 <= 256 ? 256 : 512;
+  const int join = 128 * (p.v_blocks * 64 + 4) * 4;
+  const int half = (227 * 1024) / 2 - 1024 - static_cast<int>(sizeof(AttShared)), whole = 227 * 1024 - static_cast<int>(sizeof(AttShared));
+  const bool two = copies > 1 && p.tmem_cols == 256 && q_bytes + 2 * p.stage_bytes <= half && join <= half;
+  p.stages = ((two ? half : whole) - q_bytes) / p.stage_bytes;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  int operands = q_bytes + p.stages * p.stage_bytes;
+  if (operands < join) operands = (join + 15) / 16 * 16;
+  p.shared_at = operands;
+  const size_t bytes = static_cast<size_t>(operands) + sizeof(AttShared);
+  const int64_t work = static_cast<int64_t>(a.B) * a.T * a.Hkv * p.m_tiles;
+  // Few rows: share each over the CTAs that would idle, down to one tile each.
+  const int64_t slots = static_cast<int64_t>(sm_count) * (two ? 2 : 1);
+  const int tiles = (a.K + kKeys - 1) / kKeys;
+  int cluster = 1;
+  while (cluster < 8 && work * cluster * 2 <= slots && cluster * 2 <= tiles) cluster *= 2;
+  const int64_t grid = work * cluster;
+  if (grid > INT32_MAX) return TOPK_EINVAL;
+  if (copies == 4) return launch_copies<E, 4>(p, cluster, grid, bytes, stream);
+  if (copies == 2) return launch_copies<E, 2>(p, cluster, grid, bytes, stream);
+  return launch_copies<E, 1>(p, cluster, grid, bytes, stream);
 }
 
 }  // namespace
 
-topk_status launch_attention(const sparse_attention_args& a, int, int, cudaStream_t stream) {
-  const int64_t grid = static_cast<int64_t>(a.B) * a.T * a.Hq;
-  if (grid > INT32_MAX) return TOPK_EINVAL;
-  if (a.type == SPARSE_BF16) attention_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), 32, 0, stream>>>(a);
-  if (a.type == SPARSE_FP16) attention_kernel<__half><<<static_cast<unsigned>(grid), 32, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? TOPK_OK : TOPK_ECUDA;
+topk_status launch_attention(const sparse_attention_args& a, int sm_count, cudaStream_t stream) {
+  return a.type == SPARSE_BF16 ? launch_typed<__nv_bfloat16>(a, sm_count, stream)
+                               : launch_typed<__half>(a, sm_count, stream);
 }
 
 }  // namespace tki

@@ -13,6 +13,6 @@ topk_status current_device(int* dev, int* sm_count);
 
 topk_status launch_rotary(const sparse_rotary_args& a, int sm_count, cudaStream_t stream);
 topk_status launch_scores(const sparse_scores_args& a, int sm_count, cudaStream_t stream);
-topk_status launch_attention(const sparse_attention_args& a, int dev, int sm_count, cudaStream_t stream);
+topk_status launch_attention(const sparse_attention_args& a, int sm_count, cudaStream_t stream);
 
 }  // namespace tki
