@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional
 
 import torch
@@ -47,70 +48,101 @@ class _AttentionArgs(ctypes.Structure):
                 ("softcap", _f32)]
 
 
-_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
+_FORMATS = {_i32: "i", _i64: "q", _f32: "f", _vp: "P"}
+_BF16, _FP16, _FP32, _E4M3 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+_I32, _I64, _F64 = torch.int32, torch.int64, torch.float64
+_ROTARY_TYPES = {_BF16: 0, _FP16: 1, _FP32: 2}
+_SCORES_TYPES = {_BF16: 0, _FP16: 1, _E4M3: 3}
+_ATTENTION_TYPES = {_BF16: 0, _FP16: 1}
 _LAYOUTS = {"half": 0, "interleaved": 1}
-_functions = {}
 
 
-def _function(name: str, args):
-    """The library's entry point ``name``, its signature set on first use."""
-    fn = _functions.get(name)
-    if fn is None:
-        fn = getattr(_binding.load_library(), name)
-        fn.argtypes = [ctypes.POINTER(args), _vp]
-        fn.restype = ctypes.c_int
-        _functions[name] = fn
-    return fn
+class _Call:
+    """An entry point of the library. Its arguments are packed into the bytes
+    of its C struct in one step: setting the fields of a ctypes Structure one
+    by one costs several microseconds of host time a call."""
+
+    def __init__(self, name: str, args):
+        self.name, self.fn = name, None
+        self.pack = struct.Struct("@" + "".join(_FORMATS[t] for _, t in args._fields_) + "0q").pack
+
+    def __call__(self, index: int, stream, *values) -> None:
+        fn = self.fn
+        if fn is None:
+            lib = _binding.load_library()
+            prototype = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, _vp)
+            fn = self.fn = prototype(ctypes.cast(getattr(lib, self.name), _vp).value)
+        try:
+            packed = self.pack(*values)
+        except (struct.error, OverflowError) as error:
+            raise ValueError(f"{self.name}: an argument is out of range ({error})") from None
+        if torch.cuda.current_device() == index:
+            status = fn(packed, _binding._stream_handle(index, stream))
+        else:
+            with torch.cuda.device(index):
+                status = fn(packed, _binding._stream_handle(index, stream))
+        if status != 0:
+            message = _binding.load_library().topk_status_string(status).decode()
+            raise _binding.TopkError(status, f"{self.name} failed: {message}")
 
 
-def _call(name: str, args, index: int, stream) -> None:
-    fn = _function(name, type(args))
-    sh = _binding._stream_handle(index, stream)
-    status = _binding._on_device(index, lambda: fn(ctypes.byref(args), sh))
-    if status != _binding.Status.OK:
-        message = _binding.load_library().topk_status_string(status).decode()
-        raise _binding.TopkError(status, f"{name} failed: {message}")
+_rotary, _scores, _attention = (_Call("sparse_rotary", _RotaryArgs), _Call("sparse_indexer_scores", _ScoresArgs),
+                                _Call("sparse_attention", _AttentionArgs))
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _tensor(t, name: str, dims: int, dtypes, device=None) -> None:
+def _main(t, name: str, dims: int, types):
+    """Shape, strides, type code and device of a call's main tensor."""
     if not isinstance(t, torch.Tensor) or t.dim() != dims:
         raise ValueError(f"{name} must be a {dims}-D tensor")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the other arguments")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
-
-
-def _unit_inner(t: torch.Tensor, name: str) -> None:
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    code = types.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in types)}, not {t.dtype}")
+    shape, strides = t.shape, t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
+    return shape, strides, code, index
 
 
-def _exact(t, name: str, shape, dtypes, device) -> None:
-    """A contiguous tensor of exactly this shape."""
-    _tensor(t, name, len(shape), dtypes, device)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {list(shape)}")
+def _other(t, name: str, dims: int, dtype, index: int):
+    """Shape and strides of a further tensor of this type on that device."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-D tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the other arguments")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    shape, strides = t.shape, t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return shape, strides
 
 
-def _span(t: torch.Tensor):
-    """The bytes [start, end) that the elements of ``t`` lie within."""
-    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else -1
-    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+def _whole(t, name: str, shape, dtype, index: int) -> int:
+    """The address of a contiguous tensor of exactly this shape and type."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.get_device() != index \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on the device of the "
+                         "other arguments")
+    return t.data_ptr()
 
 
-def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
-    (a0, a1), (b0, b1) = _span(a), _span(b)
-    return a0 < b1 and b0 < a1
+def _span(address: int, shape, strides, size: int):
+    """The bytes [start, end) that the elements of a tensor lie within."""
+    if 0 in shape:
+        return address, address
+    return address, address + (sum((n - 1) * s for n, s in zip(shape, strides)) + 1) * size
 
 
-def _no_self_overlap(t: torch.Tensor, name: str) -> None:
-    """An output may not be a broadcast: two of its elements at one address."""
-    if any(s == 0 and n > 1 for n, s in zip(t.shape, t.stride())):
+def _overlap(a, b) -> bool:
+    return a[0] < b[1] and b[0] < a[1]
+
+
+def _no_broadcast(shape, strides, name: str) -> None:
+    """An output may not have two of its elements at one address."""
+    if 0 in strides and any(s == 0 and n > 1 for n, s in zip(shape, strides)):
         raise ValueError(f"{name} must not be a broadcast tensor")
 
 
@@ -171,45 +203,43 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
     of the call with the same arguments. ``out`` may be ``x`` (in place). With ``slots`` (int32
     ``[T]``), ``out`` is a paged cache ``[pages, page_size, H, D]`` and token ``t`` is written at slot
     ``slots[t]`` (negative or past the cache: not written). Returns ``out``."""
-    _tensor(x, "x", 3, (torch.bfloat16, torch.float16, torch.float32))
-    _unit_inner(x, "x")
-    T, H, D = x.shape
-    _exact(positions, "positions", (T,), (torch.int32, torch.int64), x.device)
-    _tensor(frequencies, "frequencies", 1, (torch.float64,), x.device)
-    if not frequencies.is_contiguous():
-        raise ValueError("frequencies must be contiguous")
+    shape, xs, code, index = _main(x, "x", 3, _ROTARY_TYPES)
+    T, H, D = shape
+    dtype = x.dtype
+    wide = isinstance(positions, torch.Tensor) and positions.dtype == _I64
+    pos = _whole(positions, "positions", (T,), _I64 if wide else _I32, index)
+    pairs = frequencies.numel() if isinstance(frequencies, torch.Tensor) else 0
+    freq = _whole(frequencies, "frequencies", (pairs,), _F64, index)
     if layout not in _LAYOUTS:
         raise ValueError("layout must be 'half' or 'interleaved'")
     if not math.isfinite(scale):
         raise ValueError("scale must be finite")
-    a = _RotaryArgs()
-    if slots is None:
-        if out is None:
-            out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-        _tensor(out, "out", 3, (x.dtype,), x.device)
-        if out.shape != x.shape:
-            raise ValueError("out must have the shape of x")
-    else:
+    to, pages, page_size, page_stride = 0, 0, 0, 0
+    address = x.data_ptr()
+    if slots is not None:
         if out is None:
             raise ValueError("slots need the cache as out")
-        _tensor(out, "out", 4, (x.dtype,), x.device)
-        if tuple(out.shape[2:]) != (H, D):
+        os, ot = _other(out, "out", 4, dtype, index)
+        if os[2:] != (H, D):
             raise ValueError("out must be a cache [pages, page_size, H, D]")
-        _exact(slots, "slots", (T,), (torch.int32,), x.device)
-        a.slots, a.num_pages, a.page_size = slots.data_ptr(), out.shape[0], out.shape[1]
-        a.out_page_stride = out.stride(0)
-    _unit_inner(out, "out")
-    _no_self_overlap(out, "out")
-    same = slots is None and out.data_ptr() == x.data_ptr() and out.stride() == x.stride()
-    if not same and _overlap(x, out):
-        raise ValueError("out must be x itself or not overlap it")
-    a.x, a.x_token_stride, a.x_head_stride = x.data_ptr(), x.stride(0), x.stride(1)
-    a.out, a.out_token_stride, a.out_head_stride = out.data_ptr(), out.stride(-3), out.stride(-2)
-    a.positions, a.positions_64 = positions.data_ptr(), int(positions.dtype == torch.int64)
-    a.frequencies, a.rotated, a.offset = frequencies.data_ptr(), 2 * frequencies.numel(), int(offset)
-    a.T, a.H, a.D, a.layout, a.type = T, H, D, _LAYOUTS[layout], _TYPES[x.dtype]
-    a.inverse, a.scale = int(bool(inverse)), float(scale)
-    _call("sparse_rotary", a, x.get_device(), stream)
+        to = _whole(slots, "slots", (T,), _I32, index)
+        pages, page_size, page_stride = os[0], os[1], ot[0]
+    elif out is not None:
+        os, ot = _other(out, "out", 3, dtype, index)
+        if os != shape:
+            raise ValueError("out must have the shape of x")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+        target, ot = out.data_ptr(), out.stride()
+    else:
+        target = out.data_ptr()
+        _no_broadcast(os, ot, "out")
+        if slots is not None or target != address or ot != xs:
+            size = 4 if code == 2 else 2
+            if _overlap(_span(address, shape, xs, size), _span(target, os, ot, size)):
+                raise ValueError("out must be x itself or not overlap it")
+    _rotary(index, stream, address, xs[0], xs[1], target, page_stride, ot[-3], ot[-2], pos, freq, to, pages, page_size,
+            T, H, D, 2 * pairs, int(offset), _LAYOUTS[layout], code, wide, bool(inverse), scale)
     return out
 
 
@@ -228,43 +258,32 @@ def indexer_scores(q: torch.Tensor, weights: torch.Tensor, keys: torch.Tensor, l
     ``page_table`` int32 ``[B, n]`` (rows may be a broadcast). ``out`` float32 ``[B, T, width]``
     (default width: ``n * page_size``); ``out.view(B * T, width)`` is what :func:`topk_ragged`
     takes."""
-    types = (torch.bfloat16, torch.float16, torch.float8_e4m3fn)
-    _tensor(q, "q", 4, types)
-    _unit_inner(q, "q")
-    B, T, H, D = q.shape
-    _exact(weights, "weights", (B, T, H), (torch.float32,), q.device)
-    _tensor(keys, "keys", 3, (q.dtype,), q.device)
-    _unit_inner(keys, "keys")
-    if keys.shape[2] != D:
+    shape, qs, code, index = _main(q, "q", 4, _SCORES_TYPES)
+    B, T, H, D = shape
+    w = _whole(weights, "weights", (B, T, H), _FP32, index)
+    ks, kt = _other(keys, "keys", 3, q.dtype, index)
+    pages, page_size, entry = ks
+    if entry != D:
         raise ValueError("keys must have the head size of q")
-    pages, page_size = keys.shape[:2]
-    _exact(lengths, "lengths", (B, T), (torch.int32,), q.device)
-    _tensor(page_table, "page_table", 2, (torch.int32,), q.device)
-    _unit_inner(page_table, "page_table")
-    if page_table.shape[0] != B:
+    n = _whole(lengths, "lengths", (B, T), _I32, index)
+    ps, pt = _other(page_table, "page_table", 2, _I32, index)
+    if ps[0] != B:
         raise ValueError("page_table must have one row for each sequence")
-    if key_scales is not None:
-        _exact(key_scales, "key_scales", (pages, page_size), (torch.float32,), q.device)
+    scales = 0 if key_scales is None else _whole(key_scales, "key_scales", (pages, page_size), _FP32, index)
     if out is None:
-        width = page_table.shape[1] * page_size if width is None else int(width)
-        out = torch.empty((B, T, width), dtype=torch.float32, device=q.device)
+        width = ps[1] * page_size if width is None else int(width)
+        out = torch.empty((B, T, width), dtype=_FP32, device=q.device)
+        ot = out.stride()
     else:
-        _tensor(out, "out", 3, (torch.float32,), q.device)
-        if tuple(out.shape[:2]) != (B, T) or (width is not None and out.shape[2] != width):
+        os, ot = _other(out, "out", 3, _FP32, index)
+        if os[:2] != (B, T) or (width is not None and os[2] != width):
             raise ValueError("out must be a tensor [B, T, width]")
-        width = out.shape[2]
-    _unit_inner(out, "out")
-    _no_self_overlap(out, "out")
-    if width > page_table.shape[1] * page_size:
+        width = os[2]
+        _no_broadcast(os, ot, "out")
+    if width > ps[1] * page_size:
         raise ValueError("page_table is too narrow for the width of out")
-    a = _ScoresArgs(q=q.data_ptr(), q_seq_stride=q.stride(0), q_token_stride=q.stride(1),
-                    q_head_stride=q.stride(2), weights=weights.data_ptr(), keys=keys.data_ptr(),
-                    key_page_stride=keys.stride(0), key_token_stride=keys.stride(1),
-                    key_scales=_ptr(key_scales), lengths=lengths.data_ptr(), page_table=page_table.data_ptr(),
-                    table_stride=page_table.stride(0), table_width=page_table.shape[1], out=out.data_ptr(),
-                    out_seq_stride=out.stride(0), out_token_stride=out.stride(1), num_pages=pages,
-                    width=width, page_size=page_size, B=B, T=T, H=H, D=D, type=_TYPES[q.dtype])
-    _call("sparse_indexer_scores", a, q.get_device(), stream)
+    _scores(index, stream, q.data_ptr(), qs[0], qs[1], qs[2], w, keys.data_ptr(), kt[0], kt[1], scales, n,
+            page_table.data_ptr(), pt[0], ps[1], out.data_ptr(), ot[0], ot[1], pages, width, page_size, B, T, H, D, code)
     return out
 
 
@@ -288,55 +307,47 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
     int32 ``[B, T]`` earlier ones (a document's start). Returns ``out`` ``[B, T, Hq, Dv]``, with
     ``return_lse`` also the logarithm of the softmax's sum, float32 ``[B, T, Hq]``; a row that sees
     nothing has 0 and ``-inf``."""
-    _tensor(q, "q", 4, (torch.bfloat16, torch.float16))
-    _unit_inner(q, "q")
-    B, T, Hq, D = q.shape
-    _tensor(k, "k", 4, (q.dtype,), q.device)
-    _tensor(v, "v", 4, (q.dtype,), q.device)
-    _unit_inner(k, "k")
-    _unit_inner(v, "v")
-    pages, page_size, Hkv = k.shape[:3]
-    Dv = v.shape[3]
-    if k.shape[3] != D or v.shape[:3] != k.shape[:3]:
+    shape, qs, code, index = _main(q, "q", 4, _ATTENTION_TYPES)
+    B, T, Hq, D = shape
+    dtype = q.dtype
+    ks, kt = _other(k, "k", 4, dtype, index)
+    vs, vt = _other(v, "v", 4, dtype, index)
+    pages, page_size, Hkv = ks[:3]
+    Dv = vs[3]
+    if ks[3] != D or vs[:3] != ks[:3]:
         raise ValueError("k must be [pages, page_size, Hkv, D] and v [pages, page_size, Hkv, Dv]")
     if Hkv < 1 or Hq % Hkv:
         raise ValueError("the query heads must be a multiple of the key heads")
-    _tensor(indices, "indices", 3, (torch.int32,), q.device)
-    _exact(indices, "indices", (B, T, indices.shape[2]), (torch.int32,), q.device)
+    K = indices.shape[-1] if isinstance(indices, torch.Tensor) and indices.dim() else 0
+    idx = _whole(indices, "indices", (B, T, K), _I32, index)
+    table, pt, width = 0, 0, 0
     if page_table is not None:
-        _tensor(page_table, "page_table", 2, (torch.int32,), q.device)
-        _unit_inner(page_table, "page_table")
-        if page_table.shape[0] != B:
+        ps, strides = _other(page_table, "page_table", 2, _I32, index)
+        if ps[0] != B:
             raise ValueError("page_table must have one row for each sequence")
+        table, pt, width = page_table.data_ptr(), strides[0], ps[1]
     elif query_positions is not None or first is not None or slopes is not None:
         raise ValueError("slots have no position: query_positions, first and slopes need a page_table")
-    if slopes is not None:
-        _exact(slopes, "slopes", (Hq,), (torch.float32,), q.device)
-        if query_positions is None:
-            raise ValueError("slopes need query_positions")
-    for t, name in ((query_positions, "query_positions"), (first, "first")):
-        if t is not None:
-            _exact(t, name, (B, T), (torch.int32,), q.device)
+    if slopes is not None and query_positions is None:
+        raise ValueError("slopes need query_positions")
+    bias = 0 if slopes is None else _whole(slopes, "slopes", (Hq,), _FP32, index)
+    qp = 0 if query_positions is None else _whole(query_positions, "query_positions", (B, T), _I32, index)
+    begin = 0 if first is None else _whole(first, "first", (B, T), _I32, index)
     scale = D ** -0.5 if scale is None else float(scale)
     if not math.isfinite(scale) or not math.isfinite(softcap) or softcap < 0.0:
         raise ValueError("scale and softcap must be finite, softcap not negative")
+    at_q, at_k, at_v = q.data_ptr(), k.data_ptr(), v.data_ptr()
     if out is None:
-        out = torch.empty((B, T, Hq, Dv), dtype=q.dtype, device=q.device)
+        out = torch.empty((B, T, Hq, Dv), dtype=dtype, device=q.device)
+        target = out.data_ptr()
     else:
-        _exact(out, "out", (B, T, Hq, Dv), (q.dtype,), q.device)
-        if any(_overlap(out, t) for t in (q, k, v)):
+        target = _whole(out, "out", (B, T, Hq, Dv), dtype, index)
+        mine = (target, target + 2 * B * T * Hq * Dv)
+        if _overlap(mine, _span(at_q, shape, qs, 2)) or _overlap(mine, _span(at_k, ks, kt, 2)) \
+                or _overlap(mine, _span(at_v, vs, vt, 2)):
             raise ValueError("out must not overlap q, k or v")
-    lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
-    a = _AttentionArgs(q=q.data_ptr(), q_seq_stride=q.stride(0), q_token_stride=q.stride(1),
-                       q_head_stride=q.stride(2), k=k.data_ptr(), k_page_stride=k.stride(0),
-                       k_token_stride=k.stride(1), k_head_stride=k.stride(2), v=v.data_ptr(),
-                       v_page_stride=v.stride(0), v_token_stride=v.stride(1), v_head_stride=v.stride(2),
-                       indices=indices.data_ptr(), page_table=_ptr(page_table),
-                       table_stride=0 if page_table is None else page_table.stride(0),
-                       table_width=0 if page_table is None else page_table.shape[1],
-                       query_positions=_ptr(query_positions), first=_ptr(first), slopes=_ptr(slopes),
-                       out=out.data_ptr(), lse=_ptr(lse), num_pages=pages, page_size=page_size, B=B, T=T,
-                       Hq=Hq, Hkv=Hkv, D=D, Dv=Dv, K=indices.shape[2], type=_TYPES[q.dtype], scale=scale,
-                       softcap=float(softcap))
-    _call("sparse_attention", a, q.get_device(), stream)
+    lse = torch.empty((B, T, Hq), dtype=_FP32, device=q.device) if return_lse else None
+    _attention(index, stream, at_q, qs[0], qs[1], qs[2], at_k, kt[0], kt[1], kt[2], at_v, vt[0], vt[1], vt[2], idx, table,
+               pt, width, qp, begin, bias, target, 0 if lse is None else lse.data_ptr(), pages, page_size, B, T, Hq, Hkv,
+               D, Dv, K, code, scale, softcap)
     return (out, lse) if return_lse else out

@@ -395,34 +395,34 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
 }
 
 template <typename E, int STAGES, int STEP, bool BOXES>
-topk_status launch_variant(const ScoreParams& p, int sm_count, cudaStream_t stream) {
+topk_status launch_variant(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
   static_assert(sizeof(ScoreShared) <= 3072, "barriers and weights");
   const size_t bytes = 2 * static_cast<size_t>(p.cols) * 128 * p.blocks + STAGES * static_cast<size_t>(kTile) * 128 * p.blocks +
                        sizeof(ScoreShared);
-  auto kernel = scores_kernel<E, STAGES, STEP, BOXES>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
-    return TOPK_ECUDA;
+  constexpr auto kernel = scores_kernel<E, STAGES, STEP, BOXES>;
+  const topk_status st = allow_shared<kernel>(dev);
+  if (st != TOPK_OK) return st;
   const int64_t grid = p.units < sm_count ? p.units : sm_count;
   kernel<<<static_cast<unsigned>(grid), kScoreThreads, bytes, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? TOPK_OK : TOPK_ECUDA;
 }
 
 template <typename E, int STAGES, int STEP>
-topk_status launch_step(const ScoreParams& p, int sm_count, cudaStream_t stream) {
-  return p.box_rows > 0 ? launch_variant<E, STAGES, STEP, true>(p, sm_count, stream)
-                        : launch_variant<E, STAGES, STEP, false>(p, sm_count, stream);
+topk_status launch_step(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
+  return p.box_rows > 0 ? launch_variant<E, STAGES, STEP, true>(p, dev, sm_count, stream)
+                        : launch_variant<E, STAGES, STEP, false>(p, dev, sm_count, stream);
 }
 
 template <typename E, int STEP>
-topk_status launch_ring(const ScoreParams& p, int sm_count, cudaStream_t stream) {
+topk_status launch_ring(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
   // The ring gets what the queries leave of 227 KB: 6, 5 or 3 tiles.
-  if (p.cols <= 64) return launch_step<E, 6, STEP>(p, sm_count, stream);
-  if (p.cols <= 128) return launch_step<E, 5, STEP>(p, sm_count, stream);
-  return launch_step<E, 3, STEP>(p, sm_count, stream);
+  if (p.cols <= 64) return launch_step<E, 6, STEP>(p, dev, sm_count, stream);
+  if (p.cols <= 128) return launch_step<E, 5, STEP>(p, dev, sm_count, stream);
+  return launch_step<E, 3, STEP>(p, dev, sm_count, stream);
 }
 
 template <typename E>
-topk_status launch_typed(const sparse_scores_args& a, int sm_count, cudaStream_t stream) {
+topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream) {
   ScoreParams p = {};
   p.a = a;
   const int size = sizeof(E);
@@ -450,16 +450,16 @@ topk_status launch_typed(const sparse_scores_args& a, int sm_count, cudaStream_t
   const bool boxes = rows >= 8 && paged_map(&p.map, Kind<E>::map_type, size, a.keys, a.D, a.page_size, a.num_pages,
                                             a.key_token_stride, a.key_page_stride, rows);
   p.box_rows = boxes ? rows : 0;
-  return p.hp % 32 == 0 ? launch_ring<E, 32>(p, sm_count, stream) : launch_ring<E, 16>(p, sm_count, stream);
+  return p.hp % 32 == 0 ? launch_ring<E, 32>(p, dev, sm_count, stream) : launch_ring<E, 16>(p, dev, sm_count, stream);
 }
 
 }  // namespace
 
-topk_status launch_scores(const sparse_scores_args& a, int sm_count, cudaStream_t stream) {
+topk_status launch_scores(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream) {
   switch (a.type) {
-    case SPARSE_BF16: return launch_typed<__nv_bfloat16>(a, sm_count, stream);
-    case SPARSE_FP16: return launch_typed<__half>(a, sm_count, stream);
-    default: return launch_typed<__nv_fp8_e4m3>(a, sm_count, stream);
+    case SPARSE_BF16: return launch_typed<__nv_bfloat16>(a, dev, sm_count, stream);
+    case SPARSE_FP16: return launch_typed<__half>(a, dev, sm_count, stream);
+    default: return launch_typed<__nv_fp8_e4m3>(a, dev, sm_count, stream);
   }
 }
 

@@ -438,10 +438,10 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
 }
 
 template <typename E, int COPIES>
-topk_status launch_copies(const AttParams& p, int cluster, int64_t grid, size_t bytes, cudaStream_t stream) {
-  auto kernel = attention_kernel<E, COPIES>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
-    return TOPK_ECUDA;
+topk_status launch_copies(const AttParams& p, int dev, int cluster, int64_t grid, size_t bytes, cudaStream_t stream) {
+  constexpr auto kernel = attention_kernel<E, COPIES>;
+  const topk_status st = allow_shared<kernel>(dev);
+  if (st != TOPK_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kAttThreads);
@@ -458,7 +458,7 @@ topk_status launch_copies(const AttParams& p, int cluster, int64_t grid, size_t 
 }
 
 template <typename E>
-topk_status launch_typed(const sparse_attention_args& a, int sm_count, cudaStream_t stream) {
+topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, cudaStream_t stream) {
   AttParams p = {};
   p.a = a;
   p.heads = a.Hq / a.Hkv;
@@ -478,7 +478,7 @@ topk_status launch_typed(const sparse_attention_args& a, int sm_count, cudaStrea
   p.stage_bytes = kKeys * 128 * (p.d_blocks + (p.shared ? 0 : p.v_blocks));
   p.tmem_cols = 2 * kKeys + p.v_blocks * 64 <= 256 ? 256 : 512;
   const int join = 128 * (p.v_blocks * 64 + 4) * 4;
-  const int half = (227 * 1024) / 2 - 1024 - static_cast<int>(sizeof(AttShared)), whole = 227 * 1024 - static_cast<int>(sizeof(AttShared));
+  const int half = kMaxShared / 2 - 1024 - static_cast<int>(sizeof(AttShared)), whole = kMaxShared - static_cast<int>(sizeof(AttShared));
   const bool two = copies > 1 && p.tmem_cols == 256 && q_bytes + 2 * p.stage_bytes <= half && join <= half;
   p.stages = ((two ? half : whole) - q_bytes) / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
@@ -494,16 +494,16 @@ topk_status launch_typed(const sparse_attention_args& a, int sm_count, cudaStrea
   while (cluster < 8 && work * cluster * 2 <= slots && cluster * 2 <= tiles) cluster *= 2;
   const int64_t grid = work * cluster;
   if (grid > INT32_MAX) return TOPK_EINVAL;
-  if (copies == 4) return launch_copies<E, 4>(p, cluster, grid, bytes, stream);
-  if (copies == 2) return launch_copies<E, 2>(p, cluster, grid, bytes, stream);
-  return launch_copies<E, 1>(p, cluster, grid, bytes, stream);
+  if (copies == 4) return launch_copies<E, 4>(p, dev, cluster, grid, bytes, stream);
+  if (copies == 2) return launch_copies<E, 2>(p, dev, cluster, grid, bytes, stream);
+  return launch_copies<E, 1>(p, dev, cluster, grid, bytes, stream);
 }
 
 }  // namespace
 
-topk_status launch_attention(const sparse_attention_args& a, int sm_count, cudaStream_t stream) {
-  return a.type == SPARSE_BF16 ? launch_typed<__nv_bfloat16>(a, sm_count, stream)
-                               : launch_typed<__half>(a, sm_count, stream);
+topk_status launch_attention(const sparse_attention_args& a, int dev, int sm_count, cudaStream_t stream) {
+  return a.type == SPARSE_BF16 ? launch_typed<__nv_bfloat16>(a, dev, sm_count, stream)
+                               : launch_typed<__half>(a, dev, sm_count, stream);
 }
 
 }  // namespace tki

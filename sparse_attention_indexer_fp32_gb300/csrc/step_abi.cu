@@ -65,7 +65,7 @@ topk_status sparse_indexer_scores(const sparse_scores_args* args, topk_stream_t 
   int dev = 0, sms = 0;
   const topk_status st = ready(&dev, &sms);
   if (st != TOPK_OK) return st;
-  return tki::launch_scores(a, sms, reinterpret_cast<cudaStream_t>(stream));
+  return tki::launch_scores(a, dev, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 topk_status sparse_attention(const sparse_attention_args* args, topk_stream_t stream) {
@@ -96,7 +96,7 @@ topk_status sparse_attention(const sparse_attention_args* args, topk_stream_t st
   int dev = 0, sms = 0;
   const topk_status st = ready(&dev, &sms);
   if (st != TOPK_OK) return st;
-  return tki::launch_attention(a, sms, reinterpret_cast<cudaStream_t>(stream));
+  return tki::launch_attention(a, dev, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

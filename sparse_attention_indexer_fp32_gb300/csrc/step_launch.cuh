@@ -4,6 +4,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "sparse_step.h"
 
 namespace tki {
@@ -11,8 +13,22 @@ namespace tki {
 // The current device's index and SM count; TOPK_EDEVICE unless it is sm_103.
 topk_status current_device(int* dev, int* sm_count);
 
+// Dynamic shared memory of one CTA that an SM grants.
+constexpr int kMaxShared = 227 * 1024;
+
+// Lets `kernel` take all of it, once per device.
+template <auto kernel>
+topk_status allow_shared(int dev) {
+  static std::atomic<bool> done[64];
+  if (done[dev].load(std::memory_order_relaxed)) return TOPK_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared) != cudaSuccess)
+    return TOPK_ECUDA;
+  done[dev].store(true, std::memory_order_relaxed);
+  return TOPK_OK;
+}
+
 topk_status launch_rotary(const sparse_rotary_args& a, int sm_count, cudaStream_t stream);
-topk_status launch_scores(const sparse_scores_args& a, int sm_count, cudaStream_t stream);
-topk_status launch_attention(const sparse_attention_args& a, int sm_count, cudaStream_t stream);
+topk_status launch_scores(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream);
+topk_status launch_attention(const sparse_attention_args& a, int dev, int sm_count, cudaStream_t stream);
 
 }  // namespace tki

@@ -109,13 +109,29 @@ def test_binding_refuses_tensors_off_the_gpu():
 
 
 def test_overlap_and_span():
+    def span(t):
+        return _step._span(t.data_ptr(), t.shape, t.stride(), t.element_size())
+
     x = torch.zeros(64)
-    assert _step._span(x[8:16])[1] - _step._span(x[8:16])[0] == 32
-    assert _step._overlap(x[:10], x[9:]) and not _step._overlap(x[:9], x[9:])
-    assert not _step._overlap(x[:0], x)
+    assert span(x[8:16]) == (x.data_ptr() + 32, x.data_ptr() + 64)
+    assert span(x.view(8, 8)[2:4, 1:3]) == (x.data_ptr() + 4 * 17, x.data_ptr() + 4 * 27)
+    assert _step._overlap(span(x[:10]), span(x[9:])) and not _step._overlap(span(x[:9]), span(x[9:]))
+    assert not _step._overlap(span(x[:0]), span(x))
+    wide = torch.zeros((1, 4)).expand(3, 4)
     with pytest.raises(ValueError, match="broadcast"):
-        _step._no_self_overlap(torch.zeros((1, 4)).expand(3, 4), "out")
-    _step._no_self_overlap(torch.zeros((1, 4)).expand(1, 4), "out")
+        _step._no_broadcast(wide.shape, wide.stride(), "out")
+    _step._no_broadcast((1, 4), (0, 1), "out")
+
+
+def test_packed_arguments_are_the_struct():
+    """The bytes that a call packs are those of its ctypes Structure."""
+    for kind, call in ((_step._RotaryArgs, _step._rotary), (_step._ScoresArgs, _step._scores),
+                       (_step._AttentionArgs, _step._attention)):
+        values = []
+        for i, (_, t) in enumerate(kind._fields_):
+            values.append(i + 0.5 if t is ctypes.c_float else 1000003 * (i + 1))
+        packed = call.pack(*values)
+        assert bytes(kind(*values)) == packed
 
 
 def test_rotary_frequencies():
