@@ -57,7 +57,8 @@ struct AttParams {
 struct AttShared {
   float away[kMaxStages][kKeys];     // position - query's, per entry of a stage
   uint16_t seen[kMaxStages][4];      // bit per entry
-  float top[128], sum[128];          // of the rows, for joining
+  float top[128], sum[128];            // of the rows
+  float head_top[128], head_sum[128];  // of the heads: the copies joined
   uint64_t full[kMaxStages], empty[kMaxStages], q_full, s_full[2], p_full[2], pv_done;
   uint32_t tmem;
   uint32_t stop;
@@ -353,84 +354,113 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     sh.sum[threadIdx.x] = failed ? __int_as_float(0x7fc00000) : sum;
   }
 
-  // ---- join copies and CTAs ----
+  // ---- join the copies ----
+  // Every row of the buffer below is scaled to its head's maximum in this CTA.
   __syncthreads();
-  if (cluster > 1) cluster_sync();
-  const int pad = p.v_blocks * 64 + 4;  // floats per row of the joining buffer: rows 4 banks apart
+  const int pad = p.v_blocks * 64 + 4;  // floats per row: rows 4 banks apart
   float* rows = reinterpret_cast<float*>(smem);
-  const uint32_t top_addr = smem_addr(sh.top), sum_addr = smem_addr(sh.sum);
-  float lse = 0.0f;
   if (warp < 4) {
     const int h = threadIdx.x % kRows;
-    float all = __int_as_float(0xff800000), total = 0.0f;
-    for (int r = 0; r < cluster; ++r)
-      for (int c = 0; c < COPIES; ++c) {
-        const uint32_t at = 4 * (c * kRows + h);
-        const float m = cluster > 1 ? __uint_as_float(ld_dsmem_u32(map_rank(top_addr + at, r))) : sh.top[c * kRows + h];
-        all = fmaxf(all, m);
-      }
-    for (int r = 0; r < cluster; ++r)
-      for (int c = 0; c < COPIES; ++c) {
-        const uint32_t at = 4 * (c * kRows + h);
-        const float m = cluster > 1 ? __uint_as_float(ld_dsmem_u32(map_rank(top_addr + at, r))) : sh.top[c * kRows + h];
-        const float l = cluster > 1 ? __uint_as_float(ld_dsmem_u32(map_rank(sum_addr + at, r))) : sh.sum[c * kRows + h];
-        if (!is_low(m)) total += l * exp2_fast(m - all);
-        if (l != l) total = l;
-      }
-    const float weight = total != total ? total : is_low(top) ? 0.0f : exp2_fast(top - all) / total;
-    lse = is_low(all) ? all : (all + log2f(total)) * kLn2;
-    if (total != total) lse = total;
-    if (rank == 0 && a.lse != nullptr && threadIdx.x < heads && threadIdx.x < kRows)
-      a.lse[row * a.Hq + head0 + h] = lse;
+    float all = sh.top[h], total = 0.0f;
+#pragma unroll
+    for (int c = 1; c < COPIES; ++c) all = fmaxf(all, sh.top[c * kRows + h]);
+#pragma unroll
+    for (int c = 0; c < COPIES; ++c) {
+      const float m = sh.top[c * kRows + h], l = sh.sum[c * kRows + h];
+      total += l != l ? l : is_low(m) ? 0.0f : l * exp2_fast(m - all);
+    }
+    if (threadIdx.x < kRows) sh.head_top[h] = all, sh.head_sum[h] = total;
+    const float weight = is_low(top) ? 0.0f : exp2_fast(top - all);
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
     for (int c = 0; c < a.Dv; c += 16) {
-      uint32_t v[16];
+      uint32_t v[16] = {};
       if (tiles > 0) {
         tmem_ld(v, tmem_o + lanes + c);
         tmem_wait_ld(v);
       }
       float* dst = rows + threadIdx.x * pad + c;
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        float4 f;
-        f.x = weight == 0.0f ? 0.0f : __uint_as_float(v[j]) * weight;
-        f.y = weight == 0.0f ? 0.0f : __uint_as_float(v[j + 1]) * weight;
-        f.z = weight == 0.0f ? 0.0f : __uint_as_float(v[j + 2]) * weight;
-        f.w = weight == 0.0f ? 0.0f : __uint_as_float(v[j + 3]) * weight;
-        *reinterpret_cast<float4*>(dst + j) = f;
-      }
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<float4*>(dst + j) =
+            make_float4(__uint_as_float(v[j]) * weight, __uint_as_float(v[j + 1]) * weight,
+                        __uint_as_float(v[j + 2]) * weight, __uint_as_float(v[j + 3]) * weight);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (cluster > 1) cluster_sync();
-  {
-    // Eight outputs per thread, the CTAs of a cluster in turn.
-    const int per_row = a.Dv / 8, items = heads * per_row;
-    E* out = static_cast<E*>(a.out) + (row * a.Hq + head0) * a.Dv;
-    const uint32_t rows_addr = smem_addr(rows);
-    for (int i = static_cast<int>(rank) * kAttThreads + threadIdx.x; i < items; i += cluster * kAttThreads) {
-      const int h = i / per_row, c = (i - h * per_row) * 8;
-      float4 x = {}, y = {};
-      for (int r = 0; r < cluster; ++r)
+
+  // ---- write, or join the CTAs first ----
+  // Eight outputs per item.
+  const int per_row = a.Dv / 8, items = heads * per_row;
+  E* out = static_cast<E*>(a.out) + (row * a.Hq + head0) * a.Dv;
+  auto write = [&](int h, int c, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(h) * a.Dv + c) =
+        make_uint4(Pack<E>::two(x[0], x[1]), Pack<E>::two(x[2], x[3]), Pack<E>::two(x[4], x[5]), Pack<E>::two(x[6], x[7]));
+  };
+  auto add = [](float (&x)[8], float4 u, float4 v, float f) {
+    x[0] += u.x * f, x[1] += u.y * f, x[2] += u.z * f, x[3] += u.w * f;
+    x[4] += v.x * f, x[5] += v.y * f, x[6] += v.z * f, x[7] += v.w * f;
+  };
+  // A row's factor, 1 / its sum of weights: zero where nothing is seen.
+  auto inverse = [](float all, float total) { return total != total ? total : is_low(all) ? 0.0f : 1.0f / total; };
+  auto logsum = [](float all, float total) { return total != total ? total : is_low(all) ? all : (all + log2f(total)) * kLn2; };
+  for (int i = threadIdx.x; i < items; i += kAttThreads) {
+    const int h = i / per_row, c = (i - h * per_row) * 8;
+    float x[8] = {};
 #pragma unroll
-        for (int k = 0; k < COPIES; ++k) {
-          const int at = (k * kRows + h) * pad + c;
-          float4 u, v;
-          if (cluster > 1) {
-            const uint32_t from = map_rank(rows_addr + 4 * at, r);
-            u = ld_dsmem_f4(from), v = ld_dsmem_f4(from + 16);
-          } else {
-            u = *reinterpret_cast<const float4*>(rows + at), v = *reinterpret_cast<const float4*>(rows + at + 4);
-          }
-          x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
-          y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
-        }
-      *reinterpret_cast<uint4*>(out + static_cast<int64_t>(h) * a.Dv + c) =
-          make_uint4(Pack<E>::two(x.x, x.y), Pack<E>::two(x.z, x.w), Pack<E>::two(y.x, y.y), Pack<E>::two(y.z, y.w));
+    for (int k = 0; k < COPIES; ++k) {
+      const float* from = rows + (k * kRows + h) * pad + c;
+      add(x, *reinterpret_cast<const float4*>(from), *reinterpret_cast<const float4*>(from + 4), 1.0f);
+    }
+    if (cluster == 1) {
+      const float f = inverse(sh.head_top[h], sh.head_sum[h]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= f;
+      write(h, c, x);
+    } else {
+      float* to = rows + h * pad + c;
+      *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
     }
   }
-  if (cluster > 1) cluster_sync();  // the others may still read this CTA's rows
+  if (cluster == 1) {
+    if (a.lse != nullptr && threadIdx.x < heads)
+      a.lse[row * a.Hq + head0 + threadIdx.x] = logsum(sh.head_top[threadIdx.x], sh.head_sum[threadIdx.x]);
+  } else {
+    cluster_sync();
+    const uint32_t top_addr = smem_addr(sh.head_top), sum_addr = smem_addr(sh.head_sum), rows_addr = smem_addr(rows);
+    // the CTAs take items in turn; reads of all CTAs are in flight together
+    for (int i = static_cast<int>(rank) * kAttThreads + threadIdx.x; i < items; i += cluster * kAttThreads) {
+      const int h = i / per_row, c = (i - h * per_row) * 8;
+      float m[8], l[8];
+      float4 u[8], v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const uint32_t from = r < cluster ? r : 0;
+        m[r] = __uint_as_float(ld_dsmem_u32(map_rank(top_addr + 4 * h, from)));
+        l[r] = __uint_as_float(ld_dsmem_u32(map_rank(sum_addr + 4 * h, from)));
+        u[r] = ld_dsmem_f4(map_rank(rows_addr + 4 * (h * pad + c), from));
+        v[r] = ld_dsmem_f4(map_rank(rows_addr + 4 * (h * pad + c) + 16, from));
+      }
+      float all = m[0], total = 0.0f;
+#pragma unroll
+      for (int r = 1; r < 8; ++r) all = fmaxf(all, m[r]);
+      float x[8] = {};
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < cluster) {
+          const float f = is_low(m[r]) ? 0.0f : exp2_fast(m[r] - all);
+          total += l[r] != l[r] ? l[r] : l[r] * f;
+          add(x, u[r], v[r], f);
+        }
+      const float f = inverse(all, total);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= f;
+      write(h, c, x);
+      if (c == 0 && a.lse != nullptr) a.lse[row * a.Hq + head0 + h] = logsum(all, total);
+    }
+    cluster_sync();  // the others may still read this CTA's rows
+  }
   if (warp == 8) {
     tc_fence_after();
     tmem_free(tmem, p.tmem_cols);
