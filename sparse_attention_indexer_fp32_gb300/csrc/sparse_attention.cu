@@ -21,8 +21,11 @@
 // workspace, the same order on every call.
 //
 // Warps 0-3: softmax, one row per thread; 4-7: gather entries through the page
-// table into a ring with 16-byte asynchronous copies, zeros for what is not
-// seen; 8: one thread issues the products.
+// table with 16-byte asynchronous copies, zeros for what is not seen; 8: one
+// thread issues the products. Keys and values have rings of their own, filled
+// by two warps each: a stage of keys is free again right after Q K^T, so the
+// gathers run ahead of the softmax (one ring of both, two stages deep, left
+// every tile waiting for its gather: 3.5 us a tile for one CTA).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,6 +41,9 @@ namespace {
 constexpr int kKeys = 64;  // entries per tile
 constexpr int kAttThreads = 9 * 32;
 constexpr int kMaxStages = 6;
+// Masks outlive their keys' stage: tile j's are written when the products of
+// tile j - stages are done, which follow the softmax of the tile two before.
+constexpr int kMasks = kMaxStages + 2;
 constexpr float kGrowth = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -47,19 +53,21 @@ struct AttParams {
   int32_t m_tiles;    // tiles of 128 rows per key head
   int32_t d_blocks, v_blocks;  // 128-byte blocks of an entry's keys and values
   int32_t shared;     // v is a prefix of k's entries
-  int32_t stages;
-  int32_t stage_bytes, ring_at;  // bytes; the ring begins after Q
+  int32_t k_stages, v_stages;  // of the rings; no second ring when shared
+  int32_t k_bytes, v_bytes;    // of a stage
+  int32_t k_at, v_at;          // the rings, after Q
   int32_t shared_at;  // AttShared
   int32_t tmem_cols;
   bool q_vector;
 };
 
 struct AttShared {
-  float away[kMaxStages][kKeys];     // position - query's, per entry of a stage
-  uint16_t seen[kMaxStages][4];      // bit per entry
+  float away[kMasks][kKeys];           // position - query's, per entry of a tile
+  uint32_t seen[kMasks][2];            // bit per entry
   float top[128], sum[128];            // of the rows
   float head_top[128], head_sum[128];  // of the heads: the copies joined
-  uint64_t full[kMaxStages], empty[kMaxStages], q_full, s_full[2], p_full[2], pv_done;
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages], masks[kMasks];
+  uint64_t q_full, s_full[2], p_full[2], pv_done;
   uint32_t tmem;
   uint32_t stop;
 };
@@ -124,10 +132,12 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   const int all_tiles = (a.K + kKeys - 1) / kKeys;
   const int tiles = all_tiles > static_cast<int>(rank) ? (all_tiles - static_cast<int>(rank) + cluster - 1) / cluster : 0;
   const uint32_t base = smem_addr(smem);
-  const uint32_t ring = base + p.ring_at;
+  const uint32_t k_ring = base + p.k_at, v_ring = base + p.v_at;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) mbar_init(&sh.full[i], 128 + 4), mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < p.k_stages; ++i) mbar_init(&sh.k_full[i], p.shared ? 128 : 64), mbar_init(&sh.k_empty[i], 1);
+    for (int i = 0; i < p.v_stages; ++i) mbar_init(&sh.v_full[i], 64), mbar_init(&sh.v_empty[i], 1);
+    for (int i = 0; i < kMasks; ++i) mbar_init(&sh.masks[i], 2);
     mbar_init(&sh.q_full, 256);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 128);
     mbar_init(&sh.pv_done, 1);
@@ -146,61 +156,71 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
 
   if (warp >= 4 && warp < 8) {
     // ---- gather ----
-    const int w = warp - 4;
+    // Warps 0 and 1 fetch the tile's entries 0-31 and 32-63, keys; warps 2
+    // and 3 their values, or the second half of their blocks when shared.
+    const int w = warp - 4, half = w & 1;
+    const bool values = w >= 2 && !p.shared;
+    const int split = (p.d_blocks + 1) / 2;  // shared: blocks of the first two warps
+    const int c0 = w >= 2 && p.shared ? split : 0;
+    const int c1 = values ? p.v_blocks : w < 2 && p.shared ? split : p.d_blocks;
+    const int dim = values ? a.Dv : a.D;
+    const E* cache = static_cast<const E*>(values ? a.v : a.k) +
+                     static_cast<int64_t>(g) * (values ? a.v_head_stride : a.k_head_stride);
+    const int64_t page_stride = values ? a.v_page_stride : a.k_page_stride;
+    const int64_t token_stride = values ? a.v_token_stride : a.k_token_stride;
+    uint64_t* full = values ? sh.v_full : sh.k_full;
+    uint64_t* empty = values ? sh.v_empty : sh.k_empty;
+    const int stages = values ? p.v_stages : p.k_stages, stage_bytes = values ? p.v_bytes : p.k_bytes;
     const int32_t* indices = a.indices + row * a.K;
     const int32_t* table = a.page_table != nullptr ? a.page_table + b * a.table_stride : nullptr;
     const int32_t last = a.query_positions != nullptr ? a.query_positions[row] : INT32_MAX;
     const int32_t first = a.first != nullptr ? max(a.first[row], 0) : 0;
     const bool some = a.page_size > 0 && a.num_pages > 0;
-    // Lane i < 16 looks up entry 16 w + i of a tile: its index two tiles
-    // ahead, its page id one tile ahead.
+    // Each lane looks up one entry of a tile: its index two tiles ahead, its
+    // page id one tile ahead.
     auto index_of = [&](int i) -> int32_t {
-      const int64_t j = (static_cast<int64_t>(i) * cluster + rank) * kKeys + w * 16 + lane;
-      return lane < 16 && i < tiles && j < a.K && some ? indices[j] : -1;
+      const int64_t j = (static_cast<int64_t>(i) * cluster + rank) * kKeys + half * 32 + lane;
+      return i < tiles && j < a.K && some ? indices[j] : -1;
     };
     auto page_of = [&](int32_t pos) -> int32_t {
       if (pos < first || pos > last) return -1;
       const int32_t page = pos / a.page_size;
       return table == nullptr ? page : page < a.table_width ? table[page] : -1;
     };
+    // 8 lanes fetch 128 bytes of an entry; step j has entries 4 j + lane / 8.
+    const uint32_t unit16 = lane & 7, sub = lane >> 3;
+    const uint32_t at = (values ? v_ring : k_ring) + (half * 32 + sub) * 128;
+    const uint32_t even = (unit16 ^ sub) << 4, odd = (unit16 ^ (sub + 4)) << 4;
     int32_t pos = index_of(0), pos1 = index_of(1);
     int32_t page = page_of(pos);
-    bool ok = true;
+    int stage = 0, turn = 1;
     for (int i = 0; i < tiles; ++i) {
       const int32_t pos2 = index_of(i + 2);
       const int32_t page1 = page_of(pos1);
-      const int stage = i % p.stages;
-      ok = wait_or_stop(&sh.empty[stage], ((i / p.stages) & 1) ^ 1, stop);
-      if (!ok) break;
       const bool seen = page >= 0 && page < a.num_pages;
-      const int32_t place = seen ? pos % a.page_size : 0;
-      const int64_t k_at = seen ? page * a.k_page_stride + place * a.k_token_stride + g * a.k_head_stride : -1;
-      const int64_t v_at = seen ? page * a.v_page_stride + place * a.v_token_stride + g * a.v_head_stride : -1;
+      const int64_t entry = seen ? page * page_stride + pos % a.page_size * token_stride : 0;
       const uint32_t bits = __ballot_sync(0xffffffffu, seen);
-      if (lane < 16) sh.away[stage][w * 16 + lane] = static_cast<float>(seen ? pos - last : 0);
-      if (lane == 0) sh.seen[stage][w] = static_cast<uint16_t>(bits);
-      const uint32_t dst = ring + stage * p.stage_bytes;
-      const uint32_t unit16 = lane & 7;
+      if (!wait_or_stop(&empty[stage], turn, stop)) break;
+      const uint32_t dst = at + stage * stage_bytes;
+      const E* from[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 4 * j + (lane >> 3);
-        const int64_t ks = __shfl_sync(0xffffffffu, k_at, r), vs = __shfl_sync(0xffffffffu, v_at, r);
-        const uint32_t at = swizzled(w * 16 + r, unit16);
-        for (int c = 0; c < p.d_blocks; ++c) {
-          const bool real = ks >= 0 && static_cast<int>(c * 8 + unit16) * 8 < a.D;
-          copy16(dst + c * kKeys * 128 + at, real ? static_cast<const E*>(a.k) + ks + (c * 8 + unit16) * 8 : nowhere, real);
-        }
-        if (!p.shared)
-          for (int c = 0; c < p.v_blocks; ++c) {
-            const bool real = vs >= 0 && static_cast<int>(c * 8 + unit16) * 8 < a.Dv;
-            copy16(dst + (p.d_blocks + c) * kKeys * 128 + at,
-                   real ? static_cast<const E*>(a.v) + vs + (c * 8 + unit16) * 8 : nowhere, real);
-          }
+      for (int j = 0; j < 8; ++j) from[j] = cache + __shfl_sync(0xffffffffu, entry, 4 * j + sub) + unit16 * 8;
+      for (int c = c0; c < c1; ++c) {
+        const bool inside = c * 64 + static_cast<int>(unit16) * 8 < dim;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          copy16(dst + c * (kKeys * 128) + j * 512 + (j & 1 ? odd : even), inside ? from[j] + c * 64 : cache,
+                 inside && ((bits >> (4 * j + sub)) & 1));
       }
-      copy_arrive(&sh.full[stage]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.full[stage]);  // seen, away
+      copy_arrive(&full[stage]);
+      if (w < 2) {
+        sh.away[i % kMasks][half * 32 + lane] = static_cast<float>(seen ? pos - last : 0);
+        if (lane == 0) sh.seen[i % kMasks][half] = bits;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.masks[i % kMasks]);
+      }
       pos = pos1, pos1 = pos2, page = page1;
+      if (++stage == stages) stage = 0, turn ^= 1;
     }
     copy_commit();
     copy_wait<0>();
@@ -208,37 +228,53 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     // ---- products ----
     const uint32_t desc_s = mma_desc(Pack<E>::type, kKeys);
     const uint32_t desc_o = mma_desc(Pack<E>::type, (a.Dv + 15) / 16 * 16, true);
-    const int d_steps = (a.D + 15) / 16;
+    const uint64_t q_desc = operand_desc(base);
+    const uint64_t k_desc = operand_desc(k_ring);
+    const uint64_t v_desc = operand_desc(p.shared ? k_ring : v_ring, kKeys * 128);
+    int k_stage = 0, k_turn = 0, v_stage = 0, v_turn = 0;
+    const int v_stages = p.shared ? p.k_stages : p.v_stages, v_bytes = p.shared ? p.k_bytes : p.v_bytes;
+    uint64_t* v_empty = p.shared ? sh.k_empty : sh.v_empty;
     auto scores = [&](int i) -> bool {
-      if (!wait_or_stop(&sh.full[i % p.stages], (i / p.stages) & 1, stop)) return false;
+      if (!wait_or_stop(&sh.k_full[k_stage], k_turn, stop)) return false;
       fence_proxy_async_smem();
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t kb = ring + (i % p.stages) * p.stage_bytes;
-        for (int j = 0; j < d_steps; ++j)
-          mma_f16(tmem + (i & 1) * kKeys, operand_desc(base + (j >> 2) * 128 * 128 + (j & 3) * 32),
-                  operand_desc(kb + (j >> 2) * kKeys * 128 + (j & 3) * 32), desc_s, j > 0);
+      if (elect_one()) {
+        const uint64_t kd = k_desc + static_cast<uint32_t>(k_stage * p.k_bytes >> 4);
+        const uint32_t to = tmem + (i & 1) * kKeys;
+        for (int c = 0; c < p.d_blocks; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f16(to, q_desc + static_cast<uint32_t>(c * (128 * 128 >> 4) + j * 2),
+                    kd + static_cast<uint32_t>(c * (kKeys * 128 >> 4) + j * 2), desc_s, c + j > 0);
         mma_commit(&sh.s_full[i & 1]);
+        if (!p.shared) mma_commit(&sh.k_empty[k_stage]);
       }
       __syncwarp();
+      if (++k_stage == p.k_stages) k_stage = 0, k_turn ^= 1;
       return true;
     };
     bool ok = tiles > 0 && wait_or_stop(&sh.q_full, 0, stop) && scores(0);
     for (int i = 0; i < tiles && ok; ++i) {
       // the next scores go where the weights of tile i - 1 were
       if (i + 1 < tiles) ok = (i == 0 || wait_or_stop(&sh.pv_done, (i - 1) & 1, stop)) && scores(i + 1);
+      if (ok && !p.shared) {
+        ok = wait_or_stop(&sh.v_full[v_stage], v_turn, stop);
+        fence_proxy_async_smem();
+      }
       ok = ok && wait_or_stop(&sh.p_full[i & 1], (i >> 1) & 1, stop);
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t vb = ring + (i % p.stages) * p.stage_bytes + (p.shared ? 0 : p.d_blocks * kKeys * 128);
+      if (elect_one()) {
+        const uint64_t vd = v_desc + static_cast<uint32_t>(v_stage * v_bytes >> 4);
+#pragma unroll
         for (int j = 0; j < kKeys / 16; ++j)
-          mma_f16_ts(tmem_o, tmem + (i & 1) * kKeys + j * 8, operand_desc(vb + j * 16 * 128, kKeys * 128), desc_o,
+          mma_f16_ts(tmem_o, tmem + (i & 1) * kKeys + j * 8, vd + static_cast<uint32_t>(j * (16 * 128 >> 4)), desc_o,
                      i + j > 0);
-        mma_commit(&sh.empty[i % p.stages]);
+        mma_commit(&v_empty[v_stage]);
         mma_commit(&sh.pv_done);
       }
       __syncwarp();
+      if (++v_stage == v_stages) v_stage = 0, v_turn ^= 1;
     }
   } else {
     // ---- softmax ----
@@ -268,8 +304,8 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     const float cap_out = a.softcap * kLog2e, scale = a.scale * kLog2e;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
     for (int i = 0; i < tiles; ++i) {
-      const int stage = i % p.stages;
-      if (!wait_or_stop(&sh.full[stage], (i / p.stages) & 1, stop)) break;
+      const int mask = i % kMasks;
+      if (!wait_or_stop(&sh.masks[mask], (i / kMasks) & 1, stop)) break;
       if (!wait_or_stop(&sh.s_full[i & 1], (i >> 1) & 1, stop)) break;
       tc_fence_after();
       const uint32_t s_at = tmem + (i & 1) * kKeys + lanes;
@@ -280,8 +316,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
         uint32_t v[kStep];
         tmem_ld(v, s_at + copy * kPart + c);
         const int e0 = copy * kPart + c;
-        uint32_t bits = sh.seen[stage][e0 / 16];
-        if (kStep == 32) bits |= static_cast<uint32_t>(sh.seen[stage][e0 / 16 + 1]) << 16;
+        const uint32_t bits = (sh.seen[mask][e0 / 32] >> (e0 % 32)) & (kStep == 32 ? 0xffffffffu : 0xffffu);
         tmem_wait_ld(v);
         if (a.softcap > 0.0f) {
 #pragma unroll
@@ -292,7 +327,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
         }
         if (a.slopes != nullptr) {
 #pragma unroll
-          for (int j = 0; j < kStep; ++j) z[c + j] += slope * sh.away[stage][e0 + j];
+          for (int j = 0; j < kStep; ++j) z[c + j] += slope * sh.away[mask][e0 + j];
         }
         if (bits != (kStep == 32 ? 0xffffffffu : 0xffffu)) {
 #pragma unroll
@@ -504,15 +539,23 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   // to be joined. Two CTAs share an SM where two stages each fit (and TMEM
   // holds both), else one CTA has as many stages as fit.
   const int q_bytes = 128 * 128 * p.d_blocks;
-  p.ring_at = q_bytes;
-  p.stage_bytes = kKeys * 128 * (p.d_blocks + (p.shared ? 0 : p.v_blocks));
+  p.k_bytes = kKeys * 128 * p.d_blocks;
+  p.v_bytes = p.shared ? 0 : kKeys * 128 * p.v_blocks;
   p.tmem_cols = 2 * kKeys + p.v_blocks * 64 <= 256 ? 256 : 512;
   const int join = 128 * (p.v_blocks * 64 + 4) * 4;
-  const int half = kMaxShared / 2 - 1024 - static_cast<int>(sizeof(AttShared)), whole = kMaxShared - static_cast<int>(sizeof(AttShared));
-  const bool two = copies > 1 && p.tmem_cols == 256 && q_bytes + 2 * p.stage_bytes <= half && join <= half;
-  p.stages = ((two ? half : whole) - q_bytes) / p.stage_bytes;
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  int operands = q_bytes + p.stages * p.stage_bytes;
+  const int whole = kMaxShared - static_cast<int>(sizeof(AttShared));
+  const int half = kMaxShared / 2 - 1024 - static_cast<int>(sizeof(AttShared));
+  const int least = p.shared ? 3 : 2;  // stages below which two CTAs gain nothing
+  const bool two = copies > 1 && p.tmem_cols == 256 && q_bytes + least * (p.k_bytes + p.v_bytes) <= half && join <= half;
+  int room = ((two ? half : whole) - q_bytes);
+  int stages = room / (p.k_bytes + p.v_bytes);
+  if (stages > kMaxStages) stages = kMaxStages;
+  p.k_stages = stages;
+  p.v_stages = p.shared ? 0 : stages;
+  if (!p.shared && stages < kMaxStages && room - stages * (p.k_bytes + p.v_bytes) >= p.v_bytes) ++p.v_stages;
+  p.k_at = q_bytes;
+  p.v_at = q_bytes + p.k_stages * p.k_bytes;
+  int operands = p.v_at + p.v_stages * p.v_bytes;
   if (operands < join) operands = (join + 15) / 16 * 16;
   p.shared_at = operands;
   const size_t bytes = static_cast<size_t>(operands) + sizeof(AttShared);
