@@ -42,8 +42,10 @@ constexpr int kKeys = 64;  // entries per tile
 constexpr int kAttThreads = 9 * 32;
 constexpr int kMaxStages = 6;
 // Masks outlive their keys' stage: tile j's are written when the products of
-// tile j - stages are done, which follow the softmax of the tile two before.
-constexpr int kMasks = kMaxStages + 2;
+// tile j - stages are issued, which follow the softmax of the tile kMaxBufs
+// before at the latest.
+constexpr int kMaxBufs = 3;  // buffers of scores and weights in TMEM
+constexpr int kMasks = kMaxStages + kMaxBufs;
 constexpr float kGrowth = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -57,7 +59,7 @@ struct AttParams {
   int32_t k_bytes, v_bytes;    // of a stage
   int32_t k_at, v_at;          // the rings, after Q
   int32_t shared_at;  // AttShared
-  int32_t tmem_cols;
+  int32_t tmem_cols, bufs;
   bool q_vector;
 };
 
@@ -67,7 +69,7 @@ struct AttShared {
   float top[128], sum[128];            // of the rows
   float head_top[128], head_sum[128];  // of the heads: the copies joined
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages], masks[kMasks];
-  uint64_t q_full, s_full[2], p_full[2], pv_done;
+  uint64_t q_full, s_full[kMaxBufs], p_full[kMaxBufs], pv_done[kMaxBufs];
   uint32_t tmem;
   uint32_t stop;
 };
@@ -122,11 +124,11 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   const sparse_attention_args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster > 1 ? cluster_ctarank() : 0;
-  const int64_t work = blockIdx.x / cluster;
-  const int m_tile = static_cast<int>(work % p.m_tiles);
-  const int g = static_cast<int>(work / p.m_tiles % a.Hkv);
-  const int64_t row = work / p.m_tiles / a.Hkv;
-  const int64_t b = row / a.T, t = row - b * a.T;
+  const uint32_t work = blockIdx.x / cluster, pair = work / p.m_tiles;
+  const int m_tile = static_cast<int>(work - pair * p.m_tiles);
+  const uint32_t row32 = pair / a.Hkv;
+  const int g = static_cast<int>(pair - row32 * a.Hkv);
+  const int64_t row = row32, b = row32 / a.T, t = row - b * a.T;
   const int heads = min(p.heads - m_tile * 128, 128);  // real rows of this tile
   const int head0 = g * p.heads + m_tile * 128;
   const int all_tiles = (a.K + kKeys - 1) / kKeys;
@@ -134,31 +136,51 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   const uint32_t base = smem_addr(smem);
   const uint32_t k_ring = base + p.k_at, v_ring = base + p.v_at;
 
+  const int half = warp & 1;  // of a tile's entries
+  const int32_t* indices = a.indices + row * a.K;
+  const int32_t* table = a.page_table != nullptr ? a.page_table + b * a.table_stride : nullptr;
+  const int32_t last = a.query_positions != nullptr ? a.query_positions[row] : INT32_MAX;
+  const int32_t first = a.first != nullptr ? max(a.first[row], 0) : 0;
+  const bool some = a.page_size > 0 && a.num_pages > 0;
+  // Gathering: each lane looks up one entry of a tile, its index two tiles
+  // ahead, its page id one.
+  auto index_of = [&](int i) -> int32_t {
+    const int64_t j = (static_cast<int64_t>(i) * cluster + rank) * kKeys + half * 32 + lane;
+    return i < tiles && j < a.K && some ? indices[j] : -1;
+  };
+  auto page_of = [&](int32_t pos) -> int32_t {
+    if (pos < first || pos > last) return -1;
+    const int32_t page = pos / a.page_size;
+    return table == nullptr ? page : page < a.table_width ? table[page] : -1;
+  };
+  const bool gathers = warp >= 4 && warp < 8;
+  int32_t pos = gathers ? index_of(0) : -1, pos1 = gathers ? index_of(1) : -1;
+
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.k_stages; ++i) mbar_init(&sh.k_full[i], p.shared ? 128 : 64), mbar_init(&sh.k_empty[i], 1);
     for (int i = 0; i < p.v_stages; ++i) mbar_init(&sh.v_full[i], 64), mbar_init(&sh.v_empty[i], 1);
     for (int i = 0; i < kMasks; ++i) mbar_init(&sh.masks[i], 2);
     mbar_init(&sh.q_full, 256);
-    for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 128);
-    mbar_init(&sh.pv_done, 1);
+    for (int i = 0; i < p.bufs; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 128), mbar_init(&sh.pv_done[i], 1);
     sh.stop = 0;
     fence_mbar_init();
   }
   if (warp == 8) tmem_alloc(&sh.tmem, p.tmem_cols);
+  int32_t page = page_of(pos);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem, tmem_o = tmem + 2 * kKeys;
+  const uint32_t tmem = sh.tmem, tmem_o = tmem + p.bufs * kKeys;
   volatile uint32_t* stop = &sh.stop;
   const void* nowhere = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(a.q) & ~static_cast<uintptr_t>(15));
 
   float top = __int_as_float(0xff800000), sum = 0.0f;  // of this thread's row (its reference and sum of weights)
 
-  if (warp >= 4 && warp < 8) {
+  if (gathers) {
     // ---- gather ----
     // Warps 0 and 1 fetch the tile's entries 0-31 and 32-63, keys; warps 2
     // and 3 their values, or the second half of their blocks when shared.
-    const int w = warp - 4, half = w & 1;
+    const int w = warp - 4;
     const bool values = w >= 2 && !p.shared;
     const int split = (p.d_blocks + 1) / 2;  // shared: blocks of the first two warps
     const int c0 = w >= 2 && p.shared ? split : 0;
@@ -171,28 +193,10 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     uint64_t* full = values ? sh.v_full : sh.k_full;
     uint64_t* empty = values ? sh.v_empty : sh.k_empty;
     const int stages = values ? p.v_stages : p.k_stages, stage_bytes = values ? p.v_bytes : p.k_bytes;
-    const int32_t* indices = a.indices + row * a.K;
-    const int32_t* table = a.page_table != nullptr ? a.page_table + b * a.table_stride : nullptr;
-    const int32_t last = a.query_positions != nullptr ? a.query_positions[row] : INT32_MAX;
-    const int32_t first = a.first != nullptr ? max(a.first[row], 0) : 0;
-    const bool some = a.page_size > 0 && a.num_pages > 0;
-    // Each lane looks up one entry of a tile: its index two tiles ahead, its
-    // page id one tile ahead.
-    auto index_of = [&](int i) -> int32_t {
-      const int64_t j = (static_cast<int64_t>(i) * cluster + rank) * kKeys + half * 32 + lane;
-      return i < tiles && j < a.K && some ? indices[j] : -1;
-    };
-    auto page_of = [&](int32_t pos) -> int32_t {
-      if (pos < first || pos > last) return -1;
-      const int32_t page = pos / a.page_size;
-      return table == nullptr ? page : page < a.table_width ? table[page] : -1;
-    };
     // 8 lanes fetch 128 bytes of an entry; step j has entries 4 j + lane / 8.
     const uint32_t unit16 = lane & 7, sub = lane >> 3;
     const uint32_t at = (values ? v_ring : k_ring) + (half * 32 + sub) * 128;
     const uint32_t even = (unit16 ^ sub) << 4, odd = (unit16 ^ (sub + 4)) << 4;
-    int32_t pos = index_of(0), pos1 = index_of(1);
-    int32_t page = page_of(pos);
     int stage = 0, turn = 1;
     for (int i = 0; i < tiles; ++i) {
       const int32_t pos2 = index_of(i + 2);
@@ -234,19 +238,19 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     int k_stage = 0, k_turn = 0, v_stage = 0, v_turn = 0;
     const int v_stages = p.shared ? p.k_stages : p.v_stages, v_bytes = p.shared ? p.k_bytes : p.v_bytes;
     uint64_t* v_empty = p.shared ? sh.k_empty : sh.v_empty;
-    auto scores = [&](int i) -> bool {
+    auto scores = [&](uint32_t buf) -> bool {
       if (!wait_or_stop(&sh.k_full[k_stage], k_turn, stop)) return false;
       fence_proxy_async_smem();
       tc_fence_after();
       if (elect_one()) {
         const uint64_t kd = k_desc + static_cast<uint32_t>(k_stage * p.k_bytes >> 4);
-        const uint32_t to = tmem + (i & 1) * kKeys;
+        const uint32_t to = tmem + buf * kKeys;
         for (int c = 0; c < p.d_blocks; ++c)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             mma_f16(to, q_desc + static_cast<uint32_t>(c * (128 * 128 >> 4) + j * 2),
                     kd + static_cast<uint32_t>(c * (kKeys * 128 >> 4) + j * 2), desc_s, c + j > 0);
-        mma_commit(&sh.s_full[i & 1]);
+        mma_commit(&sh.s_full[buf]);
         if (!p.shared) mma_commit(&sh.k_empty[k_stage]);
       }
       __syncwarp();
@@ -254,45 +258,52 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
       return true;
     };
     bool ok = tiles > 0 && wait_or_stop(&sh.q_full, 0, stop) && scores(0);
+    uint32_t buf = 0, turn = 0, next = 1, next_turn = 1;  // next_turn: of the weights that were there before
     for (int i = 0; i < tiles && ok; ++i) {
-      // the next scores go where the weights of tile i - 1 were
-      if (i + 1 < tiles) ok = (i == 0 || wait_or_stop(&sh.pv_done, (i - 1) & 1, stop)) && scores(i + 1);
+      // the next scores go where the weights of tile i + 1 - bufs were
+      if (i + 1 < tiles) ok = wait_or_stop(&sh.pv_done[next], next_turn, stop) && scores(next);
       if (ok && !p.shared) {
         ok = wait_or_stop(&sh.v_full[v_stage], v_turn, stop);
         fence_proxy_async_smem();
       }
-      ok = ok && wait_or_stop(&sh.p_full[i & 1], (i >> 1) & 1, stop);
+      ok = ok && wait_or_stop(&sh.p_full[buf], turn, stop);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t vd = v_desc + static_cast<uint32_t>(v_stage * v_bytes >> 4);
 #pragma unroll
         for (int j = 0; j < kKeys / 16; ++j)
-          mma_f16_ts(tmem_o, tmem + (i & 1) * kKeys + j * 8, vd + static_cast<uint32_t>(j * (16 * 128 >> 4)), desc_o,
-                     i + j > 0);
+          mma_f16_ts(tmem_o, tmem + buf * kKeys + j * 8, vd + static_cast<uint32_t>(j * (16 * 128 >> 4)), desc_o, i + j > 0);
         mma_commit(&v_empty[v_stage]);
-        mma_commit(&sh.pv_done);
+        mma_commit(&sh.pv_done[buf]);
       }
       __syncwarp();
       if (++v_stage == v_stages) v_stage = 0, v_turn ^= 1;
+      buf = next;
+      if (buf == 0) turn ^= 1;
+      if (++next == static_cast<uint32_t>(p.bufs)) next = 0, next_turn ^= 1;
     }
   } else {
     // ---- softmax ----
     const int copy = threadIdx.x / kRows;
-    {  // queries first
-      const int units = p.d_blocks * 8;
+    {  // queries first: 8 threads per 128 bytes of a row
+      const int unit16 = threadIdx.x & 7, sub = threadIdx.x >> 3;
       const E* q = static_cast<const E*>(a.q) + b * a.q_seq_stride + t * a.q_token_stride + head0 * a.q_head_stride;
-      for (int i = threadIdx.x; i < 128 * units; i += 128) {
-        const int r = i / units, j = i - r * units, h = r % kRows;
-        const bool real = h < heads && j * 8 < a.D;
-        const E* src = real ? q + h * a.q_head_stride + j * 8 : nullptr;
-        const uint32_t at = (j >> 3) * 128 * 128 + swizzled(r, j & 7);
-        if (p.q_vector) {
-          copy16(base + at, real ? src : nowhere, real);
-        } else {
-          E v[8];
-          for (int e = 0; e < 8; ++e) v[e] = real ? src[e] : E(0.0f);
-          *reinterpret_cast<uint4*>(smem + at) = *reinterpret_cast<const uint4*>(v);
+      for (int c = 0; c < p.d_blocks; ++c) {
+        const int d = c * 64 + unit16 * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = 16 * j + sub, h = r % kRows;
+          const bool real = h < heads && d < a.D;
+          const uint32_t at = c * (128 * 128) + swizzled(r, unit16);
+          const E* src = q + h * a.q_head_stride + d;
+          if (p.q_vector) {
+            copy16(base + at, real ? src : nowhere, real);
+          } else {
+            E v[8];
+            for (int e = 0; e < 8; ++e) v[e] = real ? src[e] : E(0.0f);
+            *reinterpret_cast<uint4*>(smem + at) = *reinterpret_cast<const uint4*>(v);
+          }
         }
       }
       copy_arrive(&sh.q_full);
@@ -303,12 +314,13 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     const float cap_in = a.softcap > 0.0f ? a.scale * 2.0f * kLog2e / a.softcap : 0.0f;
     const float cap_out = a.softcap * kLog2e, scale = a.scale * kLog2e;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
+    uint32_t buf = 0, turn = 0, before = 0, before_turn = 0;
     for (int i = 0; i < tiles; ++i) {
       const int mask = i % kMasks;
       if (!wait_or_stop(&sh.masks[mask], (i / kMasks) & 1, stop)) break;
-      if (!wait_or_stop(&sh.s_full[i & 1], (i >> 1) & 1, stop)) break;
+      if (!wait_or_stop(&sh.s_full[buf], turn, stop)) break;
       tc_fence_after();
-      const uint32_t s_at = tmem + (i & 1) * kKeys + lanes;
+      const uint32_t s_at = tmem + buf * kKeys + lanes;
       float z[kPart];
       float high = __int_as_float(0xff800000);
 #pragma unroll
@@ -344,7 +356,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
         top = moved;
         sum *= factor;
         if (i > 0) {
-          if (!wait_or_stop(&sh.pv_done, (i - 1) & 1, stop)) break;
+          if (!wait_or_stop(&sh.pv_done[before], before_turn, stop)) break;
           tc_fence_after();
           for (int c = 0; c < a.Dv; c += 16) {  // past Dv: columns that nothing reads, within the allocation
             uint32_t v[16];
@@ -380,9 +392,11 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&sh.p_full[i & 1]);
+      mbar_arrive(&sh.p_full[buf]);
+      before = buf, before_turn = turn;
+      if (++buf == static_cast<uint32_t>(p.bufs)) buf = 0, turn ^= 1;
     }
-    if (tiles > 0) wait_or_stop(&sh.pv_done, (tiles - 1) & 1, stop);
+    if (tiles > 0) wait_or_stop(&sh.pv_done[before], before_turn, stop);
     tc_fence_after();
     const bool failed = *stop != 0;  // a wait ran out: the rows become NaN
     sh.top[threadIdx.x] = failed ? 0.0f : top;
@@ -425,8 +439,12 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   __syncthreads();
 
   // ---- write, or join the CTAs first ----
-  // Eight outputs per item.
-  const int per_row = a.Dv / 8, items = heads * per_row;
+  // Eight outputs per thread and step; a step of a warp takes as many whole
+  // rows as fit its lanes (Dv <= 256: one at least).
+  const int per_row = a.Dv / 8, at_once = 32 / per_row;
+  const int sub_row = lane / per_row, c = (lane - sub_row * per_row) * 8;
+  const int step = 9 * at_once;
+  const int row0 = sub_row < at_once ? warp * at_once + sub_row : heads;
   E* out = static_cast<E*>(a.out) + (row * a.Hq + head0) * a.Dv;
   auto write = [&](int h, int c, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(out + static_cast<int64_t>(h) * a.Dv + c) =
@@ -439,8 +457,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   // A row's factor, 1 / its sum of weights: zero where nothing is seen.
   auto inverse = [](float all, float total) { return total != total ? total : is_low(all) ? 0.0f : 1.0f / total; };
   auto logsum = [](float all, float total) { return total != total ? total : is_low(all) ? all : (all + log2f(total)) * kLn2; };
-  for (int i = threadIdx.x; i < items; i += kAttThreads) {
-    const int h = i / per_row, c = (i - h * per_row) * 8;
+  for (int h = row0; h < heads; h += step) {
     float x[8] = {};
 #pragma unroll
     for (int k = 0; k < COPIES; ++k) {
@@ -464,9 +481,8 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   } else {
     cluster_sync();
     const uint32_t top_addr = smem_addr(sh.head_top), sum_addr = smem_addr(sh.head_sum), rows_addr = smem_addr(rows);
-    // the CTAs take items in turn; reads of all CTAs are in flight together
-    for (int i = static_cast<int>(rank) * kAttThreads + threadIdx.x; i < items; i += cluster * kAttThreads) {
-      const int h = i / per_row, c = (i - h * per_row) * 8;
+    // the CTAs take rows in turn; reads of all CTAs are in flight together
+    for (int h = row0 < heads ? row0 + static_cast<int>(rank) * step : heads; h < heads; h += cluster * step) {
       float m[8], l[8];
       float4 u[8], v[8];
 #pragma unroll
@@ -542,6 +558,7 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   p.k_bytes = kKeys * 128 * p.d_blocks;
   p.v_bytes = p.shared ? 0 : kKeys * 128 * p.v_blocks;
   p.tmem_cols = 2 * kKeys + p.v_blocks * 64 <= 256 ? 256 : 512;
+  p.bufs = (p.tmem_cols - p.v_blocks * 64) / kKeys < kMaxBufs ? (p.tmem_cols - p.v_blocks * 64) / kKeys : kMaxBufs;
   const int join = 128 * (p.v_blocks * 64 + 4) * 4;
   const int whole = kMaxShared - static_cast<int>(sizeof(AttShared));
   const int half = kMaxShared / 2 - 1024 - static_cast<int>(sizeof(AttShared));
