@@ -48,6 +48,12 @@ class _AttentionArgs(ctypes.Structure):
                 ("softcap", _f32)]
 
 
+
+def _raw_stream(index: int) -> int:
+    """The handle of the device's current stream, without a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 _FORMATS = {_i32: "i", _i64: "q", _f32: "f", _vp: "P"}
 _BF16, _FP16, _FP32, _E4M3 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
 _I32, _I64, _F64 = torch.int32, torch.int64, torch.float64
@@ -76,11 +82,12 @@ class _Call:
             packed = self.pack(*values)
         except (struct.error, OverflowError) as error:
             raise ValueError(f"{self.name}: an argument is out of range ({error})") from None
+        handle = _raw_stream(index) if stream is None else stream.cuda_stream
         if torch.cuda.current_device() == index:
-            status = fn(packed, _binding._stream_handle(index, stream))
+            status = fn(packed, handle)
         else:
             with torch.cuda.device(index):
-                status = fn(packed, _binding._stream_handle(index, stream))
+                status = fn(packed, handle)
         if status != 0:
             message = _binding.load_library().topk_status_string(status).decode()
             raise _binding.TopkError(status, f"{self.name} failed: {message}")

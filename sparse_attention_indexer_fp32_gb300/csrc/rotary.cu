@@ -9,9 +9,12 @@
 // off by whole turns. Its top 32 bits go to sinpi / cospi as FP32.
 //
 // The work. Memory bound: each element is read and written once, with three
-// operations. A CTA takes a few tokens and heads, 16 bytes per item; it first
-// issues the loads of its first items, then fills a table of (cos, sin) of its
-// tokens in shared memory, once for all of their heads, then turns and stores.
+// operations. A thread owns one 16-byte item of the head (two, where the
+// second half's partner goes with it) of one token and walks over heads, so
+// that it computes its pairs' cos and sin once, in registers, while its first
+// loads are in flight; no shared memory, no barrier. (A table per CTA in shared
+// memory put two barriers between loads and stores: 87 us instead of XXX for
+// 8192 tokens x 64 heads x 128, bf16.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -24,9 +27,7 @@ namespace tki {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotUnroll = 4;        // items of one thread whose loads are in flight together
-constexpr int kRotTable = 2048;      // (cos, sin) pairs of a CTA's tokens: 16 KiB
-constexpr int kRotMaxPairs = SPARSE_ROTARY_MAX_D / 2;
+constexpr int kRotUnroll = 4;  // items of one thread whose loads are in flight together
 
 struct RotParams {
   const void* x;
@@ -40,15 +41,13 @@ struct RotParams {
   int32_t page_size;
   int32_t T, H, D, rotated, offset;
   int32_t positions_64;
-  int32_t turn_items, items;       // per head: items that turn pairs, and with those that copy
-  int32_t tokens, heads;           // per CTA
+  int32_t turn_items, items;  // per head: items that turn pairs, and with those that copy
+  int32_t rows;               // rows (a token's head) that a CTA has side by side
+  int32_t tokens, heads;      // tokens per CTA, heads of each side by side: tokens * heads <= rows
+  int32_t head_span;          // heads per CTA, in steps of `heads`
   int32_t head_chunks;
-  uint32_t inv_items, inv_heads;   // reciprocals for quotients of small numbers
   float scale, sign;
 };
-
-// e / d for e, d < 2^16 and inv = floor(2^32 / d) + 1 (0 stands for d = 1).
-__device__ __forceinline__ uint32_t quotient(uint32_t e, uint32_t inv) { return inv == 0 ? e : __umulhi(e, inv); }
 
 // f / 2 pi as a fraction of a turn, times 2^64, modulo 2^64. The mantissa m of
 // f = m 2^(e - 1075) is multiplied by round(2^66 / 2 pi) into 117 bits and
@@ -97,135 +96,97 @@ struct alignas(sizeof(E) * V) Vec {
 };
 
 // V elements per item side. HALF: an item that turns holds V elements of the
-// first half and V of the second; otherwise V consecutive ones (V / 2 pairs;
-// V = 2 where nothing is aligned). Items after `turn_items` copy V elements
-// of the head's rest (one, where V is the unaligned variant's).
+// first half and V of the second; otherwise V consecutive ones (V / 2 pairs).
+// V = 2 where nothing is aligned: one pair, or one copied element, an item.
 template <typename E, int V, bool HALF>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotParams p) {
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotParams p) {
   constexpr bool kVector = sizeof(E) * V == 16;
-  constexpr int kCopy = kVector ? V : 1;
+  constexpr int kPairs = !kVector ? 1 : HALF ? V : V / 2;  // of an item
   using VecT = Vec<E, V>;
-  __shared__ uint64_t rate[kRotMaxPairs];
-  __shared__ float2 table[kRotTable];
+  const int n = min(p.items, kRotThreads);
+  const int sub = threadIdx.x / n;
+  const int i = blockIdx.y * kRotThreads + (threadIdx.x - sub * n);
+  const int tsub = sub / p.heads;
+  const unsigned group = blockIdx.x / static_cast<unsigned>(p.head_chunks);
+  const int h0 = static_cast<int>(blockIdx.x - group * p.head_chunks) * p.head_span;
+  const int64_t t = static_cast<int64_t>(group) * p.tokens + tsub;
+  if (i >= p.items || tsub >= p.tokens || t >= p.T) return;
   const int pairs = p.rotated / 2;
-  const int64_t chunk = blockIdx.x;
-  const int t0 = static_cast<int>(chunk / p.head_chunks) * p.tokens;
-  const int h0 = static_cast<int>(chunk % p.head_chunks) * p.heads;
-  const int nt = min(p.tokens, p.T - t0), nh = min(p.heads, p.H - h0);
-  const int total = nt * p.heads * p.items;
-
-  const E* xb[kRotUnroll];
-  E* ob[kRotUnroll];
-  VecT a[kRotUnroll], b[kRotUnroll];
-  int item[kRotUnroll], tok[kRotUnroll];
-
-  auto load = [&](int base) {
-#pragma unroll
-    for (int u = 0; u < kRotUnroll; ++u) {
-      const uint32_t e = base + u * kRotThreads + threadIdx.x;
-      item[u] = -1;
-      if (e >= static_cast<uint32_t>(total)) continue;
-      const uint32_t th = quotient(e, p.inv_items);
-      const int i = static_cast<int>(e - th * p.items);
-      const uint32_t tt = quotient(th, p.inv_heads);
-      const int hh = static_cast<int>(th - tt * p.heads);
-      if (hh >= nh) continue;
-      const int64_t t = t0 + static_cast<int>(tt), h = h0 + hh;
-      E* o;
-      if (p.slots != nullptr) {
-        const int32_t s = p.slots[t];
-        if (s < 0 || s >= p.num_slots) continue;
-        const int32_t page = s / p.page_size;
-        o = static_cast<E*>(p.out) + page * p.out_page + (s - page * p.page_size) * p.out_token + h * p.out_head;
-      } else {
-        o = static_cast<E*>(p.out) + t * p.out_token + h * p.out_head;
-      }
-      const E* x = static_cast<const E*>(p.x) + t * p.x_token + h * p.x_head;
-      item[u] = i;
-      tok[u] = static_cast<int>(tt);
-      int at;
-      if (i < p.turn_items) {
-        at = p.offset + i * (HALF && !kVector ? 1 : V);
-        if constexpr (kVector) {
-          a[u] = *reinterpret_cast<const VecT*>(x + at);
-          if (HALF) b[u] = *reinterpret_cast<const VecT*>(x + at + pairs);
-        } else {
-          a[u].e[0] = x[at];
-          a[u].e[1] = x[at + (HALF ? pairs : 1)];
-        }
-      } else {
-        at = (i - p.turn_items) * kCopy;
-        if (at >= p.offset) at += p.rotated;
-        if constexpr (kVector)
-          a[u] = *reinterpret_cast<const VecT*>(x + at);
-        else
-          a[u].e[0] = x[at];
-      }
-      xb[u] = x;
-      ob[u] = o + at;
-    }
-  };
-
-  auto store = [&]() {
-#pragma unroll
-    for (int u = 0; u < kRotUnroll; ++u) {
-      if (item[u] < 0) continue;
-      E* o = ob[u];
-      if (item[u] >= p.turn_items) {
-        if constexpr (kVector)
-          *reinterpret_cast<VecT*>(o) = a[u];
-        else
-          o[0] = a[u].e[0];
-        continue;
-      }
-      if constexpr (!kVector) {
-        const float2 cs = table[tok[u] * pairs + item[u]];
-        const float r = Elem<E>::get(a[u].e[0]), s = Elem<E>::get(a[u].e[1]);
-        o[0] = Elem<E>::put(r * cs.x - s * cs.y);
-        o[HALF ? pairs : 1] = Elem<E>::put(s * cs.x + r * cs.y);
-      } else if constexpr (HALF) {
-        const float2* cs = table + tok[u] * pairs + item[u] * V;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float2 c = cs[j];
-          const float r = Elem<E>::get(a[u].e[j]), s = Elem<E>::get(b[u].e[j]);
-          a[u].e[j] = Elem<E>::put(r * c.x - s * c.y);
-          b[u].e[j] = Elem<E>::put(s * c.x + r * c.y);
-        }
-        *reinterpret_cast<VecT*>(o) = a[u];
-        *reinterpret_cast<VecT*>(o + pairs) = b[u];
-      } else {
-        const float2* cs = table + tok[u] * pairs + item[u] * (V / 2);
-#pragma unroll
-        for (int j = 0; j < V; j += 2) {
-          const float2 c = cs[j / 2];
-          const float r = Elem<E>::get(a[u].e[j]), s = Elem<E>::get(a[u].e[j + 1]);
-          a[u].e[j] = Elem<E>::put(r * c.x - s * c.y);
-          a[u].e[j + 1] = Elem<E>::put(s * c.x + r * c.y);
-        }
-        *reinterpret_cast<VecT*>(o) = a[u];
-      }
-    }
-  };
-
-  load(0);
-  for (int i = threadIdx.x; i < pairs; i += kRotThreads) rate[i] = turns_of(p.frequencies[i]);
-  __syncthreads();
-  for (int e = threadIdx.x; e < nt * pairs; e += kRotThreads) {
-    const int tt = e / pairs, i = e - tt * pairs;
-    const int64_t pos = p.positions_64 ? static_cast<const int64_t*>(p.positions)[t0 + tt]
-                                       : static_cast<const int32_t*>(p.positions)[t0 + tt];
-    const uint64_t turn = static_cast<uint64_t>(pos) * rate[i];
-    const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    table[e] = make_float2(c * p.scale, s * p.sign);
+  const bool turns = i < p.turn_items;
+  int at;  // of the item in its head
+  if (turns) {
+    at = p.offset + i * (HALF && !kVector ? 1 : V);
+  } else {
+    at = (i - p.turn_items) * (kVector ? V : 1);
+    if (at >= p.offset) at += p.rotated;
   }
-  __syncthreads();
-  store();
-  for (int base = kRotUnroll * kRotThreads; base < total; base += kRotUnroll * kRotThreads) {
-    load(base);
-    store();
+  const E* x = static_cast<const E*>(p.x) + t * p.x_token + at;
+  E* o;
+  if (p.slots != nullptr) {
+    const int32_t s = p.slots[t];
+    if (s < 0 || s >= p.num_slots) return;
+    const int32_t page = s / p.page_size;
+    o = static_cast<E*>(p.out) + page * p.out_page + (s - page * p.page_size) * p.out_token + at;
+  } else {
+    o = static_cast<E*>(p.out) + t * p.out_token + at;
+  }
+  const int partner = HALF ? pairs : 1;  // of the unaligned item's first element
+
+  VecT a[kRotUnroll], b[kRotUnroll];
+  const int end = min(h0 + p.head_span, p.H);
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kRotUnroll; ++u) {
+      const int hu = h + u * p.heads;
+      if (hu >= end) break;
+      const E* from = x + hu * p.x_head;
+      if constexpr (kVector) {
+        a[u] = *reinterpret_cast<const VecT*>(from);
+        if (HALF && turns) b[u] = *reinterpret_cast<const VecT*>(from + pairs);
+      } else {
+        a[u].e[0] = from[0];
+        if (turns) a[u].e[1] = from[partner];
+      }
+    }
+  };
+  int h = h0 + sub - tsub * p.heads;
+  load(h);
+  float cosines[kPairs], sines[kPairs];
+  if (turns) {
+    const int64_t pos = p.positions_64 ? static_cast<const int64_t*>(p.positions)[t] : static_cast<const int32_t*>(p.positions)[t];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      const uint64_t turn = static_cast<uint64_t>(pos) * turns_of(p.frequencies[i * kPairs + j]);
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sines[j], &cosines[j]);
+      cosines[j] *= p.scale, sines[j] *= p.sign;
+    }
+  }
+  while (h < end) {
+#pragma unroll
+    for (int u = 0; u < kRotUnroll; ++u) {
+      const int hu = h + u * p.heads;
+      if (hu >= end) break;
+      E* to = o + hu * p.out_head;
+      if (turns) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          E& first = a[u].e[HALF ? j : 2 * j];
+          E& second = HALF && kVector ? b[u].e[j] : a[u].e[2 * j + 1];
+          const float r = Elem<E>::get(first), s = Elem<E>::get(second);
+          first = Elem<E>::put(r * cosines[j] - s * sines[j]);
+          second = Elem<E>::put(s * cosines[j] + r * sines[j]);
+        }
+      }
+      if constexpr (kVector) {
+        *reinterpret_cast<VecT*>(to) = a[u];
+        if (HALF && turns) *reinterpret_cast<VecT*>(to + pairs) = b[u];
+      } else {
+        to[0] = a[u].e[0];
+        if (turns) to[partner] = a[u].e[1];
+      }
+    }
+    h += kRotUnroll * p.heads;
+    if (h < end) load(h);
   }
 }
 
@@ -256,23 +217,20 @@ topk_status launch_typed(const sparse_rotary_args& a, int sm_count, cudaStream_t
   const int pairs = a.rotated / 2;
   p.turn_items = vec ? (half ? pairs / V : a.rotated / V) : pairs;
   p.items = p.turn_items + (in_place ? 0 : (a.D - a.rotated) / (vec ? V : 1));
-  // Items per CTA: four per thread, so that a thread's loads overlap, once
-  // that still gives every SM several CTAs; one per thread below.
-  const int64_t all = static_cast<int64_t>(a.T) * a.H * p.items;
-  const int want = all >= static_cast<int64_t>(sm_count) * 8 * kRotThreads * kRotUnroll ? kRotThreads * kRotUnroll
-                                                                                        : kRotThreads;
-  p.heads = want / p.items < 1 ? 1 : (want / p.items < a.H ? want / p.items : a.H);
-  p.tokens = want / (p.items * p.heads);
-  if (p.tokens > kRotTable / pairs) p.tokens = kRotTable / pairs;
-  if (p.tokens > a.T) p.tokens = a.T;
-  if (p.tokens < 1) p.tokens = 1;
-  p.head_chunks = (a.H + p.heads - 1) / p.heads;
-  auto reciprocal = [](int d) { return d == 1 ? 0u : static_cast<uint32_t>((1ull << 32) / static_cast<unsigned>(d)) + 1u; };
-  p.inv_items = reciprocal(p.items);
-  p.inv_heads = reciprocal(p.heads);
-  const int64_t grid = static_cast<int64_t>((a.T + p.tokens - 1) / p.tokens) * p.head_chunks;
+  // Heads per thread: eight once that still gives every SM several CTAs, so
+  // that cos and sin are computed once for them; one while SMs would idle.
+  p.rows = p.items < kRotThreads ? kRotThreads / p.items : 1;
+  const int64_t threads = static_cast<int64_t>(a.T) * a.H * p.items;
+  const int steps = threads >= static_cast<int64_t>(sm_count) * kRotThreads * 64  ? 8
+                    : threads >= static_cast<int64_t>(sm_count) * kRotThreads * 8 ? 2
+                                                                                  : 1;
+  p.heads = (a.H + steps - 1) / steps < p.rows ? (a.H + steps - 1) / steps : p.rows;
+  p.tokens = p.rows / p.heads < a.T ? p.rows / p.heads : a.T;
+  p.head_span = p.heads * steps;
+  p.head_chunks = (a.H + p.head_span - 1) / p.head_span;
+  const int64_t grid = (static_cast<int64_t>(a.T) + p.tokens - 1) / p.tokens * p.head_chunks;
   if (grid > INT32_MAX) return TOPK_EINVAL;
-  const unsigned g = static_cast<unsigned>(grid);
+  const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>((p.items + kRotThreads - 1) / kRotThreads));
   if (vec)
     half ? rotary_kernel<E, V, true><<<g, kRotThreads, 0, stream>>>(p)
          : rotary_kernel<E, V, false><<<g, kRotThreads, 0, stream>>>(p);

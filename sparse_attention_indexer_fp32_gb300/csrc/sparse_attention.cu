@@ -533,7 +533,7 @@ topk_status launch_copies(const AttParams& p, int dev, int cluster, int64_t grid
   attr.val.clusterDim.x = static_cast<unsigned>(cluster);
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, p, cluster);
   return err == cudaSuccess ? TOPK_OK : TOPK_ECUDA;
 }
