@@ -157,7 +157,13 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) {
       const uint64_t turn = static_cast<uint64_t>(pos) * turns_of(p.frequencies[i * kPairs + j]);
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sines[j], &cosines[j]);
+      // Within half a turn either way the special function unit is good to
+      // 2^-21, 2^-10 of a 16-bit result's rounding; FP32 takes the full functions.
+      const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+      if constexpr (sizeof(E) == 2)
+        __sincosf(half_turns * 3.14159265f, &sines[j], &cosines[j]);
+      else
+        sincospif(half_turns, &sines[j], &cosines[j]);
       cosines[j] *= p.scale, sines[j] *= p.sign;
     }
   }
@@ -221,9 +227,8 @@ topk_status launch_typed(const sparse_rotary_args& a, int sm_count, cudaStream_t
   // that cos and sin are computed once for them; one while SMs would idle.
   p.rows = p.items < kRotThreads ? kRotThreads / p.items : 1;
   const int64_t threads = static_cast<int64_t>(a.T) * a.H * p.items;
-  const int steps = threads >= static_cast<int64_t>(sm_count) * kRotThreads * 64  ? 8
-                    : threads >= static_cast<int64_t>(sm_count) * kRotThreads * 8 ? 2
-                                                                                  : 1;
+  const int64_t slots = static_cast<int64_t>(sm_count) * kRotThreads;
+  const int steps = threads >= 32 * slots ? 8 : threads >= 16 * slots ? 4 : threads >= 8 * slots ? 2 : 1;
   p.heads = (a.H + steps - 1) / steps < p.rows ? (a.H + steps - 1) / steps : p.rows;
   p.tokens = p.rows / p.heads < a.T ? p.rows / p.heads : a.T;
   p.head_span = p.heads * steps;
