@@ -4,16 +4,17 @@
 //   out[b, t, s] = ks[s] sum_h w[b, t, h] max(0, q[b, t, h] . k[s])
 //
 // The products run on the tensor cores with the keys as the rows: a tile of
-// 128 positions (TMEM lanes) by the heads of up to 16 query tokens (columns,
+// 128 positions (TMEM lanes) by the heads of up to 8 query tokens (columns,
 // 256 at most). So one thread of the epilogue holds all the products of one
-// position, and the sum over heads needs no exchange: a maximum and half a
-// packed multiply-add per product. A tile of keys is fetched once for all
+// position, and the sum over heads needs no exchange: a maximum and a
+// multiply-add per product (packed multiply-adds cost a move each, 4.6
+// instructions a product in all). A tile of keys is fetched once for all
 // query tokens of its group.
 //
 // One CTA per SM, 13 warps: four fetch keys through the page table into a
 // ring (16-byte asynchronous copies, zeros for absent rows and for the
 // padding of D), one thread issues the products into two TMEM buffers, two
-// groups of four warps take the buffers in turn. Work units are (sequence,
+// groups of four warps sum over heads. Work units are (sequence,
 // range of tiles, group of query tokens); queries, weights and lengths of the
 // next unit are fetched while this one runs.
 #include <cuda_bf16.h>
@@ -33,22 +34,23 @@ namespace {
 constexpr int kTile = 128;             // positions per tile: the rows of one product
 constexpr int kScoreThreads = 13 * 32;
 constexpr int kEpilogueWarps = 8;
-constexpr int kMaxTokens = 16;         // query tokens per group
+constexpr int kMaxTokens = 8;          // query tokens per group
 constexpr int kMaxCols = 256;
 
 struct ScoreParams {
   sparse_scores_args a;
-  int32_t hp;              // heads of a token, padded to whole column steps
+  int32_t hp;              // heads of a token, padded to 32, 64 or 128
   int32_t tokens;          // query tokens per group
   int32_t cols;            // tokens * hp
   int32_t blocks;          // 128-byte blocks per key: 1 or 2
   int32_t row_units;       // 16-byte units of D
   int32_t unit_tiles;      // tiles per work unit
   int32_t chunks, groups;  // work units per sequence: chunks x groups
-  int64_t units;
-  bool q_vector;           // queries can be fetched 16 bytes at a time
-  int32_t box_rows;        // entries of one page per box of the tensor map
-  CUtensorMap map;         // of the keys, where boxes are used
+  uint32_t units;
+  bool q_boxes;            // queries come by the TMA engine ...
+  bool q_vector;           // ... or 16 bytes at a time, else element by element
+  int32_t box_rows;        // entries of one page per box of the keys' map, 0 without one
+  CUtensorMap map, q_map;
 };
 
 struct ScoreShared {
@@ -69,29 +71,23 @@ __device__ __forceinline__ int length_of(const ScoreParams& p, int b, int t) {
   return n < 0 ? 0 : min(static_cast<int64_t>(n), p.a.width);
 }
 
-__device__ __forceinline__ Unit unit_of(const ScoreParams& p, int64_t u) {
+__device__ __forceinline__ Unit unit_of(const ScoreParams& p, uint32_t u) {
   Unit r;
-  const int64_t c = u / p.groups;
+  const uint32_t c = u / static_cast<uint32_t>(p.groups);
   r.t0 = static_cast<int>(u - c * p.groups) * p.tokens;
-  r.b = static_cast<int>(c / p.chunks);
+  r.b = static_cast<int>(c / static_cast<uint32_t>(p.chunks));
   r.tokens = min(p.tokens, p.a.T - r.t0);
   const int lane = threadIdx.x & 31;
   const int longest = __reduce_max_sync(0xffffffffu, lane < r.tokens ? length_of(p, r.b, r.t0 + lane) : 0);
-  r.tile0 = static_cast<int>(c - static_cast<int64_t>(r.b) * p.chunks) * p.unit_tiles;
+  r.tile0 = static_cast<int>(c - static_cast<uint32_t>(r.b) * p.chunks) * p.unit_tiles;
   r.tile1 = min(r.tile0 + p.unit_tiles, longest / kTile + (longest % kTile != 0));
   return r;
 }
 
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
-}
-// max(0, x), a NaN kept, of two products.
-__device__ __forceinline__ uint64_t relu2(uint32_t x, uint32_t y) {
-  uint64_t r;
-  asm("{\n\t.reg .f32 a, b;\n\tmax.NaN.f32 a, %1, 0f00000000;\n\tmax.NaN.f32 b, %2, 0f00000000;\n\t"
-      "mov.b64 %0, {a, b};\n\t}"
-      : "=l"(r)
-      : "f"(__uint_as_float(x)), "f"(__uint_as_float(y)));
+// max(0, x), a NaN kept. Volatile: it stays behind the wait for the products.
+__device__ __forceinline__ float relu(uint32_t x) {
+  float r;
+  asm volatile("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(__uint_as_float(x)));
   return r;
 }
 
@@ -113,39 +109,60 @@ struct Kind<__nv_fp8_e4m3> {
   static constexpr CUtensorMapDataType map_type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 };
 
-// Queries, weights and lengths of a unit into buffer `buf`, by `n` threads.
-template <typename E>
+// Queries, weights and lengths of a unit into buffer `buf`, by N threads, each
+// of which arrives twice on q_full.
+template <typename E, int N>
 __device__ __forceinline__ void fetch_queries(const ScoreParams& p, const Unit& r, unsigned char* smem, uint32_t q_bytes,
-                                              ScoreShared& sh, uint32_t buf, int th, int n, const void* nowhere) {
-  const E* q = static_cast<const E*>(p.a.q) + r.b * p.a.q_seq_stride;
-  const int units = p.blocks * 8;
-  for (int i = th; i < p.cols * units; i += n) {
-    const int col = i / units, j = i - col * units;
-    const int t = col / p.hp, h = col - t * p.hp;
-    const bool real = t < r.tokens && h < p.a.H && j < p.row_units;
-    const E* src = real ? q + (r.t0 + t) * p.a.q_token_stride + h * p.a.q_head_stride + j * (16 / sizeof(E)) : nullptr;
-    const uint32_t at = buf * q_bytes + (j >> 3) * p.cols * 128 + swizzled(col, j & 7);
-    if (p.q_vector) {
-      copy16(smem_addr(smem) + at, real ? src : nowhere, real);
+                                              ScoreShared& sh, uint32_t buf, int th, const void* nowhere) {
+  if (p.q_boxes) {
+    if (th == 0) {
+      mbar_arrive_expect_tx(&sh.q_full[buf], q_bytes);
+      for (int c = 0; c < p.blocks; ++c)
+        box_load(smem_addr(smem) + buf * q_bytes + c * p.cols * 128, &p.q_map, c * (128 / static_cast<int>(sizeof(E))), 0,
+                 r.t0, r.b, &sh.q_full[buf]);
     } else {
-      E v[16 / sizeof(E)];
-      for (int e = 0; e < static_cast<int>(16 / sizeof(E)); ++e) v[e] = real ? src[e] : E(0.0f);
-      *reinterpret_cast<uint4*>(smem + at) = *reinterpret_cast<const uint4*>(v);
+      mbar_arrive(&sh.q_full[buf]);
     }
+  } else {
+    const int unit16 = th & 7;
+    for (int t = 0; t < p.tokens; ++t)
+      for (int h = th >> 3; h < p.hp; h += N / 8) {
+        const E* q = static_cast<const E*>(p.a.q) + r.b * p.a.q_seq_stride + (r.t0 + t) * p.a.q_token_stride +
+                     h * p.a.q_head_stride;
+        for (int c = 0; c < p.blocks; ++c) {
+          const int j = c * 8 + unit16;
+          const bool real = t < r.tokens && h < p.a.H && j < p.row_units;
+          const E* src = q + j * (16 / sizeof(E));
+          const uint32_t at = buf * q_bytes + c * p.cols * 128 + swizzled(t * p.hp + h, unit16);
+          if (p.q_vector) {
+            copy16(smem_addr(smem) + at, real ? src : nowhere, real);
+          } else {
+            E v[16 / sizeof(E)];
+            for (int e = 0; e < static_cast<int>(16 / sizeof(E)); ++e) v[e] = real ? src[e] : E(0.0f);
+            *reinterpret_cast<uint4*>(smem + at) = *reinterpret_cast<const uint4*>(v);
+          }
+        }
+      }
+    copy_arrive(&sh.q_full[buf]);
   }
-  for (int i = th; i < p.cols; i += n) {
-    const int t = i / p.hp, h = i - t * p.hp;
-    sh.weights[buf][i] =
-        t < r.tokens && h < p.a.H ? p.a.weights[(static_cast<int64_t>(r.b) * p.a.T + r.t0 + t) * p.a.H + h] : 0.0f;
-  }
+  const float* w = p.a.weights + (static_cast<int64_t>(r.b) * p.a.T + r.t0) * p.a.H;
+  for (int t = 0; t < p.tokens; ++t)
+    for (int h = th; h < p.hp; h += N) sh.weights[buf][t * p.hp + h] = t < r.tokens && h < p.a.H ? w[t * p.a.H + h] : 0.0f;
   if (th < kMaxTokens) sh.lengths[buf][th] = th < r.tokens ? length_of(p, r.b, r.t0 + th) : 0;
-  copy_arrive(&sh.q_full[buf]);
   mbar_arrive(&sh.q_full[buf]);
 }
 
-// STAGES tiles of keys in flight; STEP columns per TMEM load; keys by BOXES of
+// No copy may arrive after the CTA has left.
+__device__ __forceinline__ void queries_arrived(ScoreShared& sh, uint32_t nu) {
+  for (uint32_t i = 0; i < 2 && i < nu; ++i)
+    mbar_wait_bounded(&sh.q_full[(nu - 1 - i) & 1], ((nu - 1 - i) >> 1) & 1, 1000000000ull);
+  copy_commit();
+  copy_wait<0>();
+}
+
+// STAGES tiles of keys in flight; PER loads of 32 columns a token; keys by BOXES of
 // the TMA engine or by 16-byte copies.
-template <typename E, int STAGES, int STEP, bool BOXES>
+template <typename E, int STAGES, int PER, bool BOXES>
 __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_constant__ ScoreParams p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -161,7 +178,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       mbar_init(&sh.q_full[i], BOXES ? 192 : 256);  // the copies' arrivals and the stores'
       mbar_init(&sh.q_empty[i], 1 + kEpilogueWarps);
       mbar_init(&sh.t_full[i], 1);
-      mbar_init(&sh.t_empty[i], 128);
+      mbar_init(&sh.t_empty[i], p.tokens > 1 ? 256 : 128);
     }
     sh.stop = 0;
     fence_mbar_init();
@@ -181,7 +198,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
     const bool mine = box < boxes && block < p.blocks;
     uint32_t k = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+    for (uint32_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
       const Unit r = unit_of(p, u);
       if (r.tile0 >= r.tile1) continue;
       const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
@@ -213,22 +230,21 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
   } else if (BOXES && warp > 8 && warp < 12) {
     // ---- queries, a unit ahead ----
     uint32_t nu = 0;
-    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+    for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
       const Unit r = unit_of(p, u);
       if (r.tile0 >= r.tile1) continue;
       if (!wait_or_stop(&sh.q_empty[nu & 1], ((nu >> 1) & 1) ^ 1, stop)) break;
-      fetch_queries<E>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - 288, 96, nowhere);
+      fetch_queries<E, 96>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - 288, nowhere);
       ++nu;
     }
-    copy_commit();
-    copy_wait<0>();
+    queries_arrived(sh, nu);
   } else if (!BOXES && warp >= 8 && warp < 12) {
     // ---- keys and queries, by 16-byte copies: 8 lanes fetch a row's 128 bytes ----
     const int w = warp - 8;
     const uint32_t unit16 = lane & 7;
     uint32_t k = 0, nu = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+    for (uint32_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
       const Unit r = unit_of(p, u);
       if (r.tile0 >= r.tile1) continue;
       const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
@@ -241,7 +257,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       int32_t next = page_at(r.tile0);  // read a tile ahead
       ok = wait_or_stop(&sh.q_empty[nu & 1], ((nu >> 1) & 1) ^ 1, stop);
       if (!ok) break;
-      fetch_queries<E>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - 256, 128, nowhere);
+      fetch_queries<E, 128>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - 256, nowhere);
       ++nu;
       for (int tile = r.tile0; tile < r.tile1; ++tile, ++k) {
         const uint32_t stage = k % STAGES;
@@ -269,42 +285,45 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
         copy_arrive(&sh.full[stage]);
       }
     }
-    copy_commit();
-    copy_wait<0>();
+    queries_arrived(sh, nu);
   } else if (warp == 12) {
     // ---- products ----
     const uint32_t desc = mma_desc(Kind<E>::type, p.cols);
-    uint32_t k = 0, nu = 0;
+    const uint64_t ring_desc = operand_desc(ring_addr), q_desc = operand_desc(q_addr);
+    uint32_t k = 0, nu = 0, stage = 0, turn = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+    for (uint32_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
       const Unit r = unit_of(p, u);
       if (r.tile0 >= r.tile1) continue;
       const uint32_t buf = nu & 1;
       ok = wait_or_stop(&sh.q_full[buf], (nu >> 1) & 1, stop);
       ++nu;
+      if (!p.q_boxes) fence_proxy_async_smem();  // copies and stores are in; now the tensor cores may see them
       for (int tile = r.tile0; tile < r.tile1 && ok; ++tile, ++k) {
-        const uint32_t stage = k % STAGES, tb = k & 1;
-        ok = wait_or_stop(&sh.t_empty[tb], ((k >> 1) & 1) ^ 1, stop) &&
-             wait_or_stop(&sh.full[stage], (k / STAGES) & 1, stop);
+        const uint32_t tb = k & 1;
+        ok = wait_or_stop(&sh.t_empty[tb], ((k >> 1) & 1) ^ 1, stop) && wait_or_stop(&sh.full[stage], turn, stop);
         if (!ok) break;
-        fence_proxy_async_smem();  // the 16-byte copies are in; now the tensor cores may see them
+        if (!BOXES) fence_proxy_async_smem();
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
+          const uint64_t da = ring_desc + (stage * tile_bytes >> 4), db = q_desc + (buf * q_bytes >> 4);
+          const uint32_t to = tmem + tb * kMaxCols;
           for (int c = 0; c < p.blocks; ++c)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint64_t da = operand_desc(ring_addr + stage * tile_bytes + c * kTile * 128 + j * 32);
-              const uint64_t db = operand_desc(q_addr + buf * q_bytes + c * p.cols * 128 + j * 32);
+              const uint64_t a = da + static_cast<uint32_t>(c * (kTile * 128 >> 4) + j * 2);
+              const uint64_t b = db + static_cast<uint32_t>(c * (p.cols * 128 >> 4) + j * 2);
               if constexpr (sizeof(E) == 1)
-                mma_f8(tmem + tb * kMaxCols, da, db, desc, c + j > 0);
+                mma_f8(to, a, b, desc, c + j > 0);
               else
-                mma_f16(tmem + tb * kMaxCols, da, db, desc, c + j > 0);
+                mma_f16(to, a, b, desc, c + j > 0);
             }
           mma_commit(&sh.empty[stage]);
           mma_commit(&sh.t_full[tb]);
           if (tile + 1 == r.tile1) mma_commit(&sh.q_empty[buf]);
         }
         __syncwarp();
+        if (++stage == STAGES) stage = 0, turn ^= 1;
       }
     }
     // every product is complete before the memory it uses goes away
@@ -312,16 +331,23 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       wait_or_stop(&sh.t_full[(k - 1 - i) & 1], ((k - 1 - i) >> 1) & 1, stop);
   } else {
     // ---- sums over heads ----
+    // Two groups of four warps: they share every tile's tokens where there
+    // are several, and take tiles in turn where there is one.
     const int group = warp >> 2, quarter = warp & 3;
+    const bool share = p.tokens > 1;
+    const int tile_step = share ? 1 : 2;
+    const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
     uint32_t k = 0, nu = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+    for (uint32_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
       const Unit r = unit_of(p, u);
       if (r.tile0 >= r.tile1) continue;
       const uint32_t buf = nu & 1;
       ok = wait_or_stop(&sh.q_full[buf], (nu >> 1) & 1, stop);
       if (!ok) break;
       ++nu;
+      const int t_mid = share ? (r.tokens + 1) / 2 : r.tokens;
+      const int t_first = share && group == 1 ? t_mid : 0, t1 = share && group == 1 ? r.tokens : t_mid;
       float* out = p.a.out + r.b * p.a.out_seq_stride + r.t0 * p.a.out_token_stride;
       const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
       auto entry = [&](int tile) -> int64_t { return static_cast<int64_t>(tile) * kTile + quarter * 32 + lane; };
@@ -329,46 +355,75 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
         const int64_t s = entry(tile);
         return tile < r.tile1 && s < p.a.width ? table[static_cast<int32_t>(s) / p.a.page_size] : -1;
       };
-      const int mine = r.tile0 + static_cast<int>((k ^ group) & 1);  // this group's tiles: every other one
+      const uint32_t skip = share ? 0 : (k ^ group) & 1;
+      const int mine = r.tile0 + static_cast<int>(skip);
       int32_t next = page_at(mine);
       const uint32_t k0 = k;
-      k += mine - r.tile0;
-      for (int tile = mine; tile < r.tile1; tile += 2, k += 2) {
+      k += skip;
+      for (int tile = mine; tile < r.tile1; tile += tile_step, k += tile_step) {
         const int64_t s = entry(tile);
         const int32_t page = next;
-        next = page_at(tile + 2);
+        next = page_at(tile + tile_step);
         const bool absent = page < 0 || page >= p.a.num_pages;
         float scale = 1.0f;
         if (!absent && p.a.key_scales != nullptr)
           scale = p.a.key_scales[static_cast<int64_t>(page) * p.a.page_size + static_cast<int32_t>(s) % p.a.page_size];
-        ok = wait_or_stop(&sh.t_full[group], (k >> 1) & 1, stop);
+        const uint32_t tb = k & 1;
+        ok = wait_or_stop(&sh.t_full[tb], (k >> 1) & 1, stop);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t at = tmem + group * kMaxCols + (static_cast<uint32_t>(quarter) << 21);
-        for (int t = 0; t < r.tokens; ++t) {
-          uint64_t acc[4] = {};
-          const float* wt = sh.weights[buf] + t * p.hp;
-          for (int c = 0; c < p.hp; c += STEP) {
-            uint32_t v[STEP];
-            tmem_ld(v, at + t * p.hp + c);
-            tmem_wait_ld(v);
+        // This group's columns, 32 at a time, the next ones on their way while
+        // these are summed.
+        int left = (t1 - t_first) * PER;
+        if (left == 0) {
+          mbar_arrive(&sh.t_empty[tb]);
+          continue;
+        }
+        uint32_t at = tmem + tb * kMaxCols + lanes + t_first * p.hp;
+        const float* wt = sh.weights[buf] + t_first * p.hp;
+        const int32_t* length = sh.lengths[buf] + t_first;
+        float* o = out + t_first * p.a.out_token_stride + s;
+        float acc[4] = {};
+        uint32_t v0[32], v1[32];
+        auto release = [&]() {  // the buffer is read: the next product may have it
+          tc_fence_before();
+          mbar_arrive(&sh.t_empty[tb]);
+        };
+        auto add = [&](const uint32_t (&v)[32], const float* w) {
 #pragma unroll
-            for (int j = 0; j < STEP; j += 4) {
-              const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(wt + c + j);
-              fma2(acc[(j / 2) & 3], relu2(v[j], v[j + 1]), ww.x);
-              fma2(acc[(j / 2 + 1) & 3], relu2(v[j + 2], v[j + 3]), ww.y);
-            }
+          for (int j = 0; j < 32; j += 4) {
+            const float4 ww = *reinterpret_cast<const float4*>(w + j);
+            acc[0] = fmaf(ww.x, relu(v[j]), acc[0]);
+            acc[1] = fmaf(ww.y, relu(v[j + 1]), acc[1]);
+            acc[2] = fmaf(ww.z, relu(v[j + 2]), acc[2]);
+            acc[3] = fmaf(ww.w, relu(v[j + 3]), acc[3]);
           }
-          float sum = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            sum += __uint_as_float(static_cast<uint32_t>(acc[j])) + __uint_as_float(static_cast<uint32_t>(acc[j] >> 32));
-          if (t == r.tokens - 1) {  // the buffer is read: the next product may have it
-            tc_fence_before();
-            mbar_arrive(&sh.t_empty[group]);
+        };
+        auto finish = [&]() {
+          if (s < *length) *o = absent ? __int_as_float(0xff800000) : ((acc[0] + acc[1]) + (acc[2] + acc[3])) * scale;
+          acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+          ++length, o += p.a.out_token_stride;
+        };
+        tmem_ld(v0, at);
+        for (;; left -= 2, at += 64, wt += 64) {
+          tmem_wait_ld();
+          if (left > 1) {
+            tmem_ld(v1, at + 32);
+          } else {
+            release();
           }
-          if (s < sh.lengths[buf][t])
-            out[t * p.a.out_token_stride + s] = absent ? __int_as_float(0xff800000) : sum * scale;
+          add(v0, wt);
+          if (PER == 1) finish();
+          if (PER == 1 && left == 1) break;
+          tmem_wait_ld();
+          if (left > 2) {
+            tmem_ld(v0, at + 64);
+          } else {
+            release();
+          }
+          add(v1, wt + 32);
+          if (PER <= 2 || (left & 2) != 0) finish();
+          if (left == 2) break;
         }
       }
       k = k0 + (r.tile1 - r.tile0);
@@ -379,7 +434,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   if (*stop != 0) {  // a wait ran out: NaN, not half a result
-    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+    for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
       const Unit r = unit_of(p, u);
       for (int t = 0; t < r.tokens; ++t) {
         const int64_t end = min(static_cast<int64_t>(r.tile1) * kTile, static_cast<int64_t>(length_of(p, r.b, r.t0 + t)));
@@ -394,31 +449,31 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
   }
 }
 
-template <typename E, int STAGES, int STEP, bool BOXES>
+template <typename E, int STAGES, int PER, bool BOXES>
 topk_status launch_variant(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
   static_assert(sizeof(ScoreShared) <= 3072, "barriers and weights");
   const size_t bytes = 2 * static_cast<size_t>(p.cols) * 128 * p.blocks + STAGES * static_cast<size_t>(kTile) * 128 * p.blocks +
                        sizeof(ScoreShared);
-  constexpr auto kernel = scores_kernel<E, STAGES, STEP, BOXES>;
+  constexpr auto kernel = scores_kernel<E, STAGES, PER, BOXES>;
   const topk_status st = allow_shared<kernel>(dev);
   if (st != TOPK_OK) return st;
-  const int64_t grid = p.units < sm_count ? p.units : sm_count;
-  kernel<<<static_cast<unsigned>(grid), kScoreThreads, bytes, stream>>>(p);
+  const unsigned grid = p.units < static_cast<unsigned>(sm_count) ? p.units : static_cast<unsigned>(sm_count);
+  kernel<<<grid, kScoreThreads, bytes, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? TOPK_OK : TOPK_ECUDA;
 }
 
-template <typename E, int STAGES, int STEP>
+template <typename E, int STAGES, int PER>
 topk_status launch_step(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
-  return p.box_rows > 0 ? launch_variant<E, STAGES, STEP, true>(p, dev, sm_count, stream)
-                        : launch_variant<E, STAGES, STEP, false>(p, dev, sm_count, stream);
+  return p.box_rows > 0 ? launch_variant<E, STAGES, PER, true>(p, dev, sm_count, stream)
+                        : launch_variant<E, STAGES, PER, false>(p, dev, sm_count, stream);
 }
 
-template <typename E, int STEP>
+template <typename E, int PER>
 topk_status launch_ring(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
   // The ring gets what the queries leave of 227 KB: 6, 5 or 3 tiles.
-  if (p.cols <= 64) return launch_step<E, 6, STEP>(p, dev, sm_count, stream);
-  if (p.cols <= 128) return launch_step<E, 5, STEP>(p, dev, sm_count, stream);
-  return launch_step<E, 3, STEP>(p, dev, sm_count, stream);
+  if (p.cols <= 64) return launch_step<E, 6, PER>(p, dev, sm_count, stream);
+  if (p.cols <= 128) return launch_step<E, 5, PER>(p, dev, sm_count, stream);
+  return launch_step<E, 3, PER>(p, dev, sm_count, stream);
 }
 
 template <typename E>
@@ -426,7 +481,7 @@ topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cud
   ScoreParams p = {};
   p.a = a;
   const int size = sizeof(E);
-  p.hp = (a.H + 15) / 16 * 16;
+  p.hp = a.H <= 32 ? 32 : a.H <= 64 ? 64 : 128;
   p.tokens = kMaxCols / p.hp < kMaxTokens ? kMaxCols / p.hp : kMaxTokens;
   if (p.tokens > a.T) p.tokens = a.T;
   p.cols = p.tokens * p.hp;
@@ -440,17 +495,26 @@ topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cud
   int64_t per = (all + sm_count - 1) / sm_count;
   p.unit_tiles = static_cast<int32_t>(per < 16 ? per : 16);
   p.chunks = static_cast<int32_t>((tiles + p.unit_tiles - 1) / p.unit_tiles);
-  p.units = static_cast<int64_t>(p.chunks) * p.groups * a.B;
+  const int64_t units = static_cast<int64_t>(p.chunks) * p.groups * a.B;
+  if (units > INT32_MAX) return TOPK_EINVAL;
+  p.units = static_cast<uint32_t>(units);
   p.q_vector = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_seq_stride * size % 16 == 0 &&
                a.q_token_stride * size % 16 == 0 && a.q_head_stride * size % 16 == 0;
   // Boxes hold entries of one page: the largest power of two that divides the
   // page, where it is at least 8, the rows of a swizzle group.
   int rows = a.page_size & -a.page_size;
   rows = rows < kTile ? rows : kTile;
-  const bool boxes = rows >= 8 && paged_map(&p.map, Kind<E>::map_type, size, a.keys, a.D, a.page_size, a.num_pages,
-                                            a.key_token_stride, a.key_page_stride, rows);
-  p.box_rows = boxes ? rows : 0;
-  return p.hp % 32 == 0 ? launch_ring<E, 32>(p, dev, sm_count, stream) : launch_ring<E, 16>(p, dev, sm_count, stream);
+  const int64_t extents[3] = {a.D, a.page_size, a.num_pages}, strides[2] = {a.key_token_stride, a.key_page_stride};
+  const int box[2] = {rows, 1};
+  p.box_rows = rows >= 8 && box_map(&p.map, Kind<E>::map_type, size, a.keys, 3, extents, strides, box) ? rows : 0;
+  // A unit's queries are one box more; heads and tokens that are not there
+  // read as zeros.
+  const int64_t q_extents[4] = {a.D, a.H, a.T, a.B}, q_strides[3] = {a.q_head_stride, a.q_token_stride, a.q_seq_stride};
+  const int q_box[3] = {p.hp, p.tokens, 1};
+  p.q_boxes = box_map(&p.q_map, Kind<E>::map_type, size, a.q, 4, q_extents, q_strides, q_box);
+  if (p.hp == 32) return launch_ring<E, 1>(p, dev, sm_count, stream);
+  if (p.hp == 64) return launch_ring<E, 2>(p, dev, sm_count, stream);
+  return launch_ring<E, 4>(p, dev, sm_count, stream);
 }
 
 }  // namespace

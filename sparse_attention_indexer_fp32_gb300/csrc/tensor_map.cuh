@@ -22,19 +22,28 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// A map of a cache [pages, page_size, D] (strides in elements, `size` bytes
-// each) in boxes of 128 bytes by `rows` entries of one page, written with the
-// 128-byte swizzle. False where the engine cannot do it.
-inline bool paged_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int64_t D,
-                      int64_t page_size, int64_t pages, int64_t token_stride, int64_t page_stride, int rows) {
+// A map of a tensor of `rank` dimensions (innermost first, contiguous; strides
+// of the others in elements of `size` bytes) in boxes of 128 bytes by `rows`
+// by the further extents, written with the 128-byte swizzle; what lies outside
+// the tensor reads as zeros. False where the engine cannot do it.
+inline bool box_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int rank, const int64_t* extents,
+                    const int64_t* strides, const int* box_rows) {
   const auto encode = tensor_map_encoder();
-  if (encode == nullptr || token_stride <= 0 || page_stride <= 0 || pages < 1 || pages > INT32_MAX) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(pages)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(token_stride) * size, static_cast<cuuint64_t>(page_stride) * size};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(rows), 1};
-  const cuuint32_t steps[3] = {1, 1, 1};
-  return encode(map, type, 3, const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  if (encode == nullptr || (reinterpret_cast<uintptr_t>(base) & 15) != 0) return false;
+  cuuint64_t dims[4], bytes[3];
+  cuuint32_t box[4], steps[4];
+  for (int i = 0; i < rank; ++i) {
+    if (extents[i] < 1 || extents[i] > INT32_MAX) return false;
+    dims[i] = static_cast<cuuint64_t>(extents[i]);
+    box[i] = i == 0 ? static_cast<cuuint32_t>(128 / size) : static_cast<cuuint32_t>(box_rows[i - 1]);
+    steps[i] = 1;
+    if (i == 0) continue;
+    const int64_t stride = extents[i] == 1 ? 16 / size : strides[i - 1];  // of one: never used
+    if (stride <= 0 || stride * size % 16 != 0 || stride >= (int64_t{1} << 40) / size) return false;
+    bytes[i - 1] = static_cast<cuuint64_t>(stride) * size;
+  }
+  return encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, bytes, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
