@@ -11,10 +11,10 @@
 // instructions a product in all). A tile of keys is fetched once for all
 // query tokens of its group.
 //
-// One CTA per SM, 13 warps: four fetch keys through the page table into a
-// ring (16-byte asynchronous copies, zeros for absent rows and for the
-// padding of D), one thread issues the products into two TMEM buffers, two
-// groups of four warps sum over heads. Work units are (sequence,
+// One CTA per SM, 21 warps: one fetches keys through the page table into a
+// ring (TMA boxes, zeros for absent rows and for the padding of D) and three
+// queries and weights, or four do both by 16-byte copies; one thread issues the
+// products into two TMEM buffers; sixteen warps sum over heads. Work units are (sequence,
 // range of tiles, group of query tokens); queries, weights and lengths of the
 // next unit are fetched while this one runs.
 #include <cuda_bf16.h>
@@ -32,8 +32,9 @@ namespace tki {
 namespace {
 
 constexpr int kTile = 128;             // positions per tile: the rows of one product
-constexpr int kScoreThreads = 13 * 32;
-constexpr int kEpilogueWarps = 8;
+constexpr int kEpilogueWarps = 16;
+constexpr int kFetchWarp = kEpilogueWarps, kProductWarp = kFetchWarp + 4;
+constexpr int kScoreThreads = (kProductWarp + 1) * 32;
 constexpr int kMaxTokens = 8;          // query tokens per group
 constexpr int kMaxCols = 256;
 
@@ -56,7 +57,8 @@ struct ScoreParams {
 struct ScoreShared {
   float weights[2][kMaxCols];
   int32_t lengths[2][kMaxTokens];
-  uint64_t full[6], empty[6], q_full[2], q_empty[2], t_full[2], t_empty[2];
+  uint64_t full[6], empty[6], q_full[2], q_empty[2];
+  uint64_t t_full[4], t_empty[4];  // of tile k at k % 4: whoever waits on one has seen each of its phases
   uint32_t tmem;
   uint32_t stop;
 };
@@ -160,7 +162,7 @@ __device__ __forceinline__ void queries_arrived(ScoreShared& sh, uint32_t nu) {
   copy_wait<0>();
 }
 
-// STAGES tiles of keys in flight; PER loads of 32 columns a token; keys by BOXES of
+// STAGES tiles of keys in flight; PER loads of 16 columns a token; keys by BOXES of
 // the TMA engine or by 16-byte copies.
 template <typename E, int STAGES, int PER, bool BOXES>
 __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_constant__ ScoreParams p) {
@@ -177,13 +179,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], BOXES ? 192 : 256);  // the copies' arrivals and the stores'
       mbar_init(&sh.q_empty[i], 1 + kEpilogueWarps);
-      mbar_init(&sh.t_full[i], 1);
-      mbar_init(&sh.t_empty[i], p.tokens > 1 ? 256 : 128);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], p.tokens > 1 ? 256 : 128);
     sh.stop = 0;
     fence_mbar_init();
   }
-  if (warp == 12) tmem_alloc(&sh.tmem, 512);
+  if (warp == kProductWarp) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
 
   // what a copy of nothing points at
   const void* nowhere = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p.a.q) & ~static_cast<uintptr_t>(15));
-  if (BOXES && warp == 8) {
+  if (BOXES && warp == kFetchWarp) {
     // ---- keys, by boxes: lane i fetches block i / 16 of the box i % 16 of a tile ----
     const int box = lane & 15, block = lane >> 4, boxes = kTile / p.box_rows;
     const bool mine = box < boxes && block < p.blocks;
@@ -227,20 +228,20 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
     // no box may arrive after the CTA has left
     for (uint32_t i = 0; i < STAGES && i < k; ++i)
       mbar_wait_bounded(&sh.full[(k - 1 - i) % STAGES], ((k - 1 - i) / STAGES) & 1, 1000000000ull);
-  } else if (BOXES && warp > 8 && warp < 12) {
+  } else if (BOXES && warp > kFetchWarp && warp < kProductWarp) {
     // ---- queries, a unit ahead ----
     uint32_t nu = 0;
     for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
       const Unit r = unit_of(p, u);
       if (r.tile0 >= r.tile1) continue;
       if (!wait_or_stop(&sh.q_empty[nu & 1], ((nu >> 1) & 1) ^ 1, stop)) break;
-      fetch_queries<E, 96>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - 288, nowhere);
+      fetch_queries<E, 96>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - (kFetchWarp + 1) * 32, nowhere);
       ++nu;
     }
     queries_arrived(sh, nu);
-  } else if (!BOXES && warp >= 8 && warp < 12) {
+  } else if (!BOXES && warp >= kFetchWarp && warp < kProductWarp) {
     // ---- keys and queries, by 16-byte copies: 8 lanes fetch a row's 128 bytes ----
-    const int w = warp - 8;
+    const int w = warp - kFetchWarp;
     const uint32_t unit16 = lane & 7;
     uint32_t k = 0, nu = 0;
     bool ok = true;
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       int32_t next = page_at(r.tile0);  // read a tile ahead
       ok = wait_or_stop(&sh.q_empty[nu & 1], ((nu >> 1) & 1) ^ 1, stop);
       if (!ok) break;
-      fetch_queries<E, 128>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - 256, nowhere);
+      fetch_queries<E, 128>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - kFetchWarp * 32, nowhere);
       ++nu;
       for (int tile = r.tile0; tile < r.tile1; ++tile, ++k) {
         const uint32_t stage = k % STAGES;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       }
     }
     queries_arrived(sh, nu);
-  } else if (warp == 12) {
+  } else if (warp == kProductWarp) {
     // ---- products ----
     const uint32_t desc = mma_desc(Kind<E>::type, p.cols);
     const uint64_t ring_desc = operand_desc(ring_addr), q_desc = operand_desc(q_addr);
@@ -301,7 +302,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       if (!p.q_boxes) fence_proxy_async_smem();  // copies and stores are in; now the tensor cores may see them
       for (int tile = r.tile0; tile < r.tile1 && ok; ++tile, ++k) {
         const uint32_t tb = k & 1;
-        ok = wait_or_stop(&sh.t_empty[tb], ((k >> 1) & 1) ^ 1, stop) && wait_or_stop(&sh.full[stage], turn, stop);
+        // the buffer is free when tile k - 2 is read
+        ok = (k < 2 || wait_or_stop(&sh.t_empty[(k - 2) & 3], ((k - 2) >> 2) & 1, stop)) &&
+             wait_or_stop(&sh.full[stage], turn, stop);
         if (!ok) break;
         if (!BOXES) fence_proxy_async_smem();
         tc_fence_after();
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
                 mma_f16(to, a, b, desc, c + j > 0);
             }
           mma_commit(&sh.empty[stage]);
-          mma_commit(&sh.t_full[tb]);
+          mma_commit(&sh.t_full[k & 3]);
           if (tile + 1 == r.tile1) mma_commit(&sh.q_empty[buf]);
         }
         __syncwarp();
@@ -328,14 +331,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
     }
     // every product is complete before the memory it uses goes away
     for (uint32_t i = 0; i < 2 && i < k; ++i)
-      wait_or_stop(&sh.t_full[(k - 1 - i) & 1], ((k - 1 - i) >> 1) & 1, stop);
+      wait_or_stop(&sh.t_full[(k - 1 - i) & 3], ((k - 1 - i) >> 2) & 1, stop);
   } else {
     // ---- sums over heads ----
-    // Two groups of four warps: they share every tile's tokens where there
-    // are several, and take tiles in turn where there is one.
+    // Four groups of four warps, each with all 128 positions of a tile: two
+    // take every other tile and half of its tokens each, or, where there is
+    // one token, each takes every fourth tile. (Eight warps were bound by their
+    // own latencies: 2200 clocks a tile of 256 columns, 1020 for its products.)
     const int group = warp >> 2, quarter = warp & 3;
     const bool share = p.tokens > 1;
-    const int tile_step = share ? 1 : 2;
+    const int tile_step = share ? 2 : 4, turn_of = share ? group >> 1 : group, second = share ? group & 1 : 0;
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
     uint32_t k = 0, nu = 0;
     bool ok = true;
@@ -347,7 +352,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       if (!ok) break;
       ++nu;
       const int t_mid = share ? (r.tokens + 1) / 2 : r.tokens;
-      const int t_first = share && group == 1 ? t_mid : 0, t1 = share && group == 1 ? r.tokens : t_mid;
+      const int t_first = second ? t_mid : 0, t1 = second ? r.tokens : t_mid;
       float* out = p.a.out + r.b * p.a.out_seq_stride + r.t0 * p.a.out_token_stride;
       const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
       auto entry = [&](int tile) -> int64_t { return static_cast<int64_t>(tile) * kTile + quarter * 32 + lane; };
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
         const int64_t s = entry(tile);
         return tile < r.tile1 && s < p.a.width ? table[static_cast<int32_t>(s) / p.a.page_size] : -1;
       };
-      const uint32_t skip = share ? 0 : (k ^ group) & 1;
+      const uint32_t skip = static_cast<uint32_t>(turn_of - static_cast<int>(k)) & (tile_step - 1);
       const int mine = r.tile0 + static_cast<int>(skip);
       int32_t next = page_at(mine);
       const uint32_t k0 = k;
@@ -369,14 +374,14 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
         if (!absent && p.a.key_scales != nullptr)
           scale = p.a.key_scales[static_cast<int64_t>(page) * p.a.page_size + static_cast<int32_t>(s) % p.a.page_size];
         const uint32_t tb = k & 1;
-        ok = wait_or_stop(&sh.t_full[tb], (k >> 1) & 1, stop);
+        ok = wait_or_stop(&sh.t_full[k & 3], (k >> 2) & 1, stop);
         if (!ok) break;
         tc_fence_after();
-        // This group's columns, 32 at a time, the next ones on their way while
+        // This group's columns, 16 at a time, the next ones on their way while
         // these are summed.
         int left = (t1 - t_first) * PER;
         if (left == 0) {
-          mbar_arrive(&sh.t_empty[tb]);
+          mbar_arrive(&sh.t_empty[k & 3]);
           continue;
         }
         uint32_t at = tmem + tb * kMaxCols + lanes + t_first * p.hp;
@@ -384,14 +389,14 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
         const int32_t* length = sh.lengths[buf] + t_first;
         float* o = out + t_first * p.a.out_token_stride + s;
         float acc[4] = {};
-        uint32_t v0[32], v1[32];
+        uint32_t v0[16], v1[16];
         auto release = [&]() {  // the buffer is read: the next product may have it
           tc_fence_before();
-          mbar_arrive(&sh.t_empty[tb]);
+          mbar_arrive(&sh.t_empty[k & 3]);
         };
-        auto add = [&](const uint32_t (&v)[32], const float* w) {
+        auto add = [&](const uint32_t (&v)[16], const float* w) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = 0; j < 16; j += 4) {
             const float4 ww = *reinterpret_cast<const float4*>(w + j);
             acc[0] = fmaf(ww.x, relu(v[j]), acc[0]);
             acc[1] = fmaf(ww.y, relu(v[j + 1]), acc[1]);
@@ -405,24 +410,18 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
           ++length, o += p.a.out_token_stride;
         };
         tmem_ld(v0, at);
-        for (;; left -= 2, at += 64, wt += 64) {
+        for (;; left -= 2, at += 32, wt += 32) {
           tmem_wait_ld();
-          if (left > 1) {
-            tmem_ld(v1, at + 32);
-          } else {
-            release();
-          }
+          tmem_ld(v1, at + 16);
           add(v0, wt);
-          if (PER == 1) finish();
-          if (PER == 1 && left == 1) break;
           tmem_wait_ld();
           if (left > 2) {
-            tmem_ld(v0, at + 64);
+            tmem_ld(v0, at + 32);
           } else {
             release();
           }
-          add(v1, wt + 32);
-          if (PER <= 2 || (left & 2) != 0) finish();
+          add(v1, wt + 16);
+          if (PER == 2 || (left & (PER - 1)) == 2) finish();
           if (left == 2) break;
         }
       }
@@ -443,7 +442,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       }
     }
   }
-  if (warp == 12) {
+  if (warp == kProductWarp) {
     tc_fence_after();
     tmem_free(tmem, 512);
   }
@@ -512,9 +511,9 @@ topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cud
   const int64_t q_extents[4] = {a.D, a.H, a.T, a.B}, q_strides[3] = {a.q_head_stride, a.q_token_stride, a.q_seq_stride};
   const int q_box[3] = {p.hp, p.tokens, 1};
   p.q_boxes = box_map(&p.q_map, Kind<E>::map_type, size, a.q, 4, q_extents, q_strides, q_box);
-  if (p.hp == 32) return launch_ring<E, 1>(p, dev, sm_count, stream);
-  if (p.hp == 64) return launch_ring<E, 2>(p, dev, sm_count, stream);
-  return launch_ring<E, 4>(p, dev, sm_count, stream);
+  if (p.hp == 32) return launch_ring<E, 2>(p, dev, sm_count, stream);
+  if (p.hp == 64) return launch_ring<E, 4>(p, dev, sm_count, stream);
+  return launch_ring<E, 8>(p, dev, sm_count, stream);
 }
 
 }  // namespace

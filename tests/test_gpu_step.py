@@ -188,6 +188,19 @@ def test_scores(B, T, H, D, width, ps, dtype, lengths):
     _check_scores(_scores_case(B, T, H, D, width, ps, dtype, lengths), width)
 
 
+@pytest.mark.parametrize("B,T,H,D,ps,dtype", [(330, 1, 32, 64, 64, BF16), (120, 3, 64, 64, 16, FP16),
+                                              (330, 1, 16, 64, 7, BF16), (150, 2, 70, 128, 128, E4M3)])
+def test_scores_many_units_per_cta(B, T, H, D, ps, dtype):
+    """Several work units of many tiles on every CTA, ragged, some empty."""
+    width = 2300
+    lengths = torch.randint(-100, width + 50, (B, T), generator=_gen(B), device=DEV).flatten().tolist()
+    args = _scores_case(B, T, H, D, width, ps, dtype, lengths)
+    first = _check_scores(args, width)
+    for _ in range(3):
+        assert torch.equal(_check_scores(args, width) if _ == 0 else tk.indexer_scores(
+            *args[:5], key_scales=args[5], out=torch.full_like(first, 12345.0)), first)
+
+
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
 def test_scores_strides(dtype):
     """Padded keys, queries that are a slice (at an odd element), broadcast
