@@ -11,12 +11,12 @@
 // instructions a product in all). A tile of keys is fetched once for all
 // query tokens of its group.
 //
-// One CTA per SM, 21 warps: one fetches keys through the page table into a
-// ring (TMA boxes, zeros for absent rows and for the padding of D) and three
-// queries and weights, or four do both by 16-byte copies; one thread issues the
-// products into two TMEM buffers; sixteen warps sum over heads. Work units are (sequence,
-// range of tiles, group of query tokens); queries, weights and lengths of the
-// next unit are fetched while this one runs.
+// One CTA per SM, 20 warps: three fetch (keys through the page table into a
+// ring, by TMA boxes or, where pages are too odd for them, 16-byte copies;
+// zeros for absent rows and the padding of D; queries and weights of the next
+// work unit), one thread issues the products into two TMEM buffers, sixteen
+// warps sum over heads. Work units are (sequence, range of tiles, group of
+// query tokens).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kTile = 128;             // positions per tile: the rows of one product
 constexpr int kEpilogueWarps = 16;
-constexpr int kFetchWarp = kEpilogueWarps, kProductWarp = kFetchWarp + 4;
+constexpr int kFetchWarp = kEpilogueWarps, kProductWarp = kFetchWarp + 3;
 constexpr int kScoreThreads = (kProductWarp + 1) * 32;
 constexpr int kMaxTokens = 8;          // query tokens per group
 constexpr int kMaxCols = 256;
@@ -46,6 +46,9 @@ struct ScoreParams {
   int32_t blocks;          // 128-byte blocks per key: 1 or 2
   int32_t row_units;       // 16-byte units of D
   int32_t unit_tiles;      // tiles per work unit
+  int32_t share;           // groups of epilogue warps per tile: 1, 2 or 4
+  int32_t page_shift;      // log2 of page_size, or -1
+  uint32_t pages;
   int32_t chunks, groups;  // work units per sequence: chunks x groups
   uint32_t units;
   bool q_boxes;            // queries come by the TMA engine ...
@@ -84,6 +87,17 @@ __device__ __forceinline__ Unit unit_of(const ScoreParams& p, uint32_t u) {
   r.tile0 = static_cast<int>(c - static_cast<uint32_t>(r.b) * p.chunks) * p.unit_tiles;
   r.tile1 = min(r.tile0 + p.unit_tiles, longest / kTile + (longest % kTile != 0));
   return r;
+}
+
+__device__ __forceinline__ uint32_t page_index(const ScoreParams& p, uint32_t s) {
+  return p.page_shift >= 0 ? s >> p.page_shift : s / static_cast<uint32_t>(p.a.page_size);
+}
+__device__ __forceinline__ uint32_t place_in_page(const ScoreParams& p, uint32_t s) {
+  return s - page_index(p, s) * static_cast<uint32_t>(p.a.page_size);
+}
+// The page id of position s of a sequence, ~0 (no page) from `end` on.
+__device__ __forceinline__ uint32_t page_at(const ScoreParams& p, const int32_t* table, uint32_t s, uint32_t end) {
+  return s < end ? static_cast<uint32_t>(table[page_index(p, s)]) : 0xffffffffu;
 }
 
 // max(0, x), a NaN kept. Volatile: it stays behind the wait for the products.
@@ -162,9 +176,9 @@ __device__ __forceinline__ void queries_arrived(ScoreShared& sh, uint32_t nu) {
   copy_wait<0>();
 }
 
-// STAGES tiles of keys in flight; PER loads of 16 columns a token; keys by BOXES of
+// STAGES tiles of keys in flight; HP columns a token; keys by BOXES of
 // the TMA engine or by 16-byte copies.
-template <typename E, int STAGES, int PER, bool BOXES>
+template <typename E, int STAGES, int HP, bool BOXES>
 __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_constant__ ScoreParams p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -175,12 +189,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
   const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[i], BOXES ? 1 : 128), mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[i], BOXES ? 1 : 64), mbar_init(&sh.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], BOXES ? 192 : 256);  // the copies' arrivals and the stores'
+      mbar_init(&sh.q_full[i], BOXES ? 128 : 64);  // two of each fetching thread
       mbar_init(&sh.q_empty[i], 1 + kEpilogueWarps);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], p.tokens > 1 ? 256 : 128);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], 128 * p.share);
     sh.stop = 0;
     fence_mbar_init();
   }
@@ -203,88 +217,85 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       const Unit r = unit_of(p, u);
       if (r.tile0 >= r.tile1) continue;
       const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
-      auto entry = [&](int tile) -> int64_t { return static_cast<int64_t>(tile) * kTile + box * p.box_rows; };
-      auto page_at = [&](int tile) -> int32_t {
-        const int64_t s = entry(tile);
-        return mine && tile < r.tile1 && s < p.a.width ? table[static_cast<int32_t>(s) / p.a.page_size] : -1;
-      };
-      int32_t next = page_at(r.tile0);  // read a tile ahead
+      const uint32_t end = mine ? min(static_cast<uint32_t>(r.tile1) * kTile, static_cast<uint32_t>(p.a.width)) : 0;
+      uint32_t at = static_cast<uint32_t>(r.tile0) * kTile + box * p.box_rows;  // of the lane's box
+      uint32_t next = page_at(p, table, at, end);  // read a tile ahead
       for (int tile = r.tile0; tile < r.tile1; ++tile, ++k) {
         const uint32_t stage = k % STAGES;
-        const int32_t page = next;
-        next = page_at(tile + 1);
+        const uint32_t page = next;
+        next = page_at(p, table, at + kTile, end);
         ok = wait_or_stop(&sh.empty[stage], ((k / STAGES) & 1) ^ 1, stop);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&sh.full[stage], tile_bytes);
         __syncwarp();
         if (mine) {
-          const int z = page < 0 || page >= p.a.num_pages ? static_cast<int>(p.a.num_pages) : page;  // absent: zeros
-          const int y = static_cast<int>(static_cast<uint32_t>(entry(tile)) % static_cast<uint32_t>(p.a.page_size));
+          const int z = static_cast<int>(min(page, p.pages));  // absent: outside, zeros
+          const int y = static_cast<int>(place_in_page(p, at));
           box_load(ring_addr + stage * tile_bytes + (block * kTile + box * p.box_rows) * 128, &p.map,
                    block * (128 / static_cast<int>(sizeof(E))), y, z, &sh.full[stage]);
         }
+        at += kTile;
       }
     }
     // no box may arrive after the CTA has left
     for (uint32_t i = 0; i < STAGES && i < k; ++i)
       mbar_wait_bounded(&sh.full[(k - 1 - i) % STAGES], ((k - 1 - i) / STAGES) & 1, 1000000000ull);
-  } else if (BOXES && warp > kFetchWarp && warp < kProductWarp) {
-    // ---- queries, a unit ahead ----
-    uint32_t nu = 0;
-    for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
-      const Unit r = unit_of(p, u);
-      if (r.tile0 >= r.tile1) continue;
-      if (!wait_or_stop(&sh.q_empty[nu & 1], ((nu >> 1) & 1) ^ 1, stop)) break;
-      fetch_queries<E, 96>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - (kFetchWarp + 1) * 32, nowhere);
-      ++nu;
-    }
-    queries_arrived(sh, nu);
-  } else if (!BOXES && warp >= kFetchWarp && warp < kProductWarp) {
-    // ---- keys and queries, by 16-byte copies: 8 lanes fetch a row's 128 bytes ----
+  } else if (!BOXES && (warp == kFetchWarp || warp == kFetchWarp + 1)) {
+    // ---- keys, by 16-byte copies: 8 lanes fetch a row's 128 bytes ----
     const int w = warp - kFetchWarp;
-    const uint32_t unit16 = lane & 7;
-    uint32_t k = 0, nu = 0;
+    const uint32_t unit16 = lane & 7, sub = lane >> 3;
+    uint32_t k = 0;
     bool ok = true;
     for (uint32_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
       const Unit r = unit_of(p, u);
       if (r.tile0 >= r.tile1) continue;
       const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
-      // this lane looks up row 32 w + lane of a tile
-      auto entry = [&](int tile) -> int64_t { return static_cast<int64_t>(tile) * kTile + w * 32 + lane; };
-      auto page_at = [&](int tile) -> int32_t {
-        const int64_t s = entry(tile);
-        return tile < r.tile1 && s < p.a.width ? table[static_cast<int32_t>(s) / p.a.page_size] : -1;
-      };
-      int32_t next = page_at(r.tile0);  // read a tile ahead
-      ok = wait_or_stop(&sh.q_empty[nu & 1], ((nu >> 1) & 1) ^ 1, stop);
-      if (!ok) break;
-      fetch_queries<E, 128>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - kFetchWarp * 32, nowhere);
-      ++nu;
-      for (int tile = r.tile0; tile < r.tile1; ++tile, ++k) {
+      const uint32_t end = min(static_cast<uint32_t>(r.tile1) * kTile, static_cast<uint32_t>(p.a.width));
+      // this lane looks up rows 64 w + lane and 64 w + 32 + lane of a tile
+      uint32_t at = static_cast<uint32_t>(r.tile0) * kTile + w * 64 + lane;
+      uint32_t next[2] = {page_at(p, table, at, end), page_at(p, table, at + 32, end)};  // read a tile ahead
+      for (int tile = r.tile0; tile < r.tile1; ++tile, ++k, at += kTile) {
         const uint32_t stage = k % STAGES;
-        const int32_t page = next;
-        next = page_at(tile + 1);
+        const uint32_t page[2] = {next[0], next[1]};
+        next[0] = page_at(p, table, at + kTile, end);
+        next[1] = page_at(p, table, at + kTile + 32, end);
         ok = wait_or_stop(&sh.empty[stage], ((k / STAGES) & 1) ^ 1, stop);
         if (!ok) break;
-        const int64_t slot = page < 0 || page >= p.a.num_pages
-                                 ? -1
-                                 : page * p.a.key_page_stride +
-                                       static_cast<int32_t>(entry(tile)) % p.a.page_size * p.a.key_token_stride;
-        const uint32_t dst = ring_addr + stage * tile_bytes;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = 4 * i + (lane >> 3);
-          const int64_t s = __shfl_sync(0xffffffffu, slot, row);
-          const E* src = static_cast<const E*>(p.a.keys) + (s < 0 ? 0 : s);
-          for (int c = 0; c < p.blocks; ++c) {
-            const uint32_t j = c * 8 + unit16;
-            const bool real = s >= 0 && j < static_cast<uint32_t>(p.row_units);
-            copy16(dst + c * kTile * 128 + swizzled(w * 32 + row, unit16), real ? src + j * (16 / sizeof(E)) : nowhere,
-                   real);
+        for (int half = 0; half < 2; ++half) {
+          const bool here = page[half] < p.pages;
+          const uint32_t bits = __ballot_sync(0xffffffffu, here);
+          const int64_t slot = here ? page[half] * p.a.key_page_stride +
+                                          place_in_page(p, at + 32 * half) * p.a.key_token_stride
+                                    : 0;
+          const uint32_t dst = ring_addr + stage * tile_bytes;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + sub;
+            const E* src = static_cast<const E*>(p.a.keys) + __shfl_sync(0xffffffffu, slot, row);
+            for (int c = 0; c < p.blocks; ++c) {
+              const uint32_t j = c * 8 + unit16;
+              const bool real = ((bits >> row) & 1) && j < static_cast<uint32_t>(p.row_units);
+              copy16(dst + c * kTile * 128 + swizzled(w * 64 + half * 32 + row, unit16),
+                     real ? src + j * (16 / sizeof(E)) : nowhere, real);
+            }
           }
         }
         copy_arrive(&sh.full[stage]);
       }
+    }
+    copy_commit();
+    copy_wait<0>();
+  } else if (warp >= kFetchWarp && warp < kProductWarp) {
+    // ---- queries, a unit ahead ----
+    constexpr int kFirst = kFetchWarp + (BOXES ? 1 : 2);
+    uint32_t nu = 0;
+    for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+      const Unit r = unit_of(p, u);
+      if (r.tile0 >= r.tile1) continue;
+      if (!wait_or_stop(&sh.q_empty[nu & 1], ((nu >> 1) & 1) ^ 1, stop)) break;
+      fetch_queries<E, (kProductWarp - kFirst) * 32>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - kFirst * 32, nowhere);
+      ++nu;
     }
     queries_arrived(sh, nu);
   } else if (warp == kProductWarp) {
@@ -334,13 +345,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       wait_or_stop(&sh.t_full[(k - 1 - i) & 3], ((k - 1 - i) >> 2) & 1, stop);
   } else {
     // ---- sums over heads ----
-    // Four groups of four warps, each with all 128 positions of a tile: two
-    // take every other tile and half of its tokens each, or, where there is
-    // one token, each takes every fourth tile. (Eight warps were bound by their
-    // own latencies: 2200 clocks a tile of 256 columns, 1020 for its products.)
+    // Four groups of four warps, each with all 128 positions of a tile. Where
+    // there are tokens for them, two or four groups share a tile, else they
+    // take tiles in turn. 64 columns are read at once, so that the buffer is
+    // soon free for the next product: with 16 at a time it was held for the
+    // sums too, and 256 columns took 1800 clocks a tile, 1024 of them products.
     const int group = warp >> 2, quarter = warp & 3;
-    const bool share = p.tokens > 1;
-    const int tile_step = share ? 2 : 4, turn_of = share ? group >> 1 : group, second = share ? group & 1 : 0;
+    const int tile_step = 4 / p.share, turn_of = group / p.share, part = group % p.share;
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
     uint32_t k = 0, nu = 0;
     bool ok = true;
@@ -351,52 +362,45 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       ok = wait_or_stop(&sh.q_full[buf], (nu >> 1) & 1, stop);
       if (!ok) break;
       ++nu;
-      const int t_mid = share ? (r.tokens + 1) / 2 : r.tokens;
-      const int t_first = second ? t_mid : 0, t1 = second ? r.tokens : t_mid;
-      float* out = p.a.out + r.b * p.a.out_seq_stride + r.t0 * p.a.out_token_stride;
+      const int t_first = r.tokens * part / p.share, t1 = r.tokens * (part + 1) / p.share;
+      float* out = p.a.out + r.b * p.a.out_seq_stride + (r.t0 + t_first) * p.a.out_token_stride;
       const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
-      auto entry = [&](int tile) -> int64_t { return static_cast<int64_t>(tile) * kTile + quarter * 32 + lane; };
-      auto page_at = [&](int tile) -> int32_t {
-        const int64_t s = entry(tile);
-        return tile < r.tile1 && s < p.a.width ? table[static_cast<int32_t>(s) / p.a.page_size] : -1;
-      };
+      const uint32_t end = min(static_cast<uint32_t>(r.tile1) * kTile, static_cast<uint32_t>(p.a.width));
       const uint32_t skip = static_cast<uint32_t>(turn_of - static_cast<int>(k)) & (tile_step - 1);
       const int mine = r.tile0 + static_cast<int>(skip);
-      int32_t next = page_at(mine);
+      uint32_t s = static_cast<uint32_t>(mine) * kTile + quarter * 32 + lane;
+      uint32_t next = page_at(p, table, s, end);
       const uint32_t k0 = k;
       k += skip;
-      for (int tile = mine; tile < r.tile1; tile += tile_step, k += tile_step) {
-        const int64_t s = entry(tile);
-        const int32_t page = next;
-        next = page_at(tile + tile_step);
-        const bool absent = page < 0 || page >= p.a.num_pages;
+      for (int tile = mine; tile < r.tile1; tile += tile_step, k += tile_step, s += tile_step * kTile) {
+        const uint32_t page = next;
+        next = page_at(p, table, s + tile_step * kTile, end);
+        const bool absent = page >= p.pages;
         float scale = 1.0f;
         if (!absent && p.a.key_scales != nullptr)
-          scale = p.a.key_scales[static_cast<int64_t>(page) * p.a.page_size + static_cast<int32_t>(s) % p.a.page_size];
+          scale = p.a.key_scales[static_cast<int64_t>(page) * p.a.page_size + place_in_page(p, s)];
         const uint32_t tb = k & 1;
         ok = wait_or_stop(&sh.t_full[k & 3], (k >> 2) & 1, stop);
         if (!ok) break;
         tc_fence_after();
-        // This group's columns, 16 at a time, the next ones on their way while
-        // these are summed.
-        int left = (t1 - t_first) * PER;
+        int left = (t1 - t_first) * (HP / 32);
         if (left == 0) {
           mbar_arrive(&sh.t_empty[k & 3]);
           continue;
         }
-        uint32_t at = tmem + tb * kMaxCols + lanes + t_first * p.hp;
-        const float* wt = sh.weights[buf] + t_first * p.hp;
+        uint32_t at = tmem + tb * kMaxCols + lanes + t_first * HP;
+        const float* wt = sh.weights[buf] + t_first * HP;
         const int32_t* length = sh.lengths[buf] + t_first;
-        float* o = out + t_first * p.a.out_token_stride + s;
+        float* o = out + s;
         float acc[4] = {};
-        uint32_t v0[16], v1[16];
+        uint32_t v0[32], v1[32];
         auto release = [&]() {  // the buffer is read: the next product may have it
           tc_fence_before();
           mbar_arrive(&sh.t_empty[k & 3]);
         };
-        auto add = [&](const uint32_t (&v)[16], const float* w) {
+        auto add = [&](const uint32_t (&v)[32], const float* w) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
+          for (int j = 0; j < 32; j += 4) {
             const float4 ww = *reinterpret_cast<const float4*>(w + j);
             acc[0] = fmaf(ww.x, relu(v[j]), acc[0]);
             acc[1] = fmaf(ww.y, relu(v[j + 1]), acc[1]);
@@ -405,24 +409,22 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
           }
         };
         auto finish = [&]() {
-          if (s < *length) *o = absent ? __int_as_float(0xff800000) : ((acc[0] + acc[1]) + (acc[2] + acc[3])) * scale;
+          if (s < static_cast<uint32_t>(*length)) *o = absent ? __int_as_float(0xff800000) : ((acc[0] + acc[1]) + (acc[2] + acc[3])) * scale;
           acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
           ++length, o += p.a.out_token_stride;
         };
-        tmem_ld(v0, at);
-        for (;; left -= 2, at += 32, wt += 32) {
+        for (; left > 0; left -= 2, at += 64, wt += 64) {
+          const bool both = HP > 32 || left > 1;
+          tmem_ld(v0, at);
+          if (both) tmem_ld(v1, at + 32);
           tmem_wait_ld();
-          tmem_ld(v1, at + 16);
+          if (left <= 2) release();
           add(v0, wt);
-          tmem_wait_ld();
-          if (left > 2) {
-            tmem_ld(v0, at + 32);
-          } else {
-            release();
+          if (HP == 32) finish();
+          if (both) {
+            add(v1, wt + 32);
+            if (HP < 128 || (left & 2) != 0) finish();
           }
-          add(v1, wt + 16);
-          if (PER == 2 || (left & (PER - 1)) == 2) finish();
-          if (left == 2) break;
         }
       }
       k = k0 + (r.tile1 - r.tile0);
@@ -448,12 +450,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
   }
 }
 
-template <typename E, int STAGES, int PER, bool BOXES>
+template <typename E, int STAGES, int HP, bool BOXES>
 topk_status launch_variant(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
   static_assert(sizeof(ScoreShared) <= 3072, "barriers and weights");
   const size_t bytes = 2 * static_cast<size_t>(p.cols) * 128 * p.blocks + STAGES * static_cast<size_t>(kTile) * 128 * p.blocks +
                        sizeof(ScoreShared);
-  constexpr auto kernel = scores_kernel<E, STAGES, PER, BOXES>;
+  constexpr auto kernel = scores_kernel<E, STAGES, HP, BOXES>;
   const topk_status st = allow_shared<kernel>(dev);
   if (st != TOPK_OK) return st;
   const unsigned grid = p.units < static_cast<unsigned>(sm_count) ? p.units : static_cast<unsigned>(sm_count);
@@ -461,18 +463,18 @@ topk_status launch_variant(const ScoreParams& p, int dev, int sm_count, cudaStre
   return cudaGetLastError() == cudaSuccess ? TOPK_OK : TOPK_ECUDA;
 }
 
-template <typename E, int STAGES, int PER>
+template <typename E, int STAGES, int HP>
 topk_status launch_step(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
-  return p.box_rows > 0 ? launch_variant<E, STAGES, PER, true>(p, dev, sm_count, stream)
-                        : launch_variant<E, STAGES, PER, false>(p, dev, sm_count, stream);
+  return p.box_rows > 0 ? launch_variant<E, STAGES, HP, true>(p, dev, sm_count, stream)
+                        : launch_variant<E, STAGES, HP, false>(p, dev, sm_count, stream);
 }
 
-template <typename E, int PER>
+template <typename E, int HP>
 topk_status launch_ring(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
   // The ring gets what the queries leave of 227 KB: 6, 5 or 3 tiles.
-  if (p.cols <= 64) return launch_step<E, 6, PER>(p, dev, sm_count, stream);
-  if (p.cols <= 128) return launch_step<E, 5, PER>(p, dev, sm_count, stream);
-  return launch_step<E, 3, PER>(p, dev, sm_count, stream);
+  if (p.cols <= 64) return launch_step<E, 6, HP>(p, dev, sm_count, stream);
+  if (p.cols <= 128) return launch_step<E, 5, HP>(p, dev, sm_count, stream);
+  return launch_step<E, 3, HP>(p, dev, sm_count, stream);
 }
 
 template <typename E>
@@ -486,6 +488,11 @@ topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cud
   p.cols = p.tokens * p.hp;
   p.blocks = (a.D * size + 127) / 128;
   p.row_units = a.D * size / 16;
+  p.share = p.tokens >= 4 ? 4 : p.tokens >= 2 ? 2 : 1;
+  p.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page_size == 1 << i) p.page_shift = i;
+  p.pages = a.num_pages < INT32_MAX ? static_cast<uint32_t>(a.num_pages) : INT32_MAX;
   p.groups = (a.T + p.tokens - 1) / p.tokens;
   // Work units of at most 16 tiles: enough of them to even out the SMs, long
   // enough to hide the next unit's queries; fewer tiles while SMs would idle.
@@ -511,9 +518,9 @@ topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cud
   const int64_t q_extents[4] = {a.D, a.H, a.T, a.B}, q_strides[3] = {a.q_head_stride, a.q_token_stride, a.q_seq_stride};
   const int q_box[3] = {p.hp, p.tokens, 1};
   p.q_boxes = box_map(&p.q_map, Kind<E>::map_type, size, a.q, 4, q_extents, q_strides, q_box);
-  if (p.hp == 32) return launch_ring<E, 2>(p, dev, sm_count, stream);
-  if (p.hp == 64) return launch_ring<E, 4>(p, dev, sm_count, stream);
-  return launch_ring<E, 8>(p, dev, sm_count, stream);
+  if (p.hp == 32) return launch_ring<E, 32>(p, dev, sm_count, stream);
+  if (p.hp == 64) return launch_ring<E, 64>(p, dev, sm_count, stream);
+  return launch_ring<E, 128>(p, dev, sm_count, stream);
 }
 
 }  // namespace
