@@ -60,8 +60,8 @@ struct ScoreParams {
 struct ScoreShared {
   float weights[2][kMaxCols];
   int32_t lengths[2][kMaxTokens];
-  uint64_t full[6], empty[6], q_full[2], q_empty[2];
-  uint64_t t_full[4], t_empty[4];  // of tile k at k % 4: whoever waits on one has seen each of its phases
+  uint64_t full[6], q_full[2], q_empty[2];
+  uint64_t t_full[8], t_empty[8];  // of tile k at k % 8: nobody who waits on one lags behind by eight tiles
   uint32_t tmem;
   uint32_t stop;
 };
@@ -189,12 +189,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
   const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[i], BOXES ? 1 : 64), mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[i], BOXES ? 1 : 64);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], BOXES ? 128 : 64);  // two of each fetching thread
       mbar_init(&sh.q_empty[i], 1 + kEpilogueWarps);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], 128 * p.share);
+    for (int i = 0; i < 8; ++i) mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], 128 * p.share);
     sh.stop = 0;
     fence_mbar_init();
   }
@@ -211,31 +211,49 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
     // ---- keys, by boxes: lane i fetches block i / 16 of the box i % 16 of a tile ----
     const int box = lane & 15, block = lane >> 4, boxes = kTile / p.box_rows;
     const bool mine = box < boxes && block < p.blocks;
-    uint32_t k = 0;
+    // The next unit's length and first page ids are read while this one's
+    // boxes are under way.
+    uint32_t k = 0, u = blockIdx.x, at = 0, end = 0, next = 0;
+    const int32_t* table = nullptr;
+    Unit r = {};
+    auto advance = [&]() {  // to the next unit with work, its first lookup made
+      for (r.tile1 = 0, r.tile0 = 0; u < p.units; u += gridDim.x) {
+        r = unit_of(p, u);
+        if (r.tile0 < r.tile1) break;
+      }
+      if (r.tile0 >= r.tile1) return;
+      u += gridDim.x;
+      table = p.a.page_table + r.b * p.a.table_stride;
+      end = mine ? min(static_cast<uint32_t>(r.tile1) * kTile, static_cast<uint32_t>(p.a.width)) : 0;
+      at = static_cast<uint32_t>(r.tile0) * kTile + box * p.box_rows;  // of the lane's box
+      next = page_at(p, table, at, end);
+    };
+    advance();
+    int tiles = r.tile1 - r.tile0;
     bool ok = true;
-    for (uint32_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-      const Unit r = unit_of(p, u);
-      if (r.tile0 >= r.tile1) continue;
-      const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
-      const uint32_t end = mine ? min(static_cast<uint32_t>(r.tile1) * kTile, static_cast<uint32_t>(p.a.width)) : 0;
-      uint32_t at = static_cast<uint32_t>(r.tile0) * kTile + box * p.box_rows;  // of the lane's box
-      uint32_t next = page_at(p, table, at, end);  // read a tile ahead
-      for (int tile = r.tile0; tile < r.tile1; ++tile, ++k) {
-        const uint32_t stage = k % STAGES;
-        const uint32_t page = next;
-        next = page_at(p, table, at + kTile, end);
-        ok = wait_or_stop(&sh.empty[stage], ((k / STAGES) & 1) ^ 1, stop);
+    while (tiles > 0 && ok) {
+      int tiles_after = 0;
+      for (int i = 0; i < tiles; ++i, ++k) {
+        const uint32_t stage = k % STAGES, page = next, here = at;
+        if (i + 1 < tiles) {  // a tile ahead
+          at += kTile;
+          next = page_at(p, table, at, end);
+        } else {
+          advance();
+          tiles_after = r.tile1 - r.tile0;
+        }
+        ok = k < STAGES || wait_or_stop(&sh.t_full[(k - STAGES) & 7], ((k - STAGES) >> 3) & 1, stop);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&sh.full[stage], tile_bytes);
         __syncwarp();
         if (mine) {
           const int z = static_cast<int>(min(page, p.pages));  // absent: outside, zeros
-          const int y = static_cast<int>(place_in_page(p, at));
+          const int y = static_cast<int>(place_in_page(p, here));
           box_load(ring_addr + stage * tile_bytes + (block * kTile + box * p.box_rows) * 128, &p.map,
                    block * (128 / static_cast<int>(sizeof(E))), y, z, &sh.full[stage]);
         }
-        at += kTile;
       }
+      tiles = tiles_after;
     }
     // no box may arrive after the CTA has left
     for (uint32_t i = 0; i < STAGES && i < k; ++i)
@@ -259,7 +277,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
         const uint32_t page[2] = {next[0], next[1]};
         next[0] = page_at(p, table, at + kTile, end);
         next[1] = page_at(p, table, at + kTile + 32, end);
-        ok = wait_or_stop(&sh.empty[stage], ((k / STAGES) & 1) ^ 1, stop);
+        ok = k < STAGES || wait_or_stop(&sh.t_full[(k - STAGES) & 7], ((k - STAGES) >> 3) & 1, stop);
         if (!ok) break;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -311,17 +329,21 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       ok = wait_or_stop(&sh.q_full[buf], (nu >> 1) & 1, stop);
       ++nu;
       if (!p.q_boxes) fence_proxy_async_smem();  // copies and stores are in; now the tensor cores may see them
-      for (int tile = r.tile0; tile < r.tile1 && ok; ++tile, ++k) {
-        const uint32_t tb = k & 1;
-        // the buffer is free when tile k - 2 is read
-        ok = (k < 2 || wait_or_stop(&sh.t_empty[(k - 2) & 3], ((k - 2) >> 2) & 1, stop)) &&
-             wait_or_stop(&sh.full[stage], turn, stop);
-        if (!ok) break;
-        if (!BOXES) fence_proxy_async_smem();
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t da = ring_desc + (stage * tile_bytes >> 4), db = q_desc + (buf * q_bytes >> 4);
-          const uint32_t to = tmem + tb * kMaxCols;
+      // one thread from here: its waits need no vote
+      const int tiles = r.tile1 - r.tile0;
+      bool done = true;
+      if (ok && elect_one()) {
+        const uint64_t db = q_desc + (buf * q_bytes >> 4);
+        uint32_t st = stage, tn = turn;
+        for (int i = 0; i < tiles; ++i) {
+          const uint32_t kk = k + i, to = tmem + (kk & 1) * kMaxCols;
+          // the buffer is free when tile k - 2 is read
+          done = (kk < 2 || wait_or_stop_one(&sh.t_empty[(kk - 2) & 7], ((kk - 2) >> 3) & 1, stop)) &&
+                 wait_or_stop_one(&sh.full[st], tn, stop);
+          if (!done) break;
+          if (!BOXES) fence_proxy_async_smem();
+          tc_fence_after();
+          const uint64_t da = ring_desc + (st * tile_bytes >> 4);
           for (int c = 0; c < p.blocks; ++c)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -332,17 +354,21 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
               else
                 mma_f16(to, a, b, desc, c + j > 0);
             }
-          mma_commit(&sh.empty[stage]);
-          mma_commit(&sh.t_full[k & 3]);
-          if (tile + 1 == r.tile1) mma_commit(&sh.q_empty[buf]);
+          mma_commit(&sh.t_full[kk & 7]);
+          if (++st == STAGES) st = 0, tn ^= 1;
         }
-        __syncwarp();
-        if (++stage == STAGES) stage = 0, turn ^= 1;
+        if (done) mma_commit(&sh.q_empty[buf]);
       }
+      __syncwarp();
+      ok = ok && __all_sync(0xffffffffu, done);
+      k += tiles;
+      stage += tiles % STAGES;
+      if (((tiles / STAGES) & 1) != 0) turn ^= 1;
+      if (stage >= STAGES) stage -= STAGES, turn ^= 1;
     }
     // every product is complete before the memory it uses goes away
     for (uint32_t i = 0; i < 2 && i < k; ++i)
-      wait_or_stop(&sh.t_full[(k - 1 - i) & 3], ((k - 1 - i) >> 2) & 1, stop);
+      wait_or_stop(&sh.t_full[(k - 1 - i) & 7], ((k - 1 - i) >> 3) & 1, stop);
   } else {
     // ---- sums over heads ----
     // Four groups of four warps, each with all 128 positions of a tile: two
@@ -379,12 +405,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
         if (!absent && p.a.key_scales != nullptr)
           scale = p.a.key_scales[static_cast<int64_t>(page) * p.a.page_size + place_in_page(p, s)];
         const uint32_t tb = k & 1;
-        ok = wait_or_stop(&sh.t_full[k & 3], (k >> 2) & 1, stop);
+        ok = wait_or_stop(&sh.t_full[k & 7], (k >> 3) & 1, stop);
         if (!ok) break;
         tc_fence_after();
         int left = (t1 - t_first) * (HP / 32);
         if (left == 0) {
-          mbar_arrive(&sh.t_empty[k & 3]);
+          mbar_arrive(&sh.t_empty[k & 7]);
           continue;
         }
         uint32_t at = tmem + tb * kMaxCols + lanes + t_first * HP;
@@ -395,7 +421,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
         uint32_t v0[32], v1[32];
         auto release = [&]() {  // the buffer is read: the next product may have it
           tc_fence_before();
-          mbar_arrive(&sh.t_empty[k & 3]);
+          mbar_arrive(&sh.t_empty[k & 7]);
         };
         auto add = [&](const uint32_t (&v)[32], const float* w) {
 #pragma unroll
@@ -493,12 +519,15 @@ topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cud
     if (a.page_size == 1 << i) p.page_shift = i;
   p.pages = a.num_pages < INT32_MAX ? static_cast<uint32_t>(a.num_pages) : INT32_MAX;
   p.groups = (a.T + p.tokens - 1) / p.tokens;
-  // Work units of at most 16 tiles: enough of them to even out the SMs, long
-  // enough to hide the next unit's queries; fewer tiles while SMs would idle.
+  // Work units of at most 16 tiles, 8 where a tile is short work: enough of
+  // them to even out the SMs, long enough to hide the next unit's queries
+  // (64 x 65536, 64 columns: 156 us by 8, 160 by 16; 2048 x 8192, 256
+  // columns: 193 by 16, 195 by 8); fewer while SMs would idle.
+  const int most = p.cols <= 128 ? 8 : 16;
   const int64_t tiles = (a.width + kTile - 1) / kTile;
   const int64_t all = tiles * a.B * p.groups;
   int64_t per = (all + sm_count - 1) / sm_count;
-  p.unit_tiles = static_cast<int32_t>(per < 16 ? per : 16);
+  p.unit_tiles = static_cast<int32_t>(per < most ? per : most);
   p.chunks = static_cast<int32_t>((tiles + p.unit_tiles - 1) / p.unit_tiles);
   const int64_t units = static_cast<int64_t>(p.chunks) * p.groups * a.B;
   if (units > INT32_MAX) return TOPK_EINVAL;

@@ -194,23 +194,24 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, i
 // block in the layout above.
 __device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t unit) { return row * 128 + ((unit ^ (row & 7)) << 4); }
 
-// Waits of the warps of one CTA on each other, for a whole warp, with one
-// answer for all of its lanes. A wait that is not over after a second, far
+// Waits of the threads of one CTA on each other: false where it gave up. A wait that is not over after a second, far
 // beyond any real one, raises `stop`, which ends every other wait of the CTA
 // too; the caller then leaves its loop.
-__device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile uint32_t* stop) {
-  bool done = mbar_try_wait(bar, parity);
-  if (!done) {
-    const uint64_t t0 = global_timer_ns();
-    while (!(done = mbar_try_wait_sleep(bar, parity, 20000u))) {
-      if (*stop != 0) break;
-      if (global_timer_ns() - t0 > 1000000000ull) {
-        *stop = 1;
-        break;
-      }
+__device__ __forceinline__ bool wait_or_stop_one(uint64_t* bar, uint32_t parity, volatile uint32_t* stop) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    if (*stop != 0) return false;
+    if (global_timer_ns() - t0 > 1000000000ull) {
+      *stop = 1;
+      return false;
     }
   }
-  return __all_sync(0xffffffffu, done);
+  return true;
+}
+// The same for a whole warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile uint32_t* stop) {
+  return __all_sync(0xffffffffu, wait_or_stop_one(bar, parity, stop));
 }
 
 }  // namespace tki
