@@ -239,50 +239,48 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     const int v_stages = p.shared ? p.k_stages : p.v_stages, v_bytes = p.shared ? p.k_bytes : p.v_bytes;
     uint64_t* v_empty = p.shared ? sh.k_empty : sh.v_empty;
     auto scores = [&](uint32_t buf) -> bool {
-      if (!wait_or_stop(&sh.k_full[k_stage], k_turn, stop)) return false;
+      if (!wait_or_stop_one(&sh.k_full[k_stage], k_turn, stop)) return false;
       fence_proxy_async_smem();
       tc_fence_after();
-      if (elect_one()) {
-        const uint64_t kd = k_desc + static_cast<uint32_t>(k_stage * p.k_bytes >> 4);
-        const uint32_t to = tmem + buf * kKeys;
-        for (int c = 0; c < p.d_blocks; ++c)
+      const uint64_t kd = k_desc + static_cast<uint32_t>(k_stage * p.k_bytes >> 4);
+      const uint32_t to = tmem + buf * kKeys;
+      for (int c = 0; c < p.d_blocks; ++c)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f16(to, q_desc + static_cast<uint32_t>(c * (128 * 128 >> 4) + j * 2),
-                    kd + static_cast<uint32_t>(c * (kKeys * 128 >> 4) + j * 2), desc_s, c + j > 0);
-        mma_commit(&sh.s_full[buf]);
-        if (!p.shared) mma_commit(&sh.k_empty[k_stage]);
-      }
-      __syncwarp();
+        for (int j = 0; j < 4; ++j)
+          mma_f16(to, q_desc + static_cast<uint32_t>(c * (128 * 128 >> 4) + j * 2),
+                  kd + static_cast<uint32_t>(c * (kKeys * 128 >> 4) + j * 2), desc_s, c + j > 0);
+      mma_commit(&sh.s_full[buf]);
+      if (!p.shared) mma_commit(&sh.k_empty[k_stage]);
       if (++k_stage == p.k_stages) k_stage = 0, k_turn ^= 1;
       return true;
     };
-    bool ok = tiles > 0 && wait_or_stop(&sh.q_full, 0, stop) && scores(0);
-    uint32_t buf = 0, turn = 0, next = 1, next_turn = 1;  // next_turn: of the weights that were there before
-    for (int i = 0; i < tiles && ok; ++i) {
-      // the next scores go where the weights of tile i + 1 - bufs were
-      if (i + 1 < tiles) ok = wait_or_stop(&sh.pv_done[next], next_turn, stop) && scores(next);
-      if (ok && !p.shared) {
-        ok = wait_or_stop(&sh.v_full[v_stage], v_turn, stop);
-        fence_proxy_async_smem();
-      }
-      ok = ok && wait_or_stop(&sh.p_full[buf], turn, stop);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
+    // one thread from here: its waits need no vote
+    if (tiles > 0 && elect_one()) {
+      bool ok = wait_or_stop_one(&sh.q_full, 0, stop) && scores(0);
+      uint32_t buf = 0, turn = 0, next = 1, next_turn = 1;  // next_turn: of the weights that were there before
+      for (int i = 0; i < tiles && ok; ++i) {
+        // the next scores go where the weights of tile i + 1 - bufs were
+        if (i + 1 < tiles) ok = wait_or_stop_one(&sh.pv_done[next], next_turn, stop) && scores(next);
+        if (ok && !p.shared) {
+          ok = wait_or_stop_one(&sh.v_full[v_stage], v_turn, stop);
+          fence_proxy_async_smem();
+        }
+        ok = ok && wait_or_stop_one(&sh.p_full[buf], turn, stop);
+        if (!ok) break;
+        tc_fence_after();
         const uint64_t vd = v_desc + static_cast<uint32_t>(v_stage * v_bytes >> 4);
 #pragma unroll
         for (int j = 0; j < kKeys / 16; ++j)
           mma_f16_ts(tmem_o, tmem + buf * kKeys + j * 8, vd + static_cast<uint32_t>(j * (16 * 128 >> 4)), desc_o, i + j > 0);
         mma_commit(&v_empty[v_stage]);
         mma_commit(&sh.pv_done[buf]);
+        if (++v_stage == v_stages) v_stage = 0, v_turn ^= 1;
+        buf = next;
+        if (buf == 0) turn ^= 1;
+        if (++next == static_cast<uint32_t>(p.bufs)) next = 0, next_turn ^= 1;
       }
-      __syncwarp();
-      if (++v_stage == v_stages) v_stage = 0, v_turn ^= 1;
-      buf = next;
-      if (buf == 0) turn ^= 1;
-      if (++next == static_cast<uint32_t>(p.bufs)) next = 0, next_turn ^= 1;
     }
+    __syncwarp();
   } else {
     // ---- softmax ----
     const int copy = threadIdx.x / kRows;
