@@ -68,8 +68,10 @@ struct AttShared {
   uint32_t seen[kMasks][2];            // bit per entry
   float top[128], sum[128];            // of the rows
   float head_top[128], head_sum[128];  // of the heads: the copies joined
-  uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages], masks[kMasks];
-  uint64_t q_full, s_full[kMaxBufs], p_full[kMaxBufs], pv_done[kMaxBufs];
+  uint64_t k_full[kMaxStages], v_full[kMaxStages], masks[kMasks], q_full;
+  // Of tile i at i % 8: scores there, weights there, products with v done.
+  // Nobody who waits on one lags behind by eight tiles.
+  uint64_t s_full[8], p_full[8], pv_done[8];
   uint32_t tmem;
   uint32_t stop;
 };
@@ -157,11 +159,11 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   int32_t pos = gathers ? index_of(0) : -1, pos1 = gathers ? index_of(1) : -1;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.k_stages; ++i) mbar_init(&sh.k_full[i], p.shared ? 128 : 64), mbar_init(&sh.k_empty[i], 1);
-    for (int i = 0; i < p.v_stages; ++i) mbar_init(&sh.v_full[i], 64), mbar_init(&sh.v_empty[i], 1);
+    for (int i = 0; i < p.k_stages; ++i) mbar_init(&sh.k_full[i], p.shared ? 128 : 64);
+    for (int i = 0; i < p.v_stages; ++i) mbar_init(&sh.v_full[i], 64);
     for (int i = 0; i < kMasks; ++i) mbar_init(&sh.masks[i], 2);
     mbar_init(&sh.q_full, 256);
-    for (int i = 0; i < p.bufs; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 128), mbar_init(&sh.pv_done[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 128), mbar_init(&sh.pv_done[i], 1);
     sh.stop = 0;
     fence_mbar_init();
   }
@@ -191,20 +193,21 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     const int64_t page_stride = values ? a.v_page_stride : a.k_page_stride;
     const int64_t token_stride = values ? a.v_token_stride : a.k_token_stride;
     uint64_t* full = values ? sh.v_full : sh.k_full;
-    uint64_t* empty = values ? sh.v_empty : sh.k_empty;
+    uint64_t* used = values || p.shared ? sh.pv_done : sh.s_full;  // when a tile's stage is free
     const int stages = values ? p.v_stages : p.k_stages, stage_bytes = values ? p.v_bytes : p.k_bytes;
     // 8 lanes fetch 128 bytes of an entry; step j has entries 4 j + lane / 8.
     const uint32_t unit16 = lane & 7, sub = lane >> 3;
     const uint32_t at = (values ? v_ring : k_ring) + (half * 32 + sub) * 128;
     const uint32_t even = (unit16 ^ sub) << 4, odd = (unit16 ^ (sub + 4)) << 4;
-    int stage = 0, turn = 1;
+    int stage = 0;
     for (int i = 0; i < tiles; ++i) {
       const int32_t pos2 = index_of(i + 2);
       const int32_t page1 = page_of(pos1);
       const bool seen = page >= 0 && page < a.num_pages;
       const int64_t entry = seen ? page * page_stride + pos % a.page_size * token_stride : 0;
       const uint32_t bits = __ballot_sync(0xffffffffu, seen);
-      if (!wait_or_stop(&empty[stage], turn, stop)) break;
+      const int before = i - stages;
+      if (before >= 0 && !wait_or_stop(&used[before & 7], (before >> 3) & 1, stop)) break;
       const uint32_t dst = at + stage * stage_bytes;
       const E* from[8];
 #pragma unroll
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
         if (lane == 0) mbar_arrive(&sh.masks[i % kMasks]);
       }
       pos = pos1, pos1 = pos2, page = page1;
-      if (++stage == stages) stage = 0, turn ^= 1;
+      if (++stage == stages) stage = 0;
     }
     copy_commit();
     copy_wait<0>();
@@ -237,8 +240,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     const uint64_t v_desc = operand_desc(p.shared ? k_ring : v_ring, kKeys * 128);
     int k_stage = 0, k_turn = 0, v_stage = 0, v_turn = 0;
     const int v_stages = p.shared ? p.k_stages : p.v_stages, v_bytes = p.shared ? p.k_bytes : p.v_bytes;
-    uint64_t* v_empty = p.shared ? sh.k_empty : sh.v_empty;
-    auto scores = [&](uint32_t buf) -> bool {
+    auto scores = [&](int i, uint32_t buf) -> bool {
       if (!wait_or_stop_one(&sh.k_full[k_stage], k_turn, stop)) return false;
       fence_proxy_async_smem();
       tc_fence_after();
@@ -249,35 +251,34 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
         for (int j = 0; j < 4; ++j)
           mma_f16(to, q_desc + static_cast<uint32_t>(c * (128 * 128 >> 4) + j * 2),
                   kd + static_cast<uint32_t>(c * (kKeys * 128 >> 4) + j * 2), desc_s, c + j > 0);
-      mma_commit(&sh.s_full[buf]);
-      if (!p.shared) mma_commit(&sh.k_empty[k_stage]);
+      mma_commit(&sh.s_full[i & 7]);
       if (++k_stage == p.k_stages) k_stage = 0, k_turn ^= 1;
       return true;
     };
     // one thread from here: its waits need no vote
     if (tiles > 0 && elect_one()) {
-      bool ok = wait_or_stop_one(&sh.q_full, 0, stop) && scores(0);
-      uint32_t buf = 0, turn = 0, next = 1, next_turn = 1;  // next_turn: of the weights that were there before
+      bool ok = wait_or_stop_one(&sh.q_full, 0, stop) && scores(0, 0);
+      uint32_t buf = 0;
       for (int i = 0; i < tiles && ok; ++i) {
-        // the next scores go where the weights of tile i + 1 - bufs were
-        if (i + 1 < tiles) ok = wait_or_stop_one(&sh.pv_done[next], next_turn, stop) && scores(next);
+        const uint32_t next = buf + 1 == static_cast<uint32_t>(p.bufs) ? 0 : buf + 1;
+        if (i + 1 < tiles) {
+          const int before = i + 1 - p.bufs;  // the next scores go where its weights were
+          ok = (before < 0 || wait_or_stop_one(&sh.pv_done[before & 7], (before >> 3) & 1, stop)) && scores(i + 1, next);
+        }
         if (ok && !p.shared) {
           ok = wait_or_stop_one(&sh.v_full[v_stage], v_turn, stop);
           fence_proxy_async_smem();
         }
-        ok = ok && wait_or_stop_one(&sh.p_full[buf], turn, stop);
+        ok = ok && wait_or_stop_one(&sh.p_full[i & 7], (i >> 3) & 1, stop);
         if (!ok) break;
         tc_fence_after();
         const uint64_t vd = v_desc + static_cast<uint32_t>(v_stage * v_bytes >> 4);
 #pragma unroll
         for (int j = 0; j < kKeys / 16; ++j)
           mma_f16_ts(tmem_o, tmem + buf * kKeys + j * 8, vd + static_cast<uint32_t>(j * (16 * 128 >> 4)), desc_o, i + j > 0);
-        mma_commit(&v_empty[v_stage]);
-        mma_commit(&sh.pv_done[buf]);
+        mma_commit(&sh.pv_done[i & 7]);
         if (++v_stage == v_stages) v_stage = 0, v_turn ^= 1;
         buf = next;
-        if (buf == 0) turn ^= 1;
-        if (++next == static_cast<uint32_t>(p.bufs)) next = 0, next_turn ^= 1;
       }
     }
     __syncwarp();
@@ -312,11 +313,11 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     const float cap_in = a.softcap > 0.0f ? a.scale * 2.0f * kLog2e / a.softcap : 0.0f;
     const float cap_out = a.softcap * kLog2e, scale = a.scale * kLog2e;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
-    uint32_t buf = 0, turn = 0, before = 0, before_turn = 0;
+    uint32_t buf = 0;
     for (int i = 0; i < tiles; ++i) {
       const int mask = i % kMasks;
       if (!wait_or_stop(&sh.masks[mask], (i / kMasks) & 1, stop)) break;
-      if (!wait_or_stop(&sh.s_full[buf], turn, stop)) break;
+      if (!wait_or_stop(&sh.s_full[i & 7], (i >> 3) & 1, stop)) break;
       tc_fence_after();
       const uint32_t s_at = tmem + buf * kKeys + lanes;
       float z[kPart];
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
         top = moved;
         sum *= factor;
         if (i > 0) {
-          if (!wait_or_stop(&sh.pv_done[before], before_turn, stop)) break;
+          if (!wait_or_stop(&sh.pv_done[(i - 1) & 7], ((i - 1) >> 3) & 1, stop)) break;
           tc_fence_after();
           for (int c = 0; c < a.Dv; c += 16) {  // past Dv: columns that nothing reads, within the allocation
             uint32_t v[16];
@@ -390,11 +391,10 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&sh.p_full[buf]);
-      before = buf, before_turn = turn;
-      if (++buf == static_cast<uint32_t>(p.bufs)) buf = 0, turn ^= 1;
+      mbar_arrive(&sh.p_full[i & 7]);
+      if (++buf == static_cast<uint32_t>(p.bufs)) buf = 0;
     }
-    if (tiles > 0) wait_or_stop(&sh.pv_done[before], before_turn, stop);
+    if (tiles > 0) wait_or_stop(&sh.pv_done[(tiles - 1) & 7], ((tiles - 1) >> 3) & 1, stop);
     tc_fence_after();
     const bool failed = *stop != 0;  // a wait ran out: the rows become NaN
     sh.top[threadIdx.x] = failed ? 0.0f : top;
