@@ -55,6 +55,8 @@ struct AttParams {
   int32_t m_tiles;    // tiles of 128 rows per key head
   int32_t d_blocks, v_blocks;  // 128-byte blocks of an entry's keys and values
   int32_t shared;     // v is a prefix of k's entries
+  int32_t page_shift;  // log2 of page_size, or -1
+  uint32_t pages, table_width;
   int32_t k_stages, v_stages;  // of the rings; no second ring when shared
   int32_t k_bytes, v_bytes;    // of a stage
   int32_t k_at, v_at;          // the rings, after Q
@@ -150,10 +152,14 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     const int64_t j = (static_cast<int64_t>(i) * cluster + rank) * kKeys + half * 32 + lane;
     return i < tiles && j < a.K && some ? indices[j] : -1;
   };
-  auto page_of = [&](int32_t pos) -> int32_t {
-    if (pos < first || pos > last) return -1;
-    const int32_t page = pos / a.page_size;
-    return table == nullptr ? page : page < a.table_width ? table[page] : -1;
+  auto page_index = [&](int32_t pos) -> uint32_t {
+    return p.page_shift >= 0 ? static_cast<uint32_t>(pos) >> p.page_shift
+                             : static_cast<uint32_t>(pos) / static_cast<uint32_t>(a.page_size);
+  };
+  auto page_of = [&](int32_t pos) -> uint32_t {  // ~0: not seen
+    if (pos < first || pos > last) return 0xffffffffu;
+    const uint32_t page = page_index(pos);
+    return table == nullptr ? page : page < p.table_width ? static_cast<uint32_t>(table[page]) : 0xffffffffu;
   };
   const bool gathers = warp >= 4 && warp < 8;
   int32_t pos = gathers ? index_of(0) : -1, pos1 = gathers ? index_of(1) : -1;
@@ -168,7 +174,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     fence_mbar_init();
   }
   if (warp == 8) tmem_alloc(&sh.tmem, p.tmem_cols);
-  int32_t page = page_of(pos);
+  uint32_t page = page_of(pos);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -198,26 +204,39 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     // 8 lanes fetch 128 bytes of an entry; step j has entries 4 j + lane / 8.
     const uint32_t unit16 = lane & 7, sub = lane >> 3;
     const uint32_t at = (values ? v_ring : k_ring) + (half * 32 + sub) * 128;
+    const E* mine = cache + unit16 * 8;
     const uint32_t even = (unit16 ^ sub) << 4, odd = (unit16 ^ (sub + 4)) << 4;
     int stage = 0;
     for (int i = 0; i < tiles; ++i) {
       const int32_t pos2 = index_of(i + 2);
-      const int32_t page1 = page_of(pos1);
-      const bool seen = page >= 0 && page < a.num_pages;
-      const int64_t entry = seen ? page * page_stride + pos % a.page_size * token_stride : 0;
+      const uint32_t page1 = page_of(pos1);
+      const bool seen = page < p.pages;
+      const uint32_t place = static_cast<uint32_t>(pos) - page_index(pos) * static_cast<uint32_t>(a.page_size);
+      const int64_t entry = seen ? page * page_stride + place * token_stride : 0;
       const uint32_t bits = __ballot_sync(0xffffffffu, seen);
       const int before = i - stages;
       if (before >= 0 && !wait_or_stop(&used[before & 7], (before >> 3) & 1, stop)) break;
       const uint32_t dst = at + stage * stage_bytes;
       const E* from[8];
+      uint32_t bytes[8];  // to copy: none of an entry that is not seen, whose place stays zero
 #pragma unroll
-      for (int j = 0; j < 8; ++j) from[j] = cache + __shfl_sync(0xffffffffu, entry, 4 * j + sub) + unit16 * 8;
-      for (int c = c0; c < c1; ++c) {
-        const bool inside = c * 64 + static_cast<int>(unit16) * 8 < dim;
+      for (int j = 0; j < 8; ++j) {
+        from[j] = mine + __shfl_sync(0xffffffffu, entry, 4 * j + sub);
+        bytes[j] = (bits >> (4 * j + sub)) & 1 ? 16 : 0;
+      }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          copy16(dst + c * (kKeys * 128) + j * 512 + (j & 1 ? odd : even), inside ? from[j] + c * 64 : cache,
-                 inside && ((bits >> (4 * j + sub)) & 1));
+      for (int c = 0; c < SPARSE_ATTENTION_MAX_D / 64; ++c) {
+        if (c < c0 || c >= c1) continue;
+        if (c * 64 + 64 <= dim) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) copy_bytes(dst + c * (kKeys * 128) + j * 512 + (j & 1 ? odd : even), from[j] + c * 64, bytes[j]);
+        } else {  // the last block of a dimension that does not fill it
+          const bool inside = c * 64 + static_cast<int>(unit16) * 8 < dim;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            copy_bytes(dst + c * (kKeys * 128) + j * 512 + (j & 1 ? odd : even), inside ? from[j] + c * 64 : mine,
+                       inside ? bytes[j] : 0);
+        }
       }
       copy_arrive(&full[stage]);
       if (w < 2) {
@@ -542,6 +561,11 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   p.a = a;
   p.heads = a.Hq / a.Hkv;
   p.m_tiles = (p.heads + 127) / 128;
+  p.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page_size == 1 << i) p.page_shift = i;
+  p.pages = a.num_pages < INT32_MAX ? static_cast<uint32_t>(a.num_pages) : INT32_MAX;
+  p.table_width = a.table_width < INT32_MAX ? static_cast<uint32_t>(a.table_width) : INT32_MAX;
   p.d_blocks = (a.D + 63) / 64;
   p.v_blocks = (a.Dv + 63) / 64;
   p.shared = a.k == a.v && a.Dv <= a.D && a.k_page_stride == a.v_page_stride && a.k_token_stride == a.v_token_stride &&

@@ -156,11 +156,12 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// 16 bytes from global to shared memory, past L1; zeros, with nothing read,
-// unless `valid`.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+// 16 bytes from global to shared memory, past L1: the first `bytes` (16 or 0)
+// of them read, the rest zeros.
+__device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) { copy_bytes(dst, src, valid ? 16 : 0); }
 // One arrival on `bar` when every copy16 of this thread so far is complete;
 // it counts against the arrivals the barrier was initialised with.
 __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
