@@ -20,12 +20,13 @@
 // which join their sums through distributed shared memory: one launch, no
 // workspace, the same order on every call.
 //
-// Warps 0-3: softmax, one row per thread; 4-7: gather entries through the page
-// table with 16-byte asynchronous copies, zeros for what is not seen; 8: one
-// thread issues the products. Keys and values have rings of their own, filled
-// by two warps each: a stage of keys is free again right after Q K^T, so the
-// gathers run ahead of the softmax (one ring of both, two stages deep, left
-// every tile waiting for its gather: 3.5 us a tile for one CTA).
+// Warps 0-3: softmax, one row per thread; 4-11: gather entries through the page
+// table with 16-byte asynchronous copies, zeros for what is not seen, in two
+// sets that take tiles in turn; 12 and 13: one thread each issues Q K^T and
+// P V. Keys and values have rings of their own, filled by two warps of a set
+// each: a stage of keys is free again right after Q K^T, so the gathers run
+// ahead of the softmax (one ring of both, two stages deep, left every tile
+// waiting for its gather: 3.5 us a tile).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -39,7 +40,8 @@ namespace tki {
 namespace {
 
 constexpr int kKeys = 64;  // entries per tile
-constexpr int kAttThreads = 9 * 32;
+constexpr int kGatherWarps = 8, kMmaWarp = 4 + kGatherWarps;
+constexpr int kAttThreads = (kMmaWarp + 2) * 32;  // Q K^T, then P V
 constexpr int kMaxStages = 6;
 // Masks outlive their keys' stage: tile j's are written when the products of
 // tile j - stages are issued, which follow the softmax of the tile kMaxBufs
@@ -146,8 +148,8 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   const int32_t last = a.query_positions != nullptr ? a.query_positions[row] : INT32_MAX;
   const int32_t first = a.first != nullptr ? max(a.first[row], 0) : 0;
   const bool some = a.page_size > 0 && a.num_pages > 0;
-  // Gathering: each lane looks up one entry of a tile, its index two tiles
-  // ahead, its page id one.
+  // Gathering: each lane looks up one entry of a tile, its index two of
+  // the warp's tiles ahead, its page id one.
   auto index_of = [&](int i) -> int32_t {
     const int64_t j = (static_cast<int64_t>(i) * cluster + rank) * kKeys + half * 32 + lane;
     return i < tiles && j < a.K && some ? indices[j] : -1;
@@ -161,8 +163,9 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     const uint32_t page = page_index(pos);
     return table == nullptr ? page : page < p.table_width ? static_cast<uint32_t>(table[page]) : 0xffffffffu;
   };
-  const bool gathers = warp >= 4 && warp < 8;
-  int32_t pos = gathers ? index_of(0) : -1, pos1 = gathers ? index_of(1) : -1;
+  const bool gathers = warp >= 4 && warp < kMmaWarp;
+  const int turn = (warp - 4) >> 2;  // of the two sets of gathering warps, which take tiles in turn
+  int32_t pos = gathers ? index_of(turn) : -1, pos1 = gathers ? index_of(turn + 2) : -1;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.k_stages; ++i) mbar_init(&sh.k_full[i], p.shared ? 128 : 64);
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     sh.stop = 0;
     fence_mbar_init();
   }
-  if (warp == 8) tmem_alloc(&sh.tmem, p.tmem_cols);
+  if (warp == kMmaWarp) tmem_alloc(&sh.tmem, p.tmem_cols);
   uint32_t page = page_of(pos);
   tc_fence_before();
   __syncthreads();
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     // ---- gather ----
     // Warps 0 and 1 fetch the tile's entries 0-31 and 32-63, keys; warps 2
     // and 3 their values, or the second half of their blocks when shared.
-    const int w = warp - 4;
+    const int w = (warp - 4) & 3;
     const bool values = w >= 2 && !p.shared;
     const int split = (p.d_blocks + 1) / 2;  // shared: blocks of the first two warps
     const int c0 = w >= 2 && p.shared ? split : 0;
@@ -206,9 +209,9 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     const uint32_t at = (values ? v_ring : k_ring) + (half * 32 + sub) * 128;
     const E* mine = cache + unit16 * 8;
     const uint32_t even = (unit16 ^ sub) << 4, odd = (unit16 ^ (sub + 4)) << 4;
-    int stage = 0;
-    for (int i = 0; i < tiles; ++i) {
-      const int32_t pos2 = index_of(i + 2);
+    int stage = turn;
+    for (int i = turn; i < tiles; i += 2) {
+      const int32_t pos2 = index_of(i + 4);
       const uint32_t page1 = page_of(pos1);
       const bool seen = page < p.pages;
       const uint32_t place = static_cast<uint32_t>(pos) - page_index(pos) * static_cast<uint32_t>(a.page_size);
@@ -246,58 +249,57 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
         if (lane == 0) mbar_arrive(&sh.masks[i % kMasks]);
       }
       pos = pos1, pos1 = pos2, page = page1;
-      if (++stage == stages) stage = 0;
+      stage += 2;
+      if (stage >= stages) stage -= stages;
     }
     copy_commit();
     copy_wait<0>();
-  } else if (warp == 8) {
-    // ---- products ----
-    const uint32_t desc_s = mma_desc(Pack<E>::type, kKeys);
-    const uint32_t desc_o = mma_desc(Pack<E>::type, (a.Dv + 15) / 16 * 16, true);
-    const uint64_t q_desc = operand_desc(base);
-    const uint64_t k_desc = operand_desc(k_ring);
-    const uint64_t v_desc = operand_desc(p.shared ? k_ring : v_ring, kKeys * 128);
-    int k_stage = 0, k_turn = 0, v_stage = 0, v_turn = 0;
-    const int v_stages = p.shared ? p.k_stages : p.v_stages, v_bytes = p.shared ? p.k_bytes : p.v_bytes;
-    auto scores = [&](int i, uint32_t buf) -> bool {
-      if (!wait_or_stop_one(&sh.k_full[k_stage], k_turn, stop)) return false;
-      fence_proxy_async_smem();
-      tc_fence_after();
-      const uint64_t kd = k_desc + static_cast<uint32_t>(k_stage * p.k_bytes >> 4);
-      const uint32_t to = tmem + buf * kKeys;
-      for (int c = 0; c < p.d_blocks; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_f16(to, q_desc + static_cast<uint32_t>(c * (128 * 128 >> 4) + j * 2),
-                  kd + static_cast<uint32_t>(c * (kKeys * 128 >> 4) + j * 2), desc_s, c + j > 0);
-      mma_commit(&sh.s_full[i & 7]);
-      if (++k_stage == p.k_stages) k_stage = 0, k_turn ^= 1;
-      return true;
-    };
-    // one thread from here: its waits need no vote
-    if (tiles > 0 && elect_one()) {
-      bool ok = wait_or_stop_one(&sh.q_full, 0, stop) && scores(0, 0);
-      uint32_t buf = 0;
-      for (int i = 0; i < tiles && ok; ++i) {
-        const uint32_t next = buf + 1 == static_cast<uint32_t>(p.bufs) ? 0 : buf + 1;
-        if (i + 1 < tiles) {
-          const int before = i + 1 - p.bufs;  // the next scores go where its weights were
-          ok = (before < 0 || wait_or_stop_one(&sh.pv_done[before & 7], (before >> 3) & 1, stop)) && scores(i + 1, next);
-        }
-        if (ok && !p.shared) {
-          ok = wait_or_stop_one(&sh.v_full[v_stage], v_turn, stop);
-          fence_proxy_async_smem();
-        }
-        ok = ok && wait_or_stop_one(&sh.p_full[i & 7], (i >> 3) & 1, stop);
-        if (!ok) break;
+  } else if (warp == kMmaWarp) {
+    // ---- S = Q K^T, by one thread, whose waits need no vote ----
+    if (tiles > 0 && elect_one() && wait_or_stop_one(&sh.q_full, 0, stop)) {
+      const uint32_t desc = mma_desc(Pack<E>::type, kKeys);
+      const uint64_t q_desc = operand_desc(base), k_desc = operand_desc(k_ring);
+      int stage = 0, turn_of = 0;
+      uint32_t to = tmem;
+      for (int i = 0; i < tiles; ++i) {
+        const int before = i - p.bufs;  // these scores go where its weights were
+        if (before >= 0 && !wait_or_stop_one(&sh.pv_done[before & 7], (before >> 3) & 1, stop)) break;
+        if (!wait_or_stop_one(&sh.k_full[stage], turn_of, stop)) break;
+        fence_proxy_async_smem();
         tc_fence_after();
-        const uint64_t vd = v_desc + static_cast<uint32_t>(v_stage * v_bytes >> 4);
+        const uint64_t kd = k_desc + static_cast<uint32_t>(stage * p.k_bytes >> 4);
+        for (int c = 0; c < p.d_blocks; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f16(to, q_desc + static_cast<uint32_t>(c * (128 * 128 >> 4) + j * 2),
+                    kd + static_cast<uint32_t>(c * (kKeys * 128 >> 4) + j * 2), desc, c + j > 0);
+        mma_commit(&sh.s_full[i & 7]);
+        if (++stage == p.k_stages) stage = 0, turn_of ^= 1;
+        to = to + kKeys == tmem_o ? tmem : to + kKeys;
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp + 1) {
+    // ---- O += P V, by another, so that neither's waits hold up the other ----
+    if (tiles > 0 && elect_one()) {
+      const uint32_t desc = mma_desc(Pack<E>::type, (a.Dv + 15) / 16 * 16, true);
+      const uint64_t v_desc = operand_desc(p.shared ? k_ring : v_ring, kKeys * 128);
+      const int stages = p.shared ? p.k_stages : p.v_stages, stage_bytes = p.shared ? p.k_bytes : p.v_bytes;
+      uint64_t* full = p.shared ? sh.k_full : sh.v_full;
+      int stage = 0, turn_of = 0;
+      uint32_t from = tmem;
+      for (int i = 0; i < tiles; ++i) {
+        if (!wait_or_stop_one(&full[stage], turn_of, stop)) break;
+        fence_proxy_async_smem();
+        if (!wait_or_stop_one(&sh.p_full[i & 7], (i >> 3) & 1, stop)) break;
+        tc_fence_after();
+        const uint64_t vd = v_desc + static_cast<uint32_t>(stage * stage_bytes >> 4);
 #pragma unroll
         for (int j = 0; j < kKeys / 16; ++j)
-          mma_f16_ts(tmem_o, tmem + buf * kKeys + j * 8, vd + static_cast<uint32_t>(j * (16 * 128 >> 4)), desc_o, i + j > 0);
+          mma_f16_ts(tmem_o, from + j * 8, vd + static_cast<uint32_t>(j * (16 * 128 >> 4)), desc, i + j > 0);
         mma_commit(&sh.pv_done[i & 7]);
-        if (++v_stage == v_stages) v_stage = 0, v_turn ^= 1;
-        buf = next;
+        if (++stage == stages) stage = 0, turn_of ^= 1;
+        from = from + kKeys == tmem_o ? tmem : from + kKeys;
       }
     }
     __syncwarp();
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   // rows as fit its lanes (Dv <= 256: one at least).
   const int per_row = a.Dv / 8, at_once = 32 / per_row;
   const int sub_row = lane / per_row, c = (lane - sub_row * per_row) * 8;
-  const int step = 9 * at_once;
+  const int step = (kAttThreads / 32) * at_once;
   const int row0 = sub_row < at_once ? warp * at_once + sub_row : heads;
   E* out = static_cast<E*>(a.out) + (row * a.Hq + head0) * a.Dv;
   auto write = [&](int h, int c, const float (&x)[8]) {
@@ -500,27 +502,35 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     const uint32_t top_addr = smem_addr(sh.head_top), sum_addr = smem_addr(sh.head_sum), rows_addr = smem_addr(rows);
     // the CTAs take rows in turn; reads of all CTAs are in flight together
     for (int h = row0 < heads ? row0 + static_cast<int>(rank) * step : heads; h < heads; h += cluster * step) {
-      float m[8], l[8];
-      float4 u[8], v[8];
+      float m[8], l[8], all = __int_as_float(0xff800000), total = 0.0f;
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         const uint32_t from = r < cluster ? r : 0;
         m[r] = __uint_as_float(ld_dsmem_u32(map_rank(top_addr + 4 * h, from)));
         l[r] = __uint_as_float(ld_dsmem_u32(map_rank(sum_addr + 4 * h, from)));
-        u[r] = ld_dsmem_f4(map_rank(rows_addr + 4 * (h * pad + c), from));
-        v[r] = ld_dsmem_f4(map_rank(rows_addr + 4 * (h * pad + c) + 16, from));
       }
-      float all = m[0], total = 0.0f;
 #pragma unroll
-      for (int r = 1; r < 8; ++r) all = fmaxf(all, m[r]);
+      for (int r = 0; r < 8; ++r) all = fmaxf(all, m[r]);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        m[r] = r >= cluster || is_low(m[r]) ? 0.0f : exp2_fast(m[r] - all);
+        total += r >= cluster ? 0.0f : l[r] != l[r] ? l[r] : l[r] * m[r];
+      }
       float x[8] = {};
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r < cluster) {
-          const float f = is_low(m[r]) ? 0.0f : exp2_fast(m[r] - all);
-          total += l[r] != l[r] ? l[r] : l[r] * f;
-          add(x, u[r], v[r], f);
+      for (int r0 = 0; r0 < 8; r0 += 4) {
+        if (r0 >= cluster) break;
+        float4 u[4], v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t from = r0 + r < cluster ? r0 + r : 0;
+          u[r] = ld_dsmem_f4(map_rank(rows_addr + 4 * (h * pad + c), from));
+          v[r] = ld_dsmem_f4(map_rank(rows_addr + 4 * (h * pad + c) + 16, from));
         }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (r0 + r < cluster) add(x, u[r], v[r], m[r0 + r]);
+      }
       const float f = inverse(all, total);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] *= f;
@@ -529,7 +539,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     }
     cluster_sync();  // the others may still read this CTA's rows
   }
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_free(tmem, p.tmem_cols);
   }
