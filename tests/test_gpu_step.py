@@ -476,6 +476,24 @@ def test_repeated_calls_agree():
         assert torch.equal(tk.indexer_scores(*args[:5], out=base.clone()), one)
 
 
+def test_example_step():
+    """The example's decode step against its own plain form: the selection may
+    differ where scores are within rounding of the cutoff, a few entries of
+    2 x 10^-3 of the weight each."""
+    import os
+    import sys
+
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import sparse_step as ex
+
+    torch.manual_seed(3)
+    cache, f, token = ex.make(5, 900)
+    got = ex.step(cache, f, *token, 128)
+    want = ex.step_plain(cache, f, *token, 128)
+    # two roundings of bfloat16 results and one of its weights, then a swapped entry
+    assert (got - want).float().norm() <= (3 * 2.0 ** -8 + 0.02) * want.float().norm()
+
+
 # ---- refusals that need tensors on the GPU -----------------------------------------------------------
 
 
