@@ -49,9 +49,16 @@ class _AttentionArgs(ctypes.Structure):
 
 
 
-def _raw_stream(index: int) -> int:
-    """The handle of the device's current stream, without a Stream object."""
-    return torch._C._cuda_getCurrentRawStream(index)
+# The current device's index and the handle of its current stream, without the
+# Python objects around them (torch.cuda's own functions, a microsecond less).
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _raw_stream_slow(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream_slow)
 
 
 _FORMATS = {_i32: "i", _i64: "q", _f32: "f", _vp: "P"}
@@ -83,7 +90,7 @@ class _Call:
         except (struct.error, OverflowError) as error:
             raise ValueError(f"{self.name}: an argument is out of range ({error})") from None
         handle = _raw_stream(index) if stream is None else stream.cuda_stream
-        if torch.cuda.current_device() == index:
+        if _current_device() == index:
             status = fn(packed, handle)
         else:
             with torch.cuda.device(index):
@@ -97,17 +104,22 @@ _rotary, _scores, _attention = (_Call("sparse_rotary", _RotaryArgs), _Call("spar
                                 _Call("sparse_attention", _AttentionArgs))
 
 
+def _dims(t, name: str, dims: int) -> None:
+    raise ValueError(f"{name} must be a {dims}-D tensor")
+
+
 def _main(t, name: str, dims: int, types):
     """Shape, strides, type code and device of a call's main tensor."""
-    if not isinstance(t, torch.Tensor) or t.dim() != dims:
-        raise ValueError(f"{name} must be a {dims}-D tensor")
-    index = t.get_device()
+    try:
+        shape, strides, index, code = t.shape, t.stride(), t.get_device(), types.get(t.dtype)
+    except AttributeError:
+        _dims(t, name, dims)
+    if len(shape) != dims:
+        _dims(t, name, dims)
     if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    code = types.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be one of {', '.join(str(d) for d in types)}, not {t.dtype}")
-    shape, strides = t.shape, t.stride()
     if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
     return shape, strides, code, index
@@ -115,13 +127,16 @@ def _main(t, name: str, dims: int, types):
 
 def _other(t, name: str, dims: int, dtype, index: int):
     """Shape and strides of a further tensor of this type on that device."""
-    if not isinstance(t, torch.Tensor) or t.dim() != dims:
-        raise ValueError(f"{name} must be a {dims}-D tensor")
+    try:
+        shape, strides = t.shape, t.stride()
+    except AttributeError:
+        _dims(t, name, dims)
+    if len(shape) != dims:
+        _dims(t, name, dims)
     if t.get_device() != index:
         raise ValueError(f"{name} must be a CUDA tensor on the device of the other arguments")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    shape, strides = t.shape, t.stride()
     if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
     return shape, strides
@@ -129,11 +144,21 @@ def _other(t, name: str, dims: int, dtype, index: int):
 
 def _whole(t, name: str, shape, dtype, index: int) -> int:
     """The address of a contiguous tensor of exactly this shape and type."""
-    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.get_device() != index \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on the device of the "
-                         "other arguments")
-    return t.data_ptr()
+    try:
+        if t.dtype == dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on the device of the other "
+                     "arguments")
+
+
+def _empty(shape, dtype, like, stream):
+    """A result's memory, which belongs to the stream that the call runs on."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _span(address: int, shape, strides, size: int):
@@ -236,7 +261,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
         if os != shape:
             raise ValueError("out must have the shape of x")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
+        out = _empty(shape, dtype, x, stream)
         target, ot = out.data_ptr(), out.stride()
     else:
         target = out.data_ptr()
@@ -279,7 +304,7 @@ def indexer_scores(q: torch.Tensor, weights: torch.Tensor, keys: torch.Tensor, l
     scales = 0 if key_scales is None else _whole(key_scales, "key_scales", (pages, page_size), _FP32, index)
     if out is None:
         width = ps[1] * page_size if width is None else int(width)
-        out = torch.empty((B, T, width), dtype=_FP32, device=q.device)
+        out = _empty((B, T, width), _FP32, q, stream)
         ot = out.stride()
     else:
         os, ot = _other(out, "out", 3, _FP32, index)
@@ -345,7 +370,7 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
         raise ValueError("scale and softcap must be finite, softcap not negative")
     at_q, at_k, at_v = q.data_ptr(), k.data_ptr(), v.data_ptr()
     if out is None:
-        out = torch.empty((B, T, Hq, Dv), dtype=dtype, device=q.device)
+        out = _empty((B, T, Hq, Dv), dtype, q, stream)
         target = out.data_ptr()
     else:
         target = _whole(out, "out", (B, T, Hq, Dv), dtype, index)
@@ -353,7 +378,7 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
         if _overlap(mine, _span(at_q, shape, qs, 2)) or _overlap(mine, _span(at_k, ks, kt, 2)) \
                 or _overlap(mine, _span(at_v, vs, vt, 2)):
             raise ValueError("out must not overlap q, k or v")
-    lse = torch.empty((B, T, Hq), dtype=_FP32, device=q.device) if return_lse else None
+    lse = _empty((B, T, Hq), _FP32, q, stream) if return_lse else None
     _attention(index, stream, at_q, qs[0], qs[1], qs[2], at_k, kt[0], kt[1], kt[2], at_v, vt[0], vt[1], vt[2], idx, table,
                pt, width, qp, begin, bias, target, 0 if lse is None else lse.data_ptr(), pages, page_size, B, T, Hq, Hkv,
                D, Dv, K, code, scale, softcap)

@@ -71,7 +71,7 @@ struct AttShared {
   float away[kMasks][kKeys];           // position - query's, per entry of a tile
   uint32_t seen[kMasks][2];            // bit per entry
   float top[128], sum[128];            // of the rows
-  float head_top[128], head_sum[128];  // of the heads: the copies joined
+  float head_top[128], head_sum[128];  // of the heads, the copies joined; 1 / sum in a CTA that is alone
   uint64_t k_full[kMaxStages], v_full[kMaxStages], masks[kMasks], q_full;
   // Of tile i at i % 8: scores there, weights there, products with v done.
   // Nobody who waits on one lags behind by eight tiles.
@@ -427,6 +427,9 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   __syncthreads();
   const int pad = p.v_blocks * 64 + 4;  // floats per row: rows 4 banks apart
   float* rows = reinterpret_cast<float*>(smem);
+  // A row's factor, 1 / its sum of weights: zero where nothing is seen.
+  auto inverse = [](float all, float total) { return total != total ? total : is_low(all) ? 0.0f : 1.0f / total; };
+  auto logsum = [](float all, float total) { return total != total ? total : is_low(all) ? all : (all + log2f(total)) * kLn2; };
   if (warp < 4) {
     const int h = threadIdx.x % kRows;
     float all = sh.top[h], total = 0.0f;
@@ -437,18 +440,22 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
       const float m = sh.top[c * kRows + h], l = sh.sum[c * kRows + h];
       total += l != l ? l : is_low(m) ? 0.0f : l * exp2_fast(m - all);
     }
-    if (threadIdx.x < kRows) sh.head_top[h] = all, sh.head_sum[h] = total;
+    if (threadIdx.x < kRows) {
+      sh.head_top[h] = all;
+      sh.head_sum[h] = cluster == 1 ? inverse(all, total) : total;
+      if (cluster == 1 && a.lse != nullptr && h < heads) a.lse[row * a.Hq + head0 + h] = logsum(all, total);
+    }
     const float weight = is_low(top) ? 0.0f : exp2_fast(top - all);
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
-    for (int c = 0; c < a.Dv; c += 16) {
-      uint32_t v[16] = {};
+    for (int c = 0; c < a.Dv; c += 32) {  // past Dv: columns that nothing reads, in the rows' padding
+      uint32_t v[32] = {};
       if (tiles > 0) {
         tmem_ld(v, tmem_o + lanes + c);
         tmem_wait_ld(v);
       }
       float* dst = rows + threadIdx.x * pad + c;
 #pragma unroll
-      for (int j = 0; j < 16; j += 4)
+      for (int j = 0; j < 32; j += 4)
         *reinterpret_cast<float4*>(dst + j) =
             make_float4(__uint_as_float(v[j]) * weight, __uint_as_float(v[j + 1]) * weight,
                         __uint_as_float(v[j + 2]) * weight, __uint_as_float(v[j + 3]) * weight);
@@ -473,9 +480,6 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     x[0] += u.x * f, x[1] += u.y * f, x[2] += u.z * f, x[3] += u.w * f;
     x[4] += v.x * f, x[5] += v.y * f, x[6] += v.z * f, x[7] += v.w * f;
   };
-  // A row's factor, 1 / its sum of weights: zero where nothing is seen.
-  auto inverse = [](float all, float total) { return total != total ? total : is_low(all) ? 0.0f : 1.0f / total; };
-  auto logsum = [](float all, float total) { return total != total ? total : is_low(all) ? all : (all + log2f(total)) * kLn2; };
   for (int h = row0; h < heads; h += step) {
     float x[8] = {};
 #pragma unroll
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
       add(x, *reinterpret_cast<const float4*>(from), *reinterpret_cast<const float4*>(from + 4), 1.0f);
     }
     if (cluster == 1) {
-      const float f = inverse(sh.head_top[h], sh.head_sum[h]);
+      const float f = sh.head_sum[h];
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] *= f;
       write(h, c, x);
@@ -494,10 +498,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
       *reinterpret_cast<float4*>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
     }
   }
-  if (cluster == 1) {
-    if (a.lse != nullptr && threadIdx.x < heads)
-      a.lse[row * a.Hq + head0 + threadIdx.x] = logsum(sh.head_top[threadIdx.x], sh.head_sum[threadIdx.x]);
-  } else {
+  if (cluster > 1) {
     cluster_sync();
     const uint32_t top_addr = smem_addr(sh.head_top), sum_addr = smem_addr(sh.head_sum), rows_addr = smem_addr(rows);
     // the CTAs take rows in turn; reads of all CTAs are in flight together

@@ -460,6 +460,54 @@ def test_calls_take_their_stream_argument():
     assert torch.equal(out, want)
 
 
+def test_results_belong_to_the_calls_stream():
+    """A result allocated by a call on another stream is that stream's memory:
+    freed there, it is not handed to the current stream while in use."""
+    x, f, pos = _randn((64, 8, 64), 1, BF16), tk.rotary_frequencies(64, device=DEV), _ints(list(range(64)))
+    side = torch.cuda.Stream()
+    want = tk.rotary(x, pos, f)
+    torch.cuda.synchronize()
+    got = tk.rotary(x, pos, f, stream=side)
+    at = got.data_ptr()
+    side.synchronize()
+    assert torch.equal(got, want)
+    del got
+    assert torch.empty_like(x).data_ptr() != at  # the current stream's pool has other blocks
+
+
+@pytest.mark.parametrize("ps", [64, 48])
+def test_offsets_past_32_bits(ps):
+    """Entries behind 2^32 elements of a cache (10 GB), by boxes and by copies."""
+    pages = (1 << 32) // (ps * 128) + 64
+    keys = torch.empty((pages, ps, 128), dtype=BF16, device=DEV)
+    last = list(range(pages - 9, pages))
+    table = _ints([last])
+    keys[last[0]:] = _randn((9, ps, 128), 5, BF16)
+    width = 8 * ps + 3
+    q, w = _randn((1, 1, 8, 128), 6, BF16), _randn((1, 1, 8), 7)
+    few = keys[last[0]:].contiguous()
+    local = _ints([list(range(9))])
+    n = _ints([[width]])
+    assert torch.equal(tk.indexer_scores(q, w, keys, n, table, width=width), tk.indexer_scores(q, w, few, n, local, width=width))
+    idx = torch.arange(width, dtype=torch.int32, device=DEV).view(1, 1, -1)
+    cache, small = keys[:, :, None], few[:, :, None]
+    assert torch.equal(tk.sparse_attention(q, cache, cache, idx, table), tk.sparse_attention(q, small, small, idx, local))
+    if pages * ps < 2 ** 31:
+        f, pos = tk.rotary_frequencies(128, device=DEV), _ints([5, 6])
+        slots = _ints([pages * ps - 1, pages * ps - ps])
+        tk.rotary(q[0, 0, :2, None], pos, f, out=cache, slots=slots)
+        assert torch.equal(cache.view(-1, 1, 128)[slots.long()], tk.rotary(q[0, 0, :2, None], pos, f))
+
+
+def test_attention_keeps_nan_that_is_seen():
+    q, k, v, idx, table = _attention_case(1, 1, 8, 2, 64, 64, 100, 200, 16, BF16)
+    p = int(idx[0, 0, 40])
+    k[table[0, p // 16].long(), p % 16, 0] = math.nan
+    out, lse = tk.sparse_attention(q, k, v, idx, table, return_lse=True)
+    assert torch.isnan(out[0, 0, :4]).all() and torch.isnan(lse[0, 0, :4]).all()
+    assert torch.isfinite(out[0, 0, 4:]).all() and torch.isfinite(lse[0, 0, 4:]).all()
+
+
 def test_repeated_calls_agree():
     """Byte for byte, on a batch whose rows are split over several CTAs and on
     one that is not."""
