@@ -8,7 +8,8 @@
 // 256 at most). So one thread of the epilogue holds all the products of one
 // position, and the sum over heads needs no exchange: a maximum and a
 // multiply-add per product (packed multiply-adds cost a move each, 4.6
-// instructions a product in all). A tile of keys is fetched once for all
+// instructions a product in all; the accumulator's own layout, which needs a
+// quarter of the weights per thread, reads TMEM slower: 303 us for the prefill). A tile of keys is fetched once for all
 // query tokens of its group.
 //
 // One CTA per SM, 20 warps: three fetch (keys through the page table into a
@@ -17,6 +18,14 @@
 // work unit), one thread issues the products into two TMEM buffers, sixteen
 // warps sum over heads. Work units are (sequence, range of tiles, group of
 // query tokens).
+//
+// Measured: decode, 64 sequences of up to 65536 positions, 64 heads, bf16, 157
+// us, 6.3 TB/s (145 us for its bytes at the measured copy rate): HBM bound.
+// Prefill, 2048 tokens on 8192 positions, 170 to 180 us, 1.4 PFLOP/s (127 us at
+// the measured matrix rate): the sums over heads keep the issue slots busy about
+// as long as the products keep the tensor cores, and the two overlap only so far
+// with two TMEM buffers. e4m3, 32 sequences x 2 tokens x 32769, 40 us (20): one
+// tile is 16 KB and its fixed cost per warp shows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -6,15 +6,19 @@
 // in integer arithmetic modulo 2^64: whole turns drop out by themselves and
 // the fraction is exact up to the rate's rounding (2^-64 turns) times the
 // position, 2^-33 turns at position 2^31, where a product in FP32 would be
-// off by whole turns. Its top 32 bits go to sinpi / cospi as FP32.
+// off by whole turns. Its top 32 bits go to the trigonometric functions as FP32.
 //
 // The work. Memory bound: each element is read and written once, with three
 // operations. A thread owns one 16-byte item of the head (two, where the
 // second half's partner goes with it) of one token and walks over heads, so
 // that it computes its pairs' cos and sin once, in registers, while its first
 // loads are in flight; no shared memory, no barrier. (A table per CTA in shared
-// memory put two barriers between loads and stores: 87 us instead of 44 for
-// 8192 tokens x 64 heads x 128, bf16; reading and writing alone take 40.)
+// memory put two barriers between loads and stores: 87 us for 8192 tokens x 64
+// heads x 128, bf16.)
+//
+// Measured: that case 43 us, 6.2 TB/s, against 39.6 us for its bytes at the
+// measured copy rate; 4097 x 24 x 80 in FP32 9.2 us (9.3); four tokens 3.5 us,
+// most of it the launch and three dependent reads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -27,6 +31,7 @@ namespace tki {
 namespace {
 
 constexpr int kRotThreads = 256;
+
 struct RotParams {
   const void* x;
   int64_t x_token, x_head;
