@@ -65,6 +65,7 @@ struct AttParams {
   sparse_attention_args a;
   int32_t heads;      // query heads per key head
   int32_t m_tiles;    // tiles of 128 rows per key head
+  uint32_t works;     // (row, key head, tile of rows)
   int32_t d_blocks, v_blocks;  // 128-byte blocks of an entry's keys and values
   int32_t shared;     // v is a prefix of k's entries
   int32_t page_shift;  // log2 of page_size, or -1
@@ -86,6 +87,8 @@ struct AttShared {
   // Of tile i at i % 8: scores there, weights there, products with v done.
   // Nobody who waits on one lags behind by eight tiles.
   uint64_t s_full[8], p_full[8], pv_done[8];
+  uint64_t q_empty, o_free;  // Q used up, O read: between one work and the next
+  alignas(16) float part[64][20];  // 16 columns of rows on their way from one copy to the other, padded
   uint32_t tmem;
   uint32_t stop;
 };
@@ -129,8 +132,64 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
+struct Work {
+  int g, heads, head0;  // key head; real rows, and the first one's query head
+  int64_t row, b, t;
+};
+
+__device__ __forceinline__ Work work_of(const AttParams& p, uint32_t w) {
+  Work r;
+  const uint32_t pair = w / static_cast<uint32_t>(p.m_tiles), row = pair / static_cast<uint32_t>(p.a.Hkv);
+  const int m_tile = static_cast<int>(w - pair * p.m_tiles);
+  const uint32_t b = row / static_cast<uint32_t>(p.a.T);
+  r.g = static_cast<int>(pair - row * p.a.Hkv);
+  r.heads = min(p.heads - m_tile * 128, 128);
+  r.head0 = r.g * p.heads + m_tile * 128;
+  r.row = row, r.b = b, r.t = row - b * static_cast<uint32_t>(p.a.T);
+  return r;
+}
+
+// The four softmax warps among themselves.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Q of a work, by 128 threads, 8 per 128 bytes of a row; each arrives twice.
 template <typename E, int COPIES>
-__global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
+__device__ __forceinline__ void fetch_queries(const AttParams& p, const Work& k, unsigned char* smem, uint64_t* q_full, int th) {
+  const sparse_attention_args& a = p.a;
+  const void* nowhere = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(a.q) & ~static_cast<uintptr_t>(15));
+  const int unit16 = th & 7, sub = th >> 3;
+  const E* q = static_cast<const E*>(a.q) + k.b * a.q_seq_stride + k.t * a.q_token_stride + k.head0 * a.q_head_stride;
+  for (int c = 0; c < p.d_blocks; ++c) {
+    const int d = c * 64 + unit16 * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = 16 * j + sub, h = r % (128 / COPIES);
+      const bool real = h < k.heads && d < a.D;
+      const uint32_t at = c * (128 * 128) + swizzled(r, unit16);
+      const E* src = q + h * a.q_head_stride + d;
+      if (p.q_vector) {
+        copy16(smem_addr(smem) + at, real ? src : nowhere, real);
+      } else {
+        E v[8];
+        for (int e = 0; e < 8; ++e) v[e] = real ? src[e] : E(0.0f);
+        *reinterpret_cast<uint4*>(smem + at) = *reinterpret_cast<const uint4*>(v);
+      }
+    }
+  }
+  copy_arrive(q_full);
+  mbar_arrive(q_full);
+}
+
+// A row's factor, 1 / its sum of weights: zero where nothing is seen.
+__device__ __forceinline__ float inverse(float all, float total) {
+  return total != total ? total : is_low(all) ? 0.0f : 1.0f / total;
+}
+__device__ __forceinline__ float logsum(float all, float total) {
+  return total != total ? total : is_low(all) ? all : (all + log2f(total)) * kLn2;
+}
+
+template <typename E, int COPIES>
+__global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
     attention_kernel(const __grid_constant__ AttParams p, const int cluster) {
   extern __shared__ __align__(1024) unsigned char smem[];
   constexpr int kPart = kKeys / COPIES;             // entries of a tile that a row's copy takes
@@ -140,23 +199,26 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   const sparse_attention_args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster > 1 ? cluster_ctarank() : 0;
-  const uint32_t work = blockIdx.x / cluster, pair = work / p.m_tiles;
-  const int m_tile = static_cast<int>(work - pair * p.m_tiles);
-  const uint32_t row32 = pair / a.Hkv;
-  const int g = static_cast<int>(pair - row32 * a.Hkv);
-  const int64_t row = row32, b = row32 / a.T, t = row - b * a.T;
-  const int heads = min(p.heads - m_tile * 128, 128);  // real rows of this tile
-  const int head0 = g * p.heads + m_tile * 128;
+  // With one or two copies a CTA stays for several works, its roles running
+  // into the next one while the softmax warps end the last.
+  constexpr bool kStay = COPIES <= 2;
+  const uint32_t step_w = gridDim.x / cluster;
+  Work k = work_of(p, blockIdx.x / cluster);
   const int all_tiles = (a.K + kKeys - 1) / kKeys;
   const int tiles = all_tiles > static_cast<int>(rank) ? (all_tiles - static_cast<int>(rank) + cluster - 1) / cluster : 0;
   const uint32_t base = smem_addr(smem);
   const uint32_t k_ring = base + p.k_at, v_ring = base + p.v_at;
 
   const int half = warp & 1;  // of a tile's entries
-  const int32_t* indices = a.indices + row * a.K;
-  const int32_t* table = a.page_table != nullptr ? a.page_table + b * a.table_stride : nullptr;
-  const int32_t last = a.query_positions != nullptr ? a.query_positions[row] : INT32_MAX;
-  const int32_t first = a.first != nullptr ? max(a.first[row], 0) : 0;
+  const int32_t* indices = nullptr;
+  const int32_t* table = nullptr;
+  int32_t last = INT32_MAX, first = 0;
+  auto look_at = [&](const Work& k) {
+    indices = a.indices + k.row * a.K;
+    table = a.page_table != nullptr ? a.page_table + k.b * a.table_stride : nullptr;
+    last = a.query_positions != nullptr ? a.query_positions[k.row] : INT32_MAX;
+    first = a.first != nullptr ? max(a.first[k.row], 0) : 0;
+  };
   const bool some = a.page_size > 0 && a.num_pages > 0;
   // Gathering: each lane looks up one entry of a tile, its index two of
   // the warp's tiles ahead, its page id one.
@@ -175,6 +237,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   };
   const bool gathers = warp >= 4 && warp < kMmaWarp;
   const int turn = (warp - 4) >> 2;  // of the two sets of gathering warps, which take tiles in turn
+  if (gathers) look_at(k);
   int32_t pos = gathers ? index_of(turn) : -1, pos1 = gathers ? index_of(turn + 2) : -1;
 
   if (threadIdx.x == 0) {
@@ -183,6 +246,8 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     for (int i = 0; i < kMasks; ++i) mbar_init(&sh.masks[i], 2);
     mbar_init(&sh.q_full, 256);
     for (int i = 0; i < 8; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 128), mbar_init(&sh.pv_done[i], 1);
+    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.o_free, 128);
     sh.stop = 0;
     fence_mbar_init();
   }
@@ -193,7 +258,6 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   tc_fence_after();
   const uint32_t tmem = sh.tmem, tmem_o = tmem + p.bufs * kKeys;
   volatile uint32_t* stop = &sh.stop;
-  const void* nowhere = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(a.q) & ~static_cast<uintptr_t>(15));
 
   float top = __int_as_float(0xff800000), sum = 0.0f;  // of this thread's row (its reference and sum of weights)
 
@@ -207,8 +271,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     const int c0 = w >= 2 && p.shared ? split : 0;
     const int c1 = values ? p.v_blocks : w < 2 && p.shared ? split : p.d_blocks;
     const int dim = values ? a.Dv : a.D;
-    const E* cache = static_cast<const E*>(values ? a.v : a.k) +
-                     static_cast<int64_t>(g) * (values ? a.v_head_stride : a.k_head_stride);
+    const int64_t head_stride = values ? a.v_head_stride : a.k_head_stride;
     const int64_t page_stride = values ? a.v_page_stride : a.k_page_stride;
     const int64_t token_stride = values ? a.v_token_stride : a.k_token_stride;
     uint64_t* full = values ? sh.v_full : sh.k_full;
@@ -217,18 +280,33 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     // 8 lanes fetch 128 bytes of an entry; step j has entries 4 j + lane / 8.
     const uint32_t unit16 = lane & 7, sub = lane >> 3;
     const uint32_t at = (values ? v_ring : k_ring) + (half * 32 + sub) * 128;
-    const E* mine = cache + unit16 * 8;
     const uint32_t even = (unit16 ^ sub) << 4, odd = (unit16 ^ (sub + 4)) << 4;
-    int stage = turn;
-    for (int i = turn; i < tiles; i += 2) {
+    bool ok = true;
+    int n = 0, stage = turn;  // tiles before this work; n + i is a tile's number in the CTA
+    for (uint32_t w_at = blockIdx.x / cluster, nw = 0; w_at < p.works && ok; w_at += step_w, ++nw, n += tiles) {
+    const int i0 = (turn - n) & 1;  // the set's tiles: every other number
+    if (nw > 0) {
+      k = work_of(p, w_at);
+      look_at(k);
+      pos = index_of(i0), pos1 = index_of(i0 + 2);
+      if (tiles > 0 && turn == 0) {
+        ok = wait_or_stop(&sh.q_empty, (nw - 1) & 1, stop);
+        if (!ok) break;
+        fetch_queries<E, COPIES>(p, k, smem, &sh.q_full, threadIdx.x - 128);
+      }
+      page = page_of(pos);
+    }
+    const E* mine = static_cast<const E*>(values ? a.v : a.k) + k.g * head_stride + unit16 * 8;
+    for (int i = i0; i < tiles; i += 2) {
       const int32_t pos2 = index_of(i + 4);
       const uint32_t page1 = page_of(pos1);
       const bool seen = page < p.pages;
       const uint32_t place = static_cast<uint32_t>(pos) - page_index(pos) * static_cast<uint32_t>(a.page_size);
       const int64_t entry = seen ? page * page_stride + place * token_stride : 0;
       const uint32_t bits = __ballot_sync(0xffffffffu, seen);
-      const int before = i - stages;
-      if (before >= 0 && !wait_or_stop(&used[before & 7], (before >> 3) & 1, stop)) break;
+      const int before = n + i - stages;
+      ok = before < 0 || wait_or_stop(&used[before & 7], (before >> 3) & 1, stop);
+      if (!ok) break;
       const uint32_t dst = at + stage * stage_bytes;
       const E* from[8];
       uint32_t bytes[8];  // to copy: none of an entry that is not seen, whose place stays zero
@@ -253,39 +331,49 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
       }
       copy_arrive(&full[stage]);
       if (w < 2) {
-        sh.away[i % kMasks][half * 32 + lane] = static_cast<float>(seen ? pos - last : 0);
-        if (lane == 0) sh.seen[i % kMasks][half] = bits;
+        const int mask = (n + i) % kMasks;
+        sh.away[mask][half * 32 + lane] = static_cast<float>(seen ? pos - last : 0);
+        if (lane == 0) sh.seen[mask][half] = bits;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.masks[i % kMasks]);
+        if (lane == 0) mbar_arrive(&sh.masks[mask]);
       }
       pos = pos1, pos1 = pos2, page = page1;
       stage += 2;
       if (stage >= stages) stage -= stages;
     }
+    if (!kStay) break;
+    }
     copy_commit();
     copy_wait<0>();
   } else if (warp == kMmaWarp) {
     // ---- S = Q K^T, by one thread, whose waits need no vote ----
-    if (tiles > 0 && elect_one() && wait_or_stop_one(&sh.q_full, 0, stop)) {
+    if (tiles > 0 && elect_one()) {
       const uint32_t desc = mma_desc(Pack<E>::type, kKeys);
       const uint64_t q_desc = operand_desc(base), k_desc = operand_desc(k_ring);
-      int stage = 0, turn_of = 0;
+      int stage = 0, turn_of = 0, n = 0;
       uint32_t to = tmem;
-      for (int i = 0; i < tiles; ++i) {
-        const int before = i - p.bufs;  // these scores go where its weights were
-        if (before >= 0 && !wait_or_stop_one(&sh.pv_done[before & 7], (before >> 3) & 1, stop)) break;
-        if (!wait_or_stop_one(&sh.k_full[stage], turn_of, stop)) break;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint64_t kd = k_desc + static_cast<uint32_t>(stage * p.k_bytes >> 4);
-        for (int c = 0; c < p.d_blocks; ++c)
+      bool ok = true;
+      for (uint32_t w_at = blockIdx.x / cluster, nw = 0; w_at < p.works && ok; w_at += step_w, ++nw) {
+        ok = wait_or_stop_one(&sh.q_full, nw & 1, stop);
+        for (int i = 0; i < tiles && ok; ++i, ++n) {
+          const int before = n - p.bufs;  // these scores go where its weights were
+          ok = (before < 0 || wait_or_stop_one(&sh.pv_done[before & 7], (before >> 3) & 1, stop)) &&
+               wait_or_stop_one(&sh.k_full[stage], turn_of, stop);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const uint64_t kd = k_desc + static_cast<uint32_t>(stage * p.k_bytes >> 4);
+          for (int c = 0; c < p.d_blocks; ++c)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f16(to, q_desc + static_cast<uint32_t>(c * (128 * 128 >> 4) + j * 2),
-                    kd + static_cast<uint32_t>(c * (kKeys * 128 >> 4) + j * 2), desc, c + j > 0);
-        mma_commit(&sh.s_full[i & 7]);
-        if (++stage == p.k_stages) stage = 0, turn_of ^= 1;
-        to = to + kKeys == tmem_o ? tmem : to + kKeys;
+            for (int j = 0; j < 4; ++j)
+              mma_f16(to, q_desc + static_cast<uint32_t>(c * (128 * 128 >> 4) + j * 2),
+                      kd + static_cast<uint32_t>(c * (kKeys * 128 >> 4) + j * 2), desc, c + j > 0);
+          mma_commit(&sh.s_full[n & 7]);
+          if (++stage == p.k_stages) stage = 0, turn_of ^= 1;
+          to = to + kKeys == tmem_o ? tmem : to + kKeys;
+        }
+        if (ok) mma_commit(&sh.q_empty);
+        if (!kStay) break;
       }
     }
     __syncwarp();
@@ -296,59 +384,47 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
       const uint64_t v_desc = operand_desc(p.shared ? k_ring : v_ring, kKeys * 128);
       const int stages = p.shared ? p.k_stages : p.v_stages, stage_bytes = p.shared ? p.k_bytes : p.v_bytes;
       uint64_t* full = p.shared ? sh.k_full : sh.v_full;
-      int stage = 0, turn_of = 0;
+      int stage = 0, turn_of = 0, n = 0;
       uint32_t from = tmem;
-      for (int i = 0; i < tiles; ++i) {
-        if (!wait_or_stop_one(&full[stage], turn_of, stop)) break;
-        fence_proxy_async_smem();
-        if (!wait_or_stop_one(&sh.p_full[i & 7], (i >> 3) & 1, stop)) break;
-        tc_fence_after();
-        const uint64_t vd = v_desc + static_cast<uint32_t>(stage * stage_bytes >> 4);
+      bool ok = true;
+      for (uint32_t w_at = blockIdx.x / cluster, nw = 0; w_at < p.works && ok; w_at += step_w, ++nw) {
+        if (nw > 0) ok = wait_or_stop_one(&sh.o_free, (nw - 1) & 1, stop);
+        for (int i = 0; i < tiles && ok; ++i, ++n) {
+          ok = wait_or_stop_one(&full[stage], turn_of, stop);
+          fence_proxy_async_smem();
+          ok = ok && wait_or_stop_one(&sh.p_full[n & 7], (n >> 3) & 1, stop);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = v_desc + static_cast<uint32_t>(stage * stage_bytes >> 4);
 #pragma unroll
-        for (int j = 0; j < kKeys / 16; ++j)
-          mma_f16_ts(tmem_o, from + j * 8, vd + static_cast<uint32_t>(j * (16 * 128 >> 4)), desc, i + j > 0);
-        mma_commit(&sh.pv_done[i & 7]);
-        if (++stage == stages) stage = 0, turn_of ^= 1;
-        from = from + kKeys == tmem_o ? tmem : from + kKeys;
+          for (int j = 0; j < kKeys / 16; ++j)
+            mma_f16_ts(tmem_o, from + j * 8, vd + static_cast<uint32_t>(j * (16 * 128 >> 4)), desc, i + j > 0);
+          mma_commit(&sh.pv_done[n & 7]);
+          if (++stage == stages) stage = 0, turn_of ^= 1;
+          from = from + kKeys == tmem_o ? tmem : from + kKeys;
+        }
+        if (!kStay) break;
       }
     }
     __syncwarp();
   } else {
     // ---- softmax ----
     const int copy = threadIdx.x / kRows;
-    {  // queries first: 8 threads per 128 bytes of a row
-      const int unit16 = threadIdx.x & 7, sub = threadIdx.x >> 3;
-      const E* q = static_cast<const E*>(a.q) + b * a.q_seq_stride + t * a.q_token_stride + head0 * a.q_head_stride;
-      for (int c = 0; c < p.d_blocks; ++c) {
-        const int d = c * 64 + unit16 * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = 16 * j + sub, h = r % kRows;
-          const bool real = h < heads && d < a.D;
-          const uint32_t at = c * (128 * 128) + swizzled(r, unit16);
-          const E* src = q + h * a.q_head_stride + d;
-          if (p.q_vector) {
-            copy16(base + at, real ? src : nowhere, real);
-          } else {
-            E v[8];
-            for (int e = 0; e < 8; ++e) v[e] = real ? src[e] : E(0.0f);
-            *reinterpret_cast<uint4*>(smem + at) = *reinterpret_cast<const uint4*>(v);
-          }
-        }
-      }
-      copy_arrive(&sh.q_full);
-      mbar_arrive(&sh.q_full);
-    }
+    if (tiles > 0) fetch_queries<E, COPIES>(p, k, smem, &sh.q_full, threadIdx.x);  // the first work's
     const int h = threadIdx.x % kRows;
-    const float slope = a.slopes != nullptr && h < heads ? a.slopes[head0 + h] * kLog2e : 0.0f;
     const float cap_in = a.softcap > 0.0f ? a.scale * 2.0f * kLog2e / a.softcap : 0.0f;
     const float cap_out = a.softcap * kLog2e, scale = a.scale * kLog2e;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
     uint32_t buf = 0;
+    int n = 0;  // tiles before this work
+    for (uint32_t w_at = blockIdx.x / cluster, nw = 0; w_at < p.works; w_at += step_w, ++nw, n += tiles) {
+    if (nw > 0) k = work_of(p, w_at);
+    top = __int_as_float(0xff800000), sum = 0.0f;
+    const float slope = a.slopes != nullptr && h < k.heads ? a.slopes[k.head0 + h] * kLog2e : 0.0f;
     for (int i = 0; i < tiles; ++i) {
-      const int mask = i % kMasks;
-      if (!wait_or_stop(&sh.masks[mask], (i / kMasks) & 1, stop)) break;
-      if (!wait_or_stop(&sh.s_full[i & 7], (i >> 3) & 1, stop)) break;
+      const int at = n + i, mask = at % kMasks;
+      if (!wait_or_stop(&sh.masks[mask], (at / kMasks) & 1, stop)) break;
+      if (!wait_or_stop(&sh.s_full[at & 7], (at >> 3) & 1, stop)) break;
       tc_fence_after();
       const uint32_t s_at = tmem + buf * kKeys + lanes;
       float z[kPart];
@@ -386,7 +462,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
         top = moved;
         sum *= factor;
         if (i > 0) {
-          if (!wait_or_stop(&sh.pv_done[(i - 1) & 7], ((i - 1) >> 3) & 1, stop)) break;
+          if (!wait_or_stop(&sh.pv_done[(at - 1) & 7], ((at - 1) >> 3) & 1, stop)) break;
           tc_fence_after();
           for (int c = 0; c < a.Dv; c += 16) {  // past Dv: columns that nothing reads, within the allocation
             uint32_t v[16];
@@ -422,24 +498,79 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&sh.p_full[i & 7]);
+      mbar_arrive(&sh.p_full[at & 7]);
       if (++buf == static_cast<uint32_t>(p.bufs)) buf = 0;
     }
-    if (tiles > 0) wait_or_stop(&sh.pv_done[(tiles - 1) & 7], ((tiles - 1) >> 3) & 1, stop);
+    if (tiles > 0) wait_or_stop(&sh.pv_done[(n + tiles - 1) & 7], ((n + tiles - 1) >> 3) & 1, stop);
     tc_fence_after();
     const bool failed = *stop != 0;  // a wait ran out: the rows become NaN
     sh.top[threadIdx.x] = failed ? 0.0f : top;
     sh.sum[threadIdx.x] = failed ? __int_as_float(0x7fc00000) : sum;
+    if (!kStay || cluster > 1) break;
+    if constexpr (kStay) {
+      // ---- end of a work: join the two copies, 16 columns at a time, and write ----
+      softmax_sync();
+      float all = sh.top[h], total = 0.0f;
+      if (COPIES == 2) all = fmaxf(all, sh.top[kRows % 128 + h]);
+#pragma unroll
+      for (int c = 0; c < COPIES; ++c) {
+        const float m = sh.top[c * kRows + h], l = sh.sum[c * kRows + h];
+        total += l != l ? l : is_low(m) ? 0.0f : l * exp2_fast(m - all);
+      }
+      if (copy == 0 && a.lse != nullptr && h < k.heads) a.lse[k.row * a.Hq + k.head0 + h] = logsum(all, total);
+      const float weight = total != total ? total : is_low(top) ? 0.0f : exp2_fast(top - all) * inverse(all, total);
+      E* out = static_cast<E*>(a.out) + (k.row * a.Hq + k.head0 + h) * a.Dv;
+      for (int c = 0; c < a.Dv; c += 16) {
+        uint32_t v[16] = {};
+        if (tiles > 0) {
+          tmem_ld(v, tmem_o + lanes + c);
+          tmem_wait_ld(v);
+          if (c + 16 >= a.Dv) {  // O is read: the next work may have it
+            tc_fence_before();
+            mbar_arrive(&sh.o_free);
+          }
+        }
+        float x[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(v[j]) * weight;
+        bool writes = true;
+        if (COPIES == 2) {  // the copies write every other 16 columns
+          writes = ((c >> 4) & 1) == copy;
+          if (!writes) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+              *reinterpret_cast<float4*>(&sh.part[h & 63][j]) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+          }
+          softmax_sync();
+          if (writes) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(&sh.part[h & 63][j]);
+              x[j] += y.x, x[j + 1] += y.y, x[j + 2] += y.z, x[j + 3] += y.w;
+            }
+          }
+          softmax_sync();
+        }
+        if (writes && h < k.heads) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 8)
+            if (c + j < a.Dv)
+              *reinterpret_cast<uint4*>(out + c + j) =
+                  make_uint4(Pack<E>::two(x[j], x[j + 1]), Pack<E>::two(x[j + 2], x[j + 3]),
+                             Pack<E>::two(x[j + 4], x[j + 5]), Pack<E>::two(x[j + 6], x[j + 7]));
+        }
+      }
+      softmax_sync();  // top and sum are read
+    }
+    }
   }
 
   // ---- join the copies ----
   // Every row of the buffer below is scaled to its head's maximum in this CTA.
   __syncthreads();
+  if (!kStay || cluster > 1) {
   const int pad = p.v_blocks * 64 + 4;  // floats per row: rows 4 banks apart
   float* rows = reinterpret_cast<float*>(smem);
-  // A row's factor, 1 / its sum of weights: zero where nothing is seen.
-  auto inverse = [](float all, float total) { return total != total ? total : is_low(all) ? 0.0f : 1.0f / total; };
-  auto logsum = [](float all, float total) { return total != total ? total : is_low(all) ? all : (all + log2f(total)) * kLn2; };
   if (warp < 4) {
     const int h = threadIdx.x % kRows;
     float all = sh.top[h], total = 0.0f;
@@ -453,7 +584,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
     if (threadIdx.x < kRows) {
       sh.head_top[h] = all;
       sh.head_sum[h] = cluster == 1 ? inverse(all, total) : total;
-      if (cluster == 1 && a.lse != nullptr && h < heads) a.lse[row * a.Hq + head0 + h] = logsum(all, total);
+      if (cluster == 1 && a.lse != nullptr && h < k.heads) a.lse[k.row * a.Hq + k.head0 + h] = logsum(all, total);
     }
     const float weight = is_low(top) ? 0.0f : exp2_fast(top - all);
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
@@ -480,8 +611,9 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   const int per_row = a.Dv / 8, at_once = 32 / per_row;
   const int sub_row = lane / per_row, c = (lane - sub_row * per_row) * 8;
   const int step = (kAttThreads / 32) * at_once;
+  const int heads = k.heads;
   const int row0 = sub_row < at_once ? warp * at_once + sub_row : heads;
-  E* out = static_cast<E*>(a.out) + (row * a.Hq + head0) * a.Dv;
+  E* out = static_cast<E*>(a.out) + (k.row * a.Hq + k.head0) * a.Dv;
   auto write = [&](int h, int c, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(out + static_cast<int64_t>(h) * a.Dv + c) =
         make_uint4(Pack<E>::two(x[0], x[1]), Pack<E>::two(x[2], x[3]), Pack<E>::two(x[4], x[5]), Pack<E>::two(x[6], x[7]));
@@ -493,8 +625,8 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
   for (int h = row0; h < heads; h += step) {
     float x[8] = {};
 #pragma unroll
-    for (int k = 0; k < COPIES; ++k) {
-      const float* from = rows + (k * kRows + h) * pad + c;
+    for (int q = 0; q < COPIES; ++q) {
+      const float* from = rows + (q * kRows + h) * pad + c;
       add(x, *reinterpret_cast<const float4*>(from), *reinterpret_cast<const float4*>(from + 4), 1.0f);
     }
     if (cluster == 1) {
@@ -546,9 +678,10 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 1 ? 1 : 2)
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] *= f;
       write(h, c, x);
-      if (c == 0 && a.lse != nullptr) a.lse[row * a.Hq + head0 + h] = logsum(all, total);
+      if (c == 0 && a.lse != nullptr) a.lse[k.row * a.Hq + k.head0 + h] = logsum(all, total);
     }
     cluster_sync();  // the others may still read this CTA's rows
+  }
   }
   if (warp == kMmaWarp) {
     tc_fence_after();
@@ -606,7 +739,7 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   const int whole = kMaxShared - static_cast<int>(sizeof(AttShared));
   const int half = kMaxShared / 2 - 1024 - static_cast<int>(sizeof(AttShared));
   const int least = p.shared ? 3 : 2;  // stages below which two CTAs gain nothing
-  const bool two = copies > 1 && p.tmem_cols == 256 && q_bytes + least * (p.k_bytes + p.v_bytes) <= half && join <= half;
+  const bool two = copies == 4 && p.tmem_cols == 256 && q_bytes + least * (p.k_bytes + p.v_bytes) <= half && join <= half;
   int room = ((two ? half : whole) - q_bytes);
   int stages = room / (p.k_bytes + p.v_bytes);
   if (stages > kMaxStages) stages = kMaxStages;
@@ -620,12 +753,15 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   p.shared_at = operands;
   const size_t bytes = static_cast<size_t>(operands) + sizeof(AttShared);
   const int64_t work = static_cast<int64_t>(a.B) * a.T * a.Hkv * p.m_tiles;
+  if (work > INT32_MAX) return TOPK_EINVAL;
+  p.works = static_cast<uint32_t>(work);
   // Few rows: share each over the CTAs that would idle, down to one tile each.
   const int64_t slots = static_cast<int64_t>(sm_count) * (two ? 2 : 1);
   const int tiles = (a.K + kKeys - 1) / kKeys;
   int cluster = 1;
   while (cluster < 8 && work * cluster * 2 <= slots && cluster * 2 <= tiles) cluster *= 2;
-  const int64_t grid = work * cluster;
+  // One or two copies: CTAs stay, one on each place.
+  const int64_t grid = copies <= 2 && cluster == 1 && work > slots ? slots : work * cluster;
   if (grid > INT32_MAX) return TOPK_EINVAL;
   if (copies == 4) return launch_copies<E, 4>(p, dev, cluster, grid, bytes, stream);
   if (copies == 2) return launch_copies<E, 2>(p, dev, cluster, grid, bytes, stream);

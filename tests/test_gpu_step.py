@@ -325,6 +325,25 @@ def test_attention(B, T, Hq, Hkv, D, Dv, K, S, ps, dtype, shared, sel):
     _check_attention(*_attention_case(B, T, Hq, Hkv, D, Dv, K, S, ps, dtype, shared=shared, sel=sel))
 
 
+@pytest.mark.parametrize("rows,Hq,Hkv,D,Dv,K,shared", [(340, 40, 1, 64, 64, 130, False), (340, 70, 1, 64, 48, 64, True),
+                                                       (170, 80, 2, 128, 64, 190, False), (500, 36, 1, 128, 128, 1, True),
+                                                       (400, 8, 1, 64, 64, 70, False)])
+def test_attention_many_rows_per_cta(rows, Hq, Hkv, D, Dv, K, shared):
+    """More rows than places for CTAs, odd numbers of tiles, empty rows between
+    full ones; cap, bias and masks change from row to row."""
+    S = 300
+    q, k, v, idx, table = _attention_case(1, rows, Hq, Hkv, D, Dv, K, S, 16, BF16, shared=shared, sel="holes")
+    idx[0, ::7] = -1
+    qpos = torch.randint(0, S, (1, rows), generator=_gen(9), device=DEV).to(torch.int32)
+    first = torch.randint(-5, S // 2, (1, rows), generator=_gen(10), device=DEV).to(torch.int32)
+    slopes = torch.rand(Hq, generator=_gen(11), device=DEV) * 0.05
+    got = _check_attention(q, k, v, idx, table, query_positions=qpos, softcap=20.0, slopes=slopes, first=first)
+    again = tk.sparse_attention(q, k, v, idx, table, query_positions=qpos, softcap=20.0, slopes=slopes, first=first,
+                                return_lse=True)
+    assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    _check_attention(q, k, v, idx[:, :, :0].contiguous(), table)
+
+
 @pytest.mark.parametrize("cap,biased,masked", [(30.0, False, False), (0.0, True, False), (5.0, True, True),
                                                (0.0, False, True)])
 @pytest.mark.parametrize("Hq,Hkv", [(12, 3), (96, 1)])
