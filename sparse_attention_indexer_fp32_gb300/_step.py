@@ -156,9 +156,9 @@ def _whole(t, name: str, shape, dtype, index: int) -> int:
 def _empty(shape, dtype, like, stream):
     """A result's memory, which belongs to the stream that the call runs on."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _span(address: int, shape, strides, size: int):

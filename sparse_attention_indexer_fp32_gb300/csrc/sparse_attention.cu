@@ -73,7 +73,7 @@ struct AttParams {
   int32_t k_stages, v_stages;  // of the rings; no second ring when shared
   int32_t k_bytes, v_bytes;    // of a stage
   int32_t k_at, v_at;          // the rings, after Q
-  int32_t shared_at;  // AttShared
+  int32_t shared_at, parts_at;  // AttShared, AttParts
   int32_t tmem_cols, bufs;
   bool q_vector;
 };
@@ -88,7 +88,6 @@ struct AttShared {
   // Nobody who waits on one lags behind by eight tiles.
   uint64_t s_full[8], p_full[8], pv_done[8];
   uint64_t q_empty, o_free;  // Q used up, O read: between one work and the next
-  alignas(16) float part[64][20];  // 16 columns of rows on their way from one copy to the other, padded
   uint32_t tmem;
   uint32_t stop;
 };
@@ -131,6 +130,12 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
   const uint4 v = ld_dsmem_v4(addr);
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
+
+// With two copies of the heads: 32 columns of rows on their way from one copy
+// to the other, padded.
+struct AttParts {
+  float part[2][64][36];
+};
 
 struct Work {
   int g, heads, head0;  // key head; real rows, and the first one's query head
@@ -508,7 +513,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
     sh.sum[threadIdx.x] = failed ? __int_as_float(0x7fc00000) : sum;
     if (!kStay || cluster > 1) break;
     if constexpr (kStay) {
-      // ---- end of a work: join the two copies, 16 columns at a time, and write ----
+      // ---- end of a work: join the two copies, 32 columns at a time, and write ----
       softmax_sync();
       float all = sh.top[h], total = 0.0f;
       if (COPIES == 2) all = fmaxf(all, sh.top[kRows % 128 + h]);
@@ -520,40 +525,40 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
       if (copy == 0 && a.lse != nullptr && h < k.heads) a.lse[k.row * a.Hq + k.head0 + h] = logsum(all, total);
       const float weight = total != total ? total : is_low(top) ? 0.0f : exp2_fast(top - all) * inverse(all, total);
       E* out = static_cast<E*>(a.out) + (k.row * a.Hq + k.head0 + h) * a.Dv;
-      for (int c = 0; c < a.Dv; c += 16) {
-        uint32_t v[16] = {};
+      for (int c = 0; c < a.Dv; c += 32) {  // past Dv: columns that nothing reads, within the allocation
+        uint32_t v[32] = {};
         if (tiles > 0) {
           tmem_ld(v, tmem_o + lanes + c);
           tmem_wait_ld(v);
-          if (c + 16 >= a.Dv) {  // O is read: the next work may have it
+          if (c + 32 >= a.Dv) {  // O is read: the next work may have it
             tc_fence_before();
             mbar_arrive(&sh.o_free);
           }
         }
-        float x[16];
+        float x[32];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(v[j]) * weight;
+        for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]) * weight;
         bool writes = true;
-        if (COPIES == 2) {  // the copies write every other 16 columns
-          writes = ((c >> 4) & 1) == copy;
+        if (COPIES == 2) {  // the copies write every other 32 columns, by way of two buffers
+          float(&part)[36] = reinterpret_cast<AttParts*>(smem + p.parts_at)->part[(c >> 5) & 1][h & 63];
+          writes = ((c >> 5) & 1) == copy;
           if (!writes) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4)
-              *reinterpret_cast<float4*>(&sh.part[h & 63][j]) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(&part[j]) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
           }
           softmax_sync();
           if (writes) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 y = *reinterpret_cast<const float4*>(&sh.part[h & 63][j]);
+            for (int j = 0; j < 32; j += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(&part[j]);
               x[j] += y.x, x[j + 1] += y.y, x[j + 2] += y.z, x[j + 3] += y.w;
             }
           }
-          softmax_sync();
         }
         if (writes && h < k.heads) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 8)
+          for (int j = 0; j < 32; j += 8)
             if (c + j < a.Dv)
               *reinterpret_cast<uint4*>(out + c + j) =
                   make_uint4(Pack<E>::two(x[j], x[j + 1]), Pack<E>::two(x[j + 2], x[j + 3]),
@@ -736,7 +741,8 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   p.tmem_cols = 2 * kKeys + p.v_blocks * 64 <= 256 ? 256 : 512;
   p.bufs = (p.tmem_cols - p.v_blocks * 64) / kKeys < kMaxBufs ? (p.tmem_cols - p.v_blocks * 64) / kKeys : kMaxBufs;
   const int join = 128 * (p.v_blocks * 64 + 4) * 4;
-  const int whole = kMaxShared - static_cast<int>(sizeof(AttShared));
+  const int parts = copies == 2 ? static_cast<int>(sizeof(AttParts)) : 0;
+  const int whole = kMaxShared - parts - static_cast<int>(sizeof(AttShared));
   const int half = kMaxShared / 2 - 1024 - static_cast<int>(sizeof(AttShared));
   const int least = p.shared ? 3 : 2;  // stages below which two CTAs gain nothing
   const bool two = copies == 4 && p.tmem_cols == 256 && q_bytes + least * (p.k_bytes + p.v_bytes) <= half && join <= half;
@@ -750,8 +756,9 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   p.v_at = q_bytes + p.k_stages * p.k_bytes;
   int operands = p.v_at + p.v_stages * p.v_bytes;
   if (operands < join) operands = (join + 15) / 16 * 16;
-  p.shared_at = operands;
-  const size_t bytes = static_cast<size_t>(operands) + sizeof(AttShared);
+  p.parts_at = operands;
+  p.shared_at = operands + parts;
+  const size_t bytes = static_cast<size_t>(operands) + parts + sizeof(AttShared);
   const int64_t work = static_cast<int64_t>(a.B) * a.T * a.Hkv * p.m_tiles;
   if (work > INT32_MAX) return TOPK_EINVAL;
   p.works = static_cast<uint32_t>(work);
