@@ -31,6 +31,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 
 #include "step_launch.cuh"
@@ -66,18 +67,19 @@ struct ScoreParams {
   CUtensorMap map, q_map;
 };
 
+// A work unit: sequence, first query token and their number, range of tiles.
+struct Unit {
+  int b, t0, tokens, tile0, tile1;
+};
+
 struct ScoreShared {
-  float weights[2][kMaxCols];
+  alignas(16) float weights[2][kMaxCols];  // read four at a time
   int32_t lengths[2][kMaxTokens];
   uint64_t full[6], q_full[2], q_empty[2];
   uint64_t t_full[8], t_empty[8];  // of tile k at k % 8: nobody who waits on one lags behind by eight tiles
+  Unit units[2];  // with the queries; no tiles: the end
   uint32_t tmem;
   uint32_t stop;
-};
-
-// What every role derives alike for a unit.
-struct Unit {
-  int b, t0, tokens, tile0, tile1;
 };
 
 __device__ __forceinline__ int length_of(const ScoreParams& p, int b, int t) {
@@ -162,7 +164,7 @@ __device__ __forceinline__ void fetch_queries(const ScoreParams& p, const Unit& 
           if (p.q_vector) {
             copy16(smem_addr(smem) + at, real ? src : nowhere, real);
           } else {
-            E v[16 / sizeof(E)];
+            alignas(16) E v[16 / sizeof(E)];
             for (int e = 0; e < static_cast<int>(16 / sizeof(E)); ++e) v[e] = real ? src[e] : E(0.0f);
             *reinterpret_cast<uint4*>(smem + at) = *reinterpret_cast<const uint4*>(v);
           }
@@ -174,6 +176,7 @@ __device__ __forceinline__ void fetch_queries(const ScoreParams& p, const Unit& 
   for (int t = 0; t < p.tokens; ++t)
     for (int h = th; h < p.hp; h += N) sh.weights[buf][t * p.hp + h] = t < r.tokens && h < p.a.H ? w[t * p.a.H + h] : 0.0f;
   if (th < kMaxTokens) sh.lengths[buf][th] = th < r.tokens ? length_of(p, r.b, r.t0 + th) : 0;
+  if (th == 0) sh.units[buf] = r;
   mbar_arrive(&sh.q_full[buf]);
 }
 
@@ -324,24 +327,30 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       fetch_queries<E, (kProductWarp - kFirst) * 32>(p, r, smem, q_bytes, sh, nu & 1, threadIdx.x - kFirst * 32, nowhere);
       ++nu;
     }
+    if (wait_or_stop(&sh.q_empty[nu & 1], ((nu >> 1) & 1) ^ 1, stop)) {  // the end
+      if (threadIdx.x == kFirst * 32) sh.units[nu & 1] = Unit{};
+      mbar_arrive(&sh.q_full[nu & 1]);
+      mbar_arrive(&sh.q_full[nu & 1]);
+      ++nu;
+    }
     queries_arrived(sh, nu);
   } else if (warp == kProductWarp) {
     // ---- products ----
     const uint32_t desc = mma_desc(Kind<E>::type, p.cols);
     const uint64_t ring_desc = operand_desc(ring_addr), q_desc = operand_desc(q_addr);
-    uint32_t k = 0, nu = 0, stage = 0, turn = 0;
+    uint32_t k = 0, stage = 0, turn = 0;
     bool ok = true;
-    for (uint32_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-      const Unit r = unit_of(p, u);
-      if (r.tile0 >= r.tile1) continue;
+    for (uint32_t nu = 0; ok; ++nu) {
       const uint32_t buf = nu & 1;
       ok = wait_or_stop(&sh.q_full[buf], (nu >> 1) & 1, stop);
-      ++nu;
+      if (!ok) break;
+      const Unit r = sh.units[buf];
+      if (r.tile0 >= r.tile1) break;
       if (!p.q_boxes) fence_proxy_async_smem();  // copies and stores are in; now the tensor cores may see them
       // one thread from here: its waits need no vote
       const int tiles = r.tile1 - r.tile0;
       bool done = true;
-      if (ok && elect_one()) {
+      if (elect_one()) {
         const uint64_t db = q_desc + (buf * q_bytes >> 4);
         uint32_t st = stage, tn = turn;
         for (int i = 0; i < tiles; ++i) {
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
         if (done) mma_commit(&sh.q_empty[buf]);
       }
       __syncwarp();
-      ok = ok && __all_sync(0xffffffffu, done);
+      ok = __all_sync(0xffffffffu, done);
       k += tiles;
       stage += tiles % STAGES;
       if (((tiles / STAGES) & 1) != 0) turn ^= 1;
@@ -387,15 +396,14 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
     const int group = warp >> 2, quarter = warp & 3;
     const int tile_step = 4 / p.share, turn_of = group / p.share, part = group % p.share;
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
-    uint32_t k = 0, nu = 0;
+    uint32_t k = 0;
     bool ok = true;
-    for (uint32_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-      const Unit r = unit_of(p, u);
-      if (r.tile0 >= r.tile1) continue;
+    for (uint32_t nu = 0; ok; ++nu) {
       const uint32_t buf = nu & 1;
       ok = wait_or_stop(&sh.q_full[buf], (nu >> 1) & 1, stop);
       if (!ok) break;
-      ++nu;
+      const Unit r = sh.units[buf];
+      if (r.tile0 >= r.tile1) break;
       const int t_first = r.tokens * part / p.share, t1 = r.tokens * (part + 1) / p.share;
       float* out = p.a.out + r.b * p.a.out_seq_stride + (r.t0 + t_first) * p.a.out_token_stride;
       const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
@@ -486,7 +494,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
 
 template <typename E, int STAGES, int HP, bool BOXES>
 topk_status launch_variant(const ScoreParams& p, int dev, int sm_count, cudaStream_t stream) {
-  static_assert(sizeof(ScoreShared) <= 3072, "barriers and weights");
+  static_assert(sizeof(ScoreShared) <= 3072 && offsetof(ScoreShared, weights) == 0, "behind the ring, aligned with it");
   const size_t bytes = 2 * static_cast<size_t>(p.cols) * 128 * p.blocks + STAGES * static_cast<size_t>(kTile) * 128 * p.blocks +
                        sizeof(ScoreShared);
   constexpr auto kernel = scores_kernel<E, STAGES, HP, BOXES>;

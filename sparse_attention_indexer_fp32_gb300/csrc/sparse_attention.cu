@@ -175,7 +175,7 @@ __device__ __forceinline__ void fetch_queries(const AttParams& p, const Work& k,
       if (p.q_vector) {
         copy16(smem_addr(smem) + at, real ? src : nowhere, real);
       } else {
-        E v[8];
+        alignas(16) E v[8];
         for (int e = 0; e < 8; ++e) v[e] = real ? src[e] : E(0.0f);
         *reinterpret_cast<uint4*>(smem + at) = *reinterpret_cast<const uint4*>(v);
       }
