@@ -301,7 +301,9 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
       }
       page = page_of(pos);
     }
-    const E* mine = static_cast<const E*>(values ? a.v : a.k) + k.g * head_stride + unit16 * 8;
+    // an empty cache has no address: nothing is read from the one it gets
+    const E* mine = some ? static_cast<const E*>(values ? a.v : a.k) + k.g * head_stride + unit16 * 8
+                         : reinterpret_cast<const E*>(reinterpret_cast<uintptr_t>(a.q) & ~static_cast<uintptr_t>(15));
     for (int i = i0; i < tiles; i += 2) {
       const int32_t pos2 = index_of(i + 4);
       const uint32_t page1 = page_of(pos1);

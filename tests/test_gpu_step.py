@@ -266,6 +266,8 @@ def test_scores_nothing_to_do():
     assert tk.indexer_scores(q, w, keys, n, table, width=0).shape == (1, 1, 0)
     empty = tk.indexer_scores(q, w, keys[:0], n, table)  # every page lies outside a cache of none
     assert torch.isneginf(empty).all()
+    none = torch.empty((0, 64, 64), dtype=BF16, device=DEV)  # and without an address
+    assert torch.isneginf(tk.indexer_scores(q, w, none, n, table)).all()
 
 
 # ---- attention ---------------------------------------------------------------------------------------
@@ -317,6 +319,7 @@ ATTENTION = [
     (1, 1, 8, 2, 128, 128, 2048, 3000, 64, BF16, False, "random"),
     (2, 1, 8, 1, 128, 128, 100, 60, 16, FP16, False, "random"),  # more slots than positions
     (1, 1, 6, 2, 256, 8, 40, 60, 16, BF16, False, "random"),
+    (1, 1, 40, 1, 256, 256, 130, 300, 64, FP16, False, "holes"),  # two copies, two stages
 ]
 
 
@@ -415,6 +418,8 @@ def test_attention_nothing_to_do():
     assert (out == 0).all() and torch.isneginf(lse).all()
     out, lse = tk.sparse_attention(q, k[:0], v[:0], idx, table, return_lse=True)
     assert (out == 0).all() and torch.isneginf(lse).all()
+    none = torch.empty((0, 16, 2, 64), dtype=BF16, device=DEV)
+    assert (tk.sparse_attention(q, none, none, idx, table) == 0).all()
     assert tk.sparse_attention(q[:0], k, v, idx[:0], table[:0]).shape == (0, 1, 4, 64)
 
 
