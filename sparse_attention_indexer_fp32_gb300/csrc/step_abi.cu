@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "sparse_step.h"
 #include "step_launch.cuh"
@@ -16,7 +17,33 @@ bool whole16(int64_t elements, int64_t size) { return (elements * size) % 16 == 
 
 int64_t size_of(int32_t type) { return type == SPARSE_FP32 ? 4 : type == SPARSE_E4M3 ? 1 : 2; }
 
-topk_status ready(int* dev, int* sm_count) { return tki::current_device(dev, sm_count); }
+constexpr int kMaxDevices = 64;
+
+struct Device {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+  bool supported = false;
+  int sm_count = 0;
+};
+Device g_devices[kMaxDevices];
+
+// The current device and its SM count, checked once per device for sm_103.
+topk_status ready(int* dev, int* sm_count) {
+  if (cudaGetDevice(dev) != cudaSuccess) return TOPK_ECUDA;
+  if (*dev < 0 || *dev >= kMaxDevices) return TOPK_EDEVICE;
+  Device& d = g_devices[*dev];
+  std::call_once(d.once, [&]() {
+    int major = 0, minor = 0;
+    d.err = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev);
+    if (d.err == cudaSuccess) d.err = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev);
+    if (d.err == cudaSuccess) d.err = cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, *dev);
+    d.supported = major == 10 && minor == 3;
+  });
+  if (d.err != cudaSuccess) return TOPK_ECUDA;
+  if (!d.supported) return TOPK_EDEVICE;
+  *sm_count = d.sm_count;
+  return TOPK_OK;
+}
 
 }  // namespace
 

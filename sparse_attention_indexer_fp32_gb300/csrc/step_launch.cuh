@@ -10,9 +10,6 @@
 
 namespace tki {
 
-// The current device's index and SM count; TOPK_EDEVICE unless it is sm_103.
-topk_status current_device(int* dev, int* sm_count);
-
 // Dynamic shared memory of one CTA that an SM grants.
 constexpr int kMaxShared = 227 * 1024;
 

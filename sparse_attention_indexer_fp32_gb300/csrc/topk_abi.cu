@@ -6,7 +6,6 @@
 #include <mutex>
 
 #include "topk_indexer.h"
-#include "step_launch.cuh"
 #include "topk_launch.cuh"
 
 namespace {
@@ -395,13 +394,6 @@ topk_status static_workspace(int dev, cudaStream_t stream, void** ptr) {
 }
 
 }  // namespace
-
-topk_status tki::current_device(int* dev, int* sm_count) {
-  DeviceInfo* info = nullptr;
-  const topk_status st = device_info(dev, &info);
-  if (st == TOPK_OK) *sm_count = info->sm_count;
-  return st;
-}
 
 extern "C" {
 
