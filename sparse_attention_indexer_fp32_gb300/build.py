@@ -20,8 +20,9 @@ BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(BUILD, "libtopk_indexer.so")
 SOURCES = (["topk_abi.cu"] + [f"topk_k{k}_{o}.cu" for k in (512, 1024, 2048) for o in ("ragged", "paged")]
-           + [f"topk_short_k{k}.cu" for k in (512, 1024, 2048)] + ["topk_blocks.cu", "step_abi.cu", "rotary.cu", "indexer_scores.cu",
-                                                                      "sparse_attention.cu"])
+           + [f"topk_short_k{k}.cu" for k in (512, 1024, 2048)] + ["topk_blocks.cu"]
+           + ["step_abi.cu", "rotary.cu", "sparse_attention.cu"]
+           + [f"indexer_scores_{t}.cu" for t in ("bf16", "fp16", "e4m3")])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

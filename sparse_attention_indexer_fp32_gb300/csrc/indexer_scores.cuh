@@ -4,7 +4,7 @@
 //   out[b, t, s] = ks[s] sum_h w[b, t, h] max(0, q[b, t, h] . k[s])
 //
 // The products run on the tensor cores with the keys as the rows: a tile of
-// 128 positions (TMEM lanes) by the heads of up to 8 query tokens (columns,
+// 128 positions (TMEM lanes) by the heads of up to 32 query tokens (columns,
 // 256 at most). So one thread of the epilogue holds all the products of one
 // position, and the sum over heads needs no exchange: a maximum and a
 // multiply-add per product (packed multiply-adds cost a move each, 4.6
@@ -26,6 +26,8 @@
 // as long as the products keep the tensor cores, and the two overlap only so far
 // with two TMEM buffers. e4m3, 32 sequences x 2 tokens x 32769, 40 us (20): one
 // tile is 16 KB and its fixed cost per warp shows.
+#pragma once
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -45,12 +47,12 @@ constexpr int kTile = 128;             // positions per tile: the rows of one pr
 constexpr int kEpilogueWarps = 16;
 constexpr int kFetchWarp = kEpilogueWarps, kProductWarp = kFetchWarp + 3;
 constexpr int kScoreThreads = (kProductWarp + 1) * 32;
-constexpr int kMaxTokens = 8;          // query tokens per group
+constexpr int kMaxTokens = 32;         // query tokens per group
 constexpr int kMaxCols = 256;
 
 struct ScoreParams {
   sparse_scores_args a;
-  int32_t hp;              // heads of a token, padded to 32, 64 or 128
+  int32_t hp;              // heads of a token, padded to 8, 16, 32, 64 or 128
   int32_t tokens;          // query tokens per group
   int32_t cols;            // tokens * hp
   int32_t blocks;          // 128-byte blocks per key: 1 or 2
@@ -413,7 +415,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       if (!ok) break;
       const Unit r = sh.units[buf];
       if (r.tile0 >= r.tile1) break;
-      const int t_first = r.tokens * part / p.share, t1 = r.tokens * (part + 1) / p.share;
+      constexpr int kPer = HP < 32 ? 32 / HP : 1;  // tokens in 32 columns, which are not split
+      const int packs = (r.tokens + kPer - 1) / kPer;
+      const int t_first = packs * part / p.share * kPer, t1 = min(packs * (part + 1) / p.share * kPer, r.tokens);
       float* out = p.a.out + r.b * p.a.out_seq_stride + (r.t0 + t_first) * p.a.out_token_stride;
       const int32_t* table = p.a.page_table + r.b * p.a.table_stride;
       const uint32_t end = min(static_cast<uint32_t>(r.tile1) * kTile, static_cast<uint32_t>(p.a.width));
@@ -434,8 +438,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
         ok = wait_or_stop(&sh.t_full[k & 7], (k >> 3) & 1, stop);
         if (!ok) break;
         tc_fence_after();
-        int left = (t1 - t_first) * (HP / 32);
-        if (left == 0) {
+        int left = HP < 32 ? (t1 - t_first + kPer - 1) / kPer : (t1 - t_first) * (HP / 32);  // times 32 columns
+        if (left <= 0) {
           mbar_arrive(&sh.t_empty[k & 7]);
           continue;
         }
@@ -464,15 +468,36 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
           acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
           ++length, o += p.a.out_token_stride;
         };
+        int tokens = t1 - t_first;
+        // 32 columns that hold several tokens
+        auto add_all = [&](const uint32_t (&v)[32], const float* w) {
+#pragma unroll
+          for (int g = 0; g < kPer; ++g) {
+            if (g >= tokens) break;
+#pragma unroll
+            for (int j = 0; j < 32 / kPer; j += 4) {
+              const int e = g * (32 / kPer) + j;
+              const float4 ww = *reinterpret_cast<const float4*>(w + e);
+              acc[0] = fmaf(ww.x, relu(v[e]), acc[0]);
+              acc[1] = fmaf(ww.y, relu(v[e + 1]), acc[1]);
+              acc[2] = fmaf(ww.z, relu(v[e + 2]), acc[2]);
+              acc[3] = fmaf(ww.w, relu(v[e + 3]), acc[3]);
+            }
+            finish();
+          }
+          tokens -= kPer;
+        };
         for (; left > 0; left -= 2, at += 64, wt += 64) {
           const bool both = HP > 32 || left > 1;
           tmem_ld(v0, at);
           if (both) tmem_ld(v1, at + 32);
           tmem_wait_ld();
           if (left <= 2) release();
-          add(v0, wt);
-          if (HP == 32) finish();
-          if (both) {
+          if constexpr (HP <= 32) {
+            add_all(v0, wt);
+            if (both) add_all(v1, wt + 32);
+          } else {
+            add(v0, wt);
             add(v1, wt + 32);
             if (HP < 128 || (left & 2) != 0) finish();
           }
@@ -529,17 +554,19 @@ topk_status launch_ring(const ScoreParams& p, int dev, int sm_count, cudaStream_
 }
 
 template <typename E>
-topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream) {
+topk_status launch_scores_of(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream) {
   ScoreParams p = {};
   p.a = a;
   const int size = sizeof(E);
-  p.hp = a.H <= 32 ? 32 : a.H <= 64 ? 64 : 128;
-  p.tokens = kMaxCols / p.hp < kMaxTokens ? kMaxCols / p.hp : kMaxTokens;
-  if (p.tokens > a.T) p.tokens = a.T;
+  p.hp = a.H <= 8 ? 8 : a.H <= 16 ? 16 : a.H <= 32 ? 32 : a.H <= 64 ? 64 : 128;
+  // Tokens per group: 256 columns of them at most, in whole 32 columns.
+  const int per = p.hp < 32 ? 32 / p.hp : 1;
+  p.tokens = kMaxCols / p.hp;
+  if (p.tokens > a.T) p.tokens = (a.T + per - 1) / per * per;
   p.cols = p.tokens * p.hp;
   p.blocks = (a.D * size + 127) / 128;
   p.row_units = a.D * size / 16;
-  p.share = p.tokens >= 2 ? 2 : 1;
+  p.share = p.tokens >= 2 * per ? 2 : 1;
   p.page_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (a.page_size == 1 << i) p.page_shift = i;
@@ -552,8 +579,8 @@ topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cud
   const int most = p.cols <= 128 ? 8 : 16;
   const int64_t tiles = (a.width + kTile - 1) / kTile;
   const int64_t all = tiles * a.B * p.groups;
-  int64_t per = (all + sm_count - 1) / sm_count;
-  p.unit_tiles = static_cast<int32_t>(per < most ? per : most);
+  const int64_t even = (all + sm_count - 1) / sm_count;
+  p.unit_tiles = static_cast<int32_t>(even < most ? even : most);
   p.chunks = static_cast<int32_t>((tiles + p.unit_tiles - 1) / p.unit_tiles);
   const int64_t units = static_cast<int64_t>(p.chunks) * p.groups * a.B;
   if (units > INT32_MAX) return TOPK_EINVAL;
@@ -573,19 +600,12 @@ topk_status launch_typed(const sparse_scores_args& a, int dev, int sm_count, cud
   const int64_t q_extents[4] = {a.D, a.H, a.T, a.B}, q_strides[3] = {a.q_head_stride, a.q_token_stride, a.q_seq_stride};
   const int q_box[3] = {p.hp, p.tokens, 1};
   p.q_boxes = box_map(&p.q_map, Kind<E>::map_type, size, a.q, 4, q_extents, q_strides, q_box);
+  if (p.hp == 8) return launch_ring<E, 8>(p, dev, sm_count, stream);
+  if (p.hp == 16) return launch_ring<E, 16>(p, dev, sm_count, stream);
   if (p.hp == 32) return launch_ring<E, 32>(p, dev, sm_count, stream);
   if (p.hp == 64) return launch_ring<E, 64>(p, dev, sm_count, stream);
   return launch_ring<E, 128>(p, dev, sm_count, stream);
 }
 
 }  // namespace
-
-topk_status launch_scores(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream) {
-  switch (a.type) {
-    case SPARSE_BF16: return launch_typed<__nv_bfloat16>(a, dev, sm_count, stream);
-    case SPARSE_FP16: return launch_typed<__half>(a, dev, sm_count, stream);
-    default: return launch_typed<__nv_fp8_e4m3>(a, dev, sm_count, stream);
-  }
-}
-
 }  // namespace tki

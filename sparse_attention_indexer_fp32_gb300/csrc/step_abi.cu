@@ -92,7 +92,12 @@ topk_status sparse_indexer_scores(const sparse_scores_args* args, topk_stream_t 
   int dev = 0, sms = 0;
   const topk_status st = ready(&dev, &sms);
   if (st != TOPK_OK) return st;
-  return tki::launch_scores(a, dev, sms, reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  switch (a.type) {
+    case SPARSE_BF16: return tki::launch_scores_bf16(a, dev, sms, cs);
+    case SPARSE_FP16: return tki::launch_scores_fp16(a, dev, sms, cs);
+    default: return tki::launch_scores_e4m3(a, dev, sms, cs);
+  }
 }
 
 topk_status sparse_attention(const sparse_attention_args* args, topk_stream_t stream) {

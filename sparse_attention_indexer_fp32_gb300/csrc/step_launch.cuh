@@ -25,7 +25,9 @@ topk_status allow_shared(int dev) {
 }
 
 topk_status launch_rotary(const sparse_rotary_args& a, int sm_count, cudaStream_t stream);
-topk_status launch_scores(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream);
+topk_status launch_scores_bf16(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream);
+topk_status launch_scores_fp16(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream);
+topk_status launch_scores_e4m3(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream);
 topk_status launch_attention(const sparse_attention_args& a, int dev, int sm_count, cudaStream_t stream);
 
 }  // namespace tki

@@ -179,6 +179,11 @@ SCORES = [
     (2, 9, 33, 96, 260, 64, FP16, [260] * 9 + list(range(120, 129))),
     (1, 130, 8, 64, 300, 32, E4M3, [(7 * i) % 301 for i in range(130)]),
     (1, 3, 96, 128, 2500, 64, BF16, [2500, 1300, 900]),
+    (1, 100, 1, 128, 200, 64, BF16, [(3 * i) % 201 for i in range(100)]),
+    (2, 45, 8, 64, 300, 64, FP16, [300 - i for i in range(90)]),
+    (1, 33, 3, 32, 140, 16, E4M3, [140 - i for i in range(33)]),
+    (2, 17, 16, 128, 260, 64, BF16, [260 - 2 * i for i in range(34)]),
+    (3, 2, 10, 64, 1300, 7, BF16, [1300, 1299, 5, 4, 700, 0]),
     (1, 2, 64, 128, 128 * 40 + 1, 128, FP16, [128 * 40 + 1, 128 * 40]),
 ]
 
@@ -189,7 +194,7 @@ def test_scores(B, T, H, D, width, ps, dtype, lengths):
 
 
 @pytest.mark.parametrize("B,T,H,D,ps,dtype", [(330, 1, 32, 64, 64, BF16), (120, 3, 64, 64, 16, FP16),
-                                              (330, 1, 16, 64, 7, BF16), (150, 2, 70, 128, 128, E4M3)])
+                                              (330, 1, 16, 64, 7, BF16), (40, 70, 2, 64, 64, BF16), (150, 2, 70, 128, 128, E4M3)])
 def test_scores_many_units_per_cta(B, T, H, D, ps, dtype):
     """Several work units of many tiles on every CTA, ragged, some empty."""
     width = 2300
