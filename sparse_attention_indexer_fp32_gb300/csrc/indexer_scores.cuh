@@ -19,9 +19,9 @@
 // warps sum over heads. Work units are (sequence, range of tiles, group of
 // query tokens).
 //
-// Measured: decode, 64 sequences of up to 65536 positions, 64 heads, bf16, 157
-// us, 6.3 TB/s (145 us for its bytes at the measured copy rate): HBM bound.
-// Prefill, 2048 tokens on 8192 positions, 170 to 180 us, 1.4 PFLOP/s (127 us at
+// Measured: decode, 64 sequences of up to 65536 positions, 64 heads, bf16, 154
+// us, 6.4 TB/s (145 us for its bytes at the measured copy rate): HBM bound.
+// Prefill, 2048 tokens on 8192 positions, 168 us, 1.4 PFLOP/s (127 us at
 // the measured matrix rate): the sums over heads keep the issue slots busy about
 // as long as the products keep the tensor cores, and the two overlap only so far
 // with two TMEM buffers. e4m3, 32 sequences x 2 tokens x 32769, 40 us (20): one

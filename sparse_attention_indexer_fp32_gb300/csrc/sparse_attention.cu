@@ -32,11 +32,11 @@
 // once to the type of v, the operand type of the second product, half a step
 // (2^-9 in bf16) relative to itself; the sum that divides adds the unrounded ones.
 //
-// Measured: 64 rows x 2048 entries x 8 key heads of 128, bf16, capped, 91 us,
-// 5.9 TB/s of random 256-byte reads (80 us for its bytes at the measured copy
-// rate). 2048 rows x 512 entries of 256 + 192 shared, 64 heads: 180 us; one CTA
-// an SM takes 8 tiles in 9 us and as long again to begin and end, which nothing
-// overlaps. Four rows x 512 entries: 10 us, one tile a CTA and one exchange.
+// Measured: 64 rows x 2048 entries x 8 key heads of 128, bf16, capped, 89 us,
+// 6.0 TB/s of random 256-byte reads (80 us for its bytes at the measured copy
+// rate). 2048 rows x 512 entries of 256 + 192 shared, 64 heads: 134 us (180
+// with a CTA for every row: half of its time began and ended it). Four rows x
+// 512 entries: 10 us, one tile a CTA and one exchange.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
