@@ -740,7 +740,7 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   const int q_bytes = 128 * 128 * p.d_blocks;
   p.k_bytes = kKeys * 128 * p.d_blocks;
   p.v_bytes = p.shared ? 0 : kKeys * 128 * p.v_blocks;
-  p.tmem_cols = 2 * kKeys + p.v_blocks * 64 <= 256 ? 256 : 512;
+  p.tmem_cols = copies == 4 && 2 * kKeys + p.v_blocks * 64 <= 256 ? 256 : 512;  // two CTAs or one on an SM
   p.bufs = (p.tmem_cols - p.v_blocks * 64) / kKeys < kMaxBufs ? (p.tmem_cols - p.v_blocks * 64) / kKeys : kMaxBufs;
   const int join = 128 * (p.v_blocks * 64 + 4) * 4;
   const int parts = copies == 2 ? static_cast<int>(sizeof(AttParts)) : 0;
@@ -760,7 +760,13 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   if (operands < join) operands = (join + 15) / 16 * 16;
   p.parts_at = operands;
   p.shared_at = operands + parts;
-  const size_t bytes = static_cast<size_t>(operands) + parts + sizeof(AttShared);
+  // CTAs of this kernel that share an SM must find their TMEM free: one that
+  // waited for it could hold up its cluster, and that the CTA it waits for. So
+  // those with all 512 columns take all of the shared memory, the others more
+  // than a third.
+  size_t bytes = static_cast<size_t>(operands) + parts + sizeof(AttShared);
+  const size_t floor_bytes = p.tmem_cols == 512 ? kMaxShared : 77 * 1024;
+  if (bytes < floor_bytes) bytes = floor_bytes;
   const int64_t work = static_cast<int64_t>(a.B) * a.T * a.Hkv * p.m_tiles;
   if (work > INT32_MAX) return TOPK_EINVAL;
   p.works = static_cast<uint32_t>(work);
