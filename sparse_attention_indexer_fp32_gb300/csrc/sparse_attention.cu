@@ -650,41 +650,32 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
   if (cluster > 1) {
     cluster_sync();
     const uint32_t top_addr = smem_addr(sh.head_top), sum_addr = smem_addr(sh.head_sum), rows_addr = smem_addr(rows);
-    // the CTAs take rows in turn; reads of all CTAs are in flight together
-    for (int h = row0 < heads ? row0 + static_cast<int>(rank) * step : heads; h < heads; h += cluster * step) {
+    // four outputs per thread, all reads of all CTAs in flight together
+    const int fours = a.Dv / 4, outputs = heads * fours;
+    for (int i = static_cast<int>(rank) * kAttThreads + threadIdx.x; i < outputs; i += cluster * kAttThreads) {
+      const int h = i / fours, c = (i - h * fours) * 4;
       float m[8], l[8], all = __int_as_float(0xff800000), total = 0.0f;
+      float4 u[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         const uint32_t from = r < cluster ? r : 0;
         m[r] = __uint_as_float(ld_dsmem_u32(map_rank(top_addr + 4 * h, from)));
         l[r] = __uint_as_float(ld_dsmem_u32(map_rank(sum_addr + 4 * h, from)));
+        u[r] = ld_dsmem_f4(map_rank(rows_addr + 4 * (h * pad + c), from));
       }
 #pragma unroll
       for (int r = 0; r < 8; ++r) all = fmaxf(all, m[r]);
+      float4 x = {};
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        m[r] = r >= cluster || is_low(m[r]) ? 0.0f : exp2_fast(m[r] - all);
-        total += r >= cluster ? 0.0f : l[r] != l[r] ? l[r] : l[r] * m[r];
-      }
-      float x[8] = {};
-#pragma unroll
-      for (int r0 = 0; r0 < 8; r0 += 4) {
-        if (r0 >= cluster) break;
-        float4 u[4], v[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t from = r0 + r < cluster ? r0 + r : 0;
-          u[r] = ld_dsmem_f4(map_rank(rows_addr + 4 * (h * pad + c), from));
-          v[r] = ld_dsmem_f4(map_rank(rows_addr + 4 * (h * pad + c) + 16, from));
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (r0 + r < cluster) add(x, u[r], v[r], m[r0 + r]);
+        if (r >= cluster) continue;
+        const float f = is_low(m[r]) ? 0.0f : exp2_fast(m[r] - all);
+        total += l[r] != l[r] ? l[r] : l[r] * f;
+        x.x += u[r].x * f, x.y += u[r].y * f, x.z += u[r].z * f, x.w += u[r].w * f;
       }
       const float f = inverse(all, total);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= f;
-      write(h, c, x);
+      *reinterpret_cast<uint2*>(out + static_cast<int64_t>(h) * a.Dv + c) =
+          make_uint2(Pack<E>::two(x.x * f, x.y * f), Pack<E>::two(x.z * f, x.w * f));
       if (c == 0 && a.lse != nullptr) a.lse[k.row * a.Hq + k.head0 + h] = logsum(all, total);
     }
     cluster_sync();  // the others may still read this CTA's rows
