@@ -53,6 +53,7 @@ constexpr int kMaxCols = 256;
 struct ScoreParams {
   sparse_scores_args a;
   int32_t hp;              // heads of a token, padded to 8, 16, 32, 64 or 128
+  int32_t hp_shift;        // its logarithm
   int32_t tokens;          // query tokens per group
   int32_t cols;            // tokens * hp
   int32_t blocks;          // 128-byte blocks per key: 1 or 2
@@ -175,8 +176,17 @@ __device__ __forceinline__ void fetch_queries(const ScoreParams& p, const Unit& 
     copy_arrive(&sh.q_full[buf]);
   }
   const float* w = p.a.weights + (static_cast<int64_t>(r.b) * p.a.T + r.t0) * p.a.H;
-  for (int t = 0; t < p.tokens; ++t)
-    for (int h = th; h < p.hp; h += N) sh.weights[buf][t * p.hp + h] = t < r.tokens && h < p.a.H ? w[t * p.a.H + h] : 0.0f;
+  for (int first = th; first < p.cols; first += 4 * N) {  // four reads in flight
+    float v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = first + u * N, t = i >> p.hp_shift, h = i & (p.hp - 1);
+      v[u] = t < r.tokens && h < p.a.H ? w[t * p.a.H + h] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (first + u * N < p.cols) sh.weights[buf][first + u * N] = v[u];
+  }
   if (th < kMaxTokens) sh.lengths[buf][th] = th < r.tokens ? length_of(p, r.b, r.t0 + th) : 0;
   if (th == 0) sh.units[buf] = r;
   mbar_arrive(&sh.q_full[buf]);
@@ -559,6 +569,7 @@ topk_status launch_scores_of(const sparse_scores_args& a, int dev, int sm_count,
   p.a = a;
   const int size = sizeof(E);
   p.hp = a.H <= 8 ? 8 : a.H <= 16 ? 16 : a.H <= 32 ? 32 : a.H <= 64 ? 64 : 128;
+  p.hp_shift = p.hp == 8 ? 3 : p.hp == 16 ? 4 : p.hp == 32 ? 5 : p.hp == 64 ? 6 : 7;
   // Tokens per group: 256 columns of them at most, in whole 32 columns.
   const int per = p.hp < 32 ? 32 / p.hp : 1;
   p.tokens = kMaxCols / p.hp;
