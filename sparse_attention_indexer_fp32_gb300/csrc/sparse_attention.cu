@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
     const float slope = a.slopes != nullptr && h < k.heads ? a.slopes[k.head0 + h] * kLog2e : 0.0f;
     for (int i = 0; i < tiles; ++i) {
       const int at = n + i, mask = at % kMasks;
-      if (!wait_or_stop(&sh.masks[mask], (at / kMasks) & 1, stop)) break;
+      wait_or_stop_one(&sh.masks[mask], (at / kMasks) & 1, stop);  // giving up shows in `stop`
       if (!wait_or_stop(&sh.s_full[at & 7], (at >> 3) & 1, stop)) break;
       tc_fence_after();
       const uint32_t s_at = tmem + buf * kKeys + lanes;
