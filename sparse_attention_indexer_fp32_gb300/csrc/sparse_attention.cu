@@ -36,7 +36,7 @@
 // 6.0 TB/s of random 256-byte reads (80 us for its bytes at the measured copy
 // rate). 2048 rows x 512 entries of 256 + 192 shared, 64 heads: 134 us (180
 // with a CTA for every row: half of its time began and ended it). Four rows x
-// 512 entries: 9.3 us, one tile a CTA and one exchange.
+// 512 entries: 8.7 us, two tiles a CTA and one exchange.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -724,6 +724,8 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
              a.k_head_stride == a.v_head_stride;
   p.q_vector = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_seq_stride % 8 == 0 && a.q_token_stride % 8 == 0 &&
                a.q_head_stride % 8 == 0;
+  // As many copies as the heads leave room for: 64 rows x 2048 entries with 8
+  // heads a key head take 94 us with 4 copies, 106 with 2, 137 with 1.
   const int copies = p.heads <= 32 ? 4 : p.heads <= 64 ? 2 : 1;
   // Shared memory: Q, then the ring; at the end the same bytes hold the rows
   // to be joined. Two CTAs share an SM where two stages each fit (and TMEM
@@ -761,12 +763,16 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   const int64_t work = static_cast<int64_t>(a.B) * a.T * a.Hkv * p.m_tiles;
   if (work > INT32_MAX) return TOPK_EINVAL;
   p.works = static_cast<uint32_t>(work);
-  // Few rows: share each over the CTAs that would idle, down to one tile each.
+  // Few rows: share each over the CTAs that would idle, down to two tiles each
+  // (one row x 2048 entries, one key head: 26.8 us on one CTA, 18.6, 14.4 and
+  // 12.4 on 2, 4 and 8; 16 key-head rows x 512: 8.7 us at two tiles a CTA, 9.5
+  // at one).
   const int64_t slots = static_cast<int64_t>(sm_count) * (two ? 2 : 1);
   const int tiles = (a.K + kKeys - 1) / kKeys;
   int cluster = 1;
-  while (cluster < 8 && work * cluster * 2 <= slots && cluster * 2 <= tiles) cluster *= 2;
-  // One or two copies: CTAs stay, one on each place.
+  while (cluster < 8 && work * cluster * 2 <= slots && cluster * 4 <= tiles) cluster *= 2;
+  // One or two copies: CTAs stay, one on each place (2048 rows x 512 entries:
+  // 137 us, 168 with a CTA a row).
   const int64_t grid = copies <= 2 && cluster == 1 && work > slots ? slots : work * cluster;
   if (grid > INT32_MAX) return TOPK_EINVAL;
   if (copies == 4) return launch_copies<E, 4>(p, dev, cluster, grid, bytes, stream);
