@@ -729,7 +729,8 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   const int copies = p.heads <= 32 ? 4 : p.heads <= 64 ? 2 : 1;
   // Shared memory: Q, then the ring; at the end the same bytes hold the rows
   // to be joined. Two CTAs share an SM where two stages each fit (and TMEM
-  // holds both), else one CTA has as many stages as fit.
+  // holds both), else one CTA has as many stages as fit (64 rows x 2048 entries
+  // x 8 key heads: 94 us with two, 111 with one).
   const int q_bytes = 128 * 128 * p.d_blocks;
   p.k_bytes = kKeys * 128 * p.d_blocks;
   p.v_bytes = p.shared ? 0 : kKeys * 128 * p.v_blocks;
