@@ -117,7 +117,7 @@ topk_status sparse_indexer_scores(const sparse_scores_args* args, topk_stream_t 
  * sparse_attention - for every row (b, t) and query head h, over the
  * positions p_j = indices[b, t, j] that are seen:
  *     z_j = scale * q[b, t, h] . k[p_j, g],  g = h / (Hq / Hkv)
- *     z_j = softcap * tanh(z_j / softcap)                  (softcap > 0)
+ *     z_j = softcap * tanh(z_j / softcap)                  (softcap > 0: any, its error is relative to z_j)
  *     z_j = z_j + slopes[h] * (p_j - query_positions[b, t]) (slopes given)
  *     lse = log sum_j exp(z_j),  out = sum_j exp(z_j - lse) * v[p_j, g]
  * Position p_j is seen when it is not negative, its page id lies in the

@@ -368,6 +368,8 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
     scale = D ** -0.5 if scale is None else float(scale)
     if not math.isfinite(scale) or not math.isfinite(softcap) or softcap < 0.0:
         raise ValueError("scale and softcap must be finite, softcap not negative")
+    if 0.0 < softcap < 2.0 ** -149:
+        raise ValueError("softcap must be 0 or a positive float32")
     at_q, at_k, at_v = q.data_ptr(), k.data_ptr(), v.data_ptr()
     if out is None:
         out = _empty((B, T, Hq, Dv), dtype, q, stream)

@@ -41,6 +41,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "step_launch.cuh"
@@ -75,6 +76,8 @@ struct AttParams {
   int32_t k_at, v_at;          // the rings, after Q
   int32_t shared_at, parts_at;  // AttShared, AttParts
   int32_t tmem_cols, bufs;
+  float scale_log2e;                // of a product, to a logit in units of log 2
+  float scale_over_cap, cap_log2e;  // with a cap
   bool q_vector;
 };
 
@@ -117,11 +120,23 @@ __device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp
   return y;
 }
 
-// c tanh(x / c) = c - 2 c / (1 + e^(2 x / c)), good to a few 2^-24 of c.
-__device__ __forceinline__ float capped(float x, float cap, float two_log2e_over_cap) {
+// A capped logit c tanh(z / c), z = x scale, in units of log 2, good to 4 2^-23 of
+// itself whatever the cap. With u = z / c: c (1 - 2 / (1 + e^2u)) from |u| = kBent on;
+// below, where that difference cancels (its error is one of c, however small z is),
+// z (1 + u^2 P(u^2)), P a fit of (tanh(u) / u - 1) / u^2 to 0.4 2^-24 of the result.
+constexpr float kBent = 0.65f;
+__device__ __forceinline__ float capped_low(float x, float scale_log2e, float scale_over_cap) {
+  const float u = x * scale_over_cap, u2 = u * u;
+  float p = fmaf(-5.9329807e-3f, u2, 2.0881320e-2f);
+  p = fmaf(p, u2, -5.3825848e-2f);
+  p = fmaf(p, u2, 1.3332601e-1f);
+  p = fmaf(p, u2, -3.3333328e-1f);
+  return x * scale_log2e * fmaf(p, u2, 1.0f);
+}
+__device__ __forceinline__ float capped_high(float x, float scale_over_cap, float cap_log2e) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_fast(x * two_log2e_over_cap)));
-  return cap - 2.0f * cap * r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_fast(x * scale_over_cap * (2.0f * kLog2e))));
+  return cap_log2e * fmaf(-2.0f, r, 1.0f);
 }
 
 __device__ __forceinline__ bool is_low(float x) { return x == __int_as_float(0xff800000); }
@@ -419,8 +434,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
     const int copy = threadIdx.x / kRows;
     if (tiles > 0) fetch_queries<E, COPIES>(p, k, smem, &sh.q_full, threadIdx.x);  // the first work's
     const int h = threadIdx.x % kRows;
-    const float cap_in = a.softcap > 0.0f ? a.scale * 2.0f * kLog2e / a.softcap : 0.0f;
-    const float cap_out = a.softcap * kLog2e, scale = a.scale * kLog2e;
+    const float scale = p.scale_log2e;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
     uint32_t buf = 0;
     int n = 0;  // tiles before this work
@@ -444,8 +458,20 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
         const uint32_t bits = (sh.seen[mask][e0 / 32] >> (e0 % 32)) & (kStep == 32 ? 0xffffffffu : 0xffffu);
         tmem_wait_ld(v);
         if (a.softcap > 0.0f) {
+          // the second form only where a row of the warp needs it: logits are mostly far below their cap
+          float most = 0.0f;
 #pragma unroll
-          for (int j = 0; j < kStep; ++j) z[c + j] = capped(__uint_as_float(v[j]), cap_out, cap_in);
+          for (int j = 0; j < kStep; ++j) {
+            most = fmaxf(most, fabsf(__uint_as_float(v[j])));
+            z[c + j] = capped_low(__uint_as_float(v[j]), scale, p.scale_over_cap);
+          }
+          if (__any_sync(0xffffffffu, most * fabsf(p.scale_over_cap) >= kBent)) {
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) {
+              const float x = __uint_as_float(v[j]);
+              if (!(fabsf(x * p.scale_over_cap) < kBent)) z[c + j] = capped_high(x, p.scale_over_cap, p.cap_log2e);
+            }
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < kStep; ++j) z[c + j] = __uint_as_float(v[j]) * scale;
@@ -707,12 +733,23 @@ topk_status launch_copies(const AttParams& p, int dev, int cluster, int64_t grid
   return err == cudaSuccess ? TOPK_OK : TOPK_ECUDA;
 }
 
+// In FP32, the largest number where it has none: a product of zero stays zero.
+float finite(double x) {
+  const double most = FLT_MAX;
+  return static_cast<float>(x > most ? most : x < -most ? -most : x);
+}
+
 template <typename E>
 topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, cudaStream_t stream) {
   AttParams p = {};
   p.a = a;
   p.heads = a.Hq / a.Hkv;
   p.m_tiles = (p.heads + 127) / 128;
+  p.scale_log2e = finite(static_cast<double>(a.scale) * kLog2e);
+  if (a.softcap > 0.0f) {
+    p.scale_over_cap = finite(static_cast<double>(a.scale) / a.softcap);
+    p.cap_log2e = finite(static_cast<double>(a.softcap) * kLog2e);
+  }
   p.page_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (a.page_size == 1 << i) p.page_shift = i;

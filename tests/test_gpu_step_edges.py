@@ -1,0 +1,86 @@
+"""The operators around the selection at the edges of what they accept, against their formulas in 64 bits."""
+
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import step_reference as R  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU-only machines
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import sparse_attention_indexer_fp32_gb300 as tk  # noqa: E402
+
+DEV = torch.device("cuda:0")
+BF16, FP16, FP32, E4M3 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(shape, seed, dtype=FP32, scale=1.0):
+    return (torch.randn(shape, generator=_gen(seed), device=DEV) * scale).to(dtype)
+
+
+def _ints(values):
+    return torch.tensor(values, dtype=torch.int32, device=DEV)
+
+
+# ---- attention: the cap ------------------------------------------------------------------------------
+
+
+def _capped(q, k, v, scale, cap):
+    """(out, its bound, lse, its bound) of one row over all entries, [H, D] and [n, D]. A logit is off by
+    its product's sum and its own rounding, and by 8 U of its capped value, whatever the cap; the rest as in
+    step_reference.attention."""
+    hs, U = R.half_step(v.dtype), R.U
+    tiny = torch.finfo(v.dtype).tiny * torch.finfo(v.dtype).eps
+    q, k, v = R.np64(q), R.np64(k), R.np64(v)
+    cap = float(np.float32(cap))
+    x = q @ k.T * scale
+    z = cap * np.tanh(x / cap)
+    slope = 1.0 - np.tanh(x / cap) ** 2
+    dz = slope * ((q.shape[1] + 4) * U * abs(scale) * (np.abs(q) @ np.abs(k).T) + 4 * U * np.abs(x)) + 8 * U * np.abs(z)
+    top = z.max(axis=1, keepdims=True)
+    e = np.exp(z - top)
+    total = e.sum(axis=1, keepdims=True)
+    p = e / total
+    dz = dz + 4 * U * np.abs(z - top) + 8 * U
+    mean_dz = (p * dz).sum(axis=1) + (len(k) + 8) * U
+    out = p @ v
+    err = ((p * (hs + dz + mean_dz[:, None])) @ np.abs(v)) * 1.01 + tiny * np.abs(v).sum(axis=0) / total \
+        + hs * np.abs(out) * 1.01 + tiny
+    lse = (np.log(total) + top)[:, 0]
+    return out, err, lse, mean_dz + 4 * U * (np.abs(top[:, 0]) + np.abs(lse))
+
+
+@pytest.mark.parametrize("cap", [1e-40, 1e-30, 1e-3, 0.7, 5.0, 50.0, 1e4, 1e6, 1e8, 1e30, 3.4e38])
+@pytest.mark.parametrize("heads", [6, 40, 80])
+def test_attention_caps_of_any_size(cap, heads):
+    """The cap's error goes with the logit, not with the cap: far above the logits it changes nothing."""
+    n, D, ps = 150, 64, 16
+    pages = -(-n // ps)
+    q = _randn((1, 1, heads, D), 1, BF16, 2.0)
+    k, v = (_randn((pages, ps, 1, D), s, BF16) for s in (2, 3))
+    k[0, 3] = 0.0  # a logit of exactly 0
+    idx = torch.arange(n, dtype=torch.int32, device=DEV).view(1, 1, n)
+    out, lse = tk.sparse_attention(q, k, v, idx, softcap=cap, scale=0.25, return_lse=True)
+    want = _capped(q[0, 0], k.view(-1, D)[:n], v.view(-1, D)[:n], 0.25, cap)
+    R.assert_near(out[0, 0], want[0], want[1], "out")
+    R.assert_near(lse[0, 0], want[2], want[3], "lse")
+
+
+def test_attention_cap_under_the_smallest_number():
+    """A positive cap that FP32 cannot hold is refused, not taken for no cap."""
+    q = _randn((1, 1, 2, 64), 1, BF16)
+    k = _randn((4, 16, 1, 64), 2, BF16)
+    with pytest.raises(ValueError, match="softcap"):
+        tk.sparse_attention(q, k, k, _ints([[[0, 1]]]), softcap=1e-60)
