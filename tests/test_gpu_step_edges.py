@@ -84,3 +84,30 @@ def test_attention_cap_under_the_smallest_number():
     k = _randn((4, 16, 1, 64), 2, BF16)
     with pytest.raises(ValueError, match="softcap"):
         tk.sparse_attention(q, k, k, _ints([[[0, 1]]]), softcap=1e-60)
+
+
+# ---- indexer scores: infinite keys -------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("H", [1, 3, 8, 10, 16, 24, 32, 33, 48, 64, 65, 100, 128])
+@pytest.mark.parametrize("T,ps,dtype", [(1, 64, BF16), (5, 7, FP16)])
+def test_scores_of_infinite_keys(H, T, ps, dtype):
+    """The formula's own infinities and zeros, whatever the number of heads."""
+    width, D = 150, 64
+    pages = -(-width // ps)
+    keys = _randn((pages, ps, D), 1, dtype)
+    q = _randn((1, T, H, D), 2, dtype)
+    q[..., 3] = q[..., 3].abs() + 0.1
+    w = _randn((1, T, H), 3).abs() + 0.1
+    flat = keys.view(-1, D)
+    flat[5, 3] = math.inf     # every product +inf
+    flat[70, 3] = -math.inf   # every product -inf: nothing is added
+    flat[140, 3], flat[140, 4] = math.inf, math.nan
+    n = torch.full((1, T), width, dtype=torch.int32, device=DEV)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    got = tk.indexer_scores(q, w, keys, n, table, width=width)
+    assert (got[..., 5] == math.inf).all() and (got[..., 70] == 0.0).all() and torch.isnan(got[..., 140]).all()
+    assert (tk.indexer_scores(q, -w, keys, n, table, width=width)[..., 5] == -math.inf).all()
+    want, bound = R.scores(q, w, keys, n, table, None, width)
+    keep = [s for s in range(width) if s not in (5, 70, 140)]
+    R.assert_near(got[..., keep], want[..., keep], bound[..., keep])
