@@ -2,7 +2,9 @@
 
 As in ``_binding``: tensors are checked here, the rest by the library; every
 step runs in its CUDA kernels, on the stream given or the current one, and
-there is no CPU fallback.
+there is no CPU fallback. The calls record no gradient: tensors that require one
+are refused while gradients are recorded, and an ``out`` of the caller's counts as
+changed in place.
 """
 
 from __future__ import annotations
@@ -102,6 +104,18 @@ class _Call:
 
 _rotary, _scores, _attention = (_Call("sparse_rotary", _RotaryArgs), _Call("sparse_indexer_scores", _ScoresArgs),
                                 _Call("sparse_attention", _AttentionArgs))
+
+
+def _serves(name: str, *tensors) -> None:
+    """These calls record no backward pass, so they take nothing that would need one."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if getattr(t, "requires_grad", False):
+                raise ValueError(f"{name} records no gradient: detach its tensors, or call it under torch.no_grad()")
+
+
+# Tells autograd that the caller's tensor has changed, as an in-place operation of torch does.
+_written = torch.autograd.graph.increment_version
 
 
 def _dims(t, name: str, dims: int) -> None:
@@ -235,6 +249,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
     of the call with the same arguments. ``out`` may be ``x`` (in place). With ``slots`` (int32
     ``[T]``), ``out`` is a paged cache ``[pages, page_size, H, D]`` and token ``t`` is written at slot
     ``slots[t]`` (negative or past the cache: not written). Returns ``out``."""
+    _serves("rotary", x, frequencies, out)
     shape, xs, code, index = _main(x, "x", 3, _ROTARY_TYPES)
     T, H, D = shape
     dtype = x.dtype
@@ -247,7 +262,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
     if not math.isfinite(scale):
         raise ValueError("scale must be finite")
     to, pages, page_size, page_stride = 0, 0, 0, 0
-    address = x.data_ptr()
+    address, given = x.data_ptr(), out is not None
     if slots is not None:
         if out is None:
             raise ValueError("slots need the cache as out")
@@ -272,6 +287,8 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
                 raise ValueError("out must be x itself or not overlap it")
     _rotary(index, stream, address, xs[0], xs[1], target, page_stride, ot[-3], ot[-2], pos, freq, to, pages, page_size,
             T, H, D, 2 * pairs, int(offset), _LAYOUTS[layout], code, wide, bool(inverse), scale)
+    if given:
+        _written(out)
     return out
 
 
@@ -290,6 +307,7 @@ def indexer_scores(q: torch.Tensor, weights: torch.Tensor, keys: torch.Tensor, l
     ``page_table`` int32 ``[B, n]`` (rows may be a broadcast). ``out`` float32 ``[B, T, width]``
     (default width: ``n * page_size``); ``out.view(B * T, width)`` is what :func:`topk_ragged`
     takes."""
+    _serves("indexer_scores", q, weights, keys, key_scales, out)
     shape, qs, code, index = _main(q, "q", 4, _SCORES_TYPES)
     B, T, H, D = shape
     w = _whole(weights, "weights", (B, T, H), _FP32, index)
@@ -301,6 +319,7 @@ def indexer_scores(q: torch.Tensor, weights: torch.Tensor, keys: torch.Tensor, l
     ps, pt = _other(page_table, "page_table", 2, _I32, index)
     if ps[0] != B:
         raise ValueError("page_table must have one row for each sequence")
+    given = out is not None
     scales = 0 if key_scales is None else _whole(key_scales, "key_scales", (pages, page_size), _FP32, index)
     if out is None:
         width = ps[1] * page_size if width is None else int(width)
@@ -316,6 +335,8 @@ def indexer_scores(q: torch.Tensor, weights: torch.Tensor, keys: torch.Tensor, l
         raise ValueError("page_table is too narrow for the width of out")
     _scores(index, stream, q.data_ptr(), qs[0], qs[1], qs[2], w, keys.data_ptr(), kt[0], kt[1], scales, n,
             page_table.data_ptr(), pt[0], ps[1], out.data_ptr(), ot[0], ot[1], pages, width, page_size, B, T, H, D, code)
+    if given:
+        _written(out)
     return out
 
 
@@ -339,6 +360,7 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
     int32 ``[B, T]`` earlier ones (a document's start). Returns ``out`` ``[B, T, Hq, Dv]``, with
     ``return_lse`` also the logarithm of the softmax's sum, float32 ``[B, T, Hq]``; a row that sees
     nothing has 0 and ``-inf``."""
+    _serves("sparse_attention", q, k, v, slopes, out)
     shape, qs, code, index = _main(q, "q", 4, _ATTENTION_TYPES)
     B, T, Hq, D = shape
     dtype = q.dtype
@@ -370,6 +392,7 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
         raise ValueError("scale and softcap must be finite, softcap not negative")
     if 0.0 < softcap < 2.0 ** -149:
         raise ValueError("softcap must be 0 or a positive float32")
+    given = out is not None
     at_q, at_k, at_v = q.data_ptr(), k.data_ptr(), v.data_ptr()
     if out is None:
         out = _empty((B, T, Hq, Dv), dtype, q, stream)
@@ -384,4 +407,6 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
     _attention(index, stream, at_q, qs[0], qs[1], qs[2], at_k, kt[0], kt[1], kt[2], at_v, vt[0], vt[1], vt[2], idx, table,
                pt, width, qp, begin, bias, target, 0 if lse is None else lse.data_ptr(), pages, page_size, B, T, Hq, Hkv,
                D, Dv, K, code, scale, softcap)
+    if given:
+        _written(out)
     return (out, lse) if return_lse else out

@@ -111,3 +111,53 @@ def test_scores_of_infinite_keys(H, T, ps, dtype):
     want, bound = R.scores(q, w, keys, n, table, None, width)
     keep = [s for s in range(width) if s not in (5, 70, 140)]
     R.assert_near(got[..., keep], want[..., keep], bound[..., keep])
+
+
+# ---- autograd -----------------------------------------------------------------------------------------
+
+
+def test_nothing_that_needs_a_gradient_is_taken():
+    """Where gradients are recorded the calls refuse what would need one; without, they run."""
+    f, pos = tk.rotary_frequencies(64, device=DEV), _ints([1, 2])
+    x, w = _randn((2, 4, 64), 1, BF16), _randn((2, 1, 4), 3)
+    k = _randn((4, 16, 1, 64), 2, BF16)
+    idx, table, n = _ints([[[0, 5, 9]], [[1, 2, 3]]]), _ints([[0, 1], [2, 3]]), _ints([[20], [32]])
+    slopes, qpos = torch.zeros(4, device=DEV), _ints([[9], [9]])
+
+    def leaf(t):
+        return t.clone().requires_grad_()
+
+    calls = [lambda: tk.rotary(leaf(x), pos, f), lambda: tk.rotary(x, pos, f, out=leaf(x)),
+             lambda: tk.indexer_scores(leaf(x[:, None]), w, k[:, :, 0], n, table),
+             lambda: tk.indexer_scores(x[:, None], leaf(w), k[:, :, 0], n, table),
+             lambda: tk.indexer_scores(x[:, None], w, leaf(k[:, :, 0]), n, table),
+             lambda: tk.sparse_attention(leaf(x[:, None]), k, k, idx, table),
+             lambda: tk.sparse_attention(x[:, None], leaf(k), k, idx, table),
+             lambda: tk.sparse_attention(x[:, None], k, leaf(k), idx, table),
+             lambda: tk.sparse_attention(x[:, None], k, k, idx, table, slopes=leaf(slopes), query_positions=qpos)]
+    for call in calls:
+        with pytest.raises(ValueError, match="no gradient"):
+            call()
+        with torch.no_grad():
+            call()
+
+
+def test_a_tensor_written_in_place_is_known_to_have_changed():
+    """A backward pass that needs what `out` held before is refused by autograd, not run on the new values."""
+    f, pos = tk.rotary_frequencies(64, device=DEV), _ints([1, 2])
+    x, k = _randn((2, 4, 64), 1, BF16), _randn((4, 16, 1, 64), 2, BF16)
+    w, scores = _randn((2, 1, 4), 3), torch.zeros((2, 1, 32), device=DEV)
+    idx, table, n = _ints([[[0, 5, 9]], [[1, 2, 3]]]), _ints([[0, 1], [2, 3]]), _ints([[20], [32]])
+    out = torch.zeros((2, 1, 4, 64), dtype=BF16, device=DEV)
+    for target, call in ((x, lambda: tk.rotary(x, pos, f, out=x)),
+                         (k, lambda: tk.rotary(x[:, :1], pos, f, out=k, slots=_ints([3, 4]))),
+                         (scores, lambda: tk.indexer_scores(x[:, None], w, k[:, :, 0], n, table, out=scores)),
+                         (out, lambda: tk.sparse_attention(x[:, None], k, k, idx, table, out=out))):
+        weight = torch.ones_like(target, requires_grad=True)
+        loss = (target * weight).sum()
+        call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():  # whose tensors have no version
+        y = x.clone()
+        assert torch.equal(tk.rotary(y, pos, f, out=y), tk.rotary(x, pos, f))
