@@ -106,12 +106,10 @@ _rotary, _scores, _attention = (_Call("sparse_rotary", _RotaryArgs), _Call("spar
                                 _Call("sparse_attention", _AttentionArgs))
 
 
-def _serves(name: str, *tensors) -> None:
-    """These calls record no backward pass, so they take nothing that would need one."""
+def _no_gradient(name: str) -> None:
+    """The calls record no backward pass, so they take nothing that would need one."""
     if torch.is_grad_enabled():
-        for t in tensors:
-            if getattr(t, "requires_grad", False):
-                raise ValueError(f"{name} records no gradient: detach its tensors, or call it under torch.no_grad()")
+        raise ValueError(f"{name} requires a gradient, and the call records none: detach it, or call under torch.no_grad()")
 
 
 # Tells autograd that the caller's tensor has changed, as an in-place operation of torch does.
@@ -126,6 +124,8 @@ def _main(t, name: str, dims: int, types):
     """Shape, strides, type code and device of a call's main tensor."""
     try:
         shape, strides, index, code = t.shape, t.stride(), t.get_device(), types.get(t.dtype)
+        if t.requires_grad:
+            _no_gradient(name)
     except AttributeError:
         _dims(t, name, dims)
     if len(shape) != dims:
@@ -143,6 +143,8 @@ def _other(t, name: str, dims: int, dtype, index: int):
     """Shape and strides of a further tensor of this type on that device."""
     try:
         shape, strides = t.shape, t.stride()
+        if t.requires_grad:
+            _no_gradient(name)
     except AttributeError:
         _dims(t, name, dims)
     if len(shape) != dims:
@@ -160,6 +162,8 @@ def _whole(t, name: str, shape, dtype, index: int) -> int:
     """The address of a contiguous tensor of exactly this shape and type."""
     try:
         if t.dtype == dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            if t.requires_grad:
+                _no_gradient(name)
             return t.data_ptr()
     except AttributeError:
         pass
@@ -249,7 +253,6 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
     of the call with the same arguments. ``out`` may be ``x`` (in place). With ``slots`` (int32
     ``[T]``), ``out`` is a paged cache ``[pages, page_size, H, D]`` and token ``t`` is written at slot
     ``slots[t]`` (negative or past the cache: not written). Returns ``out``."""
-    _serves("rotary", x, frequencies, out)
     shape, xs, code, index = _main(x, "x", 3, _ROTARY_TYPES)
     T, H, D = shape
     dtype = x.dtype
@@ -307,7 +310,6 @@ def indexer_scores(q: torch.Tensor, weights: torch.Tensor, keys: torch.Tensor, l
     ``page_table`` int32 ``[B, n]`` (rows may be a broadcast). ``out`` float32 ``[B, T, width]``
     (default width: ``n * page_size``); ``out.view(B * T, width)`` is what :func:`topk_ragged`
     takes."""
-    _serves("indexer_scores", q, weights, keys, key_scales, out)
     shape, qs, code, index = _main(q, "q", 4, _SCORES_TYPES)
     B, T, H, D = shape
     w = _whole(weights, "weights", (B, T, H), _FP32, index)
@@ -360,7 +362,6 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
     int32 ``[B, T]`` earlier ones (a document's start). Returns ``out`` ``[B, T, Hq, Dv]``, with
     ``return_lse`` also the logarithm of the softmax's sum, float32 ``[B, T, Hq]``; a row that sees
     nothing has 0 and ``-inf``."""
-    _serves("sparse_attention", q, k, v, slopes, out)
     shape, qs, code, index = _main(q, "q", 4, _ATTENTION_TYPES)
     B, T, Hq, D = shape
     dtype = q.dtype
