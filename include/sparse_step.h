@@ -58,8 +58,9 @@ typedef enum sparse_rotary_layout {
  *     u' = scale * (u cos a_i - v sin a_i),  v' = scale * (v cos a_i + u sin a_i)
  * and the rest of the head copied. `inverse` turns by -a_i, which with the
  * same scale is the gradient of the call. The angle is exact modulo whole
- * turns up to the rounding of frequencies[i] / 2 pi to 2^-64 turns, so
- * positions of the whole 32-bit range are as accurate as small ones.
+ * turns up to the rounding of frequencies[i] / 2 pi to 2^-63 turns, times the
+ * position (2^-32 turns at the end of the 32-bit range), and 2^-32 turns of its
+ * own: positions of that whole range are as accurate as small ones.
  *
  * out may be x itself with the same strides (in place; only the rotated part
  * is then touched); it must not overlap x in any other way. With `slots`, out
@@ -73,7 +74,7 @@ typedef struct sparse_rotary_args {
   void* out;                 /* as x, or the cache when slots != NULL */
   int64_t out_page_stride;   /* used with slots */
   int64_t out_token_stride, out_head_stride;
-  const void* positions;     /* [T] int32, or int64 when positions_64 (low 32 bits used modulo 2^64) */
+  const void* positions;     /* [T] int32, or int64 when positions_64 */
   const double* frequencies; /* [rotated / 2], |f| < 2^40 */
   const int32_t* slots;      /* [T] or NULL */
   int64_t num_pages;         /* with slots */

@@ -4,8 +4,8 @@
 // f_i / 2 pi turns; only the fraction of a turn counts. So the rate is held as
 // a fixed-point fraction of a turn in 64 bits and multiplied by the position
 // in integer arithmetic modulo 2^64: whole turns drop out by themselves and
-// the fraction is exact up to the rate's rounding (2^-64 turns) times the
-// position, 2^-33 turns at position 2^31, where a product in FP32 would be
+// the fraction is exact up to the rate's rounding (2^-63 turns) times the
+// position, 2^-32 turns at position 2^31, where a product in FP32 would be
 // off by whole turns. Its top 32 bits go to the trigonometric functions as FP32.
 //
 // The work. Memory bound: each element is read and written once, with three
@@ -52,26 +52,29 @@ struct RotParams {
   float scale, sign;
 };
 
-// f / 2 pi as a fraction of a turn, times 2^64, modulo 2^64. The mantissa m of
-// f = m 2^(e - 1075) is multiplied by round(2^66 / 2 pi) into 117 bits and
-// shifted.
+// f / 2 pi as a fraction of a turn, times 2^64, modulo 2^64, to 2 of its last
+// places. The mantissa m of f = m 2^(e - 1075) is multiplied by 2^66 / 2 pi and
+// shifted. The constant's next word adds less than 2^53 before the shift: under
+// one last place for |f| < 4, counted from there on.
 __device__ __forceinline__ uint64_t turns_of(double f) {
   const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
   const int e = static_cast<int>((bits >> 52) & 0x7ff);
   if (e == 0) return 0;  // zero, or under 2^-1022
   const uint64_t m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
-  const uint64_t c = 0xa2f9836e4e44152aull;
+  const uint64_t c = 0xa2f9836e4e441529ull, c_next = 0xfc2757d1f534ddc0ull;
   const uint64_t lo = m * c, hi = __umul64hi(m, c);
   const int shift = 1077 - e;
   uint64_t t;
-  if (shift <= 0)
-    t = 0;  // 2^54 radians a position and more: outside the contract
-  else if (shift < 64)
-    t = (lo >> shift) | (hi << (64 - shift));
-  else if (shift < 128)
-    t = hi >> (shift - 64);
-  else
+  if (shift >= 128)
     t = 0;
+  else if (shift >= 64)
+    t = hi >> (shift - 64);
+  else if (shift >= 53)
+    t = (lo >> shift) | (hi << (64 - shift));
+  else if (shift > 0)
+    t = ((lo >> shift) | (hi << (64 - shift))) + (__umul64hi(m, c_next) >> shift);
+  else
+    t = 0;  // 2^54 radians a position and more: outside the contract
   return (bits >> 63) ? 0ull - t : t;
 }
 

@@ -1,6 +1,7 @@
 """The operators around the selection at the edges of what they accept, against their formulas in 64 bits."""
 
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -113,6 +114,26 @@ def test_scores_of_infinite_keys(H, T, ps, dtype):
     R.assert_near(got[..., keep], want[..., keep], bound[..., keep])
 
 
+# ---- rotary: rates ------------------------------------------------------------------------------------
+
+TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+def test_rotary_fast_rates_at_far_positions():
+    """Rates up to the limit of 2^40 radians a position, at both ends of 32 bits: the angle is that of the
+    exact product. 2^-32 turns of the fraction, 2 ulp of the functions and three roundings: 16 U."""
+    rates = [1.0, 0.1, 12345.678, 3.0e5, -(2.0 ** 30) * 1.1, 2.0 ** 35 + 0.37, 1.3 * 2.0 ** 39, 2.0 ** -30]
+    pos = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 12345, 77, -1]
+    x = _randn((len(pos), 3, 2 * len(rates)), 1)
+    f = torch.tensor(rates, dtype=torch.float64, device=DEV)
+    got = R.np64(tk.rotary(x, _ints(pos), f))
+    angle = np.array([[float((Fraction(r) * p / TWO_PI) % 1) for r in rates] for p in pos]) * 2 * math.pi
+    c, s = np.cos(angle)[:, None], np.sin(angle)[:, None]
+    u, v = np.split(R.np64(x), 2, axis=-1)
+    want = np.concatenate([u * c - v * s, v * c + u * s], axis=-1)
+    R.assert_near(got, want, np.tile(16 * R.U * np.hypot(u, v), 2))
+
+
 # ---- autograd -----------------------------------------------------------------------------------------
 
 
@@ -136,7 +157,7 @@ def test_nothing_that_needs_a_gradient_is_taken():
              lambda: tk.sparse_attention(x[:, None], k, leaf(k), idx, table),
              lambda: tk.sparse_attention(x[:, None], k, k, idx, table, slopes=leaf(slopes), query_positions=qpos)]
     for call in calls:
-        with pytest.raises(ValueError, match="no gradient"):
+        with pytest.raises(ValueError, match="requires a gradient"):
             call()
         with torch.no_grad():
             call()
