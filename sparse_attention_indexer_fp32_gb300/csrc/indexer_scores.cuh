@@ -574,8 +574,7 @@ topk_status launch_variant(const ScoreParams& p, int dev, int sm_count, cudaStre
   const topk_status st = allow_shared<kernel>(dev);
   if (st != TOPK_OK) return st;
   const unsigned grid = p.units < static_cast<unsigned>(sm_count) ? p.units : static_cast<unsigned>(sm_count);
-  kernel<<<grid, kScoreThreads, bytes, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TOPK_OK : TOPK_ECUDA;
+  return launch(kernel, p, dim3(grid), kScoreThreads, bytes, stream);
 }
 
 template <typename E, int STAGES, int HP>

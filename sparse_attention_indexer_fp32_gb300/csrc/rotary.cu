@@ -254,13 +254,9 @@ topk_status launch_typed(const sparse_rotary_args& a, int sm_count, cudaStream_t
   const int64_t grid = (static_cast<int64_t>(a.T) + p.tokens - 1) / p.tokens * p.head_chunks;
   if (grid > INT32_MAX) return TOPK_EINVAL;
   const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>((p.items + kRotThreads - 1) / kRotThreads));
-  if (vec)
-    half ? rotary_kernel<E, V, true><<<g, kRotThreads, 0, stream>>>(p)
-         : rotary_kernel<E, V, false><<<g, kRotThreads, 0, stream>>>(p);
-  else
-    half ? rotary_kernel<E, 2, true><<<g, kRotThreads, 0, stream>>>(p)
-         : rotary_kernel<E, 2, false><<<g, kRotThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TOPK_OK : TOPK_ECUDA;
+  const auto kernel = vec ? (half ? rotary_kernel<E, V, true> : rotary_kernel<E, V, false>)
+                          : (half ? rotary_kernel<E, 2, true> : rotary_kernel<E, 2, false>);
+  return launch(kernel, p, g, kRotThreads, 0, stream);
 }
 
 }  // namespace

@@ -729,8 +729,7 @@ topk_status launch_copies(const AttParams& p, int dev, int cluster, int64_t grid
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, p, cluster);
-  return err == cudaSuccess ? TOPK_OK : TOPK_ECUDA;
+  return status_of(cudaLaunchKernelEx(&cfg, kernel, p, cluster));
 }
 
 // In FP32, the largest number where it has none: a product of zero stays zero.

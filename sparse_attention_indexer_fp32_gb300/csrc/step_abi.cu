@@ -29,7 +29,8 @@ Device g_devices[kMaxDevices];
 
 // The current device and its SM count, checked once per device for sm_103.
 topk_status ready(int* dev, int* sm_count) {
-  if (cudaGetDevice(dev) != cudaSuccess) return TOPK_ECUDA;
+  const topk_status st = tki::status_of(cudaGetDevice(dev));
+  if (st != TOPK_OK) return st;
   if (*dev < 0 || *dev >= kMaxDevices) return TOPK_EDEVICE;
   Device& d = g_devices[*dev];
   std::call_once(d.once, [&]() {
@@ -39,7 +40,7 @@ topk_status ready(int* dev, int* sm_count) {
     if (d.err == cudaSuccess) d.err = cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, *dev);
     d.supported = major == 10 && minor == 3;
   });
-  if (d.err != cudaSuccess) return TOPK_ECUDA;
+  if (d.err != cudaSuccess) return tki::status_of(d.err);
   if (!d.supported) return TOPK_EDEVICE;
   *sm_count = d.sm_count;
   return TOPK_OK;

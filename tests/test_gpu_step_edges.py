@@ -1,5 +1,6 @@
 """The operators around the selection at the edges of what they accept, against their formulas in 64 bits."""
 
+import ctypes
 import math
 from fractions import Fraction
 
@@ -132,6 +133,49 @@ def test_rotary_fast_rates_at_far_positions():
     u, v = np.split(R.np64(x), 2, axis=-1)
     want = np.concatenate([u * c - v * s, v * c + u * s], axis=-1)
     R.assert_near(got, want, np.tile(16 * R.U * np.hypot(u, v), 2))
+
+
+# ---- errors left behind -------------------------------------------------------------------------------
+
+
+def test_an_earlier_failure_is_not_reported_again():
+    """A call whose launch is refused (the legacy stream while another stream that waits for it is being captured)
+    reports it, and the next calls, whose launches go through, do not."""
+    cuda = ctypes.CDLL("libcuda.so.1")
+    f, pos = tk.rotary_frequencies(64, device=DEV), _ints([1, 2])
+    x = _randn((2, 4, 64), 1, BF16)
+    k = _randn((4, 16, 1, 64), 2, BF16)
+    idx, table, n = _ints([[[0, 5, 9]], [[1, 2, 3]]]), _ints([[0, 1], [2, 3]]), _ints([[20], [32]])
+    w = _randn((2, 1, 4), 3)
+    bufs = torch.empty_like(x), torch.empty((2, 1, 32), device=DEV), torch.empty((2, 1, 4, 64), dtype=BF16, device=DEV)
+
+    def rotary():
+        return tk.rotary(x, pos, f, out=bufs[0])
+
+    def scores():
+        return tk.indexer_scores(x[:, None], w, k[:, :, 0], n, table, out=bufs[1])
+
+    def attention():
+        return tk.sparse_attention(x[:, None], k, k, idx, table, out=bufs[2])
+
+    for call in (rotary, scores, attention):
+        call()
+    torch.cuda.synchronize()
+    for failing in (rotary, scores, attention):
+        stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+        assert cuda.cuStreamCreate(ctypes.byref(stream), 0) == 0
+        try:
+            assert cuda.cuStreamBeginCapture_v2(stream, 0) == 0
+            try:
+                with pytest.raises(tk.TopkError):
+                    failing()
+            finally:
+                cuda.cuStreamEndCapture(stream, ctypes.byref(graph))
+        finally:
+            assert cuda.cuStreamDestroy_v2(stream) == 0
+        for call in (rotary, scores, attention):
+            call()
+        torch.cuda.synchronize()
 
 
 # ---- autograd -----------------------------------------------------------------------------------------
