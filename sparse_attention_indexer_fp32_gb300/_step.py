@@ -284,7 +284,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
     else:
         target = out.data_ptr()
         _no_broadcast(os, ot, "out")
-        if slots is not None or target != address or ot != xs:
+        if slots is not None or target != address or any(n > 1 and u != v for n, u, v in zip(shape, xs, ot)):
             size = 4 if code == 2 else 2
             if _overlap(_span(address, shape, xs, size), _span(target, os, ot, size)):
                 raise ValueError("out must be x itself or not overlap it")

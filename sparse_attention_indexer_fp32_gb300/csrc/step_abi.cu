@@ -17,6 +17,13 @@ bool whole16(int64_t elements, int64_t size) { return (elements * size) % 16 == 
 
 int64_t size_of(int32_t type) { return type == SPARSE_FP32 ? 4 : type == SPARSE_E4M3 ? 1 : 2; }
 
+// The stride of a dimension of one element, which nothing is reached by, is 0
+// from here on, whatever the caller's: no rule on strides counts it.
+template <typename... S>
+void unused(int64_t extent, S&... strides) {
+  if (extent == 1) ((strides = 0), ...);
+}
+
 constexpr int kMaxDevices = 64;
 
 struct Device {
@@ -52,7 +59,7 @@ extern "C" {
 
 topk_status sparse_rotary(const sparse_rotary_args* args, topk_stream_t stream) {
   if (args == nullptr) return TOPK_EINVAL;
-  const sparse_rotary_args& a = *args;
+  sparse_rotary_args a = *args;
   if (a.T < 0 || a.H < 0 || a.D < 1 || a.D > SPARSE_ROTARY_MAX_D) return TOPK_EINVAL;
   if (a.rotated < 2 || a.rotated % 2 != 0 || a.offset < 0 || a.offset > a.D - a.rotated) return TOPK_EINVAL;
   if (a.type != SPARSE_BF16 && a.type != SPARSE_FP16 && a.type != SPARSE_FP32) return TOPK_EINVAL;
@@ -62,6 +69,14 @@ topk_status sparse_rotary(const sparse_rotary_args* args, topk_stream_t stream) 
   if (a.T == 0 || a.H == 0 || (a.slots != nullptr && (a.num_pages == 0 || a.page_size == 0))) return TOPK_OK;
   if (a.slots != nullptr && a.num_pages > INT64_MAX / a.page_size) return TOPK_EINVAL;
   if (a.x == nullptr || a.out == nullptr || a.positions == nullptr || a.frequencies == nullptr) return TOPK_EINVAL;
+  if (a.slots == nullptr) {
+    unused(a.T, a.x_token_stride, a.out_token_stride);
+  } else {
+    unused(a.T, a.x_token_stride);
+    unused(a.page_size, a.out_token_stride);
+    unused(a.num_pages, a.out_page_stride);
+  }
+  unused(a.H, a.x_head_stride, a.out_head_stride);
   const uintptr_t size = static_cast<uintptr_t>(size_of(a.type));
   if (!aligned(a.x, size) || !aligned(a.out, size) || !aligned(a.positions, a.positions_64 ? 8 : 4) ||
       !aligned(a.frequencies, 8) || !aligned(a.slots, 4))
@@ -74,7 +89,7 @@ topk_status sparse_rotary(const sparse_rotary_args* args, topk_stream_t stream) 
 
 topk_status sparse_indexer_scores(const sparse_scores_args* args, topk_stream_t stream) {
   if (args == nullptr) return TOPK_EINVAL;
-  const sparse_scores_args& a = *args;
+  sparse_scores_args a = *args;
   if (a.type != SPARSE_BF16 && a.type != SPARSE_FP16 && a.type != SPARSE_E4M3) return TOPK_EINVAL;
   const int64_t size = size_of(a.type);
   if (a.B < 0 || a.T < 0 || a.H < 1 || a.H > SPARSE_SCORES_MAX_H) return TOPK_EINVAL;
@@ -86,6 +101,11 @@ topk_status sparse_indexer_scores(const sparse_scores_args* args, topk_stream_t 
   if (a.q == nullptr || a.weights == nullptr || a.lengths == nullptr || a.page_table == nullptr || a.out == nullptr ||
       (a.keys == nullptr && a.num_pages > 0))
     return TOPK_EINVAL;
+  unused(a.B, a.q_seq_stride, a.table_stride, a.out_seq_stride);
+  unused(a.T, a.q_token_stride, a.out_token_stride);
+  unused(a.H, a.q_head_stride);
+  unused(a.num_pages, a.key_page_stride);
+  unused(a.page_size, a.key_token_stride);
   if (!aligned(a.keys, 16) || !whole16(a.key_page_stride, size) || !whole16(a.key_token_stride, size)) return TOPK_EINVAL;
   if (!aligned(a.q, static_cast<uintptr_t>(size)) || !aligned(a.weights, 4) || !aligned(a.key_scales, 4) ||
       !aligned(a.lengths, 4) || !aligned(a.page_table, 4) || !aligned(a.out, 4))
@@ -103,7 +123,7 @@ topk_status sparse_indexer_scores(const sparse_scores_args* args, topk_stream_t 
 
 topk_status sparse_attention(const sparse_attention_args* args, topk_stream_t stream) {
   if (args == nullptr) return TOPK_EINVAL;
-  const sparse_attention_args& a = *args;
+  sparse_attention_args a = *args;
   if (a.type != SPARSE_BF16 && a.type != SPARSE_FP16) return TOPK_EINVAL;
   if (a.B < 0 || a.T < 0 || a.Hkv < 1 || a.Hq < 0 || a.Hq % a.Hkv != 0 || a.K < 0) return TOPK_EINVAL;
   if (a.D < 8 || a.D > SPARSE_ATTENTION_MAX_D || a.D % 8 != 0) return TOPK_EINVAL;
@@ -119,6 +139,12 @@ topk_status sparse_attention(const sparse_attention_args* args, topk_stream_t st
   if (a.q == nullptr || a.out == nullptr || (a.K > 0 && a.indices == nullptr) ||
       (entries && (a.k == nullptr || a.v == nullptr)))
     return TOPK_EINVAL;
+  unused(a.B, a.q_seq_stride, a.table_stride);
+  unused(a.T, a.q_token_stride);
+  unused(a.Hq, a.q_head_stride);
+  unused(a.num_pages, a.k_page_stride, a.v_page_stride);
+  unused(a.page_size, a.k_token_stride, a.v_token_stride);
+  unused(a.Hkv, a.k_head_stride, a.v_head_stride);
   if (!aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.out, 16) || !aligned(a.q, 2)) return TOPK_EINVAL;
   for (const int64_t s : {a.k_page_stride, a.k_token_stride, a.k_head_stride, a.v_page_stride, a.v_token_stride,
                           a.v_head_stride})

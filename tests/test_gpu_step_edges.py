@@ -178,6 +178,31 @@ def test_an_earlier_failure_is_not_reported_again():
         torch.cuda.synchronize()
 
 
+# ---- dimensions of one ---------------------------------------------------------------------------------
+
+
+def test_strides_of_single_elements_do_not_matter():
+    """A stride that no element is reached by may be anything."""
+    D, ps, n = 64, 32, 20
+    q = _randn((1, 1, 6, D), 1, BF16)
+    k = _randn((1, ps, 1, D), 2, BF16)
+    odd = k.as_strided(k.shape, (3, D, 5, 1))
+    idx, table, length = torch.arange(n, dtype=torch.int32, device=DEV).view(1, 1, n), _ints([[0]]), _ints([[n]])
+    assert torch.equal(tk.sparse_attention(q, odd, odd, idx, table), tk.sparse_attention(q, k, k, idx, table))
+    w = _randn((1, 1, 6), 3)
+    want = tk.indexer_scores(q, w, k[:, :, 0], length, table)
+    assert torch.equal(tk.indexer_scores(q, w, odd[:, :, 0], length, table)[..., :n], want[..., :n])
+    single = k[:, :1].as_strided((1, 1, 1, D), (3, 7, 5, 1))  # pages of one entry
+    assert torch.equal(tk.sparse_attention(q, single, single, idx[..., :1].contiguous(), table),
+                       tk.sparse_attention(q, k[:, :1], k[:, :1], idx[..., :1].contiguous(), table))
+    f, pos = tk.rotary_frequencies(D, device=DEV), _ints([7])
+    x = _randn((1, 3, D), 4, BF16)
+    want = tk.rotary(x, pos, f)
+    strange = x.as_strided(x.shape, (1, D, 1))
+    assert torch.equal(tk.rotary(strange, pos, f), want)
+    assert tk.rotary(strange, pos, f, out=x) is x and torch.equal(x, want)  # in place through another view of it
+
+
 # ---- autograd -----------------------------------------------------------------------------------------
 
 
