@@ -47,6 +47,7 @@ typedef enum sparse_rotary_layout {
 } sparse_rotary_layout;
 
 #define SPARSE_ROTARY_MAX_D 1024
+#define SPARSE_ROTARY_MAX_H (1 << 30)
 #define SPARSE_SCORES_MAX_D 128
 #define SPARSE_SCORES_MAX_H 128
 #define SPARSE_ATTENTION_MAX_D 256

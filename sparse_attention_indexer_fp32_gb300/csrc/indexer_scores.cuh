@@ -610,14 +610,15 @@ topk_status launch_scores_of(const sparse_scores_args& a, int dev, int sm_count,
   for (int i = 0; i < 31; ++i)
     if (a.page_size == 1 << i) p.page_shift = i;
   p.pages = a.num_pages < INT32_MAX ? static_cast<uint32_t>(a.num_pages) : INT32_MAX;
-  p.groups = (a.T + p.tokens - 1) / p.tokens;
+  p.groups = a.T / p.tokens + (a.T % p.tokens != 0);
   // Work units of at most 16 tiles, 8 where a tile is short work: enough of
   // them to even out the SMs, long enough to hide the next unit's queries
   // (64 x 65536, 64 columns: 156 us by 8, 160 by 16; 2048 x 8192, 256
   // columns: 193 by 16, 195 by 8); fewer while SMs would idle.
   const int most = p.cols <= 128 ? 8 : 16;
   const int64_t tiles = (a.width + kTile - 1) / kTile;
-  const int64_t all = tiles * a.B * p.groups;
+  if (tiles * p.groups > (INT64_MAX - sm_count) / a.B) return TOPK_EINVAL;
+  const int64_t all = tiles * p.groups * a.B;
   const int64_t even = (all + sm_count - 1) / sm_count;
   p.unit_tiles = static_cast<int32_t>(even < most ? even : most);
   p.chunks = static_cast<int32_t>((tiles + p.unit_tiles - 1) / p.unit_tiles);

@@ -244,8 +244,8 @@ topk_status launch_typed(const sparse_rotary_args& a, int sm_count, cudaStream_t
   // Heads per thread: as many as leave every SM a few CTAs, up to sixteen, so
   // that cos and sin are computed once for them.
   p.rows = p.items < kRotThreads ? kRotThreads / p.items : 1;
-  const int64_t threads = static_cast<int64_t>(a.T) * a.H * p.items;
-  const int64_t slots = static_cast<int64_t>(sm_count) * kRotThreads;
+  const double threads = static_cast<double>(a.T) * a.H * p.items;
+  const double slots = static_cast<double>(sm_count) * kRotThreads;
   const int steps = threads >= 64 * slots ? 16 : threads >= 32 * slots ? 8 : threads >= 16 * slots ? 4 : threads >= 8 * slots ? 2 : 1;
   p.heads = (a.H + steps - 1) / steps < p.rows ? (a.H + steps - 1) / steps : p.rows;
   p.tokens = p.rows / p.heads < a.T ? p.rows / p.heads : a.T;

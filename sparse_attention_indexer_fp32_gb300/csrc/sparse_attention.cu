@@ -152,6 +152,8 @@ struct AttParts {
   float part[2][64][36];
 };
 
+__host__ __device__ __forceinline__ int tiles_of(int32_t entries) { return entries / kKeys + (entries % kKeys != 0); }
+
 struct Work {
   int g, heads, head0;  // key head; real rows, and the first one's query head
   int64_t row, b, t;
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
   constexpr bool kStay = COPIES <= 2;
   const uint32_t step_w = gridDim.x / cluster;
   Work k = work_of(p, blockIdx.x / cluster);
-  const int all_tiles = (a.K + kKeys - 1) / kKeys;
+  const int all_tiles = tiles_of(a.K);
   const int tiles = all_tiles > static_cast<int>(rank) ? (all_tiles - static_cast<int>(rank) + cluster - 1) / cluster : 0;
   const uint32_t base = smem_addr(smem);
   const uint32_t k_ring = base + p.k_at, v_ring = base + p.v_at;
@@ -743,7 +745,7 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   AttParams p = {};
   p.a = a;
   p.heads = a.Hq / a.Hkv;
-  p.m_tiles = (p.heads + 127) / 128;
+  p.m_tiles = p.heads / 128 + (p.heads % 128 != 0);
   p.scale_log2e = finite(static_cast<double>(a.scale) * kLog2e);
   if (a.softcap > 0.0f) {
     p.scale_over_cap = finite(static_cast<double>(a.scale) / a.softcap);
@@ -798,20 +800,19 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   const size_t floor_bytes = p.tmem_cols == 512 ? kMaxShared : 77 * 1024;
   if (bytes < floor_bytes) bytes = floor_bytes;
   const int64_t work = static_cast<int64_t>(a.B) * a.T * a.Hkv * p.m_tiles;
-  if (work > INT32_MAX) return TOPK_EINVAL;
   p.works = static_cast<uint32_t>(work);
   // Few rows: share each over the CTAs that would idle, down to two tiles each
   // (one row x 2048 entries, one key head: 26.8 us on one CTA, 18.6, 14.4 and
   // 12.4 on 2, 4 and 8; 16 key-head rows x 512: 8.7 us at two tiles a CTA, 9.5
   // at one).
   const int64_t slots = static_cast<int64_t>(sm_count) * (two ? 2 : 1);
-  const int tiles = (a.K + kKeys - 1) / kKeys;
+  const int tiles = tiles_of(a.K);
   int cluster = 1;
   while (cluster < 8 && work * cluster * 2 <= slots && cluster * 4 <= tiles) cluster *= 2;
   // One or two copies: CTAs stay, one on each place (2048 rows x 512 entries:
   // 137 us, 168 with a CTA a row).
   const int64_t grid = copies <= 2 && cluster == 1 && work > slots ? slots : work * cluster;
-  if (grid > INT32_MAX) return TOPK_EINVAL;
+  if ((work / grid + 1) * tiles > INT32_MAX) return TOPK_EINVAL;  // a CTA counts its tiles
   if (copies == 4) return launch_copies<E, 4>(p, dev, cluster, grid, bytes, stream);
   if (copies == 2) return launch_copies<E, 2>(p, dev, cluster, grid, bytes, stream);
   return launch_copies<E, 1>(p, dev, cluster, grid, bytes, stream);

@@ -60,7 +60,7 @@ extern "C" {
 topk_status sparse_rotary(const sparse_rotary_args* args, topk_stream_t stream) {
   if (args == nullptr) return TOPK_EINVAL;
   sparse_rotary_args a = *args;
-  if (a.T < 0 || a.H < 0 || a.D < 1 || a.D > SPARSE_ROTARY_MAX_D) return TOPK_EINVAL;
+  if (a.T < 0 || a.H < 0 || a.H > SPARSE_ROTARY_MAX_H || a.D < 1 || a.D > SPARSE_ROTARY_MAX_D) return TOPK_EINVAL;
   if (a.rotated < 2 || a.rotated % 2 != 0 || a.offset < 0 || a.offset > a.D - a.rotated) return TOPK_EINVAL;
   if (a.type != SPARSE_BF16 && a.type != SPARSE_FP16 && a.type != SPARSE_FP32) return TOPK_EINVAL;
   if (a.layout != SPARSE_ROTARY_HALF && a.layout != SPARSE_ROTARY_INTERLEAVED) return TOPK_EINVAL;
@@ -135,6 +135,8 @@ topk_status sparse_attention(const sparse_attention_args* args, topk_stream_t st
   if (a.slopes != nullptr && a.query_positions == nullptr) return TOPK_EINVAL;
   if (a.B == 0 || a.T == 0 || a.Hq == 0) return TOPK_OK;
   if (a.page_size > 0 && a.num_pages > INT64_MAX / a.page_size) return TOPK_EINVAL;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T, heads = a.Hq / a.Hkv;
+  if (rows > INT32_MAX || rows * a.Hkv > INT32_MAX || rows * a.Hkv * ((heads + 127) / 128) > INT32_MAX) return TOPK_EINVAL;
   const bool entries = a.K > 0 && a.num_pages > 0 && a.page_size > 0;
   if (a.q == nullptr || a.out == nullptr || (a.K > 0 && a.indices == nullptr) ||
       (entries && (a.k == nullptr || a.v == nullptr)))

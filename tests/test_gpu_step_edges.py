@@ -251,3 +251,49 @@ def test_a_tensor_written_in_place_is_known_to_have_changed():
     with torch.inference_mode():  # whose tensors have no version
         y = x.clone()
         assert torch.equal(tk.rotary(y, pos, f, out=y), tk.rotary(x, pos, f))
+
+
+# ---- the longest ---------------------------------------------------------------------------------------
+
+
+def test_attention_over_the_longest_list():
+    """2^31 - 1 indices (8.6 GB), all but a few of them of nothing."""
+    K, D = 2 ** 31 - 1, 64
+    idx = torch.full((1, 1, K), -1, dtype=torch.int32, device=DEV)
+    at = [0, 63, 64, 2 ** 30, K - 65, K - 64, K - 1]
+    idx[0, 0, at] = torch.arange(len(at), dtype=torch.int32, device=DEV)
+    q, k = _randn((1, 1, 2, D), 1, BF16), _randn((1, 16, 1, D), 2, BF16)
+    short = torch.arange(len(at), dtype=torch.int32, device=DEV).view(1, 1, -1)
+    got, lse = tk.sparse_attention(q, k, k, idx, return_lse=True)
+    want = R.attention(q, k, k, short, None, None, D ** -0.5, 0.0, None, None)
+    R.assert_near(got, want[0], want[1])
+    R.assert_near(lse, want[2], want[3])
+
+
+def test_scores_of_the_most_tokens():
+    """2^31 - 1 query tokens of one sequence, one score each (26 GB)."""
+    T, D = 2 ** 31 - 1, 16
+    q, keys = _randn((1, 1, 1, D), 1, BF16), _randn((1, 1, D), 2, BF16)
+    if float(q.float().flatten() @ keys.float().flatten()) < 0:
+        q = -q
+    w = torch.ones((1, T, 1), device=DEV)
+    n = torch.ones((1, T), dtype=torch.int32, device=DEV)
+    out = torch.zeros((1, T, 1), device=DEV)
+    tk.indexer_scores(q.expand(1, T, 1, D), w, keys, n, _ints([[0]]), out=out)
+    few = tk.indexer_scores(q, w[:, :1], keys, n[:, :1], _ints([[0]]))
+    assert (out == few).all()
+
+
+def test_scores_of_too_many_units_are_refused():
+    from sparse_attention_indexer_fp32_gb300 import _step
+
+    some, most = torch.zeros(64, device=DEV), 2 ** 31 - 1
+    lib = tk.load_library()
+    fn, kind = lib.sparse_indexer_scores, _step._ScoresArgs
+    fn.argtypes, fn.restype = [ctypes.POINTER(kind), ctypes.c_void_p], ctypes.c_int
+    for sizes in (dict(B=most, T=most, width=64, table_width=64), dict(B=most, T=most, width=most, table_width=most),
+                  dict(B=most, T=1, width=most, table_width=most)):
+        a = kind(q=some.data_ptr(), q_seq_stride=0, q_token_stride=0, q_head_stride=0, weights=some.data_ptr(),
+                 keys=some.data_ptr(), key_page_stride=0, key_token_stride=0, lengths=some.data_ptr(),
+                 page_table=some.data_ptr(), out=some.data_ptr(), num_pages=1, page_size=1, H=1, D=16, **sizes)
+        assert fn(ctypes.byref(a), None) == tk.Status.EINVAL, sizes

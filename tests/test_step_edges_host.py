@@ -5,6 +5,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import sparse_attention_indexer_fp32_gb300 as tk  # noqa: E402
+from sparse_attention_indexer_fp32_gb300 import _step  # noqa: E402
+from test_step_host import ATTENTION, ROTARY, _status, lib  # noqa: E402, F401
 
 
 def test_gradients_are_refused():
@@ -21,3 +23,14 @@ def test_gradients_are_refused():
         tk.sparse_attention(q, q, q, n[None])
     with torch.no_grad(), pytest.raises(ValueError, match="x must be a CUDA tensor"):
         tk.rotary(x, pos, f)
+
+
+def test_sizes_past_the_counters_are_refused(lib):  # noqa: F811
+    """Products of sizes that pass 32 (or 64) bits, and heads whose count in steps would, before any CUDA call."""
+    most = 2 ** 31 - 1
+    for change in (dict(H=most), dict(H=2 ** 30 + 1, T=1)):
+        assert _status(lib, "sparse_rotary", _step._RotaryArgs, ROTARY, **change) == tk.Status.EINVAL, change
+    # 2^62, 2^64 (0 in 64 bits), 2^32 rows and heads, 2^31 tiles of heads
+    for change in (dict(B=most, T=most), dict(B=2 ** 30, T=2 ** 30, Hkv=16, Hq=16), dict(B=2 ** 30, T=1, Hkv=4),
+                   dict(B=2 ** 8, T=1, Hkv=1, Hq=most)):
+        assert _status(lib, "sparse_attention", _step._AttentionArgs, ATTENTION, **change) == tk.Status.EINVAL, change
