@@ -80,6 +80,7 @@ struct ScoreShared {
   int32_t lengths[2][kMaxTokens];
   uint64_t full[6], q_full[2], q_empty[2];
   uint64_t t_full[8], t_empty[8];  // of tile k at k % 8: nobody who waits on one lags behind by eight tiles
+  uint64_t drained;
   Unit units[2];  // with the queries; no tiles: the end
   uint32_t tmem;
   uint32_t stop;
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       mbar_init(&sh.q_empty[i], 1 + kEpilogueWarps);
     }
     for (int i = 0; i < 8; ++i) mbar_init(&sh.t_full[i], 1), mbar_init(&sh.t_empty[i], 128 * p.share);
+    mbar_init(&sh.drained, 1);
     sh.stop = 0;
     fence_mbar_init();
   }
@@ -250,6 +252,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   volatile uint32_t* stop = &sh.stop;
+  bool one = false;  // the thread that issues products
 
   // what a copy of nothing points at
   const void* nowhere = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p.a.q) & ~static_cast<uintptr_t>(15));
@@ -383,6 +386,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
     const uint64_t ring_desc = operand_desc(ring_addr), q_desc = operand_desc(q_addr);
     uint32_t k = 0, stage = 0, turn = 0;
     bool ok = true;
+    one = elect_one();
     for (uint32_t nu = 0; ok; ++nu) {
       const uint32_t buf = nu & 1;
       ok = wait_or_stop(&sh.q_full[buf], (nu >> 1) & 1, stop);
@@ -393,7 +397,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       // one thread from here: its waits need no vote
       const int tiles = r.tile1 - r.tile0;
       bool done = true;
-      if (elect_one()) {
+      if (one) {
         const uint64_t db = q_desc + (buf * q_bytes >> 4);
         uint32_t st = stage, tn = turn;
         for (int i = 0; i < tiles; ++i) {
@@ -427,9 +431,6 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
       if (((tiles / STAGES) & 1) != 0) turn ^= 1;
       if (stage >= STAGES) stage -= STAGES, turn ^= 1;
     }
-    // every product is complete before the memory it uses goes away
-    for (uint32_t i = 0; i < 2 && i < k; ++i)
-      wait_or_stop(&sh.t_full[(k - 1 - i) & 7], ((k - 1 - i) >> 3) & 1, stop);
   } else {
     // ---- sums over heads ----
     // Four groups of four warps, each with all 128 positions of a tile: two
@@ -550,6 +551,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   if (*stop != 0) {  // a wait ran out: NaN, not half a result
+    if (one) mma_drain(&sh.drained);
+    __syncwarp();
     for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
       const Unit r = unit_of(p, u);
       for (int t = 0; t < r.tokens; ++t) {

@@ -91,6 +91,7 @@ struct AttShared {
   // Nobody who waits on one lags behind by eight tiles.
   uint64_t s_full[8], p_full[8], pv_done[8];
   uint64_t q_empty, o_free;  // Q used up, O read: between one work and the next
+  uint64_t drained[2];       // of the threads that issue Q K^T and P V
   uint32_t tmem;
   uint32_t stop;
 };
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
     for (int i = 0; i < 8; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 128), mbar_init(&sh.pv_done[i], 1);
     mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.o_free, 128);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.drained[i], 1);
     sh.stop = 0;
     fence_mbar_init();
   }
@@ -280,6 +282,7 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem, tmem_o = tmem + p.bufs * kKeys;
   volatile uint32_t* stop = &sh.stop;
+  bool one = false;  // a thread that issues products
 
   float top = __int_as_float(0xff800000), sum = 0.0f;  // of this thread's row (its reference and sum of weights)
 
@@ -371,7 +374,8 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
     copy_wait<0>();
   } else if (warp == kMmaWarp) {
     // ---- S = Q K^T, by one thread, whose waits need no vote ----
-    if (tiles > 0 && elect_one()) {
+    one = elect_one();
+    if (tiles > 0 && one) {
       const uint32_t desc = mma_desc(Pack<E>::type, kKeys);
       const uint64_t q_desc = operand_desc(base), k_desc = operand_desc(k_ring);
       int stage = 0, turn_of = 0, n = 0;
@@ -403,7 +407,8 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
     __syncwarp();
   } else if (warp == kMmaWarp + 1) {
     // ---- O += P V, by another, so that neither's waits hold up the other ----
-    if (tiles > 0 && elect_one()) {
+    one = elect_one();
+    if (tiles > 0 && one) {
       const uint32_t desc = mma_desc(Pack<E>::type, (a.Dv + 15) / 16 * 16, true);
       const uint64_t v_desc = operand_desc(p.shared ? k_ring : v_ring, kKeys * 128);
       const int stages = p.shared ? p.k_stages : p.v_stages, stage_bytes = p.shared ? p.k_bytes : p.v_bytes;
@@ -603,6 +608,12 @@ __global__ void __launch_bounds__(kAttThreads, COPIES == 4 ? 2 : 1)
   // ---- join the copies ----
   // Every row of the buffer below is scaled to its head's maximum in this CTA.
   __syncthreads();
+  if (*stop != 0) {  // a wait ran out: nobody may have waited for what is in flight
+    if (one) mma_drain(&sh.drained[warp - kMmaWarp]);
+    copy_commit();
+    copy_wait<0>();
+    __syncthreads();
+  }
   if (!kStay || cluster > 1) {
   const int pad = p.v_blocks * 64 + 4;  // floats per row: rows 4 banks apart
   float* rows = reinterpret_cast<float*>(smem);

@@ -185,15 +185,24 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, i
 // block in the layout above.
 __device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t unit) { return row * 128 + ((unit ^ (row & 7)) << 4); }
 
-// Waits of the threads of one CTA on each other: false where it gave up. A wait that is not over after a second, far
-// beyond any real one, raises `stop`, which ends every other wait of the CTA
-// too; the caller then leaves its loop.
+// How long a wait inside a kernel may take: a second, far beyond any real one,
+// unless a test builds the kernels with less.
+#ifndef SPARSE_WAIT_LIMIT_NS
+#define SPARSE_WAIT_LIMIT_NS 1000000000
+#endif
+constexpr uint64_t kWaitLimit = SPARSE_WAIT_LIMIT_NS;
+constexpr bool kNap = kWaitLimit >= 1000000;  // a look that sleeps may outlast a shorter limit
+
+// Waits of the threads of one CTA on each other: false where it gave up. A
+// wait that is not over in time raises `stop`, which ends every other wait of
+// the CTA too; the caller then leaves its loop, but not the kernel before what
+// it has in flight itself is complete.
 __device__ __forceinline__ bool wait_or_stop_one(uint64_t* bar, uint32_t parity, volatile uint32_t* stop) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (kNap ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+  while (!(kNap ? mbar_try_wait_sleep(bar, parity, 20000u) : mbar_test_wait(bar, parity))) {
     if (*stop != 0) return false;
-    if (global_timer_ns() - t0 > 1000000000ull) {
+    if (global_timer_ns() - t0 > kWaitLimit) {
       *stop = 1;
       return false;
     }
@@ -203,6 +212,14 @@ __device__ __forceinline__ bool wait_or_stop_one(uint64_t* bar, uint32_t parity,
 // The same for a whole warp, with one answer for all of its lanes.
 __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile uint32_t* stop) {
   return __all_sync(0xffffffffu, wait_or_stop_one(bar, parity, stop));
+}
+
+// Until every product that this thread has issued is complete, whatever was
+// given up: their operands, sums and barriers may go away after it. `bar`
+// is used for nothing else.
+__device__ __forceinline__ void mma_drain(uint64_t* bar) {
+  mma_commit(bar);
+  mbar_wait_bounded(bar, 0, 1000000000ull);
 }
 
 }  // namespace tki

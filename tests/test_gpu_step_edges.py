@@ -2,6 +2,8 @@
 
 import ctypes
 import math
+import os
+import subprocess
 from fractions import Fraction
 
 import numpy as np
@@ -17,6 +19,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU-only machines
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import sparse_attention_indexer_fp32_gb300 as tk  # noqa: E402
+from sparse_attention_indexer_fp32_gb300 import _step  # noqa: E402
 
 DEV = torch.device("cuda:0")
 BF16, FP16, FP32, E4M3 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
@@ -285,8 +288,6 @@ def test_scores_of_the_most_tokens():
 
 
 def test_scores_of_too_many_units_are_refused():
-    from sparse_attention_indexer_fp32_gb300 import _step
-
     some, most = torch.zeros(64, device=DEV), 2 ** 31 - 1
     lib = tk.load_library()
     fn, kind = lib.sparse_indexer_scores, _step._ScoresArgs
@@ -297,3 +298,76 @@ def test_scores_of_too_many_units_are_refused():
                  keys=some.data_ptr(), key_page_stride=0, key_token_stride=0, lengths=some.data_ptr(),
                  page_table=some.data_ptr(), out=some.data_ptr(), num_pages=1, page_size=1, H=1, D=16, **sizes)
         assert fn(ctypes.byref(a), None) == tk.Status.EINVAL, sizes
+
+
+# ---- waits that run out --------------------------------------------------------------------------------
+
+
+@pytest.fixture(scope="module")
+def hurried(tmp_path_factory):
+    """The library once more, with waits that give up at once or after 3 us: {limit in ns: {call: its function}}."""
+    from sparse_attention_indexer_fp32_gb300 import build as cuda_build
+
+    units = ["step_abi.cu", "rotary.cu", "sparse_attention.cu", "indexer_scores_bf16.cu", "indexer_scores_fp16.cu",
+             "indexer_scores_e4m3.cu"]
+    out = tmp_path_factory.mktemp("hurried")
+    jobs = []
+    for ns in (0, 3000):
+        for u in units:
+            jobs.append(subprocess.Popen([cuda_build.nvcc(), *cuda_build.ARCH, "-O3", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
+                                          "-I", cuda_build.INCLUDE, f"-DSPARSE_WAIT_LIMIT_NS={ns}", "-c",
+                                          os.path.join(cuda_build.CSRC, u), "-o", str(out / f"{ns}_{u}.o")]))
+    assert [job.wait() for job in jobs] == [0] * len(jobs)
+    calls = {}
+    for ns in (0, 3000):
+        path = str(out / f"libhurried_{ns}.so")
+        subprocess.check_call([cuda_build.nvcc(), *cuda_build.ARCH, "-shared", "-o", path,
+                               *(str(out / f"{ns}_{u}.o") for u in units)])
+        lib = ctypes.CDLL(path)
+        prototype = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, ctypes.c_void_p)
+        calls[ns] = {call: prototype(ctypes.cast(getattr(lib, call.name), ctypes.c_void_p).value)
+                     for call in (_step._scores, _step._attention)}
+    return calls
+
+
+def _right_or_nan(hurried, monkeypatch, call):
+    """With waits that run out each number is what it is without, or NaN, and the calls after are right again."""
+    want = call()
+    for ns in (0, 3000, 0):
+        with monkeypatch.context() as patch:
+            for entry, fn in hurried[ns].items():
+                patch.setattr(entry, "fn", fn)
+            got = call()
+        torch.cuda.synchronize()
+        lost = 0
+        for g, w in zip(got, want):
+            nan = torch.isnan(g)
+            lost += int(nan.sum())
+            assert torch.equal(torch.where(nan, w, g), w), f"neither right nor NaN with a limit of {ns} ns"
+        assert ns > 0 or lost > 0, "no wait ran out"
+        for g, w in zip(call(), want):
+            assert torch.equal(g, w), f"the call after one with a limit of {ns} ns"
+
+
+@pytest.mark.parametrize("B,T,H,ps,dtype", [(2, 1, 64, 64, BF16), (3, 5, 24, 7, FP16), (200, 1, 32, 64, BF16),
+                                            (1, 300, 16, 16, E4M3), (1, 64, 128, 64, BF16)])
+def test_scores_whose_waits_run_out(hurried, monkeypatch, B, T, H, ps, dtype):
+    width, D = 2300, 64
+    pages = -(-width // ps)
+    q, w = _randn((B, T, H, D), 1).to(dtype), _randn((B, T, H), 2)
+    keys = _randn((B * pages, ps, D), 3).to(dtype)
+    table = torch.arange(B * pages, dtype=torch.int32, device=DEV).view(B, pages)
+    n = torch.randint(0, width + 1, (B, T), generator=_gen(4), device=DEV).to(torch.int32)
+    _right_or_nan(hurried, monkeypatch,
+                  lambda: (tk.indexer_scores(q, w, keys, n, table, out=torch.full((B, T, width), 7.0, device=DEV)),))
+
+
+@pytest.mark.parametrize("rows,Hq,Hkv,K,shared", [(1, 8, 1, 2048, False), (3, 16, 4, 700, True), (100, 8, 4, 300, False),
+                                                  (2, 40, 1, 900, False), (340, 40, 1, 130, False), (340, 70, 1, 64, True),
+                                                  (20, 150, 1, 200, False)])
+def test_attention_whose_waits_run_out(hurried, monkeypatch, rows, Hq, Hkv, K, shared):
+    D, ps = 64, 16
+    q, k = _randn((rows, 1, Hq, D), 1, BF16), _randn((200, ps, Hkv, D), 2, BF16)
+    v = k if shared else _randn(k.shape, 3, BF16)
+    idx = torch.randint(-1, 200 * ps, (rows, 1, K), generator=_gen(4), device=DEV).to(torch.int32)
+    _right_or_nan(hurried, monkeypatch, lambda: tk.sparse_attention(q, k, v, idx, softcap=30.0, return_lse=True))
