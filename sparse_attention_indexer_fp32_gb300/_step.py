@@ -205,8 +205,8 @@ def rotary_frequencies(rotated: int, base: float = 10000.0, *, scaling: Optional
     ``scaling`` stretches a context of ``original_length`` positions by ``factor``: ``"linear"``
     divides every frequency by it; ``"base"`` raises the base to ``base * factor ** (rotated /
     (rotated - 2))``, which keeps the fastest pair and divides the slowest by the factor; ``"ramp"``
-    keeps pairs that turn more than ``fast`` times within ``original_length``, divides those that turn
-    less than ``slow`` times, and blends linearly over the pairs between (the by-parts interpolation of
+    keeps pairs that turn more than ``fast`` times within ``original_length`` (the first at least),
+    divides those that turn less than ``slow`` times, and blends linearly over the pairs between (the by-parts interpolation of
     the YaRN paper, Peng et al. 2023, section 3.2; its section 3.3 goes with ``scale = 0.1 *
     math.log(factor) + 1`` in :func:`rotary`)."""
     if rotated < 2 or rotated % 2:
@@ -224,14 +224,14 @@ def rotary_frequencies(rotated: int, base: float = 10000.0, *, scaling: Optional
     elif scaling == "ramp":
         if original_length < 1 or not fast > slow > 0.0:
             raise ValueError("the ramp needs original_length >= 1 and fast > slow > 0")
-        if base == 1.0:
-            raise ValueError("the ramp needs a base other than 1")
+        if base <= 1.0:
+            raise ValueError("the ramp needs a base above 1")
 
         def pair(turns: float) -> float:  # the (fractional) pair that turns so often
             return rotated * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
 
-        low = min(max(math.floor(pair(fast)), 0), rotated // 2 - 1)
-        high = min(max(math.ceil(pair(slow)), 0), rotated // 2 - 1)
+        # either end may lie past the last pair: the ramp is then cut off there
+        low, high = max(math.floor(pair(fast)), 0), max(math.ceil(pair(slow)), 0)
         ramp = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
         f = f * (1.0 - ramp) + f / factor * ramp
     elif scaling not in (None, "base"):

@@ -1,5 +1,7 @@
 """The operators around the selection at the edges of what they accept, on the host."""
 
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -34,3 +36,23 @@ def test_sizes_past_the_counters_are_refused(lib):  # noqa: F811
     for change in (dict(B=most, T=most), dict(B=2 ** 30, T=2 ** 30, Hkv=16, Hq=16), dict(B=2 ** 30, T=1, Hkv=4),
                    dict(B=2 ** 8, T=1, Hkv=1, Hq=most)):
         assert _status(lib, "sparse_attention", _step._AttentionArgs, ATTENTION, **change) == tk.Status.EINVAL, change
+
+
+@pytest.mark.parametrize("base,rotated,length", [(10000.0, 64, 4096), (10000.0, 64, 131072), (10000.0, 128, 2 ** 20),
+                                                 (500.0, 32, 65536), (1e6, 64, 8192), (10000.0, 16, 2 ** 27)])
+def test_the_ramp_ends_where_the_pairs_turn_once(base, rotated, length):
+    """Pairs that turn more than `fast` times are kept, those under `slow` times divided, and those between lie
+    between, also where all pairs turn more than `slow` times and the ramp would end past the last."""
+    plain = tk.rotary_frequencies(rotated, base, device="cpu")
+    ramp = tk.rotary_frequencies(rotated, base, scaling="ramp", factor=8.0, original_length=length, device="cpu")
+    turns, kept = plain * length / (2 * math.pi), ramp / plain
+    assert torch.allclose(kept[turns > 32.0], torch.ones((), dtype=torch.float64), rtol=1e-14)
+    assert torch.allclose(kept[turns < 1.0], torch.full((), 0.125, dtype=torch.float64), rtol=1e-14)
+    assert (kept[turns > 1.001] > 0.1251).all()
+    assert (kept[1:] <= kept[:-1] + 1e-14).all()
+
+
+def test_the_ramp_needs_falling_frequencies():
+    for base in (1.0, 0.5):
+        with pytest.raises(ValueError, match="base above 1"):
+            tk.rotary_frequencies(8, base, scaling="ramp", device="cpu")
