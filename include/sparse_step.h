@@ -131,7 +131,10 @@ topk_status sparse_indexer_scores(const sparse_scores_args* args, topk_stream_t 
  * position: query_positions, first and slopes must be NULL.
  * v may be a prefix of the entries of k (same pointer and strides): the entry
  * is then fetched once.
- * An infinity or NaN that is seen makes NaN of every result it enters.
+ * A NaN that is seen makes NaN of every result it enters, and so does a
+ * logit of +infinity without a cap; with one an infinite logit is +-softcap. A
+ * logit of -infinity has weight 0; a row of nothing else sees nothing. An
+ * infinity of v that is seen makes its column infinite or NaN.
  * Sums, statistics and the accumulation of out are FP32; the weights
  * exp(z_j - m) are rounded to the type of v for the second product, once.
  */

@@ -91,6 +91,45 @@ def test_attention_cap_under_the_smallest_number():
         tk.sparse_attention(q, k, k, _ints([[[0, 1]]]), softcap=1e-60)
 
 
+# ---- attention: infinities ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("heads", [4, 40, 80])
+def test_attention_infinities_that_are_seen(heads):
+    """Infinite logits by the formula: the cap's ends, weight 0, NaN; an infinite value stays in its column."""
+    n, D, ps = 100, 64, 16
+    q = _randn((1, 1, heads, D), 1, BF16)
+    q[..., 3] = q[..., 3].abs() + 0.1
+    k, v = (_randn((7, ps, 1, D), s, BF16) for s in (2, 3))
+    idx = torch.arange(n, dtype=torch.int32, device=DEV).view(1, 1, n)
+
+    def call(k, v, idx=idx, **kw):
+        return tk.sparse_attention(q, k, v, idx, return_lse=True, **kw)
+
+    low, high = k.clone(), k.clone()
+    low.view(-1, D)[70, 3], high.view(-1, D)[70, 3] = -math.inf, math.inf
+    rest = torch.cat([idx[..., :70], idx[..., 71:]], dim=-1).contiguous()
+    want = R.attention(q, k, v, rest, None, None, D ** -0.5, 0.0, None, None)
+    got = call(low, v)
+    R.assert_near(got[0], want[0], want[1])
+    R.assert_near(got[1], want[2], want[3])
+    assert all(torch.isnan(t).all() for t in call(high, v))
+    out, lse = call(low, v, idx[..., 70:71].contiguous())
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    only = torch.zeros_like(k)  # logits past any cap, then so far past it that they are it
+    only.view(-1, D)[70, 3], only.view(-1, D)[71, 3] = -math.inf, math.inf
+    far = only.nan_to_num(posinf=1e30, neginf=-1e30)
+    for g, w in zip(call(only, v, softcap=2.0), call(far, v, softcap=2.0)):
+        assert torch.equal(g, w) and torch.isfinite(g).all()
+    value = v.clone()
+    value.view(-1, D)[50, 9] = math.inf
+    out, lse = call(k, value)
+    plain, want = call(k, v)
+    assert not torch.isfinite(out[..., 9]).any() and torch.equal(lse, want)
+    keep = [d for d in range(D) if d != 9]
+    assert torch.equal(out[..., keep], plain[..., keep])
+
+
 # ---- indexer scores: infinite keys -------------------------------------------------------------------
 
 
