@@ -410,3 +410,34 @@ def test_attention_whose_waits_run_out(hurried, monkeypatch, rows, Hq, Hkv, K, s
     v = k if shared else _randn(k.shape, 3, BF16)
     idx = torch.randint(-1, 200 * ps, (rows, 1, K), generator=_gen(4), device=DEV).to(torch.int32)
     _right_or_nan(hurried, monkeypatch, lambda: tk.sparse_attention(q, k, v, idx, softcap=30.0, return_lse=True))
+
+
+# ---- two streams ---------------------------------------------------------------------------------------
+
+
+def test_scores_and_attention_side_by_side():
+    """Kernels of both calls, with all or half of an SM's TMEM, with clusters and without, on two streams at once."""
+    q, k = _randn((40, 1, 32, 128), 1, BF16), _randn((300, 16, 4, 128), 2, BF16)
+    idx = torch.randint(-1, 4800, (40, 1, 600), generator=_gen(3), device=DEV).to(torch.int32)
+    wide, entry = _randn((3, 1, 40, 256), 4, BF16), _randn((300, 16, 1, 256), 5, BF16)
+    some = torch.randint(-1, 4800, (3, 1, 900), generator=_gen(6), device=DEV).to(torch.int32)
+    iq, w = _randn((16, 1, 32, 64), 7, BF16), _randn((16, 1, 32), 8)
+    keys, table = k.view(300, 16, 8, 64)[:, :, 0], torch.arange(300, dtype=torch.int32, device=DEV).expand(16, -1)
+    n = torch.full((16, 1), 4800, dtype=torch.int32, device=DEV)
+    calls = [lambda: tk.sparse_attention(q, k, k, idx), lambda: tk.indexer_scores(iq, w, keys, n, table),
+             lambda: tk.sparse_attention(wide, entry, entry, some), lambda: tk.sparse_attention(q[:2], k, k, idx[:2]),
+             lambda: tk.indexer_scores(iq[:3], w[:3], keys, n[:3], table[:3])]
+    want = [call() for call in calls]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for turn in range(1, len(calls)):
+        got = [[], []]
+        for _ in range(10):
+            for i in range(len(calls)):
+                for side, stream in enumerate(streams):
+                    with torch.cuda.stream(stream):
+                        got[side].append(calls[(i + side * turn) % len(calls)]())
+        torch.cuda.synchronize()
+        for side in range(2):
+            for i, g in enumerate(got[side]):
+                assert torch.equal(g, want[(i + side * turn) % len(calls)])
