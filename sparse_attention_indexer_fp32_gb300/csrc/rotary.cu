@@ -101,15 +101,16 @@ struct alignas(sizeof(E) * V) Vec {
   E e[V];
 };
 
-// Marked as read and written once: 8192 x 64 x 128 in 45 us, 57 without.
+// One access of 16 bytes: 8192 x 64 x 128 in 41.6 us, 56 element by element (and
+// 42.6 marked as read and written once).
 template <typename T>
 __device__ __forceinline__ T load16(const void* from) {
-  const uint4 v = __ldcs(static_cast<const uint4*>(from));
+  const uint4 v = *static_cast<const uint4*>(from);
   return *reinterpret_cast<const T*>(&v);
 }
 template <typename T>
 __device__ __forceinline__ void store16(void* to, const T& v) {
-  __stcs(static_cast<uint4*>(to), *reinterpret_cast<const uint4*>(&v));
+  *static_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(&v);
 }
 
 // V elements per item side. HALF: an item that turns holds V elements of the
@@ -242,7 +243,8 @@ topk_status launch_typed(const sparse_rotary_args& a, int sm_count, cudaStream_t
   p.turn_items = vec ? (half ? pairs / V : a.rotated / V) : pairs;
   p.items = p.turn_items + (in_place ? 0 : (a.D - a.rotated) / (vec ? V : 1));
   // Heads per thread: as many as leave every SM a few CTAs, up to sixteen, so
-  // that cos and sin are computed once for them.
+  // that cos and sin are computed once for them (8192 tokens x 64 heads: 122 us by
+  // one head, 72, 48, 42 and 42 by 2, 4, 8 and 16; four tokens: 3.5 us by one, 6.6 by 16).
   p.rows = p.items < kRotThreads ? kRotThreads / p.items : 1;
   const double threads = static_cast<double>(a.T) * a.H * p.items;
   const double slots = static_cast<double>(sm_count) * kRotThreads;
