@@ -250,7 +250,8 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
     joint query-key-value tensor), ``positions`` int32 or int64 ``[T]``, ``frequencies`` float64 on
     the GPU (:func:`rotary_frequencies`). ``layout`` ``"half"`` pairs element ``i`` with ``i +
     rotated / 2``, ``"interleaved"`` ``2 i`` with ``2 i + 1``. ``inverse`` turns back: the gradient
-    of the call with the same arguments. ``out`` may be ``x`` (in place). With ``slots`` (int32
+    of the call with the same arguments. ``out`` may be ``x`` (in place); the addresses of any other
+    ``out`` lie wholly before or behind those of ``x``. With ``slots`` (int32
     ``[T]``), ``out`` is a paged cache ``[pages, page_size, H, D]`` and token ``t`` is written at slot
     ``slots[t]`` (negative or past the cache: not written). Returns ``out``."""
     shape, xs, code, index = _main(x, "x", 3, _ROTARY_TYPES)

@@ -9,8 +9,8 @@
 // position, and the sum over heads needs no exchange: a maximum and a
 // multiply-add per product (packed multiply-adds cost a move each, 4.6
 // instructions a product in all; the accumulator's own layout, which needs a
-// quarter of the weights per thread, reads TMEM slower: 303 us for the prefill). A tile of keys is fetched once for all
-// query tokens of its group.
+// quarter of the weights per thread, reads TMEM slower: half as long again). A
+// tile of keys is fetched once for all query tokens of its group.
 //
 // One CTA per SM, 20 warps: three fetch (keys through the page table into a
 // ring, by TMA boxes or, where pages are too odd for them, 16-byte copies;
@@ -19,13 +19,14 @@
 // warps sum over heads. Work units are (sequence, range of tiles, group of
 // query tokens).
 //
-// Measured: decode, 64 sequences of up to 65536 positions, 64 heads, bf16, 154
-// us, 6.4 TB/s (145 us for its bytes at the measured copy rate): HBM bound.
-// Prefill, 2048 tokens on 8192 positions, 168 us, 1.4 PFLOP/s (127 us at
-// the measured matrix rate): the sums over heads keep the issue slots busy about
-// as long as the products keep the tensor cores, and the two overlap only so far
-// with two TMEM buffers. e4m3, 32 sequences x 2 tokens x 32769, 40 us (20): one
-// tile is 16 KB and its fixed cost per warp shows.
+// Measured: decode, 64 sequences of up to 65536 positions, 64 heads, bf16, 155
+// us, 6.3 TB/s (145 us for its bytes at the measured copy rate): HBM bound.
+// Prefill, 2048 tokens on 8192 positions, 165 us, 1.5 PFLOP/s (127 us at
+// the measured matrix rate): the tensor pipe is busy in 66 % of the cycles and
+// the issue slots in 67 %; with two TMEM buffers products wait for a buffer's
+// whole read and sums for a whole product. e4m3, 32 sequences x 2 tokens x 32769,
+// pages of 16, 40 us (20): HBM at 39 %, the tensor pipe at 9 %; every role makes
+// a round of waits for each tile, which is half the bytes of a 16-bit one.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -435,8 +436,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) scores_kernel(const __grid_c
     // ---- sums over heads ----
     // Four groups of four warps, each with all 128 positions of a tile: two
     // share every other tile's tokens, or, where there is one token, each takes
-    // every fourth tile. (All four on one tile wait and sum in step: 214
-    // instead of 191 us for 2048 x 8192; eight warps in all: 270.)
+    // every fourth tile. (2048 x 8192: 165 us by two; by one 188, by all four,
+    // which then wait and sum in step, 198. Two tokens, e4m3: 39.9 by two, 38.5 by one.)
     const int group = warp >> 2, quarter = warp & 3;
     const int tile_step = 4 / p.share, turn_of = group / p.share, part = group % p.share;
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
@@ -616,8 +617,10 @@ topk_status launch_scores_of(const sparse_scores_args& a, int dev, int sm_count,
   p.groups = a.T / p.tokens + (a.T % p.tokens != 0);
   // Work units of at most 16 tiles, 8 where a tile is short work: enough of
   // them to even out the SMs, long enough to hide the next unit's queries
-  // (64 x 65536, 64 columns: 156 us by 8, 160 by 16; 2048 x 8192, 256
-  // columns: 193 by 16, 195 by 8); fewer while SMs would idle.
+  // (64 x 65536, 64 columns: 155.5 us by 8, 159 by 16; e4m3, 32 x 2 x 32769, 64
+  // columns: 40.0 and 43.4; e4m3, 8 x 8 x 32769, 256 columns: 19.5 and 17.4. Two bytes and
+  // 256 columns go either way: 2048 x 8192 161 by 8 and 164.5 by 16 with 64 heads, 323 and
+  // 310 with 128); fewer while SMs would idle.
   const int most = p.cols <= 128 ? 8 : 16;
   const int64_t tiles = (a.width + kTile - 1) / kTile;
   if (tiles * p.groups > (INT64_MAX - sm_count) / a.B) return TOPK_EINVAL;
@@ -631,8 +634,8 @@ topk_status launch_scores_of(const sparse_scores_args& a, int dev, int sm_count,
   p.q_vector = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_seq_stride * size % 16 == 0 &&
                a.q_token_stride * size % 16 == 0 && a.q_head_stride * size % 16 == 0;
   // Boxes hold entries of one page: the largest power of two that divides the
-  // page, where it is at least 16 (64 x 65536: 185 us by boxes of 16, 277 by
-  // boxes of 8, 220 to 256 by copies).
+  // page, where it is at least 16 (64 x 65536: pages of 16 181 us by boxes, 199 by
+  // copies; of 48 211 and 252; of 8 273 and 199).
   int rows = a.page_size & -a.page_size;
   rows = rows < kTile ? rows : kTile;
   const int64_t extents[3] = {a.D, a.page_size, a.num_pages}, strides[2] = {a.key_token_stride, a.key_page_stride};

@@ -12,13 +12,14 @@
 // operations. A thread owns one 16-byte item of the head (two, where the
 // second half's partner goes with it) of one token and walks over heads, so
 // that it computes its pairs' cos and sin once, in registers, while its first
-// loads are in flight; no shared memory, no barrier. (A table per CTA in shared
-// memory put two barriers between loads and stores: 87 us for 8192 tokens x 64
-// heads x 128, bf16.)
+// loads are in flight; no shared memory, no barrier (a table per CTA in shared
+// memory puts two barriers between loads and stores, and took twice as long).
 //
-// Measured: that case 43 us, 6.2 TB/s, against 39.6 us for its bytes at the
-// measured copy rate; 4097 x 24 x 80 in FP32 9.2 us (9.3); four tokens 3.5 us,
-// most of it the launch and three dependent reads.
+// Measured: 8192 tokens x 64 heads x 128, bf16, 41.7 us, 6.4 TB/s, against 39.5 us
+// for its bytes at the measured copy rate; 4097 x 24 x 80 in FP32 8.0 us, partly
+// from L2 (9.3 from HBM); four tokens 3.5 us, most of it the launch and three
+// dependent reads. 2048 x 64 x 130, where nothing is aligned, 23.5 us for 9.6 of
+// the 128: two bytes an access.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

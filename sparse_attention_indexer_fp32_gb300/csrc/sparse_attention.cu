@@ -26,17 +26,17 @@
 // P V. Keys and values have rings of their own, filled by two warps of a set
 // each: a stage of keys is free again right after Q K^T, so the gathers run
 // ahead of the softmax (one ring of both, two stages deep, left every tile
-// waiting for its gather: 3.5 us a tile).
+// waiting for its gather).
 //
 // Precision. Scores, statistics and O are FP32; a weight 2^(z - r) is rounded
 // once to the type of v, the operand type of the second product, half a step
-// (2^-9 in bf16) relative to itself; the sum that divides adds the unrounded ones.
+// (2^-8 in bf16) relative to itself; the sum that divides adds the unrounded ones.
 //
-// Measured: 64 rows x 2048 entries x 8 key heads of 128, bf16, capped, 89 us,
-// 6.0 TB/s of random 256-byte reads (80 us for its bytes at the measured copy
-// rate). 2048 rows x 512 entries of 256 + 192 shared, 64 heads: 134 us (180
-// with a CTA for every row: half of its time began and ended it). Four rows x
-// 512 entries: 8.7 us, two tiles a CTA and one exchange.
+// Measured: 64 rows x 2048 entries x 8 key heads of 128, bf16, capped, 92 us,
+// 5.9 TB/s of random 256-byte reads (79 us for its bytes at the measured copy
+// rate). 2048 rows x 512 entries of 256 + 192 shared, 64 heads: 131 us, the tensor
+// pipe busy in 40 % of the cycles (31 us at the measured matrix rate). Four rows x
+// 512 entries: 8.5 us, two tiles a CTA and one exchange.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -818,12 +818,12 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   p.q_vector = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_seq_stride % 8 == 0 && a.q_token_stride % 8 == 0 &&
                a.q_head_stride % 8 == 0;
   // As many copies as the heads leave room for: 64 rows x 2048 entries with 8
-  // heads a key head take 94 us with 4 copies, 106 with 2, 137 with 1.
+  // heads a key head take 92 us with 4 copies, 103 with 2, 142 with 1.
   const int copies = p.heads <= 32 ? 4 : p.heads <= 64 ? 2 : 1;
   // Shared memory: Q, then the ring; at the end the same bytes hold the rows
   // to be joined. Two CTAs share an SM where two stages each fit (and TMEM
   // holds both), else one CTA has as many stages as fit (64 rows x 2048 entries
-  // x 8 key heads: 94 us with two, 111 with one).
+  // x 8 key heads: 92 us with two, 109 with one).
   const int q_bytes = 128 * 128 * p.d_blocks;
   p.k_bytes = kKeys * 128 * p.d_blocks;
   p.v_bytes = p.shared ? 0 : kKeys * 128 * p.v_blocks;
@@ -857,15 +857,15 @@ topk_status launch_typed(const sparse_attention_args& a, int dev, int sm_count, 
   const int64_t work = static_cast<int64_t>(a.B) * a.T * a.Hkv * p.m_tiles;
   p.works = static_cast<uint32_t>(work);
   // Few rows: share each over the CTAs that would idle, down to two tiles each
-  // (one row x 2048 entries, one key head: 26.8 us on one CTA, 18.6, 14.4 and
-  // 12.4 on 2, 4 and 8; 16 key-head rows x 512: 8.7 us at two tiles a CTA, 9.5
-  // at one).
+  // (one row x 2048 entries, one key head: 25.5 us on one CTA, 16.9, 12.0 and
+  // 9.8 on 2, 4 and 8; 16 key-head rows x 512: 8.4 us at two tiles a CTA, 9.4
+  // at one and at four).
   const int64_t slots = static_cast<int64_t>(sm_count) * (two ? 2 : 1);
   const int tiles = tiles_of(a.K);
   int cluster = 1;
   while (cluster < 8 && work * cluster * 2 <= slots && cluster * 4 <= tiles) cluster *= 2;
   // One or two copies: CTAs stay, one on each place (2048 rows x 512 entries:
-  // 137 us, 168 with a CTA a row).
+  // 131 us, 166 with a CTA a row, half of which begins and ends it).
   const int64_t grid = copies <= 2 && cluster == 1 && work > slots ? slots : work * cluster;
   if ((work / grid + 1) * tiles > INT32_MAX) return TOPK_EINVAL;  // a CTA counts its tiles
   if (copies == 4) return launch_copies<E, 4>(p, dev, cluster, grid, bytes, stream);
