@@ -11,12 +11,12 @@
  *                          cache (the consumer of their output)
  *
  * All pointers are DEVICE pointers owned by the caller, all strides are in
- * elements; the stride of a dimension of one element is not used. A call enqueues one kernel on `stream`, allocates nothing, keeps
- * nothing and never synchronises. Invalid arguments, and sizes that would need
- * more than 2^31 - 1 work units, return TOPK_EINVAL before anything is
- * enqueued, a device other than sm_103 TOPK_EDEVICE, a failing CUDA call
- * TOPK_ECUDA. Waits inside a kernel end after a second; results that such a
- * wait left unfinished are NaN.
+ * elements; the stride of a dimension of one element is not used. A call
+ * enqueues one kernel on `stream`, allocates nothing, keeps nothing and never
+ * synchronises. Invalid arguments, and sizes that would need more than 2^31 - 1
+ * work units, return TOPK_EINVAL before anything is enqueued, a device other
+ * than sm_103 TOPK_EDEVICE, a failing CUDA call TOPK_ECUDA. Waits inside a kernel
+ * end after a second; results that such a wait left unfinished are NaN.
  *
  * A paged cache is read and written through page ids: entry i of a sequence
  * lies at page page_table[i / page_size], place i % page_size. An id or a

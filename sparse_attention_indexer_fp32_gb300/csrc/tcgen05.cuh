@@ -185,6 +185,19 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, i
 // block in the layout above.
 __device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t unit) { return row * 128 + ((unit ^ (row & 7)) << 4); }
 
+// As mbar_try_wait, without any sleep.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // How long a wait inside a kernel may take: a second, far beyond any real one,
 // unless a test builds the kernels with less.
 #ifndef SPARSE_WAIT_LIMIT_NS
