@@ -172,7 +172,7 @@ def prepare(case, seed):
 
 
 def _turned(state):
-    """The rotated keys in 32 bits, the angles in 64; and what bounds them at any angle: the length of each pair."""
+    """The rotated keys in 32 bits, the angles in 64; and what bounds them at any angle: the sum of each pair's sizes."""
     case, x = state["case"], state["k"].float()
     R, offset = case["rotated"], case["offset"]
     angle = state["positions"].double()[:, None] * state["frequencies"]
@@ -185,7 +185,7 @@ def _turned(state):
         a, b = part[..., 0::2], part[..., 1::2]
         turned = torch.stack([a * cos - b * sin, b * cos + a * sin], dim=-1).flatten(-2)
     rest = (x[..., :offset], x[..., offset + R:])
-    return torch.cat([rest[0], turned, rest[1]], dim=-1), torch.cat([rest[0].abs(), torch.sqrt(a * a + b * b), rest[1].abs()], dim=-1)
+    return torch.cat([rest[0], turned, rest[1]], dim=-1), torch.cat([rest[0].abs(), a.abs() + b.abs(), rest[1].abs()], dim=-1)
 
 
 def _store(state, side, y, sizes):
@@ -337,10 +337,9 @@ def _exact_append(s, case):
         one, two = slice(o, o + R // 2), slice(o + R // 2, o + R)
     else:
         one, two = slice(o, o + R, 2), slice(o + 1, o + R, 2)
-    pairs = torch.complex(k[..., one], k[..., two])
     y, size = k.clone(), k.abs()
-    size[..., one] = size[..., two] = pairs.abs()
-    z = pairs * torch.polar(torch.ones_like(turn), turn)
+    size[..., one] = size[..., two] = size[..., one] + size[..., two]
+    z = torch.complex(k[..., one], k[..., two]) * torch.polar(torch.ones_like(turn), turn)
     y[..., one], y[..., two] = z.real, z.imag
     got = {}
     got["k_cache"], got["k_scales"] = _exact_side(s, "k", y, size.amax(dim=-1))
