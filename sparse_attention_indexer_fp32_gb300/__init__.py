@@ -14,6 +14,8 @@ CUDA kernels (``_build/libtopk_indexer.so``):
   :func:`sparse_attention` - the steps around the selection: rotary positions
   (also into a paged cache), the indexer's scores over a paged key cache, and
   attention over the selected entries;
+* :func:`cache_append` - keys, rotated on the way, and values into paged caches,
+  of their own type or in 8 bits with a scale for each block of tokens and head;
 * :func:`topk_select_ex` - diagnostics: a forced internal path, path counters;
   :func:`max_active_clusters` - the CUDA driver's cluster residency per size.
 
@@ -39,10 +41,11 @@ from ._binding import (  # noqa: F401
     topk_select_ex,
     workspace_bytes,
 )
+from ._cache import cache_append  # noqa: F401
 from ._step import indexer_scores, rotary, rotary_frequencies, sparse_attention  # noqa: F401
 
 __all__ = ["topk_ragged", "topk_paged", "topk_select_ex", "topk_select_bf16", "workspace_bytes",
            "amax8_varlen", "sort_candidate_blocks", "max_active_clusters", "rotary", "rotary_frequencies",
-           "indexer_scores", "sparse_attention", "TopkError", "Status", "Counter",
+           "indexer_scores", "sparse_attention", "cache_append", "TopkError", "Status", "Counter",
            "load_library", "raw_library", "LIB_PATH", "TOPK_MAX_K", "NUM_COUNTERS",
            "DEVICE_ERROR_INDEX"]

@@ -1,0 +1,147 @@
+"""ctypes binding of the operators of a paged cache in 8 bits
+(``include/sparse_cache.h``), by the same rules as ``_step``."""
+
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+from ._step import (_BF16, _E4M3, _F64, _FP16, _FP32, _I32, _I64, _LAYOUTS, _ROTARY_TYPES, _Call, _main, _no_broadcast,
+                    _other, _overlap, _span, _whole, _written)
+
+_i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+
+
+class _AppendArgs(ctypes.Structure):
+    _fields_ = [("k", _vp), ("k_token_stride", _i64), ("k_head_stride", _i64),
+                ("v", _vp), ("v_token_stride", _i64), ("v_head_stride", _i64),
+                ("k_cache", _vp), ("k_cache_page_stride", _i64), ("k_cache_token_stride", _i64),
+                ("k_cache_head_stride", _i64),
+                ("v_cache", _vp), ("v_cache_page_stride", _i64), ("v_cache_token_stride", _i64),
+                ("v_cache_head_stride", _i64),
+                ("k_scales", _vp), ("v_scales", _vp), ("positions", _vp), ("frequencies", _vp), ("slots", _vp),
+                ("num_pages", _i64), ("page_size", _i32), ("blocks", _i32), ("T", _i32), ("H", _i32), ("D", _i32),
+                ("Dv", _i32), ("rotated", _i32), ("offset", _i32), ("layout", _i32), ("type", _i32),
+                ("cache_type", _i32), ("positions_64", _i32), ("scale", _f32)]
+
+
+_append = _Call("sparse_append", _AppendArgs)
+
+
+def _scales_of(scales, name: str, pages: int, page_size: int, heads: int, index: int):
+    """The address of a cache's scales, and its blocks a page."""
+    blocks = scales.shape[1] if isinstance(scales, torch.Tensor) and scales.dim() == 3 else 0
+    if blocks < 1 or page_size % blocks:
+        raise ValueError(f"{name} must be [pages, blocks, heads], with blocks that divide the page size")
+    return _whole(scales, name, (pages, blocks, heads), _FP32, index), blocks
+
+
+def _entries(cache, name: str, like, heads: int, size: int, index: int):
+    """Shape and strides of a cache of these heads, its entries in 8 bits or of the type of `like`."""
+    if not isinstance(cache, torch.Tensor) or cache.dtype not in (like, _E4M3):
+        raise ValueError(f"{name} must be a 4-D tensor of {like} or {_E4M3}")
+    shape, strides = _other(cache, name, 4, cache.dtype, index)
+    if shape[2:] != (heads, size):
+        raise ValueError(f"{name} must be [pages, page_size, {heads}, {size}]")
+    _no_broadcast(shape, strides, name)
+    return shape, strides
+
+
+def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                 frequencies: Optional[torch.Tensor], k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
+                 slots: torch.Tensor, *, k_scales: Optional[torch.Tensor] = None,
+                 v_scales: Optional[torch.Tensor] = None, layout: str = "half", offset: int = 0, scale: float = 1.0,
+                 stream=None) -> None:
+    """Keys, rotated as by :func:`rotary`, and values into paged caches of their own type or in 8 bits.
+
+    ``k`` bfloat16, float16 or float32 ``[T, H, D]`` and ``v`` ``[T, H, Dv]`` of the same type (any
+    strides, unit in the last dimension; ``None``, with ``v_cache``, for keys alone); ``positions`` int32 or
+    int64 ``[T]`` and ``frequencies`` float64 (:func:`rotary_frequencies`; ``None``, then ``positions`` may be
+    ``None`` too, for keys that are not rotated); ``layout``, ``offset`` and ``scale`` as in :func:`rotary`.
+    Token ``t`` is written at slot ``slots[t]`` (int32; negative or past the cache: not written) of
+    ``k_cache`` ``[pages, page_size, H, D]`` and ``v_cache`` ``[pages, page_size, H, Dv]``.
+
+    Caches in float8_e4m3fn hold entries in units of ``k_scales`` and ``v_scales``, float32 ``[pages, blocks,
+    H]``: the ``page_size // blocks`` entries of a block share one for each head. Tokens of one block follow
+    one another in the call. A block that a call begins at its first place gets the smallest power of two that
+    holds the call's tokens; one that is continued keeps its scale while that holds them, otherwise the scale
+    grows and the entries before are rounded again (places behind the call's first one count as empty, and so
+    does a block whose scale is 0). ``[pages, page_size, 1]`` for one head is what :func:`indexer_scores` takes as
+    ``key_scales``; :func:`sparse_attention` reads any."""
+    shape, xs, code, index = _main(k, "k", 3, _ROTARY_TYPES)
+    T, H, D = shape
+    dtype = k.dtype
+    to = _whole(slots, "slots", (T,), _I32, index)
+    ks, kt = _entries(k_cache, "k_cache", dtype, H, D, index)
+    pages, page_size = ks[:2]
+    eight = k_cache.dtype == _E4M3
+    pos, freq, pairs, wide = 0, 0, 0, False
+    if frequencies is not None:
+        pairs = frequencies.numel() if isinstance(frequencies, torch.Tensor) else 0
+        freq = _whole(frequencies, "frequencies", (pairs,), _F64, index)
+        wide = isinstance(positions, torch.Tensor) and positions.dtype == _I64
+        pos = _whole(positions, "positions", (T,), _I64 if wide else _I32, index)
+    if layout not in _LAYOUTS:
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    if not math.isfinite(scale):
+        raise ValueError("scale must be finite")
+    if (v is None) != (v_cache is None):
+        raise ValueError("v and v_cache go together")
+    Dv, vx, vt, at_v, to_v = 0, (0, 0), (0, 0, 0), 0, 0
+    bytes_in = k.element_size()
+    size = 1 if eight else bytes_in
+    at_k, to_k = k.data_ptr(), k_cache.data_ptr()
+    mine, keys = _span(at_k, shape, xs, bytes_in), _span(to_k, ks, kt, size)
+    if _overlap(mine, keys):
+        raise ValueError("k_cache must not overlap k")
+    if v is not None:
+        vs, vx = _other(v, "v", 3, dtype, index)
+        if vs[:2] != (T, H):
+            raise ValueError("v must be [T, H, Dv]")
+        Dv = vs[2]
+        cs, vt = _entries(v_cache, "v_cache", dtype, H, Dv, index)
+        if cs[:2] != ks[:2] or v_cache.dtype != k_cache.dtype:
+            raise ValueError("v_cache must have the pages and the type of k_cache")
+        at_v, to_v = v.data_ptr(), v_cache.data_ptr()
+        theirs, values = _span(at_v, vs, vx, bytes_in), _span(to_v, cs, vt, size)
+        if _overlap(theirs, keys) or _overlap(theirs, values) or _overlap(mine, values):
+            raise ValueError("the caches must not overlap k or v")
+        if _overlap(keys, values) and _meet(ks, kt, vt, Dv, to_v - to_k, size):
+            raise ValueError("v_cache must not overlap k_cache")
+    units_k, units_v, blocks = 0, 0, 0
+    if eight:
+        units_k, blocks = _scales_of(k_scales, "k_scales", pages, page_size, H, index)
+        if v is not None:
+            units_v, other = _scales_of(v_scales, "v_scales", pages, page_size, H, index)
+            if other != blocks:
+                raise ValueError("v_scales must have the blocks of k_scales")
+            if units_v == units_k and pages * H > 0:
+                raise ValueError("v_scales must not be k_scales: each cache has its own")
+    elif k_scales is not None or v_scales is not None:
+        raise ValueError("only caches in float8_e4m3fn have scales")
+    _append(index, stream, at_k, xs[0], xs[1], at_v, vx[0], vx[1], to_k, kt[0], kt[1], kt[2], to_v, vt[0], vt[1], vt[2],
+            units_k, units_v, pos, freq, to, pages, page_size, blocks, T, H, D, Dv, 2 * pairs, int(offset),
+            _LAYOUTS[layout], code, 3 if eight else code, wide, scale)
+    for t in (k_cache, v_cache, k_scales, v_scales):
+        if t is not None:
+            _written(t)
+
+
+def _meet(shape, strides, others, second: int, gap: int, size: int) -> bool:
+    """Whether two caches of these pages and heads share an element, the second one's entries `second`
+    elements long and its start `gap` bytes behind the first one's. Parts of one tensor do not: they have its
+    strides and lie side by side in its pages, tokens or entries. Any other two whose addresses mix may."""
+    if gap % size or any(n > 1 and s != t for n, s, t in zip(shape[:3], strides, others)):
+        return True
+    dims = sorted(((s, n) for n, s in zip(shape[:3], strides) if n > 1), reverse=True)
+
+    def meet(gap, dims):
+        if not dims:
+            return -second < gap < shape[3]
+        step, n = dims[0]
+        return any(meet(gap - d * step, dims[1:]) for d in (gap // step, gap // step + 1) if -n < d < n)
+
+    return meet(gap // size, dims)
