@@ -79,6 +79,28 @@ typedef struct sparse_append_args {
 } sparse_append_args;
 topk_status sparse_append(const sparse_append_args* args, topk_stream_t stream);
 
+/*
+ * sparse_attention_e4m3 - sparse_attention (its masks, cap, biases, empty rows
+ * and slots, word for word) over a cache whose entries stand for k = k_scales[b,
+ * g] * the numbers of attention.k, v = v_scales[b, g] * those of attention.v, with b
+ * the entry's block and g the key head. attention.type is the type of q and out.
+ * Scales are finite; values' scales of 2^-60 to 2^60 lose nothing, below that the
+ * values fade out. A NaN in an entry that is seen makes NaN of every result it
+ * enters, and so does a query that is not finite.
+ * Products are exact: a bf16 or fp16 query is split into two or three E4M3 terms
+ * (elements below 2^-13 of their head's largest one keep steps of 2^-20, or 2^-24, of
+ * that); sums and statistics are FP32. A weight, times its value's scale, is rounded to
+ * 9 bits (SPARSE_BF16) or to fp16's 11 (SPARSE_FP16) for the second product, once;
+ * weights below 2^-10 of a head's largest keep steps of 2^-19, or 2^-23, of it.
+ */
+typedef struct sparse_attention_e4m3_args {
+  sparse_attention_args attention; /* k, v: SPARSE_E4M3, 16-byte aligned, strides multiples of 16; D, Dv <= 256, multiples of 16 */
+  const float* k_scales;           /* [num_pages, blocks, Hkv] contiguous */
+  const float* v_scales;           /* the same, or the same ones */
+  int32_t blocks;                  /* divides page_size */
+} sparse_attention_e4m3_args;
+topk_status sparse_attention_e4m3(const sparse_attention_e4m3_args* args, topk_stream_t stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -10,7 +10,7 @@ from typing import Optional
 import torch
 
 from ._step import (_BF16, _E4M3, _F64, _FP16, _FP32, _I32, _I64, _LAYOUTS, _ROTARY_TYPES, _Call, _main, _no_broadcast,
-                    _other, _overlap, _span, _whole, _written)
+                    _other, _overlap, _scales_of, _span, _whole, _written)
 
 _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -29,14 +29,6 @@ class _AppendArgs(ctypes.Structure):
 
 
 _append = _Call("sparse_append", _AppendArgs)
-
-
-def _scales_of(scales, name: str, pages: int, page_size: int, heads: int, index: int):
-    """The address of a cache's scales, and its blocks a page."""
-    blocks = scales.shape[1] if isinstance(scales, torch.Tensor) and scales.dim() == 3 else 0
-    if blocks < 1 or page_size % blocks:
-        raise ValueError(f"{name} must be [pages, blocks, heads], with blocks that divide the page size")
-    return _whole(scales, name, (pages, blocks, heads), _FP32, index), blocks
 
 
 def _entries(cache, name: str, like, heads: int, size: int, index: int):

@@ -50,6 +50,9 @@ class _AttentionArgs(ctypes.Structure):
                 ("softcap", _f32)]
 
 
+class _AttentionE4m3Args(ctypes.Structure):  # the attention's own arguments first (include/sparse_cache.h)
+    _fields_ = _AttentionArgs._fields_ + [("k_scales", _vp), ("v_scales", _vp), ("blocks", _i32)]
+
 
 # The current device's index and the handle of its current stream, without the
 # Python objects around them (torch.cuda's own functions, a microsecond less).
@@ -104,6 +107,7 @@ class _Call:
 
 _rotary, _scores, _attention = (_Call("sparse_rotary", _RotaryArgs), _Call("sparse_indexer_scores", _ScoresArgs),
                                 _Call("sparse_attention", _AttentionArgs))
+_attention_e4m3 = _Call("sparse_attention_e4m3", _AttentionE4m3Args)
 
 
 def _no_gradient(name: str) -> None:
@@ -169,6 +173,14 @@ def _whole(t, name: str, shape, dtype, index: int) -> int:
         pass
     raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on the device of the other "
                      "arguments")
+
+
+def _scales_of(scales, name: str, pages: int, page_size: int, heads: int, index: int):
+    """The address of an 8-bit cache's scales, and its blocks a page."""
+    blocks = scales.shape[1] if isinstance(scales, torch.Tensor) and scales.dim() == 3 else 0
+    if blocks < 1 or page_size % blocks:
+        raise ValueError(f"{name} must be [pages, blocks, heads], with blocks that divide the page size")
+    return _whole(scales, name, (pages, blocks, heads), _FP32, index), blocks
 
 
 def _empty(shape, dtype, like, stream):
@@ -347,7 +359,8 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
                      page_table: Optional[torch.Tensor] = None, *,
                      query_positions: Optional[torch.Tensor] = None, scale: Optional[float] = None,
                      softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
-                     first: Optional[torch.Tensor] = None, return_lse: bool = False,
+                     first: Optional[torch.Tensor] = None, k_scales: Optional[torch.Tensor] = None,
+                     v_scales: Optional[torch.Tensor] = None, return_lse: bool = False,
                      out: Optional[torch.Tensor] = None, stream=None):
     """Attention of every query token over its selected entries of a paged cache.
 
@@ -356,6 +369,10 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
     ``indices`` int32 ``[B, T, K]``, the selected positions, negative where there is none
     (:func:`topk_ragged`), mapped through ``page_table`` int32 ``[B, n]``; without a page table they
     are slots (:func:`topk_paged`).
+
+    A cache in 8 bits: ``k`` and ``v`` float8_e4m3fn with ``k_scales`` and ``v_scales`` float32 ``[pages,
+    blocks, Hkv]``, a scale for each ``page_size // blocks`` entries and head (:func:`cache_append`); ``q`` and the
+    result then stay bfloat16 or float16, ``D`` and ``Dv`` are multiples of 16.
 
     ``scale`` (default ``D ** -0.5``) multiplies the products, ``softcap`` caps them by ``softcap *
     tanh(z / softcap)``, ``slopes`` float32 ``[Hq]`` adds ``slopes[h] * (position -
@@ -366,8 +383,10 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
     shape, qs, code, index = _main(q, "q", 4, _ATTENTION_TYPES)
     B, T, Hq, D = shape
     dtype = q.dtype
-    ks, kt = _other(k, "k", 4, dtype, index)
-    vs, vt = _other(v, "v", 4, dtype, index)
+    eight = k_scales is not None or v_scales is not None
+    held = _E4M3 if eight else dtype
+    ks, kt = _other(k, "k", 4, held, index)
+    vs, vt = _other(v, "v", 4, held, index)
     pages, page_size, Hkv = ks[:3]
     Dv = vs[3]
     if ks[3] != D or vs[:3] != ks[:3]:
@@ -381,7 +400,8 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
         ps, strides = _other(page_table, "page_table", 2, _I32, index)
         if ps[0] != B:
             raise ValueError("page_table must have one row for each sequence")
-        table, pt, width = page_table.data_ptr(), strides[0], ps[1]
+        # a table without a page has no address, and none is read: it is still not the call without a table
+        table, pt, width = page_table.data_ptr() or 16, strides[0], ps[1]
     elif query_positions is not None or first is not None or slopes is not None:
         raise ValueError("slots have no position: query_positions, first and slopes need a page_table")
     if slopes is not None and query_positions is None:
@@ -401,14 +421,25 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
         target = out.data_ptr()
     else:
         target = _whole(out, "out", (B, T, Hq, Dv), dtype, index)
-        mine = (target, target + 2 * B * T * Hq * Dv)
-        if _overlap(mine, _span(at_q, shape, qs, 2)) or _overlap(mine, _span(at_k, ks, kt, 2)) \
-                or _overlap(mine, _span(at_v, vs, vt, 2)):
+        mine, size = (target, target + 2 * B * T * Hq * Dv), 1 if eight else 2
+        if _overlap(mine, _span(at_q, shape, qs, 2)) or _overlap(mine, _span(at_k, ks, kt, size)) \
+                or _overlap(mine, _span(at_v, vs, vt, size)):
             raise ValueError("out must not overlap q, k or v")
+    call, scales = _attention, ()
+    if eight:
+        units, blocks = _scales_of(k_scales, "k_scales", pages, page_size, Hkv, index)
+        if v_scales is k_scales:
+            scales = (units, units, blocks)
+        else:
+            others, same = _scales_of(v_scales, "v_scales", pages, page_size, Hkv, index)
+            if same != blocks:
+                raise ValueError("v_scales must have the blocks of k_scales")
+            scales = (units, others, blocks)
+        call = _attention_e4m3
     lse = _empty((B, T, Hq), _FP32, q, stream) if return_lse else None
-    _attention(index, stream, at_q, qs[0], qs[1], qs[2], at_k, kt[0], kt[1], kt[2], at_v, vt[0], vt[1], vt[2], idx, table,
-               pt, width, qp, begin, bias, target, 0 if lse is None else lse.data_ptr(), pages, page_size, B, T, Hq, Hkv,
-               D, Dv, K, code, scale, softcap)
+    call(index, stream, at_q, qs[0], qs[1], qs[2], at_k, kt[0], kt[1], kt[2], at_v, vt[0], vt[1], vt[2], idx, table,
+         pt, width, qp, begin, bias, target, 0 if lse is None else lse.data_ptr(), pages, page_size, B, T, Hq, Hkv,
+         D, Dv, K, code, scale, softcap, *scales)
     if given:
         _written(out)
     return (out, lse) if return_lse else out

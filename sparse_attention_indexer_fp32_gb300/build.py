@@ -22,6 +22,7 @@ LIB = os.path.join(BUILD, "libtopk_indexer.so")
 SOURCES = (["topk_abi.cu"] + [f"topk_k{k}_{o}.cu" for k in (512, 1024, 2048) for o in ("ragged", "paged")]
            + [f"topk_short_k{k}.cu" for k in (512, 1024, 2048)] + ["topk_blocks.cu"]
            + ["step_abi.cu", "rotary.cu", "sparse_attention.cu", "cache_abi.cu", "cache_append.cu"]
+           + [f"cache_attention_{t}.cu" for t in ("bf16", "fp16")]
            + [f"indexer_scores_{t}.cu" for t in ("bf16", "fp16", "e4m3")])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -9,5 +9,7 @@
 namespace tki {
 
 topk_status launch_append(const sparse_append_args& a, int sm_count, cudaStream_t stream);
+topk_status launch_cache_attention_bf16(const sparse_attention_e4m3_args& a, int dev, int sm_count, cudaStream_t stream);
+topk_status launch_cache_attention_fp16(const sparse_attention_e4m3_args& a, int dev, int sm_count, cudaStream_t stream);
 
 }  // namespace tki

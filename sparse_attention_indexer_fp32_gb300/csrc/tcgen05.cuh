@@ -66,6 +66,17 @@ __device__ __forceinline__ void tmem_ld(uint32_t (&v)[16], uint32_t addr) {
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(addr));
 }
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t (&v)[8], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(addr));
+}
 __device__ __forceinline__ void tmem_ld(uint32_t (&v)[32], uint32_t addr) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
@@ -84,6 +95,12 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&v)[16]) 
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // ---- matrix products --------------------------------------------------------
 
 // Descriptor of a shared-memory operand in the layout above. `other` is the
@@ -96,9 +113,9 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t other =
 
 // Instruction descriptor: FP32 accumulators, M = 128 rows, N columns; `type`
 // is 0 for fp16 (kind f16) and e4m3 (kind f8f6f4), 1 for bf16. With `b_rows`
-// B's rows run along the inner dimension.
-__device__ __forceinline__ constexpr uint32_t mma_desc(uint32_t type, uint32_t n, bool b_rows = false) {
-  return (1u << 4) | (type << 7) | (type << 10) | (b_rows ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+// (`a_rows`) B's (A's) rows run along the inner dimension.
+__device__ __forceinline__ constexpr uint32_t mma_desc(uint32_t type, uint32_t n, bool b_rows = false, bool a_rows = false) {
+  return (1u << 4) | (type << 7) | (type << 10) | (a_rows ? 1u << 15 : 0u) | (b_rows ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 // D[tmem] (+)= A[smem] B[smem], issued by one thread.
@@ -152,6 +169,10 @@ __device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, uint32
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) { copy_bytes(dst, src, valid ? 16 : 0); }
+// The same for 4 bytes.
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
 // One arrival on `bar` when every copy16 of this thread so far is complete;
 // it counts against the arrivals the barrier was initialised with.
 __device__ __forceinline__ void copy_arrive(uint64_t* bar) {

@@ -83,3 +83,67 @@ def append(x, positions, frequencies, cache, scales, slots, block, layout="half"
         flat[slots[t]] = np.where(np.isfinite(exact), np.clip(exact, -448.0, 448.0), np.nan)
         err[slots[t]] = off + np.maximum((np.abs(exact) + off) * 2.0 ** -4, 2.0 ** -10) + 2.0 ** -22 * np.abs(exact)
     return got, err.reshape(got.shape), new
+
+
+def entries(cache, scales):
+    """What the entries of a cache in 8 bits stand for, float64 [pages, page_size, heads, size], and their scales."""
+    page_size, blocks = cache.shape[1], scales.shape[1]
+    units = np.repeat(R.np64(scales), page_size // blocks, axis=1)[..., None]
+    return R.np64(cache.float()), units
+
+
+def attention(q, k, v, k_scales, v_scales, indices, table, query_positions, scale, softcap=0.0, slopes=None, first=None):
+    """(out, its bound, lse, its bound). As step_reference.attention, with what this form rounds: a query's terms
+    end at half a step of 2^-20 (bf16) or 2^-24 of its largest element; a weight is rounded to fp16 and to 9 bits
+    (bf16) or to fp16, and ends at half a step of 2^-19 or 2^-23 of the largest weight, each times its value's scale."""
+    B, T, Hq, D = q.shape
+    pages, ps, Hkv, Dv = v.shape
+    q_type, U, three = q.dtype, R.U, q.dtype == torch.float16
+    rounded = 2.0 ** -11 if three else 2.0 ** -9 + 2.0 ** -11
+    query_end, weight_end = (2.0 ** -25, 2.0 ** -24) if three else (2.0 ** -21, 2.0 ** -20)
+    hs, tiny = R.half_step(q.dtype), torch.finfo(q.dtype).tiny * torch.finfo(q.dtype).eps
+    (kf, ku), (vf, vu) = entries(k, k_scales), entries(v, v_scales)
+    kf, ku, vf, vu = kf.reshape(-1, Hkv, D), ku.reshape(-1, Hkv), vf.reshape(-1, Hkv, Dv), vu.reshape(-1, Hkv)
+    q, idx, table, qp, first, slopes = R.np64(q), R.npi(indices), R.npi(table), R.npi(query_positions), R.npi(first), R.np64(slopes)
+    out, oerr = np.zeros((B, T, Hq, Dv)), np.zeros((B, T, Hq, Dv))
+    lse, lerr = np.full((B, T, Hq), -np.inf), np.zeros((B, T, Hq))
+    for b in range(B):
+        for t in range(T):
+            pos = idx[b, t]
+            sl = R.slots_of(None if table is None else table[b], pos, ps, pages) if pages * ps else np.full(len(pos), -1)
+            ok = sl >= 0
+            if qp is not None:
+                ok &= pos <= qp[b, t]
+            if first is not None:
+                ok &= pos >= first[b, t]
+            sl, pos = sl[ok], pos[ok]
+            if not len(sl):
+                continue
+            for h in range(Hq):
+                g = h // (Hq // Hkv)
+                x, kk, vv, vs = q[b, t, h], kf[sl, g] * ku[sl, g, None], vf[sl, g], vu[sl, g]
+                z = kk @ x * scale
+                dz = abs(scale) * ((D + 8) * U * (np.abs(kk) @ np.abs(x)) + query_end * np.abs(x).max() * np.abs(kk).sum(1))
+                dz = dz + 6 * U * np.abs(z)
+                if softcap:
+                    z = softcap * np.tanh(z / softcap)
+                    dz = dz + 8 * U * np.abs(z)
+                if slopes is not None:
+                    away = slopes[h] * (pos - qp[b, t])
+                    z = z + away
+                    dz = dz + 4 * U * (np.abs(away) + np.abs(z))
+                top = z.max()
+                e = np.exp(z - top)
+                dz = dz + 4 * U * np.abs(z - top) + 8 * U
+                p, total = e / e.sum(), e.sum()
+                w = p * vs
+                out[b, t, h] = w @ vv
+                mean_dz = p @ dz + (len(sl) + 8) * U
+                end = weight_end * (p * np.maximum(np.abs(vs), 2.0 ** -60)).max()
+                oerr[b, t, h] = ((np.abs(w) * (rounded + dz + mean_dz) + end) @ np.abs(vv)) * 1.01 \
+                    + hs * np.abs(out[b, t, h]) * 1.01 + tiny
+                lse[b, t, h] = np.log(total) + top
+                lerr[b, t, h] = mean_dz + 4 * U * (abs(top) + abs(lse[b, t, h]))
+    with np.errstate(invalid="ignore"):  # a result past the type's largest number rounds to infinity
+        out = np.where(np.abs(out) > torch.finfo(q_type).max * (1 + 2 * hs), np.copysign(np.inf, out), out)
+    return out, oerr, lse, lerr

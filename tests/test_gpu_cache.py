@@ -300,3 +300,249 @@ def test_append_in_a_graph_and_on_a_stream():
     _append(c, stream=side)
     side.synchronize()
     _check(c, want)
+
+
+# ---- attention over a cache in 8 bits ----------------------------------------------------------------
+
+
+def _attend(B, T, Hq, Hkv, D, Dv, K, S, ps, blocks, dtype, seed=0, shared=False, spread=1.0, **more):
+    """The arguments of a call on ragged sequences in a pool whose unread parts are NaN, scales among them."""
+    g, pages = _gen(seed), -(-S // ps)
+    pool = B * pages + 3
+    table = torch.randperm(pool, generator=g, device=DEV)[:B * pages].to(torch.int32).view(B, pages)
+    k, ks = _codes((pool, ps, Hkv, D), seed + 1), torch.exp2(torch.rand((pool, blocks, Hkv), generator=g, device=DEV) * 2 - 8.5)
+    v, vs = _codes((pool, ps, Hkv, Dv), seed + 2), torch.exp2(torch.rand((pool, blocks, Hkv), generator=g, device=DEV) * 2 - 8.5)
+    if shared:
+        v, vs = k[..., :Dv], ks
+    last = torch.randint(S // 2, S, (B, 1), generator=g, device=DEV)
+    qpos = (last - T + 1 + torch.arange(T, device=DEV)).clamp(min=0).to(torch.int32)
+    idx = torch.stack([torch.stack([torch.randperm(S, generator=g, device=DEV)[:K] if K <= S else
+                                    torch.randint(0, S, (K,), generator=g, device=DEV) for _ in range(T)]) for _ in range(B)])
+    idx = torch.where(torch.rand(idx.shape, generator=g, device=DEV) < 0.05, -1, idx).to(torch.int32)
+    # entries that no row sees, and scales of blocks without one that is seen, are NaN
+    used = torch.zeros((pool, ps), dtype=torch.bool, device=DEV)
+    for b in range(B):
+        seen = idx[b][(idx[b] >= 0) & (idx[b] <= qpos[b][:, None])].long()
+        used[table[b].long()[seen // ps], seen % ps] = True
+    free = ~used.view(pool, blocks, -1).any(-1)
+    k.view(torch.uint8)[~used] = 0x7f
+    ks[free] = math.nan
+    if not shared:
+        v.view(torch.uint8)[~used] = 0x7f
+        vs[free] = math.nan
+    q = _randn((B, T, Hq, D), seed + 3, dtype, 1.5 * spread)
+    return dict(q=q, k=k, v=v, indices=idx.contiguous(), page_table=table, k_scales=ks, v_scales=vs, query_positions=qpos,
+                scale=D ** -0.5, **more)
+
+
+def _attention_check(c, what=""):
+    out, lse = tk.sparse_attention(**c, return_lse=True)
+    clean = {n: torch.nan_to_num(c[n].float(), nan=0.0) for n in ("k_scales", "v_scales")}
+    k, v = (torch.where(torch.isnan(c[n].float()), 0.0, c[n].float()).to(E4M3) for n in ("k", "v"))
+    want = C.attention(c["q"], k, v, clean["k_scales"], clean["v_scales"], c["indices"], c.get("page_table"),
+                       c.get("query_positions"), c["scale"], c.get("softcap", 0.0), c.get("slopes"), c.get("first"))
+    R.assert_near(lse, want[2], want[3], what + " lse")
+    R.assert_near(out, want[0], want[1], what + " out")
+    return out, lse
+
+
+ATTEND = [
+    # B, T, Hq, Hkv, D, Dv, K, S, page_size, blocks, dtype
+    (1, 1, 8, 1, 128, 128, 128, 300, 64, 1, BF16),
+    (1, 1, 1, 1, 64, 64, 1, 5, 16, 1, BF16),
+    (2, 1, 32, 4, 128, 128, 512, 1000, 64, 4, BF16),
+    (2, 1, 32, 4, 128, 128, 512, 1000, 64, 4, FP16),
+    (3, 2, 15, 5, 96, 64, 129, 400, 17, 17, FP16),
+    (3, 2, 14, 2, 80, 144, 127, 400, 51, 3, BF16),
+    (1, 3, 24, 2, 16, 16, 300, 400, 1, 1, BF16),  # 12 heads
+    (1, 3, 32, 2, 128, 128, 300, 400, 64, 1, FP16),
+    (2, 1, 20, 1, 256, 192, 200, 333, 48, 6, BF16),
+    (2, 1, 64, 2, 192, 256, 260, 333, 48, 6, FP16),
+    (1, 2, 64, 1, 256, 256, 270, 500, 64, 64, BF16),
+    (1, 2, 50, 1, 128, 80, 270, 500, 64, 2, FP16),  # two tiles of heads in fp16
+    (1, 1, 150, 1, 64, 64, 200, 500, 64, 1, BF16),  # three tiles of heads
+    (1, 1, 8, 1, 128, 128, 2048, 5000, 64, 1, BF16),  # a cluster of eight
+    (1, 1, 64, 1, 128, 128, 1000, 5000, 64, 1, BF16),
+    (5, 1, 40, 1, 64, 240, 700, 900, 256, 2, FP16),
+    (2, 2, 4, 4, 32, 32, 6, 4, 4, 2, BF16),  # more entries than positions: listed twice
+    (170, 2, 8, 1, 64, 64, 130, 140, 16, 1, BF16),  # more works than places
+]
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,Dv,K,S,ps,blocks,dtype", ATTEND)
+def test_attention(B, T, Hq, Hkv, D, Dv, K, S, ps, blocks, dtype):
+    _attention_check(_attend(B, T, Hq, Hkv, D, Dv, K, S, ps, blocks, dtype, seed=K))
+
+
+@pytest.mark.parametrize("heads,D,Dv,dtype", [(8, 128, 128, BF16), (64, 256, 192, BF16), (16, 256, 256, FP16), (128, 128, 64, BF16),
+                                              (30, 144, 48, FP16)])
+def test_attention_shared_entries(heads, D, Dv, dtype):
+    """Values that are the first elements of the keys."""
+    _attention_check(_attend(2, 3, heads, 1, D, Dv, 333, 600, 64, 64, dtype, seed=heads, shared=True))
+
+
+@pytest.mark.parametrize("heads,dtype", [(8, BF16), (16, FP16), (40, BF16)])
+@pytest.mark.parametrize("cap", [0.0, 1e-3, 5.0, 30.0])
+@pytest.mark.parametrize("bias", [False, True])
+def test_attention_cap_bias_documents(heads, dtype, cap, bias):
+    c = _attend(2, 2, heads, 1, 64, 64, 300, 500, 32, 2, dtype, seed=5, softcap=cap, spread=3.0)
+    if bias:
+        c["slopes"] = _randn((heads,), 6, FP32, 0.05)
+    c["first"] = (c["query_positions"] * 0.3).to(torch.int32)
+    c["first"][0, 1] = 2 ** 31 - 1  # a row that sees nothing
+    c["first"][1, 0] = -5
+    out, lse = _attention_check(c)
+    assert (out[0, 1] == 0).all() and torch.isneginf(lse[0, 1]).all()
+
+
+def test_attention_that_sees_nothing():
+    """No entry, no index, no page, pages outside the cache and the table."""
+    c = _attend(2, 1, 8, 2, 64, 64, 40, 100, 16, 1, BF16)
+    for change in (dict(indices=torch.full_like(c["indices"], -1)), dict(indices=c["indices"][..., :0].contiguous()),
+                   dict(page_table=torch.full_like(c["page_table"], -1)), dict(page_table=torch.full_like(c["page_table"], 2 ** 31 - 1)),
+                   dict(page_table=c["page_table"][:, :0]), dict(query_positions=torch.full_like(c["query_positions"], -1)),
+                   dict(k=c["k"][:0], v=c["v"][:0], k_scales=c["k_scales"][:0], v_scales=c["v_scales"][:0])):
+        out, lse = tk.sparse_attention(**{**c, **change}, return_lse=True)
+        assert (out == 0).all() and torch.isneginf(lse).all(), change.keys()
+    assert tk.sparse_attention(**{**c, "q": c["q"][:0], "indices": c["indices"][:0], "page_table": c["page_table"][:0],
+                                  "query_positions": c["query_positions"][:0]}).shape == (0, 1, 8, 64)
+
+
+def test_attention_slots_and_strides():
+    """Slots instead of positions; caches that are parts of one, queries that are not aligned, a shared page table."""
+    H, D, ps, pages, K = 2, 64, 16, 20, 200
+    both = _codes((pages, 2, ps, H, D), 1)
+    ks, vs = _scales((pages, 4, H), 2), _scales((pages, 4, H), 3)
+    idx = torch.randint(-1, pages * ps, (2, 3, K), generator=_gen(4), device=DEV).to(torch.int32)
+    joint = _randn((2, 3, 8 * D + 9), 5, FP16)
+    q = joint[..., 3:3 + 8 * D].unflatten(-1, (8, D))
+    c = dict(q=q, k=both[:, 0], v=both[:, 1], indices=idx, k_scales=ks, v_scales=vs, scale=0.2)
+    one = _attention_check(c, "slots")
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).expand(2, pages)
+    two = _attention_check({**c, "page_table": table}, "shared table")
+    assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+    out = torch.empty((2, 3, 8, D), dtype=FP16, device=DEV)
+    assert tk.sparse_attention(**c, out=out) is out and torch.equal(out, one[0])
+
+
+@pytest.mark.parametrize("heads,dtype", [(8, BF16), (8, FP16), (16, BF16), (32, FP16), (64, BF16)])
+def test_attention_whose_logits_grow(heads, dtype):
+    """Every tile's logits above those of the one before, by little and by much: the references move each time. Then
+    one entry far above a flat rest, which the smallest weights carry."""
+    D, K, ps = 64, 900, 16
+    c = _attend(1, 1, heads, 1, D, D, K, K, ps, 1, dtype, seed=7)
+    c["k"], c["v"] = _codes(c["k"].shape, 1), _codes(c["v"].shape, 2)
+    c["k_scales"], c["v_scales"] = _scales(c["k_scales"].shape, 3), _scales(c["v_scales"].shape, 4)
+    c["indices"] = torch.arange(K, dtype=torch.int32, device=DEV).view(1, 1, K)
+    c["query_positions"] = _ints([[K]])
+    c["slopes"] = torch.linspace(0.0005, 0.5, heads, device=DEV)
+    _attention_check(c, "growing")
+    c["slopes"] = -c["slopes"]
+    _attention_check(c, "falling")
+    del c["slopes"]
+    for at in (0, 500, K - 1):
+        flat = c["k"].clone()
+        flat[...] = 0.0
+        page, place = int(c["page_table"][0, at // ps]), at % ps
+        c["q"][..., 0] = 3.0
+        flat[page, place, 0, 0] = 448.0
+        for logit in (5.0, 9.0, 12.0):
+            units = torch.full_like(c["k_scales"], logit / (448.0 * 3.0 * c["scale"]))
+            _attention_check({**c, "k": flat, "k_scales": units}, f"one above the rest by {logit}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_attention_scales_far_apart(dtype):
+    """Scales of 0, of the least size, and of sizes 2^40 apart, those of the keys and of the values."""
+    c = _attend(2, 1, 8, 1, 64, 64, 400, 400, 16, 2, dtype, seed=8)
+    c["k"], c["v"] = _codes(c["k"].shape, 1), _codes(c["v"].shape, 2)
+    base = _scales(c["k_scales"].shape, 3)
+    for far in (0.0, 2.0 ** -126, 2.0 ** -40, 2.0 ** 30):
+        odd = base.clone()
+        odd[::3] = far
+        c["k_scales"], c["v_scales"] = base, odd
+        _attention_check(c, f"values {far}")
+        c["k_scales"], c["v_scales"] = (odd if far < 1.0 else base), base
+        _attention_check(c, f"keys {far}")
+    c["v_scales"] = torch.zeros_like(base)
+    assert (_attention_check(c, "no values")[0] == 0).all()
+
+
+def test_attention_what_is_not_finite():
+    """A query's NaN or infinity makes NaN of its head, an entry's NaN of what it enters."""
+    c = _attend(2, 1, 16, 2, 64, 64, 300, 400, 16, 2, BF16, seed=9)
+    c["k"], c["v"] = _codes(c["k"].shape, 1), _codes(c["v"].shape, 2)
+    c["k_scales"], c["v_scales"] = _scales(c["k_scales"].shape, 3), _scales(c["v_scales"].shape, 4)
+    good, lse = _attention_check(c)
+    q = c["q"].clone()
+    q[0, 0, 3, 5], q[1, 0, 9, 0] = math.nan, math.inf
+    out, got = tk.sparse_attention(**{**c, "q": q}, return_lse=True)
+    for b, h in ((0, 3), (1, 9)):
+        assert torch.isnan(out[b, 0, h]).all() and torch.isnan(got[b, 0, h])
+        out[b, 0, h], got[b, 0, h] = good[b, 0, h], lse[b, 0, h]
+    assert torch.equal(out, good) and torch.equal(got, lse)
+    seen = c["indices"][0, 0][(c["indices"][0, 0] >= 0) & (c["indices"][0, 0] <= c["query_positions"][0, 0])][-1].item()
+    page, place = int(c["page_table"][0, seen // 16]), seen % 16
+    v = c["v"].clone()
+    v[page, place, 1, 7] = math.nan
+    out, got = tk.sparse_attention(**{**c, "v": v}, return_lse=True)
+    assert torch.isnan(out[0, 0, 8:, 7]).all() and torch.isnan(out).sum() == 8 and torch.equal(got, lse)
+    k = c["k"].clone()
+    k[page, place, 0, 1] = math.nan
+    out, got = tk.sparse_attention(**{**c, "k": k}, return_lse=True)
+    assert torch.isnan(out[0, 0, :8]).all() and torch.isnan(got[0, 0, :8]).all()
+    assert torch.equal(out[0, 0, 8:], good[0, 0, 8:]) and torch.equal(out[1], good[1])
+
+
+def test_attention_far_entries():
+    """Entries whose offsets pass 2^32."""
+    pages, ps, H, D = 70, 64, 1, 128
+    wide = torch.zeros(2 ** 32 + 2 ** 29, dtype=torch.uint8, device=DEV).view(E4M3)
+    k = wide.as_strided((pages, ps, H, D), (2 ** 26 - 2 ** 18, 2 ** 19 + 16, D, 1))
+    idx = torch.cat([torch.arange(65 * 64, 70 * 64), torch.arange(0, 70)]).to(torch.int32).to(DEV).view(1, 1, -1)
+    k[65:], k[:2] = _codes((5, ps, H, D), 1), _codes((2, ps, H, D), 2)
+    scales = _scales((pages, 1, H), 3)
+    c = dict(q=_randn((1, 1, 6, D), 4, BF16), k=k, v=k[..., :64], indices=idx, k_scales=scales, v_scales=scales, scale=0.1)
+    got = tk.sparse_attention(**c, return_lse=True)
+    near = torch.cat([idx[..., :320] - 65 * 64, idx[..., 320:] + 5 * 64], dim=-1).to(torch.int32).contiguous()
+    few = torch.cat([k[65:], k[:2]]).contiguous()
+    some = torch.cat([scales[65:], scales[:2]]).contiguous()
+    want = tk.sparse_attention(c["q"], few, few[..., :64], near, k_scales=some, v_scales=some, scale=0.1, return_lse=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_attention_in_a_graph_and_on_streams():
+    """Captured and replayed on other indices, and side by side with itself and with the 16-bit attention on two streams."""
+    c = _attend(20, 1, 32, 4, 128, 128, 600, 700, 64, 1, BF16, seed=11)
+    c["k"], c["v"] = _codes(c["k"].shape, 1), _codes(c["v"].shape, 2)
+    c["k_scales"], c["v_scales"] = _scales(c["k_scales"].shape, 3), _scales(c["v_scales"].shape, 4)
+    out = torch.empty((20, 1, 32, 128), dtype=BF16, device=DEV)
+    tk.sparse_attention(**c, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tk.sparse_attention(**c, out=out)
+    for seed in range(3):
+        c["indices"].copy_(torch.randint(-1, 700, c["indices"].shape, generator=_gen(seed), device=DEV))
+        c["q"].copy_(_randn(c["q"].shape, seed, BF16))
+        graph.replay()
+        assert torch.equal(out, tk.sparse_attention(**c))
+    wide = _attend(3, 1, 64, 1, 256, 192, 900, 1000, 64, 1, BF16, seed=12, shared=True)
+    k16 = _randn((300, 16, 4, 128), 2, BF16)
+    some = torch.randint(-1, 4800, (40, 1, 600), generator=_gen(3), device=DEV).to(torch.int32)
+    q16, wide16 = _randn((40, 1, 32, 128), 1, BF16), _randn((40, 1, 256, 128), 1, BF16)
+    calls = [lambda: tk.sparse_attention(**c), lambda: tk.sparse_attention(**wide),
+             lambda: tk.sparse_attention(q16, k16, k16, some), lambda: tk.sparse_attention(wide16, k16, k16, some)]
+    want = [call() for call in calls]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for turn in range(1, len(calls)):
+        got = [[], []]
+        for _ in range(10):
+            for i in range(len(calls)):
+                for side, stream in enumerate(streams):
+                    with torch.cuda.stream(stream):
+                        got[side].append(calls[(i + side * turn) % len(calls)]())
+        torch.cuda.synchronize()
+        for side in range(2):
+            for i, g in enumerate(got[side]):
+                assert torch.equal(g, want[(i + side * turn) % len(calls)])
