@@ -6,32 +6,36 @@
 // so queries and weights are split into E4M3 terms, x = u (t0 + t1 / 16 + t2 / 256),
 // each the rounded rest of those before. A term adds five bits (four and the
 // rest's sign): two hold 9, a bf16 query exactly; three hold 14, an fp16 query
-// exactly. Two terms of a weight round it to 2^-9 of itself, half a step of bf16's,
-// three are good to fp16's 2^-11, which it is rounded to first. A query's unit u is a
-// power of two, its head's own.
+// exactly. Two terms of a weight round it to 2^-9 of itself, half a step of bf16's;
+// three are good to fp16's 2^-11, which it is rounded to first. A query's unit u is
+// a power of two, its head's own.
 //
-// The tile. 128 entries are the rows of both products and their (term, head) pairs the
-// columns: S = K Q^T, and O^T += V^T P with P read along the entries. So few heads a key
-// head cost few columns instead of empty rows, each term has sums of its own, which are
-// joined with their factors in FP32 registers, and one thread has one entry: its scales,
-// mask and position are scalars, and every exponential is one thread's own.
+// The tile. 128 entries are the rows of both products and their (term, head) pairs
+// the columns: S = K Q^T, and O^T += V^T P with P read along the entries. So few
+// heads a key head cost few columns instead of empty rows, each term has sums of
+// its own, joined with their factors in FP32 registers, and one thread has one
+// entry: its scales, mask and position are scalars, and every exponential is one
+// thread's own.
 //
 // The scales. A key's scale multiplies its logit. A value's multiplies its weight
-// before that is split: w = 2^(z - r) s. The reference r of a head is moved, for all
-// threads at once, when a weight would pass E4M3's 448, and then to leave the largest
-// in (2^6, 2^7]: a weight's terms keep their digits down to 2^-14 / 2^6 of the largest
-// one's (three terms: 2^-18). The sum that divides adds the weights in FP32, unrounded
-// and without the values' scales. r is a whole number, so moving it is exact.
+// before that is split: w = 2^(z - r) s. The reference r of a head is moved, for
+// all threads at once, when a weight would pass E4M3's 448, and then to leave the
+// largest in (2^4, 2^5], so that it seldom moves again: terms end at steps of
+// 2^-13 / 2^4 of the largest weight (three terms: 2^-17 / 2^4), by which all of 2048
+// entries together lose half a step of the result at most. The sum that divides
+// adds the weights in FP32, unrounded and without the values' scales. r is a whole
+// number, so moving it is exact.
 //
-// The rest is as in sparse_attention.cu: entries gathered by 16-byte copies into rings
-// of keys and values, few rows shared by a cluster whose CTAs join through distributed
-// shared memory, CTAs that stay for several rows where there are many.
+// The rest is as in sparse_attention.cu: entries gathered by 16-byte copies into
+// rings of keys and values, few rows shared by a cluster whose CTAs join through
+// distributed shared memory, CTAs that stay for several rows where there are many.
 //
-// Warps: 4 softmax warps for each 16 heads (8: G = 8), one entry a thread; 8 that gather; one
-// thread each for S and for O; two that split the queries of the next row.
+// Warps: 4 softmax warps for each 16 heads (G = 8: for all 8), one entry a thread;
+// 4 or 8 that gather; one thread issues all products; 3 or 4 split queries ahead.
 #include <cuda_runtime.h>
 
 #include <cfloat>
+#include <cstddef>
 #include <cstdint>
 #include <type_traits>
 
@@ -45,25 +49,24 @@ namespace tki {
 namespace {
 
 constexpr int kEntries = 128;  // of a tile
-constexpr int kGather = 8, kQuery = 2;  // warps
 constexpr int kMaxStages = 6;
-constexpr int kBufs = 2;                  // buffers of scores in TMEM
+constexpr int kBufs = 2;  // buffers of scores in TMEM, of weights and queries in shared memory
 constexpr int kMaxNotes = kMaxStages + kBufs;  // see E4Params::notes
 constexpr float kNothing = -1073741824.0f;  // a reference below any logit in use; its negative for heads that are none
-constexpr float kLimit = 448.0f;
-constexpr float kLeast = 0x1p-60f;  // values' scales below count as this for the reference
+constexpr float kLogLimit = 8.8073549f;     // log2(448)
+constexpr float kLeast = 0x1p-60f;          // values' scales below count as this for the reference
 
 template <typename E, int G>
 struct Shape {
   static constexpr int terms = std::is_same<E, __nv_bfloat16>::value ? 2 : 3;
   static constexpr int set_heads = G < 16 ? G : 16;  // of one set of four softmax warps
   static constexpr int sets = G / set_heads;
-  static constexpr int rows = terms * G;              // (term, head) pairs
-  static constexpr int N = (rows + 15) / 16 * 16;     // columns; those past the rows come from whatever follows them
-  static constexpr int q_bufs = G <= 16 ? 2 : 1, p_bufs = G <= 16 ? 1 : 2;
-  static constexpr int softmax = 4 * sets;            // warps
-  static constexpr int mma = softmax + kGather, query = mma + 2;
-  static constexpr int threads = (query + kQuery) * 32;
+  static constexpr int rows = terms * G;           // (term, head) pairs
+  static constexpr int N = (rows + 15) / 16 * 16;  // columns; those past the rows hold nothing
+  static constexpr int p_bytes = N * kEntries;     // of a buffer of weights
+  static constexpr int softmax = 4 * sets, gather = G <= 32 ? 8 : 4, queries = G <= 16 ? 3 : 4;  // warps
+  static constexpr int mma = softmax + gather, query = mma + 1;
+  static constexpr int threads = (query + queries) * 32;
   static constexpr int per_sm = G <= 16 ? 2 : 1;
 };
 
@@ -71,12 +74,12 @@ struct E4Params {
   sparse_attention_args a;
   const float* k_scales;
   const float* v_scales;
-  int32_t block, blocks;     // entries of a block, blocks a page
-  int32_t heads, h_tiles;    // query heads per key head, tiles of G of them
-  uint32_t works;            // (row, key head, tile of heads)
+  int32_t block, blocks;   // entries of a block, blocks a page
+  int32_t heads, h_tiles;  // query heads per key head, tiles of G of them
+  uint32_t works;          // (row, key head, tile of heads)
   int32_t d_blocks, v_blocks, d_steps;  // 128-byte blocks of an entry, 32-byte steps of its keys
-  int32_t shared;            // v is a prefix of k's entries
-  int32_t page_shift, block_shift;  // log2, or -1
+  int32_t shared;                       // v is a prefix of k's entries
+  int32_t page_shift, block_shift;      // log2, or -1
   uint32_t pages, table_width;
   int32_t k_stages, v_stages, k_bytes, v_bytes;
   // What is noted of each entry (scales, distance, mask) outlives its keys' stage:
@@ -99,22 +102,23 @@ struct Notes {
 
 template <int G, int SETS, int HS>
 struct E4Shared {
-  float ref[G], factor[G], inverse[G];
-  float unit[4][G];  // of the queries, of the last four works
+  alignas(16) float nref[G];  // a head's reference, negative
+  alignas(16) float factor[G];
+  alignas(16) float inverse[G];
+  alignas(16) float unit[4][G];  // of the queries, of the last four works
   float most[SETS * 4][HS], sum[SETS * 4][HS];
   float head_ref[G], head_sum[G];  // for the other CTAs of a cluster
   uint64_t k_full[kMaxStages], v_full[kMaxStages], noted[kMaxNotes];
-  uint64_t q_full[2], q_empty[2], units[4];
+  uint64_t q_full[kBufs], q_empty[kBufs], units[4];
   // Of tile i at i % 8: scores there, weights there, products with v done.
   uint64_t s_full[8], p_full[8], pv_done[8];
-  uint64_t o_free;
-  uint64_t drained[2];
+  uint64_t drained;
   uint32_t tmem;
   uint32_t stop;
 };
 
 struct E4Work {
-  int g, heads, head0;
+  int g, heads, head0;  // key head; real heads, and the first one's query head
   int64_t row, b, t;
 };
 
@@ -129,6 +133,10 @@ __device__ __forceinline__ E4Work e4_work(const E4Params& p, uint32_t w) {
   r.head0 = r.g * p.heads + tile * G;
   r.row = row, r.b = b, r.t = row - b * static_cast<uint32_t>(p.a.T);
   return r;
+}
+
+__device__ __forceinline__ void put16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 // Among the 128 threads of a set: whether any of them says yes.
@@ -169,6 +177,20 @@ __device__ __forceinline__ float sum_lanes(float (&v)[HS], int lane) {
   return v[0];
 }
 
+// The two numbers of 32 bits of queries.
+template <typename E>
+struct Two;
+template <>
+struct Two<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 get(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+};
+template <>
+struct Two<__half> {
+  static __device__ __forceinline__ float2 get(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+};
+
 __device__ __forceinline__ uint32_t half_two(float x, float y) {
   const __half2 v = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -183,14 +205,19 @@ __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
   return r;
 }
-// 16 (x - y), exactly where x - y is what a term of x leaves.
+// 16 (x - y), exact where y is a term of x.
 __device__ __forceinline__ uint32_t rest16(uint32_t x, uint32_t y) {
   const __half2 a = *reinterpret_cast<const __half2*>(&x), b = *reinterpret_cast<const __half2*>(&y);
   const __half2 r = __hmul2(__hsub2(a, b), __float2half2_rn(16.0f));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ void put_byte(uint32_t at, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+
+// Descriptor of the weights: units of 16 (term, head) pairs, one behind the other, entry e
+// of a unit at byte e * 16 of it. Not swizzled: a thread writes whole units, its neighbours
+// the next ones.
+__device__ __forceinline__ uint64_t weights_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>((8 * 16) >> 4) << 16) |
+         (static_cast<uint64_t>((kEntries * 16) >> 4) << 32) | (1ull << 46);
 }
 
 // 1 / a sum of weights, zero where nothing is seen; and its logarithm with the reference.
@@ -216,17 +243,17 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
   const uint32_t base = smem_addr(smem);
   const uint32_t k_ring = base + p.k_at, v_ring = base + p.v_at, p_at = base + p.p_at;
   const int q_block = S::rows * 128, q_bytes = q_block * p.d_blocks;
+  constexpr int kSets = S::gather / 4;  // of gathering warps, which take tiles in turn
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.k_stages; ++i) mbar_init(&sh.k_full[i], p.shared ? 256 : 128);
+    for (int i = 0; i < p.k_stages; ++i) mbar_init(&sh.k_full[i], 128);
     for (int i = 0; i < p.v_stages; ++i) mbar_init(&sh.v_full[i], 128);
     for (int i = 0; i < p.notes; ++i) mbar_init(&sh.noted[i], 128 + 4);
-    for (int i = 0; i < 2; ++i) mbar_init(&sh.q_full[i], kQuery * 32), mbar_init(&sh.q_empty[i], 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.units[i], kQuery * 32);
+    for (int i = 0; i < kBufs; ++i) mbar_init(&sh.q_full[i], S::queries * 32), mbar_init(&sh.q_empty[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.units[i], S::queries * 32);
     for (int i = 0; i < 8; ++i)
       mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 128 * SETS), mbar_init(&sh.pv_done[i], 1);
-    mbar_init(&sh.o_free, 128 * SETS);
-    for (int i = 0; i < 2; ++i) mbar_init(&sh.drained[i], 1);
+    mbar_init(&sh.drained, 1);
     sh.stop = 0;
     fence_mbar_init();
   }
@@ -236,39 +263,28 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
   tc_fence_after();
   const uint32_t tmem_s = sh.tmem, tmem_o = tmem_s + kBufs * N;
   volatile uint32_t* stop = &sh.stop;
-  bool one = false;  // a thread that issues products
+  bool one = false;  // the thread that issues products
 
   if (warp >= S::softmax && warp < S::mma) {
-    // ---- gather ----
-    // Four warps fetch the tile's keys, 32 entries each, and note what belongs to
-    // them; four their values, or the second half of their blocks when shared.
-    const int w = warp - S::softmax, part = w & 3;
-    const bool second = w >= 4, values = second && !p.shared;
-    const int split = (p.d_blocks + 1) / 2;
-    const int c0 = second && p.shared ? split : 0;
-    const int c1 = values ? p.v_blocks : !second && p.shared ? split : p.d_blocks;
-    // 16-byte units of an entry: those that it has, and those that are read (a whole
-    // step of the keys' product, of the values those that it has)
-    const int units = (values ? a.Dv : a.D) / 16, read = values ? units : p.d_steps * 2;
-    const int64_t head_stride = values ? a.v_head_stride : a.k_head_stride;
-    const int64_t page_stride = values ? a.v_page_stride : a.k_page_stride;
-    const int64_t token_stride = values ? a.v_token_stride : a.k_token_stride;
-    uint64_t* full = values ? sh.v_full : sh.k_full;
-    uint64_t* used = values || p.shared ? sh.pv_done : sh.s_full;  // when a tile's stage is free
-    const int stages = values ? p.v_stages : p.k_stages, stage_bytes = values ? p.v_bytes : p.k_bytes;
+    // ---- gather: a warp has 32 entries of every tile of its set ----
+    const int w = warp - S::softmax, part = w & 3, turn = w >> 2;
+    // 16-byte units of an entry's keys: those that it has, and those that are read
+    const int k_units = a.D / 16, k_read = p.d_steps * 2, v_units = a.Dv / 16;
     const uint32_t unit16 = lane & 7, sub = lane >> 3;
-    const uint32_t at = (values ? v_ring : k_ring) + (part * 32 + sub) * 128;
+    const uint32_t at = (part * 32 + sub) * 128;
     const uint32_t even = (unit16 ^ sub) << 4, odd = (unit16 ^ (sub + 4)) << 4;
     const bool some = a.page_size > 0 && a.num_pages > 0;
+    // an empty cache has no address: nothing is read from the one it gets
+    const char* nowhere = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(a.q) & ~static_cast<uintptr_t>(15));
     bool ok = true;
-    int stage = 0, note = 0, n = 0;
+    int n = 0, k_stage = turn % p.k_stages, v_stage = p.shared ? 0 : turn % p.v_stages, note = turn;
     for (uint32_t w_at = first_w; w_at < p.works && ok; w_at += step_w, n += tiles) {
       const E4Work k = e4_work<G>(p, w_at);
       const int32_t* indices = a.indices + k.row * a.K;
       const int32_t* table = a.page_table != nullptr ? a.page_table + k.b * a.table_stride : nullptr;
       const int32_t last = a.query_positions != nullptr ? a.query_positions[k.row] : INT32_MAX;
       const int32_t first = a.first != nullptr ? max(a.first[k.row], 0) : 0;
-      // Each lane looks up one entry of a tile, its index two tiles ahead, its page id one.
+      // Each lane looks up one entry of a tile, its index two of the set's tiles ahead, its page id one.
       auto index_of = [&](int i) -> int32_t {
         const int64_t j = (static_cast<int64_t>(i) * cluster + rank) * kEntries + part * 32 + lane;
         return i < tiles && j < a.K && some ? indices[j] : -1;
@@ -282,114 +298,134 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         const uint32_t page = page_index(pos);
         return table == nullptr ? page : page < p.table_width ? static_cast<uint32_t>(table[page]) : 0xffffffffu;
       };
-      int32_t pos = index_of(0), pos1 = index_of(1);
+      const int i0 = (turn - n) & (kSets - 1);
+      int32_t pos = index_of(i0), pos1 = index_of(i0 + kSets);
       uint32_t page = page_of(pos);
-      // an empty cache has no address: nothing is read from the one it gets
-      const char* nowhere = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(a.q) & ~static_cast<uintptr_t>(15));
-      const char* mine = some ? static_cast<const char*>(values ? a.v : a.k) + k.g * head_stride + unit16 * 16 : nowhere;
-      for (int i = 0; i < tiles; ++i) {
-        const int32_t pos2 = index_of(i + 2);
+      const char* keys = some ? static_cast<const char*>(a.k) + k.g * a.k_head_stride + unit16 * 16 : nowhere;
+      const char* values = some ? static_cast<const char*>(a.v) + k.g * a.v_head_stride + unit16 * 16 : nowhere;
+      for (int i = i0; i < tiles; i += kSets) {
+        const int32_t pos2 = index_of(i + 2 * kSets);
         const uint32_t page1 = page_of(pos1);
         const bool seen = page < p.pages;
         const uint32_t place = static_cast<uint32_t>(pos) - page_index(pos) * static_cast<uint32_t>(a.page_size);
-        const int64_t entry = seen ? page * page_stride + place * token_stride : 0;
         const uint32_t bits = __ballot_sync(0xffffffffu, seen);
-        const int before = n + i - stages;
+        // 8 lanes fetch 128 bytes of an entry; step j has entries 4 j + lane / 8. What is not
+        // seen is zeros; of a last block that is not full, the units up to `read`.
+        auto fetch = [&](uint32_t dst, const char* from, int64_t entry, int blocks, int units, int read) {
+          const char* rows[8];
+          uint32_t bytes[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            rows[j] = from + __shfl_sync(0xffffffffu, entry, 4 * j + sub);
+            bytes[j] = (bits >> (4 * j + sub)) & 1 ? 16 : 0;
+          }
+#pragma unroll
+          for (int c = 0; c < SPARSE_ATTENTION_MAX_D / 128; ++c) {
+            if (c >= blocks) continue;
+            const int u = c * 8 + static_cast<int>(unit16);
+            if (c * 8 + 8 <= units) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                copy_bytes(dst + c * (kEntries * 128) + j * 512 + (j & 1 ? odd : even), rows[j] + c * 128, bytes[j]);
+            } else if (u < read) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                copy_bytes(dst + c * (kEntries * 128) + j * 512 + (j & 1 ? odd : even), u < units ? rows[j] + c * 128 : from,
+                           u < units ? bytes[j] : 0);
+            }
+          }
+        };
+        int before = n + i - p.k_stages;
+        uint64_t* used = p.shared ? sh.pv_done : sh.s_full;  // when a stage of keys is free
         ok = before < 0 || wait_or_stop(&used[before & 7], (before >> 3) & 1, stop);
         if (!ok) break;
-        const uint32_t dst = at + stage * stage_bytes;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const char* from = mine + __shfl_sync(0xffffffffu, entry, 4 * j + sub);
-          const bool there = (bits >> (4 * j + sub)) & 1;  // what is not seen is zeros
-          for (int c = c0; c < c1; ++c) {
-            const int u = c * 8 + static_cast<int>(unit16);
-            if (u < read)
-              copy_bytes(dst + c * (kEntries * 128) + j * 512 + (j & 1 ? odd : even), u < units ? from + c * 128 : mine,
-                         there && u < units ? 16 : 0);
-          }
-        }
-        copy_arrive(&full[stage]);
-        if (!second) {
-          Notes& notes = *reinterpret_cast<Notes*>(smem + p.note_at + note * p.note_bytes);
-          const int e = part * 32 + lane;
-          const uint32_t block = p.block_shift >= 0 ? place >> p.block_shift : place / static_cast<uint32_t>(p.block);
-          const int64_t unit = seen ? (static_cast<int64_t>(page) * p.blocks + block) * a.Hkv + k.g : 0;
-          copy4(smem_addr(&notes.ks[e]), some ? reinterpret_cast<const char*>(p.k_scales + unit) : nowhere, seen);
-          copy4(smem_addr(&notes.vs[e]), some ? reinterpret_cast<const char*>(p.v_scales + unit) : nowhere, seen);
-          copy_arrive(&sh.noted[note]);
-          if (a.slopes != nullptr) notes.away[e] = static_cast<float>(seen ? pos - last : 0);
-          if (lane == 0) notes.seen[part] = bits;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.noted[note]);
+        fetch(k_ring + k_stage * p.k_bytes + at, keys, seen ? page * a.k_page_stride + place * a.k_token_stride : 0,
+              p.d_blocks, k_units, k_read);
+        Notes& notes = *reinterpret_cast<Notes*>(smem + p.note_at + note * p.note_bytes);
+        const int e = part * 32 + lane;
+        const uint32_t block = p.block_shift >= 0 ? place >> p.block_shift : place / static_cast<uint32_t>(p.block);
+        const int64_t unit = seen ? (static_cast<int64_t>(page) * p.blocks + block) * a.Hkv + k.g : 0;
+        copy4(smem_addr(&notes.ks[e]), some ? reinterpret_cast<const char*>(p.k_scales + unit) : nowhere, seen);
+        copy4(smem_addr(&notes.vs[e]), some ? reinterpret_cast<const char*>(p.v_scales + unit) : nowhere, seen);
+        copy_arrive(&sh.k_full[k_stage]);
+        copy_arrive(&sh.noted[note]);
+        if (a.slopes != nullptr) notes.away[e] = static_cast<float>(seen ? pos - last : 0);
+        if (lane == 0) notes.seen[part] = bits;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.noted[note]);
+        if (!p.shared) {
+          before = n + i - p.v_stages;
+          ok = before < 0 || wait_or_stop(&sh.pv_done[before & 7], (before >> 3) & 1, stop);
+          if (!ok) break;
+          fetch(v_ring + v_stage * p.v_bytes + at, values, seen ? page * a.v_page_stride + place * a.v_token_stride : 0,
+                p.v_blocks, v_units, v_units);
+          copy_arrive(&sh.v_full[v_stage]);
+          v_stage += kSets;
+          while (v_stage >= p.v_stages) v_stage -= p.v_stages;
         }
         pos = pos1, pos1 = pos2, page = page1;
-        if (++stage == stages) stage = 0;
-        if (++note == p.notes) note = 0;
+        k_stage += kSets, note += kSets;
+        while (k_stage >= p.k_stages) k_stage -= p.k_stages;
+        if (note >= p.notes) note -= p.notes;
       }
     }
     copy_commit();
     copy_wait<0>();
   } else if (warp == S::mma) {
-    // ---- S = K Q^T, by one thread ----
+    // ---- products, all by one thread: S of the next tile, then O^T of this one ----
+    // So scores that are there say that the weights of the tile two before were used, and
+    // a work's first weights that the sums of the one before have been read.
     one = elect_one();
     if (tiles > 0 && one) {
-      const uint32_t desc = mma_desc(0, N);
+      const uint32_t s_desc = mma_desc(0, N), o_desc = mma_desc(0, N, true, true);
       const uint64_t q_desc = operand_desc(base), k_desc = operand_desc(k_ring);
-      int stage = 0, turn_of = 0, n = 0, nw = 0;
+      const uint64_t v_desc = operand_desc(p.shared ? k_ring : v_ring), p_desc = weights_desc(p_at);
+      const int v_stages = p.shared ? p.k_stages : p.v_stages, v_bytes = p.shared ? p.k_bytes : p.v_bytes;
+      const int last = static_cast<int>((p.works - first_w + step_w - 1) / step_w) * tiles;  // first_w < works
+      int k_stage = 0, k_turn = 0, v_stage = 0, v_turn = 0;
+      int s_work = 0, s_tile = 0, o_tile = 0;
       bool ok = true;
-      for (uint32_t w_at = first_w; w_at < p.works && ok; w_at += step_w, ++nw) {
-        const int qb = nw % S::q_bufs;
+      auto scores = [&](int n) {
+        const int qb = s_work & 1;
+        if (s_tile == 0) ok = wait_or_stop_one(&sh.q_full[qb], (s_work >> 1) & 1, stop);
+        ok = ok && wait_or_stop_one(&sh.k_full[k_stage], k_turn, stop);
+        if (!ok) return;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t kd = k_desc + static_cast<uint32_t>(k_stage * p.k_bytes >> 4);
         const uint64_t qd = q_desc + static_cast<uint32_t>(qb * q_bytes >> 4);
-        ok = wait_or_stop_one(&sh.q_full[qb], (nw / S::q_bufs) & 1, stop);
-        for (int i = 0; i < tiles && ok; ++i, ++n) {
-          const int before = n - kBufs;  // whose scores were there
-          ok = (before < 0 || wait_or_stop_one(&sh.p_full[before & 7], (before >> 3) & 1, stop)) &&
-               wait_or_stop_one(&sh.k_full[stage], turn_of, stop);
-          if (!ok) break;
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const uint64_t kd = k_desc + static_cast<uint32_t>(stage * p.k_bytes >> 4);
-          const uint32_t to = tmem_s + (n & 1) * N;
-          for (int j = 0; j < p.d_steps; ++j) {
-            const uint32_t c = j >> 2, in = (j & 3) * 2;
-            mma_f8(to, kd + (c * (kEntries * 128 >> 4) + in), qd + (c * (S::rows * 128 >> 4) + in), desc, j > 0);
-          }
-          mma_commit(&sh.s_full[n & 7]);
-          if (++stage == p.k_stages) stage = 0, turn_of ^= 1;
+        const uint32_t to = tmem_s + (n & 1) * N;
+        for (int j = 0; j < p.d_steps; ++j) {
+          const uint32_t c = j >> 2, in = (j & 3) * 2;
+          mma_f8(to, kd + (c * (kEntries * 128 >> 4) + in), qd + (c * (S::rows * 128 >> 4) + in), s_desc, j > 0);
         }
-        if (ok) mma_commit(&sh.q_empty[qb]);
-      }
-    }
-    __syncwarp();
-  } else if (warp == S::mma + 1) {
-    // ---- O^T += V^T P, by another ----
-    one = elect_one();
-    if (tiles > 0 && one) {
-      const uint32_t desc = mma_desc(0, N, false, true);
-      const uint64_t v_desc = operand_desc(p.shared ? k_ring : v_ring), p_desc = operand_desc(p_at);
-      const int stages = p.shared ? p.k_stages : p.v_stages, stage_bytes = p.shared ? p.k_bytes : p.v_bytes;
-      uint64_t* full = p.shared ? sh.k_full : sh.v_full;
-      int stage = 0, turn_of = 0, n = 0, nw = 0;
-      bool ok = true;
-      for (uint32_t w_at = first_w; w_at < p.works && ok; w_at += step_w, ++nw) {
-        if (nw > 0) ok = wait_or_stop_one(&sh.o_free, (nw - 1) & 1, stop);
-        for (int i = 0; i < tiles && ok; ++i, ++n) {
-          ok = wait_or_stop_one(&full[stage], turn_of, stop);
+        mma_commit(&sh.s_full[n & 7]);
+        if (++k_stage == p.k_stages) k_stage = 0, k_turn ^= 1;
+        if (++s_tile == tiles) {
+          mma_commit(&sh.q_empty[qb]);
+          s_tile = 0, ++s_work;
+        }
+      };
+      scores(0);
+      for (int n = 0; n < last && ok; ++n) {
+        if (n + 1 < last) scores(n + 1);
+        if (!p.shared) {
+          ok = ok && wait_or_stop_one(&sh.v_full[v_stage], v_turn, stop);
           fence_proxy_async_smem();
-          ok = ok && wait_or_stop_one(&sh.p_full[n & 7], (n >> 3) & 1, stop);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t vd = v_desc + static_cast<uint32_t>(stage * stage_bytes >> 4);
-          const uint64_t pd = p_desc + static_cast<uint32_t>((n % S::p_bufs) * (S::rows * 128) >> 4);
-          for (int m = 0; m < p.v_blocks; ++m)
+        }
+        ok = ok && wait_or_stop_one(&sh.p_full[n & 7], (n >> 3) & 1, stop);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = v_desc + static_cast<uint32_t>(v_stage * v_bytes >> 4);
+        const uint64_t pd = p_desc + static_cast<uint32_t>((n & 1) * S::p_bytes >> 4);
+        for (int m = 0; m < p.v_blocks; ++m)
 #pragma unroll
-            for (int j = 0; j < kEntries / 32; ++j)
-              mma_f8(tmem_o + m * N, vd + static_cast<uint32_t>((m * (kEntries * 128) + j * (32 * 128)) >> 4),
-                     pd + static_cast<uint32_t>(j * 2), desc, i + j > 0);
-          mma_commit(&sh.pv_done[n & 7]);
-          if (++stage == stages) stage = 0, turn_of ^= 1;
-        }
+          for (int j = 0; j < kEntries / 32; ++j)
+            mma_f8(tmem_o + m * N, vd + static_cast<uint32_t>((m * (kEntries * 128) + j * (32 * 128)) >> 4),
+                   pd + static_cast<uint32_t>(j * (32 * 16) >> 4), o_desc, o_tile + j > 0);
+        mma_commit(&sh.pv_done[n & 7]);
+        if (++v_stage == v_stages) v_stage = 0, v_turn ^= 1;
+        if (++o_tile == tiles) o_tile = 0;
       }
     }
     __syncwarp();
@@ -397,62 +433,61 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
     // ---- queries: a power of two for each head and terms in units of it ----
     const int who = warp - S::query;
     int nw = 0;
-    bool ok = true;
     for (uint32_t w_at = first_w; tiles > 0 && w_at < p.works; w_at += step_w, ++nw) {
       const E4Work k = e4_work<G>(p, w_at);
-      const int qb = nw % S::q_bufs;
-      if (nw >= S::q_bufs) ok = wait_or_stop(&sh.q_empty[qb], (nw / S::q_bufs - 1) & 1, stop);
-      if (!ok) break;
+      const int qb = nw & 1;
+      if (nw >= kBufs && !wait_or_stop(&sh.q_empty[qb], ((nw >> 1) - 1) & 1, stop)) break;
       unsigned char* to = smem + qb * q_bytes;
       const E* q = static_cast<const E*>(a.q) + k.b * a.q_seq_stride + k.t * a.q_token_stride + k.head0 * a.q_head_stride;
       constexpr int kAhead = 4;
-      for (int h0 = who; h0 < G; h0 += kQuery * kAhead) {
-        alignas(16) E e[kAhead][8];
+      for (int h0 = who; h0 < G; h0 += S::queries * kAhead) {
+        uint4 raw[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const int h = h0 + u * kQuery;
+          const int h = h0 + u * S::queries;
           const E* from = q + h * a.q_head_stride + lane * 8;
-          const bool real = h < k.heads && lane * 8 < a.D;  // D is a multiple of 16
-          if (real && p.q_vector) {
-            *reinterpret_cast<uint4*>(e[u]) = *reinterpret_cast<const uint4*>(from);
+          raw[u] = make_uint4(0, 0, 0, 0);
+          if (h >= k.heads || lane * 8 >= a.D) continue;  // D is a multiple of 16
+          if (p.q_vector) {
+            raw[u] = *reinterpret_cast<const uint4*>(from);
           } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[u][j] = real ? from[j] : E(0.0f);
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(from);
+            auto two = [&](int j) { return e[j] | static_cast<uint32_t>(e[j + 1]) << 16; };
+            raw[u] = make_uint4(two(0), two(2), two(4), two(6));
           }
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const int h = h0 + u * kQuery;
+          const int h = h0 + u * S::queries;
           if (h >= G) continue;
-          float x[8];
+          const uint32_t in[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
           uint32_t most = 0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            x[j] = static_cast<float>(e[u][j]);
-            most = max(most, __float_as_uint(x[j]) & 0x7fffffffu);
-          }
-          most = __reduce_max_sync(0xffffffffu, most);
+          for (int j = 0; j < 4; ++j) most = __vmaxu2(most, in[j] & 0x7fff7fffu);
+          most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+          const uint32_t top = __float_as_uint(Two<E>::get(most).x);
           // the largest in [2^7, 2^8) units; a query that is not finite is NaN throughout
-          const bool bad = most >= 0x7f800000u;
-          const int exponent = max(static_cast<int>(most >> 23) - 127 - 7, -120);
+          const bool bad = top >= 0x7f800000u;
+          const int exponent = max(static_cast<int>(top >> 23) - 127 - 7, -120);
           const float over = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
           if (lane == 0) sh.unit[nw & 3][h] = h < k.heads ? __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23) : 0.0f;
+          uint32_t x[4];  // in fp16: exact from 2^-14 units on, below the last term's steps
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = bad ? __int_as_float(0x7fc00000) : x[j] * over;
-          if (lane * 8 < p.d_blocks * 128) {
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = Two<E>::get(in[j]);
+            x[j] = bad ? 0x7fff7fffu : half_two(y.x * over, y.y * over);
+          }
+          if (lane * 8 >= p.d_blocks * 128) continue;
 #pragma unroll
-            for (int t = 0; t < TERMS; ++t) {
-              uint32_t two[4];
+          for (int t = 0; t < TERMS; ++t) {
+            uint32_t two[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                two[j] = e4m3_two(x[2 * j], x[2 * j + 1]);
-                const float2 y = e4m3_both(two[j]);
-                x[2 * j] = (x[2 * j] - y.x) * 16.0f, x[2 * j + 1] = (x[2 * j + 1] - y.y) * 16.0f;
-              }
-              const int row = t * G + h;
-              *reinterpret_cast<uint2*>(to + (lane >> 4) * q_block + swizzled(row, (lane >> 1) & 7) + (lane & 1) * 8) =
-                  make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
+            for (int j = 0; j < 4; ++j) {
+              two[j] = e4m3_of_half2(x[j]);
+              if (t + 1 < TERMS) x[j] = rest16(x[j], half2_of_e4m3(two[j]));
             }
+            *reinterpret_cast<uint2*>(to + (lane >> 4) * q_block + swizzled(t * G + h, (lane >> 1) & 7) + (lane & 1) * 8) =
+                make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
           }
         }
       }
@@ -464,18 +499,19 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
     // ---- softmax: thread `e` of a set has entry e of each tile, for the set's heads ----
     const int set = warp >> 2, e = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t p_mine = p_at + e;  // of row 0, whose 16-byte units stand in order
-    float* ref = sh.ref + set * HS;
+    const uint32_t p_mine = p_at + e * 16 + (HS == 16 ? set * (kEntries * 16) : 0);
+    float* nref = sh.nref + set * HS;
+    const uint64_t* held = reinterpret_cast<const uint64_t*>(nref);
     int n = 0, nw = 0, note = 0;
     for (uint32_t w_at = first_w; w_at < p.works; w_at += step_w, ++nw, n += tiles) {
       const E4Work k = e4_work<G>(p, w_at);
       const int heads = min(max(k.heads - set * HS, 0), HS);
-      const float* unit = sh.unit[nw & 3] + set * HS;
+      const uint64_t* unit = reinterpret_cast<const uint64_t*>(sh.unit[nw & 3] + set * HS);
       const float* slopes = a.slopes != nullptr ? a.slopes + k.head0 + set * HS : nullptr;
-      float sum[HS];
+      uint64_t sum[HS / 2];  // of the weights of two heads
 #pragma unroll
-      for (int h = 0; h < HS; ++h) sum[h] = 0.0f;
-      if (e < HS) ref[e] = e < heads ? kNothing : -kNothing;
+      for (int h = 0; h < HS / 2; ++h) sum[h] = 0;
+      if (e < HS) nref[e] = e < heads ? -kNothing : kNothing;
       bool ok = true;
       if (tiles > 0) ok = wait_or_stop(&sh.units[nw & 3], (nw >> 2) & 1, stop);
       set_sync(set);
@@ -487,62 +523,78 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         ok = wait_or_stop(&sh.noted[note], (at / p.notes) & 1, stop) && ok;
         const float ks = notes.ks[e], vs = notes.vs[e];
         const bool seen = (notes.seen[e >> 5] >> (e & 31)) & 1;
-        const float away = a.slopes != nullptr ? notes.away[e] : 0.0f;
         ok = wait_or_stop(&sh.s_full[at & 7], (at >> 3) & 1, stop) && ok;
         tc_fence_after();
-        float z[HS];
-        {
-          uint32_t v[TERMS][HS];
-          const uint32_t s_at = tmem_s + (at & 1) * N + lanes + set * HS;
+        // Logits in units of log 2, two heads at a time, less the reference or as they are.
+        uint64_t z[HS / 2];
+        auto logits = [&](bool less) {
+          {
+            uint32_t v[TERMS][HS];
+            const uint32_t s_at = tmem_s + (at & 1) * N + lanes + set * HS;
 #pragma unroll
-          for (int t = 0; t < TERMS; ++t) tmem_ld(v[t], s_at + t * G);
+            for (int t = 0; t < TERMS; ++t) tmem_ld(v[t], s_at + t * G);
 #pragma unroll
-          for (int t = 0; t < TERMS; ++t) tmem_wait_ld(v[t]);
+            for (int t = 0; t < TERMS; ++t) tmem_wait_ld(v[t]);
+            auto of = [&](int t, int h) { return pair(__uint_as_float(v[t][2 * h]), __uint_as_float(v[t][2 * h + 1])); };
 #pragma unroll
-          for (int h = 0; h < HS; ++h) {
-            float x = __uint_as_float(v[TERMS - 1][h]);
+            for (int h = 0; h < HS / 2; ++h) {
+              z[h] = of(TERMS - 1, h);
 #pragma unroll
-            for (int t = TERMS - 2; t >= 0; --t) x = fmaf(x, 0x1p-4f, __uint_as_float(v[t][h]));
-            z[h] = x;
-          }
-        }
-        if (a.softcap > 0.0f) {
-#pragma unroll
-          for (int h = 0; h < HS; h += 2) {
-            const uint64_t x = mul2(pair(z[h], z[h + 1]), mul2(twice(ks), pair(unit[h], unit[h + 1])));
-            const uint64_t u = mul2(x, twice(p.scale_over_cap));
-            const float2 in = both(u), low = capped_low(x, u, p.scale_log2e);
-            z[h] = low.x, z[h + 1] = low.y;
-            if (__any_sync(0xffffffffu, !(fabsf(in.x) < kBent && fabsf(in.y) < kBent))) {
-              const float2 high = capped_high(u, p.cap_log2e);
-              if (!(fabsf(in.x) < kBent)) z[h] = high.x;
-              if (!(fabsf(in.y) < kBent)) z[h + 1] = high.y;
+              for (int t = TERMS - 2; t >= 0; --t) z[h] = fma2(z[h], twice(0x1p-4f), of(t, h));
             }
           }
-        } else {
-          const float factor = ks * p.scale_log2e;
+          if (a.softcap > 0.0f) {
 #pragma unroll
-          for (int h = 0; h < HS; ++h) z[h] *= factor * unit[h];
-        }
-        if (slopes != nullptr) {
+            for (int h = 0; h < HS / 2; ++h) {
+              const uint64_t x = mul2(z[h], mul2(twice(ks), unit[h])), u = mul2(x, twice(p.scale_over_cap));
+              const float2 in = both(u);
+              float2 y = capped_low(x, u, p.scale_log2e);
+              if (__any_sync(0xffffffffu, !(fabsf(in.x) < kBent && fabsf(in.y) < kBent))) {
+                const float2 high = capped_high(u, p.cap_log2e);
+                if (!(fabsf(in.x) < kBent)) y.x = high.x;
+                if (!(fabsf(in.y) < kBent)) y.y = high.y;
+              }
+              z[h] = pair(y.x, y.y);
+              if (slopes == nullptr) z[h] = add2(z[h], less ? held[h] : 0);
+            }
+          } else {
+            const uint64_t factor = twice(ks * p.scale_log2e);
 #pragma unroll
-          for (int h = 0; h < HS; ++h) z[h] = fmaf((h < heads ? slopes[h] : 0.0f) * kLog2e, away, z[h]);
-        }
-        const float vs_least = fmaxf(fabsf(vs), kLeast), most = kLimit / vs_least;
-        bool over = false;
+            for (int h = 0; h < HS / 2; ++h) {
+              const uint64_t c = mul2(factor, unit[h]);
+              z[h] = slopes == nullptr ? fma2(z[h], c, less ? held[h] : 0) : mul2(z[h], c);
+            }
+          }
+          if (slopes != nullptr) {
+            const float away = notes.away[e] * kLog2e;
 #pragma unroll
-        for (int h = 0; h < HS; ++h) over = over || exp2_fast(z[h] - ref[h]) > most;
-        // where its weights go, those of p_bufs tiles ago have been used
-        if (i >= S::p_bufs) {
-          const int before = at - S::p_bufs;
-          ok = wait_or_stop(&sh.pv_done[before & 7], (before >> 3) & 1, stop) && ok;
+            for (int h = 0; h < HS / 2; ++h) {
+              const uint64_t s = pair(2 * h < heads ? slopes[2 * h] : 0.0f, 2 * h + 1 < heads ? slopes[2 * h + 1] : 0.0f);
+              z[h] = add2(fma2(s, twice(away), z[h]), less ? held[h] : 0);
+            }
+          }
+        };
+        const float log_vs = log2f(fmaxf(fabsf(vs), kLeast));
+        bool move = true;
+        if (i > 0) {
+          logits(true);
+          const float most = kLogLimit - log_vs;
+          bool over = false;
+#pragma unroll
+          for (int h = 0; h < HS / 2; ++h) {
+            const float2 y = both(z[h]);
+            over = over || y.x > most || y.y > most;
+          }
+          move = set_any(set, over && seen);
         }
-        if (set_any(set, over && seen)) {
-          // Move the references, by whole numbers, to leave the largest weight in (2^6, 2^7].
-          const float more = log2f(vs_least);
+        if (move) {
+          // Move the references, by whole numbers, to leave the largest weight in (2^4, 2^5].
+          logits(false);
 #pragma unroll
           for (int h = 0; h < HS; ++h) {
-            const float w = seen && z[h] == z[h] ? z[h] + more : __int_as_float(0xff800000);
+            const float2 y = both(z[h / 2]);
+            const float x = h & 1 ? y.y : y.x;
+            const float w = seen && x == x ? x + log_vs : __int_as_float(0xff800000);
             const int32_t m = __reduce_max_sync(0xffffffffu, ordered(w));
             if (lane == 0) sh.most[warp][h] = from_ordered(m);
           }
@@ -550,45 +602,56 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           if (e < HS) {
             const float(*m)[HS] = &sh.most[set * 4];
             const float top = fmaxf(fmaxf(m[0][e], m[1][e]), fmaxf(m[2][e], m[3][e]));
-            const float moved = fmaxf(ref[e], ceilf(top) - 7.0f);
-            sh.factor[set * HS + e] = moved == ref[e] ? 1.0f : exp2_fast(ref[e] - moved);
-            ref[e] = moved;
+            const float was = -nref[e], moved = fmaxf(was, ceilf(top) - 5.0f);
+            sh.factor[set * HS + e] = moved == was ? 1.0f : exp2_fast(was - moved);
+            nref[e] = -moved;
           }
           set_sync(set);
-          const float* factor = sh.factor + set * HS;
 #pragma unroll
-          for (int h = 0; h < HS; ++h) sum[h] *= factor[h];
+          for (int h = 0; h < HS / 2; ++h) z[h] = add2(z[h], held[h]);
           if (i > 0) {
+            const uint64_t* factor = reinterpret_cast<const uint64_t*>(sh.factor + set * HS);
+#pragma unroll
+            for (int h = 0; h < HS / 2; ++h) sum[h] = mul2(sum[h], factor[h]);
             ok = wait_or_stop(&sh.pv_done[(at - 1) & 7], ((at - 1) >> 3) & 1, stop) && ok;
             tc_fence_after();
             for (int m = 0; m < p.v_blocks; ++m)
-#pragma unroll
+#pragma unroll 1
               for (int t = 0; t < TERMS; ++t) {
                 uint32_t v[HS];
                 const uint32_t o_at = tmem_o + m * N + lanes + t * G + set * HS;
                 tmem_ld(v, o_at);
                 tmem_wait_ld(v);
 #pragma unroll
-                for (int h = 0; h < HS; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * factor[h]);
+                for (int h = 0; h < HS; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * sh.factor[set * HS + h]);
                 tmem_st(o_at, v);
               }
             tmem_wait_st();
           }
         }
-        const uint32_t to = p_mine + (at % S::p_bufs) * (S::rows * 128) + set * HS * 128;
+        uint32_t words[TERMS][HS / 4];  // the weights' terms, four heads each
 #pragma unroll
-        for (int h = 0; h < HS; h += 2) {
-          const float w0 = seen ? exp2_fast(z[h] - ref[h]) : 0.0f, w1 = seen ? exp2_fast(z[h + 1] - ref[h + 1]) : 0.0f;
-          sum[h] += w0, sum[h + 1] += w1;
-          uint32_t x = half_two(w0 * vs, w1 * vs);
+        for (int h = 0; h < HS / 2; ++h) {
+          const float2 y = both(z[h]);
+          const uint64_t w = pair(seen ? exp2_fast(y.x) : 0.0f, seen ? exp2_fast(y.y) : 0.0f);
+          sum[h] = add2(sum[h], w);
+          const float2 scaled = both(mul2(w, twice(vs)));
+          uint32_t x = half_two(scaled.x, scaled.y);
 #pragma unroll
           for (int t = 0; t < TERMS; ++t) {
             const uint32_t two = e4m3_of_half2(x);
             if (t + 1 < TERMS) x = rest16(x, half2_of_e4m3(two));
-            // row t G + h of 128 bytes, in the swizzle: G and the set's first head are whole groups of 8 rows
-            put_byte((to ^ ((h & 7) << 4)) + (t * G + h) * 128, two);
-            put_byte((to ^ (((h + 1) & 7) << 4)) + (t * G + h + 1) * 128, two >> 8);
+            words[t][h / 2] = h & 1 ? words[t][h / 2] | two << 16 : two;
           }
+        }
+        const uint32_t to = p_mine + (at & 1) * S::p_bytes;
+        if constexpr (HS == 16) {
+#pragma unroll
+          for (int t = 0; t < TERMS; ++t)
+            put16(to + t * SETS * (kEntries * 16), words[t][0], words[t][1], words[t][2], words[t][3]);
+        } else {  // two terms of eight heads a unit; the other half of the third's is nobody's
+          put16(to, words[0][0], words[0][1], words[1][0], words[1][1]);
+          if constexpr (TERMS == 3) put16(to + kEntries * 16, words[2][0], words[2][1], 0, 0);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -599,19 +662,23 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       // ---- end of a work ----
       if (tiles > 0) ok = wait_or_stop(&sh.pv_done[(n + tiles - 1) & 7], ((n + tiles - 1) >> 3) & 1, stop) && ok;
       tc_fence_after();
+      float sums[HS];
 #pragma unroll
-      for (int h = 0; h < HS; ++h) sum[h] = ok ? sum[h] : __int_as_float(0x7fc00000);
-      const float part = sum_lanes<HS>(sum, lane);
+      for (int h = 0; h < HS; ++h) {
+        const float2 y = both(sum[h / 2]);
+        sums[h] = ok ? h & 1 ? y.y : y.x : __int_as_float(0x7fc00000);
+      }
+      const float part = sum_lanes<HS>(sums, lane);
       if (lane % (32 / HS) == 0) sh.sum[warp][lane / (32 / HS)] = part;
       set_sync(set);
       if (e < HS) {
         const float(*m)[HS] = &sh.sum[set * 4];
         const float total = (m[0][e] + m[1][e]) + (m[2][e] + m[3][e]);
         if (cluster > 1) {
-          sh.head_ref[set * HS + e] = ref[e], sh.head_sum[set * HS + e] = total;
+          sh.head_ref[set * HS + e] = -nref[e], sh.head_sum[set * HS + e] = total;
         } else {
           sh.inverse[set * HS + e] = e4_inverse(total);
-          if (a.lse != nullptr && e < heads) a.lse[k.row * a.Hq + k.head0 + set * HS + e] = e4_logsum(ref[e], total);
+          if (a.lse != nullptr && e < heads) a.lse[k.row * a.Hq + k.head0 + set * HS + e] = e4_logsum(-nref[e], total);
         }
       }
       set_sync(set);
@@ -636,10 +703,6 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
 #pragma unroll
             for (int t = TERMS - 2; t >= 0; --t) x[h] = fmaf(x[h], 0x1p-4f, __uint_as_float(v[t][h]));
           }
-          if (m == p.v_blocks - 1) {  // O is read: the next work may have it
-            tc_fence_before();
-            mbar_arrive(&sh.o_free);
-          }
         }
         const int d = m * 128 + e;
         if (cluster > 1) {
@@ -651,13 +714,14 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
             if (h < heads) out[static_cast<int64_t>(h) * a.Dv + d] = E(x[h] * inverse[h]);
         }
       }
-      set_sync(set);  // what the set shares is read
+      tc_fence_before();  // O is read: the next work's first weights say so
+      set_sync(set);      // and what the set shares
     }
   }
 
   __syncthreads();
   if (*stop != 0) {  // a wait ran out: nobody may have waited for what is in flight
-    if (one) mma_drain(&sh.drained[warp - S::mma]);
+    if (one) mma_drain(&sh.drained);
     copy_commit();
     copy_wait<0>();
     __syncthreads();
@@ -738,7 +802,7 @@ topk_status launch_heads(const sparse_attention_e4m3_args& args, int dev, int sm
   p.tmem_cols = 32;
   while (p.tmem_cols < columns) p.tmem_cols *= 2;
   using Shared = E4Shared<G, S::sets, S::set_heads>;
-  const int q_bytes = S::rows * 128 * p.d_blocks * S::q_bufs, p_bytes = S::rows * 128 * S::p_bufs;
+  const int q_bytes = kBufs * S::rows * 128 * p.d_blocks, p_bytes = kBufs * S::p_bytes;
   const int fixed = q_bytes + p_bytes + static_cast<int>(sizeof(Shared)) + kBufs * p.note_bytes;
   const int stage = p.k_bytes + p.v_bytes + p.note_bytes;
   const int join = G * p.v_blocks * 128 * 4;  // rows for the other CTAs, over the queries and the rings
@@ -747,7 +811,7 @@ topk_status launch_heads(const sparse_attention_e4m3_args& args, int dev, int sm
   const bool two = S::per_sm == 2 && fixed + 2 * stage <= half && p.tmem_cols <= 256 && join <= half - fixed + q_bytes;
   const int room = (two ? half : kMaxShared) - fixed;
   p.k_stages = room / stage < kMaxStages ? room / stage : kMaxStages;
-  if (p.k_stages < 1) return TOPK_EINVAL;
+  if (p.k_stages < (p.shared ? 2 : 1)) return TOPK_EINVAL;  // S of a tile goes ahead of O^T of the one before
   p.v_stages = p.shared ? 0 : p.k_stages;
   if (!p.shared && p.k_stages < kMaxStages && room - p.k_stages * stage >= p.v_bytes) ++p.v_stages;
   p.notes = p.k_stages + kBufs;
@@ -797,10 +861,9 @@ topk_status launch_cache_attention(const sparse_attention_e4m3_args& a, int dev,
   const int heads = a.attention.Hq / a.attention.Hkv;
   if (heads <= 8) return launch_heads<E, 8>(a, dev, sm_count, stream);
   if (heads <= 16) return launch_heads<E, 16>(a, dev, sm_count, stream);
-  // Three terms of 64 heads would not leave TMEM for their scores.
-  if (heads <= 32 || !std::is_same<E, __nv_bfloat16>::value) return launch_heads<E, 32>(a, dev, sm_count, stream);
-  if constexpr (std::is_same<E, __nv_bfloat16>::value) return launch_heads<E, 64>(a, dev, sm_count, stream);
-  return TOPK_EINVAL;
+  if constexpr (std::is_same<E, __nv_bfloat16>::value)  // TMEM has no room for three terms of 64 heads
+    if (heads > 32) return launch_heads<E, 64>(a, dev, sm_count, stream);
+  return launch_heads<E, 32>(a, dev, sm_count, stream);
 }
 
 }  // namespace
