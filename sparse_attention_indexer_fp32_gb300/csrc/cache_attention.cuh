@@ -152,13 +152,6 @@ __device__ __forceinline__ bool set_any(int set, bool yes) {
 }
 __device__ __forceinline__ void set_sync(int set) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(set + 1) : "memory"); }
 
-// A float as an integer of the same order, and back.
-__device__ __forceinline__ int32_t ordered(float x) {
-  const int32_t i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7fffffff);
-}
-__device__ __forceinline__ float from_ordered(int32_t i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
-
 // Sums of HS numbers over the lanes of a warp: lane l is left with that of number
 // l / (32 / HS).
 template <int HS>
@@ -174,6 +167,23 @@ __device__ __forceinline__ float sum_lanes(float (&v)[HS], int lane) {
   }
 #pragma unroll
   for (int bit = 32 / HS / 2; bit >= 1; bit /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+  return v[0];
+}
+
+// The same for the largest.
+template <int HS>
+__device__ __forceinline__ float max_lanes(float (&v)[HS], int lane) {
+#pragma unroll
+  for (int w = HS / 2, bit = 16; w >= 1; w /= 2, bit /= 2) {
+    const bool high = lane & bit;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float give = high ? v[i] : v[i + w], keep = high ? v[i + w] : v[i];
+      v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, bit));
+    }
+  }
+#pragma unroll
+  for (int bit = 32 / HS / 2; bit >= 1; bit /= 2) v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
   return v[0];
 }
 
@@ -245,6 +255,44 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
   const int q_block = S::rows * 128, q_bytes = q_block * p.d_blocks;
   constexpr int kSets = S::gather / 4;  // of gathering warps, which take tiles in turn
 
+  // A gathering warp has 32 entries of every tile of its set, one a lane to look up: in the
+  // list two of the set's tiles ahead, in the page table one; the first before anything else.
+  const bool gathers = warp >= S::softmax && warp < S::mma;
+  const int part = (warp - S::softmax) & 3, turn = (warp - S::softmax) >> 2;
+  const bool some = a.page_size > 0 && a.num_pages > 0;
+  struct Look {
+    const int32_t* indices;
+    const int32_t* table;
+    int32_t last, first, g;
+  };
+  auto enter = [&](uint32_t w_at) -> Look {
+    const E4Work k = e4_work<G>(p, w_at);
+    Look l;
+    l.indices = a.indices + k.row * a.K;
+    l.table = a.page_table != nullptr ? a.page_table + k.b * a.table_stride : nullptr;
+    l.last = a.query_positions != nullptr ? a.query_positions[k.row] : INT32_MAX;
+    l.first = a.first != nullptr ? max(a.first[k.row], 0) : 0;
+    l.g = k.g;
+    return l;
+  };
+  auto index_of = [&](const Look& l, int i) -> int32_t {
+    const int64_t j = (static_cast<int64_t>(i) * cluster + rank) * kEntries + part * 32 + lane;
+    return i < tiles && j < a.K && some ? l.indices[j] : -1;
+  };
+  auto page_index = [&](int32_t pos) -> uint32_t {
+    return p.page_shift >= 0 ? static_cast<uint32_t>(pos) >> p.page_shift
+                             : static_cast<uint32_t>(pos) / static_cast<uint32_t>(a.page_size);
+  };
+  auto page_of = [&](const Look& l, int32_t pos) -> uint32_t {  // ~0: not seen
+    if (pos < l.first || pos > l.last) return 0xffffffffu;
+    const uint32_t page = page_index(pos);
+    return l.table == nullptr ? page : page < p.table_width ? static_cast<uint32_t>(l.table[page]) : 0xffffffffu;
+  };
+  Look look = {};
+  int32_t pos = -1, pos1 = -1;
+  uint32_t page = 0xffffffffu;
+  if (gathers) look = enter(first_w), pos = index_of(look, turn), pos1 = index_of(look, turn + kSets);
+
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.k_stages; ++i) mbar_init(&sh.k_full[i], 128);
     for (int i = 0; i < p.v_stages; ++i) mbar_init(&sh.v_full[i], 128);
@@ -258,6 +306,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
     fence_mbar_init();
   }
   if (warp == S::mma) tmem_alloc(&sh.tmem, p.tmem_cols);
+  if (gathers) page = page_of(look, pos);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -265,100 +314,71 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
   volatile uint32_t* stop = &sh.stop;
   bool one = false;  // the thread that issues products
 
-  if (warp >= S::softmax && warp < S::mma) {
-    // ---- gather: a warp has 32 entries of every tile of its set ----
-    const int w = warp - S::softmax, part = w & 3, turn = w >> 2;
+  if (gathers) {
+    // ---- gather ----
     // 16-byte units of an entry's keys: those that it has, and those that are read
     const int k_units = a.D / 16, k_read = p.d_steps * 2, v_units = a.Dv / 16;
     const uint32_t unit16 = lane & 7, sub = lane >> 3;
     const uint32_t at = (part * 32 + sub) * 128;
     const uint32_t even = (unit16 ^ sub) << 4, odd = (unit16 ^ (sub + 4)) << 4;
-    const bool some = a.page_size > 0 && a.num_pages > 0;
     // an empty cache has no address: nothing is read from the one it gets
     const char* nowhere = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(a.q) & ~static_cast<uintptr_t>(15));
     bool ok = true;
-    int n = 0, k_stage = turn % p.k_stages, v_stage = p.shared ? 0 : turn % p.v_stages, note = turn;
-    for (uint32_t w_at = first_w; w_at < p.works && ok; w_at += step_w, n += tiles) {
-      const E4Work k = e4_work<G>(p, w_at);
-      const int32_t* indices = a.indices + k.row * a.K;
-      const int32_t* table = a.page_table != nullptr ? a.page_table + k.b * a.table_stride : nullptr;
-      const int32_t last = a.query_positions != nullptr ? a.query_positions[k.row] : INT32_MAX;
-      const int32_t first = a.first != nullptr ? max(a.first[k.row], 0) : 0;
-      // Each lane looks up one entry of a tile, its index two of the set's tiles ahead, its page id one.
-      auto index_of = [&](int i) -> int32_t {
-        const int64_t j = (static_cast<int64_t>(i) * cluster + rank) * kEntries + part * 32 + lane;
-        return i < tiles && j < a.K && some ? indices[j] : -1;
-      };
-      auto page_index = [&](int32_t pos) -> uint32_t {
-        return p.page_shift >= 0 ? static_cast<uint32_t>(pos) >> p.page_shift
-                                 : static_cast<uint32_t>(pos) / static_cast<uint32_t>(a.page_size);
-      };
-      auto page_of = [&](int32_t pos) -> uint32_t {  // ~0: not seen
-        if (pos < first || pos > last) return 0xffffffffu;
-        const uint32_t page = page_index(pos);
-        return table == nullptr ? page : page < p.table_width ? static_cast<uint32_t>(table[page]) : 0xffffffffu;
-      };
-      const int i0 = (turn - n) & (kSets - 1);
-      int32_t pos = index_of(i0), pos1 = index_of(i0 + kSets);
-      uint32_t page = page_of(pos);
-      const char* keys = some ? static_cast<const char*>(a.k) + k.g * a.k_head_stride + unit16 * 16 : nowhere;
-      const char* values = some ? static_cast<const char*>(a.v) + k.g * a.v_head_stride + unit16 * 16 : nowhere;
+    int k_stage = turn % p.k_stages, v_stage = p.shared ? 0 : turn % p.v_stages, note = turn;
+    int before_w = 0;  // tiles of the works before
+    for (uint32_t w_at = first_w; w_at < p.works && ok; w_at += step_w, before_w += tiles) {
+      const int i0 = (turn - before_w) & (kSets - 1), next_i0 = (turn - before_w - tiles) & (kSets - 1);
+      const char* keys = some ? static_cast<const char*>(a.k) + look.g * a.k_head_stride + unit16 * 16 : nowhere;
+      const char* values = some ? static_cast<const char*>(a.v) + look.g * a.v_head_stride + unit16 * 16 : nowhere;
+      // the next work's first entries
+      Look next = look;
+      int32_t next_pos = -1, next_pos1 = -1;
+      uint32_t next_page = 0xffffffffu;
+      const bool more = w_at + step_w < p.works;
+      if (more) next = enter(w_at + step_w), next_pos = index_of(next, next_i0), next_pos1 = index_of(next, next_i0 + kSets);
       for (int i = i0; i < tiles; i += kSets) {
-        const int32_t pos2 = index_of(i + 2 * kSets);
-        const uint32_t page1 = page_of(pos1);
+        const int n = before_w + i;  // the tile's number in the CTA
+        const int32_t pos2 = index_of(look, i + 2 * kSets);
+        const uint32_t page1 = page_of(look, pos1);
         const bool seen = page < p.pages;
         const uint32_t place = static_cast<uint32_t>(pos) - page_index(pos) * static_cast<uint32_t>(a.page_size);
         const uint32_t bits = __ballot_sync(0xffffffffu, seen);
         // 8 lanes fetch 128 bytes of an entry; step j has entries 4 j + lane / 8. What is not
         // seen is zeros; of a last block that is not full, the units up to `read`.
-        auto fetch = [&](uint32_t dst, const char* from, int64_t entry, int blocks, int units, int read) {
-          const char* rows[8];
-          uint32_t bytes[8];
+        auto fetch = [&](uint32_t dst, const char* from, int64_t entry, int units, int read) {
+          const int u = static_cast<int>(unit16);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            rows[j] = from + __shfl_sync(0xffffffffu, entry, 4 * j + sub);
-            bytes[j] = (bits >> (4 * j + sub)) & 1 ? 16 : 0;
-          }
-#pragma unroll
-          for (int c = 0; c < SPARSE_ATTENTION_MAX_D / 128; ++c) {
-            if (c >= blocks) continue;
-            const int u = c * 8 + static_cast<int>(unit16);
-            if (c * 8 + 8 <= units) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                copy_bytes(dst + c * (kEntries * 128) + j * 512 + (j & 1 ? odd : even), rows[j] + c * 128, bytes[j]);
-            } else if (u < read) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                copy_bytes(dst + c * (kEntries * 128) + j * 512 + (j & 1 ? odd : even), u < units ? rows[j] + c * 128 : from,
-                           u < units ? bytes[j] : 0);
-            }
+            const char* row = from + __shfl_sync(0xffffffffu, entry, 4 * j + sub);
+            const uint32_t bytes = (bits >> (4 * j + sub)) & 1 ? 16 : 0, to = dst + j * 512 + (j & 1 ? odd : even);
+            if (u < read) copy_bytes(to, row, u < units ? bytes : 0);
+            if (u + 8 < read) copy_bytes(to + kEntries * 128, row + 128, u + 8 < units ? bytes : 0);
           }
         };
-        int before = n + i - p.k_stages;
+        int before = n - p.k_stages;
         uint64_t* used = p.shared ? sh.pv_done : sh.s_full;  // when a stage of keys is free
         ok = before < 0 || wait_or_stop(&used[before & 7], (before >> 3) & 1, stop);
         if (!ok) break;
         fetch(k_ring + k_stage * p.k_bytes + at, keys, seen ? page * a.k_page_stride + place * a.k_token_stride : 0,
-              p.d_blocks, k_units, k_read);
+              k_units, k_read);
         Notes& notes = *reinterpret_cast<Notes*>(smem + p.note_at + note * p.note_bytes);
         const int e = part * 32 + lane;
         const uint32_t block = p.block_shift >= 0 ? place >> p.block_shift : place / static_cast<uint32_t>(p.block);
-        const int64_t unit = seen ? (static_cast<int64_t>(page) * p.blocks + block) * a.Hkv + k.g : 0;
+        const int64_t unit = seen ? (static_cast<int64_t>(page) * p.blocks + block) * a.Hkv + look.g : 0;
         copy4(smem_addr(&notes.ks[e]), some ? reinterpret_cast<const char*>(p.k_scales + unit) : nowhere, seen);
         copy4(smem_addr(&notes.vs[e]), some ? reinterpret_cast<const char*>(p.v_scales + unit) : nowhere, seen);
         copy_arrive(&sh.k_full[k_stage]);
         copy_arrive(&sh.noted[note]);
-        if (a.slopes != nullptr) notes.away[e] = static_cast<float>(seen ? pos - last : 0);
+        if (a.slopes != nullptr) notes.away[e] = static_cast<float>(seen ? pos - look.last : 0);
         if (lane == 0) notes.seen[part] = bits;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.noted[note]);
         if (!p.shared) {
-          before = n + i - p.v_stages;
+          before = n - p.v_stages;
           ok = before < 0 || wait_or_stop(&sh.pv_done[before & 7], (before >> 3) & 1, stop);
           if (!ok) break;
           fetch(v_ring + v_stage * p.v_bytes + at, values, seen ? page * a.v_page_stride + place * a.v_token_stride : 0,
-                p.v_blocks, v_units, v_units);
+                v_units, v_units);
           copy_arrive(&sh.v_full[v_stage]);
           v_stage += kSets;
           while (v_stage >= p.v_stages) v_stage -= p.v_stages;
@@ -367,7 +387,10 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         k_stage += kSets, note += kSets;
         while (k_stage >= p.k_stages) k_stage -= p.k_stages;
         if (note >= p.notes) note -= p.notes;
+        if (i + 2 * kSets >= tiles && i + kSets < tiles && more) next_page = page_of(next, next_pos);
       }
+      if (more && i0 + kSets >= tiles) next_page = page_of(next, next_pos);
+      look = next, pos = next_pos, pos1 = next_pos1, page = next_page;
     }
     copy_commit();
     copy_wait<0>();
@@ -544,13 +567,21 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
             }
           }
           if (a.softcap > 0.0f) {
+            // the second form only where a logit of the warp needs it
+            float most = 0.0f;
 #pragma unroll
             for (int h = 0; h < HS / 2; ++h) {
-              const uint64_t x = mul2(z[h], mul2(twice(ks), unit[h])), u = mul2(x, twice(p.scale_over_cap));
-              const float2 in = both(u);
-              float2 y = capped_low(x, u, p.scale_log2e);
-              if (__any_sync(0xffffffffu, !(fabsf(in.x) < kBent && fabsf(in.y) < kBent))) {
-                const float2 high = capped_high(u, p.cap_log2e);
+              z[h] = mul2(z[h], mul2(twice(ks), unit[h]));
+              const float2 y = both(z[h]);
+              most = fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y)));
+            }
+            const bool bent = __any_sync(0xffffffffu, !(most * fabsf(p.scale_over_cap) < kBent));
+#pragma unroll
+            for (int h = 0; h < HS / 2; ++h) {
+              const uint64_t u = mul2(z[h], twice(p.scale_over_cap));
+              float2 y = capped_low(z[h], u, p.scale_log2e);
+              if (bent) {
+                const float2 in = both(u), high = capped_high(u, p.cap_log2e);
                 if (!(fabsf(in.x) < kBent)) y.x = high.x;
                 if (!(fabsf(in.y) < kBent)) y.y = high.y;
               }
@@ -579,25 +610,25 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         if (i > 0) {
           logits(true);
           const float most = kLogLimit - log_vs;
-          bool over = false;
+          float high = -FLT_MAX;
 #pragma unroll
           for (int h = 0; h < HS / 2; ++h) {
             const float2 y = both(z[h]);
-            over = over || y.x > most || y.y > most;
+            high = fmaxf(high, fmaxf(y.x, y.y));
           }
-          move = set_any(set, over && seen);
+          move = set_any(set, high > most && seen);
         }
         if (move) {
           // Move the references, by whole numbers, to leave the largest weight in (2^4, 2^5].
           logits(false);
+          float w[HS];  // a NaN is no maximum
 #pragma unroll
           for (int h = 0; h < HS; ++h) {
             const float2 y = both(z[h / 2]);
-            const float x = h & 1 ? y.y : y.x;
-            const float w = seen && x == x ? x + log_vs : __int_as_float(0xff800000);
-            const int32_t m = __reduce_max_sync(0xffffffffu, ordered(w));
-            if (lane == 0) sh.most[warp][h] = from_ordered(m);
+            w[h] = seen ? fmaxf((h & 1 ? y.y : y.x) + log_vs, -FLT_MAX) : -FLT_MAX;
           }
+          const float top = max_lanes<HS>(w, lane);
+          if (lane % (32 / HS) == 0) sh.most[warp][lane / (32 / HS)] = top;
           set_sync(set);
           if (e < HS) {
             const float(*m)[HS] = &sh.most[set * 4];
