@@ -108,7 +108,7 @@ struct E4Shared {
   alignas(16) float unit[4][G];  // of the queries, of the last four works
   float most[SETS * 4][HS], sum[SETS * 4][HS];
   float head_ref[G], head_sum[G];  // for the other CTAs of a cluster
-  uint64_t k_full[kMaxStages], v_full[kMaxStages], noted[kMaxNotes];
+  uint64_t k_full[kMaxStages], v_full[kMaxStages];
   uint64_t q_full[kBufs], q_empty[kBufs], units[4];
   // Of tile i at i % 8: scores there, weights there, products with v done.
   uint64_t s_full[8], p_full[8], pv_done[8];
@@ -137,6 +137,20 @@ __device__ __forceinline__ E4Work e4_work(const E4Params& p, uint32_t w) {
 
 __device__ __forceinline__ void put16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// As wait_or_stop_one, by the one thread that everybody waits for: it does not sleep.
+__device__ __forceinline__ bool wait_spinning(uint64_t* bar, uint32_t parity, volatile uint32_t* stop) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_test_wait(bar, parity)) {
+    if (*stop != 0) return false;
+    if (global_timer_ns() - t0 > kWaitLimit) {
+      *stop = 1;
+      return false;
+    }
+  }
+  return true;
 }
 
 // Among the 128 threads of a set: whether any of them says yes.
@@ -201,6 +215,11 @@ struct Two<__half> {
   static __device__ __forceinline__ float2 get(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 };
 
+__device__ __forceinline__ float log2_fast(float x) {  // to 2^-22 of 1 or of itself
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t half_two(float x, float y) {
   const __half2 v = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -294,13 +313,12 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
   if (gathers) look = enter(first_w), pos = index_of(look, turn), pos1 = index_of(look, turn + kSets);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.k_stages; ++i) mbar_init(&sh.k_full[i], 128);
+    for (int i = 0; i < p.k_stages; ++i) mbar_init(&sh.k_full[i], 128 + 4);
     for (int i = 0; i < p.v_stages; ++i) mbar_init(&sh.v_full[i], 128);
-    for (int i = 0; i < p.notes; ++i) mbar_init(&sh.noted[i], 128 + 4);
-    for (int i = 0; i < kBufs; ++i) mbar_init(&sh.q_full[i], S::queries * 32), mbar_init(&sh.q_empty[i], 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.units[i], S::queries * 32);
+    for (int i = 0; i < kBufs; ++i) mbar_init(&sh.q_full[i], S::queries), mbar_init(&sh.q_empty[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.units[i], S::queries);
     for (int i = 0; i < 8; ++i)
-      mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 128 * SETS), mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.s_full[i], 2), mbar_init(&sh.p_full[i], S::softmax), mbar_init(&sh.pv_done[i], 1);
     mbar_init(&sh.drained, 1);
     sh.stop = 0;
     fence_mbar_init();
@@ -368,11 +386,10 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         copy4(smem_addr(&notes.ks[e]), some ? reinterpret_cast<const char*>(p.k_scales + unit) : nowhere, seen);
         copy4(smem_addr(&notes.vs[e]), some ? reinterpret_cast<const char*>(p.v_scales + unit) : nowhere, seen);
         copy_arrive(&sh.k_full[k_stage]);
-        copy_arrive(&sh.noted[note]);
         if (a.slopes != nullptr) notes.away[e] = static_cast<float>(seen ? pos - look.last : 0);
         if (lane == 0) notes.seen[part] = bits;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.noted[note]);
+        if (lane == 0) mbar_arrive(&sh.k_full[k_stage]);
         if (!p.shared) {
           before = n - p.v_stages;
           ok = before < 0 || wait_or_stop(&sh.pv_done[before & 7], (before >> 3) & 1, stop);
@@ -410,8 +427,8 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       bool ok = true;
       auto scores = [&](int n) {
         const int qb = s_work & 1;
-        if (s_tile == 0) ok = wait_or_stop_one(&sh.q_full[qb], (s_work >> 1) & 1, stop);
-        ok = ok && wait_or_stop_one(&sh.k_full[k_stage], k_turn, stop);
+        if (s_tile == 0) ok = wait_spinning(&sh.q_full[qb], (s_work >> 1) & 1, stop);
+        ok = ok && wait_spinning(&sh.k_full[k_stage], k_turn, stop);
         if (!ok) return;
         fence_proxy_async_smem();
         tc_fence_after();
@@ -423,6 +440,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           mma_f8(to, kd + (c * (kEntries * 128 >> 4) + in), qd + (c * (S::rows * 128 >> 4) + in), s_desc, j > 0);
         }
         mma_commit(&sh.s_full[n & 7]);
+        mbar_arrive(&sh.s_full[n & 7]);  // by this thread, which has seen the tile's notes
         if (++k_stage == p.k_stages) k_stage = 0, k_turn ^= 1;
         if (++s_tile == tiles) {
           mma_commit(&sh.q_empty[qb]);
@@ -433,10 +451,10 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       for (int n = 0; n < last && ok; ++n) {
         if (n + 1 < last) scores(n + 1);
         if (!p.shared) {
-          ok = ok && wait_or_stop_one(&sh.v_full[v_stage], v_turn, stop);
+          ok = ok && wait_spinning(&sh.v_full[v_stage], v_turn, stop);
           fence_proxy_async_smem();
         }
-        ok = ok && wait_or_stop_one(&sh.p_full[n & 7], (n >> 3) & 1, stop);
+        ok = ok && wait_spinning(&sh.p_full[n & 7], (n >> 3) & 1, stop);
         if (!ok) break;
         tc_fence_after();
         const uint64_t vd = v_desc + static_cast<uint32_t>(v_stage * v_bytes >> 4);
@@ -454,36 +472,50 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
     __syncwarp();
   } else if (warp >= S::query) {
     // ---- queries: a power of two for each head and terms in units of it ----
+    // A warp has every so many heads, kAhead of them at once; the next ones, of this work or
+    // the next, are on their way meanwhile.
     const int who = warp - S::query;
+    constexpr int kAhead = 4;
+    uint4 raw[kAhead];
+    auto load = [&](const E4Work& k, int h0) {
+      const E* q = static_cast<const E*>(a.q) + k.b * a.q_seq_stride + k.t * a.q_token_stride + k.head0 * a.q_head_stride;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int h = h0 + u * S::queries;
+        const E* from = q + h * a.q_head_stride + lane * 8;
+        raw[u] = make_uint4(0, 0, 0, 0);
+        if (h >= k.heads || lane * 8 >= a.D) continue;  // D is a multiple of 16
+        if (p.q_vector) {
+          raw[u] = *reinterpret_cast<const uint4*>(from);
+        } else {
+          const uint16_t* e = reinterpret_cast<const uint16_t*>(from);
+          auto two = [&](int j) { return e[j] | static_cast<uint32_t>(e[j + 1]) << 16; };
+          raw[u] = make_uint4(two(0), two(2), two(4), two(6));
+        }
+      }
+    };
     int nw = 0;
+    E4Work k = e4_work<G>(p, first_w);
+    if (tiles > 0) load(k, who);
     for (uint32_t w_at = first_w; tiles > 0 && w_at < p.works; w_at += step_w, ++nw) {
-      const E4Work k = e4_work<G>(p, w_at);
-      const int qb = nw & 1;
+      const int qb = nw & 1, heads = k.heads;
       if (nw >= kBufs && !wait_or_stop(&sh.q_empty[qb], ((nw >> 1) - 1) & 1, stop)) break;
       unsigned char* to = smem + qb * q_bytes;
-      const E* q = static_cast<const E*>(a.q) + k.b * a.q_seq_stride + k.t * a.q_token_stride + k.head0 * a.q_head_stride;
-      constexpr int kAhead = 4;
       for (int h0 = who; h0 < G; h0 += S::queries * kAhead) {
-        uint4 raw[kAhead];
+        uint4 now[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int h = h0 + u * S::queries;
-          const E* from = q + h * a.q_head_stride + lane * 8;
-          raw[u] = make_uint4(0, 0, 0, 0);
-          if (h >= k.heads || lane * 8 >= a.D) continue;  // D is a multiple of 16
-          if (p.q_vector) {
-            raw[u] = *reinterpret_cast<const uint4*>(from);
-          } else {
-            const uint16_t* e = reinterpret_cast<const uint16_t*>(from);
-            auto two = [&](int j) { return e[j] | static_cast<uint32_t>(e[j + 1]) << 16; };
-            raw[u] = make_uint4(two(0), two(2), two(4), two(6));
-          }
+        for (int u = 0; u < kAhead; ++u) now[u] = raw[u];
+        if (h0 + S::queries * kAhead < G) {
+          load(k, h0 + S::queries * kAhead);
+        } else if (w_at + step_w < p.works) {
+          k = e4_work<G>(p, w_at + step_w);
+          load(k, who);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           const int h = h0 + u * S::queries;
           if (h >= G) continue;
-          const uint32_t in[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+          const uint32_t in[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
           uint32_t most = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) most = __vmaxu2(most, in[j] & 0x7fff7fffu);
@@ -493,7 +525,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           const bool bad = top >= 0x7f800000u;
           const int exponent = max(static_cast<int>(top >> 23) - 127 - 7, -120);
           const float over = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
-          if (lane == 0) sh.unit[nw & 3][h] = h < k.heads ? __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23) : 0.0f;
+          if (lane == 0) sh.unit[nw & 3][h] = h < heads ? __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23) : 0.0f;
           uint32_t x[4];  // in fp16: exact from 2^-14 units on, below the last term's steps
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -515,8 +547,8 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sh.q_full[qb]);
-      mbar_arrive(&sh.units[nw & 3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full[qb]), mbar_arrive(&sh.units[nw & 3]);
     }
   } else {
     // ---- softmax: thread `e` of a set has entry e of each tile, for the set's heads ----
@@ -543,14 +575,16 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       for (int i = 0; i < tiles; ++i) {
         const int at = n + i;
         const Notes& notes = *reinterpret_cast<const Notes*>(smem + p.note_at + note * p.note_bytes);
-        ok = wait_or_stop(&sh.noted[note], (at / p.notes) & 1, stop) && ok;
-        const float ks = notes.ks[e], vs = notes.vs[e];
-        const bool seen = (notes.seen[e >> 5] >> (e & 31)) & 1;
         ok = wait_or_stop(&sh.s_full[at & 7], (at >> 3) & 1, stop) && ok;
         tc_fence_after();
-        // Logits in units of log 2, two heads at a time, less the reference or as they are.
+        const float ks = notes.ks[e], vs = notes.vs[e];
+        const bool seen = (notes.seen[e >> 5] >> (e & 31)) & 1;
+        const float log_vs = log2_fast(fmaxf(fabsf(vs), kLeast));
+        // Logits in units of log 2, two heads at a time: less the references, and if a
+        // weight is then too large (or the first tile's), as they are.
         uint64_t z[HS / 2];
-        auto logits = [&](bool less) {
+        bool move = i == 0;
+        for (;;) {
           {
             uint32_t v[TERMS][HS];
             const uint32_t s_at = tmem_s + (at & 1) * N + lanes + set * HS;
@@ -586,41 +620,39 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
                 if (!(fabsf(in.y) < kBent)) y.y = high.y;
               }
               z[h] = pair(y.x, y.y);
-              if (slopes == nullptr) z[h] = add2(z[h], less ? held[h] : 0);
-            }
-          } else {
-            const uint64_t factor = twice(ks * p.scale_log2e);
-#pragma unroll
-            for (int h = 0; h < HS / 2; ++h) {
-              const uint64_t c = mul2(factor, unit[h]);
-              z[h] = slopes == nullptr ? fma2(z[h], c, less ? held[h] : 0) : mul2(z[h], c);
             }
           }
           if (slopes != nullptr) {
             const float away = notes.away[e] * kLog2e;
+            const uint64_t factor = twice(ks * p.scale_log2e);
 #pragma unroll
             for (int h = 0; h < HS / 2; ++h) {
+              if (!(a.softcap > 0.0f)) z[h] = mul2(z[h], mul2(factor, unit[h]));
               const uint64_t s = pair(2 * h < heads ? slopes[2 * h] : 0.0f, 2 * h + 1 < heads ? slopes[2 * h + 1] : 0.0f);
-              z[h] = add2(fma2(s, twice(away), z[h]), less ? held[h] : 0);
+              z[h] = fma2(s, twice(away), z[h]);
             }
           }
-        };
-        const float log_vs = log2f(fmaxf(fabsf(vs), kLeast));
-        bool move = true;
-        if (i > 0) {
-          logits(true);
-          const float most = kLogLimit - log_vs;
+          // what is left to do: z, or x c where neither cap nor slopes took the scales
+          const bool plain = !(a.softcap > 0.0f) && slopes == nullptr;
+          const uint64_t factor = twice(plain ? ks * p.scale_log2e : 1.0f);
+#pragma unroll
+          for (int h = 0; h < HS / 2; h += 2) {
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&unit[h]), r = *reinterpret_cast<const ulonglong2*>(&held[h]);
+            const uint64_t c0 = plain ? mul2(factor, u.x) : factor, c1 = plain ? mul2(factor, u.y) : factor;
+            z[h] = fma2(z[h], c0, move ? 0 : r.x), z[h + 1] = fma2(z[h + 1], c1, move ? 0 : r.y);
+          }
+          if (move) break;
           float high = -FLT_MAX;
 #pragma unroll
           for (int h = 0; h < HS / 2; ++h) {
             const float2 y = both(z[h]);
             high = fmaxf(high, fmaxf(y.x, y.y));
           }
-          move = set_any(set, high > most && seen);
+          move = set_any(set, seen && high > kLogLimit - log_vs);
+          if (!move) break;
         }
         if (move) {
           // Move the references, by whole numbers, to leave the largest weight in (2^4, 2^5].
-          logits(false);
           float w[HS];  // a NaN is no maximum
 #pragma unroll
           for (int h = 0; h < HS; ++h) {
@@ -686,7 +718,8 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&sh.p_full[at & 7]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[at & 7]);
         if (++note == p.notes) note = 0;
       }
 
