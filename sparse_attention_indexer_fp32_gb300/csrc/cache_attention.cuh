@@ -102,7 +102,8 @@ struct Notes {
 
 template <int G, int SETS, int HS>
 struct E4Shared {
-  alignas(16) float nref[G];  // a head's reference, negative
+  alignas(16) float nref[G];  // a head's reference, negative; +0: nothing seen yet, a reference of 0 is -0
+  alignas(16) float step[G];  // what was last added to nref, and the factor of its sums
   alignas(16) float factor[G];
   alignas(16) float inverse[G];
   alignas(16) float unit[4][G];  // of the queries, of the last four works
@@ -137,20 +138,6 @@ __device__ __forceinline__ E4Work e4_work(const E4Params& p, uint32_t w) {
 
 __device__ __forceinline__ void put16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-
-// As wait_or_stop_one, by the one thread that everybody waits for: it does not sleep.
-__device__ __forceinline__ bool wait_spinning(uint64_t* bar, uint32_t parity, volatile uint32_t* stop) {
-  if (mbar_test_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_test_wait(bar, parity)) {
-    if (*stop != 0) return false;
-    if (global_timer_ns() - t0 > kWaitLimit) {
-      *stop = 1;
-      return false;
-    }
-  }
-  return true;
 }
 
 // Among the 128 threads of a set: whether any of them says yes.
@@ -248,6 +235,9 @@ __device__ __forceinline__ uint64_t weights_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>((8 * 16) >> 4) << 16) |
          (static_cast<uint64_t>((kEntries * 16) >> 4) << 32) | (1ull << 46);
 }
+
+// Whether a negative reference is still that of a head that has seen nothing.
+__device__ __forceinline__ bool begins(float nref) { return __float_as_uint(nref) == 0; }
 
 // 1 / a sum of weights, zero where nothing is seen; and its logarithm with the reference.
 __device__ __forceinline__ float e4_inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
@@ -427,8 +417,8 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       bool ok = true;
       auto scores = [&](int n) {
         const int qb = s_work & 1;
-        if (s_tile == 0) ok = wait_spinning(&sh.q_full[qb], (s_work >> 1) & 1, stop);
-        ok = ok && wait_spinning(&sh.k_full[k_stage], k_turn, stop);
+        if (s_tile == 0) ok = wait_or_stop_one(&sh.q_full[qb], (s_work >> 1) & 1, stop);
+        ok = ok && wait_or_stop_one(&sh.k_full[k_stage], k_turn, stop);
         if (!ok) return;
         fence_proxy_async_smem();
         tc_fence_after();
@@ -451,10 +441,10 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       for (int n = 0; n < last && ok; ++n) {
         if (n + 1 < last) scores(n + 1);
         if (!p.shared) {
-          ok = ok && wait_spinning(&sh.v_full[v_stage], v_turn, stop);
+          ok = ok && wait_or_stop_one(&sh.v_full[v_stage], v_turn, stop);
           fence_proxy_async_smem();
         }
-        ok = ok && wait_spinning(&sh.p_full[n & 7], (n >> 3) & 1, stop);
+        ok = ok && wait_or_stop_one(&sh.p_full[n & 7], (n >> 3) & 1, stop);
         if (!ok) break;
         tc_fence_after();
         const uint64_t vd = v_desc + static_cast<uint32_t>(v_stage * v_bytes >> 4);
@@ -566,8 +556,8 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       uint64_t sum[HS / 2];  // of the weights of two heads
 #pragma unroll
       for (int h = 0; h < HS / 2; ++h) sum[h] = 0;
-      if (e < HS) nref[e] = e < heads ? -kNothing : kNothing;
-      bool ok = true;
+      if (e < HS) nref[e] = e < heads ? 0.0f : kNothing;
+      bool ok = true, fresh = true;  // a head of the set has seen nothing yet
       if (tiles > 0) ok = wait_or_stop(&sh.units[nw & 3], (nw >> 2) & 1, stop);
       set_sync(set);
       // A wait that ran out ends nothing here: the set's threads stay together, and
@@ -580,11 +570,9 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         const float ks = notes.ks[e], vs = notes.vs[e];
         const bool seen = (notes.seen[e >> 5] >> (e & 31)) & 1;
         const float log_vs = log2_fast(fmaxf(fabsf(vs), kLeast));
-        // Logits in units of log 2, two heads at a time: less the references, and if a
-        // weight is then too large (or the first tile's), as they are.
+        // Logits in units of log 2, two heads at a time, less the references.
         uint64_t z[HS / 2];
-        bool move = i == 0;
-        for (;;) {
+        {
           {
             uint32_t v[TERMS][HS];
             const uint32_t s_at = tmem_s + (at & 1) * N + lanes + set * HS;
@@ -639,20 +627,17 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           for (int h = 0; h < HS / 2; h += 2) {
             const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&unit[h]), r = *reinterpret_cast<const ulonglong2*>(&held[h]);
             const uint64_t c0 = plain ? mul2(factor, u.x) : factor, c1 = plain ? mul2(factor, u.y) : factor;
-            z[h] = fma2(z[h], c0, move ? 0 : r.x), z[h + 1] = fma2(z[h + 1], c1, move ? 0 : r.y);
+            z[h] = fma2(z[h], c0, r.x), z[h + 1] = fma2(z[h + 1], c1, r.y);
           }
-          if (move) break;
-          float high = -FLT_MAX;
-#pragma unroll
-          for (int h = 0; h < HS / 2; ++h) {
-            const float2 y = both(z[h]);
-            high = fmaxf(high, fmaxf(y.x, y.y));
-          }
-          move = set_any(set, seen && high > kLogLimit - log_vs);
-          if (!move) break;
         }
-        if (move) {
-          // Move the references, by whole numbers, to leave the largest weight in (2^4, 2^5].
+        float high = -FLT_MAX;
+#pragma unroll
+        for (int h = 0; h < HS / 2; ++h) {
+          const float2 y = both(z[h]);
+          high = fmaxf(high, fmaxf(y.x, y.y));
+        }
+        if (set_any(set, seen && (fresh || high + log_vs > kLogLimit))) {
+          // Move the references, by whole numbers.
           float w[HS];  // a NaN is no maximum
 #pragma unroll
           for (int h = 0; h < HS; ++h) {
@@ -664,33 +649,42 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           set_sync(set);
           if (e < HS) {
             const float(*m)[HS] = &sh.most[set * 4];
-            const float top = fmaxf(fmaxf(m[0][e], m[1][e]), fmaxf(m[2][e], m[3][e]));
-            const float was = -nref[e], moved = fmaxf(was, ceilf(top) - 5.0f);
-            sh.factor[set * HS + e] = moved == was ? 1.0f : exp2_fast(was - moved);
-            nref[e] = -moved;
+            const float top = fmaxf(fmaxf(m[0][e], m[1][e]), fmaxf(m[2][e], m[3][e])), by = ceilf(top) - (begins(nref[e]) ? 4.0f : 5.0f);
+            // From nothing to where the first logits are; then up where a weight is too large:
+            // what a head's references are depends on its own logits alone.
+            const bool first = begins(nref[e]), moves = e < heads && (first ? by > -1e30f : top > kLogLimit);
+            sh.step[set * HS + e] = moves ? -by : 0.0f;
+            sh.factor[set * HS + e] = moves && !first ? exp2_fast(-by) : 1.0f;
+            if (moves) nref[e] = nref[e] == by ? -0.0f : nref[e] - by;
           }
           set_sync(set);
+          const uint64_t* step = reinterpret_cast<const uint64_t*>(sh.step + set * HS);
 #pragma unroll
-          for (int h = 0; h < HS / 2; ++h) z[h] = add2(z[h], held[h]);
+          for (int h = 0; h < HS / 2; ++h) z[h] = add2(z[h], step[h]);
           if (i > 0) {
-            const uint64_t* factor = reinterpret_cast<const uint64_t*>(sh.factor + set * HS);
-#pragma unroll
-            for (int h = 0; h < HS / 2; ++h) sum[h] = mul2(sum[h], factor[h]);
             ok = wait_or_stop(&sh.pv_done[(at - 1) & 7], ((at - 1) >> 3) & 1, stop) && ok;
             tc_fence_after();
-            for (int m = 0; m < p.v_blocks; ++m)
-#pragma unroll 1
-              for (int t = 0; t < TERMS; ++t) {
-                uint32_t v[HS];
-                const uint32_t o_at = tmem_o + m * N + lanes + t * G + set * HS;
-                tmem_ld(v, o_at);
-                tmem_wait_ld(v);
+            const ulonglong2* factor = reinterpret_cast<const ulonglong2*>(sh.factor + set * HS);
 #pragma unroll
-                for (int h = 0; h < HS; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * sh.factor[set * HS + h]);
-                tmem_st(o_at, v);
-              }
+            for (int h = 0; h < HS / 4; ++h) {
+              const ulonglong2 f = factor[h];
+              sum[2 * h] = mul2(sum[2 * h], f.x), sum[2 * h + 1] = mul2(sum[2 * h + 1], f.y);
+            }
+            // eight columns at a time: more would not leave registers for the logits
+#pragma unroll 1
+            for (int c = 0; c < p.v_blocks * TERMS * (HS / 8); ++c) {
+              const int block = c / (HS / 8), at8 = (c % (HS / 8)) * 8;
+              const uint32_t o_at = tmem_o + (block / TERMS) * N + lanes + (block % TERMS) * G + set * HS + at8;
+              uint32_t v[8];
+              tmem_ld(v, o_at);
+              tmem_wait_ld(v);
+#pragma unroll
+              for (int h = 0; h < 8; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * sh.factor[set * HS + at8 + h]);
+              tmem_st(o_at, v);
+            }
             tmem_wait_st();
           }
+          fresh = set_any(set, e < heads && begins(nref[e]));
         }
         uint32_t words[TERMS][HS / 4];  // the weights' terms, four heads each
 #pragma unroll
@@ -724,8 +718,6 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       }
 
       // ---- end of a work ----
-      if (tiles > 0) ok = wait_or_stop(&sh.pv_done[(n + tiles - 1) & 7], ((n + tiles - 1) >> 3) & 1, stop) && ok;
-      tc_fence_after();
       float sums[HS];
 #pragma unroll
       for (int h = 0; h < HS; ++h) {
@@ -739,15 +731,22 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         const float(*m)[HS] = &sh.sum[set * 4];
         const float total = (m[0][e] + m[1][e]) + (m[2][e] + m[3][e]);
         if (cluster > 1) {
-          sh.head_ref[set * HS + e] = -nref[e], sh.head_sum[set * HS + e] = total;
+          sh.head_ref[set * HS + e] = begins(nref[e]) ? kNothing : -nref[e], sh.head_sum[set * HS + e] = total;
         } else {
           sh.inverse[set * HS + e] = e4_inverse(total);
           if (a.lse != nullptr && e < heads) a.lse[k.row * a.Hq + k.head0 + set * HS + e] = e4_logsum(-nref[e], total);
         }
       }
       set_sync(set);
-      const float* inverse = sh.inverse + set * HS;
-      E* out = static_cast<E*>(a.out) + (k.row * a.Hq + k.head0 + set * HS) * a.Dv;
+      if (tiles > 0 && !wait_or_stop(&sh.pv_done[(n + tiles - 1) & 7], ((n + tiles - 1) >> 3) & 1, stop)) ok = false;
+      tc_fence_after();
+      // Results by way of the set's own units of the weights' buffers, which are free: a
+      // thread has one element of every head, and writes 16 bytes of one. Four heads, of up
+      // to 512 bytes, a unit.
+      auto row_of = [&](int h) {
+        const int unit = h / 4, buf = HS == 16 ? unit / TERMS : unit, t = HS == 16 ? unit % TERMS : 0;
+        return smem + p.p_at + buf * S::p_bytes + (t * SETS + set) * (kEntries * 16) + (h & 3) * 512;
+      };
       const int pad = p.v_blocks * 128;
       float* rows = reinterpret_cast<float*>(smem) + set * HS * pad;
       for (int m = 0; m < p.v_blocks; ++m) {
@@ -771,11 +770,28 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         const int d = m * 128 + e;
         if (cluster > 1) {
 #pragma unroll
-          for (int h = 0; h < HS; ++h) rows[h * pad + d] = x[h];
+          for (int h = 0; h < HS; ++h) rows[h * pad + d] = ok ? x[h] : __int_as_float(0x7fc00000);
         } else if (d < a.Dv) {
 #pragma unroll
-          for (int h = 0; h < HS; ++h)
-            if (h < heads) out[static_cast<int64_t>(h) * a.Dv + d] = E(x[h] * inverse[h]);
+          for (int h = 0; h < HS; h += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&sh.inverse[set * HS + h]);
+            E* row = reinterpret_cast<E*>(row_of(h)) + d;
+            row[0] = E(ok ? x[h] * f.x : __int_as_float(0x7fc00000));
+            row[256] = E(ok ? x[h + 1] * f.y : __int_as_float(0x7fc00000));
+            row[512] = E(ok ? x[h + 2] * f.z : __int_as_float(0x7fc00000));
+            row[768] = E(ok ? x[h + 3] * f.w : __int_as_float(0x7fc00000));
+          }
+        }
+      }
+      if (cluster == 1) {
+        set_sync(set);
+        const int units = a.Dv / 8;  // of 16 bytes, up to 32
+#pragma unroll
+        for (int j = 0; j < HS / 4; ++j) {
+          const int h = (warp & 3) * (HS / 4) + j;
+          if (h < heads && lane < units)
+            reinterpret_cast<uint4*>(static_cast<E*>(a.out) + (k.row * a.Hq + k.head0 + set * HS + h) * a.Dv)[lane] =
+                reinterpret_cast<const uint4*>(row_of(h))[lane];
         }
       }
       tc_fence_before();  // O is read: the next work's first weights say so

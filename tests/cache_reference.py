@@ -95,12 +95,12 @@ def entries(cache, scales):
 def attention(q, k, v, k_scales, v_scales, indices, table, query_positions, scale, softcap=0.0, slopes=None, first=None):
     """(out, its bound, lse, its bound). As step_reference.attention, with what this form rounds: a query's terms
     end at half a step of 2^-20 (bf16) or 2^-24 of its largest element; a weight is rounded to fp16 and to 9 bits
-    (bf16) or to fp16, and ends at half a step of 2^-17 or 2^-21 of the largest weight, each times its value's scale."""
+    (bf16) or to fp16, and ends at half a step of 2^-16 or 2^-20 of the largest weight, each times its value's scale."""
     B, T, Hq, D = q.shape
     pages, ps, Hkv, Dv = v.shape
     q_type, U, three = q.dtype, R.U, q.dtype == torch.float16
     rounded = 2.0 ** -11 if three else 2.0 ** -9 + 2.0 ** -11
-    query_end, weight_end = (2.0 ** -25, 2.0 ** -22) if three else (2.0 ** -21, 2.0 ** -18)
+    query_end, weight_end = (2.0 ** -25, 2.0 ** -21) if three else (2.0 ** -21, 2.0 ** -17)
     hs, tiny = R.half_step(q.dtype), torch.finfo(q.dtype).tiny * torch.finfo(q.dtype).eps
     (kf, ku), (vf, vu) = entries(k, k_scales), entries(v, v_scales)
     kf, ku, vf, vu = kf.reshape(-1, Hkv, D), ku.reshape(-1, Hkv), vf.reshape(-1, Hkv, Dv), vu.reshape(-1, Hkv)
