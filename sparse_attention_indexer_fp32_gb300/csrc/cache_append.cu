@@ -9,11 +9,14 @@
 //
 // The work. Memory bound: each element is read once and written once, in half or
 // a quarter of its size. The tokens of a block follow one another, so a CTA takes
-// the runs of tokens that begin in its share of the call, whole, for up to four
+// the runs of tokens that begin in its share of the call, whole, for one or two
 // heads of one side (keys or values): it finds the runs from the slots alone, the
-// largest size of each run and head by an integer maximum in shared memory
-// (sizes are not negative), then reads its tokens again from L1, turns and rounds
-// them. No atomics to memory, no workspace; every block's scale has one writer.
+// largest size of each run and head by an integer maximum in shared memory (sizes
+// are not negative), then turns and rounds its tokens. A thread has 32 bytes of a
+// token's heads, in registers from the one step to the other where the CTA's
+// tokens fit its threads (a prompt's block does), from L1 otherwise; sine and
+// cosine are computed while its loads are in flight. No atomics to memory, no
+// workspace; every block's scale has one writer.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -27,8 +30,9 @@
 namespace tki {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRuns = 64;  // tokens whose runs a CTA takes, so runs of a CTA
+constexpr int kMostThreads = 512;
+constexpr int kRuns = 64;     // tokens whose runs a CTA takes, so runs of a CTA
+constexpr int kMostHeads = 2;  // of a CTA
 
 struct AppendSide {
   const void* x;
@@ -38,7 +42,7 @@ struct AppendSide {
   float* scales;
   int32_t D, rotated, offset;
   int32_t turn_items, items;  // of a head: items that turn pairs, and with those that do not
-  bool vector;                // 16-byte items; otherwise a pair, or one element, each
+  bool vector;                // items of two 16-byte units; otherwise of a pair, or one element
   bool rows16;                // entries of the cache in whole 16-byte units
 };
 
@@ -61,8 +65,8 @@ struct AppendShared {
   unsigned long long leads;                 // bit per token of the share: it begins a run
   int64_t end;                              // of the last run
   int32_t first[kRuns], block[kRuns];       // of a run: least place, and block of the cache
-  uint32_t size[kThreads];                  // of a run and head: the largest size / 2, as its bits
-  float unit[kThreads], ratio[kThreads];    // 1 / scale; what its earlier entries are multiplied by
+  uint32_t size[kRuns * kMostHeads];        // of a run and head: the largest size / 2, as its bits
+  float unit[kRuns * kMostHeads], ratio[kRuns * kMostHeads];  // 1 / scale; what its earlier entries are multiplied by
 };
 
 // The smallest power of two s >= 2^-126 with 2 half <= 448 s = 1.75 2^8 s.
@@ -73,20 +77,22 @@ __device__ __forceinline__ float scale_for(float half) {
   return __uint_as_float(static_cast<uint32_t>(max(n, -126) + 127) << 23);
 }
 
-// One side of a CTA. V elements an item side; items and layouts as in rotary.cu,
-// V = 2 where nothing is aligned.
+// One side of a CTA. An item that turns holds two units of V elements: of the first
+// half and of the second (HALF), or one behind the other; so does one that does not.
+// Without `vector` (V = 2) it holds one pair, or one element.
 template <typename E, int V, bool HALF, bool SCALED, int U>
-__device__ __forceinline__ void append_side(const AppendParams& p, const AppendSide& s, AppendShared& sh, bool turns_any) {
+__device__ __forceinline__ void append_side(const AppendParams& p, const AppendSide& s, AppendShared& sh) {
   constexpr bool kVector = sizeof(E) * V == 16;
-  constexpr int kPairs = !kVector ? 1 : HALF ? V : V / 2;  // of an item
+  constexpr int kPairs = kVector ? V : 1;  // of an item
   using VecT = Vec<E, V>;
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
   const int64_t share = blockIdx.x / static_cast<unsigned>(p.head_groups);
   const int h0 = static_cast<int>(blockIdx.x - share * p.head_groups) * U;
   const int heads = min(p.H - h0, U);
   const int64_t t0 = share * p.share, t1 = min(t0 + p.share, static_cast<int64_t>(p.T));
-  const int per = min(s.items, kThreads);
-  const int sub = tid / per, i0 = tid - sub * per, side_by_side = kThreads / per;
+  const int per = min(s.items, threads);
+  const int sub = tid / per, i0 = tid - sub * per, side_by_side = threads / per;
+  const int pairs = s.rotated / 2, units = s.rotated / V, rest = (s.D - s.rotated) / V;
   auto slot_of = [&](int64_t t) -> int32_t {  // -1: not written
     const int32_t slot = p.slots[t];
     return slot >= 0 && slot < p.num_slots ? slot : -1;
@@ -96,21 +102,79 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
     return slot < 0 ? -1 : slot / p.block;
   };
 
-  if (turns_any)
-    for (int i = tid; i < s.rotated / 2; i += kThreads) sh.rates[i] = turns_of(p.frequencies[i]);
+  // ---- an item of a token ----
+  const E* x = static_cast<const E*>(s.x) + h0 * s.x_head;
+  struct Item {
+    bool turns, two;  // it turns pairs; it has a second unit, or a pair's second element
+    int at, other;    // of the first and the second in the head
+  };
+  auto item_of = [&](int i) -> Item {
+    auto past = [&](int at) { return at >= s.offset && s.rotated > 0 ? at + s.rotated : at; };
+    Item m;
+    m.turns = i < s.turn_items;
+    if (!kVector) {
+      m.two = m.turns;
+      m.at = m.turns ? s.offset + i * (HALF ? 1 : 2) : past(i - s.turn_items);
+      m.other = m.at + (HALF ? pairs : 1);
+    } else if (m.turns && HALF) {
+      m.two = true, m.at = s.offset + i * V, m.other = m.at + pairs;
+    } else if (m.turns) {
+      m.two = 2 * i + 1 < units, m.at = s.offset + 2 * i * V, m.other = m.at + V;
+    } else {
+      const int u = 2 * (i - s.turn_items);
+      m.two = u + 1 < rest, m.at = past(u * V), m.other = past((u + 1) * V);
+    }
+    return m;
+  };
+  VecT a[U], b[U];
+  float cosines[kPairs], sines[kPairs];
+  auto load = [&](int64_t t, const Item& m) {
+    const E* from = x + t * s.x_token;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u >= heads) continue;
+      if constexpr (kVector) {
+        a[u] = load16<VecT>(from + u * s.x_head + m.at);
+        if (m.two) b[u] = load16<VecT>(from + u * s.x_head + m.other);
+      } else {
+        a[u].e[0] = from[u * s.x_head + m.at];
+        if (m.two) a[u].e[1] = from[u * s.x_head + m.other];
+      }
+    }
+  };
+  auto angles = [&](int64_t t, int i, const Item& m) {
+    if (!m.turns) return;
+    const int64_t pos = p.positions_64 ? static_cast<const int64_t*>(p.positions)[t] : static_cast<const int32_t*>(p.positions)[t];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      const int pair = i * kPairs + j;
+      const uint64_t turn = static_cast<uint64_t>(pos) * sh.rates[pair < pairs ? pair : 0];
+      const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+      // 2^-21 by the special function unit: 2^-10 of a 16-bit result's
+      // rounding, 2^-17 of an 8-bit one's; FP32 takes the full functions.
+      if constexpr (SCALED || sizeof(E) == 2)
+        __sincosf(half_turns * 3.14159265f, &sines[j], &cosines[j]);
+      else
+        sincospif(half_turns, &sines[j], &cosines[j]);
+      cosines[j] *= p.scale, sines[j] *= p.scale;
+    }
+  };
+
+  for (int i = tid; i < pairs; i += threads) sh.rates[i] = turns_of(p.frequencies[i]);
   int64_t begin = t0, end = t1;
   unsigned long long leads = 0;
   int runs = 0;
   float before = 0.0f;  // the scale that this thread's run and head has
   if constexpr (SCALED) {
-    sh.size[tid] = 0;
+    for (int i = tid; i < kRuns * U; i += threads) sh.size[i] = 0;
     if (tid < kRuns) sh.first[tid] = INT32_MAX;
     if (tid < 32) {
 #pragma unroll
       for (int part = 0; part < kRuns; part += 32) {
         const int64_t t = t0 + part + lane;
         const int32_t block = t < t1 ? block_of(t) : -1;
-        const bool lead = block >= 0 && (t == 0 || block_of(t - 1) != block);
+        const int32_t last = t < t1 && t > 0 ? block_of(t - 1) : -1;
+        const bool lead = block >= 0 && last != block;
         const uint32_t bits = __ballot_sync(0xffffffffu, lead);
         if (lead) sh.block[__popcll(leads) + __popc(bits & ((1u << lane) - 1))] = block;
         leads |= static_cast<unsigned long long>(bits) << part;
@@ -131,66 +195,75 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
     if (leads == 0) return;
     runs = __popcll(leads);
     begin = t0 + __ffsll(static_cast<long long>(leads)) - 1;
-    const int r = tid / U;
+    const int r = tid / U;  // threads >= kRuns * U: one each
     if (r < runs && tid % U < heads) before = s.scales[static_cast<int64_t>(sh.block[r]) * p.H + h0 + tid % U];
   } else {
     __syncthreads();
   }
   // The run of a token between begin and end that is written.
   auto run_of = [&](int64_t t) { return t < t1 ? __popcll(leads & ((2ull << (t - t0)) - 1)) - 1 : runs - 1; };
-
-  // An item of a token's head.
-  const E* x = static_cast<const E*>(s.x) + h0 * s.x_head;
-  const int pairs = s.rotated / 2;
-  const int partner = HALF ? pairs : 1;  // of the unaligned item's first element
-  auto place_of = [&](int i) {
-    if (i < s.turn_items) return s.offset + i * (HALF && !kVector ? 1 : V);
-    const int at = (i - s.turn_items) * (kVector ? V : 1);
-    return at >= s.offset && s.rotated > 0 ? at + s.rotated : at;
-  };
-  auto load = [&](const E* from, bool turns, VecT& a, VecT& b) {
-    if constexpr (kVector) {
-      a = load16<VecT>(from);
-      if (HALF && turns) b = load16<VecT>(from + pairs);
-    } else {
-      a.e[0] = from[0];
-      if (turns) a.e[1] = from[partner];
-    }
-  };
+  const bool once = end - begin <= side_by_side && s.items <= threads;  // what is loaded stays
 
   if constexpr (SCALED) {
-    // ---- the largest sizes ----
-    for (int64_t t = begin + sub; sub < side_by_side && t < end; t += side_by_side) {
-      const int32_t slot = slot_of(t);
-      if (slot < 0) continue;
-      const int run = run_of(t);
-      if (i0 == 0) atomicMin(&sh.first[run], slot % p.block);
-      for (int i = i0; i < s.items; i += per) {
-        const bool turns = i < s.turn_items;
-        const E* from = x + t * s.x_token + place_of(i);
-        VecT a[U], b[U];
+    // ---- the largest sizes; a warp's threads stay together ----
+    for (int64_t t = begin + sub, from = begin; from < end; t += side_by_side, from += side_by_side) {
+      const int32_t slot = sub < side_by_side && t < end ? slot_of(t) : -1;
+      const int run = slot >= 0 ? run_of(t) : -1;
+      if (slot >= 0 && i0 == 0) atomicMin(&sh.first[run], slot % p.block);
+      uint32_t most[U] = {};
+      if (slot >= 0) {
+        for (int i = i0; i < s.items; i += per) {
+          const Item m = item_of(i);
+          load(t, m);
+          if (once) angles(t, i, m);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (u < heads) load(from + u * s.x_head, turns, a[u], b[u]);
+          for (int u = 0; u < U; ++u) {
+            if (u >= heads) continue;
+            float high = 0.0f;
+            auto count = [&](float size) {  // a NaN or an infinity does not count
+              if (size <= FLT_MAX) high = fmaxf(high, size);
+            };
+            auto half = [](E e) { return 0.5f * fabsf(Elem<E>::get(e)); };
+            if (!kVector) {
+              if (m.turns)
+                count((half(a[u].e[0]) + half(a[u].e[1])) * fabsf(p.scale));
+              else
+                count(half(a[u].e[0]));
+            } else if (m.turns) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (u >= heads) continue;
-          float most = 0.0f;
-          auto count = [&](float size) {  // a NaN or an infinity does not count
-            if (size <= FLT_MAX) most = fmaxf(most, size);
-          };
-          auto half = [](E e) { return 0.5f * fabsf(Elem<E>::get(e)); };
-          if (turns) {
+              for (int j = 0; j < V; ++j) {
+                if (HALF)
+                  count((half(a[u].e[j]) + half(b[u].e[j])) * fabsf(p.scale));
+                else if (j % 2 == 0)
+                  count((half(a[u].e[j]) + half(a[u].e[j + 1])) * fabsf(p.scale));
+              }
+              if (!HALF && m.two) {
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
-              const E second = HALF && kVector ? b[u].e[j] : a[u].e[2 * j + 1];
-              count((half(a[u].e[HALF ? j : 2 * j]) + half(second)) * fabsf(p.scale));
+                for (int j = 0; j < V; j += 2) count((half(b[u].e[j]) + half(b[u].e[j + 1])) * fabsf(p.scale));
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < V; ++j) count(half(a[u].e[j]));
+              if (m.two) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) count(half(b[u].e[j]));
+              }
             }
-          } else {
-#pragma unroll
-            for (int j = 0; j < (kVector ? V : 1); ++j) count(half(a[u].e[j]));
+            most[u] = max(most[u], __float_as_uint(high));
           }
-          atomicMax(&sh.size[run * U + u], __float_as_uint(most));
+        }
+      }
+      // one number a warp where it is all of one run (or idle), one a thread otherwise
+      const int any = __reduce_max_sync(0xffffffffu, run);
+      const bool same = __all_sync(0xffffffffu, run < 0 || run == any);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u >= heads || any < 0) continue;
+        if (same) {
+          const uint32_t all = __reduce_max_sync(0xffffffffu, most[u]);
+          if (lane == 0) atomicMax(&sh.size[any * U + u], all);
+        } else if (run >= 0) {
+          atomicMax(&sh.size[run * U + u], most[u]);
         }
       }
     }
@@ -216,51 +289,36 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
     const int64_t entry = page * s.page + (slot - page * p.page_size) * s.entry + h0 * s.head;
     const int run = SCALED ? run_of(t) : 0;
     for (int i = i0; i < s.items; i += per) {
-      const bool turns = i < s.turn_items;
-      const int at = place_of(i);
-      const E* from = x + t * s.x_token + at;
-      VecT a[U], b[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < heads) load(from + u * s.x_head, turns, a[u], b[u]);
-      float cosines[kPairs], sines[kPairs];
-      if (turns) {
-        const int64_t pos = p.positions_64 ? static_cast<const int64_t*>(p.positions)[t] : static_cast<const int32_t*>(p.positions)[t];
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-          const uint64_t turn = static_cast<uint64_t>(pos) * sh.rates[i * kPairs + j];
-          const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
-          // 2^-21 by the special function unit: 2^-10 of a 16-bit result's
-          // rounding, 2^-17 of an 8-bit one's; FP32 takes the full functions.
-          if constexpr (SCALED || sizeof(E) == 2)
-            __sincosf(half_turns * 3.14159265f, &sines[j], &cosines[j]);
-          else
-            sincospif(half_turns, &sines[j], &cosines[j]);
-          cosines[j] *= p.scale, sines[j] *= p.scale;
-        }
-      }
+      const Item m = item_of(i);
+      if (!SCALED || !once) load(t, m), angles(t, i, m);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (u >= heads) continue;
-        float y[V], z[V];  // the item's elements, and with HALF their partners
+        float y[V], z[V];  // the item's elements, of the second unit in z
         if constexpr (kVector) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) y[j] = Elem<E>::get(a[u].e[j]), z[j] = HALF ? Elem<E>::get(b[u].e[j]) : 0.0f;
+          for (int j = 0; j < V; ++j) y[j] = Elem<E>::get(a[u].e[j]), z[j] = m.two ? Elem<E>::get(b[u].e[j]) : 0.0f;
         } else {
-          y[0] = Elem<E>::get(a[u].e[0]), y[1] = turns ? Elem<E>::get(a[u].e[1]) : 0.0f;
+          y[0] = Elem<E>::get(a[u].e[0]), y[1] = m.two ? Elem<E>::get(a[u].e[1]) : 0.0f;
         }
-        if (turns) {
-#pragma unroll
-          for (int j = 0; j < kPairs; ++j) {
-            float& first = y[HALF ? j : 2 * j];
-            float& second = HALF && kVector ? z[j] : y[2 * j + 1];
+        if (m.turns) {
+          auto turn = [&](float& first, float& second, int j) {
             const float r = first, q = second;
             first = r * cosines[j] - q * sines[j];
             second = q * cosines[j] + r * sines[j];
+          };
+          if constexpr (!kVector) {
+            turn(y[0], y[1], 0);
+          } else if constexpr (HALF) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) turn(y[j], z[j], j);
+          } else {
+#pragma unroll
+            for (int j = 0; j < V; j += 2) turn(y[j], y[j + 1], j / 2), turn(z[j], z[j + 1], (V + j) / 2);
           }
         }
         if constexpr (SCALED) {
-          uint8_t* to = static_cast<uint8_t*>(s.cache) + entry + u * s.head + at;
+          uint8_t* to = static_cast<uint8_t*>(s.cache) + entry + u * s.head;
           const float unit = sh.unit[run * U + u];
           // a product with 0 is 0, or NaN of what is not finite
           auto two = [&](float m, float n) { return e4m3_two(fmaf(m, unit, m * 0.0f), fmaf(n, unit, n * 0.0f)); };
@@ -274,28 +332,28 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
               else
                 *reinterpret_cast<uint32_t*>(to) = w[0];
             };
-            put(to, y);
-            if (HALF && turns) put(to + pairs, z);
+            put(to + m.at, y);
+            if (m.two) put(to + m.other, z);
           } else {
             const uint32_t w = two(y[0], y[1]);
-            to[0] = static_cast<uint8_t>(w);
-            if (turns) to[partner] = static_cast<uint8_t>(w >> 8);
+            to[m.at] = static_cast<uint8_t>(w);
+            if (m.two) to[m.other] = static_cast<uint8_t>(w >> 8);
           }
         } else {
-          E* to = static_cast<E*>(s.cache) + entry + u * s.head + at;
+          E* to = static_cast<E*>(s.cache) + entry + u * s.head;
           if constexpr (kVector) {
             VecT c;
 #pragma unroll
             for (int j = 0; j < V; ++j) c.e[j] = Elem<E>::put(y[j]);
-            store16(to, c);
-            if (HALF && turns) {
+            store16(to + m.at, c);
+            if (m.two) {
 #pragma unroll
               for (int j = 0; j < V; ++j) c.e[j] = Elem<E>::put(z[j]);
-              store16(to + pairs, c);
+              store16(to + m.other, c);
             }
           } else {
-            to[0] = Elem<E>::put(y[0]);
-            if (turns) to[partner] = Elem<E>::put(y[1]);
+            to[m.at] = Elem<E>::put(y[0]);
+            if (m.two) to[m.other] = Elem<E>::put(y[1]);
           }
         }
       }
@@ -304,7 +362,7 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
 
   if constexpr (SCALED) {
     // ---- earlier entries of blocks whose scale grew, one run and head a warp ----
-    for (int j = tid >> 5; j < runs * U; j += kThreads / 32) {
+    for (int j = tid >> 5; j < runs * U; j += threads / 32) {
       const int r = j / U, u = j - r * U;
       if (u >= heads || sh.ratio[j] == 1.0f) continue;
       const float ratio = sh.ratio[j];
@@ -350,13 +408,13 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
 }
 
 template <typename E, bool HALF, bool SCALED, int U>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kMostThreads, 2) append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ AppendShared sh;
   const AppendSide& s = p.side[blockIdx.y];
   if (s.vector)
-    append_side<E, 16 / sizeof(E), HALF, SCALED, U>(p, s, sh, s.rotated > 0);
+    append_side<E, 16 / sizeof(E), HALF, SCALED, U>(p, s, sh);
   else
-    append_side<E, 2, HALF, SCALED, U>(p, s, sh, s.rotated > 0);
+    append_side<E, 2, HALF, SCALED, U>(p, s, sh);
 }
 
 bool aligned_to(const void* q, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(q) & (bytes - 1)) == 0; }
@@ -364,26 +422,22 @@ bool aligned_to(const void* q, uintptr_t bytes) { return (reinterpret_cast<uintp
 template <typename E, bool HALF, bool SCALED>
 topk_status launch_layout(const AppendParams& p, int sides, int sm_count, cudaStream_t stream) {
   AppendParams q = p;
-  auto groups = [&](int share, int u) { return ((static_cast<int64_t>(p.T) + share - 1) / share) * ((p.H + u - 1) / u); };
-  // Four heads a thread share their tokens' angles and have their loads in
-  // flight together; one where that leaves SMs idle.
-  int most = 1;  // tokens of one CTA side by side
-  for (int i = 0; i < sides; ++i) {
-    const int per = q.side[i].items < kThreads ? q.side[i].items : kThreads;
-    if (kThreads / per > most) most = kThreads / per;
-  }
+  int items = 0;  // of a token
+  for (int i = 0; i < sides; ++i) items += p.side[i].items;
+  // Many tokens: CTAs of 512 threads, which a block of 64 tokens with heads of 128
+  // fits, and two heads a thread. Few: small CTAs, so that all SMs have some.
+  const bool many = static_cast<double>(p.T) * p.H * items >= 1024.0 * sm_count;
+  const int u = many ? 2 : 1, threads = many ? kMostThreads : 128;
+  auto groups = [&](int share) { return ((static_cast<int64_t>(p.T) + share - 1) / share) * ((p.H + u - 1) / u); };
   int share = kRuns;
-  const bool four = groups(share, 4) * sides >= 2 * sm_count;
-  const int u = four ? 4 : 1;
-  while (share > 1 && groups(share, u) * sides < sm_count) share /= 2;
-  if (!SCALED)
-    while (share > 1 && share > most) share /= 2;
+  const int side_by_side = threads / (items / sides < threads ? items / sides : threads);
+  while (share > 1 && (groups(share) * sides < 2 * sm_count || (!SCALED && share > side_by_side))) share /= 2;
   q.share = share;
   q.head_groups = (p.H + u - 1) / u;
-  const int64_t grid = groups(share, u);
+  const int64_t grid = groups(share);
   if (grid > INT32_MAX) return TOPK_EINVAL;
   const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>(sides));
-  return launch(four ? append_kernel<E, HALF, SCALED, 4> : append_kernel<E, HALF, SCALED, 1>, q, g, kThreads, 0, stream);
+  return launch(many ? append_kernel<E, HALF, SCALED, 2> : append_kernel<E, HALF, SCALED, 1>, q, g, threads, 0, stream);
 }
 
 template <typename E>
@@ -410,9 +464,9 @@ topk_status launch_typed(const sparse_append_args& a, int sm_count, cudaStream_t
     s.vector = aligned_to(s.x, 16) && aligned_to(s.cache, static_cast<uintptr_t>(V * size)) && whole(s.x_token) && whole(s.x_head) &&
                whole(s.page) && whole(s.entry) && whole(s.head) && whole(s.D) && whole(s.offset) &&
                whole(half ? s.rotated / 2 : s.rotated);
-    const int pairs = s.rotated / 2;
-    s.turn_items = s.vector ? (half ? pairs / V : s.rotated / V) : pairs;
-    s.items = s.turn_items + (s.D - s.rotated) / (s.vector ? V : 1);
+    // two units an item
+    s.turn_items = s.vector ? (s.rotated / V + 1) / 2 : s.rotated / 2;
+    s.items = s.turn_items + (s.vector ? ((s.D - s.rotated) / V + 1) / 2 : s.D - s.rotated);
     s.rows16 = aligned_to(s.cache, 16) && s.page % 16 == 0 && s.entry % 16 == 0 && s.head % 16 == 0 && s.D % 16 == 0;
   }
   if (scaled) return half ? launch_layout<E, true, true>(p, sides, sm_count, stream) : launch_layout<E, false, true>(p, sides, sm_count, stream);

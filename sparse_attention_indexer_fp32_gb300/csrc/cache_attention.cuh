@@ -240,9 +240,9 @@ __device__ __forceinline__ uint64_t weights_desc(uint32_t addr) {
 __device__ __forceinline__ bool begins(float nref) { return __float_as_uint(nref) == 0; }
 
 // 1 / a sum of weights, zero where nothing is seen; and its logarithm with the reference.
-__device__ __forceinline__ float e4_inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+__device__ __forceinline__ float e4_inverse(float sum) { return sum == 0.0f ? 0.0f : reciprocal(sum); }
 __device__ __forceinline__ float e4_logsum(float ref, float sum) {
-  return sum != sum ? sum : sum == 0.0f ? __int_as_float(0xff800000) : (ref + log2f(sum)) * kLn2;
+  return sum != sum ? sum : sum == 0.0f ? __int_as_float(0xff800000) : (ref + log2_fast(sum)) * kLn2;
 }
 
 template <typename E, int G>
@@ -727,17 +727,17 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       const float part = sum_lanes<HS>(sums, lane);
       if (lane % (32 / HS) == 0) sh.sum[warp][lane / (32 / HS)] = part;
       set_sync(set);
+      float total = 0.0f;
       if (e < HS) {
         const float(*m)[HS] = &sh.sum[set * 4];
-        const float total = (m[0][e] + m[1][e]) + (m[2][e] + m[3][e]);
-        if (cluster > 1) {
+        total = (m[0][e] + m[1][e]) + (m[2][e] + m[3][e]);
+        if (cluster > 1)
           sh.head_ref[set * HS + e] = begins(nref[e]) ? kNothing : -nref[e], sh.head_sum[set * HS + e] = total;
-        } else {
+        else
           sh.inverse[set * HS + e] = e4_inverse(total);
-          if (a.lse != nullptr && e < heads) a.lse[k.row * a.Hq + k.head0 + set * HS + e] = e4_logsum(-nref[e], total);
-        }
       }
       set_sync(set);
+      if (cluster == 1 && a.lse != nullptr && e < heads) a.lse[k.row * a.Hq + k.head0 + set * HS + e] = e4_logsum(-nref[e], total);
       if (tiles > 0 && !wait_or_stop(&sh.pv_done[(n + tiles - 1) & 7], ((n + tiles - 1) >> 3) & 1, stop)) ok = false;
       tc_fence_after();
       // Results by way of the set's own units of the weights' buffers, which are free: a
@@ -767,19 +767,23 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
             for (int t = TERMS - 2; t >= 0; --t) x[h] = fmaf(x[h], 0x1p-4f, __uint_as_float(v[t][h]));
           }
         }
+        if (!ok) {
+#pragma unroll
+          for (int h = 0; h < HS; ++h) x[h] = __int_as_float(0x7fc00000);
+        }
         const int d = m * 128 + e;
         if (cluster > 1) {
 #pragma unroll
-          for (int h = 0; h < HS; ++h) rows[h * pad + d] = ok ? x[h] : __int_as_float(0x7fc00000);
+          for (int h = 0; h < HS; ++h) rows[h * pad + d] = x[h];
         } else if (d < a.Dv) {
 #pragma unroll
           for (int h = 0; h < HS; h += 4) {
             const float4 f = *reinterpret_cast<const float4*>(&sh.inverse[set * HS + h]);
             E* row = reinterpret_cast<E*>(row_of(h)) + d;
-            row[0] = E(ok ? x[h] * f.x : __int_as_float(0x7fc00000));
-            row[256] = E(ok ? x[h + 1] * f.y : __int_as_float(0x7fc00000));
-            row[512] = E(ok ? x[h + 2] * f.z : __int_as_float(0x7fc00000));
-            row[768] = E(ok ? x[h + 3] * f.w : __int_as_float(0x7fc00000));
+            row[0] = E(x[h] * f.x);
+            row[256] = E(x[h + 1] * f.y);
+            row[512] = E(x[h + 2] * f.z);
+            row[768] = E(x[h + 3] * f.w);
           }
         }
       }
