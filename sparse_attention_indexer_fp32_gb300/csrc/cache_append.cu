@@ -21,7 +21,9 @@
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
+#include "attention_math.cuh"
 #include "cache_launch.cuh"
 #include "e4m3.cuh"
 #include "rotary_math.cuh"
@@ -31,7 +33,7 @@ namespace tki {
 namespace {
 
 constexpr int kMostThreads = 512;
-constexpr int kRuns = 64;     // tokens whose runs a CTA takes, so runs of a CTA
+constexpr int kRuns = 64;      // tokens whose runs a CTA takes, so runs of a CTA
 constexpr int kMostHeads = 2;  // of a CTA
 
 struct AppendSide {
@@ -53,6 +55,7 @@ struct AppendParams {
   const int32_t* slots;
   int64_t num_slots;
   int32_t page_size, block;
+  int32_t page_shift, block_shift;  // log2, or -1
   int32_t T, H;
   int32_t positions_64;
   int32_t head_groups;
@@ -62,11 +65,9 @@ struct AppendParams {
 
 struct AppendShared {
   uint64_t rates[SPARSE_APPEND_MAX_D / 2];  // of the pairs, in turns a position
-  unsigned long long leads;                 // bit per token of the share: it begins a run
-  int64_t end;                              // of the last run
-  int32_t first[kRuns], block[kRuns];       // of a run: least place, and block of the cache
-  uint32_t size[kRuns * kMostHeads];        // of a run and head: the largest size / 2, as its bits
-  float unit[kRuns * kMostHeads], ratio[kRuns * kMostHeads];  // 1 / scale; what its earlier entries are multiplied by
+  int32_t first[kRuns], block[kRuns];       // of a run: the least place in its block, and that of the cache
+  uint32_t size[kRuns * kMostHeads];        // of a run and head: the largest size / 2, as its bits; then 1 / scale
+  float ratio[kRuns * kMostHeads];          // what its earlier entries are multiplied by
 };
 
 // The smallest power of two s >= 2^-126 with 2 half <= 448 s = 1.75 2^8 s.
@@ -75,6 +76,15 @@ __device__ __forceinline__ float scale_for(float half) {
   const int e = static_cast<int>(bits >> 23) - 127;
   const int n = e - 7 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
   return __uint_as_float(static_cast<uint32_t>(max(n, -126) + 127) << 23);
+}
+
+// The two numbers of 32 bits of a 16-bit type.
+template <typename E>
+__device__ __forceinline__ float2 floats_of(uint32_t two) {
+  if constexpr (std::is_same<E, __half>::value)
+    return __half22float2(*reinterpret_cast<const __half2*>(&two));
+  else
+    return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
 }
 
 // One side of a CTA. An item that turns holds two units of V elements: of the first
@@ -97,9 +107,8 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
     const int32_t slot = p.slots[t];
     return slot >= 0 && slot < p.num_slots ? slot : -1;
   };
-  auto block_of = [&](int64_t t) -> int32_t {
-    const int32_t slot = slot_of(t);
-    return slot < 0 ? -1 : slot / p.block;
+  auto block_of = [&](int32_t slot) -> int32_t {
+    return slot < 0 ? -1 : p.block_shift >= 0 ? slot >> p.block_shift : slot / p.block;
   };
 
   // ---- an item of a token ----
@@ -126,7 +135,7 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
     }
     return m;
   };
-  VecT a[U], b[U];
+  VecT a[U], b[U];  // of an item without a second unit, b is zeros
   float cosines[kPairs], sines[kPairs];
   auto load = [&](int64_t t, const Item& m) {
     const E* from = x + t * s.x_token;
@@ -135,7 +144,10 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
       if (u >= heads) continue;
       if constexpr (kVector) {
         a[u] = load16<VecT>(from + u * s.x_head + m.at);
-        if (m.two) b[u] = load16<VecT>(from + u * s.x_head + m.other);
+        if (m.two)
+          b[u] = load16<VecT>(from + u * s.x_head + m.other);
+        else
+          *reinterpret_cast<uint4*>(&b[u]) = make_uint4(0, 0, 0, 0);
       } else {
         a[u].e[0] = from[u * s.x_head + m.at];
         if (m.two) a[u].e[1] = from[u * s.x_head + m.other];
@@ -160,96 +172,129 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
     }
   };
 
-  for (int i = tid; i < pairs; i += threads) sh.rates[i] = turns_of(p.frequencies[i]);
+  // ---- the runs, which every warp finds for itself ----
   int64_t begin = t0, end = t1;
-  unsigned long long leads = 0;
+  unsigned long long leads = 0;  // bit per token of the share: it begins a run
   int runs = 0;
-  float before = 0.0f;  // the scale that this thread's run and head has
   if constexpr (SCALED) {
     for (int i = tid; i < kRuns * U; i += threads) sh.size[i] = 0;
     if (tid < kRuns) sh.first[tid] = INT32_MAX;
-    if (tid < 32) {
+    int32_t last = t0 > 0 ? block_of(slot_of(t0 - 1)) : -1;
 #pragma unroll
-      for (int part = 0; part < kRuns; part += 32) {
-        const int64_t t = t0 + part + lane;
-        const int32_t block = t < t1 ? block_of(t) : -1;
-        const int32_t last = t < t1 && t > 0 ? block_of(t - 1) : -1;
-        const bool lead = block >= 0 && last != block;
-        const uint32_t bits = __ballot_sync(0xffffffffu, lead);
-        if (lead) sh.block[__popcll(leads) + __popc(bits & ((1u << lane) - 1))] = block;
-        leads |= static_cast<unsigned long long>(bits) << part;
-      }
-      if (leads != 0) {  // the last run may go on behind the share
-        const int32_t last = block_of(t1 - 1);
-        while (last >= 0) {
-          const bool on = end + lane < p.T && block_of(end + lane) == last;
-          const uint32_t off = ~__ballot_sync(0xffffffffu, on);
-          end += off != 0 ? __ffs(off) - 1 : 32;
-          if (off != 0) break;
-        }
-      }
-      if (tid == 0) sh.leads = leads, sh.end = end;
+    for (int part = 0; part < kRuns; part += 32) {
+      if (t0 + part >= t1) continue;
+      const int64_t t = t0 + part + lane;
+      const int32_t block = t < t1 ? block_of(slot_of(t)) : -1;
+      const int32_t up = __shfl_up_sync(0xffffffffu, block, 1);
+      const bool lead = block >= 0 && (lane == 0 ? last : up) != block;
+      const uint32_t bits = __ballot_sync(0xffffffffu, lead);
+      if (lead && tid < 32) sh.block[__popcll(leads) + __popc(bits & ((1u << lane) - 1))] = block;
+      leads |= static_cast<unsigned long long>(bits) << part;
+      last = __shfl_sync(0xffffffffu, block, static_cast<int>(min(t1 - t0 - part, int64_t{32})) - 1);
     }
-    __syncthreads();
-    leads = sh.leads, end = sh.end;
     if (leads == 0) return;
+    while (last >= 0) {  // the last run may go on behind the share
+      const bool on = end + lane < p.T && block_of(slot_of(end + lane)) == last;
+      const uint32_t off = ~__ballot_sync(0xffffffffu, on);
+      end += off != 0 ? __ffs(off) - 1 : 32;
+      if (off != 0) break;
+    }
     runs = __popcll(leads);
     begin = t0 + __ffsll(static_cast<long long>(leads)) - 1;
-    const int r = tid / U;  // threads >= kRuns * U: one each
-    if (r < runs && tid % U < heads) before = s.scales[static_cast<int64_t>(sh.block[r]) * p.H + h0 + tid % U];
-  } else {
-    __syncthreads();
   }
   // The run of a token between begin and end that is written.
   auto run_of = [&](int64_t t) { return t < t1 ? __popcll(leads & ((2ull << (t - t0)) - 1)) - 1 : runs - 1; };
   const bool once = end - begin <= side_by_side && s.items <= threads;  // what is loaded stays
+  for (int i = tid; i < pairs; i += threads) sh.rates[i] = turns_of(p.frequencies[i]);
 
-  if constexpr (SCALED) {
+  bool odd = false;  // something that this thread holds may not be finite, or not its results
+  // Half the largest size of an item's heads, without what is not finite.
+  auto sizes_of = [&](const Item& m, uint32_t(&most)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u >= heads) continue;
+      float high = 0.0f;
+      bool plain = false;
+      if constexpr (kVector && sizeof(E) == 2) {
+        // the largest number as bits, two at a time: nothing is near the end of FP32's range
+        const uint32_t* wa = reinterpret_cast<const uint32_t*>(&a[u]);
+        const uint32_t* wb = reinterpret_cast<const uint32_t*>(&b[u]);
+        uint32_t bits = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bits = __vmaxu2(__vmaxu2(bits, wa[j] & 0x7fff7fffu), wb[j] & 0x7fff7fffu);
+        bits = max(bits & 0xffffu, bits >> 16);
+        plain = bits < (std::is_same<E, __half>::value ? 0x7c00u : 0x7e00u);
+        if (plain && !m.turns) {
+          high = 0.5f * floats_of<E>(bits).x;
+        } else if (plain) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = floats_of<E>(wa[j]), z = floats_of<E>(wb[j]);
+            if (HALF)
+              high = fmaxf(high, fmaxf(fmaf(fabsf(y.x), 0.5f, 0.5f * fabsf(z.x)), fmaf(fabsf(y.y), 0.5f, 0.5f * fabsf(z.y))));
+            else
+              high = fmaxf(high, fmaxf(fmaf(fabsf(y.x), 0.5f, 0.5f * fabsf(y.y)), fmaf(fabsf(z.x), 0.5f, 0.5f * fabsf(z.y))));
+          }
+          high *= fabsf(p.scale);
+          plain = high < 0x1p126f;
+        }
+      }
+      if (!plain) {
+        odd = true, high = 0.0f;
+        auto count = [&](float size) {
+          if (size <= FLT_MAX) high = fmaxf(high, size);
+        };
+        auto half = [](E e) { return 0.5f * fabsf(Elem<E>::get(e)); };
+        if (!kVector) {
+          if (m.turns)
+            count((half(a[u].e[0]) + half(a[u].e[1])) * fabsf(p.scale));
+          else
+            count(half(a[u].e[0]));
+        } else if (m.turns) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            if (HALF) {
+              count((half(a[u].e[j]) + half(b[u].e[j])) * fabsf(p.scale));
+            } else if (j % 2 == 0) {
+              count((half(a[u].e[j]) + half(a[u].e[j + 1])) * fabsf(p.scale));
+              count((half(b[u].e[j]) + half(b[u].e[j + 1])) * fabsf(p.scale));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) count(half(a[u].e[j])), count(half(b[u].e[j]));
+        }
+      }
+      most[u] = max(most[u], __float_as_uint(high));
+    }
+  };
+
+  if constexpr (!SCALED) {
+    __syncthreads();
+  } else {
     // ---- the largest sizes; a warp's threads stay together ----
-    for (int64_t t = begin + sub, from = begin; from < end; t += side_by_side, from += side_by_side) {
-      const int32_t slot = sub < side_by_side && t < end ? slot_of(t) : -1;
+    int64_t t = begin + sub;
+    int32_t slot = sub < side_by_side && t < end ? slot_of(t) : -1;
+    const Item mine = item_of(i0);
+    if (once && slot >= 0) load(t, mine);  // on their way before the shared memory is ready
+    __syncthreads();
+    if (once && slot >= 0) angles(t, i0, mine);
+    const int r = tid / U;
+    const bool has = tid < runs * U && tid % U < heads;  // a run and head: threads >= kRuns * U
+    float* scale = s.scales + (has ? static_cast<int64_t>(sh.block[r]) * p.H + h0 + tid % U : 0);
+    const float before = has ? *scale : 0.0f;
+    for (int64_t from = begin; from < end; from += side_by_side) {
       const int run = slot >= 0 ? run_of(t) : -1;
-      if (slot >= 0 && i0 == 0) atomicMin(&sh.first[run], slot % p.block);
       uint32_t most[U] = {};
       if (slot >= 0) {
-        for (int i = i0; i < s.items; i += per) {
-          const Item m = item_of(i);
-          load(t, m);
-          if (once) angles(t, i, m);
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (u >= heads) continue;
-            float high = 0.0f;
-            auto count = [&](float size) {  // a NaN or an infinity does not count
-              if (size <= FLT_MAX) high = fmaxf(high, size);
-            };
-            auto half = [](E e) { return 0.5f * fabsf(Elem<E>::get(e)); };
-            if (!kVector) {
-              if (m.turns)
-                count((half(a[u].e[0]) + half(a[u].e[1])) * fabsf(p.scale));
-              else
-                count(half(a[u].e[0]));
-            } else if (m.turns) {
-#pragma unroll
-              for (int j = 0; j < V; ++j) {
-                if (HALF)
-                  count((half(a[u].e[j]) + half(b[u].e[j])) * fabsf(p.scale));
-                else if (j % 2 == 0)
-                  count((half(a[u].e[j]) + half(a[u].e[j + 1])) * fabsf(p.scale));
-              }
-              if (!HALF && m.two) {
-#pragma unroll
-                for (int j = 0; j < V; j += 2) count((half(b[u].e[j]) + half(b[u].e[j + 1])) * fabsf(p.scale));
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < V; ++j) count(half(a[u].e[j]));
-              if (m.two) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) count(half(b[u].e[j]));
-              }
-            }
-            most[u] = max(most[u], __float_as_uint(high));
+        if (i0 == 0) atomicMin(&sh.first[run], slot - block_of(slot) * p.block);
+        if (once) {
+          sizes_of(mine, most);
+        } else {
+          for (int i = i0; i < s.items; i += per) {
+            const Item m = item_of(i);
+            load(t, m);
+            sizes_of(m, most);
           }
         }
       }
@@ -266,16 +311,17 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
           atomicMax(&sh.size[run * U + u], most[u]);
         }
       }
+      t += side_by_side;
+      slot = sub < side_by_side && t < end ? slot_of(t) : -1;
     }
     __syncthreads();
     // ---- the scales ----
-    const int r = tid / U;
-    if (r < runs && tid % U < heads) {
+    if (has) {
       const float need = scale_for(__uint_as_float(sh.size[tid]));
       const bool begins = sh.first[r] == 0;
       const float now = begins ? need : fmaxf(before, need);
-      if (begins || now != before) s.scales[static_cast<int64_t>(sh.block[r]) * p.H + h0 + tid % U] = now;
-      sh.unit[tid] = 1.0f / now;
+      if (begins || now != before) *scale = now;
+      sh.size[tid] = __float_as_uint(1.0f / now);
       sh.ratio[tid] = begins ? 1.0f : before / now;
     }
     __syncthreads();
@@ -285,7 +331,7 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
   for (int64_t t = begin + sub; sub < side_by_side && t < end; t += side_by_side) {
     const int32_t slot = slot_of(t);
     if (slot < 0) continue;
-    const int32_t page = slot / p.page_size;
+    const int32_t page = p.page_shift >= 0 ? slot >> p.page_shift : slot / p.page_size;
     const int64_t entry = page * s.page + (slot - page * p.page_size) * s.entry + h0 * s.head;
     const int run = SCALED ? run_of(t) : 0;
     for (int i = i0; i < s.items; i += per) {
@@ -294,39 +340,53 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (u >= heads) continue;
-        float y[V], z[V];  // the item's elements, of the second unit in z
+        // the item's elements, two at a time, of the second unit in z
+        constexpr int kTwos = V / 2;
+        uint64_t y[kTwos], z[kTwos];
         if constexpr (kVector) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) y[j] = Elem<E>::get(a[u].e[j]), z[j] = m.two ? Elem<E>::get(b[u].e[j]) : 0.0f;
+          for (int j = 0; j < kTwos; ++j) {
+            y[j] = pair(Elem<E>::get(a[u].e[2 * j]), Elem<E>::get(a[u].e[2 * j + 1]));
+            z[j] = pair(Elem<E>::get(b[u].e[2 * j]), Elem<E>::get(b[u].e[2 * j + 1]));
+          }
         } else {
-          y[0] = Elem<E>::get(a[u].e[0]), y[1] = m.two ? Elem<E>::get(a[u].e[1]) : 0.0f;
+          y[0] = pair(Elem<E>::get(a[u].e[0]), m.two ? Elem<E>::get(a[u].e[1]) : 0.0f), z[0] = 0;
         }
         if (m.turns) {
-          auto turn = [&](float& first, float& second, int j) {
-            const float r = first, q = second;
-            first = r * cosines[j] - q * sines[j];
-            second = q * cosines[j] + r * sines[j];
-          };
-          if constexpr (!kVector) {
-            turn(y[0], y[1], 0);
-          } else if constexpr (HALF) {
+          if constexpr (kVector && HALF) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) turn(y[j], z[j], j);
+            for (int j = 0; j < kTwos; ++j) {
+              const uint64_t c = pair(cosines[2 * j], cosines[2 * j + 1]), d = pair(sines[2 * j], sines[2 * j + 1]);
+              const uint64_t first = fma2(y[j], c, mul2(z[j], pair(-sines[2 * j], -sines[2 * j + 1])));
+              z[j] = fma2(z[j], c, mul2(y[j], d));
+              y[j] = first;
+            }
           } else {
+            auto turn = [&](uint64_t& v, int j) {
+              const float2 w = both(v);
+              v = pair(w.x * cosines[j] - w.y * sines[j], w.y * cosines[j] + w.x * sines[j]);
+            };
 #pragma unroll
-            for (int j = 0; j < V; j += 2) turn(y[j], y[j + 1], j / 2), turn(z[j], z[j + 1], (V + j) / 2);
+            for (int j = 0; j < kTwos; ++j) {
+              turn(y[j], j);
+              if constexpr (kVector) turn(z[j], kTwos + j);
+            }
           }
         }
         if constexpr (SCALED) {
           uint8_t* to = static_cast<uint8_t*>(s.cache) + entry + u * s.head;
-          const float unit = sh.unit[run * U + u];
-          // a product with 0 is 0, or NaN of what is not finite
-          auto two = [&](float m, float n) { return e4m3_two(fmaf(m, unit, m * 0.0f), fmaf(n, unit, n * 0.0f)); };
+          const uint64_t unit = twice(__uint_as_float(sh.size[run * U + u]));
+          const bool plain = once && !odd;
+          auto two = [&](uint64_t v) -> uint32_t {
+            // a product with 0 is 0, or NaN of what is not finite
+            const float2 w = both(plain ? mul2(v, unit) : fma2(v, unit, mul2(v, 0)));
+            return e4m3_two(w.x, w.y);
+          };
           if constexpr (kVector) {
-            auto put = [&](uint8_t* to, const float(&y)[V]) {
+            auto put = [&](uint8_t* to, const uint64_t(&y)[kTwos]) {
               uint32_t w[V / 4];
 #pragma unroll
-              for (int j = 0; j < V; j += 4) w[j / 4] = two(y[j], y[j + 1]) | two(y[j + 2], y[j + 3]) << 16;
+              for (int j = 0; j < V / 4; ++j) w[j] = two(y[2 * j]) | two(y[2 * j + 1]) << 16;
               if constexpr (V == 8)
                 *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
               else
@@ -335,25 +395,27 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
             put(to + m.at, y);
             if (m.two) put(to + m.other, z);
           } else {
-            const uint32_t w = two(y[0], y[1]);
+            const uint32_t w = two(y[0]);
             to[m.at] = static_cast<uint8_t>(w);
             if (m.two) to[m.other] = static_cast<uint8_t>(w >> 8);
           }
         } else {
           E* to = static_cast<E*>(s.cache) + entry + u * s.head;
-          if constexpr (kVector) {
-            VecT c;
+          VecT c;
+          auto pack = [&](const uint64_t(&y)[kTwos]) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) c.e[j] = Elem<E>::put(y[j]);
-            store16(to + m.at, c);
-            if (m.two) {
-#pragma unroll
-              for (int j = 0; j < V; ++j) c.e[j] = Elem<E>::put(z[j]);
-              store16(to + m.other, c);
+            for (int j = 0; j < kTwos; ++j) {
+              const float2 w = both(y[j]);
+              c.e[2 * j] = Elem<E>::put(w.x), c.e[2 * j + 1] = Elem<E>::put(w.y);
             }
+          };
+          pack(y);
+          if constexpr (kVector) {
+            store16(to + m.at, c);
+            if (m.two) pack(z), store16(to + m.other, c);
           } else {
-            to[m.at] = Elem<E>::put(y[0]);
-            if (m.two) to[m.other] = Elem<E>::put(y[1]);
+            to[m.at] = c.e[0];
+            if (m.two) to[m.other] = c.e[1];
           }
         }
       }
@@ -450,6 +512,11 @@ topk_status launch_typed(const sparse_append_args& a, int sm_count, cudaStream_t
   p.positions = a.positions, p.frequencies = a.frequencies, p.slots = a.slots;
   p.num_slots = a.num_pages * a.page_size;
   p.page_size = a.page_size, p.block = scaled ? a.page_size / a.blocks : 1;
+  p.page_shift = p.block_shift = -1;
+  for (int i = 0; i < 31; ++i) {
+    if (p.page_size == 1 << i) p.page_shift = i;
+    if (p.block == 1 << i) p.block_shift = i;
+  }
   p.T = a.T, p.H = a.H, p.positions_64 = a.positions_64, p.scale = a.scale;
   const int sides = a.v != nullptr ? 2 : 1;
   for (int i = 0; i < sides; ++i) {
