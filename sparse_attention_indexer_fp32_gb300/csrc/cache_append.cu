@@ -7,16 +7,16 @@
 // grows is multiplied by a power of two and rounded again only below E4M3's
 // smallest normal number.
 //
-// The work. Memory bound: each element is read once and written once, in half or
-// a quarter of its size. The tokens of a block follow one another, so a CTA takes
-// the runs of tokens that begin in its share of the call, whole, for one or two
-// heads of one side (keys or values): it finds the runs from the slots alone, the
-// largest size of each run and head by an integer maximum in shared memory (sizes
-// are not negative), then turns and rounds its tokens. A thread has 32 bytes of a
-// token's heads, in registers from the one step to the other where the CTA's
-// tokens fit its threads (a prompt's block does), from L1 otherwise; sine and
-// cosine are computed while its loads are in flight. No atomics to memory, no
-// workspace; every block's scale has one writer.
+// The work. Each element is read once and written once, in half or a quarter of its
+// size; the arithmetic on it takes longer than that, so what tokens and heads share is
+// done once. The tokens of a block follow one another, so a CTA takes the runs of
+// tokens that begin in its share of the call, whole, for two heads of one side (keys or
+// values): it finds the runs from the slots alone, the largest size of each run and head
+// by an integer maximum in shared memory (sizes are not negative), then turns and
+// rounds its tokens. A thread has 32 bytes of two tokens and two heads at once, in
+// registers from the one step to the other where the CTA's tokens fit (a block of 64
+// with heads of 128 does), read again from L1 otherwise; a token's sine and cosine serve
+// both heads. No atomics to memory, no workspace; every block's scale has one writer.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -32,9 +32,8 @@
 namespace tki {
 namespace {
 
-constexpr int kMostThreads = 512;
-constexpr int kRuns = 64;      // tokens whose runs a CTA takes, so runs of a CTA
-constexpr int kMostHeads = 2;  // of a CTA
+constexpr int kRuns = 64;      // tokens whose runs a CTA takes at most, so runs of a CTA
+constexpr int kMostHeads = 4;  // of a CTA
 
 struct AppendSide {
   const void* x;
@@ -56,9 +55,8 @@ struct AppendParams {
   int64_t num_slots;
   int32_t page_size, block;
   int32_t page_shift, block_shift;  // log2, or -1
-  int32_t T, H;
+  int32_t T, H, head_groups;
   int32_t positions_64;
-  int32_t head_groups;
   int32_t share;  // tokens whose runs a CTA takes; without scales, its tokens
   float scale;
 };
@@ -66,8 +64,10 @@ struct AppendParams {
 struct AppendShared {
   uint64_t rates[SPARSE_APPEND_MAX_D / 2];  // of the pairs, in turns a position
   int32_t first[kRuns], block[kRuns];       // of a run: the least place in its block, and that of the cache
-  uint32_t size[kRuns * kMostHeads];        // of a run and head: the largest size / 2, as its bits; then 1 / scale
-  float ratio[kRuns * kMostHeads];          // what its earlier entries are multiplied by
+  uint32_t size[kRuns * kMostHeads];            // of a run and head: the largest size / 2, as its bits; then 1 / scale
+  float ratio[kRuns * kMostHeads];              // what its earlier entries are multiplied by
+  unsigned long long leads;                 // bit per token of the share: it begins a run
+  int64_t end;                              // of the last run
 };
 
 // The smallest power of two s >= 2^-126 with 2 half <= 448 s = 1.75 2^8 s.
@@ -76,6 +76,12 @@ __device__ __forceinline__ float scale_for(float half) {
   const int e = static_cast<int>(bits >> 23) - 127;
   const int n = e - 7 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
   return __uint_as_float(static_cast<uint32_t>(max(n, -126) + 127) << 23);
+}
+
+__device__ __forceinline__ uint32_t max_two(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
 }
 
 // The two numbers of 32 bits of a 16-bit type.
@@ -87,21 +93,28 @@ __device__ __forceinline__ float2 floats_of(uint32_t two) {
     return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
 }
 
+// What a CTA and its threads take.
+template <int THREADS, int ROWS, int HEADS, int PER_SM, int SHARE>
+struct FormOf {
+  static constexpr int threads = THREADS, rows = ROWS, heads = HEADS, per_sm = PER_SM, share = SHARE;
+};
+
 // One side of a CTA. An item that turns holds two units of V elements: of the first
 // half and of the second (HALF), or one behind the other; so does one that does not.
 // Without `vector` (V = 2) it holds one pair, or one element.
-template <typename E, int V, bool HALF, bool SCALED, int U>
+template <typename E, int V, bool HALF, bool SCALED, typename Form>
 __device__ __forceinline__ void append_side(const AppendParams& p, const AppendSide& s, AppendShared& sh) {
+  constexpr int kThreads = Form::threads, kRows = Form::rows, kHeads = Form::heads;
   constexpr bool kVector = sizeof(E) * V == 16;
   constexpr int kPairs = kVector ? V : 1;  // of an item
   using VecT = Vec<E, V>;
-  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int64_t share = blockIdx.x / static_cast<unsigned>(p.head_groups);
-  const int h0 = static_cast<int>(blockIdx.x - share * p.head_groups) * U;
-  const int heads = min(p.H - h0, U);
+  const int h0 = static_cast<int>(blockIdx.x - share * p.head_groups) * kHeads, heads = min(p.H - h0, kHeads);
   const int64_t t0 = share * p.share, t1 = min(t0 + p.share, static_cast<int64_t>(p.T));
-  const int per = min(s.items, threads);
-  const int sub = tid / per, i0 = tid - sub * per, side_by_side = threads / per;
+  const int per = min(s.items, kThreads);
+  const int sub = tid / per, i0 = tid - sub * per, side_by_side = kThreads / per;
+  const int sweep = kRows * side_by_side;  // tokens at once
   const int pairs = s.rotated / 2, units = s.rotated / V, rest = (s.D - s.rotated) / V;
   auto slot_of = [&](int64_t t) -> int32_t {  // -1: not written
     const int32_t slot = p.slots[t];
@@ -110,6 +123,8 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
   auto block_of = [&](int32_t slot) -> int32_t {
     return slot < 0 ? -1 : p.block_shift >= 0 ? slot >> p.block_shift : slot / p.block;
   };
+
+  int64_t begin = t0, end = t1;  // of the CTA's tokens
 
   // ---- an item of a token ----
   const E* x = static_cast<const E*>(s.x) + h0 * s.x_head;
@@ -135,22 +150,35 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
     }
     return m;
   };
-  VecT a[U], b[U];  // of an item without a second unit, b is zeros
+  VecT a[kRows][kHeads], b[kRows][kHeads];  // of an item without a second unit, b is zeros
+  int32_t slots[kRows];
   float cosines[kPairs], sines[kPairs];
-  auto load = [&](int64_t t, const Item& m) {
-    const E* from = x + t * s.x_token;
+  auto slots_of = [&](int64_t t) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (u >= heads) continue;
-      if constexpr (kVector) {
-        a[u] = load16<VecT>(from + u * s.x_head + m.at);
-        if (m.two)
-          b[u] = load16<VecT>(from + u * s.x_head + m.other);
-        else
-          *reinterpret_cast<uint4*>(&b[u]) = make_uint4(0, 0, 0, 0);
-      } else {
-        a[u].e[0] = from[u * s.x_head + m.at];
-        if (m.two) a[u].e[1] = from[u * s.x_head + m.other];
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t at = t + u * side_by_side;
+      slots[u] = sub < side_by_side && at < end ? slot_of(at) : -1;
+    }
+  };
+  auto load = [&](int64_t t, const Item& m) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (slots[r] < 0) continue;
+      const E* from = x + (t + r * side_by_side) * s.x_token;
+#pragma unroll
+      for (int u = 0; u < kHeads; ++u) {
+        if (u >= heads) continue;
+        const E* at = from + u * s.x_head;
+        if constexpr (kVector) {
+          a[r][u] = load16<VecT>(at + m.at);
+          if (m.two)
+            b[r][u] = load16<VecT>(at + m.other);
+          else
+            *reinterpret_cast<uint4*>(&b[r][u]) = make_uint4(0, 0, 0, 0);
+        } else {
+          a[r][u].e[0] = at[m.at];
+          if (m.two) a[r][u].e[1] = at[m.other];
+        }
       }
     }
   };
@@ -172,56 +200,64 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
     }
   };
 
-  // ---- the runs, which every warp finds for itself ----
-  int64_t begin = t0, end = t1;
+  // ---- the runs ----
+  for (int i = tid; i < pairs; i += kThreads) sh.rates[i] = turns_of(p.frequencies[i]);
   unsigned long long leads = 0;  // bit per token of the share: it begins a run
   int runs = 0;
   if constexpr (SCALED) {
-    for (int i = tid; i < kRuns * U; i += threads) sh.size[i] = 0;
+    for (int i = tid; i < kRuns * kHeads; i += kThreads) sh.size[i] = 0;
     if (tid < kRuns) sh.first[tid] = INT32_MAX;
-    int32_t last = t0 > 0 ? block_of(slot_of(t0 - 1)) : -1;
+    if (tid < 32) {
+      int32_t last = t0 > 0 ? block_of(slot_of(t0 - 1)) : -1;
 #pragma unroll
-    for (int part = 0; part < kRuns; part += 32) {
-      if (t0 + part >= t1) continue;
-      const int64_t t = t0 + part + lane;
-      const int32_t block = t < t1 ? block_of(slot_of(t)) : -1;
-      const int32_t up = __shfl_up_sync(0xffffffffu, block, 1);
-      const bool lead = block >= 0 && (lane == 0 ? last : up) != block;
-      const uint32_t bits = __ballot_sync(0xffffffffu, lead);
-      if (lead && tid < 32) sh.block[__popcll(leads) + __popc(bits & ((1u << lane) - 1))] = block;
-      leads |= static_cast<unsigned long long>(bits) << part;
-      last = __shfl_sync(0xffffffffu, block, static_cast<int>(min(t1 - t0 - part, int64_t{32})) - 1);
+      for (int part = 0; part < kRuns; part += 32) {
+        if (t0 + part >= t1) continue;
+        const int64_t t = t0 + part + lane;
+        const int32_t block = t < t1 ? block_of(slot_of(t)) : -1;
+        const int32_t up = __shfl_up_sync(0xffffffffu, block, 1);
+        const bool lead = block >= 0 && (lane == 0 ? last : up) != block;
+        const uint32_t bits = __ballot_sync(0xffffffffu, lead);
+        if (lead) sh.block[__popcll(leads) + __popc(bits & ((1u << lane) - 1))] = block;
+        leads |= static_cast<unsigned long long>(bits) << part;
+        last = __shfl_sync(0xffffffffu, block, static_cast<int>(min(t1 - t0 - part, int64_t{32})) - 1);
+      }
+      while (leads != 0 && last >= 0) {  // the last run may go on behind the share
+        const bool on = end + lane < p.T && block_of(slot_of(end + lane)) == last;
+        const uint32_t off = ~__ballot_sync(0xffffffffu, on);
+        end += off != 0 ? __ffs(off) - 1 : 32;
+        if (off != 0) break;
+      }
+      if (lane == 0) sh.leads = leads, sh.end = end;
     }
+    __syncthreads();
+    leads = sh.leads, end = sh.end;
     if (leads == 0) return;
-    while (last >= 0) {  // the last run may go on behind the share
-      const bool on = end + lane < p.T && block_of(slot_of(end + lane)) == last;
-      const uint32_t off = ~__ballot_sync(0xffffffffu, on);
-      end += off != 0 ? __ffs(off) - 1 : 32;
-      if (off != 0) break;
-    }
     runs = __popcll(leads);
     begin = t0 + __ffsll(static_cast<long long>(leads)) - 1;
+  } else {
+    __syncthreads();
   }
   // The run of a token between begin and end that is written.
   auto run_of = [&](int64_t t) { return t < t1 ? __popcll(leads & ((2ull << (t - t0)) - 1)) - 1 : runs - 1; };
-  const bool once = end - begin <= side_by_side && s.items <= threads;  // what is loaded stays
-  for (int i = tid; i < pairs; i += threads) sh.rates[i] = turns_of(p.frequencies[i]);
+  const bool once = end - begin <= sweep && s.items <= kThreads;  // what is loaded stays
 
   bool odd = false;  // something that this thread holds may not be finite, or not its results
-  // Half the largest size of an item's heads, without what is not finite.
-  auto sizes_of = [&](const Item& m, uint32_t(&most)[U]) {
+  // Half the largest size of an item of each token, without what is not finite.
+  auto sizes_of = [&](const Item& m, uint32_t(&most)[kRows][kHeads]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (u >= heads) continue;
+    for (int ru = 0; ru < kRows * kHeads; ++ru) {
+      const int r = ru / kHeads, u = ru % kHeads;
+      if (slots[r] < 0 || u >= heads) continue;
+      const VecT &av = a[r][u], &bv = b[r][u];
       float high = 0.0f;
       bool plain = false;
       if constexpr (kVector && sizeof(E) == 2) {
         // the largest number as bits, two at a time: nothing is near the end of FP32's range
-        const uint32_t* wa = reinterpret_cast<const uint32_t*>(&a[u]);
-        const uint32_t* wb = reinterpret_cast<const uint32_t*>(&b[u]);
+        const uint32_t* wa = reinterpret_cast<const uint32_t*>(&av);
+        const uint32_t* wb = reinterpret_cast<const uint32_t*>(&bv);
         uint32_t bits = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bits = __vmaxu2(__vmaxu2(bits, wa[j] & 0x7fff7fffu), wb[j] & 0x7fff7fffu);
+        for (int j = 0; j < 4; ++j) bits = max_two(bits, max_two(wa[j] & 0x7fff7fffu, wb[j] & 0x7fff7fffu));
         bits = max(bits & 0xffffu, bits >> 16);
         plain = bits < (std::is_same<E, __half>::value ? 0x7c00u : 0x7e00u);
         if (plain && !m.turns) {
@@ -247,78 +283,73 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
         auto half = [](E e) { return 0.5f * fabsf(Elem<E>::get(e)); };
         if (!kVector) {
           if (m.turns)
-            count((half(a[u].e[0]) + half(a[u].e[1])) * fabsf(p.scale));
+            count((half(av.e[0]) + half(av.e[1])) * fabsf(p.scale));
           else
-            count(half(a[u].e[0]));
+            count(half(av.e[0]));
         } else if (m.turns) {
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             if (HALF) {
-              count((half(a[u].e[j]) + half(b[u].e[j])) * fabsf(p.scale));
+              count((half(av.e[j]) + half(bv.e[j])) * fabsf(p.scale));
             } else if (j % 2 == 0) {
-              count((half(a[u].e[j]) + half(a[u].e[j + 1])) * fabsf(p.scale));
-              count((half(b[u].e[j]) + half(b[u].e[j + 1])) * fabsf(p.scale));
+              count((half(av.e[j]) + half(av.e[j + 1])) * fabsf(p.scale));
+              count((half(bv.e[j]) + half(bv.e[j + 1])) * fabsf(p.scale));
             }
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < V; ++j) count(half(a[u].e[j])), count(half(b[u].e[j]));
+          for (int j = 0; j < V; ++j) count(half(av.e[j])), count(half(bv.e[j]));
         }
       }
-      most[u] = max(most[u], __float_as_uint(high));
+      most[r][u] = max(most[r][u], __float_as_uint(high));
     }
   };
 
-  if constexpr (!SCALED) {
-    __syncthreads();
-  } else {
+  if constexpr (SCALED) {
     // ---- the largest sizes; a warp's threads stay together ----
-    int64_t t = begin + sub;
-    int32_t slot = sub < side_by_side && t < end ? slot_of(t) : -1;
+    slots_of(begin + sub);
     const Item mine = item_of(i0);
-    if (once && slot >= 0) load(t, mine);  // on their way before the shared memory is ready
-    __syncthreads();
-    if (once && slot >= 0) angles(t, i0, mine);
-    const int r = tid / U;
-    const bool has = tid < runs * U && tid % U < heads;  // a run and head: threads >= kRuns * U
-    float* scale = s.scales + (has ? static_cast<int64_t>(sh.block[r]) * p.H + h0 + tid % U : 0);
+    if (once) load(begin + sub, mine);
+    const bool has = tid < runs * kHeads && tid % kHeads < heads;  // a run and head
+    float* scale = s.scales + (has ? static_cast<int64_t>(sh.block[tid / kHeads]) * p.H + h0 + tid % kHeads : 0);
     const float before = has ? *scale : 0.0f;
-    for (int64_t from = begin; from < end; from += side_by_side) {
-      const int run = slot >= 0 ? run_of(t) : -1;
-      uint32_t most[U] = {};
-      if (slot >= 0) {
-        if (i0 == 0) atomicMin(&sh.first[run], slot - block_of(slot) * p.block);
-        if (once) {
-          sizes_of(mine, most);
-        } else {
-          for (int i = i0; i < s.items; i += per) {
-            const Item m = item_of(i);
-            load(t, m);
-            sizes_of(m, most);
+    for (int64_t from = begin; from < end; from += sweep) {
+      if (from > begin) slots_of(from + sub);
+      uint32_t most[kRows][kHeads] = {};
+      if (once) {
+        sizes_of(mine, most);
+      } else {
+        for (int i = i0; i < s.items; i += per) {
+          const Item m = item_of(i);
+          load(from + sub, m);
+          sizes_of(m, most);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int run = slots[r] >= 0 ? run_of(from + sub + r * side_by_side) : -1;
+        if (run >= 0 && i0 == 0) atomicMin(&sh.first[run], slots[r] - block_of(slots[r]) * p.block);
+        // one number a warp where it is all of one run (or idle), one a thread otherwise
+        const int any = __reduce_max_sync(0xffffffffu, run);
+        if (any < 0) continue;
+        const bool same = __all_sync(0xffffffffu, run < 0 || run == any);
+#pragma unroll
+        for (int u = 0; u < kHeads; ++u) {
+          if (u >= heads) continue;
+          if (same) {
+            const uint32_t all = __reduce_max_sync(0xffffffffu, most[r][u]);
+            if (lane == 0) atomicMax(&sh.size[any * kHeads + u], all);
+          } else if (run >= 0) {
+            atomicMax(&sh.size[run * kHeads + u], most[r][u]);
           }
         }
       }
-      // one number a warp where it is all of one run (or idle), one a thread otherwise
-      const int any = __reduce_max_sync(0xffffffffu, run);
-      const bool same = __all_sync(0xffffffffu, run < 0 || run == any);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u >= heads || any < 0) continue;
-        if (same) {
-          const uint32_t all = __reduce_max_sync(0xffffffffu, most[u]);
-          if (lane == 0) atomicMax(&sh.size[any * U + u], all);
-        } else if (run >= 0) {
-          atomicMax(&sh.size[run * U + u], most[u]);
-        }
-      }
-      t += side_by_side;
-      slot = sub < side_by_side && t < end ? slot_of(t) : -1;
     }
     __syncthreads();
     // ---- the scales ----
     if (has) {
       const float need = scale_for(__uint_as_float(sh.size[tid]));
-      const bool begins = sh.first[r] == 0;
+      const bool begins = sh.first[tid / kHeads] == 0;
       const float now = begins ? need : fmaxf(before, need);
       if (begins || now != before) *scale = now;
       sh.size[tid] = __float_as_uint(1.0f / now);
@@ -328,29 +359,35 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
   }
 
   // ---- the tokens ----
-  for (int64_t t = begin + sub; sub < side_by_side && t < end; t += side_by_side) {
-    const int32_t slot = slot_of(t);
-    if (slot < 0) continue;
-    const int32_t page = p.page_shift >= 0 ? slot >> p.page_shift : slot / p.page_size;
-    const int64_t entry = page * s.page + (slot - page * p.page_size) * s.entry + h0 * s.head;
-    const int run = SCALED ? run_of(t) : 0;
+  for (int64_t from = begin; from < end; from += sweep) {
+    const int64_t t = from + sub;
+    if (!SCALED || !once) slots_of(t);
     for (int i = i0; i < s.items; i += per) {
       const Item m = item_of(i);
-      if (!SCALED || !once) load(t, m), angles(t, i, m);
+      if (!SCALED || !once) load(t, m);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int r = 0; r < kRows; ++r) {
+        const int32_t slot = slots[r];
+        if (slot < 0) continue;
+        const int32_t page = p.page_shift >= 0 ? slot >> p.page_shift : slot / p.page_size;
+        const int64_t entry = page * s.page + (slot - page * p.page_size) * s.entry + h0 * s.head;
+        const int run = SCALED ? run_of(t + r * side_by_side) : 0;
+        angles(t + r * side_by_side, i, m);
+#pragma unroll
+        for (int u = 0; u < kHeads; ++u) {
         if (u >= heads) continue;
+        const VecT &av = a[r][u], &bv = b[r][u];
         // the item's elements, two at a time, of the second unit in z
         constexpr int kTwos = V / 2;
         uint64_t y[kTwos], z[kTwos];
         if constexpr (kVector) {
 #pragma unroll
           for (int j = 0; j < kTwos; ++j) {
-            y[j] = pair(Elem<E>::get(a[u].e[2 * j]), Elem<E>::get(a[u].e[2 * j + 1]));
-            z[j] = pair(Elem<E>::get(b[u].e[2 * j]), Elem<E>::get(b[u].e[2 * j + 1]));
+            y[j] = pair(Elem<E>::get(av.e[2 * j]), Elem<E>::get(av.e[2 * j + 1]));
+            z[j] = pair(Elem<E>::get(bv.e[2 * j]), Elem<E>::get(bv.e[2 * j + 1]));
           }
         } else {
-          y[0] = pair(Elem<E>::get(a[u].e[0]), m.two ? Elem<E>::get(a[u].e[1]) : 0.0f), z[0] = 0;
+          y[0] = pair(Elem<E>::get(av.e[0]), m.two ? Elem<E>::get(av.e[1]) : 0.0f), z[0] = 0;
         }
         if (m.turns) {
           if constexpr (kVector && HALF) {
@@ -375,11 +412,13 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
         }
         if constexpr (SCALED) {
           uint8_t* to = static_cast<uint8_t*>(s.cache) + entry + u * s.head;
-          const uint64_t unit = twice(__uint_as_float(sh.size[run * U + u]));
-          const bool plain = once && !odd;
+          const uint64_t unit = twice(__uint_as_float(sh.size[run * kHeads + u]));
+          if (!once || odd) {  // a product with 0 is 0, or NaN of what is not finite
+#pragma unroll
+            for (int j = 0; j < kTwos; ++j) y[j] = fma2(y[j], 0, y[j]), z[j] = fma2(z[j], 0, z[j]);
+          }
           auto two = [&](uint64_t v) -> uint32_t {
-            // a product with 0 is 0, or NaN of what is not finite
-            const float2 w = both(plain ? mul2(v, unit) : fma2(v, unit, mul2(v, 0)));
+            const float2 w = both(mul2(v, unit));
             return e4m3_two(w.x, w.y);
           };
           if constexpr (kVector) {
@@ -418,14 +457,15 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
             if (m.two) to[m.other] = c.e[1];
           }
         }
+        }
       }
     }
   }
 
   if constexpr (SCALED) {
     // ---- earlier entries of blocks whose scale grew, one run and head a warp ----
-    for (int j = tid >> 5; j < runs * U; j += threads / 32) {
-      const int r = j / U, u = j - r * U;
+    for (int j = tid >> 5; j < runs * kHeads; j += kThreads / 32) {
+      const int r = j / kHeads, u = j % kHeads;
       if (u >= heads || sh.ratio[j] == 1.0f) continue;
       const float ratio = sh.ratio[j];
       const int32_t block = sh.block[r], per_page = p.page_size / p.block, page = block / per_page;
@@ -469,37 +509,46 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
   }
 }
 
-template <typename E, bool HALF, bool SCALED, int U>
-__global__ void __launch_bounds__(kMostThreads, 2) append_kernel(const __grid_constant__ AppendParams p) {
+template <typename E, bool HALF, bool SCALED, typename Form>
+__global__ void __launch_bounds__(Form::threads, Form::per_sm) append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ AppendShared sh;
   const AppendSide& s = p.side[blockIdx.y];
   if (s.vector)
-    append_side<E, 16 / sizeof(E), HALF, SCALED, U>(p, s, sh);
+    append_side<E, 16 / sizeof(E), HALF, SCALED, Form>(p, s, sh);
   else
-    append_side<E, 2, HALF, SCALED, U>(p, s, sh);
+    append_side<E, 2, HALF, SCALED, Form>(p, s, sh);
 }
 
 bool aligned_to(const void* q, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(q) & (bytes - 1)) == 0; }
 
-template <typename E, bool HALF, bool SCALED>
-topk_status launch_layout(const AppendParams& p, int sides, int sm_count, cudaStream_t stream) {
+// Many tokens: a block of 64 with heads of 128 stays in a CTA's registers (8192 tokens
+// x 8 heads x (128 + 128), bf16, into 8 bits: 30 us by two heads a thread and three CTAs
+// an SM, 35 by two CTAs, 36 by four heads; into 16 bits, which wait on nothing between,
+// 12.3 for 10.4 by four heads). Few: small CTAs, so that all SMs have some (64 tokens
+// 7.2 us, 12 by large ones).
+using ScaledForm = FormOf<256, 2, 2, 3, 64>;
+using PlainForm = FormOf<256, 2, 4, 2, 64>;
+using FewForm = FormOf<128, 1, 1, 4, 16>;
+
+template <typename E, bool HALF, bool SCALED, typename Form>
+topk_status launch_form(const AppendParams& p, int sides, int sm_count, cudaStream_t stream) {
   AppendParams q = p;
-  int items = 0;  // of a token
-  for (int i = 0; i < sides; ++i) items += p.side[i].items;
-  // Many tokens: CTAs of 512 threads, which a block of 64 tokens with heads of 128
-  // fits, and two heads a thread. Few: small CTAs, so that all SMs have some.
-  const bool many = static_cast<double>(p.T) * p.H * items >= 1024.0 * sm_count;
-  const int u = many ? 2 : 1, threads = many ? kMostThreads : 128;
-  auto groups = [&](int share) { return ((static_cast<int64_t>(p.T) + share - 1) / share) * ((p.H + u - 1) / u); };
-  int share = kRuns;
-  const int side_by_side = threads / (items / sides < threads ? items / sides : threads);
-  while (share > 1 && (groups(share) * sides < 2 * sm_count || (!SCALED && share > side_by_side))) share /= 2;
-  q.share = share;
-  q.head_groups = (p.H + u - 1) / u;
-  const int64_t grid = groups(share);
+  q.head_groups = (p.H + Form::heads - 1) / Form::heads;
+  auto grid_of = [&](int share) { return (static_cast<int64_t>(p.T) + share - 1) / share * q.head_groups; };
+  q.share = Form::share;
+  while (q.share > 1 && grid_of(q.share) * sides < 2 * sm_count) q.share /= 2;
+  const int64_t grid = grid_of(q.share);
   if (grid > INT32_MAX) return TOPK_EINVAL;
   const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>(sides));
-  return launch(many ? append_kernel<E, HALF, SCALED, 2> : append_kernel<E, HALF, SCALED, 1>, q, g, threads, 0, stream);
+  return launch(append_kernel<E, HALF, SCALED, Form>, q, g, Form::threads, 0, stream);
+}
+
+template <typename E, bool HALF, bool SCALED>
+topk_status launch_layout(const AppendParams& p, int sides, int sm_count, cudaStream_t stream) {
+  double items = 0.0;
+  for (int i = 0; i < sides; ++i) items += p.side[i].items;
+  if (items * p.T * p.H >= 1024.0 * sm_count) return launch_form<E, HALF, SCALED, std::conditional_t<SCALED, ScaledForm, PlainForm>>(p, sides, sm_count, stream);
+  return launch_form<E, HALF, SCALED, FewForm>(p, sides, sm_count, stream);
 }
 
 template <typename E>
