@@ -9,8 +9,8 @@ from typing import Optional
 
 import torch
 
-from ._step import (_BF16, _E4M3, _F64, _FP16, _FP32, _I32, _I64, _LAYOUTS, _ROTARY_TYPES, _Call, _main, _no_broadcast,
-                    _other, _overlap, _scales_of, _span, _whole, _written)
+from ._step import (_E4M3, _F64, _I32, _I64, _LAYOUTS, _ROTARY_TYPES, _Call, _main, _no_broadcast, _other, _scales_of,
+                    _whole, _written)
 
 _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -32,14 +32,23 @@ _append = _Call("sparse_append", _AppendArgs)
 
 
 def _entries(cache, name: str, like, heads: int, size: int, index: int):
-    """Shape and strides of a cache of these heads, its entries in 8 bits or of the type of `like`."""
-    if not isinstance(cache, torch.Tensor) or cache.dtype not in (like, _E4M3):
+    """Shape, strides and type of a cache of these heads, its entries in 8 bits or of the type of `like`."""
+    held = cache.dtype if isinstance(cache, torch.Tensor) else None
+    if held != _E4M3 and held != like:
         raise ValueError(f"{name} must be a 4-D tensor of {like} or {_E4M3}")
-    shape, strides = _other(cache, name, 4, cache.dtype, index)
-    if shape[2:] != (heads, size):
+    shape, strides = _other(cache, name, 4, held, index)
+    if shape[2] != heads or shape[3] != size:
         raise ValueError(f"{name} must be [pages, page_size, {heads}, {size}]")
     _no_broadcast(shape, strides, name)
-    return shape, strides
+    return shape, strides, held
+
+
+def _end(address: int, shape, strides, size: int) -> int:
+    """The address behind the last element of a tensor of three or four dimensions, `address` if it has none."""
+    if 0 in shape:
+        return address
+    last = (shape[0] - 1) * strides[0] + (shape[1] - 1) * strides[1] + (shape[2] - 1) * strides[2] + 1
+    return address + (last + (shape[3] - 1) * strides[3] if len(shape) == 4 else last) * size
 
 
 def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -67,9 +76,9 @@ def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], positions: Optional
     T, H, D = shape
     dtype = k.dtype
     to = _whole(slots, "slots", (T,), _I32, index)
-    ks, kt = _entries(k_cache, "k_cache", dtype, H, D, index)
-    pages, page_size = ks[:2]
-    eight = k_cache.dtype == _E4M3
+    ks, kt, held = _entries(k_cache, "k_cache", dtype, H, D, index)
+    pages, page_size = ks[0], ks[1]
+    eight = held == _E4M3
     pos, freq, pairs, wide = 0, 0, 0, False
     if frequencies is not None:
         pairs = frequencies.numel() if isinstance(frequencies, torch.Tensor) else 0
@@ -83,25 +92,25 @@ def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], positions: Optional
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache go together")
     Dv, vx, vt, at_v, to_v = 0, (0, 0), (0, 0, 0), 0, 0
-    bytes_in = k.element_size()
+    bytes_in = 4 if code == 2 else 2
     size = 1 if eight else bytes_in
     at_k, to_k = k.data_ptr(), k_cache.data_ptr()
-    mine, keys = _span(at_k, shape, xs, bytes_in), _span(to_k, ks, kt, size)
-    if _overlap(mine, keys):
+    end_k, end_keys = _end(at_k, shape, xs, bytes_in), _end(to_k, ks, kt, size)
+    if at_k < end_keys and to_k < end_k:
         raise ValueError("k_cache must not overlap k")
     if v is not None:
         vs, vx = _other(v, "v", 3, dtype, index)
-        if vs[:2] != (T, H):
+        if vs[0] != T or vs[1] != H:
             raise ValueError("v must be [T, H, Dv]")
         Dv = vs[2]
-        cs, vt = _entries(v_cache, "v_cache", dtype, H, Dv, index)
-        if cs[:2] != ks[:2] or v_cache.dtype != k_cache.dtype:
+        cs, vt, other = _entries(v_cache, "v_cache", dtype, H, Dv, index)
+        if cs[0] != pages or cs[1] != page_size or other != held:
             raise ValueError("v_cache must have the pages and the type of k_cache")
         at_v, to_v = v.data_ptr(), v_cache.data_ptr()
-        theirs, values = _span(at_v, vs, vx, bytes_in), _span(to_v, cs, vt, size)
-        if _overlap(theirs, keys) or _overlap(theirs, values) or _overlap(mine, values):
+        end_v, end_values = _end(at_v, vs, vx, bytes_in), _end(to_v, cs, vt, size)
+        if at_v < end_keys and to_k < end_v or at_v < end_values and to_v < end_v or at_k < end_values and to_v < end_k:
             raise ValueError("the caches must not overlap k or v")
-        if _overlap(keys, values) and _meet(ks, kt, vt, Dv, to_v - to_k, size):
+        if to_k < end_values and to_v < end_keys and _meet(ks, kt, vt, Dv, to_v - to_k, size):
             raise ValueError("v_cache must not overlap k_cache")
     units_k, units_v, blocks = 0, 0, 0
     if eight:
@@ -117,9 +126,7 @@ def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], positions: Optional
     _append(index, stream, at_k, xs[0], xs[1], at_v, vx[0], vx[1], to_k, kt[0], kt[1], kt[2], to_v, vt[0], vt[1], vt[2],
             units_k, units_v, pos, freq, to, pages, page_size, blocks, T, H, D, Dv, 2 * pairs, int(offset),
             _LAYOUTS[layout], code, 3 if eight else code, wide, scale)
-    for t in (k_cache, v_cache, k_scales, v_scales):
-        if t is not None:
-            _written(t)
+    _written([t for t in (k_cache, v_cache, k_scales, v_scales) if t is not None])
 
 
 def _meet(shape, strides, others, second: int, gap: int, size: int) -> bool:

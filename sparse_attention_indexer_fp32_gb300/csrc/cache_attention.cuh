@@ -718,6 +718,9 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       }
 
       // ---- end of a work ----
+      // A barrier that was given up may look over to who comes to it eight tiles on, in
+      // a later work: those are lost whole.
+      if (*stop != 0) ok = false;
       float sums[HS];
 #pragma unroll
       for (int h = 0; h < HS; ++h) {

@@ -83,3 +83,56 @@ def test_rounding_of_the_reference():
     assert np.isnan(C.round_e4m3([np.nan, np.inf, -np.inf])).all()
     for most, want in ((0.0, 2.0 ** -126), (448.0, 1.0), (448.1, 2.0), (3.5, 2.0 ** -7), (3.6, 2.0 ** -6), (1e38, 2.0 ** 118)):
         assert C.power_for(most) == want
+
+
+ATTENTION = dict(q=SOME, q_seq_stride=256, q_token_stride=256, q_head_stride=64, k=SOME, k_page_stride=2048,
+                 k_token_stride=128, k_head_stride=64, v=SOME, v_page_stride=2048, v_token_stride=128,
+                 v_head_stride=64, indices=SOME, page_table=SOME, table_stride=4, table_width=4, out=SOME,
+                 num_pages=8, page_size=16, B=2, T=1, Hq=4, Hkv=2, D=64, Dv=64, K=8, type=0, scale=0.125,
+                 k_scales=SOME, v_scales=SOME, blocks=4)
+
+
+def test_attention_refusals(lib):  # noqa: F811
+    from sparse_attention_indexer_fp32_gb300 import _step
+
+    most = 2 ** 31 - 1
+    bad = [dict(type=2), dict(type=3), dict(B=-1), dict(T=-1), dict(Hkv=0), dict(Hq=3), dict(Hq=-2), dict(K=-1),
+           dict(D=0), dict(D=72), dict(D=8), dict(D=272), dict(Dv=0), dict(Dv=8), dict(Dv=24), dict(Dv=272),
+           dict(scale=math.nan), dict(scale=math.inf), dict(softcap=-1.0), dict(softcap=math.nan), dict(softcap=math.inf),
+           dict(num_pages=-1), dict(page_size=-1), dict(table_width=-1), dict(table_stride=-1), dict(slopes=SOME),
+           dict(page_table=None, first=SOME), dict(page_table=None, query_positions=SOME), dict(q=None), dict(k=None),
+           dict(v=None), dict(indices=None), dict(out=None), dict(k=SOME + 8), dict(v=SOME + 8), dict(out=SOME + 8),
+           dict(q=SOME + 1), dict(k_page_stride=2056), dict(k_token_stride=136), dict(k_head_stride=72),
+           dict(v_page_stride=2056), dict(v_token_stride=136), dict(v_head_stride=72), dict(indices=SOME + 2),
+           dict(page_table=SOME + 2), dict(query_positions=SOME + 2), dict(first=SOME + 2), dict(lse=SOME + 2),
+           dict(slopes=SOME + 2, query_positions=SOME), dict(num_pages=2 ** 60), dict(k_scales=None),
+           dict(v_scales=None), dict(k_scales=SOME + 2), dict(v_scales=SOME + 2), dict(blocks=0), dict(blocks=3),
+           dict(blocks=-4), dict(blocks=32), dict(B=most, T=most), dict(B=2 ** 30, T=1, Hkv=4),
+           dict(B=2 ** 12, T=1, Hkv=1, Hq=most)]
+    for change in bad:
+        assert _status(lib, "sparse_attention_e4m3", _step._AttentionE4m3Args, ATTENTION, **change) == tk.Status.EINVAL, change
+    for change in (dict(B=0), dict(T=0), dict(Hq=0)):
+        assert _status(lib, "sparse_attention_e4m3", _step._AttentionE4m3Args, ATTENTION, **change) == tk.Status.OK, change
+    assert lib.sparse_attention_e4m3(None, None) == tk.Status.EINVAL
+    kind, call = _step._AttentionE4m3Args, _step._attention_e4m3
+    values = [i + 0.5 if t is ctypes.c_float else 1000003 * (i + 1) for i, (_, t) in enumerate(kind._fields_)]
+    packed = call.pack(*values)
+    assert bytes(kind(*values))[:len(packed)] == packed or bytes(kind(*values)) == packed
+
+
+def test_scales_are_checked():
+    """Scales of another shape, or blocks that do not divide the page, are refused by name before anything else of them."""
+    from sparse_attention_indexer_fp32_gb300 import _step
+
+    for scales in (None, torch.zeros((2, 3)), torch.zeros((2, 0, 4)), torch.zeros((2, 3, 4))):
+        with pytest.raises(ValueError, match="k_scales must be"):
+            _step._scales_of(scales, "k_scales", 2, 16, 4, 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        _step._scales_of(torch.zeros((2, 4, 4)), "k_scales", 2, 16, 4, 0)  # not on the GPU
+
+
+def test_addresses_behind_the_last_element():
+    for t in (torch.zeros((3, 4, 8)), torch.zeros((3, 4, 8, 2)), torch.zeros((5, 6, 7))[1:4, ::2, 2:5], torch.zeros((3, 0, 8)),
+              torch.zeros((4, 1, 2, 9)).transpose(0, 2)):
+        want = t.data_ptr() + 4 * (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) if t.numel() else t.data_ptr()
+        assert _cache._end(t.data_ptr(), t.shape, t.stride(), 4) == want

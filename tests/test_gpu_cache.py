@@ -1,6 +1,9 @@
 """The operators of a paged cache in 8 bits on the GPU against their formulas in 64 bits (``cache_reference``)."""
 
+import ctypes
 import math
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -546,3 +549,159 @@ def test_attention_in_a_graph_and_on_streams():
         for side in range(2):
             for i, g in enumerate(got[side]):
                 assert torch.equal(g, want[(i + side * turn) % len(calls)])
+
+
+# ---- the whole way -----------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_a_step_in_8_bits(dtype):
+    """Prompts and then single tokens appended (keys and values; the indexer's keys with a scale each), scores over the
+    8-bit keys, the selection and attention over the 8-bit entries: each call on what the one before left."""
+    B, Hq, Hkv, D, ps, blocks, H, select = 3, 16, 2, 64, 32, 2, 8, 512
+    pages, f = 24, tk.rotary_frequencies(32, device=DEV)
+    table = torch.randperm(B * pages, generator=_gen(1), device=DEV).to(torch.int32).view(B, pages)
+    caches = [torch.zeros((B * pages, ps, Hkv, D), device=DEV).to(E4M3) for _ in range(2)]
+    scales = [torch.zeros((B * pages, blocks, Hkv), device=DEV) for _ in range(2)]
+    index_cache = torch.zeros((B * pages, ps, 1, D), device=DEV).to(E4M3)
+    index_scales = torch.zeros((B * pages, ps, 1), device=DEV)
+    held = [[], [], []]  # what was appended, in 64 bits, by sequence
+    at = torch.zeros(B, dtype=torch.int64)
+    for step, counts in enumerate(([601, 0, 330], [1, 1, 1], [1, 0, 1], [1, 40, 1])):
+        T = sum(counts) + 2  # idle tokens behind the last sequence
+        k, v = _randn((T, Hkv, D), 10 + step, dtype, 2.0 ** step), _randn((T, Hkv, D), 20 + step, dtype, 2.0 ** -step)
+        ik = _randn((T, 1, D), 30 + step, dtype)
+        where = [int(at[b]) + i for b in range(B) for i in range(counts[b])]
+        owner = [b for b in range(B) for _ in range(counts[b])]
+        slots = _ints([int(table[b, w // ps]) * ps + w % ps for b, w in zip(owner, where)] + [-1, -1])
+        positions = _ints(where + [0, 0])
+        tk.cache_append(k, v, positions, f, *caches, slots, k_scales=scales[0], v_scales=scales[1])
+        tk.cache_append(ik, None, positions, f, index_cache, None, slots, k_scales=index_scales)
+        turned = [R.np64(tk.rotary(x.float(), positions, f)) for x in (k, ik)]
+        for b in range(B):
+            mine = [i for i, o in enumerate(owner) if o == b]
+            held[b].append([turned[0][mine], R.np64(v)[mine], turned[1][mine]])
+        at += torch.tensor(counts)
+    lengths = at.to(torch.int32).to(DEV)
+    width = pages * ps
+    iq, w = _randn((B, 1, H, D), 2), _randn((B, 1, H), 3)
+    scores = tk.indexer_scores((iq * 16.0).to(E4M3), w, index_cache[:, :, 0], lengths[:, None], table, key_scales=index_scales[..., 0],
+                               out=torch.zeros((B, 1, width), device=DEV))
+    chosen = tk.topk_ragged(scores.view(B, width), lengths, select)
+    q = _randn((B, 1, Hq, D), 4, dtype)
+    c = dict(q=q, k=caches[0], v=caches[1], indices=chosen[:, None].contiguous(), page_table=table, k_scales=scales[0],
+             v_scales=scales[1], query_positions=(lengths - 1)[:, None].contiguous(), scale=D ** -0.5)
+    out, lse = _attention_check(c)
+    # and against what was appended, before any rounding to 8 bits
+    flat = [R.np64(t.float()).reshape(B * pages, blocks, ps // blocks, Hkv, D) * R.np64(s)[:, :, None, :, None] for t, s in zip(caches, scales)]
+    index_flat = R.np64(index_cache.float()) * R.np64(index_scales)[..., None]
+    for b in range(B):
+        parts = [np.concatenate([h[i] for h in held[b]]) for i in range(3)]
+        order = np.asarray([int(table[b, p // ps]) * ps + p % ps for p in range(int(at[b]))])
+        for got, want, unit in ((flat[0], parts[0], scales[0]), (flat[1], parts[1], scales[1])):
+            got = got.reshape(-1, Hkv, D)[order]
+            units = np.repeat(R.np64(unit), ps // blocks, axis=1).reshape(-1, Hkv)[order][..., None]
+            # rounded once and, where a scale grew, again below the type's normal numbers, for each of three growths
+            assert (np.abs(got - want) <= np.abs(want) * (2.0 ** -4 + 2.0 ** -18) + 4 * 2.0 ** -10 * units).all()
+        assert (np.abs(index_flat.reshape(-1, 1, D)[order] - parts[2]) <= np.abs(parts[2]) * (2.0 ** -4 + 2.0 ** -18)
+                + 2.0 ** -10 * R.np64(index_scales).reshape(-1, 1)[order][..., None]).all()
+        # the selection is that of the scores of the 8-bit entries
+        n, idx = int(at[b]), chosen[b][chosen[b] >= 0].cpu().numpy()
+        s = scores[b, 0, :n].cpu().numpy()
+        assert len(idx) == min(n, select) and (n <= select or s[idx].min() >= np.delete(s, idx).max())
+        # attention on the numbers themselves: the 8-bit entries are within 2^-4 of them
+        kk, vv = (p[idx].repeat(Hq // Hkv, axis=1) for p in parts[:2])
+        z = np.einsum("hd,nhd->hn", R.np64(q)[b, 0], kk) * D ** -0.5
+        p = np.exp(z - z.max(axis=1, keepdims=True))
+        want = np.einsum("hn,nhd->hd", p / p.sum(axis=1, keepdims=True), vv)
+        assert np.linalg.norm(R.np64(out)[b, 0] - want) < 0.25 * np.linalg.norm(want)
+
+
+# ---- waits that run out ------------------------------------------------------------------------------
+
+
+@pytest.fixture(scope="module")
+def hurried(tmp_path_factory):
+    """The library's calls once more, with waits that give up at once or after 3 us: {limit in ns: {call: its function}}."""
+    from sparse_attention_indexer_fp32_gb300 import _step
+    from sparse_attention_indexer_fp32_gb300 import build as cuda_build
+
+    units = ["cache_abi.cu", "cache_append.cu", "cache_attention_bf16.cu", "cache_attention_fp16.cu"]
+    out = tmp_path_factory.mktemp("hurried_cache")
+    jobs = []
+    for ns in (0, 3000):
+        for u in units:
+            jobs.append(subprocess.Popen([cuda_build.nvcc(), *cuda_build.ARCH, "-O3", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
+                                          "-I", cuda_build.INCLUDE, f"-DSPARSE_WAIT_LIMIT_NS={ns}", "-c",
+                                          os.path.join(cuda_build.CSRC, u), "-o", str(out / f"{ns}_{u}.o")]))
+    assert [job.wait() for job in jobs] == [0] * len(jobs)
+    calls = {}
+    for ns in (0, 3000):
+        path = str(out / f"libhurried_cache_{ns}.so")
+        subprocess.check_call([cuda_build.nvcc(), *cuda_build.ARCH, "-shared", "-o", path, *(str(out / f"{ns}_{u}.o") for u in units)])
+        prototype = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, ctypes.c_void_p)
+        call = _step._attention_e4m3
+        calls[ns] = {call: prototype(ctypes.cast(getattr(ctypes.CDLL(path), call.name), ctypes.c_void_p).value)}
+    return calls
+
+
+@pytest.mark.parametrize("rows,Hq,Hkv,K,dtype", [(1, 8, 1, 2048, BF16), (3, 16, 4, 700, FP16), (400, 8, 1, 300, BF16),
+                                                 (2, 40, 1, 900, BF16), (340, 40, 1, 130, FP16), (340, 64, 1, 400, BF16),
+                                                 (330, 12, 1, 200, BF16)])
+def test_attention_whose_waits_run_out(hurried, monkeypatch, rows, Hq, Hkv, K, dtype):
+    """With waits that run out each number is what it is without, or NaN, and the calls after are right again."""
+    D, ps = 64, 16
+    q, k, v = _randn((rows, 1, Hq, D), 1, dtype), _codes((200, ps, Hkv, D), 2), _codes((200, ps, Hkv, D), 3)
+    ks, vs = _scales((200, 1, Hkv), 4), _scales((200, 1, Hkv), 5)
+    idx = torch.randint(-1, 200 * ps, (rows, 1, K), generator=_gen(6), device=DEV).to(torch.int32)
+
+    def call():
+        return tk.sparse_attention(q, k, v, idx, k_scales=ks, v_scales=vs, softcap=30.0, return_lse=True)
+
+    want = call()
+    for ns in (0, 3000, 0):
+        with monkeypatch.context() as patch:
+            for entry, fn in hurried[ns].items():
+                patch.setattr(entry, "fn", fn)
+            got = call()
+        torch.cuda.synchronize()
+        lost = 0
+        for g, w in zip(got, want):
+            nan = torch.isnan(g)
+            lost += int(nan.sum())
+            assert torch.equal(torch.where(nan, w, g), w), f"neither right nor NaN with a limit of {ns} ns"
+        assert ns > 0 or lost > 0, "no wait ran out"
+        for g, w in zip(call(), want):
+            assert torch.equal(g, w), f"the call after one with a limit of {ns} ns"
+
+
+def test_refusals():
+    """What the binding cannot hand on: scales of another shape, caches that overlap, types that do not go together."""
+    c = _attend(2, 1, 8, 2, 64, 64, 40, 100, 16, 2, BF16)
+    bad = [(dict(v_scales=None), "v_scales"), (dict(k_scales=None), "k_scales"), (dict(k_scales=c["k_scales"][:, :1]), "contiguous"),
+           (dict(v_scales=c["v_scales"].sum(1, keepdim=True)), "blocks of k_scales"), (dict(k=c["k"].float()), "float8"),
+           (dict(k_scales=None, v_scales=None), "k must be"), (dict(q=c["q"].float()), "q must be"),
+           (dict(k_scales=c["k_scales"].double()), "float32")]
+    for change, match in bad:
+        with pytest.raises(ValueError, match=match):
+            tk.sparse_attention(**{**c, **change})
+    a = _case([6], 2, 64, 64, 64, 8, 2, BF16)
+    both = _codes((4, 8, 2, 100), 1)
+    bad = [(dict(k_scales=None), "k_scales"), (dict(v_scales=a["k_scales"]), "its own"), (dict(v=None), "go together"),
+           (dict(v_cache=a["v_cache"].float()), "v_cache must be"), (dict(v_cache=a["k_cache"]), "overlap k_cache"),
+           (dict(v_cache=a["v_cache"].to(BF16)), "type of k_cache"), (dict(k_cache=both[..., :64], v_cache=both[..., 36:]), "overlap"),
+           (dict(v=a["v"].half()), "v must be"), (dict(slots=a["slots"].long()), "slots"), (dict(k=a["k"].double()), "k must be"),
+           (dict(f=a["f"].float()), "frequencies"), (dict(positions=None), "positions"),
+           (dict(v_scales=a["v_scales"][:, :1].contiguous()), "blocks of k_scales"),
+           (dict(k_cache=a["k_cache"][:, :, :, :1].expand(-1, -1, -1, 64)), "unit stride"),
+           (dict(k_cache=a["k_cache"][:1].expand(9, -1, -1, -1)), "broadcast")]
+    for change, match in bad:
+        with pytest.raises(ValueError, match=match):
+            _append({**a, **change})
+    with pytest.raises(ValueError, match="float8_e4m3fn have scales"):
+        _append({**a, "k_cache": a["k_cache"].to(BF16), "v_cache": a["v_cache"].to(BF16)})
+    with pytest.raises(tk.TopkError):
+        _append(a, offset=2)
+    versions = [a[n]._version for n in ("k_cache", "v_scales")]
+    _append(a)
+    assert [a[n]._version for n in ("k_cache", "v_scales")] > versions
