@@ -54,6 +54,7 @@ constexpr int kBufs = 2;  // buffers of scores in TMEM, of weights and queries i
 constexpr int kMaxNotes = kMaxStages + kBufs;  // see E4Params::notes
 constexpr float kNothing = -1073741824.0f;  // a reference below any logit in use; its negative for heads that are none
 constexpr float kLogLimit = 8.8073549f;     // log2(448)
+constexpr float kFar = 16.0f;  // a reference that moves further has left logits with less than 2^-20 of their digits
 constexpr float kLeast = 0x1p-60f;          // values' scales below count as this for the reference
 
 template <typename E, int G>
@@ -242,7 +243,7 @@ __device__ __forceinline__ bool begins(float nref) { return __float_as_uint(nref
 // 1 / a sum of weights, zero where nothing is seen; and its logarithm with the reference.
 __device__ __forceinline__ float e4_inverse(float sum) { return sum == 0.0f ? 0.0f : reciprocal(sum); }
 __device__ __forceinline__ float e4_logsum(float ref, float sum) {
-  return sum != sum ? sum : sum == 0.0f ? __int_as_float(0xff800000) : (ref + log2_fast(sum)) * kLn2;
+  return sum != sum ? sum : sum == 0.0f ? __int_as_float(0xff800000) : (ref + log2f(sum)) * kLn2;
 }
 
 template <typename E, int G>
@@ -284,8 +285,10 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
     l.g = k.g;
     return l;
   };
+  // Tiles are taken from the list's last to its first: a selection comes in ascending order,
+  // and with a distance bias the nearest entries have the largest logits.
   auto index_of = [&](const Look& l, int i) -> int32_t {
-    const int64_t j = (static_cast<int64_t>(i) * cluster + rank) * kEntries + part * 32 + lane;
+    const int64_t j = (all_tiles - 1 - (static_cast<int64_t>(i) * cluster + rank)) * kEntries + part * 32 + lane;
     return i < tiles && j < a.K && some ? l.indices[j] : -1;
   };
   auto page_index = [&](int32_t pos) -> uint32_t {
@@ -570,9 +573,11 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         const float ks = notes.ks[e], vs = notes.vs[e];
         const bool seen = (notes.seen[e >> 5] >> (e & 31)) & 1;
         const float log_vs = log2_fast(fmaxf(fabsf(vs), kLeast));
-        // Logits in units of log 2, two heads at a time, less the references.
+        // Logits in units of log 2, two heads at a time, less the references; once more where
+        // those moved so far that what is left after them was rounded away.
         uint64_t z[HS / 2];
-        {
+#pragma unroll 1
+        for (bool more = true, again = true; more;) {
           {
             uint32_t v[TERMS][HS];
             const uint32_t s_at = tmem_s + (at & 1) * N + lanes + set * HS;
@@ -629,14 +634,15 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
             const uint64_t c0 = plain ? mul2(factor, u.x) : factor, c1 = plain ? mul2(factor, u.y) : factor;
             z[h] = fma2(z[h], c0, r.x), z[h + 1] = fma2(z[h + 1], c1, r.y);
           }
-        }
         float high = -FLT_MAX;
 #pragma unroll
         for (int h = 0; h < HS / 2; ++h) {
           const float2 y = both(z[h]);
           high = fmaxf(high, fmaxf(y.x, y.y));
         }
-        if (set_any(set, seen && (fresh || high + log_vs > kLogLimit))) {
+        const bool moves_any = set_any(set, seen && (fresh || high + log_vs > kLogLimit));
+        if (!moves_any) break;
+        {
           // Move the references, by whole numbers.
           float w[HS];  // a NaN is no maximum
 #pragma unroll
@@ -647,6 +653,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           const float top = max_lanes<HS>(w, lane);
           if (lane % (32 / HS) == 0) sh.most[warp][lane / (32 / HS)] = top;
           set_sync(set);
+          bool far = false;
           if (e < HS) {
             const float(*m)[HS] = &sh.most[set * 4];
             const float top = fmaxf(fmaxf(m[0][e], m[1][e]), fmaxf(m[2][e], m[3][e])), by = ceilf(top) - (begins(nref[e]) ? 4.0f : 5.0f);
@@ -656,7 +663,10 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
             sh.step[set * HS + e] = moves ? -by : 0.0f;
             sh.factor[set * HS + e] = moves && !first ? exp2_fast(-by) : 1.0f;
             if (moves) nref[e] = nref[e] == by ? -0.0f : nref[e] - by;
+            far = moves && !first && by > kFar;
           }
+          more = again && set_any(set, far);
+          again = false;
           set_sync(set);
           const uint64_t* step = reinterpret_cast<const uint64_t*>(sh.step + set * HS);
 #pragma unroll
@@ -685,6 +695,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
             tmem_wait_st();
           }
           fresh = set_any(set, e < heads && begins(nref[e]));
+        }
         }
         uint32_t words[TERMS][HS / 4];  // the weights' terms, four heads each
 #pragma unroll

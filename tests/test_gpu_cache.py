@@ -454,6 +454,29 @@ def test_attention_whose_logits_grow(heads, dtype):
             _attention_check({**c, "k": flat, "k_scales": units}, f"one above the rest by {logit}")
 
 
+@pytest.mark.parametrize("heads,dtype", [(8, BF16), (16, FP16), (64, BF16)])
+@pytest.mark.parametrize("order", [1, -1])
+def test_attention_near_entries_behind_far_ones(heads, dtype, order):
+    """Two entries near the query, and a tile (or several) thousands of positions away, before them or behind: what the
+    far ones leave of the near ones' logits is as exact as without them."""
+    D, ps, now = 64, 64, 9000
+    c = _attend(1, 1, heads, 1, D, D, 2, now + 1, ps, 1, dtype, seed=21)
+    c["k"], c["v"] = _codes(c["k"].shape, 1), _codes(c["v"].shape, 2)
+    c["k_scales"], c["v_scales"] = _scales(c["k_scales"].shape, 3), _scales(c["v_scales"].shape, 4)
+    c["query_positions"], c["slopes"] = _ints([[now]]), torch.full((heads,), 1.0, device=DEV)
+    near = [now - 1, now]
+    c["indices"] = _ints(near).view(1, 1, 2)
+    _attention_check(c, "alone")
+    for far in (128, 300):
+        idx = _ints((list(range(far)) + near)[::order]).view(1, 1, far + 2)
+        # the far entries' weights are 0: the bound is that of two entries
+        want = C.attention(c["q"], c["k"], c["v"], c["k_scales"], c["v_scales"], c["indices"], c["page_table"], c["query_positions"],
+                           c["scale"], 0.0, c["slopes"])
+        out, lse = tk.sparse_attention(**{**c, "indices": idx}, return_lse=True)
+        R.assert_near(lse, want[2], want[3], f"lse, {far} far")
+        R.assert_near(out, want[0], want[1], f"out, {far} far")
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 def test_attention_scales_far_apart(dtype):
     """Scales of 0, of the least size, and of sizes 2^40 apart, those of the keys and of the values."""
