@@ -78,12 +78,6 @@ __device__ __forceinline__ float scale_for(float half) {
   return __uint_as_float(static_cast<uint32_t>(max(n, -126) + 127) << 23);
 }
 
-__device__ __forceinline__ uint32_t max_two(uint32_t x, uint32_t y) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
-
 // The two numbers of 32 bits of a 16-bit type.
 template <typename E>
 __device__ __forceinline__ float2 floats_of(uint32_t two) {

@@ -65,11 +65,26 @@ struct Shape {
   static constexpr int rows = terms * G;           // (term, head) pairs
   static constexpr int N = (rows + 15) / 16 * 16;  // columns; those past the rows hold nothing
   static constexpr int p_bytes = N * kEntries;     // of a buffer of weights
-  static constexpr int softmax = 4 * sets, gather = G <= 32 ? 8 : 4, queries = G <= 16 ? 3 : 4;  // warps
+  static constexpr int softmax = 4 * sets, gather = G <= 32 ? 8 : 4, queries = G <= 16 ? 3 : 7;  // warps
   static constexpr int mma = softmax + gather, query = mma + 1;
   static constexpr int threads = (query + queries) * 32;
   static constexpr int per_sm = G <= 16 ? 2 : 1;
+  // Registers a thread: at the launch, and of the groups of four warps of each kind.
+  static constexpr int regs = G <= 16 ? 64 : G == 32 ? 80 : 72;
+  static constexpr int softmax_regs = G <= 16 ? 80 : G == 32 ? 88 : 88;
+  static constexpr int gather_regs = G <= 16 ? 64 : G == 32 ? 64 : 48, query_regs = G <= 16 ? 48 : G == 32 ? 56 : 48;
+  static_assert(softmax % 4 == 0 && gather % 4 == 0 && (queries + 1) % 4 == 0);
+  static_assert(softmax * softmax_regs + gather * gather_regs + (queries + 1) * query_regs <= (threads / 32) * regs);
 };
+
+// The registers of each thread of four warps.
+template <int FROM, int TO>
+__device__ __forceinline__ void registers() {
+  if constexpr (TO > FROM)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TO));
+  else if constexpr (TO < FROM)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TO));
+}
 
 struct E4Params {
   sparse_attention_args a;
@@ -327,6 +342,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
 
   if (gathers) {
     // ---- gather ----
+    registers<S::regs, S::gather_regs>();
     // 16-byte units of an entry's keys: those that it has, and those that are read
     const int k_units = a.D / 16, k_read = p.d_steps * 2, v_units = a.Dv / 16;
     const uint32_t unit16 = lane & 7, sub = lane >> 3;
@@ -404,146 +420,150 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
     }
     copy_commit();
     copy_wait<0>();
-  } else if (warp == S::mma) {
-    // ---- products, all by one thread: S of the next tile, then O^T of this one ----
-    // So scores that are there say that the weights of the tile two before were used, and
-    // a work's first weights that the sums of the one before have been read.
-    one = elect_one();
-    if (tiles > 0 && one) {
-      const uint32_t s_desc = mma_desc(0, N), o_desc = mma_desc(0, N, true, true);
-      const uint64_t q_desc = operand_desc(base), k_desc = operand_desc(k_ring);
-      const uint64_t v_desc = operand_desc(p.shared ? k_ring : v_ring), p_desc = weights_desc(p_at);
-      const int v_stages = p.shared ? p.k_stages : p.v_stages, v_bytes = p.shared ? p.k_bytes : p.v_bytes;
-      const int last = static_cast<int>((p.works - first_w + step_w - 1) / step_w) * tiles;  // first_w < works
-      int k_stage = 0, k_turn = 0, v_stage = 0, v_turn = 0;
-      int s_work = 0, s_tile = 0, o_tile = 0;
-      bool ok = true;
-      auto scores = [&](int n) {
-        const int qb = s_work & 1;
-        if (s_tile == 0) ok = wait_or_stop_one(&sh.q_full[qb], (s_work >> 1) & 1, stop);
-        ok = ok && wait_or_stop_one(&sh.k_full[k_stage], k_turn, stop);
-        if (!ok) return;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint64_t kd = k_desc + static_cast<uint32_t>(k_stage * p.k_bytes >> 4);
-        const uint64_t qd = q_desc + static_cast<uint32_t>(qb * q_bytes >> 4);
-        const uint32_t to = tmem_s + (n & 1) * N;
-        for (int j = 0; j < p.d_steps; ++j) {
-          const uint32_t c = j >> 2, in = (j & 3) * 2;
-          mma_f8(to, kd + (c * (kEntries * 128 >> 4) + in), qd + (c * (S::rows * 128 >> 4) + in), s_desc, j > 0);
-        }
-        mma_commit(&sh.s_full[n & 7]);
-        mbar_arrive(&sh.s_full[n & 7]);  // by this thread, which has seen the tile's notes
-        if (++k_stage == p.k_stages) k_stage = 0, k_turn ^= 1;
-        if (++s_tile == tiles) {
-          mma_commit(&sh.q_empty[qb]);
-          s_tile = 0, ++s_work;
-        }
-      };
-      scores(0);
-      for (int n = 0; n < last && ok; ++n) {
-        if (n + 1 < last) scores(n + 1);
-        if (!p.shared) {
-          ok = ok && wait_or_stop_one(&sh.v_full[v_stage], v_turn, stop);
+    registers<S::gather_regs, S::regs>();
+  } else if (warp >= S::mma) {
+    registers<S::regs, S::query_regs>();  // one instruction for the four warps of a group
+    if (warp == S::mma) {
+      // ---- products, all by one thread: S of the next tile, then O^T of this one ----
+      // So scores that are there say that the weights of the tile two before were used, and
+      // a work's first weights that the sums of the one before have been read.
+      one = elect_one();
+      if (tiles > 0 && one) {
+        const uint32_t s_desc = mma_desc(0, N), o_desc = mma_desc(0, N, true, true);
+        const uint64_t q_desc = operand_desc(base), k_desc = operand_desc(k_ring);
+        const uint64_t v_desc = operand_desc(p.shared ? k_ring : v_ring), p_desc = weights_desc(p_at);
+        const int v_stages = p.shared ? p.k_stages : p.v_stages, v_bytes = p.shared ? p.k_bytes : p.v_bytes;
+        const int last = static_cast<int>((p.works - first_w + step_w - 1) / step_w) * tiles;  // first_w < works
+        int k_stage = 0, k_turn = 0, v_stage = 0, v_turn = 0;
+        int s_work = 0, s_tile = 0, o_tile = 0;
+        bool ok = true;
+        auto scores = [&](int n) {
+          const int qb = s_work & 1;
+          if (s_tile == 0) ok = wait_or_stop_one(&sh.q_full[qb], (s_work >> 1) & 1, stop);
+          ok = ok && wait_or_stop_one(&sh.k_full[k_stage], k_turn, stop);
+          if (!ok) return;
           fence_proxy_async_smem();
-        }
-        ok = ok && wait_or_stop_one(&sh.p_full[n & 7], (n >> 3) & 1, stop);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t vd = v_desc + static_cast<uint32_t>(v_stage * v_bytes >> 4);
-        const uint64_t pd = p_desc + static_cast<uint32_t>((n & 1) * S::p_bytes >> 4);
-        for (int m = 0; m < p.v_blocks; ++m)
+          tc_fence_after();
+          const uint64_t kd = k_desc + static_cast<uint32_t>(k_stage * p.k_bytes >> 4);
+          const uint64_t qd = q_desc + static_cast<uint32_t>(qb * q_bytes >> 4);
+          const uint32_t to = tmem_s + (n & 1) * N;
+          for (int j = 0; j < p.d_steps; ++j) {
+            const uint32_t c = j >> 2, in = (j & 3) * 2;
+            mma_f8(to, kd + (c * (kEntries * 128 >> 4) + in), qd + (c * (S::rows * 128 >> 4) + in), s_desc, j > 0);
+          }
+          mma_commit(&sh.s_full[n & 7]);
+          mbar_arrive(&sh.s_full[n & 7]);  // by this thread, which has seen the tile's notes
+          if (++k_stage == p.k_stages) k_stage = 0, k_turn ^= 1;
+          if (++s_tile == tiles) {
+            mma_commit(&sh.q_empty[qb]);
+            s_tile = 0, ++s_work;
+          }
+        };
+        scores(0);
+        for (int n = 0; n < last && ok; ++n) {
+          if (n + 1 < last) scores(n + 1);
+          if (!p.shared) ok = ok && wait_or_stop_one(&sh.v_full[v_stage], v_turn, stop);
+          ok = ok && wait_or_stop_one(&sh.p_full[n & 7], (n >> 3) & 1, stop);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const uint64_t vd = v_desc + static_cast<uint32_t>(v_stage * v_bytes >> 4);
+          const uint64_t pd = p_desc + static_cast<uint32_t>((n & 1) * S::p_bytes >> 4);
+          for (int m = 0; m < p.v_blocks; ++m)
 #pragma unroll
-          for (int j = 0; j < kEntries / 32; ++j)
-            mma_f8(tmem_o + m * N, vd + static_cast<uint32_t>((m * (kEntries * 128) + j * (32 * 128)) >> 4),
-                   pd + static_cast<uint32_t>(j * (32 * 16) >> 4), o_desc, o_tile + j > 0);
-        mma_commit(&sh.pv_done[n & 7]);
-        if (++v_stage == v_stages) v_stage = 0, v_turn ^= 1;
-        if (++o_tile == tiles) o_tile = 0;
-      }
-    }
-    __syncwarp();
-  } else if (warp >= S::query) {
-    // ---- queries: a power of two for each head and terms in units of it ----
-    // A warp has every so many heads, kAhead of them at once; the next ones, of this work or
-    // the next, are on their way meanwhile.
-    const int who = warp - S::query;
-    constexpr int kAhead = 4;
-    uint4 raw[kAhead];
-    auto load = [&](const E4Work& k, int h0) {
-      const E* q = static_cast<const E*>(a.q) + k.b * a.q_seq_stride + k.t * a.q_token_stride + k.head0 * a.q_head_stride;
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int h = h0 + u * S::queries;
-        const E* from = q + h * a.q_head_stride + lane * 8;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (h >= k.heads || lane * 8 >= a.D) continue;  // D is a multiple of 16
-        if (p.q_vector) {
-          raw[u] = *reinterpret_cast<const uint4*>(from);
-        } else {
-          const uint16_t* e = reinterpret_cast<const uint16_t*>(from);
-          auto two = [&](int j) { return e[j] | static_cast<uint32_t>(e[j + 1]) << 16; };
-          raw[u] = make_uint4(two(0), two(2), two(4), two(6));
+            for (int j = 0; j < kEntries / 32; ++j)
+              mma_f8(tmem_o + m * N, vd + static_cast<uint32_t>((m * (kEntries * 128) + j * (32 * 128)) >> 4),
+                     pd + static_cast<uint32_t>(j * (32 * 16) >> 4), o_desc, o_tile + j > 0);
+          mma_commit(&sh.pv_done[n & 7]);
+          if (++v_stage == v_stages) v_stage = 0, v_turn ^= 1;
+          if (++o_tile == tiles) o_tile = 0;
         }
       }
-    };
-    int nw = 0;
-    E4Work k = e4_work<G>(p, first_w);
-    if (tiles > 0) load(k, who);
-    for (uint32_t w_at = first_w; tiles > 0 && w_at < p.works; w_at += step_w, ++nw) {
-      const int qb = nw & 1, heads = k.heads;
-      if (nw >= kBufs && !wait_or_stop(&sh.q_empty[qb], ((nw >> 1) - 1) & 1, stop)) break;
-      unsigned char* to = smem + qb * q_bytes;
-      for (int h0 = who; h0 < G; h0 += S::queries * kAhead) {
-        uint4 now[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) now[u] = raw[u];
-        if (h0 + S::queries * kAhead < G) {
-          load(k, h0 + S::queries * kAhead);
-        } else if (w_at + step_w < p.works) {
-          k = e4_work<G>(p, w_at + step_w);
-          load(k, who);
-        }
+      __syncwarp();
+    } else {
+      // ---- queries: a power of two for each head and terms in units of it ----
+      // A warp has every so many heads, kAhead of them at once; the next ones, of this work or
+      // the next, are on their way meanwhile.
+      const int who = warp - S::query;
+      constexpr int kAhead = 2;
+      uint4 raw[kAhead];
+      auto load = [&](const E4Work& k, int h0) {
+        const E* q = static_cast<const E*>(a.q) + k.b * a.q_seq_stride + k.t * a.q_token_stride + k.head0 * a.q_head_stride;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           const int h = h0 + u * S::queries;
-          if (h >= G) continue;
-          const uint32_t in[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
-          uint32_t most = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) most = __vmaxu2(most, in[j] & 0x7fff7fffu);
-          most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
-          const uint32_t top = __float_as_uint(Two<E>::get(most).x);
-          // the largest in [2^7, 2^8) units; a query that is not finite is NaN throughout
-          const bool bad = top >= 0x7f800000u;
-          const int exponent = max(static_cast<int>(top >> 23) - 127 - 7, -120);
-          const float over = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
-          if (lane == 0) sh.unit[nw & 3][h] = h < heads ? __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23) : 0.0f;
-          uint32_t x[4];  // in fp16: exact from 2^-14 units on, below the last term's steps
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 y = Two<E>::get(in[j]);
-            x[j] = bad ? 0x7fff7fffu : half_two(y.x * over, y.y * over);
-          }
-          if (lane * 8 >= p.d_blocks * 128) continue;
-#pragma unroll
-          for (int t = 0; t < TERMS; ++t) {
-            uint32_t two[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              two[j] = e4m3_of_half2(x[j]);
-              if (t + 1 < TERMS) x[j] = rest16(x[j], half2_of_e4m3(two[j]));
-            }
-            *reinterpret_cast<uint2*>(to + (lane >> 4) * q_block + swizzled(t * G + h, (lane >> 1) & 7) + (lane & 1) * 8) =
-                make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
+          const E* from = q + h * a.q_head_stride + lane * 8;
+          raw[u] = make_uint4(0, 0, 0, 0);
+          if (h >= k.heads || lane * 8 >= a.D) continue;  // D is a multiple of 16
+          if (p.q_vector) {
+            raw[u] = *reinterpret_cast<const uint4*>(from);
+          } else {
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(from);
+            auto two = [&](int j) { return e[j] | static_cast<uint32_t>(e[j + 1]) << 16; };
+            raw[u] = make_uint4(two(0), two(2), two(4), two(6));
           }
         }
+      };
+      int nw = 0;
+      E4Work k = e4_work<G>(p, first_w);
+      if (tiles > 0) load(k, who);
+      for (uint32_t w_at = first_w; tiles > 0 && w_at < p.works; w_at += step_w, ++nw) {
+        const int qb = nw & 1, heads = k.heads;
+        if (nw >= kBufs && !wait_or_stop(&sh.q_empty[qb], ((nw >> 1) - 1) & 1, stop)) break;
+        unsigned char* to = smem + qb * q_bytes;
+        for (int h0 = who; h0 < G; h0 += S::queries * kAhead) {
+          uint4 now[kAhead];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) now[u] = raw[u];
+          if (h0 + S::queries * kAhead < G) {
+            load(k, h0 + S::queries * kAhead);
+          } else if (w_at + step_w < p.works) {
+            k = e4_work<G>(p, w_at + step_w);
+            load(k, who);
+          }
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const int h = h0 + u * S::queries;
+            if (h >= G) continue;
+            const uint32_t in[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
+            uint32_t most = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) most = max_two(most, in[j] & 0x7fff7fffu);
+            most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+            const uint32_t top = __float_as_uint(Two<E>::get(most).x);
+            // the largest in [2^7, 2^8) units; a query that is not finite is NaN throughout
+            const bool bad = top >= 0x7f800000u;
+            const int exponent = max(static_cast<int>(top >> 23) - 127 - 7, -120);
+            const float over = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
+            if (lane == 0) sh.unit[nw & 3][h] = h < heads ? __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23) : 0.0f;
+            uint32_t x[4];  // in fp16: exact from 2^-14 units on, below the last term's steps
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 y = Two<E>::get(in[j]);
+              x[j] = bad ? 0x7fff7fffu : half_two(y.x * over, y.y * over);
+            }
+            if (lane * 8 >= p.d_blocks * 128) continue;
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t) {
+              uint32_t two[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                two[j] = e4m3_of_half2(x[j]);
+                if (t + 1 < TERMS) x[j] = rest16(x[j], half2_of_e4m3(two[j]));
+              }
+              *reinterpret_cast<uint2*>(to + (lane >> 4) * q_block + swizzled(t * G + h, (lane >> 1) & 7) + (lane & 1) * 8) =
+                  make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full[qb]), mbar_arrive(&sh.units[nw & 3]);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.q_full[qb]), mbar_arrive(&sh.units[nw & 3]);
     }
+    __syncwarp();
+    registers<S::query_regs, S::regs>();
   } else {
+    registers<S::regs, S::softmax_regs>();
     // ---- softmax: thread `e` of a set has entry e of each tile, for the set's heads ----
     const int set = warp >> 2, e = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
@@ -576,6 +596,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         // Logits in units of log 2, two heads at a time, less the references; once more where
         // those moved so far that what is left after them was rounded away.
         uint64_t z[HS / 2];
+        bool moved = false;  // sums have to follow
 #pragma unroll 1
         for (bool more = true, again = true; more;) {
           {
@@ -640,8 +661,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           const float2 y = both(z[h]);
           high = fmaxf(high, fmaxf(y.x, y.y));
         }
-        const bool moves_any = set_any(set, seen && (fresh || high + log_vs > kLogLimit));
-        if (!moves_any) break;
+        if (!fresh && !set_any(set, seen && high + log_vs > kLogLimit)) break;
         {
           // Move the references, by whole numbers.
           float w[HS];  // a NaN is no maximum
@@ -661,47 +681,37 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
             // what a head's references are depends on its own logits alone.
             const bool first = begins(nref[e]), moves = e < heads && (first ? by > -1e30f : top > kLogLimit);
             sh.step[set * HS + e] = moves ? -by : 0.0f;
-            sh.factor[set * HS + e] = moves && !first ? exp2_fast(-by) : 1.0f;
+            const float factor = moves && !first ? exp2_fast(-by) : 1.0f;
+            sh.factor[set * HS + e] = again ? factor : factor * sh.factor[set * HS + e];
             if (moves) nref[e] = nref[e] == by ? -0.0f : nref[e] - by;
             far = moves && !first && by > kFar;
           }
-          more = again && set_any(set, far);
+          more = i > 0 && again && set_any(set, far);
           again = false;
-          set_sync(set);
+          fresh = set_any(set, e < heads && begins(nref[e]));
           const uint64_t* step = reinterpret_cast<const uint64_t*>(sh.step + set * HS);
 #pragma unroll
           for (int h = 0; h < HS / 2; ++h) z[h] = add2(z[h], step[h]);
-          if (i > 0) {
-            ok = wait_or_stop(&sh.pv_done[(at - 1) & 7], ((at - 1) >> 3) & 1, stop) && ok;
-            tc_fence_after();
-            const ulonglong2* factor = reinterpret_cast<const ulonglong2*>(sh.factor + set * HS);
-#pragma unroll
-            for (int h = 0; h < HS / 4; ++h) {
-              const ulonglong2 f = factor[h];
-              sum[2 * h] = mul2(sum[2 * h], f.x), sum[2 * h + 1] = mul2(sum[2 * h + 1], f.y);
-            }
-            // eight columns at a time: more would not leave registers for the logits
-#pragma unroll 1
-            for (int c = 0; c < p.v_blocks * TERMS * (HS / 8); ++c) {
-              const int block = c / (HS / 8), at8 = (c % (HS / 8)) * 8;
-              const uint32_t o_at = tmem_o + (block / TERMS) * N + lanes + (block % TERMS) * G + set * HS + at8;
-              uint32_t v[8];
-              tmem_ld(v, o_at);
-              tmem_wait_ld(v);
-#pragma unroll
-              for (int h = 0; h < 8; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * sh.factor[set * HS + at8 + h]);
-              tmem_st(o_at, v);
-            }
-            tmem_wait_st();
-          }
-          fresh = set_any(set, e < heads && begins(nref[e]));
+          moved = i > 0;
         }
+        }
+        if (moved) {
+          const ulonglong2* factor = reinterpret_cast<const ulonglong2*>(sh.factor + set * HS);
+#pragma unroll
+          for (int h = 0; h < HS / 4; ++h) {
+            const ulonglong2 f = factor[h];
+            sum[2 * h] = mul2(sum[2 * h], f.x), sum[2 * h + 1] = mul2(sum[2 * h + 1], f.y);
+          }
+        }
+        if (notes.seen[e >> 5] != 0xffffffffu && !seen) {
+#pragma unroll
+          for (int h = 0; h < HS / 2; ++h) z[h] = twice(__int_as_float(0xff800000));
         }
         uint32_t words[TERMS][HS / 4];  // the weights' terms, four heads each
 #pragma unroll
         for (int h = 0; h < HS / 2; ++h) {
           const float2 y = both(z[h]);
-          const uint64_t w = pair(seen ? exp2_fast(y.x) : 0.0f, seen ? exp2_fast(y.y) : 0.0f);
+          const uint64_t w = pair(exp2_fast(y.x), exp2_fast(y.y));
           sum[h] = add2(sum[h], w);
           const float2 scaled = both(mul2(w, twice(vs)));
           uint32_t x = half_two(scaled.x, scaled.y);
@@ -721,7 +731,33 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           put16(to, words[0][0], words[0][1], words[1][0], words[1][1]);
           if constexpr (TERMS == 3) put16(to + kEntries * 16, words[2][0], words[2][1], 0, 0);
         }
-        fence_proxy_async_smem();
+        if (moved) {
+          // the columns of the heads that moved
+          ok = wait_or_stop(&sh.pv_done[(at - 1) & 7], ((at - 1) >> 3) & 1, stop) && ok;
+          tc_fence_after();
+          uint32_t which = __ballot_sync(0xffffffffu, lane < HS && sh.factor[set * HS + (lane & (HS - 1))] != 1.0f);
+#pragma unroll 1
+          for (; which != 0; which &= which - 1) {
+            const int h = set * HS + __ffs(which) - 1;
+            const float f = sh.factor[h];
+            uint32_t v[2][TERMS];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int t = 0; t < TERMS; ++t)
+                if (m < p.v_blocks) tmem_ld(v[m][t], tmem_o + m * N + lanes + t * G + h);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int t = 0; t < TERMS; ++t) tmem_wait_ld(v[m][t]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int t = 0; t < TERMS; ++t)
+                if (m < p.v_blocks) tmem_st(tmem_o + m * N + lanes + t * G + h, __float_as_uint(__uint_as_float(v[m][t]) * f));
+          }
+          tmem_wait_st();
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[at & 7]);
@@ -764,9 +800,9 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       const int pad = p.v_blocks * 128;
       float* rows = reinterpret_cast<float*>(smem) + set * HS * pad;
       for (int m = 0; m < p.v_blocks; ++m) {
-        float x[HS];
+        uint64_t x[HS / 2];  // of two heads
 #pragma unroll
-        for (int h = 0; h < HS; ++h) x[h] = 0.0f;
+        for (int h = 0; h < HS / 2; ++h) x[h] = 0;
         if (tiles > 0) {
           uint32_t v[TERMS][HS];
           const uint32_t o_at = tmem_o + m * N + lanes + set * HS;
@@ -774,30 +810,32 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           for (int t = 0; t < TERMS; ++t) tmem_ld(v[t], o_at + t * G);
 #pragma unroll
           for (int t = 0; t < TERMS; ++t) tmem_wait_ld(v[t]);
+          auto of = [&](int t, int h) { return pair(__uint_as_float(v[t][2 * h]), __uint_as_float(v[t][2 * h + 1])); };
 #pragma unroll
-          for (int h = 0; h < HS; ++h) {
-            x[h] = __uint_as_float(v[TERMS - 1][h]);
+          for (int h = 0; h < HS / 2; ++h) {
+            x[h] = of(TERMS - 1, h);
 #pragma unroll
-            for (int t = TERMS - 2; t >= 0; --t) x[h] = fmaf(x[h], 0x1p-4f, __uint_as_float(v[t][h]));
+            for (int t = TERMS - 2; t >= 0; --t) x[h] = fma2(x[h], twice(0x1p-4f), of(t, h));
           }
         }
         if (!ok) {
 #pragma unroll
-          for (int h = 0; h < HS; ++h) x[h] = __int_as_float(0x7fc00000);
+          for (int h = 0; h < HS / 2; ++h) x[h] = twice(__int_as_float(0x7fc00000));
         }
         const int d = m * 128 + e;
         if (cluster > 1) {
 #pragma unroll
-          for (int h = 0; h < HS; ++h) rows[h * pad + d] = x[h];
+          for (int h = 0; h < HS / 2; ++h) {
+            const float2 y = both(x[h]);
+            rows[2 * h * pad + d] = y.x, rows[(2 * h + 1) * pad + d] = y.y;
+          }
         } else if (d < a.Dv) {
 #pragma unroll
           for (int h = 0; h < HS; h += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&sh.inverse[set * HS + h]);
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sh.inverse[set * HS + h]);
+            const float2 y = both(mul2(x[h / 2], f.x)), z = both(mul2(x[h / 2 + 1], f.y));
             E* row = reinterpret_cast<E*>(row_of(h)) + d;
-            row[0] = E(x[h] * f.x);
-            row[256] = E(x[h + 1] * f.y);
-            row[512] = E(x[h + 2] * f.z);
-            row[768] = E(x[h + 3] * f.w);
+            row[0] = E(y.x), row[256] = E(y.y), row[512] = E(z.x), row[768] = E(z.y);
           }
         }
       }
@@ -815,6 +853,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       tc_fence_before();  // O is read: the next work's first weights say so
       set_sync(set);      // and what the set shares
     }
+    registers<S::softmax_regs, S::regs>();
   }
 
   __syncthreads();
@@ -937,6 +976,12 @@ topk_status launch_heads(const sparse_attention_e4m3_args& args, int dev, int sm
   const int64_t grid = cluster == 1 && work > slots ? slots : work * cluster;
   if ((work / grid + 1) * tiles > INT32_MAX) return TOPK_EINVAL;  // a CTA counts its tiles
   constexpr auto kernel = cache_attention_kernel<E, G>;
+  // What the groups of warps trade is what the launch brings.
+  static const int regs = [] {
+    cudaFuncAttributes f = {};
+    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (regs != S::regs) return TOPK_ECUDA;
   const topk_status st = allow_shared<kernel>(dev);
   if (st != TOPK_OK) return st;
   cudaLaunchConfig_t cfg = {};

@@ -21,4 +21,11 @@ __device__ __forceinline__ float2 e4m3_both(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// The larger ones of two pairs of 16-bit numbers without a sign.
+__device__ __forceinline__ uint32_t max_two(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
 }  // namespace tki

@@ -66,6 +66,10 @@ __device__ __forceinline__ void tmem_ld(uint32_t (&v)[16], uint32_t addr) {
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(addr));
 }
+__device__ __forceinline__ void tmem_wait_ld(uint32_t& v) { asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(v) : : "memory"); }
+__device__ __forceinline__ void tmem_ld(uint32_t& v, uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(addr));
+}
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
@@ -95,6 +99,9 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&v)[16]) 
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st(uint32_t addr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
