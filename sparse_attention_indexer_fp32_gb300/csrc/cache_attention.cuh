@@ -790,13 +790,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       if (cluster == 1 && a.lse != nullptr && e < heads) a.lse[k.row * a.Hq + k.head0 + set * HS + e] = e4_logsum(-nref[e], total);
       if (tiles > 0 && !wait_or_stop(&sh.pv_done[(n + tiles - 1) & 7], ((n + tiles - 1) >> 3) & 1, stop)) ok = false;
       tc_fence_after();
-      // Results by way of the set's own units of the weights' buffers, which are free: a
-      // thread has one element of every head, and writes 16 bytes of one. Four heads, of up
-      // to 512 bytes, a unit.
-      auto row_of = [&](int h) {
-        const int unit = h / 4, buf = HS == 16 ? unit / TERMS : unit, t = HS == 16 ? unit % TERMS : 0;
-        return smem + p.p_at + buf * S::p_bytes + (t * SETS + set) * (kEntries * 16) + (h & 3) * 512;
-      };
+      // A thread has one element of every head: two bytes a store, side by side in a warp.
       const int pad = p.v_blocks * 128;
       float* rows = reinterpret_cast<float*>(smem) + set * HS * pad;
       for (int m = 0; m < p.v_blocks; ++m) {
@@ -834,20 +828,12 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           for (int h = 0; h < HS; h += 4) {
             const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sh.inverse[set * HS + h]);
             const float2 y = both(mul2(x[h / 2], f.x)), z = both(mul2(x[h / 2 + 1], f.y));
-            E* row = reinterpret_cast<E*>(row_of(h)) + d;
-            row[0] = E(y.x), row[256] = E(y.y), row[512] = E(z.x), row[768] = E(z.y);
+            E* row = static_cast<E*>(a.out) + (k.row * a.Hq + k.head0 + set * HS + h) * a.Dv + d;
+            if (h < heads) row[0] = E(y.x);
+            if (h + 1 < heads) row[a.Dv] = E(y.y);
+            if (h + 2 < heads) row[2 * a.Dv] = E(z.x);
+            if (h + 3 < heads) row[3 * a.Dv] = E(z.y);
           }
-        }
-      }
-      if (cluster == 1) {
-        set_sync(set);
-        const int units = a.Dv / 8;  // of 16 bytes, up to 32
-#pragma unroll
-        for (int j = 0; j < HS / 4; ++j) {
-          const int h = (warp & 3) * (HS / 4) + j;
-          if (h < heads && lane < units)
-            reinterpret_cast<uint4*>(static_cast<E*>(a.out) + (k.row * a.Hq + k.head0 + set * HS + h) * a.Dv)[lane] =
-                reinterpret_cast<const uint4*>(row_of(h))[lane];
         }
       }
       tc_fence_before();  // O is read: the next work's first weights say so
