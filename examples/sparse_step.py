@@ -4,8 +4,9 @@ For every sequence of a batch: the new token's key is rotated on its way into th
 queries are rotated, the indexer scores every position of the sequence, the selection takes the best
 ``k``, and attention runs over those entries only. All of it is enqueued on one stream and can be
 captured in a CUDA graph: nothing is allocated where the buffers are given, and nothing is read back.
+With ``--eight`` keys and values are held in 8 bits, with a scale for each page and head.
 
-    python examples/sparse_step.py [--batch 8] [--length 4000] [--k 512]
+    python examples/sparse_step.py [--batch 8] [--length 4000] [--k 512] [--eight]
 """
 
 from __future__ import annotations
@@ -24,11 +25,13 @@ import sparse_attention_indexer_fp32_gb300 as tk  # noqa: E402
 class Cache:
     """Pages of keys, values and indexer keys, and the page tables of the batch's sequences."""
 
-    def __init__(self, batch, width, page_size=64, kv_heads=4, head=128, index_head=128, device="cuda"):
+    def __init__(self, batch, width, page_size=64, kv_heads=4, head=128, index_head=128, device="cuda", eight=False):
         pages = -(-width // page_size)
         shape = (batch * pages, page_size)
-        self.k = torch.zeros((*shape, kv_heads, head), dtype=torch.bfloat16, device=device)
-        self.v = torch.zeros_like(self.k)
+        dtype = torch.float8_e4m3fn if eight else torch.bfloat16
+        self.k, self.v = (torch.zeros((*shape, kv_heads, head), dtype=dtype, device=device) for _ in range(2))
+        self.k_scales = torch.zeros((batch * pages, 1, kv_heads), device=device) if eight else None
+        self.v_scales = torch.zeros_like(self.k_scales) if eight else None
         self.index_k = torch.zeros((*shape, index_head), dtype=torch.bfloat16, device=device)
         self.table = torch.randperm(batch * pages, device=device).to(torch.int32).view(batch, pages)
         self.width, self.page_size = width, page_size
@@ -38,6 +41,11 @@ class Cache:
         page = self.table.gather(1, (positions // self.page_size).long()[:, None])[:, 0]
         return page * self.page_size + positions % self.page_size
 
+    def entries(self, held, scales, slots):
+        """Entries [n, Hkv, D] of slots in float32."""
+        x = held.flatten(0, 1)[slots].float()
+        return x if scales is None else x * scales[slots // self.page_size, 0, :, None]
+
 
 def step(cache, frequencies, q, k, v, index_q, index_weights, index_k, lengths, select):
     """One token a sequence. ``lengths`` [B] counts the token itself; ``q`` [B, Hq, D], ``k`` and ``v``
@@ -46,8 +54,12 @@ def step(cache, frequencies, q, k, v, index_q, index_weights, index_k, lengths, 
     B = lengths.numel()
     positions = lengths - 1
     slots = cache.slots(positions)
-    tk.rotary(k, positions, frequencies, out=cache.k, slots=slots)
-    cache.v.view(-1, *v.shape[1:])[slots.long()] = v
+    if cache.k_scales is None:
+        tk.rotary(k, positions, frequencies, out=cache.k, slots=slots)
+        cache.v.view(-1, *v.shape[1:])[slots.long()] = v
+    else:
+        tk.cache_append(k, v, positions, frequencies, cache.k, cache.v, slots, k_scales=cache.k_scales,
+                        v_scales=cache.v_scales)
     tk.rotary(index_k[:, None], positions, frequencies, out=cache.index_k[:, :, None], slots=slots)
     q = tk.rotary(q, positions, frequencies)
     index_q = tk.rotary(index_q, positions, frequencies)
@@ -55,7 +67,8 @@ def step(cache, frequencies, q, k, v, index_q, index_weights, index_k, lengths, 
                                width=cache.width)
     chosen = tk.topk_ragged(scores.view(B, -1), lengths, select)
     return tk.sparse_attention(q[:, None], cache.k, cache.v, chosen[:, None], cache.table,
-                               query_positions=positions[:, None])[:, 0]
+                               query_positions=positions[:, None], k_scales=cache.k_scales,
+                               v_scales=cache.v_scales)[:, 0]
 
 
 def step_plain(cache, frequencies, q, k, v, index_q, index_weights, index_k, lengths, select):
@@ -76,17 +89,21 @@ def step_plain(cache, frequencies, q, k, v, index_q, index_weights, index_k, len
         keys = cache.index_k.flatten(0, 1)[slots].float()
         scores = index_weights[b] @ torch.relu(tiq[b] @ keys.T)
         chosen = slots[scores.topk(min(select, n)).indices]
-        kk, vv = (c.flatten(0, 1)[chosen].float().repeat_interleave(q.shape[1] // c.shape[2], dim=1)
-                  for c in (cache.k, cache.v))
+        kk, vv = (cache.entries(c, s, chosen).repeat_interleave(q.shape[1] // c.shape[2], dim=1)
+                  for c, s in ((cache.k, cache.k_scales), (cache.v, cache.v_scales)))
         weights = torch.softmax(torch.einsum("hd,nhd->hn", tq[b], kk) * q.shape[2] ** -0.5, dim=-1)
         out[b] = torch.einsum("hn,nhd->hd", weights, vv).to(out.dtype)
     return out
 
 
-def make(batch, length, device="cuda", heads=32, kv_heads=4, head=128, index_heads=32, index_head=128):
+def make(batch, length, device="cuda", heads=32, kv_heads=4, head=128, index_heads=32, index_head=128, eight=False):
     """A cache with ragged sequences in it, the next token of each, and the frequencies."""
-    cache = Cache(batch, length + 1, kv_heads=kv_heads, head=head, index_head=index_head, device=device)
-    for t in (cache.k, cache.v, cache.index_k):
+    cache = Cache(batch, length + 1, kv_heads=kv_heads, head=head, index_head=index_head, device=device, eight=eight)
+    if eight:
+        for t, scales in ((cache.k, cache.k_scales), (cache.v, cache.v_scales)):
+            t.copy_(torch.randn(t.shape, device=device) * 64)
+            scales.fill_(1 / 64)
+    for t in (cache.index_k,) if eight else (cache.k, cache.v, cache.index_k):
         t.normal_()
     lengths = torch.randint(max(1, length // 2), length + 1, (batch,), device=device).to(torch.int32) + 1
 
@@ -104,9 +121,10 @@ def main() -> None:
     p.add_argument("--batch", type=int, default=8)
     p.add_argument("--length", type=int, default=4000)
     p.add_argument("--k", type=int, default=512)
+    p.add_argument("--eight", action="store_true")
     a = p.parse_args()
     torch.manual_seed(0)
-    cache, frequencies, token = make(a.batch, a.length)
+    cache, frequencies, token = make(a.batch, a.length, eight=a.eight)
     got = step(cache, frequencies, *token, a.k)
     want = step_plain(cache, frequencies, *token, a.k)
     print(f"relative difference from the formulas: {((got - want).float().norm() / want.float().norm()).item():.2e}")

@@ -13,7 +13,7 @@ CUDA kernels (``_build/libtopk_indexer.so``):
 * :func:`rotary` (with :func:`rotary_frequencies`), :func:`indexer_scores`,
   :func:`sparse_attention` - the steps around the selection: rotary positions
   (also into a paged cache), the indexer's scores over a paged key cache, and
-  attention over the selected entries;
+  attention over the selected entries of caches in 16 or 8 bits;
 * :func:`cache_append` - keys, rotated on the way, and values into paged caches,
   of their own type or in 8 bits with a scale for each block of tokens and head;
 * :func:`topk_select_ex` - diagnostics: a forced internal path, path counters;

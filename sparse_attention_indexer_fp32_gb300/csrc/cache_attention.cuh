@@ -19,19 +19,36 @@
 //
 // The scales. A key's scale multiplies its logit. A value's multiplies its weight
 // before that is split: w = 2^(z - r) s. The reference r of a head is moved, for
-// all threads at once, when a weight would pass E4M3's 448, and then to leave the
-// largest in (2^4, 2^5], so that it seldom moves again: terms end at steps of
-// 2^-13 / 2^4 of the largest weight (three terms: 2^-17 / 2^4), by which all of 2048
-// entries together lose half a step of the result at most. The sum that divides
-// adds the weights in FP32, unrounded and without the values' scales. r is a whole
-// number, so moving it is exact.
+// all threads at once, when a weight would pass E4M3's 448: first to leave the largest
+// in (2^3, 2^4], so that it seldom moves again, then in (2^4, 2^5]. The last term ends at
+// steps of 2^-13 (three terms: 2^-17), 2^-16 (2^-20) of the largest weight there is. The
+// sum that divides adds the weights in FP32, unrounded and without the values' scales. r
+// is a whole number, so moving it is exact but for logits that were rounded next to the
+// old one: past kFar those are computed anew. A head's references follow from its own
+// logits alone, so neither the rows nor the heads of a call change its bits.
 //
 // The rest is as in sparse_attention.cu: entries gathered by 16-byte copies into
 // rings of keys and values, few rows shared by a cluster whose CTAs join through
 // distributed shared memory, CTAs that stay for several rows where there are many.
 //
 // Warps: 4 softmax warps for each 16 heads (G = 8: for all 8), one entry a thread;
-// 4 or 8 that gather; one thread issues all products; 3 or 4 split queries ahead.
+// 4 or 8 that gather; one thread issues all products; 3 or 7 split queries ahead. Softmax
+// warps take registers from the others (setmaxnreg; 88 instead of 72 with 64 heads: a tile
+// that moves a reference spilled them, 182 us against 150 below).
+//
+// Bounds. Few heads and long lists: the entries' bytes. Many heads: the softmax warps, some
+// ten operations a logit (two terms joined, scaled, an exponential, a sum, two roundings
+// to E4M3 and the rest between them), and a row's end, where they wait for the last product,
+// sum and write while the tensor cores wait for them; TMEM has no room for a second set of
+// sums. Figures, in a CUDA graph:
+//   2048 rows x 64 heads over 512 shared entries of 256: 149 us, 32 of them at the rate of
+//   bf16 products (143 where no reference moves; 242 over 1024 entries, 80 over 128; 32 heads
+//   123, 16 heads 83, 8 heads 62, there 4.3 TB/s of entries out of L2);
+//   64 rows x 8 x 8 heads of 128 over 2048 entries: 57 us, 6 TB/s less a start of some 12 us
+//   (launch, list, page, entries, one behind the other); 4 rows over 512 entries 11.6 us.
+// Lost: dedicated warps that read the sums out (226 us: registers), two CTAs an SM with tiles
+// of 32 heads for 64 (270: entries are read twice), all columns of a set multiplied where one
+// reference moves (179), results by way of shared memory (129 for the 123).
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -69,10 +86,12 @@ struct Shape {
   static constexpr int mma = softmax + gather, query = mma + 1;
   static constexpr int threads = (query + queries) * 32;
   static constexpr int per_sm = G <= 16 ? 2 : 1;
-  // Registers a thread: at the launch, and of the groups of four warps of each kind.
+  // Registers a thread: at the launch, and of the groups of four warps of each kind. Gathering
+  // wants 64 where entries are few heads' (64 x 8 x 8 heads 57 us, 59.6 with 56 and 96 for softmax);
+  // with 64 heads softmax wants them (150 us, 156 with 80, 56 and 56).
   static constexpr int regs = G <= 16 ? 64 : G == 32 ? 80 : 72;
-  static constexpr int softmax_regs = G <= 16 ? 80 : G == 32 ? 88 : 88;
-  static constexpr int gather_regs = G <= 16 ? 64 : G == 32 ? 64 : 48, query_regs = G <= 16 ? 48 : G == 32 ? 56 : 48;
+  static constexpr int softmax_regs = G <= 16 ? 80 : 88;
+  static constexpr int gather_regs = G <= 32 ? 64 : 48, query_regs = G == 32 ? 56 : 48;
   static_assert(softmax % 4 == 0 && gather % 4 == 0 && (queries + 1) % 4 == 0);
   static_assert(softmax * softmax_regs + gather * gather_regs + (queries + 1) * query_regs <= (threads / 32) * regs);
 };
@@ -655,14 +674,13 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
             const uint64_t c0 = plain ? mul2(factor, u.x) : factor, c1 = plain ? mul2(factor, u.y) : factor;
             z[h] = fma2(z[h], c0, r.x), z[h + 1] = fma2(z[h + 1], c1, r.y);
           }
-        float high = -FLT_MAX;
+          float high = -FLT_MAX;
 #pragma unroll
-        for (int h = 0; h < HS / 2; ++h) {
-          const float2 y = both(z[h]);
-          high = fmaxf(high, fmaxf(y.x, y.y));
-        }
-        if (!fresh && !set_any(set, seen && high + log_vs > kLogLimit)) break;
-        {
+          for (int h = 0; h < HS / 2; ++h) {
+            const float2 y = both(z[h]);
+            high = fmaxf(high, fmaxf(y.x, y.y));
+          }
+          if (!fresh && !set_any(set, seen && high + log_vs > kLogLimit)) break;
           // Move the references, by whole numbers.
           float w[HS];  // a NaN is no maximum
 #pragma unroll
@@ -694,8 +712,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           for (int h = 0; h < HS / 2; ++h) z[h] = add2(z[h], step[h]);
           moved = i > 0;
         }
-        }
-        if (moved) {
+        if (moved) {  // the sums follow; O^T's columns do below, when the weights are out
           const ulonglong2* factor = reinterpret_cast<const ulonglong2*>(sh.factor + set * HS);
 #pragma unroll
           for (int h = 0; h < HS / 4; ++h) {
@@ -732,10 +749,10 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           if constexpr (TERMS == 3) put16(to + kEntries * 16, words[2][0], words[2][1], 0, 0);
         }
         if (moved) {
-          // the columns of the heads that moved
           ok = wait_or_stop(&sh.pv_done[(at - 1) & 7], ((at - 1) >> 3) & 1, stop) && ok;
           tc_fence_after();
           uint32_t which = __ballot_sync(0xffffffffu, lane < HS && sh.factor[set * HS + (lane & (HS - 1))] != 1.0f);
+          // one head's columns at a time: few move, and there are no registers for more
 #pragma unroll 1
           for (; which != 0; which &= which - 1) {
             const int h = set * HS + __ffs(which) - 1;
@@ -984,7 +1001,8 @@ topk_status launch_heads(const sparse_attention_e4m3_args& args, int dev, int sm
   return status_of(cudaLaunchKernelEx(&cfg, kernel, p, cluster));
 }
 
-// The least padded heads that hold those of a key head, or tiles of the most.
+// The least padded heads that hold those of a key head, or tiles of the most: columns cost the
+// softmax warps whether they hold a head or not, and a tile more reads the entries once more.
 template <typename E>
 topk_status launch_cache_attention(const sparse_attention_e4m3_args& a, int dev, int sm_count, cudaStream_t stream) {
   const int heads = a.attention.Hq / a.attention.Hkv;

@@ -102,11 +102,6 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&v)[16]) 
 __device__ __forceinline__ void tmem_st(uint32_t addr, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
 
 // ---- matrix products --------------------------------------------------------
 
