@@ -4,6 +4,7 @@ import ctypes
 import math
 import os
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -454,6 +455,16 @@ def test_attention_whose_logits_grow(heads, dtype):
             _attention_check({**c, "k": flat, "k_scales": units}, f"one above the rest by {logit}")
 
 
+@pytest.mark.parametrize("heads,Dv,dtype", [(8, 256, BF16), (8, 64, FP16), (16, 144, BF16), (16, 256, FP16), (32, 256, BF16),
+                                            (32, 128, FP16), (64, 256, BF16), (64, 128, BF16)])
+def test_attention_some_heads_references_move(heads, Dv, dtype):
+    """Heads of very different logits: in each tile a few references move, by a little or far, over one or two blocks
+    of values, in several rows a CTA."""
+    c = _attend(3, 2, heads, 1, 128, Dv, 700, 900, 64, 4, dtype, seed=heads + Dv)
+    c["q"] = c["q"] * torch.exp2((torch.arange(heads, device=DEV) * 5 % 7 - 3).float())[:, None].to(dtype)
+    _attention_check(c)
+
+
 @pytest.mark.parametrize("heads,dtype", [(8, BF16), (16, FP16), (64, BF16)])
 @pytest.mark.parametrize("order", [1, -1])
 def test_attention_near_entries_behind_far_ones(heads, dtype, order):
@@ -575,6 +586,38 @@ def test_attention_in_a_graph_and_on_streams():
 
 
 # ---- the whole way -----------------------------------------------------------------------------------
+
+
+def test_first_calls_of_a_process_are_captured():
+    """Nothing has to run eagerly before: a graph of the first calls gives what they give."""
+    code = """
+import torch, sparse_attention_indexer_fp32_gb300 as tk
+def randn(*shape):
+    return torch.randn(shape, device="cuda").to(torch.bfloat16)
+torch.manual_seed(0)
+k, v, q = randn(128, 2, 64), randn(128, 2, 64), randn(1, 1, 16, 64)
+caches = [torch.zeros((2, 64, 2, 64), device="cuda").to(torch.float8_e4m3fn) for _ in range(2)]
+scales = [torch.zeros((2, 1, 2), device="cuda") for _ in range(2)]
+slots = torch.arange(128, dtype=torch.int32, device="cuda")
+listed, freq = slots.view(1, 1, 128).clone(), tk.rotary_frequencies(64, device="cuda")
+out = torch.zeros((1, 1, 16, 64), dtype=torch.bfloat16, device="cuda")
+def call():
+    tk.cache_append(k, v, slots, freq, *caches, slots, k_scales=scales[0], v_scales=scales[1])
+    tk.sparse_attention(q, *caches, listed, k_scales=scales[0], v_scales=scales[1], out=out)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    call()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.view(torch.uint8).clone() for t in (*caches, *scales, out)]
+assert out.abs().max() > 0
+call()
+torch.cuda.synchronize()
+assert all(torch.equal(a, t.view(torch.uint8)) for a, t in zip(got, (*caches, *scales, out)))
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=120,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16])
