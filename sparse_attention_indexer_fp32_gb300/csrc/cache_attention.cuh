@@ -559,7 +559,11 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float2 y = Two<E>::get(in[j]);
-              x[j] = bad ? 0x7fff7fffu : half_two(y.x * over, y.y * over);
+              x[j] = half_two(y.x * over, y.y * over);
+            }
+            if (bad) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[j] = 0x7fff7fffu;
             }
             if (lane * 8 >= p.d_blocks * 128) continue;
 #pragma unroll
@@ -665,14 +669,21 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
               z[h] = fma2(s, twice(away), z[h]);
             }
           }
-          // what is left to do: z, or x c where neither cap nor slopes took the scales
+          // less the references; times the scales where neither cap nor slopes took them
           const bool plain = !(a.softcap > 0.0f) && slopes == nullptr;
-          const uint64_t factor = twice(plain ? ks * p.scale_log2e : 1.0f);
+          const uint64_t factor = twice(ks * p.scale_log2e);
+          if (plain) {
 #pragma unroll
-          for (int h = 0; h < HS / 2; h += 2) {
-            const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&unit[h]), r = *reinterpret_cast<const ulonglong2*>(&held[h]);
-            const uint64_t c0 = plain ? mul2(factor, u.x) : factor, c1 = plain ? mul2(factor, u.y) : factor;
-            z[h] = fma2(z[h], c0, r.x), z[h + 1] = fma2(z[h + 1], c1, r.y);
+            for (int h = 0; h < HS / 2; h += 2) {
+              const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&unit[h]), r = *reinterpret_cast<const ulonglong2*>(&held[h]);
+              z[h] = fma2(z[h], mul2(factor, u.x), r.x), z[h + 1] = fma2(z[h + 1], mul2(factor, u.y), r.y);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < HS / 2; h += 2) {
+              const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&held[h]);
+              z[h] = add2(z[h], r.x), z[h + 1] = add2(z[h + 1], r.y);
+            }
           }
           float high = -FLT_MAX;
 #pragma unroll
