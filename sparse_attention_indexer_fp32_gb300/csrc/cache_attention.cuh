@@ -36,19 +36,20 @@
 // warps take registers from the others (setmaxnreg; 88 instead of 72 with 64 heads: a tile
 // that moves a reference spilled them, 182 us against 150 below).
 //
-// Bounds. Few heads and long lists: the entries' bytes. Many heads: the softmax warps, some
-// ten operations a logit (two terms joined, scaled, an exponential, a sum, two roundings
-// to E4M3 and the rest between them), and a row's end, where they wait for the last product,
+// Bounds. Few heads and long lists: the entries' bytes. Many heads: the softmax warps (a
+// logit's two terms joined, scaled, an exponential, a sum, two roundings to E4M3 and the
+// rest between them: with loads and gathers thirty instructions), and a row's end, where they wait for the last product,
 // sum and write while the tensor cores wait for them; TMEM has no room for a second set of
 // sums. Figures, in a CUDA graph:
-//   2048 rows x 64 heads over 512 shared entries of 256: 149 us, 32 of them at the rate of
-//   bf16 products (143 where no reference moves; 242 over 1024 entries, 80 over 128; 32 heads
-//   123, 16 heads 83, 8 heads 62, there 4.3 TB/s of entries out of L2);
-//   64 rows x 8 x 8 heads of 128 over 2048 entries: 57 us, 6 TB/s less a start of some 12 us
+//   2048 rows x 64 heads over 512 shared entries of 256: 147 us, 32 of them at the rate of
+//   bf16 products (142 where no reference moves; 238 over 1024 entries, 80 over 128; 32 heads
+//   122, 16 heads 80, 8 heads 62, there 4.3 TB/s of entries out of L2). 53 thousand warp
+//   instructions a row: 7.6 a tile, 23 for queries, first references and the end; issue slots 65 %;
+//   64 rows x 8 x 8 heads of 128 over 2048 entries: 56.5 us, 6 TB/s less a start of some 12 us
 //   (launch, list, page, entries, one behind the other); 4 rows over 512 entries 11.6 us.
 // Lost: dedicated warps that read the sums out (226 us: registers), two CTAs an SM with tiles
 // of 32 heads for 64 (270: entries are read twice), all columns of a set multiplied where one
-// reference moves (179), results by way of shared memory (129 for the 123).
+// reference moves (179), results by way of shared memory (32 heads 129 for 123).
 #include <cuda_runtime.h>
 
 #include <cfloat>
