@@ -42,8 +42,8 @@
 // sum and write while the tensor cores wait for them; TMEM has no room for a second set of
 // sums. Figures, in a CUDA graph:
 //   2048 rows x 64 heads over 512 shared entries of 256: 147 us, 32 of them at the rate of
-//   bf16 products (142 where no reference moves; 238 over 1024 entries, 80 over 128; 32 heads
-//   122, 16 heads 80, 8 heads 62, there 4.3 TB/s of entries out of L2). 53 thousand warp
+//   bf16 products (137 where no reference moves; 233 over 1024 entries, 80 over 128; 32 heads
+//   119, 16 heads 80, 8 heads 62, there 4.3 TB/s of entries out of L2). 53 thousand warp
 //   instructions a row: 7.6 a tile, 23 for queries, first references and the end; issue slots 65 %;
 //   64 rows x 8 x 8 heads of 128 over 2048 entries: 56.5 us, 6 TB/s less a start of some 12 us
 //   (launch, list, page, entries, one behind the other); 4 rows over 512 entries 11.6 us.
@@ -89,10 +89,11 @@ struct Shape {
   static constexpr int per_sm = G <= 16 ? 2 : 1;
   // Registers a thread: at the launch, and of the groups of four warps of each kind. Gathering
   // wants 64 where entries are few heads' (64 x 8 x 8 heads 57 us, 59.6 with 56 and 96 for softmax);
-  // with 64 heads softmax wants them (150 us, 156 with 80, 56 and 56).
+  // with 64 heads softmax wants them (150 us, 156 with 80, 56 and 56), then gathering (137 us without
+  // a moved reference, 142 with 48).
   static constexpr int regs = G <= 16 ? 64 : G == 32 ? 80 : 72;
-  static constexpr int softmax_regs = G <= 16 ? 80 : 88;
-  static constexpr int gather_regs = G <= 32 ? 64 : 48, query_regs = G == 32 ? 56 : 48;
+  static constexpr int softmax_regs = G <= 16 ? 80 : G == 32 ? 120 : 88;
+  static constexpr int gather_regs = G <= 32 ? 64 : 56, query_regs = G == 32 ? 56 : 48;
   static_assert(softmax % 4 == 0 && gather % 4 == 0 && (queries + 1) % 4 == 0);
   static_assert(softmax * softmax_regs + gather * gather_regs + (queries + 1) * query_regs <= (threads / 32) * regs);
 };
