@@ -70,7 +70,7 @@ constexpr int kEntries = 128;  // of a tile
 constexpr int kMaxStages = 6;
 constexpr int kBufs = 2;  // buffers of scores in TMEM, of weights and queries in shared memory
 constexpr int kMaxNotes = kMaxStages + kBufs;  // see E4Params::notes
-constexpr float kNothing = -1073741824.0f;  // a reference below any logit in use; its negative for heads that are none
+constexpr float kNoHead = 1073741824.0f;  // the reference of heads that are none: no weight
 constexpr float kLogLimit = 8.8073549f;     // log2(448)
 constexpr float kFar = 16.0f;  // a reference that moves further has left logits with less than 2^-20 of their digits
 constexpr float kLeast = 0x1p-60f;          // values' scales below count as this for the reference
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
       uint64_t sum[HS / 2];  // of the weights of two heads
 #pragma unroll
       for (int h = 0; h < HS / 2; ++h) sum[h] = 0;
-      if (e < HS) nref[e] = e < heads ? 0.0f : kNothing;
+      if (e < HS) nref[e] = e < heads ? 0.0f : -kNoHead;
       bool ok = true, fresh = true;  // a head of the set has seen nothing yet
       if (tiles > 0) ok = wait_or_stop(&sh.units[nw & 3], (nw >> 2) & 1, stop);
       set_sync(set);
@@ -695,11 +695,12 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           }
           if (!fresh && !set_any(set, seen && high + log_vs > kLogLimit)) break;
           // Move the references, by whole numbers.
+          const float low = __int_as_float(0xff800000);
           float w[HS];  // a NaN is no maximum
 #pragma unroll
           for (int h = 0; h < HS; ++h) {
             const float2 y = both(z[h / 2]);
-            w[h] = seen ? fmaxf((h & 1 ? y.y : y.x) + log_vs, -FLT_MAX) : -FLT_MAX;
+            w[h] = seen ? fmaxf((h & 1 ? y.y : y.x) + log_vs, low) : low;
           }
           const float top = max_lanes<HS>(w, lane);
           if (lane % (32 / HS) == 0) sh.most[warp][lane / (32 / HS)] = top;
@@ -710,7 +711,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
             const float top = fmaxf(fmaxf(m[0][e], m[1][e]), fmaxf(m[2][e], m[3][e])), by = ceilf(top) - (begins(nref[e]) ? 4.0f : 5.0f);
             // From nothing to where the first logits are; then up where a weight is too large:
             // what a head's references are depends on its own logits alone.
-            const bool first = begins(nref[e]), moves = e < heads && (first ? by > -1e30f : top > kLogLimit);
+            const bool first = begins(nref[e]), moves = e < heads && (first ? by > low : top > kLogLimit);
             sh.step[set * HS + e] = moves ? -by : 0.0f;
             const float factor = moves && !first ? exp2_fast(-by) : 1.0f;
             sh.factor[set * HS + e] = again ? factor : factor * sh.factor[set * HS + e];
@@ -812,7 +813,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
         const float(*m)[HS] = &sh.sum[set * 4];
         total = (m[0][e] + m[1][e]) + (m[2][e] + m[3][e]);
         if (cluster > 1)
-          sh.head_ref[set * HS + e] = begins(nref[e]) ? kNothing : -nref[e], sh.head_sum[set * HS + e] = total;
+          sh.head_ref[set * HS + e] = begins(nref[e]) ? __int_as_float(0xff800000) : -nref[e], sh.head_sum[set * HS + e] = total;
         else
           sh.inverse[set * HS + e] = e4_inverse(total);
       }
@@ -889,7 +890,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
     const int fours = a.Dv / 4, outputs = k.heads * fours;
     for (int i = static_cast<int>(rank) * S::threads + threadIdx.x; i < outputs; i += cluster * S::threads) {
       const int h = i / fours, c = (i - h * fours) * 4;
-      float m[8], l[8], all = kNothing, total = 0.0f;
+      float m[8], l[8], all = __int_as_float(0xff800000), total = 0.0f;
       float4 u[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r) {

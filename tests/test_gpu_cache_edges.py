@@ -1,0 +1,73 @@
+"""The operators of a paged cache in 8 bits on the GPU where their range, their order or their larger forms end,
+against the formulas in 64 bits (``cache_reference``) or what follows from them."""
+
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import cache_reference as C  # noqa: E402
+import step_reference as R  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU-only machines
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import sparse_attention_indexer_fp32_gb300 as tk  # noqa: E402
+
+DEV = torch.device("cuda:0")
+BF16, FP16, FP32, E4M3 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(shape, seed, dtype=FP32, scale=1.0):
+    return (torch.randn(shape, generator=_gen(seed), device=DEV) * scale).to(dtype)
+
+
+def _ints(values):
+    return torch.tensor(values, dtype=torch.int32, device=DEV)
+
+
+def _codes(shape, seed):
+    return (torch.randn(shape, generator=_gen(seed), device=DEV) * 110.0).clamp(-448.0, 448.0).to(E4M3)
+
+
+def _scales(shape, seed, low=-9, high=-5):
+    return torch.exp2(torch.randint(low, high, shape, generator=_gen(seed), device=DEV).float())
+
+
+# ---- attention: logits at the ends of FP32 ------------------------------------------------------------
+
+
+def _one_row(heads, K, dtype, ps=64, D=64):
+    """One query token at position 2 K over the positions 0 to K - 1 of a cache of its own."""
+    pages = -(-K // ps)
+    return dict(q=_randn((1, 1, heads, D), 1, dtype), k=_codes((pages, ps, 1, D), 2), v=_codes((pages, ps, 1, D), 3),
+                indices=torch.arange(K, dtype=torch.int32, device=DEV).view(1, 1, K), query_positions=_ints([[2 * K]]),
+                page_table=torch.arange(pages, dtype=torch.int32, device=DEV).view(1, pages),
+                k_scales=_scales((pages, 1, 1), 4), v_scales=_scales((pages, 1, 1), 5), scale=D ** -0.5)
+
+
+@pytest.mark.parametrize("heads,dtype", [(8, BF16), (16, FP16), (40, BF16)])
+@pytest.mark.parametrize("slope", [1e6, 1e30])
+@pytest.mark.parametrize("rows", [1, 200])
+def test_attention_logits_far_below(heads, dtype, slope, rows):
+    """The nearest entry's logit is -2e9 or -2e33, the next one's lower by 1e6 or 1e30: it has all the weight, whether
+    CTAs share the row or not."""
+    K = 2048
+    c = _one_row(heads, K, dtype)
+    c["slopes"] = torch.full((heads,), slope, device=DEV)
+    for n in ("q", "indices", "query_positions", "page_table"):
+        c[n] = c[n].expand(rows, *c[n].shape[1:]).contiguous()
+    out, lse = tk.sparse_attention(**c, return_lse=True)
+    want = R.np64(c["v"].float())[-1, -1, 0] * float(c["v_scales"][-1, 0, 0])
+    assert np.abs(R.np64(out) - want).max() <= R.half_step(dtype) * np.abs(want).max()
+    assert np.abs(R.np64(lse) / (-slope * (K + 1)) - 1).max() < 2.0 ** -20  # products and sums of FP32
