@@ -708,10 +708,12 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
           bool far = false;
           if (e < HS) {
             const float(*m)[HS] = &sh.most[set * 4];
-            const float top = fmaxf(fmaxf(m[0][e], m[1][e]), fmaxf(m[2][e], m[3][e])), by = ceilf(top) - (begins(nref[e]) ? 4.0f : 5.0f);
+            const float top = fmaxf(fmaxf(m[0][e], m[1][e]), fmaxf(m[2][e], m[3][e]));
+            // An infinite logit makes a reference of NaN, which all that follows takes on.
+            const float by = top > FLT_MAX ? __int_as_float(0x7fc00000) : ceilf(top) - (begins(nref[e]) ? 4.0f : 5.0f);
             // From nothing to where the first logits are; then up where a weight is too large:
             // what a head's references are depends on its own logits alone.
-            const bool first = begins(nref[e]), moves = e < heads && (first ? by > low : top > kLogLimit);
+            const bool first = begins(nref[e]), moves = e < heads && (first ? top > low : top > kLogLimit);
             sh.step[set * HS + e] = moves ? -by : 0.0f;
             const float factor = moves && !first ? exp2_fast(-by) : 1.0f;
             sh.factor[set * HS + e] = again ? factor : factor * sh.factor[set * HS + e];

@@ -71,3 +71,28 @@ def test_attention_logits_far_below(heads, dtype, slope, rows):
     want = R.np64(c["v"].float())[-1, -1, 0] * float(c["v_scales"][-1, 0, 0])
     assert np.abs(R.np64(out) - want).max() <= R.half_step(dtype) * np.abs(want).max()
     assert np.abs(R.np64(lse) / (-slope * (K + 1)) - 1).max() < 2.0 ** -20  # products and sums of FP32
+
+
+@pytest.mark.parametrize("heads,dtype", [(8, BF16), (16, FP16), (64, BF16)])
+@pytest.mark.parametrize("at", [5, 140, 290])
+def test_attention_infinite_logits(heads, dtype, at):
+    """One head's logit of one entry passes FP32's largest number, in the first tile or a later one: that head is NaN,
+    and the others are what they are without."""
+    K, D = 300, 64
+    c = _one_row(heads, K, dtype, ps=1)
+    c["q"][..., 0] = 0.0
+    c["k"].view(torch.uint8)[at] = 0
+    plain = tk.sparse_attention(**c, return_lse=True)
+    c["q"][0, 0, 3, 0] = 16.0
+    c["k"][at, 0, 0, 0] = 448.0
+    c["k_scales"][at] = 2.0 ** 120  # 2^120 * 448 * 16 / 8, past 2^128 in units of log 2
+    out, lse = tk.sparse_attention(**c, return_lse=True)
+    assert torch.isnan(out[0, 0, 3]).all() and torch.isnan(lse[0, 0, 3])
+    rest = [h for h in range(heads) if h != 3]
+    assert torch.equal(out[0, 0, rest], plain[0][0, 0, rest]) and torch.equal(lse[0, 0, rest], plain[1][0, 0, rest])
+    c["k"][at, 0, 0, 0] = -448.0  # a logit of -infinity has weight 0
+    out, lse = tk.sparse_attention(**c, return_lse=True)
+    hidden = c["indices"].clone()
+    hidden[0, 0, at] = -1
+    want = tk.sparse_attention(**{**c, "indices": hidden}, return_lse=True)
+    assert torch.equal(out[0, 0, 3], want[0][0, 0, 3]) and torch.equal(lse[0, 0, 3], want[1][0, 0, 3])
