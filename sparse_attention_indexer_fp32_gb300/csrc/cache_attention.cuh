@@ -19,9 +19,9 @@
 //
 // The scales. A key's scale multiplies its logit. A value's multiplies its weight
 // before that is split: w = 2^(z - r) s. The reference r of a head is moved, for
-// all threads at once, when a weight would pass E4M3's 448: first to leave the largest
-// in (2^3, 2^4], so that it seldom moves again, then in (2^4, 2^5]. The last term ends at
-// steps of 2^-13 (three terms: 2^-17), 2^-16 (2^-20) of the largest weight there is. The
+// all threads at once, when a weight would pass E4M3's 448, to leave the largest in
+// (2^6, 2^7]. The last term ends at steps of 2^-13 (three terms: 2^-17), 2^-19 (2^-23) of
+// the largest weight there is. The
 // sum that divides adds the weights in FP32, unrounded and without the values' scales. r
 // is a whole number, so moving it is exact but for logits that were rounded next to the
 // old one: past kFar those are computed anew. A head's references follow from its own
@@ -72,6 +72,11 @@ constexpr int kBufs = 2;  // buffers of scores in TMEM, of weights and queries i
 constexpr int kMaxNotes = kMaxStages + kBufs;  // see E4Params::notes
 constexpr float kNoHead = 1073741824.0f;  // the reference of heads that are none: no weight
 constexpr float kLogLimit = 8.8073549f;     // log2(448)
+// A reference leaves the largest weight in (2^(kTop - 1), 2^kTop] when it is set, so that it seldom
+// moves again and the last term's steps are 2^-19 (2^-23) of that weight at most: half a step of each
+// of 2048 entries is a quarter of a step of bf16 (an eighth of fp16's) together. 64 heads on 512 shared entries 167 us;
+// 146 by (2^3, 2^4], steps of 2^-16, with which the rest beside one large weight loses its digits.
+constexpr float kTop = 7.0f;
 constexpr float kFar = 16.0f;  // a reference that moves further has left logits with less than 2^-20 of their digits
 constexpr float kLeast = 0x1p-60f;          // values' scales below count as this for the reference
 
@@ -710,7 +715,7 @@ __global__ void __launch_bounds__(Shape<E, G>::threads, Shape<E, G>::per_sm)
             const float(*m)[HS] = &sh.most[set * 4];
             const float top = fmaxf(fmaxf(m[0][e], m[1][e]), fmaxf(m[2][e], m[3][e]));
             // An infinite logit makes a reference of NaN, which all that follows takes on.
-            const float by = top > FLT_MAX ? __int_as_float(0x7fc00000) : ceilf(top) - (begins(nref[e]) ? 4.0f : 5.0f);
+            const float by = top > FLT_MAX ? __int_as_float(0x7fc00000) : ceilf(top) - kTop;
             // From nothing to where the first logits are; then up where a weight is too large:
             // what a head's references are depends on its own logits alone.
             const bool first = begins(nref[e]), moves = e < heads && (first ? top > low : top > kLogLimit);

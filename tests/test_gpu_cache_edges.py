@@ -96,3 +96,46 @@ def test_attention_infinite_logits(heads, dtype, at):
     hidden[0, 0, at] = -1
     want = tk.sparse_attention(**{**c, "indices": hidden}, return_lse=True)
     assert torch.equal(out[0, 0, 3], want[0][0, 0, 3]) and torch.equal(lse[0, 0, 3], want[1][0, 0, 3])
+
+
+# ---- attention: what small weights keep --------------------------------------------------------------
+
+
+def _sink(heads, dtype, rows, n, fall, at, D=64, Dv=64):
+    """One entry with a value of 0 at place `at`, n others with a value of 1 whose weights are 2^-fall of its."""
+    q = torch.zeros((rows, 1, heads, D), dtype=dtype, device=DEV)
+    q[..., 0] = 1.0
+    k = torch.zeros((n + 1, 1, 1, D), device=DEV)
+    k[..., 0] = 256.0
+    v = torch.ones((n + 1, 1, 1, Dv), device=DEV)
+    v[at] = 0.0
+    units = torch.full((n + 1, 1, 1), 2.0 ** -8, device=DEV)
+    units[at] = (1.0 + fall * math.log(2.0)) * 2.0 ** -8
+    c = dict(q=q, k=k.to(E4M3), v=v.to(E4M3), k_scales=units, v_scales=torch.ones_like(units), scale=1.0,
+             indices=torch.arange(n + 1, dtype=torch.int32, device=DEV).expand(rows, 1, -1).contiguous())
+    z = 256.0 * R.np64(units).ravel()
+    p = np.exp(z - z.max())
+    p /= p.sum()
+    return c, 1.0 - p[at], p[at]
+
+
+def _sink_bound(dtype, tail, top, n, fall, D=64):
+    """What the header says of a weight: rounded to 9 bits or fp16, in steps of 2^-19 or 2^-23 of the largest one;
+    logits and sums in FP32, the result rounded to its type."""
+    rounded = 2.0 ** -11 if dtype == FP16 else 2.0 ** -9 + 2.0 ** -11
+    step = 2.0 ** -23 if dtype == FP16 else 2.0 ** -19
+    logits = (D + 16) * R.U * (2.0 + fall) + (n + 9) * R.U
+    return tail * (rounded + 2.0 * logits + 1.01 * R.half_step(dtype)) + n * top * step / 2
+
+
+@pytest.mark.parametrize("heads,dtype", [(8, BF16), (16, BF16), (64, BF16), (8, FP16), (32, FP16)])
+@pytest.mark.parametrize("rows", [1, 320])
+@pytest.mark.parametrize("at", [0, 1000, 2047])
+def test_attention_one_entry_far_above_a_flat_rest(heads, dtype, rows, at):
+    """An attention sink: one entry of no value has most of the weight, and the others' small weights are the result."""
+    n = 2047
+    for fall in (9.3, 12.2, 13.6, 14.5, 15.2, 16.4, 17.2, 17.6, 19.5, 21.6):
+        c, tail, top = _sink(heads, dtype, rows, n, fall, at)
+        out, lse = tk.sparse_attention(**c, return_lse=True)
+        bound = _sink_bound(dtype, tail, top, n, fall)
+        assert np.abs(R.np64(out) - tail).max() <= bound, f"{fall}: {np.abs(R.np64(out) - tail).max()} for {bound} of {tail}"
