@@ -91,7 +91,8 @@ topk_status sparse_append(const sparse_append_args* args, topk_stream_t stream);
  * (elements below 2^-13 of their head's largest one keep steps of 2^-20, or 2^-24, of
  * that); sums and statistics are FP32. A weight, times its value's scale, is rounded to
  * 9 bits (SPARSE_BF16) or to fp16's 11 (SPARSE_FP16) for the second product, once;
- * weights below 2^-10 of a head's largest keep steps of 2^-19, or 2^-23, of it.
+ * weights below 2^-10 of a head's largest keep steps of 2^-19, or 2^-23, of it, where a
+ * list has more than 2048 entries those of each of up to eight parts of it by themselves.
  */
 typedef struct sparse_attention_e4m3_args {
   sparse_attention_args attention; /* k, v: SPARSE_E4M3, 16-byte aligned, strides multiples of 16; D, Dv <= 256, multiples of 16 */

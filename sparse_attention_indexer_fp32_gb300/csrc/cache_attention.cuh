@@ -77,6 +77,7 @@ constexpr float kLogLimit = 8.8073549f;     // log2(448)
 // of 2048 entries is a quarter of a step of bf16 (an eighth of fp16's) together. 64 heads on 512 shared entries 167 us;
 // 146 by (2^3, 2^4], steps of 2^-16, with which the rest beside one large weight loses its digits.
 constexpr float kTop = 7.0f;
+constexpr int kLongest = 2048;  // entries of one reference; CTAs share longer lists, up to eight
 constexpr float kFar = 16.0f;  // a reference that moves further has left logits with less than 2^-20 of their digits
 constexpr float kLeast = 0x1p-60f;          // values' scales below count as this for the reference
 
@@ -992,13 +993,18 @@ topk_status launch_heads(const sparse_attention_e4m3_args& args, int dev, int sm
   const int64_t work = static_cast<int64_t>(a.B) * a.T * a.Hkv * p.h_tiles;
   if (work > INT32_MAX) return TOPK_EINVAL;
   p.works = static_cast<uint32_t>(work);
-  // Few rows: share each over the CTAs that would idle, down to two tiles each.
+  // Few rows: share each over the CTAs that would idle, down to two tiles each. Long lists: share
+  // each, so that a CTA, which has references of its own, has kLongest entries: what its last steps
+  // lose is relative to its own largest weight, so all together lose what one list of 2048 does. A
+  // CTA then ends with its row: 512 rows of 64 heads over 4096 entries 309 us (243 unshared), 64 x 8
+  // heads' lists of 4096 118 (100).
   const int64_t slots = static_cast<int64_t>(sm_count) * (two ? 2 : 1);
   const int tiles = a.K / kEntries + (a.K % kEntries != 0);
   int cluster = 1;
-  while (cluster < 8 && work * cluster * 2 <= slots && cluster * 4 <= tiles) cluster *= 2;
+  while (cluster < 8 && ((work * cluster * 2 <= slots && cluster * 4 <= tiles) || tiles > cluster * (kLongest / kEntries)))
+    cluster *= 2;
   const int64_t grid = cluster == 1 && work > slots ? slots : work * cluster;
-  if ((work / grid + 1) * tiles > INT32_MAX) return TOPK_EINVAL;  // a CTA counts its tiles
+  if (grid > INT32_MAX || (work / grid + 1) * tiles > INT32_MAX) return TOPK_EINVAL;  // a CTA counts its tiles
   constexpr auto kernel = cache_attention_kernel<E, G>;
   // What the groups of warps trade is what the launch brings.
   static const int regs = [] {

@@ -139,3 +139,15 @@ def test_attention_one_entry_far_above_a_flat_rest(heads, dtype, rows, at):
         out, lse = tk.sparse_attention(**c, return_lse=True)
         bound = _sink_bound(dtype, tail, top, n, fall)
         assert np.abs(R.np64(out) - tail).max() <= bound, f"{fall}: {np.abs(R.np64(out) - tail).max()} for {bound} of {tail}"
+
+
+@pytest.mark.parametrize("heads,dtype", [(8, BF16), (64, BF16), (12, FP16), (32, FP16)])
+@pytest.mark.parametrize("rows,n", [(1, 4095), (320, 4095), (320, 8190), (40, 16383), (200, 16383)])
+def test_attention_long_lists(heads, dtype, rows, n):
+    """The same beside lists past 2048 entries: what is lost beside the one entry is lost of 2048 entries at most."""
+    for fall in (14.5, 17.6, 19.5, 20.7, 23.4):
+        c, tail, top = _sink(heads, dtype, rows, n, fall, n // 3)
+        out, lse = tk.sparse_attention(**c, return_lse=True)
+        bound = _sink_bound(dtype, tail, top, n, fall) - (n - 2047) * top * (2.0 ** -23 if dtype == FP16 else 2.0 ** -19) / 2
+        bound += 2 * tail * (n + 9) * R.U  # more sums in FP32, and the join
+        assert np.abs(R.np64(out) - tail).max() <= bound, f"{fall}: {np.abs(R.np64(out) - tail).max()} for {bound} of {tail}"
