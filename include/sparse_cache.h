@@ -38,8 +38,8 @@ extern "C" {
  *
  * A cache of the inputs' type takes the results rounded to it. A cache in
  * SPARSE_E4M3 takes them in units of their block's scale s:
- *   - Tokens of one block follow one another in the call, with no other token
- *     between; `first` is the least of their places in the block.
+ *   - `first` is the least place in a block of the call's tokens, which may come in
+ *     any order (fastest with those of a block one behind the other).
  *   - size = scale (|u| + |v|) for the pairs (u, v) that turn, |x| for the rest and
  *     for values, bounds the stored numbers at any position. need = the smallest
  *     power of two, 2^-126 at least, with size <= 448 need for all of the block's

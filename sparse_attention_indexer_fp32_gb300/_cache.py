@@ -66,12 +66,12 @@ def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], positions: Optional
     ``k_cache`` ``[pages, page_size, H, D]`` and ``v_cache`` ``[pages, page_size, H, Dv]``.
 
     Caches in float8_e4m3fn hold entries in units of ``k_scales`` and ``v_scales``, float32 ``[pages, blocks,
-    H]``: the ``page_size // blocks`` entries of a block share one for each head. Tokens of one block follow
-    one another in the call. A block that a call begins at its first place gets the smallest power of two that
-    holds the call's tokens; one that is continued keeps its scale while that holds them, otherwise the scale
-    grows and the entries before are rounded again (places behind the call's first one count as empty, and so
-    does a block whose scale is 0). ``[pages, page_size, 1]`` for one head is what :func:`indexer_scores` takes as
-    ``key_scales``; :func:`sparse_attention` reads any."""
+    H]``: the ``page_size // blocks`` entries of a block share one for each head. Tokens may come in any order,
+    each at a slot of its own (fastest with those of a block one behind the other). A block that a call begins
+    at its first place gets the smallest power of two that holds the call's tokens; one that is continued keeps
+    its scale while that holds them, otherwise the scale grows and the entries before are rounded again (places
+    behind the call's first one count as empty, and so does a block whose scale is 0). ``[pages, page_size, 1]``
+    for one head is what :func:`indexer_scores` takes as ``key_scales``; :func:`sparse_attention` reads any."""
     shape, xs, code, index = _main(k, "k", 3, _ROTARY_TYPES)
     T, H, D = shape
     dtype = k.dtype

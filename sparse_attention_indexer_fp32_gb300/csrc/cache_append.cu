@@ -9,7 +9,7 @@
 //
 // The work. Each element is read once and written once, in half or a quarter of its
 // size; the arithmetic on it takes longer than that, so what tokens and heads share is
-// done once. The tokens of a block follow one another, so a CTA takes the runs of
+// done once. The tokens of a block mostly follow one another, so a CTA takes the runs of
 // tokens that begin in its share of the call, whole, for two heads of one side (keys or
 // values): it finds the runs from the slots alone, the largest size of each run and head
 // by an integer maximum in shared memory (sizes are not negative), then turns and
@@ -18,11 +18,18 @@
 // with heads of 128 does), read again from L1 otherwise; a token's sine and cosine serve
 // both heads. No atomics to memory, no workspace; every block's scale has one writer.
 //
-// Measured, in a CUDA graph: 8192 tokens x 8 heads x (128 + 128), bf16, into 8 bits 29 us for
+// Any order. A block may have several runs, only where none fills it: a CTA with a run that does not
+// looks through the call's other slots (a bit per hash of its blocks, eight slots a thread at once)
+// and adds up the sizes of the tokens it finds, so that each run's CTA comes to the same scale; that
+// of the first one writes it and what the block held before. This costs an ordered call 1.3 us with 64
+// tokens, 4.5 with 8192 of four prompts (34.4; 29.8 without, wrong in other orders), 10 with 8192
+// single tokens (44), where every CTA looks; and the call's tokens squared where they lie shuffled.
+//
+// Measured, in a CUDA graph: 8192 tokens x 8 heads x (128 + 128), bf16, into 8 bits 34 us for
 // 7.4 at the copy rate. It is bound by instructions and by what they wait for: 24 an element,
 // issue slots 45 % busy, DRAM 16 %; a CTA's three barriers (slots, sizes, scales) leave its
 // warps idle where the CTA beside it has nothing to issue. 4096 tokens x 8 x (128 + 128), fp16,
-// as they are 10.4 us (4.8); 64 tokens 7.3 us, a launch and reads of slot, scale and token one
+// as they are 10.4 us (4.8); 64 tokens 8.4 us, a launch and reads of slot, scale and token one
 // behind the other; 8192 index keys of 128 with a scale each 8.3 us.
 #include <cuda_runtime.h>
 
@@ -41,6 +48,7 @@ namespace {
 
 constexpr int kRuns = 64;      // tokens whose runs a CTA takes at most, so runs of a CTA
 constexpr int kMostHeads = 4;  // of a CTA
+constexpr int kMarks = 32768;  // for the blocks of a CTA's runs
 
 struct AppendSide {
   const void* x;
@@ -73,6 +81,9 @@ struct AppendShared {
   int32_t first[kRuns], block[kRuns];       // of a run: the least place in its block, and that of the cache
   uint32_t size[kRuns * kMostHeads];        // of a run and head: the largest size / 2, as its bits; then 1 / scale
   float ratio[kRuns * kMostHeads];          // what its earlier entries are multiplied by
+  uint4 marks[kMarks / 128];                // bit per hash of a block: a run may have it
+  uint8_t same[kRuns], later[kRuns];        // the share's first run of the same block; whether a token of an earlier share has it
+  bool parts, twice;                        // a run has not all of its block: others may have tokens of it; runs of this share may
   unsigned long long leads;                 // bit per token of the share: it begins a run
   int64_t end;                              // of the last run
 };
@@ -100,6 +111,154 @@ struct FormOf {
   static constexpr int threads = THREADS, rows = ROWS, heads = HEADS, per_sm = PER_SM, share = SHARE;
 };
 
+// A thread's and a CTA's indices, read anew where they are wanted, so that nothing the compiler makes
+// of them in find_runs takes registers from what follows.
+__device__ __forceinline__ int thread_index() {
+  int v;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t block_index() {
+  uint32_t v;
+  asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(v));
+  return v;
+}
+
+// What a CTA takes: the first of its heads, their number, and the tokens whose runs it has.
+struct Share {
+  int h0, heads;
+  int64_t t0, t1;
+};
+template <typename Form>
+__device__ __forceinline__ Share share_of(const AppendParams& p) {
+  const uint32_t at = block_index(), share = at / static_cast<uint32_t>(p.head_groups);
+  Share c;
+  c.h0 = static_cast<int>(at - share * p.head_groups) * Form::heads, c.heads = min(p.H - c.h0, Form::heads);
+  c.t0 = static_cast<int64_t>(share) * p.share, c.t1 = min(c.t0 + p.share, static_cast<int64_t>(p.T));
+  return c;
+}
+
+__device__ __forceinline__ int32_t slot_of(const AppendParams& p, int64_t t) {  // -1: not written
+  const int32_t slot = p.slots[t];
+  return slot >= 0 && slot < p.num_slots ? slot : -1;
+}
+__device__ __forceinline__ int32_t block_of(const AppendParams& p, int32_t slot) {
+  return slot < 0 ? -1 : p.block_shift >= 0 ? slot >> p.block_shift : slot / p.block;
+}
+
+// The CTA's runs, into `sh`. Where a run does not fill its block, other runs may have tokens of that:
+// each share that has some finds the same scale, from all of them, and the first one writes it and what
+// the block held before. For that the other slots of the call are looked through.
+template <typename E, bool HALF, typename Form>
+__device__ __forceinline__ void find_runs(const AppendParams& p, const AppendSide& s, AppendShared& sh) {
+  constexpr int kThreads = Form::threads, kHeads = Form::heads;
+  const int tid = thread_index(), lane = tid & 31;
+  const Share c = share_of<Form>(p);
+  const int64_t t0 = c.t0, t1 = c.t1;
+  for (int i = tid; i < Form::share * kHeads; i += kThreads) sh.size[i] = 0;
+  if (tid < Form::share) sh.first[tid] = INT32_MAX, sh.same[tid] = static_cast<uint8_t>(tid), sh.later[tid] = 0;
+  for (int i = tid; i < kMarks / 128; i += kThreads) sh.marks[i] = make_uint4(0, 0, 0, 0);
+  if (tid < 32) {
+    unsigned long long leads = 0;
+    int64_t end = t1, kept = 0;  // tokens of the runs
+    int32_t last = t0 > 0 ? block_of(p, slot_of(p, t0 - 1)) : -1;
+#pragma unroll
+    for (int part = 0; part < Form::share; part += 32) {
+      if (t0 + part >= t1) continue;
+      const int64_t t = t0 + part + lane;
+      const int32_t block = t < t1 ? block_of(p, slot_of(p, t)) : -1;
+      const int32_t up = __shfl_up_sync(0xffffffffu, block, 1);
+      const bool lead = block >= 0 && (lane == 0 ? last : up) != block;
+      const uint32_t bits = __ballot_sync(0xffffffffu, lead), all = __ballot_sync(0xffffffffu, block >= 0);
+      if (lead) sh.block[__popcll(leads) + __popc(bits & ((1u << lane) - 1))] = block;
+      kept += __popc(leads != 0 ? all : bits != 0 ? all & ~((bits & (0u - bits)) - 1) : 0);
+      leads |= static_cast<unsigned long long>(bits) << part;
+      last = __shfl_sync(0xffffffffu, block, static_cast<int>(min(t1 - t0 - part, int64_t{32})) - 1);
+    }
+    while (leads != 0 && last >= 0) {  // the last run may go on behind the share
+      const bool on = end + lane < p.T && block_of(p, slot_of(p, end + lane)) == last;
+      const uint32_t off = ~__ballot_sync(0xffffffffu, on);
+      end += off != 0 ? __ffs(off) - 1 : 32;
+      if (off != 0) break;
+    }
+    // no run has more tokens than its block has places
+    const bool parts = kept + (end - t1) != static_cast<int64_t>(__popcll(leads)) * p.block;
+    if (lane == 0) sh.leads = leads, sh.end = end, sh.parts = parts, sh.twice = false;
+  }
+  __syncthreads();
+  if (!sh.parts) return;
+
+  const int runs = __popcll(sh.leads), pairs = s.rotated / 2;
+  uint32_t* marks = reinterpret_cast<uint32_t*>(sh.marks);
+  auto hash_of = [](uint32_t block) { return block * 0x9e3779b1u; };  // bits 17 to 31 are a mark's
+  if (tid < runs) {
+    const uint32_t h = hash_of(sh.block[tid]), bit = 1u << (h >> 17 & 31);
+    if (atomicOr(&marks[h >> 22], bit) & bit) sh.twice = true;
+  }
+  __syncthreads();
+  if (sh.twice && tid < runs)
+    for (int r = tid - 1; r >= 0; --r)
+      if (sh.block[r] == sh.block[tid]) sh.same[tid] = static_cast<uint8_t>(r);
+  // whether a slot's block may be a run's; of a slot that is none, anything
+  auto marked = [&](uint32_t slot) -> uint32_t {
+    const uint32_t h = hash_of(p.block_shift >= 0 ? slot >> p.block_shift : slot / p.block);
+    return __funnelshift_r(marks[h >> 22], 0, h >> 17) & 1;
+  };
+  const int64_t begin = t0 + __ffsll(static_cast<long long>(sh.leads)) - 1;
+  // Tokens that may be of a run's block, one a lane at most: a warp adds up one at a time, they are rare.
+  auto add = [&](int64_t t, bool may) {
+    const int32_t slot = may ? slot_of(p, t) : -1, block = block_of(p, slot);
+    int run = -1;
+    if (block >= 0)
+      for (int r = runs - 1; r >= 0; --r) run = sh.block[r] == block ? r : run;
+    if (run >= 0) {
+      atomicMin(&sh.first[run], slot - block * p.block);
+      if (t < begin) sh.later[run] = 1;
+    }
+    for (uint32_t which = __ballot_sync(0xffffffffu, run >= 0); which != 0; which &= which - 1) {
+      const int src = __ffs(which) - 1, r = __shfl_sync(0xffffffffu, run, src);
+      const E* token = static_cast<const E*>(s.x) + c.h0 * s.x_head + (t - lane + src) * s.x_token;
+      for (int u = 0; u < c.heads; ++u) {
+        const E* of = token + u * s.x_head;
+        float high = 0.0f;
+        auto half = [&](int at) { return 0.5f * fabsf(Elem<E>::get(of[at])); };
+        auto count = [&](float size) {
+          if (size <= FLT_MAX) high = fmaxf(high, size);
+        };
+        for (int j = lane; j < pairs; j += 32) {
+          const int at = s.offset + (HALF ? j : 2 * j);
+          count((half(at) + half(at + (HALF ? pairs : 1))) * fabsf(p.scale));
+        }
+        for (int j = lane; j < s.D - s.rotated; j += 32) count(half(s.rotated > 0 && j >= s.offset ? j + s.rotated : j));
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(high));
+        if (lane == 0) atomicMax(&sh.size[r * kHeads + u], most);
+      }
+    }
+  };
+  // What lies before the CTA's tokens, and what behind: kAhead slots a thread at once.
+  constexpr int kAhead = 8;
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const int64_t to = side == 0 ? begin : p.T;
+#pragma unroll 1
+    for (int64_t t = (side == 0 ? 0 : sh.end) + tid; t - lane < to; t += kThreads * kAhead) {
+      const int32_t* slots = p.slots + t;
+      const int left = static_cast<int>(min(to - t, int64_t{kThreads * kAhead}));  // 0 and below: none of this lane's
+      uint32_t slot[kAhead], hits = 0;
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) slot[a] = a * kThreads < left ? slots[a * kThreads] : 0xffffffffu;
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) hits |= marked(slot[a]) << a;
+#pragma unroll 1
+      for (uint32_t any = __reduce_or_sync(0xffffffffu, hits); any != 0; any &= any - 1) {
+        const int a = __ffs(any) - 1;
+        add(t + a * kThreads, (hits >> a & 1) != 0 && a * kThreads < left);
+      }
+    }
+  }
+  __syncthreads();
+}
+
 // One side of a CTA. An item that turns holds two units of V elements: of the first
 // half and of the second (HALF), or one behind the other; so does one that does not.
 // Without `vector` (V = 2) it holds one pair, or one element.
@@ -109,22 +268,14 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
   constexpr bool kVector = sizeof(E) * V == 16;
   constexpr int kPairs = kVector ? V : 1;  // of an item
   using VecT = Vec<E, V>;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t share = blockIdx.x / static_cast<unsigned>(p.head_groups);
-  const int h0 = static_cast<int>(blockIdx.x - share * p.head_groups) * kHeads, heads = min(p.H - h0, kHeads);
-  const int64_t t0 = share * p.share, t1 = min(t0 + p.share, static_cast<int64_t>(p.T));
+  const int tid = thread_index(), lane = tid & 31;
+  const Share c = share_of<Form>(p);
+  const int h0 = c.h0, heads = c.heads;
+  const int64_t t0 = c.t0, t1 = c.t1;
   const int per = min(s.items, kThreads);
   const int sub = tid / per, i0 = tid - sub * per, side_by_side = kThreads / per;
   const int sweep = kRows * side_by_side;  // tokens at once
   const int pairs = s.rotated / 2, units = s.rotated / V, rest = (s.D - s.rotated) / V;
-  auto slot_of = [&](int64_t t) -> int32_t {  // -1: not written
-    const int32_t slot = p.slots[t];
-    return slot >= 0 && slot < p.num_slots ? slot : -1;
-  };
-  auto block_of = [&](int32_t slot) -> int32_t {
-    return slot < 0 ? -1 : p.block_shift >= 0 ? slot >> p.block_shift : slot / p.block;
-  };
-
   int64_t begin = t0, end = t1;  // of the CTA's tokens
 
   // ---- an item of a token ----
@@ -158,7 +309,7 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       const int64_t at = t + u * side_by_side;
-      slots[u] = sub < side_by_side && at < end ? slot_of(at) : -1;
+      slots[u] = sub < side_by_side && at < end ? slot_of(p, at) : -1;
     }
   };
   auto load = [&](int64_t t, const Item& m) {
@@ -202,44 +353,16 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
   };
 
   // ---- the runs ----
-  for (int i = tid; i < pairs; i += kThreads) sh.rates[i] = turns_of(p.frequencies[i]);
   unsigned long long leads = 0;  // bit per token of the share: it begins a run
   int runs = 0;
   if constexpr (SCALED) {
-    for (int i = tid; i < kRuns * kHeads; i += kThreads) sh.size[i] = 0;
-    if (tid < kRuns) sh.first[tid] = INT32_MAX;
-    if (tid < 32) {
-      int32_t last = t0 > 0 ? block_of(slot_of(t0 - 1)) : -1;
-#pragma unroll
-      for (int part = 0; part < kRuns; part += 32) {
-        if (t0 + part >= t1) continue;
-        const int64_t t = t0 + part + lane;
-        const int32_t block = t < t1 ? block_of(slot_of(t)) : -1;
-        const int32_t up = __shfl_up_sync(0xffffffffu, block, 1);
-        const bool lead = block >= 0 && (lane == 0 ? last : up) != block;
-        const uint32_t bits = __ballot_sync(0xffffffffu, lead);
-        if (lead) sh.block[__popcll(leads) + __popc(bits & ((1u << lane) - 1))] = block;
-        leads |= static_cast<unsigned long long>(bits) << part;
-        last = __shfl_sync(0xffffffffu, block, static_cast<int>(min(t1 - t0 - part, int64_t{32})) - 1);
-      }
-      while (leads != 0 && last >= 0) {  // the last run may go on behind the share
-        const bool on = end + lane < p.T && block_of(slot_of(end + lane)) == last;
-        const uint32_t off = ~__ballot_sync(0xffffffffu, on);
-        end += off != 0 ? __ffs(off) - 1 : 32;
-        if (off != 0) break;
-      }
-      if (lane == 0) sh.leads = leads, sh.end = end;
-    }
-    __syncthreads();
     leads = sh.leads, end = sh.end;
     if (leads == 0) return;
     runs = __popcll(leads);
     begin = t0 + __ffsll(static_cast<long long>(leads)) - 1;
-  } else {
-    __syncthreads();
   }
-  // The run of a token between begin and end that is written.
-  auto run_of = [&](int64_t t) { return t < t1 ? __popcll(leads & ((2ull << (t - t0)) - 1)) - 1 : runs - 1; };
+  // The run of a token between begin and end that is written, the first one of its block.
+  auto run_of = [&](int64_t t) -> int { return sh.same[t < t1 ? __popcll(leads & ((2ull << (t - t0)) - 1)) - 1 : runs - 1]; };
   const bool once = end - begin <= sweep && s.items <= kThreads;  // what is loaded stays
 
   bool odd = false;  // something that this thread holds may not be finite, or not its results
@@ -311,7 +434,7 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
     slots_of(begin + sub);
     const Item mine = item_of(i0);
     if (once) load(begin + sub, mine);
-    const bool has = tid < runs * kHeads && tid % kHeads < heads;  // a run and head
+    const bool has = tid < runs * kHeads && tid % kHeads < heads && sh.same[tid / kHeads] == tid / kHeads;  // a run and head
     float* scale = s.scales + (has ? static_cast<int64_t>(sh.block[tid / kHeads]) * p.H + h0 + tid % kHeads : 0);
     const float before = has ? *scale : 0.0f;
     for (int64_t from = begin; from < end; from += sweep) {
@@ -329,7 +452,7 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         const int run = slots[r] >= 0 ? run_of(from + sub + r * side_by_side) : -1;
-        if (run >= 0 && i0 == 0) atomicMin(&sh.first[run], slots[r] - block_of(slots[r]) * p.block);
+        if (run >= 0 && i0 == 0) atomicMin(&sh.first[run], slots[r] - block_of(p, slots[r]) * p.block);
         // one number a warp where it is all of one run (or idle), one a thread otherwise
         const int any = __reduce_max_sync(0xffffffffu, run);
         if (any < 0) continue;
@@ -350,11 +473,13 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
     // ---- the scales ----
     if (has) {
       const float need = scale_for(__uint_as_float(sh.size[tid]));
-      const bool begins = sh.first[tid / kHeads] == 0;
-      const float now = begins ? need : fmaxf(before, need);
-      if (begins || now != before) *scale = now;
+      const bool begins = sh.first[tid / kHeads] == 0, first = sh.later[tid / kHeads] == 0;
+      const float now = begins ? need : fmaxf(before, need);  // whether or not another share has written it already
+      if (first && (begins || now != before)) *scale = now;
       sh.size[tid] = __float_as_uint(1.0f / now);
-      sh.ratio[tid] = begins ? 1.0f : before / now;
+      sh.ratio[tid] = begins || !first ? 1.0f : before / now;
+    } else if (tid < runs * kHeads) {
+      sh.ratio[tid] = 1.0f;
     }
     __syncthreads();
   }
@@ -514,6 +639,11 @@ template <typename E, bool HALF, bool SCALED, typename Form>
 __global__ void __launch_bounds__(Form::threads, Form::per_sm) append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ AppendShared sh;
   const AppendSide& s = p.side[blockIdx.y];
+  for (int i = threadIdx.x; i < s.rotated / 2; i += Form::threads) sh.rates[i] = turns_of(p.frequencies[i]);
+  if constexpr (SCALED)
+    find_runs<E, HALF, Form>(p, s, sh);
+  else
+    __syncthreads();
   if (s.vector)
     append_side<E, 16 / sizeof(E), HALF, SCALED, Form>(p, s, sh);
   else

@@ -151,3 +151,95 @@ def test_attention_long_lists(heads, dtype, rows, n):
         bound = _sink_bound(dtype, tail, top, n, fall) - (n - 2047) * top * (2.0 ** -23 if dtype == FP16 else 2.0 ** -19) / 2
         bound += 2 * tail * (n + 9) * R.U  # more sums in FP32, and the join
         assert np.abs(R.np64(out) - tail).max() <= bound, f"{fall}: {np.abs(R.np64(out) - tail).max()} for {bound} of {tail}"
+
+
+# ---- append: tokens in any order ---------------------------------------------------------------------
+
+
+def _prompts(counts, ps, seed, start=None):
+    """(slots, positions, pages) of sequences of these many tokens each, from a place of their first page on."""
+    g = np.random.default_rng(seed)
+    pages = sum(-(-n // ps) + 1 for n in counts)
+    order, slots, positions = list(g.permutation(pages + 2)), [], []
+    for n in counts:
+        at = int(g.integers(0, ps)) if start is None else start
+        mine = [int(order.pop()) for _ in range((at + n - 1) // ps + 1)]
+        slots.append([mine[w // ps] * ps + w % ps for w in range(at, at + n)])
+        positions.append(list(range(at, at + n)))
+    return slots, positions, pages + 2
+
+
+def _steps(counts, lists):
+    """Token by token over the sequences."""
+    return [lists[b][i] for i in range(max(counts)) for b in range(len(counts)) if i < counts[b]]
+
+
+def _append_case(slots, positions, pages, H, D, Dv, rotated, ps, blocks, dtype, seed=0):
+    T = len(slots)
+    grow = torch.exp2(torch.randint(-3, 4, (T, H, 1), generator=_gen(seed + 9), device=DEV).float())
+    scaled = blocks > 0
+    c = dict(k=(_randn((T, H, D), seed + 1) * grow).to(dtype), v=(_randn((T, H, Dv), seed + 2) * grow).to(dtype) if Dv else None,
+             slots=_ints(slots), positions=_ints(positions), f=tk.rotary_frequencies(rotated, device=DEV) if rotated else None,
+             v_cache=None, k_scales=None, v_scales=None)
+    for i, (side, d) in enumerate((("k", D), ("v", Dv))):
+        if d:
+            shape = (pages, ps, H, d)
+            c[side + "_cache"] = _codes(shape, seed + 3 + i) if scaled else _randn(shape, seed + 3 + i, dtype)
+            c[side + "_scales"] = _scales((pages, blocks, H), seed + 5 + i) if scaled else None
+    return c
+
+
+def _append_check(c, layout="half", offset=0, scale=1.0):
+    want = []
+    for side in ("k", "v"):
+        cache, scales = c[side + "_cache"], c[side + "_scales"]
+        if cache is not None:
+            block = cache.shape[1] // scales.shape[1] if scales is not None else 1
+            want.append((side, *C.append(c[side], c["positions"], c["f"] if side == "k" else None, cache, scales, c["slots"],
+                                         block, layout, offset, scale)))
+    tk.cache_append(c["k"], c["v"], c["positions"], c["f"], c["k_cache"], c["v_cache"], c["slots"], k_scales=c["k_scales"],
+                    v_scales=c["v_scales"], layout=layout, offset=offset, scale=scale)
+    for side, cache, bound, scales in want:
+        if scales is not None:
+            assert np.array_equal(R.np64(c[side + "_scales"]), scales), f"{side} scales"
+        R.assert_near(c[side + "_cache"].float(), cache, bound, side)
+
+
+@pytest.mark.parametrize("order", ["steps", "idle", "shuffled"])
+@pytest.mark.parametrize("counts,H,D,Dv,rotated,ps,blocks,dtype,layout", [
+    ([2, 2], 2, 64, 64, 64, 16, 1, BF16, "half"),
+    ([3] * 40, 3, 64, 48, 32, 64, 2, FP16, "half"),
+    ([70, 1, 33], 5, 40, 18, 6, 12, 2, FP32, "interleaved"),
+    ([130, 64, 65], 2, 128, 0, 128, 64, 1, BF16, "interleaved"),
+    ([50, 20], 1, 64, 64, 0, 8, 8, BF16, "half"),  # a scale each
+    ([400] * 13, 4, 64, 64, 64, 64, 1, BF16, "half"),  # large forms
+    ([901, 700, 3, 1200], 9, 64, 64, 48, 48, 3, FP32, "interleaved"),
+    ([2] * 1200, 9, 64, 64, 64, 1, 1, FP16, "half"),
+])
+def test_append_in_any_order(order, counts, H, D, Dv, rotated, ps, blocks, dtype, layout):
+    """A block's tokens anywhere in the call: step by step over the sequences, with idle tokens between, or shuffled."""
+    lists, where, pages = _prompts(counts, ps, len(counts), start=0 if ps == 1 else None)
+    if order == "idle":
+        slots = [s for mine in lists for one in mine for s in (one, -1)]
+        positions = [s for mine in where for one in mine for s in (one, 0)]
+    else:
+        slots, positions = _steps(counts, lists), _steps(counts, where)
+    if order == "shuffled":
+        to = np.random.default_rng(1).permutation(len(slots))
+        slots, positions = [slots[i] for i in to], [positions[i] for i in to]
+    _append_check(_append_case(slots, positions, pages, H, D, Dv, rotated, ps, blocks, dtype), layout)
+
+
+@pytest.mark.parametrize("T", [300, 6000])
+def test_append_one_block_in_many_parts(T):
+    """Two blocks' tokens by turns, of one from its last place to its first."""
+    ps, H, D = T, 2, 64
+    slots = [s for i in range(T // 2) for s in (T // 2 - 1 - i, T + i)]
+    c = _append_case(slots, list(range(T)), 2, H, D, D, D, ps, 1, BF16)
+    c["k"][T // 2] *= 64.0
+    _append_check(c)
+    first = {n: c[n].clone().view(torch.uint8) for n in ("k_cache", "v_cache", "k_scales", "v_scales")}
+    for _ in range(3):  # the same tokens once more change nothing
+        tk.cache_append(c["k"], c["v"], c["positions"], c["f"], c["k_cache"], c["v_cache"], c["slots"], k_scales=c["k_scales"],
+                        v_scales=c["v_scales"])
+        assert all(torch.equal(c[n].view(torch.uint8), b) for n, b in first.items())
