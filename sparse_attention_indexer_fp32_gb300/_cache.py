@@ -130,17 +130,23 @@ def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], positions: Optional
 
 
 def _meet(shape, strides, others, second: int, gap: int, size: int) -> bool:
-    """Whether two caches of these pages and heads share an element, the second one's entries `second`
+    """Whether two caches of these pages and heads may share an element, the second one's entries `second`
     elements long and its start `gap` bytes behind the first one's. Parts of one tensor do not: they have its
-    strides and lie side by side in its pages, tokens or entries. Any other two whose addresses mix may."""
+    strides, each past what the smaller ones reach, and lie side by side in its pages, tokens or entries. Any
+    other two whose addresses mix may."""
     if gap % size or any(n > 1 and s != t for n, s, t in zip(shape[:3], strides, others)):
         return True
-    dims = sorted(((s, n) for n, s in zip(shape[:3], strides) if n > 1), reverse=True)
+    dims, reach = [], max(shape[3], second) - 1  # how far two elements lie apart in the smaller dimensions
+    for step, n in sorted((s, n) for n, s in zip(shape[:3], strides) if n > 1):
+        if step <= reach:
+            return True
+        dims.append((step, n))
+        reach += step * (n - 1)
 
     def meet(gap, dims):
         if not dims:
             return -second < gap < shape[3]
-        step, n = dims[0]
-        return any(meet(gap - d * step, dims[1:]) for d in (gap // step, gap // step + 1) if -n < d < n)
+        step, n = dims[-1]  # the smaller ones reach less than a step: two places at most
+        return any(meet(gap - d * step, dims[:-1]) for d in (gap // step, gap // step + 1) if -n < d < n)
 
     return meet(gap // size, dims)

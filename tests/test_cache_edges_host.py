@@ -1,0 +1,47 @@
+"""The operators of a paged cache in 8 bits on the host where their checks end."""
+
+import itertools
+import random
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from sparse_attention_indexer_fp32_gb300 import _cache  # noqa: E402
+
+
+def _elements(shape, strides, start=0):
+    return {start + sum(i * s for i, s in zip(at, strides)) for at in itertools.product(*(range(n) for n in shape))}
+
+
+def test_caches_that_share_an_element_are_found():
+    """Whatever the strides: no two caches that share an element pass, parts side by side do."""
+
+    def meet(shape, strides, second, gap):
+        return _cache._meet((*shape[:3], shape[3]), (*strides, 1), (*strides, 1), second, gap, 1)
+
+    # pages and heads 33 and 21 apart, entries 5: the element at 48 is reached by another way than the strides' order
+    shape, strides = (2, 2, 3, 2), (5, 33, 21)
+    shared = _elements(shape, (*strides, 1)) & _elements((*shape[:3], 1), (*strides, 1), 48)
+    assert shared and meet(shape, strides, 1, 48)
+    rng = random.Random(1)
+    found = 0
+    for _ in range(4000):
+        shape = tuple(rng.randint(1, 4) for _ in range(4))
+        strides = [rng.randint(1, 12) for _ in range(3)]
+        if rng.random() < 0.5:  # strides of a tensor, its dimensions in any order
+            order, step = rng.sample(range(3), 3), shape[3] + rng.randint(0, 4)
+            for d in order:
+                strides[d], step = step, step * shape[d] + rng.randint(0, 3)
+        second, gap = rng.randint(1, 4), rng.randint(-40, 40)
+        shared = _elements(shape, (*strides, 1)) & _elements((*shape[:3], second), (*strides, 1), gap)
+        found += bool(shared)
+        assert not shared or meet(shape, strides, second, gap), (shape, strides, second, gap)
+    assert found > 500
+    # what lies side by side in pages, entries, heads or the pool is let through
+    for shape, strides, second, gap in (((5, 4, 3, 8), (192, 24, 8), 8, 96), ((5, 4, 3, 8), (192, 24, 8), 8, -96),
+                                        ((5, 4, 3, 8), (240, 60, 20), 12, 8), ((5, 4, 3, 12), (240, 60, 20), 8, -8),
+                                        ((5, 4, 3, 8), (96, 8, 32), 8, 480), ((3, 4, 3, 8), (96, 24, 8), 8, 288),
+                                        ((3, 4, 3, 8), (192, 24, 8), 8, 96), ((1, 1, 1, 8), (7, 3, 5), 8, 8)):
+        assert not _elements(shape, (*strides, 1)) & _elements((*shape[:3], second), (*strides, 1), gap)
+        assert not meet(shape, strides, second, gap), (shape, strides, second, gap)
