@@ -121,12 +121,29 @@ def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], positions: Optional
                 raise ValueError("v_scales must have the blocks of k_scales")
             if units_v == units_k and pages * H > 0:
                 raise ValueError("v_scales must not be k_scales: each cache has its own")
+        size_of_scales = 4 * pages * blocks * H
+        spans = [(at_k, end_k), (to_k, end_keys), (to, to + 4 * T)]
+        if freq:
+            spans += (pos, pos + (8 if wide else 4) * T), (freq, freq + 8 * pairs)
+        if v is not None:
+            spans += (at_v, end_v), (to_v, end_values)
+            if _clash(units_v, size_of_scales, spans):
+                raise ValueError("v_scales must not overlap any other tensor of the call")
+            spans.append((units_v, units_v + size_of_scales))
+        if _clash(units_k, size_of_scales, spans):
+            raise ValueError("k_scales must not overlap any other tensor of the call")
     elif k_scales is not None or v_scales is not None:
         raise ValueError("only caches in float8_e4m3fn have scales")
     _append(index, stream, at_k, xs[0], xs[1], at_v, vx[0], vx[1], to_k, kt[0], kt[1], kt[2], to_v, vt[0], vt[1], vt[2],
             units_k, units_v, pos, freq, to, pages, page_size, blocks, T, H, D, Dv, 2 * pairs, int(offset),
             _LAYOUTS[layout], code, 3 if eight else code, wide, scale)
     _written([t for t in (k_cache, v_cache, k_scales, v_scales) if t is not None])
+
+
+def _clash(begin: int, size: int, spans) -> bool:
+    """Whether `size` bytes from `begin` overlap one of the spans [start, end)."""
+    end = begin + size
+    return size > 0 and any([start < end and begin < stop and start < stop for start, stop in spans])
 
 
 def _meet(shape, strides, others, second: int, gap: int, size: int) -> bool:

@@ -435,6 +435,8 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, indices:
             if same != blocks:
                 raise ValueError("v_scales must have the blocks of k_scales")
             scales = (units, others, blocks)
+        if given and any([_overlap(mine, (at, at + 4 * pages * blocks * Hkv)) for at in scales[:2]]):
+            raise ValueError("out must not overlap k_scales or v_scales")
         call = _attention_e4m3
     lse = _empty((B, T, Hq), _FP32, q, stream) if return_lse else None
     call(index, stream, at_q, qs[0], qs[1], qs[2], at_k, kt[0], kt[1], kt[2], at_v, vt[0], vt[1], vt[2], idx, table,

@@ -45,3 +45,10 @@ def test_caches_that_share_an_element_are_found():
                                         ((3, 4, 3, 8), (192, 24, 8), 8, 96), ((1, 1, 1, 8), (7, 3, 5), 8, 8)):
         assert not _elements(shape, (*strides, 1)) & _elements((*shape[:3], second), (*strides, 1), gap)
         assert not meet(shape, strides, second, gap), (shape, strides, second, gap)
+
+
+def test_spans_that_overlap():
+    for size, spans, want in ((8, [(108, 120), (92, 100)], False), (8, [(107, 120)], True),
+                              (8, [(90, 101)], True), (8, [(102, 104)], True), (8, [(90, 120)], True), (0, [(90, 120)], False),
+                              (8, [(104, 104)], False), (8, [(100, 108)], True), (8, [(100, 104)], True), (8, [(104, 108)], True)):
+        assert _cache._clash(100, size, spans) is want, (size, spans)

@@ -243,3 +243,44 @@ def test_append_one_block_in_many_parts(T):
         tk.cache_append(c["k"], c["v"], c["positions"], c["f"], c["k_cache"], c["v_cache"], c["slots"], k_scales=c["k_scales"],
                         v_scales=c["v_scales"])
         assert all(torch.equal(c[n].view(torch.uint8), b) for n, b in first.items())
+
+
+def test_append_scales_that_overlap():
+    """Scales share no memory with each other, the caches or the inputs."""
+    H, D, ps, pages = 2, 64, 8, 4
+    lists, where, _ = _prompts([6], ps, 1)
+    base = _append_case(lists[0], where[0], pages, H, D, D, D, ps, 2, BF16)
+    pool = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
+
+    def at(start, like):
+        return pool[start:start + like.numel() * like.element_size()].view(like.dtype).view(like.shape)
+
+    size = base["k_scales"].numel() * 4
+    for name in ("k_scales", "v_scales"):
+        other = "v_scales" if name == "k_scales" else "k_scales"
+        for of in ("k", "v", "k_cache", "v_cache", "slots", "positions", "f", other):
+            c = dict(base)
+            c[of] = at(1024, base[of])
+            end = 1024 + base[of].numel() * base[of].element_size()
+            for start in (1024 - size + 8, end - 8):
+                c[name] = at(start, base[name])
+                with pytest.raises(ValueError, match="_scales must not overlap"):
+                    tk.cache_append(c["k"], c["v"], c["positions"], c["f"], c["k_cache"], c["v_cache"], c["slots"],
+                                    k_scales=c["k_scales"], v_scales=c["v_scales"])
+    c = dict(base, k_scales=at(1024, base["k_scales"]), v_scales=at(1024 + size, base["v_scales"]))
+    _append_check(c)  # one behind the other
+
+
+def test_attention_scales_that_overlap_the_result():
+    c = _one_row(8, 100, BF16)
+    pool = torch.zeros(1 << 14, dtype=torch.uint8, device=DEV)
+    out = pool[4096:4096 + 8 * 64 * 2].view(BF16).view(1, 1, 8, 64)
+    want = tk.sparse_attention(**c)
+    for name in ("k_scales", "v_scales"):
+        for start in (4096 - 4, 4096 + 8 * 64 * 2 - 4):
+            part = pool[start:start + 8].view(FP32).view(c[name].shape)
+            with pytest.raises(ValueError, match="out must not overlap k_scales"):
+                tk.sparse_attention(**{**c, name: part}, out=out)
+        part = pool[4096 - 8:4096].view(FP32).view(c[name].shape)
+        part.copy_(c[name])
+        assert torch.equal(tk.sparse_attention(**{**c, name: part}, out=out), want)
