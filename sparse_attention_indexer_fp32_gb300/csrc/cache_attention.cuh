@@ -1007,12 +1007,9 @@ topk_status launch_heads(const sparse_attention_e4m3_args& args, int dev, int sm
   if (grid > INT32_MAX || (work / grid + 1) * tiles > INT32_MAX) return TOPK_EINVAL;  // a CTA counts its tiles
   constexpr auto kernel = cache_attention_kernel<E, G>;
   // What the groups of warps trade is what the launch brings.
-  static const int regs = [] {
-    cudaFuncAttributes f = {};
-    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
-  }();
-  if (regs != S::regs) return TOPK_ECUDA;
-  const topk_status st = allow_shared<kernel>(dev);
+  topk_status st = has_registers<kernel>(S::regs);
+  if (st != TOPK_OK) return st;
+  st = allow_shared<kernel>(dev);
   if (st != TOPK_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));

@@ -43,6 +43,20 @@ topk_status allow_shared(int dev) {
   return TOPK_OK;
 }
 
+// Whether `kernel` has the registers a thread that it was laid out for, asked once: an answer that did
+// not come is asked for again by the next call.
+template <auto kernel>
+topk_status has_registers(int registers) {
+  static std::atomic<bool> done;
+  if (done.load(std::memory_order_relaxed)) return TOPK_OK;
+  cudaFuncAttributes f = {};
+  const topk_status st = status_of(cudaFuncGetAttributes(&f, kernel));
+  if (st != TOPK_OK) return st;
+  if (f.numRegs != registers) return TOPK_ECUDA;
+  done.store(true, std::memory_order_relaxed);
+  return TOPK_OK;
+}
+
 topk_status launch_rotary(const sparse_rotary_args& a, int sm_count, cudaStream_t stream);
 topk_status launch_scores_bf16(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream);
 topk_status launch_scores_fp16(const sparse_scores_args& a, int dev, int sm_count, cudaStream_t stream);

@@ -1,13 +1,17 @@
 """The operators of a paged cache in 8 bits on the host where their checks end."""
 
 import itertools
+import os
 import random
+import subprocess
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
+import sparse_attention_indexer_fp32_gb300 as tk  # noqa: E402
 from sparse_attention_indexer_fp32_gb300 import _cache  # noqa: E402
+from sparse_attention_indexer_fp32_gb300 import build as cuda_build  # noqa: E402
 
 
 def _elements(shape, strides, start=0):
@@ -52,3 +56,45 @@ def test_spans_that_overlap():
                               (8, [(90, 101)], True), (8, [(102, 104)], True), (8, [(90, 120)], True), (0, [(90, 120)], False),
                               (8, [(104, 104)], False), (8, [(100, 108)], True), (8, [(100, 104)], True), (8, [(104, 108)], True)):
         assert _cache._clash(100, size, spans) is want, (size, spans)
+
+
+# ---- the registers that attention's warps trade ------------------------------------------------------
+
+PROGRAM = r"""
+#include <cstdio>
+#include "step_launch.cuh"
+
+__global__ void kernel(int* x) { *x = 1; }
+
+extern int calls;
+
+int main() {
+  for (int i = 0; i < 5; ++i) std::printf("%d ", static_cast<int>(tki::has_registers<kernel>(64)));
+  std::printf("%d\n", calls);
+}
+"""
+
+FAKE = r"""
+#include <cuda_runtime_api.h>
+
+// The CUDA call, with answers of the test's: an error at first, then registers.
+int calls = 0, answers[] = {-1, 40, 64, -1, 1};
+cudaError_t CUDARTAPI cudaFuncGetAttributes(cudaFuncAttributes* f, const void*) {
+  const int a = answers[calls++];
+  f->numRegs = a;
+  return a < 0 ? cudaErrorUnknown : cudaSuccess;
+}
+"""
+
+
+def test_an_answer_that_did_not_come_is_asked_for_again(tmp_path):
+    """A register count that CUDA fails to tell, or another one than was laid out for, refuses that call alone; once it
+    was right it is not asked for again."""
+    source, fake, program = tmp_path / "registers.cu", tmp_path / "fake.cpp", tmp_path / "registers"
+    source.write_text(PROGRAM), fake.write_text(FAKE)
+    libraries = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cuda_build.nvcc()))), "lib64")
+    subprocess.run([cuda_build.nvcc(), *cuda_build.ARCH, "-std=c++17", "-cudart", "shared", "-I", cuda_build.INCLUDE, "-I",
+                    cuda_build.CSRC, str(source), str(fake), "-o", str(program)], check=True, timeout=300)
+    got = subprocess.run([str(program)], check=True, timeout=60, capture_output=True, text=True,
+                         env={**os.environ, "LD_LIBRARY_PATH": libraries}).stdout.split()
+    assert [int(x) for x in got] == [tk.Status.ECUDA, tk.Status.ECUDA, tk.Status.OK, tk.Status.OK, tk.Status.OK, 3]
