@@ -17,6 +17,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU-only machines
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import sparse_attention_indexer_fp32_gb300 as tk  # noqa: E402
+from test_gpu_cache import _attend  # noqa: E402
 
 DEV = torch.device("cuda:0")
 BF16, FP16, FP32, E4M3 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
@@ -284,3 +285,79 @@ def test_attention_scales_that_overlap_the_result():
         part = pool[4096 - 8:4096].view(FP32).view(c[name].shape)
         part.copy_(c[name])
         assert torch.equal(tk.sparse_attention(**{**c, name: part}, out=out), want)
+
+
+# ---- the larger forms --------------------------------------------------------------------------------
+
+MANY = [
+    # rows, query heads, key heads, D, Dv, K, dtype, shared: one, two or three works a CTA, of one to five tiles
+    (650, 8, 1, 64, 64, 130, BF16, False),
+    (650, 16, 1, 128, 256, 300, BF16, False),
+    (650, 16, 1, 256, 64, 129, FP16, True),
+    (650, 12, 1, 128, 128, 260, FP16, False),
+    (420, 32, 1, 192, 128, 400, BF16, False),
+    (420, 24, 1, 128, 240, 300, FP16, False),
+    (420, 32, 1, 256, 192, 520, FP16, True),
+    (420, 64, 1, 256, 256, 300, BF16, False),  # one stage
+    (420, 64, 1, 256, 192, 130, BF16, True),
+    (420, 40, 1, 96, 80, 100, BF16, False),
+    (210, 32, 4, 64, 128, 390, BF16, False),
+    (170, 50, 1, 128, 80, 200, FP16, False),  # two tiles of heads
+    (130, 35, 5, 96, 64, 300, FP16, False),
+]
+
+
+@pytest.mark.parametrize("rows,Hq,Hkv,D,Dv,K,dtype,shared", MANY)
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, True)])
+def test_attention_several_rows_a_cta(rows, Hq, Hkv, D, Dv, K, dtype, shared, cap, bias):
+    """More works than CTAs, the heads' logits of different sizes, so that in every tile some references move: a sample
+    of the rows, first, second and third ones of their CTAs among them."""
+    c = _attend(rows, 1, Hq, Hkv, D, Dv, K, 2 * K, 48, 3, dtype, seed=K + Hq, shared=shared)
+    c["q"] = c["q"] * torch.exp2((torch.arange(Hq, device=DEV) * 5 % 7 - 3).float())[:, None].to(dtype)
+    c["indices"][7] = -1  # a row that sees nothing, between others
+    if bias:
+        c["slopes"], c["softcap"] = _randn((Hq,), 6, FP32, 0.05), cap
+    out, lse = tk.sparse_attention(**c, return_lse=True)
+    assert torch.equal(out, tk.sparse_attention(**c))
+    some = sorted({0, 7, 8, 151 % rows, 152 % rows, 153 % rows, 303 % rows, 304 % rows, 305 % rows, 455 % rows, 456 % rows,
+                   608 % rows, 609 % rows, rows - 2, rows - 1})
+    some = torch.tensor(some, device=DEV)
+    pages = c["page_table"][some].flatten().long()
+    clean = {n: torch.nan_to_num(c[n][pages].float(), nan=0.0) for n in ("k", "v", "k_scales", "v_scales")}
+    table = torch.arange(pages.numel(), device=DEV).view(len(some), -1)
+    want = C.attention(c["q"][some], clean["k"].to(E4M3), clean["v"].to(E4M3), clean["k_scales"], clean["v_scales"],
+                       c["indices"][some], table, c["query_positions"][some], c["scale"], c.get("softcap", 0.0), c.get("slopes"))
+    R.assert_near(lse[some], want[2], want[3], "lse")
+    R.assert_near(out[some], want[0], want[1], "out")
+
+
+LARGE = [
+    # counts, H, D, Dv, rotated, offset, page size, blocks (0: of the inputs' type), dtype, layout
+    ([1501, 800], 6, 128, 96, 128, 0, 64, 0, BF16, "half"),
+    ([1501, 800], 9, 96, 128, 64, 32, 17, 0, FP16, "interleaved"),
+    ([1401], 5, 128, 64, 96, 16, 64, 0, FP32, "half"),
+    ([1000, 1], 3, 66, 18, 32, 2, 16, 0, BF16, "half"),  # nothing aligned
+    ([1600, 1], 3, 33, 18, 32, 1, 16, 0, FP32, "interleaved"),
+    ([2300, 33], 7, 128, 96, 64, 64, 64, 1, FP16, "half"),
+    ([901, 700], 5, 112, 80, 48, 64, 48, 3, FP32, "interleaved"),
+    ([901, 700], 5, 96, 64, 96, 0, 64, 4, FP32, "half"),
+    ([1000, 3], 3, 65, 18, 32, 1, 16, 2, BF16, "interleaved"),  # nothing aligned
+    ([1000, 3], 3, 66, 31, 30, 5, 16, 1, FP16, "half"),
+    ([1500, 700], 7, 64, 128, 64, 0, 512, 1, BF16, "interleaved"),  # runs of several sweeps
+    ([700, 500], 3, 512, 256, 512, 0, 64, 1, FP16, "half"),  # read twice
+    ([300, 300], 2, 1024, 1000, 64, 960, 32, 1, FP32, "half"),
+    ([400, 200], 1, 1023, 515, 1022, 1, 32, 2, BF16, "interleaved"),  # more items than threads
+    ([3000, 2500], 9, 64, 0, 64, 0, 64, 64, BF16, "half"),  # keys alone, a scale each
+]
+
+
+@pytest.mark.parametrize("counts,H,D,Dv,rotated,offset,ps,blocks,dtype,layout", LARGE)
+@pytest.mark.parametrize("idle", [False, True])
+def test_append_large(counts, H, D, Dv, rotated, offset, ps, blocks, dtype, layout, idle):
+    """Calls of as many tokens as prompts have, in all that the forms for them tell apart, idle tokens between or not."""
+    lists, where, pages = _prompts(counts, ps, len(counts))
+    slots, positions = sum(lists, []), sum(where, [])
+    if idle:
+        slots = [s for i, one in enumerate(slots) for s in ((one, -1) if i % 5 == 0 else (one,))]
+        positions = [s for i, one in enumerate(positions) for s in ((one, 0) if i % 5 == 0 else (one,))]
+    _append_check(_append_case(slots, positions, pages, H, D, Dv, rotated, ps, blocks, dtype), layout, offset, 0.75)
