@@ -1,10 +1,11 @@
 """A decode step of sparse attention, from one token's projections to its attention output.
 
-For every sequence of a batch: the new token's key is rotated on its way into the paged cache, its
-queries are rotated, the indexer scores every position of the sequence, the selection takes the best
-``k``, and attention runs over those entries only. All of it is enqueued on one stream and can be
+For every sequence of a batch: the new token's keys, rotated on the way, and values go into the paged
+caches, its queries are rotated, the indexer scores every position of the sequence, the selection takes
+the best ``k``, and attention runs over those entries only. All of it is enqueued on one stream and can be
 captured in a CUDA graph: nothing is allocated where the buffers are given, and nothing is read back.
-With ``--eight`` keys and values are held in 8 bits, with a scale for each page and head.
+With ``--eight`` all keys and values are held in 8 bits: the attention's with a scale for each page and
+head, the indexer's with one for each key.
 
     python examples/sparse_step.py [--batch 8] [--length 4000] [--k 512] [--eight]
 """
@@ -32,7 +33,8 @@ class Cache:
         self.k, self.v = (torch.zeros((*shape, kv_heads, head), dtype=dtype, device=device) for _ in range(2))
         self.k_scales = torch.zeros((batch * pages, 1, kv_heads), device=device) if eight else None
         self.v_scales = torch.zeros_like(self.k_scales) if eight else None
-        self.index_k = torch.zeros((*shape, index_head), dtype=torch.bfloat16, device=device)
+        self.index_k = torch.zeros((*shape, index_head), dtype=dtype, device=device)
+        self.index_scales = torch.zeros((*shape, 1), device=device) if eight else None
         self.table = torch.randperm(batch * pages, device=device).to(torch.int32).view(batch, pages)
         self.width, self.page_size = width, page_size
 
@@ -47,6 +49,12 @@ class Cache:
         return x if scales is None else x * scales[slots // self.page_size, 0, :, None]
 
 
+def in_eight(x):
+    """Vectors in 8 bits, and the scale of each."""
+    units = x.float().abs().amax(dim=-1).clamp(min=1e-30) / 448.0
+    return (x.float() / units[..., None]).to(torch.float8_e4m3fn), units
+
+
 def step(cache, frequencies, q, k, v, index_q, index_weights, index_k, lengths, select):
     """One token a sequence. ``lengths`` [B] counts the token itself; ``q`` [B, Hq, D], ``k`` and ``v``
     [B, Hkv, D], ``index_q`` [B, H, Di], ``index_weights`` [B, H], ``index_k`` [B, Di]. Returns the
@@ -54,17 +62,18 @@ def step(cache, frequencies, q, k, v, index_q, index_weights, index_k, lengths, 
     B = lengths.numel()
     positions = lengths - 1
     slots = cache.slots(positions)
-    if cache.k_scales is None:
-        tk.rotary(k, positions, frequencies, out=cache.k, slots=slots)
-        cache.v.view(-1, *v.shape[1:])[slots.long()] = v
-    else:
-        tk.cache_append(k, v, positions, frequencies, cache.k, cache.v, slots, k_scales=cache.k_scales,
-                        v_scales=cache.v_scales)
-    tk.rotary(index_k[:, None], positions, frequencies, out=cache.index_k[:, :, None], slots=slots)
+    tk.cache_append(k, v, positions, frequencies, cache.k, cache.v, slots, k_scales=cache.k_scales,
+                    v_scales=cache.v_scales)
+    tk.cache_append(index_k[:, None], None, positions, frequencies, cache.index_k[:, :, None], None, slots,
+                    k_scales=cache.index_scales)
     q = tk.rotary(q, positions, frequencies)
     index_q = tk.rotary(index_q, positions, frequencies)
+    key_scales = None
+    if cache.index_scales is not None:  # the queries' scales go into the weights
+        index_q, units = in_eight(index_q)
+        index_weights, key_scales = index_weights * units, cache.index_scales[..., 0]
     scores = tk.indexer_scores(index_q[:, None], index_weights[:, None], cache.index_k, lengths[:, None], cache.table,
-                               width=cache.width)
+                               key_scales=key_scales, width=cache.width)
     chosen = tk.topk_ragged(scores.view(B, -1), lengths, select)
     return tk.sparse_attention(q[:, None], cache.k, cache.v, chosen[:, None], cache.table,
                                query_positions=positions[:, None], k_scales=cache.k_scales,
@@ -82,11 +91,16 @@ def step_plain(cache, frequencies, q, k, v, index_q, index_weights, index_k, len
 
     out = torch.empty_like(q)
     tq, tiq = turn(q, lengths - 1), turn(index_q, lengths - 1)
+    if cache.index_scales is not None:
+        codes, units = in_eight(tiq)
+        tiq = codes.float() * units[..., None]
     for b in range(lengths.numel()):
         n = int(lengths[b])
         s = torch.arange(n, device=q.device)
         slots = cache.table[b, s // cache.page_size].long() * cache.page_size + s % cache.page_size
         keys = cache.index_k.flatten(0, 1)[slots].float()
+        if cache.index_scales is not None:
+            keys = keys * cache.index_scales.flatten(0, 1)[slots]
         scores = index_weights[b] @ torch.relu(tiq[b] @ keys.T)
         chosen = slots[scores.topk(min(select, n)).indices]
         kk, vv = (cache.entries(c, s, chosen).repeat_interleave(q.shape[1] // c.shape[2], dim=1)
@@ -99,12 +113,12 @@ def step_plain(cache, frequencies, q, k, v, index_q, index_weights, index_k, len
 def make(batch, length, device="cuda", heads=32, kv_heads=4, head=128, index_heads=32, index_head=128, eight=False):
     """A cache with ragged sequences in it, the next token of each, and the frequencies."""
     cache = Cache(batch, length + 1, kv_heads=kv_heads, head=head, index_head=index_head, device=device, eight=eight)
-    if eight:
-        for t, scales in ((cache.k, cache.k_scales), (cache.v, cache.v_scales)):
+    for t, scales in ((cache.k, cache.k_scales), (cache.v, cache.v_scales), (cache.index_k, cache.index_scales)):
+        if eight:
             t.copy_(torch.randn(t.shape, device=device) * 64)
             scales.fill_(1 / 64)
-    for t in (cache.index_k,) if eight else (cache.k, cache.v, cache.index_k):
-        t.normal_()
+        else:
+            t.normal_()
     lengths = torch.randint(max(1, length // 2), length + 1, (batch,), device=device).to(torch.int32) + 1
 
     def randn(*shape):

@@ -2,6 +2,8 @@
 against the formulas in 64 bits (``cache_reference``) or what follows from them."""
 
 import math
+import os
+import sys
 
 import numpy as np
 import pytest
@@ -361,3 +363,29 @@ def test_append_large(counts, H, D, Dv, rotated, offset, ps, blocks, dtype, layo
         slots = [s for i, one in enumerate(slots) for s in ((one, -1) if i % 5 == 0 else (one,))]
         positions = [s for i, one in enumerate(positions) for s in ((one, 0) if i % 5 == 0 else (one,))]
     _append_check(_append_case(slots, positions, pages, H, D, Dv, rotated, ps, blocks, dtype), layout, offset, 0.75)
+
+
+# ---- the example's step ------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_example_step_fills_its_caches(eight):
+    """The step on caches of either kind against its plain form, and what it appended against the formulas."""
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import sparse_step as ex
+
+    torch.manual_seed(4)
+    cache, f, token = ex.make(5, 900, eight=eight)
+    q, k, v, index_q, weights, index_k, lengths = token
+    positions = lengths - 1
+    slots, block = cache.slots(positions), 1 if not eight else None
+    wants = [C.append(x, positions, turn, held, units, slots, block or held.shape[1] // units.shape[1])
+             for x, turn, held, units in ((k, f, cache.k, cache.k_scales), (v, None, cache.v, cache.v_scales),
+                                          (index_k[:, None], f, cache.index_k[:, :, None],
+                                           None if not eight else cache.index_scales))]
+    got = ex.step(cache, f, *token, 128)
+    for (want, bound, _), held in zip(wants, (cache.k, cache.v, cache.index_k[:, :, None])):
+        R.assert_near(held.float(), want, bound)
+    plain = ex.step_plain(cache, f, *token, 128)
+    # the queries' and the result's roundings and the weights', then a swapped entry
+    assert (got - plain).float().norm() <= (3 * 2.0 ** -8 + 0.02) * plain.float().norm()
