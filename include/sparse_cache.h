@@ -51,7 +51,7 @@ extern "C" {
  *     that holds nothing yet; any other is positive and normal. What lies behind
  *     `first` counts as nothing.
  *   - Numbers are rounded to nearest, once; results that are not finite become NaN.
- * The angle is as exact as sparse_rotary's, sine and cosine good to 2^-21 where
+ * The angle is as exact as sparse_rotary's, sine and cosine good to 2^-20 where
  * the cache has less than 32 bits, to 2 ulp in SPARSE_FP32.
  */
 typedef struct sparse_append_args {

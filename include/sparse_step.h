@@ -62,7 +62,7 @@ typedef enum sparse_rotary_layout {
  * turns up to the rounding of frequencies[i] / 2 pi to 2^-63 turns, times the
  * position (2^-32 turns at the end of the 32-bit range), and 2^-32 turns of its
  * own: positions of that whole range are as accurate as small ones. Sine and
- * cosine are good to 2 ulp in SPARSE_FP32, to 2^-21 in the 16-bit types.
+ * cosine are good to 2 ulp in SPARSE_FP32, to 2^-20 in the 16-bit types.
  *
  * out may be x itself with the same strides (in place; only the rotated part
  * is then touched); it must not overlap x in any other way. With `slots`, out

@@ -342,8 +342,8 @@ __device__ __forceinline__ void append_side(const AppendParams& p, const AppendS
       const int pair = i * kPairs + j;
       const uint64_t turn = static_cast<uint64_t>(pos) * sh.rates[pair < pairs ? pair : 0];
       const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
-      // 2^-21 by the special function unit: 2^-10 of a 16-bit result's
-      // rounding, 2^-17 of an 8-bit one's; FP32 takes the full functions.
+      // 2^-20 by the special function unit (see rotary.cu): 2^-9 of fp16's
+      // rounding, 2^-16 of an 8-bit one's; FP32 takes the full functions.
       if constexpr (SCALED || sizeof(E) == 2)
         __sincosf(half_turns * 3.14159265f, &sines[j], &cosines[j]);
       else

@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     for (int j = 0; j < kPairs; ++j) {
       const uint64_t turn = static_cast<uint64_t>(pos) * turns_of(p.frequencies[i * kPairs + j]);
       // Within half a turn either way the special function unit is good to
-      // 2^-21, 2^-10 of a 16-bit result's rounding; FP32 takes the full functions.
+      // 2^-20 (the special function unit's 2^-21.2, and 2^-21.6 of the angle: its rounding, that of pi and of
+      // their product), 2^-9 of fp16's rounding; FP32 takes the full functions.
       const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
       if constexpr (sizeof(E) == 2)
         __sincosf(half_turns * 3.14159265f, &sines[j], &cosines[j]);

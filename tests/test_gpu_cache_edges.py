@@ -389,3 +389,29 @@ def test_example_step_fills_its_caches(eight):
     plain = ex.step_plain(cache, f, *token, 128)
     # the queries' and the result's roundings and the weights', then a swapped entry
     assert (got - plain).float().norm() <= (3 * 2.0 ** -8 + 0.02) * plain.float().norm()
+
+
+# ---- sines and cosines -------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("call", ["rotary", "cache_append"])
+def test_small_sines_and_cosines(call):
+    """Pairs (1, 0) turn to a cosine and a sine: in fp16, whose steps are small near zero, each is off by 2^-20 and its
+    rounding at most."""
+    T, pairs = 4000, 128
+    f = torch.rand(pairs, dtype=torch.float64, generator=_gen(1), device=DEV) * 3.0
+    positions = torch.randint(-(2 ** 20), 2 ** 20, (T,), generator=_gen(2), device=DEV)
+    x = torch.zeros((T, 1, 2 * pairs), dtype=FP16, device=DEV)
+    x[..., :pairs] = 1.0
+    if call == "rotary":
+        got = tk.rotary(x, positions, f)
+    else:
+        got = torch.zeros((1, T, 1, 2 * pairs), dtype=FP16, device=DEV)
+        tk.cache_append(x, None, positions, f, got, None, torch.arange(T, dtype=torch.int32, device=DEV))
+    angle = R.npi(positions).astype(np.longdouble)[:, None] * R.np64(f).astype(np.longdouble)
+    want = np.concatenate([np.cos(angle), np.sin(angle)], axis=1).astype(np.float64)
+    off = np.abs(R.np64(got).reshape(T, -1) - want)
+    assert (off <= 2.0 ** -20 + (np.abs(want) + 2.0 ** -20) * 2.0 ** -11 + 2.0 ** -25).all()
+    near = np.abs(want) < 2.0 ** -9
+    assert near.sum() > 1000
+    print(f"off by 2^{np.log2(off[near].max()):.2f} near zero")
