@@ -143,7 +143,10 @@ def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], positions: Optional
 def _clash(begin: int, size: int, spans) -> bool:
     """Whether `size` bytes from `begin` overlap one of the spans [start, end)."""
     end = begin + size
-    return size > 0 and any([start < end and begin < stop and start < stop for start, stop in spans])
+    for start, stop in spans:
+        if start < end and begin < stop and start < stop:
+            return size > 0
+    return False
 
 
 def _meet(shape, strides, others, second: int, gap: int, size: int) -> bool:
