@@ -84,7 +84,8 @@ topk_status sparse_append(const sparse_append_args* args, topk_stream_t stream);
  * and slots, word for word) over a cache whose entries stand for k = k_scales[b,
  * g] * the numbers of attention.k, v = v_scales[b, g] * those of attention.v, with b
  * the entry's block and g the key head. attention.type is the type of q and out.
- * Scales are finite; values' scales of 2^-60 to 2^60 lose nothing, below that the
+ * Scales are finite, and so is a key's scale times attention.scale times a 2^7th part of a query
+ * head's largest element, in FP32; values' scales of 2^-60 to 2^60 lose nothing, below that the
  * values fade out. A NaN in an entry that is seen makes NaN of every result it
  * enters, and so does a query that is not finite.
  * Products are exact: a bf16 or fp16 query is split into two or three E4M3 terms

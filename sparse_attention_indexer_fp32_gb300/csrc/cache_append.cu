@@ -26,9 +26,10 @@
 // single tokens (44), where every CTA looks; and the call's tokens squared where they lie shuffled.
 //
 // Measured, in a CUDA graph: 8192 tokens x 8 heads x (128 + 128), bf16, into 8 bits 34 us for
-// 7.4 at the copy rate. It is bound by instructions and by what they wait for: 24 an element,
-// issue slots 45 % busy, DRAM 16 %; a CTA's three barriers (slots, sizes, scales) leave its
-// warps idle where the CTA beside it has nothing to issue. 4096 tokens x 8 x (128 + 128), fp16,
+// 7.4 at the copy rate. It is bound by instructions and by what they wait for: 26 an element,
+// issue slots 41 % busy, DRAM 12 %; a CTA's three barriers (slots, sizes, scales) leave its
+// warps idle where the CTA beside it has nothing to issue, and so do instructions that are not
+// in the cache (2.2 of an issue's 13 cycles, 0.5 without the look through other slots). 4096 tokens x 8 x (128 + 128), fp16,
 // as they are 10.4 us (4.8); 64 tokens 8.4 us, a launch and reads of slot, scale and token one
 // behind the other; 8192 index keys of 128 with a scale each 8.3 us.
 #include <cuda_runtime.h>
@@ -653,10 +654,10 @@ __global__ void __launch_bounds__(Form::threads, Form::per_sm) append_kernel(con
 bool aligned_to(const void* q, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(q) & (bytes - 1)) == 0; }
 
 // Many tokens: a block of 64 with heads of 128 stays in a CTA's registers (8192 tokens
-// x 8 heads x (128 + 128), bf16, into 8 bits: 30 us by two heads a thread and three CTAs
-// an SM, 35 by two CTAs, 36 by four heads; into 16 bits, which wait on nothing between,
+// x 8 heads x (128 + 128), bf16, into 8 bits: 34 us by two heads a thread and three CTAs
+// an SM, 40 by two CTAs, 39 by four heads; into 16 bits, which wait on nothing between,
 // 12.3 for 10.4 by four heads). Few: small CTAs, so that all SMs have some (64 tokens
-// 7.2 us, 12 by large ones).
+// 8.4 us, 14.6 by large ones).
 using ScaledForm = FormOf<256, 2, 2, 3, 64>;
 using PlainForm = FormOf<256, 2, 4, 2, 64>;
 using FewForm = FormOf<128, 1, 1, 4, 16>;

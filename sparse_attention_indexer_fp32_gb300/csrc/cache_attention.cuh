@@ -6,7 +6,7 @@
 // so queries and weights are split into E4M3 terms, x = u (t0 + t1 / 16 + t2 / 256),
 // each the rounded rest of those before. A term adds five bits (four and the
 // rest's sign): two hold 9, a bf16 query exactly; three hold 14, an fp16 query
-// exactly. Two terms of a weight round it to 2^-9 of itself, half a step of bf16's;
+// exactly. Two terms of a weight round it to 2^-9 of itself, half of what bf16 would;
 // three are good to fp16's 2^-11, which it is rounded to first. A query's unit u is
 // a power of two, its head's own.
 //
@@ -24,8 +24,10 @@
 // the largest weight there is. The
 // sum that divides adds the weights in FP32, unrounded and without the values' scales. r
 // is a whole number, so moving it is exact but for logits that were rounded next to the
-// old one: past kFar those are computed anew. A head's references follow from its own
-// logits alone, so neither the rows nor the heads of a call change its bits.
+// old one: past kFar those are computed anew. Whether a head's reference moves in a tile, and
+// by how much, follows from its own logits and the CTA's tiles. Its last bits follow from
+// more: from how many CTAs share a row, which the call's works decide, and from the other
+// heads of its set, where one of them passes kFar and all logits are rounded once, not twice.
 //
 // The rest is as in sparse_attention.cu: entries gathered by 16-byte copies into
 // rings of keys and values, few rows shared by a cluster whose CTAs join through
@@ -39,15 +41,18 @@
 // Bounds. Few heads and long lists: the entries' bytes. Many heads: the softmax warps (a
 // logit's two terms joined, scaled, an exponential, a sum, two roundings to E4M3 and the
 // rest between them: with loads and gathers thirty instructions), and a row's end, where they wait for the last product,
-// sum and write while the tensor cores wait for them; TMEM has no room for a second set of
-// sums. Figures, in a CUDA graph:
-//   2048 rows x 64 heads over 512 shared entries of 256: 147 us, 32 of them at the rate of
-//   bf16 products (137 where no reference moves; 233 over 1024 entries, 80 over 128; 32 heads
-//   119, 16 heads 80, 8 heads 62, there 4.3 TB/s of entries out of L2). 53 thousand warp
-//   instructions a row: 7.6 a tile, 23 for queries, first references and the end; issue slots 65 %;
-//   64 rows x 8 x 8 heads of 128 over 2048 entries: 56.5 us, 6 TB/s less a start of some 12 us
-//   (launch, list, page, entries, one behind the other); 4 rows over 512 entries 11.6 us.
-// Lost: dedicated warps that read the sums out (226 us: registers), two CTAs an SM with tiles
+// sum and write while the tensor cores wait for them: there is one set of sums, though TMEM
+// would hold a second one but for values past 128 with 64 heads (fp16: 32, and 16 with two CTAs
+// an SM); and a moved reference, for which a set waits for the product before.
+// Figures, in a CUDA graph:
+//   2048 rows x 64 heads over 512 shared entries of 256: 166 us, 32 of them at the rate of
+//   bf16 products (135 where no reference moves; 270 over 1024 entries, 80 over 128; 32 heads
+//   130, 16 heads 91, 8 heads 64, there 4.2 TB/s of entries out of L2). 62 thousand warp
+//   instructions a row, some 7.6 of them a tile that moves nothing; issue slots 70 %. In fp16 268,
+//   141, 103 and 70 us for 64, 32, 16 and 8 heads;
+//   64 rows x 8 x 8 heads of 128 over 2048 entries: 59 us, 6 TB/s less a start of some 12 us
+//   (launch, list, page, entries, one behind the other); 4 rows over 512 entries 12.1 us.
+// Lost, against 147 to 150 us with references that moved less: dedicated warps that read the sums out (226 us: registers), two CTAs an SM with tiles
 // of 32 heads for 64 (270: entries are read twice), all columns of a set multiplied where one
 // reference moves (179), results by way of shared memory (32 heads 129 for 123).
 #include <cuda_runtime.h>
@@ -95,8 +100,8 @@ struct Shape {
   static constexpr int per_sm = G <= 16 ? 2 : 1;
   // Registers a thread: at the launch, and of the groups of four warps of each kind. Gathering
   // wants 64 where entries are few heads' (64 x 8 x 8 heads 57 us, 59.6 with 56 and 96 for softmax);
-  // with 64 heads softmax wants them (150 us, 156 with 80, 56 and 56), then gathering (137 us without
-  // a moved reference, 142 with 48).
+  // with 64 heads softmax wants them (150 us, 156 with 80, 56 and 56, when references moved less), then
+  // gathering (137 us without a moved reference, 142 with 48).
   static constexpr int regs = G <= 16 ? 64 : G == 32 ? 80 : 72;
   static constexpr int softmax_regs = G <= 16 ? 80 : G == 32 ? 120 : 88;
   static constexpr int gather_regs = G <= 32 ? 64 : 56, query_regs = G == 32 ? 56 : 48;
