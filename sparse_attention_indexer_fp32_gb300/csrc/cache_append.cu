@@ -22,8 +22,9 @@
 // looks through the call's other slots (a bit per hash of its blocks, eight slots a thread at once)
 // and adds up the sizes of the tokens it finds, so that each run's CTA comes to the same scale; that
 // of the first one writes it and what the block held before. This costs an ordered call 1.3 us with 64
-// tokens, 4.5 with 8192 of four prompts (34.4; 29.8 without, wrong in other orders), 10 with 8192
-// single tokens (44), where every CTA looks; and the call's tokens squared where they lie shuffled.
+// tokens, 4 with 8192 of four prompts (33.7; 29.8 without, wrong in other orders), 9 with 8192
+// single tokens (43), where every CTA looks. Four tokens of each of 64 sequences step by step 16.4 us
+// (9.6 in order); shuffled prompts cost their tokens squared (4 x 512 279 us, 4 x 2048 1090).
 //
 // Measured, in a CUDA graph: 8192 tokens x 8 heads x (128 + 128), bf16, into 8 bits 34 us for
 // 7.4 at the copy rate. It is bound by instructions and by what they wait for: 26 an element,
@@ -206,7 +207,8 @@ __device__ __forceinline__ void find_runs(const AppendParams& p, const AppendSid
     return __funnelshift_r(marks[h >> 22], 0, h >> 17) & 1;
   };
   const int64_t begin = t0 + __ffsll(static_cast<long long>(sh.leads)) - 1;
-  // Tokens that may be of a run's block, one a lane at most: a warp adds up one at a time, they are rare.
+  // Tokens that may be of a run's block, one a lane at most: a warp adds up kOnce at a time (one by one
+  // 64 sequences' four tokens take 26 us in place of 16).
   auto add = [&](int64_t t, bool may) {
     const int32_t slot = may ? slot_of(p, t) : -1, block = block_of(p, slot);
     int run = -1;
@@ -216,23 +218,37 @@ __device__ __forceinline__ void find_runs(const AppendParams& p, const AppendSid
       atomicMin(&sh.first[run], slot - block * p.block);
       if (t < begin) sh.later[run] = 1;
     }
-    for (uint32_t which = __ballot_sync(0xffffffffu, run >= 0); which != 0; which &= which - 1) {
-      const int src = __ffs(which) - 1, r = __shfl_sync(0xffffffffu, run, src);
-      const E* token = static_cast<const E*>(s.x) + c.h0 * s.x_head + (t - lane + src) * s.x_token;
+    constexpr int kOnce = 4;
+    for (uint32_t which = __ballot_sync(0xffffffffu, run >= 0); which != 0;) {
+      const E* token[kOnce];
+      int to[kOnce];
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i) {  // the last one again where there is none
+        const int src = which != 0 ? __ffs(which) - 1 : 0;
+        to[i] = which != 0 ? __shfl_sync(0xffffffffu, run, src) : to[i > 0 ? i - 1 : 0];
+        token[i] = which != 0 ? static_cast<const E*>(s.x) + c.h0 * s.x_head + (t - lane + src) * s.x_token : token[i > 0 ? i - 1 : 0];
+        which &= which - 1;
+      }
       for (int u = 0; u < c.heads; ++u) {
-        const E* of = token + u * s.x_head;
-        float high = 0.0f;
-        auto half = [&](int at) { return 0.5f * fabsf(Elem<E>::get(of[at])); };
-        auto count = [&](float size) {
-          if (size <= FLT_MAX) high = fmaxf(high, size);
-        };
-        for (int j = lane; j < pairs; j += 32) {
-          const int at = s.offset + (HALF ? j : 2 * j);
-          count((half(at) + half(at + (HALF ? pairs : 1))) * fabsf(p.scale));
+        float high[kOnce] = {};
+#pragma unroll 1
+        for (int j = lane; j < s.D - pairs; j += 32) {  // pairs that turn, then elements that do not
+          const int n = j - pairs, at = n < 0 ? s.offset + (HALF ? j : 2 * j) : n >= s.offset ? n + s.rotated : n;
+          const float factor = n < 0 ? fabsf(p.scale) : 1.0f;
+#pragma unroll
+          for (int i = 0; i < kOnce; ++i) {
+            const E* of = token[i] + u * s.x_head + at;
+            const float one = 0.5f * fabsf(Elem<E>::get(of[0]));
+            const float two = n < 0 ? 0.5f * fabsf(Elem<E>::get(of[HALF ? pairs : 1])) : 0.0f;
+            const float size = (one + two) * factor;
+            if (size <= FLT_MAX) high[i] = fmaxf(high[i], size);
+          }
         }
-        for (int j = lane; j < s.D - s.rotated; j += 32) count(half(s.rotated > 0 && j >= s.offset ? j + s.rotated : j));
-        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(high));
-        if (lane == 0) atomicMax(&sh.size[r * kHeads + u], most);
+#pragma unroll
+        for (int i = 0; i < kOnce; ++i) {
+          const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(high[i]));
+          if (lane == 0) atomicMax(&sh.size[to[i] * kHeads + u], most);
+        }
       }
     }
   };
